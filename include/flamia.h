@@ -353,6 +353,102 @@ int flamia_bwd_static_scratch(const flamia_qtensor* q, const flamia_qtensor* k, 
                               int head_dim, int causal, float softmax_scale, const flamia_options* opt,
                               const void* plan, void* dq_bf16, void* dk_bf16, void* dv_bf16, void* stream);
 
+/* ----------------------------------------------------------- scored attention
+ * Attention over bf16 operands for the layers whose scores are changed before
+ * the softmax: a tanh cap, a bias that falls with the distance, a bias by
+ * clipped distance (a learned relative position bias), windows and a prefix
+ * that every query of the document sees.  Such scores are not quantized: the
+ * cap and the biases need the score itself, so these calls take bf16 Q, K and
+ * V, and the products run as bf16 MMAs with fp32 accumulation.  For query i and
+ * key j of a document (document-local positions):
+ *   s = softmax_scale * q_i . k_j
+ *   t = softcap * tanh(s / softcap)                  (softcap 0: t = s)
+ *   u = t - slopes[h] |j - i| + rel_bias[h][clamp(j - i, -rel_max, rel_max)]
+ *   j is visible iff i - window_left <= j <= i + window_right
+ *                    or j < prefix_lens[document]
+ *   O_i = sum_j exp(u_ij - LSE_i) v_j,  LSE_i = ln sum_j exp(u_ij)
+ * over the visible keys of the document, the bounds as in flamia_options
+ * (causal = 1: right bound 0).  The prefix lengthens what a query sees; it
+ * hides nothing, so under a window it keeps a document's first tokens visible.
+ * A row whose visible keys all have bias -inf gets O 0 and LSE +inf, as rows
+ * outside every document do, and contributes no gradient. */
+typedef struct flamia_score_options {
+  float softcap;              /* 0 (default): none; else a finite positive cap */
+  const float* slopes;        /* device float [hq], finite, or NULL (default): no distance bias.
+                                 Constants of the call: no gradient is computed for them. */
+  const float* rel_bias;      /* device float [hq, 2 rel_max + 1], entry r + rel_max for key minus
+                                 query position r, or NULL (default): none.  Entries are finite or
+                                 -inf; below -2^100 (the lowest float among them) they hide the
+                                 pair, as -inf does. */
+  int rel_max;                /* with rel_bias: 1 .. FLAMIA_REL_MAX; else ignored */
+  const int32_t* prefix_lens; /* device int32 [num_seqs], or NULL (default): none; values are
+                                 clamped to the document's length */
+  int window_left;            /* visible keys as in flamia_options (default -1, -1: no limit) */
+  int window_right;
+} flamia_score_options;
+#define FLAMIA_REL_MAX 1024
+
+void flamia_default_score_options(flamia_score_options* opt);
+
+/* Forward.  q: bf16 [T, hq, head_dim]; k, v: bf16 [T, hkv, head_dim]; out: bf16
+ * [T, hq, head_dim]; lse: float [hq, T] (natural log).  opt may be NULL
+ * (defaults).  plan: any plan of the same cu_seqlens; one built for the call's
+ * own window orders the work best.  Non-finite values of K or V reach the rows
+ * of their own document only, hidden or not: inside a document a hidden key
+ * enters its tile's product with weight 0.  Rows behind the last document are
+ * not read.  Calls on one plan may overlap on the GPU. */
+int flamia_scored_fwd(const void* q_bf16, const void* k_bf16, const void* v_bf16, const int32_t* cu_seqlens,
+                      int num_seqs, int64_t total_tokens, int hq, int hkv, int head_dim, int causal,
+                      float softmax_scale, const flamia_score_options* opt, const void* plan, void* out_bf16,
+                      float* lse, void* stream);
+
+/* Backward, from the forward's inputs and outputs (out as returned, lse as
+ * returned) and dout: with P_ij = exp(u_ij - LSE_i), D_i = dO_i . O_i and
+ * dU = P o (dO V^T - D),
+ *   dV = P^T dO, dS = dU (1 - tanh(s / softcap)^2),
+ *   dQ = softmax_scale dS K, dK = softmax_scale dS^T Q (summed over the query
+ *   heads that share the kv head),
+ *   drel_bias[h][r] = sum of dU over the visible pairs of head h whose clipped
+ *   distance is r (all documents).
+ * dq: bf16 [T, hq, head_dim]; dk, dv: bf16 [T, hkv, head_dim]; drel_bias:
+ * float [hq, 2 rel_max + 1], or NULL (not computed; needs rel_bias otherwise).
+ * Results do not depend on the order in which the GPU runs the call: equal
+ * inputs give equal bits.  workspace: device scratch of
+ * flamia_scored_bwd_workspace_bytes() bytes (rel_max = 0: a call without
+ * drel_bias), 256-byte aligned; its contents on return are unspecified, and
+ * calls that overlap on the GPU need one each. */
+size_t flamia_scored_bwd_workspace_bytes(int64_t total_tokens, int num_seqs, int hq, int hkv, int head_dim,
+                                         int rel_max);
+int flamia_scored_bwd(const void* q_bf16, const void* k_bf16, const void* v_bf16, const void* out_bf16,
+                      const float* lse, const void* dout_bf16, const int32_t* cu_seqlens, int num_seqs,
+                      int64_t total_tokens, int hq, int hkv, int head_dim, int causal, float softmax_scale,
+                      const flamia_score_options* opt, const void* plan, void* dq_bf16, void* dk_bf16,
+                      void* dv_bf16, float* drel_bias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------------------- bucketed relative bias
+ * A learned relative position bias has one entry per (bucket, head), and a
+ * pair's bucket follows from its distance r = key - query position: with
+ * n = |r| for bidirectional = 1 (later keys, r > 0, use the upper half of the
+ * buckets, and B below is num_buckets / 2) and n = max(-r, 0), B = num_buckets
+ * otherwise, and e = B / 2 (whole-number division),
+ *   bucket = n                                                     (n < e)
+ *   bucket = min(B - 1, e + floor((B - e) ln(n / e) / ln(max_distance / e)))
+ * where a distance at which the quotient is a whole number belongs to the
+ * upper bucket.  From max_distance on the bucket is B - 1, so the bias is a
+ * function of the clipped distance, and flamia_scored_fwd / _bwd take it as
+ * rel_bias with any rel_max >= max_distance.
+ *
+ * flamia_relbias_expand: rel_bias[h][r + rel_max] = table[bucket(r)][h].
+ * flamia_relbias_reduce: dtable[b][h] = sum of drel_bias[h][r + rel_max] over
+ * the r of bucket b, in a fixed order (buckets no r falls into: 0).
+ * table, dtable: float [num_buckets, hq]; rel_bias, drel_bias: float [hq,
+ * 2 rel_max + 1].  num_buckets 2 .. 1024 (bidirectional: even, 4 at least),
+ * e < max_distance <= rel_max <= FLAMIA_REL_MAX, 1 <= hq <= 1024. */
+int flamia_relbias_expand(const float* table, int num_buckets, int hq, int max_distance, int bidirectional,
+                          float* rel_bias, int rel_max, void* stream);
+int flamia_relbias_reduce(const float* drel_bias, int rel_max, int num_buckets, int hq, int max_distance,
+                          int bidirectional, float* dtable, void* stream);
+
 /* ----------------------------------------------------------- status */
 /* Copy the plan's device status word into *status_out (synchronises `stream`). */
 int flamia_get_device_status(const void* plan, int* status_out, void* stream);

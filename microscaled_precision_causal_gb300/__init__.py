@@ -9,7 +9,10 @@ The functions mirror the C ABI in ``include/flamia.h``:
 ``flamia_plan_bytes``, ``flamia_plan_build``, ``flamia_quantize_tokenblock``,
 ``flamia_fwd``, ``flamia_bwd_workspace_bytes``, ``flamia_bwd``,
 ``flamia_get_device_status``; ``FlamiaAttention`` strings them into the
-training call (quantize Q/K/V, forward, backward).
+training call (quantize Q/K/V, forward, backward).  ``flamia_scored_fwd``,
+``flamia_scored_bwd``, ``flamia_relbias_expand`` and ``flamia_relbias_reduce``
+are the bf16 attention calls with changed scores (tanh cap, distance bias,
+bucketed relative bias, prefix); ``FlamiaScoredAttention`` strings those.
 """
 from __future__ import annotations
 
@@ -28,9 +31,11 @@ EXPORTED = (
     "flamia_default_options", "flamia_plan_bytes", "flamia_plan_build", "flamia_quantize_tokenblock",
     "flamia_fwd", "flamia_bwd_workspace_bytes", "flamia_bwd", "flamia_get_device_status",
     "flamia_status_string", "flamia_bwd_static_scratch", "flamia_quantize_nvfp4", "flamia_plan_build_window",
-    "flamia_quantize_hadamard", "flamia_quantize_qkv",
+    "flamia_quantize_hadamard", "flamia_quantize_qkv", "flamia_default_score_options", "flamia_scored_fwd",
+    "flamia_scored_bwd_workspace_bytes", "flamia_scored_bwd", "flamia_relbias_expand", "flamia_relbias_reduce",
 )
 STATIC_SCRATCH_BYTES = 64 << 20
+REL_MAX = 1024
 
 
 class FlamiaError(RuntimeError):
@@ -58,6 +63,12 @@ class MixedOperands(ctypes.Structure):
                                                "v_tok_codes", "v_tok_scales")]
 
 
+class ScoreOptions(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("rel_bias", ctypes.c_void_p),
+                ("rel_max", ctypes.c_int), ("prefix_lens", ctypes.c_void_p), ("window_left", ctypes.c_int),
+                ("window_right", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -72,6 +83,7 @@ def lib():
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
     f32 = ctypes.c_float
     qp = ctypes.POINTER(QTensor)
+    sp = ctypes.POINTER(ScoreOptions)
     op = ctypes.POINTER(Options)
     sig = {
         "flamia_default_options": (None, [op]),
@@ -91,6 +103,13 @@ def lib():
         "flamia_quantize_hadamard": (i32, [vp, i64, i32, i32, vp, i32, vp, vp, vp, vp, vp]),
         "flamia_quantize_qkv": (i32, [vp, vp, vp, i64, i32, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp,
                                       vp]),
+        "flamia_default_score_options": (None, [sp]),
+        "flamia_scored_fwd": (i32, [vp, vp, vp, vp, i32, i64, i32, i32, i32, i32, f32, sp, vp, vp, vp, vp]),
+        "flamia_scored_bwd_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32]),
+        "flamia_scored_bwd": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32, f32, sp, vp, vp, vp, vp,
+                                    vp, vp, sz, vp]),
+        "flamia_relbias_expand": (i32, [vp, i32, i32, i32, i32, vp, i32, vp]),
+        "flamia_relbias_reduce": (i32, [vp, i32, i32, i32, i32, i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -215,6 +234,49 @@ def flamia_bwd_static_scratch(q: QTensor, k: QTensor, v: QTensor, out, lse, dout
                                            causal, softmax_scale, ctypes.byref(opts) if opts else None, _ptr(plan),
                                            _ptr(dq), _ptr(dk), _ptr(dv), _stream(stream)),
            "flamia_bwd_static_scratch")
+
+
+def default_score_options() -> ScoreOptions:
+    o = ScoreOptions()
+    lib().flamia_default_score_options(ctypes.byref(o))
+    return o
+
+
+def flamia_scored_fwd(q, k, v, cu_seqlens, num_seqs: int, plan, out, lse, softmax_scale: float = 0.0,
+                      opts: Optional[ScoreOptions] = None, causal: int = 1, stream=None):
+    T, hq, d = q.shape
+    _check(lib().flamia_scored_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), num_seqs, T, hq, k.shape[1], d, causal,
+                                   softmax_scale, ctypes.byref(opts) if opts else None, _ptr(plan), _ptr(out), _ptr(lse),
+                                   _stream(stream)), "flamia_scored_fwd")
+
+
+def flamia_scored_bwd_workspace_bytes(total_tokens: int, num_seqs: int, hq: int, hkv: int, head_dim: int,
+                                      rel_max: int = 0) -> int:
+    return int(lib().flamia_scored_bwd_workspace_bytes(total_tokens, num_seqs, hq, hkv, head_dim, rel_max))
+
+
+def flamia_scored_bwd(q, k, v, out, lse, dout, cu_seqlens, num_seqs: int, plan, dq, dk, dv, workspace, drel_bias=None,
+                      softmax_scale: float = 0.0, opts: Optional[ScoreOptions] = None, causal: int = 1, stream=None):
+    T, hq, d = q.shape
+    _check(lib().flamia_scored_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(cu_seqlens),
+                                   num_seqs, T, hq, k.shape[1], d, causal, softmax_scale,
+                                   ctypes.byref(opts) if opts else None, _ptr(plan), _ptr(dq), _ptr(dk), _ptr(dv),
+                                   _ptr(drel_bias), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                   _stream(stream)), "flamia_scored_bwd")
+
+
+def flamia_relbias_expand(table, max_distance: int, bidirectional: bool, rel_bias, stream=None):
+    """table: float [buckets, hq]; rel_bias: float [hq, 2 rel_max + 1] (written)."""
+    _check(lib().flamia_relbias_expand(_ptr(table), table.shape[0], table.shape[1], max_distance, int(bidirectional),
+                                       _ptr(rel_bias), rel_bias.shape[1] // 2, _stream(stream)),
+           "flamia_relbias_expand")
+
+
+def flamia_relbias_reduce(drel_bias, max_distance: int, bidirectional: bool, dtable, stream=None):
+    """drel_bias: float [hq, 2 rel_max + 1]; dtable: float [buckets, hq] (written)."""
+    _check(lib().flamia_relbias_reduce(_ptr(drel_bias), drel_bias.shape[1] // 2, dtable.shape[0], dtable.shape[1],
+                                       max_distance, int(bidirectional), _ptr(dtable), _stream(stream)),
+           "flamia_relbias_reduce")
 
 
 def flamia_get_device_status(plan, stream=None) -> int:
@@ -356,3 +418,139 @@ class FlamiaAttention:
         off = rnd(n_codes)
         scales = self.workspace[off:off + T * H].view(T, H)
         return codes, scales
+
+
+class FlamiaScoredAttention:
+    """Buffers and calls of attention with changed scores for one packed layout.
+
+    The bf16 counterpart of FlamiaAttention for layers whose scores are capped by
+    a tanh (softcap > 0), fall with the distance (slopes, given per call), get a
+    learned relative position bias by buckets (buckets = (number of buckets,
+    max_distance, bidirectional), the table given per call) or see a prefix of
+    their document whatever the mask (prefix_lens, given per call).  causal and
+    window as in FlamiaAttention.
+
+    The object owns the plan, the outputs and the backward workspace; each call
+    overwrites the tensors that the last one returned.  Nothing is allocated per
+    call, so calls can be captured into a CUDA graph.  Tensors are contiguous, on
+    the object's device: q [T, hq, d], k and v [T, hkv, d] bf16; cu_seqlens
+    [N + 1] and prefix_lens [N] int32; slopes [hq] and table [buckets, hq] fp32.
+    Anything else raises FlamiaError.  Calls run on `stream`, by default the
+    object's device's current stream."""
+
+    def __init__(self, total_tokens: int, num_seqs: int, hq: int, hkv: int, head_dim: int, device="cuda",
+                 causal: bool = True, window=(-1, -1), softcap: float = 0.0, buckets=None):
+        import torch
+        if total_tokens < 0 or num_seqs < 0 or hq <= 0 or hkv <= 0 or hq % hkv or head_dim not in (64, 128):
+            raise FlamiaError(f"FlamiaScoredAttention: sizes {(total_tokens, num_seqs, hq, hkv, head_dim)} are not supported")
+        self.T, self.N, self.hq, self.hkv, self.d = total_tokens, num_seqs, hq, hkv, head_dim
+        self.causal = 1 if causal else 0
+        self.window = (int(window[0]), int(window[1]))
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        dev = self.device
+        self.opts = default_score_options()
+        self.opts.softcap = float(softcap)
+        self.opts.window_left, self.opts.window_right = self.window
+        self.rel_max = 0
+        f32, bf16 = torch.float32, torch.bfloat16
+        if buckets is not None:
+            self.num_buckets, self.max_distance, both = int(buckets[0]), int(buckets[1]), bool(buckets[2])
+            side = self.num_buckets // 2 if both else self.num_buckets
+            if side < 2 or (both and self.num_buckets % 2) or not side // 2 < self.max_distance <= REL_MAX:
+                raise FlamiaError(f"FlamiaScoredAttention: buckets {tuple(buckets)} are not supported")
+            self.bidirectional = both
+            self.rel_max = self.max_distance
+            self.rel_bias = torch.empty(hq, 2 * self.rel_max + 1, dtype=f32, device=dev)
+            self.drel_bias = torch.empty_like(self.rel_bias)
+            self.dtable = torch.empty(self.num_buckets, hq, dtype=f32, device=dev)
+        self.plan = torch.empty(flamia_plan_bytes(total_tokens, num_seqs), dtype=torch.uint8, device=dev)
+        self.out = torch.empty(total_tokens, hq, head_dim, dtype=bf16, device=dev)
+        self.lse = torch.empty(hq, total_tokens, dtype=f32, device=dev)
+        self.dq = torch.empty_like(self.out)
+        self.dk = torch.empty(total_tokens, hkv, head_dim, dtype=bf16, device=dev)
+        self.dv = torch.empty_like(self.dk)
+        ws = flamia_scored_bwd_workspace_bytes(total_tokens, num_seqs, hq, hkv, head_dim, self.rel_max)
+        self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+
+    def _want(self, name, t, shape, dtype):
+        if t.dtype != dtype or tuple(t.shape) != shape or t.device != self.device or not t.is_contiguous():
+            raise FlamiaError(f"{name}: want contiguous {dtype} {shape} on {self.device}, got {t.dtype} {tuple(t.shape)} "
+                              f"on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+    def _options(self, cu_seqlens, slopes, prefix_lens, table):
+        import torch
+        self._want("cu_seqlens", cu_seqlens, (self.N + 1,), torch.int32)
+        o = ScoreOptions.from_buffer_copy(self.opts)
+        if slopes is not None:
+            self._want("slopes", slopes, (self.hq,), torch.float32)
+            o.slopes = slopes.data_ptr()
+        if prefix_lens is not None:
+            self._want("prefix_lens", prefix_lens, (self.N,), torch.int32)
+            o.prefix_lens = prefix_lens.data_ptr()
+        if (table is not None) != (self.rel_max > 0):
+            raise FlamiaError("table: given to an object without buckets" if self.rel_max == 0 else
+                              "table: an object with buckets needs one")
+        if table is not None:
+            self._want("table", table, (self.num_buckets, self.hq), torch.float32)
+            o.rel_bias, o.rel_max = self.rel_bias.data_ptr(), self.rel_max
+        return o
+
+    def _inputs(self, q, k, v):
+        import torch
+        self._want("q", q, (self.T, self.hq, self.d), torch.bfloat16)
+        self._want("k", k, (self.T, self.hkv, self.d), torch.bfloat16)
+        self._want("v", v, (self.T, self.hkv, self.d), torch.bfloat16)
+
+    def _on_device(self):
+        import torch
+        if self.device.type != "cuda":
+            raise FlamiaError(f"FlamiaScoredAttention runs on a CUDA device, not on {self.device}")
+        return torch.cuda.device(self.device)
+
+    def plan_build(self, cu_seqlens, stream=None):
+        import torch
+        self._want("cu_seqlens", cu_seqlens, (self.N + 1,), torch.int32)
+        with self._on_device():
+            flamia_plan_build_window(cu_seqlens, self.N, self.T, self.causal, self.window[0], self.window[1], self.plan,
+                                     stream)
+
+    def forward(self, q, k, v, cu_seqlens, softmax_scale: float = 0.0, slopes=None, prefix_lens=None, table=None,
+                stream=None):
+        """(out bf16 [T, hq, d], lse fp32 [hq, T])."""
+        self._inputs(q, k, v)
+        o = self._options(cu_seqlens, slopes, prefix_lens, table)
+        with self._on_device():
+            stream = _stream(stream)
+            if table is not None:
+                flamia_relbias_expand(table, self.max_distance, self.bidirectional, self.rel_bias, stream)
+            flamia_scored_fwd(q, k, v, cu_seqlens, self.N, self.plan, self.out, self.lse, softmax_scale, o, self.causal,
+                              stream)
+        return self.out, self.lse
+
+    def backward(self, q, k, v, out, lse, dout, cu_seqlens, softmax_scale: float = 0.0, slopes=None, prefix_lens=None,
+                 table=None, stream=None):
+        """(dq, dk, dv) in bf16 and, with a table, its gradient in fp32.  out and lse: what forward returned for
+        these inputs."""
+        import torch
+        self._inputs(q, k, v)
+        self._want("out", out, (self.T, self.hq, self.d), torch.bfloat16)
+        self._want("dout", dout, (self.T, self.hq, self.d), torch.bfloat16)
+        self._want("lse", lse, (self.hq, self.T), torch.float32)
+        o = self._options(cu_seqlens, slopes, prefix_lens, table)
+        with self._on_device():
+            stream = _stream(stream)
+            if table is not None:
+                flamia_relbias_expand(table, self.max_distance, self.bidirectional, self.rel_bias, stream)
+            flamia_scored_bwd(q, k, v, out, lse, dout, cu_seqlens, self.N, self.plan, self.dq, self.dk, self.dv,
+                              self.workspace, self.drel_bias if table is not None else None, softmax_scale, o,
+                              self.causal, stream)
+            if table is None:
+                return self.dq, self.dk, self.dv
+            flamia_relbias_reduce(self.drel_bias, self.max_distance, self.bidirectional, self.dtable, stream)
+        return self.dq, self.dk, self.dv, self.dtable
+
+    def device_status(self, stream=None) -> int:
+        with self._on_device():
+            return flamia_get_device_status(self.plan, stream)

@@ -19,8 +19,8 @@ LIB = os.path.join(HERE, "libflamia.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["plan.cu", "quantize.cu", "attn_fwd.cu", "attn_fwd_coop.cu", "attn_bwd.cu", "abi.cu",
-           "static_scratch.cu"]
-HEADERS = ["common.cuh", "ptx.cuh", "tmap.h"]
+           "static_scratch.cu", "scored.cu", "relbias.cu"]
+HEADERS = ["common.cuh", "ptx.cuh", "tmap.h", "scored.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "scored.cuh"
 
 namespace flamia {
 cudaError_t launch_plan(const int32_t* cu, int N, int T, Window win, void* plan, cudaStream_t s);
@@ -37,6 +38,11 @@ cudaError_t launch_bwd(int D, const void* qc, const void* qs, const void* kc, co
                        const void* plan, void* dq_acc, void* dq, void* dk, void* dv, cudaStream_t stream,
                        void* const* ev, bool strict, const void* q4c, const void* q4s, const void* k4c,
                        const void* k4s, float* dbg, Window win, bool rot);
+cudaError_t launch_scored_fwd(int D, const ScoredParams& p, cudaStream_t stream);
+cudaError_t launch_scored_bwd(int D, const ScoredParams& p, cudaStream_t stream);
+cudaError_t launch_relbias_expand(const float* table, int nb, int hq, int md, int both, float* rel, int R, cudaStream_t s);
+cudaError_t launch_relbias_reduce(const float* drel, int R, int nb, int hq, int md, int both, float* dtable,
+                                  cudaStream_t s);
 }  // namespace flamia
 
 using namespace flamia;
@@ -136,6 +142,52 @@ BwdWorkspace bwd_layout(int64_t T, int N, int hq, int d) {
   w.dq_acc = off; off = round256(off + dq_acc_bytes(T, N, hq, d));   // fp16 chunks per (document tile, head, slice)
   w.total = off;
   return w;
+}
+
+int check_score_opts(const flamia_score_options* o) {
+  if (!o) return FLAMIA_OK;
+  if (!(o->softcap >= 0.f) || std::isinf(o->softcap)) return FLAMIA_ERR_INVALID_ARG;
+  // a cap whose reciprocal leaves the fp32 range has no use
+  if (o->softcap > 0.f && (o->softcap < 1e-30f || o->softcap > 1e30f)) return FLAMIA_ERR_UNSUPPORTED;
+  if (o->rel_bias && o->rel_max < 1) return FLAMIA_ERR_INVALID_ARG;
+  if (o->rel_bias && o->rel_max > FLAMIA_REL_MAX) return FLAMIA_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(o->slopes) | reinterpret_cast<uintptr_t>(o->rel_bias) |
+       reinterpret_cast<uintptr_t>(o->prefix_lens)) & 3u)
+    return FLAMIA_ERR_MISALIGNED;
+  return FLAMIA_OK;
+}
+
+ScoredParams scored_params(const void* q, const void* k, const void* v, const int32_t* cu, int N, int64_t T, int hq,
+                           int hkv, int d, int causal, float scale, const flamia_score_options* o, const void* plan) {
+  ScoredParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.cu = cu;
+  p.plan = static_cast<const int*>(plan);
+  p.N = N;
+  p.T = (int)T;
+  p.hq = hq;
+  p.hkv = hkv;
+  p.scale = resolve_scale(scale, d);
+  p.win = resolve_window(causal, o ? o->window_left : -1, o ? o->window_right : -1, T);
+  if (o) {
+    p.cap = o->softcap;
+    p.slopes = o->slopes;
+    p.rel = o->rel_bias;
+    p.R = o->rel_bias ? o->rel_max : 0;
+    p.prefix = o->prefix_lens;
+  }
+  return p;
+}
+
+int check_buckets(int nb, int hq, int md, int both, int R) {
+  if (nb < 2 || hq < 1 || md < 1 || R < 1 || (both != 0 && both != 1)) return FLAMIA_ERR_INVALID_ARG;
+  if (both && (nb < 4 || (nb & 1))) return FLAMIA_ERR_INVALID_ARG;
+  const int e = (both ? nb / 2 : nb) / 2;
+  if (md <= e || md > R) return FLAMIA_ERR_INVALID_ARG;
+  if (nb > 1024 || hq > 1024 || R > FLAMIA_REL_MAX) return FLAMIA_ERR_UNSUPPORTED;
+  return FLAMIA_OK;
 }
 
 }  // namespace
@@ -345,6 +397,99 @@ int flamia_bwd(const flamia_qtensor* q, const flamia_qtensor* k, const flamia_qt
                    is_mixed(opt) ? opt->mixed->k_codes_e2m1 : nullptr,
                    is_mixed(opt) ? opt->mixed->k_scales_e4m3 : nullptr, dbg, win, is_rotated(opt));
   return cuda_status(e);
+}
+
+void flamia_default_score_options(flamia_score_options* opt) {
+  if (!opt) return;
+  std::memset(opt, 0, sizeof(*opt));
+  opt->window_left = -1;
+  opt->window_right = -1;
+}
+
+int flamia_scored_fwd(const void* q_bf16, const void* k_bf16, const void* v_bf16, const int32_t* cu_seqlens,
+                      int num_seqs, int64_t total_tokens, int hq, int hkv, int head_dim, int causal,
+                      float softmax_scale, const flamia_score_options* opt, const void* plan, void* out_bf16,
+                      float* lse, void* stream) {
+  int rc = check_common(total_tokens, num_seqs, cu_seqlens, plan);
+  if (!rc) rc = check_heads(hq, hkv, head_dim);
+  if (!rc) rc = check_score_opts(opt);
+  if (rc) return rc;
+  if (causal != 0 && causal != 1) return FLAMIA_ERR_INVALID_ARG;
+  if (!q_bf16 || !k_bf16 || !v_bf16 || !out_bf16 || !lse) return FLAMIA_ERR_INVALID_ARG;
+  if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(out_bf16) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return FLAMIA_ERR_MISALIGNED;
+  if (total_tokens == 0) return FLAMIA_OK;
+  ScoredParams p = scored_params(q_bf16, k_bf16, v_bf16, cu_seqlens, num_seqs, total_tokens, hq, hkv, head_dim, causal,
+                                 softmax_scale, opt, plan);
+  p.out = static_cast<__nv_bfloat16*>(out_bf16);
+  p.lse = lse;
+  return cuda_status(launch_scored_fwd(head_dim, p, (cudaStream_t)stream));
+}
+
+size_t flamia_scored_bwd_workspace_bytes(int64_t total_tokens, int num_seqs, int hq, int hkv, int head_dim,
+                                         int rel_max) {
+  (void)hkv;
+  if (total_tokens < 0 || num_seqs < 0 || hq <= 0 || head_dim <= 0 || rel_max < 0) return 0;
+  return scored_bwd_layout(total_tokens, num_seqs, hq, rel_max).total;
+}
+
+int flamia_scored_bwd(const void* q_bf16, const void* k_bf16, const void* v_bf16, const void* out_bf16,
+                      const float* lse, const void* dout_bf16, const int32_t* cu_seqlens, int num_seqs,
+                      int64_t total_tokens, int hq, int hkv, int head_dim, int causal, float softmax_scale,
+                      const flamia_score_options* opt, const void* plan, void* dq_bf16, void* dk_bf16,
+                      void* dv_bf16, float* drel_bias, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_common(total_tokens, num_seqs, cu_seqlens, plan);
+  if (!rc) rc = check_heads(hq, hkv, head_dim);
+  if (!rc) rc = check_score_opts(opt);
+  if (rc) return rc;
+  if (causal != 0 && causal != 1) return FLAMIA_ERR_INVALID_ARG;
+  if (!q_bf16 || !k_bf16 || !v_bf16 || !out_bf16 || !lse || !dout_bf16 || !dq_bf16 || !dk_bf16 || !dv_bf16 || !workspace)
+    return FLAMIA_ERR_INVALID_ARG;
+  if (drel_bias && !(opt && opt->rel_bias)) return FLAMIA_ERR_INVALID_ARG;
+  if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(out_bf16) || !aligned16(dout_bf16) ||
+      !aligned16(dq_bf16) || !aligned16(dk_bf16) || !aligned16(dv_bf16) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(drel_bias) & 3u))
+    return FLAMIA_ERR_MISALIGNED;
+  ScoredParams p = scored_params(q_bf16, k_bf16, v_bf16, cu_seqlens, num_seqs, total_tokens, hq, hkv, head_dim, causal,
+                                 softmax_scale, opt, plan);
+  const ScoredBwdWorkspace w = scored_bwd_layout(total_tokens, num_seqs, hq, drel_bias ? p.R : 0);
+  if (workspace_bytes < w.total) return FLAMIA_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (total_tokens == 0)
+    return drel_bias ? cuda_status(cudaMemsetAsync(drel_bias, 0, (size_t)hq * (2 * p.R + 1) * 4, s)) : FLAMIA_OK;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.out = const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>(out_bf16));
+  p.lse = const_cast<float*>(lse);
+  p.dout = static_cast<const __nv_bfloat16*>(dout_bf16);
+  p.dq = static_cast<__nv_bfloat16*>(dq_bf16);
+  p.dk = static_cast<__nv_bfloat16*>(dk_bf16);
+  p.dv = static_cast<__nv_bfloat16*>(dv_bf16);
+  p.drel = drel_bias;
+  p.dvec = reinterpret_cast<float*>(ws + w.dvec);
+  p.drel_part = reinterpret_cast<float*>(ws + w.drel);
+  return cuda_status(launch_scored_bwd(head_dim, p, s));
+}
+
+int flamia_relbias_expand(const float* table, int num_buckets, int hq, int max_distance, int bidirectional,
+                          float* rel_bias, int rel_max, void* stream) {
+  if (!table || !rel_bias) return FLAMIA_ERR_INVALID_ARG;
+  const int rc = check_buckets(num_buckets, hq, max_distance, bidirectional, rel_max);
+  if (rc) return rc;
+  if ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(rel_bias)) & 3u) return FLAMIA_ERR_MISALIGNED;
+  return cuda_status(launch_relbias_expand(table, num_buckets, hq, max_distance, bidirectional, rel_bias, rel_max,
+                                           (cudaStream_t)stream));
+}
+
+int flamia_relbias_reduce(const float* drel_bias, int rel_max, int num_buckets, int hq, int max_distance,
+                          int bidirectional, float* dtable, void* stream) {
+  if (!drel_bias || !dtable) return FLAMIA_ERR_INVALID_ARG;
+  const int rc = check_buckets(num_buckets, hq, max_distance, bidirectional, rel_max);
+  if (rc) return rc;
+  if ((reinterpret_cast<uintptr_t>(drel_bias) | reinterpret_cast<uintptr_t>(dtable)) & 3u) return FLAMIA_ERR_MISALIGNED;
+  return cuda_status(launch_relbias_reduce(drel_bias, rel_max, num_buckets, hq, max_distance, bidirectional, dtable,
+                                           (cudaStream_t)stream));
 }
 
 int flamia_get_device_status(const void* plan, int* status_out, void* stream) {

@@ -1,0 +1,80 @@
+// Bucketed relative position bias: a table [buckets, heads] spread over the clipped
+// distances (expand), and a gradient by clipped distance summed back (reduce).
+//
+// A pair's bucket depends on its distance only, and from max_distance on it stays the
+// same, so the scored attention kernels see a bias by clipped distance: 2R + 1 floats a
+// head instead of a bucket per pair.  Both kernels touch a few KB (32 buckets, 16 heads,
+// R = 128: 16 KB each) and are bound by their launch.
+#include "common.cuh"
+
+namespace flamia {
+
+namespace {
+
+// Bucket of distance r (key minus query).  The logarithms are in 64 bits: a distance n
+// with ((n / e) ^ (B - e) a whole power of max_distance / e) lies on a bucket's border, and
+// 2^-30 puts it into the upper bucket whatever the last bit of the quotient; no other n up
+// to 1024 comes that close to a border from below.
+__device__ int rel_bucket(int r, int nb, int md, int both) {
+  int base = 0, n;
+  if (both) {
+    nb >>= 1;
+    base = r > 0 ? nb : 0;
+    n = r < 0 ? -r : r;
+  } else {
+    n = r < 0 ? -r : 0;
+  }
+  const int e = nb >> 1;
+  if (n < e) return base + n;
+  if (n >= md) return base + nb - 1;
+  const double x = log((double)n / e) / log((double)md / e) * (nb - e);
+  const int b = e + (int)floor(x + 0x1p-30);
+  return base + (b < nb - 1 ? b : nb - 1);
+}
+
+__global__ void relbias_expand_kernel(const float* __restrict__ table, int nb, int hq, int md, int both,
+                                      float* __restrict__ rel, int R) {
+  const int width = 2 * R + 1;
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= width) return;
+  const int b = rel_bucket(i - R, nb, md, both);
+  for (int h = blockIdx.y; h < hq; h += gridDim.y) rel[(size_t)h * width + i] = table[(size_t)b * hq + h];
+}
+
+// One block per head: the entries' buckets go to shared memory, then thread b sums its own
+// bucket's entries in increasing distance.  A bucket's entries are consecutive distances on
+// each side, so the scan over all 2R + 1 (one shared read per entry, broadcast) is short.
+__global__ void relbias_reduce_kernel(const float* __restrict__ drel, int R, int nb, int hq, int md, int both,
+                                      float* __restrict__ dtable) {
+  __shared__ float val[2 * FLAMIA_REL_MAX + 1];
+  __shared__ short id[2 * FLAMIA_REL_MAX + 1];
+  const int width = 2 * R + 1, h = blockIdx.x;
+  for (int i = threadIdx.x; i < width; i += blockDim.x) {
+    val[i] = drel[(size_t)h * width + i];
+    id[i] = (short)rel_bucket(i - R, nb, md, both);
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < nb; b += blockDim.x) {
+    float s = 0.f;
+    for (int i = 0; i < width; ++i)
+      if (id[i] == b) s += val[i];
+    dtable[(size_t)b * hq + h] = s;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_relbias_expand(const float* table, int nb, int hq, int md, int both, float* rel, int R,
+                                  cudaStream_t s) {
+  const dim3 grid((2 * R + 1 + 127) / 128, hq < 32 ? hq : 32);
+  relbias_expand_kernel<<<grid, 128, 0, s>>>(table, nb, hq, md, both, rel, R);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_relbias_reduce(const float* drel, int R, int nb, int hq, int md, int both, float* dtable,
+                                  cudaStream_t s) {
+  relbias_reduce_kernel<<<hq, 256, 0, s>>>(drel, R, nb, hq, md, both, dtable);
+  return cudaGetLastError();
+}
+
+}  // namespace flamia
