@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libflamia.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["plan.cu", "quantize.cu", "attn_fwd.cu", "attn_fwd_coop.cu", "attn_bwd.cu", "abi.cu",
-           "static_scratch.cu", "scored.cu", "relbias.cu"]
+           "static_scratch.cu", "scored_fwd.cu", "scored_bwd.cu", "relbias.cu"]
 HEADERS = ["common.cuh", "ptx.cuh", "tmap.h", "scored.cuh"]
 
 NVCC_FLAGS = [

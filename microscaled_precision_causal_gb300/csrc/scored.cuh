@@ -42,8 +42,158 @@ inline ScoredBwdWorkspace scored_bwd_layout(int64_t T, int N, int hq, int R) {
   return w;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+
 // Bias entries below this hide the pair, as -inf does (the lowest float would lose the
 // score's own value in the sum and overflow in base 2).
 constexpr float kHideBelow = -1.2676506002282294e30f;   // -2^100
+
+// ---------------------------------------------------------------- visible tiles
+// Key tiles that a run of query tiles [t0, t1] of a document sees, in increasing order:
+// the a tiles of the prefix that lie before the window's first tile, then the n - a tiles
+// from lo on (the window's, and prefix tiles behind its first).
+struct KeyTiles {
+  int a, lo, n;
+  __device__ __forceinline__ int tile(int k) const { return k < a ? k : lo + (k - a); }
+};
+__device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int nt, int pre_tiles, Window w) {
+  KeyTiles s;
+  s.lo = win_klo(t0, w);
+  s.a = min(pre_tiles, s.lo);
+  const int hi = max(win_khi(t1, nt, w), pre_tiles - 1);
+  s.n = s.a + hi - s.lo + 1;
+  return s;
+}
+// True when some key of key tile u is hidden from a query of tile t or lies outside the document.
+__device__ __forceinline__ bool scored_masked(int t, int u, int len, int pre, Window w) {
+  if ((u + 1) * kTile > len) return true;
+  return (u + 1) * kTile > pre && win_masked(t, u, len, w);
+}
+// Bits of 32 columns starting at column c0: the columns [lo, hi] and those below pre.
+__device__ __forceinline__ uint32_t below_mask(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
+__device__ __forceinline__ uint32_t column_mask(int lo, int hi, int pre, int c0) {
+  return (below_mask(hi + 1 - c0) & ~below_mask(lo - c0)) | below_mask(pre - c0);
+}
+
+// ---------------------------------------------------------------- scores in base 2
+// The kernels hold u log2(e), so that the softmax is 2^x.
+//
+// tanh cap: y = cap tanh(z), z = s / cap.  Where every |z| of a warp's 32 columns is at
+// most kTanhPolyTo an odd polynomial of degree 11 gives tanh to 1.2e-7 (least squares,
+// reweighted towards equal ripple, on Chebyshev nodes of z^2); it runs on the fp32 pipe,
+// 4 packed instructions a pair.  Else tanh(z) = 1 - 2 / (1 + 2^(2 z log2 e)), to 2^-22
+// absolute, which costs two MUFU operations beside the softmax's own.
+constexpr float kTanhPolyTo = 0.875f;
+__device__ __forceinline__ float2 tanh_poly(float2 z) {
+  const float2 w = fmul2(z, z);
+  auto c = [](float x) { return make_float2(x, x); };
+  float2 p = ffma2(w, c(-0.0036076765973120928f), c(0.01778564415872097f));
+  p = ffma2(w, p, c(-0.05228739604353905f));
+  p = ffma2(w, p, c(0.13298341631889343f));
+  p = ffma2(w, p, c(-0.3333015441894531f));
+  p = ffma2(w, p, c(0.9999991655349731f));
+  return fmul2(z, p);
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float tanh_any(float z) {
+  return fmaf(-2.f, fast_rcp(1.f + fast_exp2(z * (2.f * kLog2e))), 1.f);
+}
+
+// Constants of one query head, and how the bias enters one tile.
+struct ScoreHead {
+  float scale2;     // softmax scale log2 e
+  float zscale;     // softmax scale / cap
+  float cap2;       // cap log2 e
+  float slope2;     // slope log2 e (0: none)
+};
+struct TileBias {
+  const float* tab; // table entry of the thread's column 0, or null: the constant c
+  float c;
+  float rel0;       // distance (key - query) at the thread's column 0
+  float sl;         // bias per unit of distance; 0: none, NaN: both signs occur in the tile
+};
+// 32 raw products of columns c0 .. c0 + 31 (distance rel0 + DIR * column) -> u log2 e.
+// Without CAP and BIAS the raw products stay: the caller's exponent scales them.
+template <bool CAP, bool BIAS, int DIR>
+__device__ __forceinline__ void score_chunk(uint32_t (&v)[32], int c0, const ScoreHead& H, const TileBias& B) {
+  auto get = [&](int j) { return make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])); };
+  auto put = [&](int j, float2 x) {
+    v[j] = __float_as_uint(x.x);
+    v[j + 1] = __float_as_uint(x.y);
+  };
+  if constexpr (CAP) {
+    float mx = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) mx = fmax3(mx, fabsf(__uint_as_float(v[j])), fabsf(__uint_as_float(v[j + 1])));
+    const float2 zs = make_float2(H.zscale, H.zscale), c2 = make_float2(H.cap2, H.cap2);
+    if (!__any_sync(0xffffffffu, !(mx * H.zscale <= kTanhPolyTo))) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) put(j, fmul2(tanh_poly(fmul2(get(j), zs)), c2));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(H.cap2 * tanh_any(__uint_as_float(v[j]) * H.zscale));
+    }
+  }
+  if constexpr (BIAS) {
+    const float f = CAP ? 1.f : H.scale2;
+    const float2 f2 = make_float2(f, f);
+    if (B.tab) {
+      const float* tab = B.tab + DIR * c0;
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) put(j, ffma2(get(j), f2, make_float2(tab[DIR * j], tab[DIR * (j + 1)])));
+    } else {
+      const float2 b2 = make_float2(B.c, B.c);
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) put(j, ffma2(get(j), f2, b2));
+    }
+    if (B.sl != 0.f) {
+      const float r0 = B.rel0 + (float)(DIR * c0);
+      if (B.sl == B.sl) {
+        const float2 s2 = make_float2(B.sl, B.sl), r2 = make_float2(r0, r0);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2)
+          put(j, ffma2(fadd2(r2, make_float2((float)(DIR * j), (float)(DIR * (j + 1)))), s2, get(j)));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          v[j] = __float_as_uint(fmaf(fabsf(r0 + (float)(DIR * j)), -H.slope2, __uint_as_float(v[j])));
+      }
+    }
+  }
+}
+
+// Staged bias of one head: entry r + R + 255 holds the bias of distance r log2 e, clipped
+// to R on both sides and long enough for every tile that holds a distance below R, so that
+// no index is clipped in the loops.
+constexpr int kBiasReach = 2 * kTile - 1;
+constexpr int kBiasTab = 2 * (FLAMIA_REL_MAX + kBiasReach) + 1;
+__device__ __forceinline__ float bias_base2(float b) {
+  return b < kHideBelow ? -INFINITY : fminf(b, -kHideBelow) * kLog2e;
+}
+__device__ __forceinline__ void stage_bias(float* tab, const float* rel, int R, int h, int first, int stride) {
+  const float* src = rel + (size_t)h * (2 * R + 1);
+  for (int i = first; i < 2 * (R + kBiasReach) + 1; i += stride)
+    tab[i] = bias_base2(src[min(max(i - kBiasReach, 0), 2 * R)]);
+}
+// The bias of query tile t x key tile u for the thread whose column 0 has distance rel0.
+__device__ __forceinline__ TileBias tile_bias(const float* tab, bool has_rel, int R, float slope2, int t, int u, int rel0) {
+  const int rmax = (u - t) * kTile + kTile - 1, rmin = (u - t) * kTile - (kTile - 1);
+  TileBias B;
+  B.tab = nullptr;
+  B.c = 0.f;
+  B.rel0 = (float)rel0;
+  if (has_rel) {
+    if (rmax <= -R) B.c = tab[0];
+    else if (rmin >= R) B.c = tab[2 * (R + kBiasReach)];
+    else B.tab = tab + rel0 + R + kBiasReach;
+  }
+  B.sl = slope2 == 0.f ? 0.f : (rmax <= 0 ? slope2 : (rmin >= 0 ? -slope2 : __int_as_float(0x7fffffff)));
+  return B;
+}
 
 }  // namespace flamia

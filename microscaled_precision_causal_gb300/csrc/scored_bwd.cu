@@ -1,4 +1,4 @@
-// Scored attention, forward and backward: one warp per row, fp32 throughout.
+// Scored attention, backward: one warp per row, fp32 throughout.
 //
 // For query i and key j of a document:  s = scale q_i . k_j,  t = cap tanh(s / cap),
 // u = t - slope |j - i| + rel[clamp(j - i)];  O_i = sum_j softmax_j(u_ij) v_j with a running
@@ -66,36 +66,6 @@ __device__ __forceinline__ float score(const ScoredParams& p, float dotp, int h,
     u = b < kHideBelow ? -INFINITY : u + b;
   }
   return u;
-}
-
-template <int D>
-__global__ void scored_fwd_kernel(const ScoredParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (id >= (int64_t)p.T * p.hq) return;
-  const int t = (int)(id / p.hq), h = (int)(id % p.hq), hk = h / (p.hq / p.hkv);
-  Row r;
-  float o[D / 32] = {};
-  float m = -INFINITY, l = 0.f;
-  if (find_row(p, t, r)) {
-    float q[D / 32], k[D / 32], v[D / 32], g;
-    load_row<D>(p.q + ((int64_t)t * p.hq + h) * D, lane, q);
-    for (int j = 0; j < r.len; ++j) {
-      if (!visible(p, r.pos, j, r.pre)) continue;
-      const int64_t kr = ((int64_t)(r.start + j) * p.hkv + hk) * D;
-      load_row<D>(p.k + kr, lane, k);
-      const float u = score(p, dot<D>(q, k), h, j - r.pos, g);
-      if (u == -INFINITY) continue;
-      load_row<D>(p.v + kr, lane, v);
-      const float mn = fmaxf(m, u), a = expf(m - mn), e = expf(u - mn);
-      l = l * a + e;
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x) o[x] = o[x] * a + e * v[x];
-      m = mn;
-    }
-  }
-  store_row<D>(p.out + ((int64_t)t * p.hq + h) * D, lane, o, l > 0.f ? 1.f / l : 0.f);
-  if (lane == 0) p.lse[(int64_t)h * p.T + t] = l > 0.f ? m + logf(l) : INFINITY;
 }
 
 template <int D>
@@ -190,14 +160,6 @@ cudaError_t bwd_d(const ScoredParams& p, cudaStream_t s) {
 }
 
 }  // namespace
-
-cudaError_t launch_scored_fwd(int D, const ScoredParams& p, cudaStream_t s) {
-  if ((int64_t)p.T * p.hq > 0x7fffffffLL * kWarps) return cudaErrorInvalidValue;
-  const unsigned g = blocks((int64_t)p.T * p.hq);
-  if (D == 128) scored_fwd_kernel<128><<<g, kWarps * 32, 0, s>>>(p);
-  else scored_fwd_kernel<64><<<g, kWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_scored_bwd(int D, const ScoredParams& p, cudaStream_t s) {
   if ((int64_t)p.T * p.hq > 0x7fffffffLL * kWarps) return cudaErrorInvalidValue;
