@@ -76,6 +76,29 @@ __device__ __forceinline__ uint32_t column_mask(int lo, int hi, int pre, int c0)
   return (below_mask(hi + 1 - c0) & ~below_mask(lo - c0)) | below_mask(pre - c0);
 }
 
+// Unit number k of this CTA, or -1: boustrophedon rounds over the cost-sorted list.
+__device__ __forceinline__ int unit_index(int k, int n_units) {
+  const int G = gridDim.x, c = blockIdx.x;
+  if ((int64_t)k * G >= n_units) return -1;
+  const int i = k * G + ((k & 1) ? G - 1 - c : c);
+  return i < n_units ? i : -1;
+}
+__device__ __forceinline__ int prefix_of(const ScoredParams& p, int doc, int len) {
+  return p.prefix ? min(max(p.prefix[doc], 0), len) : 0;
+}
+// Clear rows first .. 127 of a TMA-staged [128][D] bf16 tile (64-column boxes): the tile's
+// rows behind the document belong to the next one, or to nobody, and may hold anything;
+// weight 0 does not silence an infinity.  r: the calling thread's row.
+template <int D>
+__device__ __forceinline__ void clear_row(uint8_t* tile, int r) {
+#pragma unroll
+  for (int b = 0; b < D / 64; ++b) {
+    uint4* row = reinterpret_cast<uint4*>(tile + b * kTile * 128 + r * 128);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
+  }
+}
+
 // ---------------------------------------------------------------- scores in base 2
 // The kernels hold u log2(e), so that the softmax is 2^x.
 //
@@ -117,54 +140,60 @@ struct TileBias {
   float rel0;       // distance (key - query) at the thread's column 0
   float sl;         // bias per unit of distance; 0: none, NaN: both signs occur in the tile
 };
-// 32 raw products of columns c0 .. c0 + 31 (distance rel0 + DIR * column) -> u log2 e.
-// Without CAP and BIAS the raw products stay: the caller's exponent scales them.
+__device__ __forceinline__ float2 pair_of(const uint32_t (&v)[32], int j) {
+  return make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+}
+__device__ __forceinline__ void put_pair(uint32_t (&v)[32], int j, float2 x) {
+  v[j] = __float_as_uint(x.x);
+  v[j + 1] = __float_as_uint(x.y);
+}
+// 32 raw products -> cap log2 e tanh(s / cap).
+__device__ __forceinline__ void cap_chunk(uint32_t (&v)[32], const ScoreHead& H) {
+  float mx = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) mx = fmax3(mx, fabsf(__uint_as_float(v[j])), fabsf(__uint_as_float(v[j + 1])));
+  const float2 zs = make_float2(H.zscale, H.zscale), c2 = make_float2(H.cap2, H.cap2);
+  if (!__any_sync(0xffffffffu, !(mx * H.zscale <= kTanhPolyTo))) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) put_pair(v, j, fmul2(tanh_poly(fmul2(pair_of(v, j), zs)), c2));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(H.cap2 * tanh_any(__uint_as_float(v[j]) * H.zscale));
+  }
+}
+// x f + bias for columns c0 .. c0 + 31 (distance rel0 + DIR * column).
+template <int DIR>
+__device__ __forceinline__ void bias_chunk(uint32_t (&v)[32], int c0, float f, float slope2, const TileBias& B) {
+  const float2 f2 = make_float2(f, f);
+  if (B.tab) {
+    const float* tab = B.tab + DIR * c0;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) put_pair(v, j, ffma2(pair_of(v, j), f2, make_float2(tab[DIR * j], tab[DIR * (j + 1)])));
+  } else {
+    const float2 b2 = make_float2(B.c, B.c);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) put_pair(v, j, ffma2(pair_of(v, j), f2, b2));
+  }
+  if (B.sl != 0.f) {
+    const float r0 = B.rel0 + (float)(DIR * c0);
+    if (B.sl == B.sl) {
+      const float2 s2 = make_float2(B.sl, B.sl), r2 = make_float2(r0, r0);
+#pragma unroll
+      for (int j = 0; j < 32; j += 2)
+        put_pair(v, j, ffma2(fadd2(r2, make_float2((float)(DIR * j), (float)(DIR * (j + 1)))), s2, pair_of(v, j)));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        v[j] = __float_as_uint(fmaf(fabsf(r0 + (float)(DIR * j)), -slope2, __uint_as_float(v[j])));
+    }
+  }
+}
+// 32 raw products of columns c0 .. c0 + 31 -> u log2 e.  Without CAP and BIAS the raw
+// products stay: the caller's exponent scales them.
 template <bool CAP, bool BIAS, int DIR>
 __device__ __forceinline__ void score_chunk(uint32_t (&v)[32], int c0, const ScoreHead& H, const TileBias& B) {
-  auto get = [&](int j) { return make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])); };
-  auto put = [&](int j, float2 x) {
-    v[j] = __float_as_uint(x.x);
-    v[j + 1] = __float_as_uint(x.y);
-  };
-  if constexpr (CAP) {
-    float mx = 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) mx = fmax3(mx, fabsf(__uint_as_float(v[j])), fabsf(__uint_as_float(v[j + 1])));
-    const float2 zs = make_float2(H.zscale, H.zscale), c2 = make_float2(H.cap2, H.cap2);
-    if (!__any_sync(0xffffffffu, !(mx * H.zscale <= kTanhPolyTo))) {
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) put(j, fmul2(tanh_poly(fmul2(get(j), zs)), c2));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(H.cap2 * tanh_any(__uint_as_float(v[j]) * H.zscale));
-    }
-  }
-  if constexpr (BIAS) {
-    const float f = CAP ? 1.f : H.scale2;
-    const float2 f2 = make_float2(f, f);
-    if (B.tab) {
-      const float* tab = B.tab + DIR * c0;
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) put(j, ffma2(get(j), f2, make_float2(tab[DIR * j], tab[DIR * (j + 1)])));
-    } else {
-      const float2 b2 = make_float2(B.c, B.c);
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) put(j, ffma2(get(j), f2, b2));
-    }
-    if (B.sl != 0.f) {
-      const float r0 = B.rel0 + (float)(DIR * c0);
-      if (B.sl == B.sl) {
-        const float2 s2 = make_float2(B.sl, B.sl), r2 = make_float2(r0, r0);
-#pragma unroll
-        for (int j = 0; j < 32; j += 2)
-          put(j, ffma2(fadd2(r2, make_float2((float)(DIR * j), (float)(DIR * (j + 1)))), s2, get(j)));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          v[j] = __float_as_uint(fmaf(fabsf(r0 + (float)(DIR * j)), -H.slope2, __uint_as_float(v[j])));
-      }
-    }
-  }
+  if constexpr (CAP) cap_chunk(v, H);
+  if constexpr (BIAS) bias_chunk<DIR>(v, c0, CAP ? 1.f : H.scale2, H.slope2, B);
 }
 
 // Staged bias of one head: entry r + R + 255 holds the bias of distance r log2 e, clipped

@@ -1,169 +1,992 @@
-// Scored attention, backward: one warp per row, fp32 throughout.
+// Scored attention, backward, on bf16 tcgen05 MMAs with TMEM accumulators.
 //
-// For query i and key j of a document:  s = scale q_i . k_j,  t = cap tanh(s / cap),
-// u = t - slope |j - i| + rel[clamp(j - i)];  O_i = sum_j softmax_j(u_ij) v_j with a running
-// maximum and sum; backward P = exp(u - LSE), dU = P o (dO V^T - D), dS = dU (1 - tanh^2).
+//   P = 2^(u log2 e - LSE log2 e), dU = P o (dO V^T - D), dS = dU o (1 - tanh^2),
+//   dV = P^T dO, dK = scale dS^T Q, dQ = scale dS K, drel[h][r] = sum of dU at distance r.
+//
+// Three launches: D = rowsum(dO o O) (memory-bound), then dK and dV per key tile, then dQ
+// per query tile.  P and dS are computed in both of the latter: 7 tile products a pair of
+// tiles instead of the 5 of a single pass.  A single pass has to add its dQ partials into
+// memory from every key tile: an fp32 tile (64 KB) per step through shared memory and L2,
+// in an order that changes from run to run, and needs dS^T once more as a shared-memory
+// operand.  Here dS and P are A operands straight from tensor memory, nothing is written to
+// shared memory in the loops, and the results are the same bits every time.
+//
+// P and dS enter their products in bf16 (their partners are bf16): half a step of 2^-8 per
+// element, as the rounding of the gradients themselves; sums stay in fp32.
+#include <algorithm>
+
+#include "ptx.cuh"
 #include "scored.cuh"
+#include "tmap.h"
 
 namespace flamia {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
+constexpr int kRegCtl = 88, kRegCompute = 208;
+static_assert(kRegCtl * 128 + kRegCompute * 256 <= kLaunchRegs * kThreads, "register split");
+constexpr int kStats = 4;        // staged LSE / D rows in flight
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
+// ---------------------------------------------------------------- D = rowsum(dO o O)
+// D/8 threads a row, one 16-byte load of each operand per thread; rows outside every
+// document get zero gradients.
 template <int D>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, int lane, float (&r)[D / 32]) {
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) r[e] = __bfloat162float(p[lane * (D / 32) + e]);
-}
-template <int D>
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, int lane, const float (&r)[D / 32], float f) {
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) p[lane * (D / 32) + e] = __float2bfloat16(r[e] * f);
-}
-template <int D>
-__device__ __forceinline__ float dot(const float (&a)[D / 32], const float (&b)[D / 32]) {
+__global__ void __launch_bounds__(256) scored_prep_kernel(const ScoredParams p) {
+  constexpr int kPer = D / 8, kRows = 256 / kPer;
+  const int sub = threadIdx.x % kPer;
+  const int64_t nb = (p.T + kRows - 1) / kRows;
+  const int h = (int)(blockIdx.x / nb);
+  const int64_t t = (blockIdx.x % nb) * kRows + threadIdx.x / kPer;
+  const bool in = t < p.T;
   float s = 0.f;
+  if (in) {
+    const int64_t at = (t * p.hq + h) * D + sub * 8;
+    if (t < p.plan[kPlanValid]) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p.out + at), b = *reinterpret_cast<const uint4*>(p.dout + at);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) s = fmaf(a[e], b[e], s);
-  return warp_sum(s);
-}
-
-// Row -> document-local position; false for a row outside every document.
-struct Row {
-  int start, len, pos, pre;
-};
-__device__ __forceinline__ bool find_row(const ScoredParams& p, int t, Row& r) {
-  if (t >= p.plan[kPlanValid]) return false;
-  const int n = upper_doc(p.cu, p.N, t);
-  r.start = p.cu[n];
-  r.len = p.cu[n + 1] - r.start;
-  r.pos = t - r.start;
-  r.pre = p.prefix ? min(max(p.prefix[n], 0), r.len) : 0;
-  return true;
-}
-__device__ __forceinline__ bool visible(const ScoredParams& p, int i, int j, int pre) {
-  return j < pre || ((p.win.left < 0 || j >= i - p.win.left) && (p.win.right < 0 || j <= i + p.win.right));
-}
-// u of one pair and, for the backward, 1 - tanh^2.
-__device__ __forceinline__ float score(const ScoredParams& p, float dotp, int h, int rel, float& g) {
-  float u = dotp * p.scale;
-  g = 1.f;
-  if (p.cap > 0.f) {
-    const float th = tanhf(u / p.cap);
-    u = p.cap * th;
-    g = 1.f - th * th;
-  }
-  if (p.slopes) u -= p.slopes[h] * fabsf((float)rel);
-  if (p.rel) {
-    const float b = p.rel[(size_t)h * (2 * p.R + 1) + min(max(rel, -p.R), p.R) + p.R];
-    u = b < kHideBelow ? -INFINITY : u + b;
-  }
-  return u;
-}
-
-template <int D>
-__global__ void scored_dvec_kernel(const ScoredParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (id >= (int64_t)p.T * p.hq) return;
-  float a[D / 32], b[D / 32];
-  load_row<D>(p.out + id * D, lane, a);
-  load_row<D>(p.dout + id * D, lane, b);
-  const float s = dot<D>(a, b);
-  if (lane == 0) p.dvec[(id % p.hq) * p.T + id / p.hq] = s;
-}
-
-template <int D>
-__global__ void scored_dq_kernel(const ScoredParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (id >= (int64_t)p.T * p.hq) return;
-  const int t = (int)(id / p.hq), h = (int)(id % p.hq), hk = h / (p.hq / p.hkv);
-  Row r;
-  float dq[D / 32] = {};
-  if (find_row(p, t, r)) {
-    float q[D / 32], k[D / 32], v[D / 32], gr[D / 32], g;
-    load_row<D>(p.q + id * D, lane, q);
-    load_row<D>(p.dout + id * D, lane, gr);
-    const float lse = p.lse[(int64_t)h * p.T + t], dv = p.dvec[(int64_t)h * p.T + t];
-    for (int j = 0; j < r.len; ++j) {
-      if (!visible(p, r.pos, j, r.pre)) continue;
-      const int64_t kr = ((int64_t)(r.start + j) * p.hkv + hk) * D;
-      load_row<D>(p.k + kr, lane, k);
-      load_row<D>(p.v + kr, lane, v);
-      const float u = score(p, dot<D>(q, k), h, j - r.pos, g);
-      const float e = u == -INFINITY ? 0.f : expf(u - lse);
-      const float du = e * (dot<D>(gr, v) - dv);
-      if (p.drel && lane == 0)
-        atomicAdd(p.drel + (size_t)h * (2 * p.R + 1) + min(max(j - r.pos, -p.R), p.R) + p.R, du);
-      const float ds = du * g * p.scale;
-#pragma unroll
-      for (int x = 0; x < D / 32; ++x) dq[x] = fmaf(ds, k[x], dq[x]);
+      for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(aw[i] << 16), __uint_as_float(bw[i] << 16), s);
+        s = fmaf(__uint_as_float(aw[i] & 0xffff0000u), __uint_as_float(bw[i] & 0xffff0000u), s);
+      }
+    } else {
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(p.dq + at) = z;
+      if (h < p.hkv) {
+        const int64_t kt = (t * p.hkv + h) * D + sub * 8;
+        *reinterpret_cast<uint4*>(p.dk + kt) = z;
+        *reinterpret_cast<uint4*>(p.dv + kt) = z;
+      }
     }
   }
-  store_row<D>(p.dq + id * D, lane, dq, 1.f);
+#pragma unroll
+  for (int o = kPer / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (in && sub == 0) p.dvec[(int64_t)h * p.T + t] = s;
+}
+
+// One row of D / 2 fp32 accumulators (columns c0 ..) -> bf16 in global memory, times f.
+template <int COLS>
+__device__ __forceinline__ void store_acc(uint32_t taddr, __nv_bfloat16* dst, float f, bool valid) {
+#pragma unroll 1
+  for (int c = 0; c < COLS / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld32(taddr + 32 * c, o);
+    tmem_ld_wait();
+    if (valid) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * q + 2 * e]) * f,
+                                                          __uint_as_float(o[8 * q + 2 * e + 1]) * f);
+          w[e] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
+        *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+__device__ __forceinline__ uint32_t pack2(float2 x) {
+  const __nv_bfloat162 b2 = __floats2bfloat162_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t*>(&b2);
+}
+// 1 - tanh^2 from the capped score y = cap log2 e tanh.
+__device__ __forceinline__ float2 cap_slope(float2 y, float inv_cap2) {
+  const float2 t = fmul2(y, make_float2(inv_cap2, inv_cap2));
+  return ffma2(t, make_float2(-t.x, -t.y), make_float2(1.f, 1.f));
 }
 
 template <int D>
-__global__ void scored_dkv_kernel(const ScoredParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (id >= (int64_t)p.T * p.hkv) return;
-  const int t = (int)(id / p.hkv), hk = (int)(id % p.hkv), group = p.hq / p.hkv;
-  Row r;
-  float dk[D / 32] = {}, dv[D / 32] = {};
-  if (find_row(p, t, r)) {
-    float q[D / 32], k[D / 32], v[D / 32], gr[D / 32], g;
-    load_row<D>(p.k + id * D, lane, k);
-    load_row<D>(p.v + id * D, lane, v);
-    for (int h = hk * group; h < (hk + 1) * group; ++h) {
-      for (int i = 0; i < r.len; ++i) {
-        if (!visible(p, i, r.pos, r.pre)) continue;
-        const int64_t tq = r.start + i, qr = (tq * p.hq + h) * D;
-        load_row<D>(p.q + qr, lane, q);
-        load_row<D>(p.dout + qr, lane, gr);
-        const float u = score(p, dot<D>(q, k), h, r.pos - i, g);
-        const float e = u == -INFINITY ? 0.f : expf(u - p.lse[(int64_t)h * p.T + tq]);
-        const float ds = e * (dot<D>(gr, v) - p.dvec[(int64_t)h * p.T + tq]) * g * p.scale;
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int h, int row) {
+  mbar_arrive_expect_tx(bar, kTile * D * 2);
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          dv[x] = fmaf(e, gr[x], dv[x]);
-          dk[x] = fmaf(ds, q[x], dk[x]);
+  for (int b = 0; b < D / 64; ++b) tma_load_3d(dst + b * kTile * 128, tm, bar, 64 * b, h, row);
+}
+
+// ================================================================ dK, dV
+// One CTA per SM walks (key tile, kv head) units; a step is a query tile of one of the kv
+// head's query heads.  S^T = K Q^T and dP^T = V dO^T have keys in the TMEM lanes, so P^T and
+// dS^T are written back over their own columns and are the A operands of dV += P^T dO and
+// dK += dS^T Q.  The next step's S^T runs behind dV (while dS^T is computed), its dP^T
+// behind dK (while the next P^T is computed), across units too: K is free once the unit's
+// last S^T is done, V once its last dP^T is.
+// Roles: warp 0 TMA, warp 1 MMA, warp 2 TMEM, warp 3 stages LSE and D of a step's queries,
+// warps 4-11 compute: thread = key row, warpgroup = 64 of the 128 query columns.
+// TMEM columns: dV [0, D), dK [128, 128 + D), S^T [256, 384), dP^T [384, 512).
+template <int D>
+struct DkvSmem {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kK = 0, kV = kTileBytes;
+  static constexpr int kQ = 2 * kTileBytes;                    // [2]
+  static constexpr int kDO = 4 * kTileBytes;                   // [2]
+  static constexpr int kStat = 6 * kTileBytes;                 // [kStats][-LSE log2 e 128, D 128]
+  static constexpr int kBias = kStat + kStats * 1024;          // [kBiasTab]
+  static constexpr int kAcc = kBias + (kBiasTab + 1) * 4;      // [2 R + 1] drel of the current head
+  static constexpr int kDiag = kAcc + (2 * FLAMIA_REL_MAX + 2) * 4;   // [2][8 warps][96]
+  static constexpr int kBar = (kDiag + 2 * 8 * 96 * 4 + 15) & ~15;
+  static constexpr int kBytes = kBar + 256;
+  static constexpr int kAlloc = kBytes + 1024;
+};
+
+struct KeyUnit {
+  int item, hk, u, start, len, nt, pre, tlo, nq;
+};
+__device__ __forceinline__ KeyUnit key_unit(const ScoredParams& p, const PlanView& pv, int i) {
+  KeyUnit U;
+  U.item = i / p.hkv;
+  U.hk = i % p.hkv;
+  const int4 item = pv.bwd_items[U.item];
+  const int2 span = pv.bwd_span[U.item];
+  U.u = item.y;
+  U.start = span.x;
+  U.len = span.y;
+  U.nt = (U.len + kTile - 1) / kTile;
+  U.pre = prefix_of(p, item.x, U.len);
+  const bool all = U.u * kTile < U.pre;        // every query of the document sees a prefix key
+  U.tlo = all ? 0 : win_tlo(U.u, p.win);
+  U.nq = (all ? U.nt - 1 : win_thi(U.u, U.nt, p.win)) - U.tlo + 1;
+  return U;
+}
+
+// The steps of this CTA, unit after unit.
+struct KeySteps {
+  int n, n_units, group;
+  KeyUnit U;
+  int h, t;                 // the step's query head and query tile
+  __device__ __forceinline__ bool unit(const ScoredParams& p, const PlanView& pv) {
+    const int i = unit_index(n, n_units);
+    if (i < 0) return false;
+    U = key_unit(p, pv, i);
+    h = U.hk * group;
+    t = U.tlo;
+    return true;
+  }
+  __device__ __forceinline__ bool begin(const ScoredParams& p, const PlanView& pv) {
+    n = 0;
+    n_units = p.plan[kPlanBwdItems] * p.hkv;
+    group = p.hq / p.hkv;
+    return unit(p, pv);
+  }
+  __device__ __forceinline__ bool head_first() const { return t == U.tlo; }
+  __device__ __forceinline__ bool head_last() const { return t == U.tlo + U.nq - 1; }
+  __device__ __forceinline__ bool first() const { return h == U.hk * group && head_first(); }
+  __device__ __forceinline__ bool last() const { return h == (U.hk + 1) * group - 1 && head_last(); }
+  __device__ __forceinline__ bool next(const ScoredParams& p, const PlanView& pv) {
+    if (last()) {
+      ++n;
+      return unit(p, pv);
+    }
+    if (head_last()) {
+      ++h;
+      t = U.tlo;
+    } else {
+      ++t;
+    }
+    return true;
+  }
+};
+
+// BIAS: 0 none, 1 a bias, 2 a bias whose gradient is wanted.
+template <int D, bool CAP, int BIAS>
+__global__ void __launch_bounds__(kThreads, 1)
+    scored_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                      const ScoredParams p) {
+  using L = DkvSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t *k_full = bars, *k_empty = bars + 1, *v_full = bars + 2, *v_empty = bars + 3;
+  uint64_t *q_full = bars + 4, *q_empty = bars + 6, *do_full = bars + 8, *do_empty = bars + 10;   // [2] each
+  uint64_t *s_full = bars + 12, *dp_full = bars + 13, *p_ready = bars + 14, *ds_ready = bars + 15;
+  uint64_t *acc_full = bars + 16, *drain = bars + 17;
+  uint64_t *st_full = bars + 18, *st_empty = st_full + kStats;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(st_empty + kStats);
+  int* status = const_cast<int*>(p.plan) + kPlanStatus;
+  const PlanView pv = plan_view(p.plan, p.T, p.N);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 14; ++i) mbar_init(bars + i, 1);
+    mbar_init(p_ready, 256);
+    mbar_init(ds_ready, 256);
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    for (int i = 0; i < kStats; ++i) {
+      mbar_init(&st_full[i], 32);
+      mbar_init(&st_empty[i], 256);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_do);
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  constexpr uint32_t kTV = 0, kTK = 128, kTS = 256, kTP = 384;
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegCtl>();
+    KeySteps S;
+    bool more = S.begin(p, pv), ok = true;
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
+      uint32_t nk = 0, nv = 0, nq = 0, nd = 0;       // tiles loaded
+      for (; more && ok; more = S.next(p, pv)) {
+        const int row = S.U.start + S.t * kTile, krow = S.U.start + S.U.u * kTile;
+        if (S.first()) {
+          if (nk && !(ok = mbar_wait(k_empty, (nk - 1) & 1, status))) break;
+          load_tile<D>(smem + L::kK, &tm_k, k_full, S.U.hk, krow);
+          ++nk;
+        }
+        if (nq >= 2 && !(ok = mbar_wait(&q_empty[nq & 1], ((nq >> 1) - 1) & 1, status))) break;
+        load_tile<D>(smem + L::kQ + (nq & 1) * L::kTileBytes, &tm_q, &q_full[nq & 1], S.h, row);
+        ++nq;
+        if (S.first()) {
+          if (nv && !(ok = mbar_wait(v_empty, (nv - 1) & 1, status))) break;
+          load_tile<D>(smem + L::kV, &tm_v, v_full, S.U.hk, krow);
+          ++nv;
+        }
+        if (nd >= 2 && !(ok = mbar_wait(&do_empty[nd & 1], ((nd >> 1) - 1) & 1, status))) break;
+        load_tile<D>(smem + L::kDO + (nd & 1) * L::kTileBytes, &tm_do, &do_full[nd & 1], S.h, row);
+        ++nd;
+      }
+      // nothing may land after the CTA has left (open only when a wait ran out)
+      if (nk) mbar_wait(k_full, (nk - 1) & 1, status);
+      if (nv) mbar_wait(v_full, (nv - 1) & 1, status);
+      for (uint32_t x = nq > 2 ? nq - 2 : 0; x < nq; ++x) mbar_wait(&q_full[x & 1], (x >> 1) & 1, status);
+      for (uint32_t x = nd > 2 ? nd - 2 : 0; x < nd; ++x) mbar_wait(&do_full[x & 1], (x >> 1) & 1, status);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      const bool leader = elect_one();
+      const uint32_t base16 = (smem_u32(smem) & 0x3FFFFu) >> 4;
+      auto scores = [&](uint32_t a_off, uint32_t b_off, uint32_t d, uint64_t* bar) {     // both operands K-major
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = (s / 4) * kTile * 128 + (s % 4) * 32;
+          if (leader)
+            mma_bf16(tbase + d, sdesc_at(base16, a_off + off, 16, 1024, kSwizzle128B),
+                     sdesc_at(base16, b_off + off, 16, 1024, kSwizzle128B), idesc_bf16(128, 128, 0, 0), s > 0);
+        }
+        if (leader) mma_commit(bar);
+      };
+      auto accum = [&](uint32_t a, uint32_t b_off, uint32_t d, bool first) {             // A from TMEM, B over its rows
+#pragma unroll
+        for (int s = 0; s < kTile / 16; ++s)
+          if (leader)
+            mma_bf16_ta(tbase + d, tbase + a + (s < 4 ? 8 * s : 64 + 8 * (s - 4)),
+                        sdesc_at(base16, b_off + s * 2048, kTile * 128, 1024, kSwizzle128B), idesc_bf16(128, D, 0, 1),
+                        (!first || s > 0));
+      };
+      auto issue_s = [&](uint32_t g) {
+        if (S.first() && !(ok = warp_wait(k_full, S.n & 1, status))) return;
+        if (!(ok = warp_wait(&q_full[g & 1], (g >> 1) & 1, status))) return;
+        tc_fence_after();
+        scores(L::kK, L::kQ + (g & 1) * L::kTileBytes, kTS, s_full);
+        if (S.last() && leader) mma_commit(k_empty);
+      };
+      auto issue_dp = [&](uint32_t g) {
+        if (S.first() && !(ok = warp_wait(v_full, S.n & 1, status))) return;
+        if (!(ok = warp_wait(&do_full[g & 1], (g >> 1) & 1, status))) return;
+        tc_fence_after();
+        scores(L::kV, L::kDO + (g & 1) * L::kTileBytes, kTP, dp_full);
+        if (S.last() && leader) mma_commit(v_empty);
+      };
+      if (more) {
+        issue_s(0);
+        if (ok) issue_dp(0);
+        for (uint32_t g = 0; more && ok; ++g) {
+          const bool first = S.first(), last = S.last();
+          if (!(ok = warp_wait(p_ready, g & 1, status))) break;
+          tc_fence_after();
+          accum(kTS, L::kDO + (g & 1) * L::kTileBytes, kTV, first);
+          if (leader) mma_commit(&do_empty[g & 1]);
+          more = S.next(p, pv);
+          if (more) issue_s(g + 1);
+          if (!ok || !(ok = warp_wait(ds_ready, g & 1, status))) break;
+          tc_fence_after();
+          accum(kTP, L::kQ + (g & 1) * L::kTileBytes, kTK, first);
+          if (leader) {
+            mma_commit(&q_empty[g & 1]);
+            if (last) mma_commit(acc_full);
+          }
+          if (more) issue_dp(g + 1);
+        }
+      }
+      if (leader) {
+        mma_commit(drain);
+        mbar_wait(drain, 0, status);
+      }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------- LSE and D of a step's queries
+      float* stat = reinterpret_cast<float*>(smem + L::kStat);
+      for (uint32_t g = 0; more && ok; more = S.next(p, pv), ++g) {
+        const int b = g % kStats;
+        float l[4], d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int q = S.t * kTile + 32 * e + lane;
+          const int64_t at = (int64_t)S.h * p.T + S.U.start + q;
+          l[e] = q < S.U.len ? p.lse[at] : INFINITY;
+          d[e] = q < S.U.len ? p.dvec[at] : 0.f;
+        }
+        if (g >= kStats && !(ok = warp_wait(&st_empty[b], (g / kStats - 1) & 1, status))) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          stat[b * 256 + 32 * e + lane] = -l[e] * kLog2e;
+          stat[b * 256 + 128 + 32 * e + lane] = d[e];
+        }
+        mbar_arrive(&st_full[b]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ compute
+    setmaxnreg_inc<kRegCompute>();
+    const int w = (warp - 4) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane, tid = threadIdx.x - 128;
+    const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t s_addr = lane_base + kTS + 64 * w, dp_addr = lane_base + kTP + 64 * w;
+    float* tab = reinterpret_cast<float*>(smem + L::kBias);
+    float* acc = reinterpret_cast<float*>(smem + L::kAcc);
+    const bool has_rel = BIAS && p.rel != nullptr;
+    const int R = p.R;
+    ScoreHead H;
+    H.scale2 = p.scale * kLog2e;
+    H.zscale = CAP ? p.scale / p.cap : 0.f;
+    H.cap2 = p.cap * kLog2e;
+    H.slope2 = 0.f;
+    const float inv_cap2 = CAP ? 1.f / H.cap2 : 0.f;
+    int staged = -1, buf = 0;
+    float far_lo = 0.f, far_hi = 0.f;
+    bool ok = true;
+    KeySteps S;
+    // a warp whose wait ran out goes on through the steps without work: it still meets the others
+    // at the barriers
+    uint32_t g = 0;
+    for (bool more = S.begin(p, pv); more; ++g) {
+      const KeyUnit& U = S.U;
+      const int t = S.t, kj = U.u * kTile + r;
+      if constexpr (BIAS != 0) {
+        if (S.head_first() && staged != S.h) {
+          if (p.slopes) H.slope2 = p.slopes[S.h] * kLog2e;
+          if (has_rel) {
+            named_bar_sync(1, 256);
+            stage_bias(tab, p.rel, R, S.h, tid, 256);
+            named_bar_sync(1, 256);
+          }
+          staged = S.h;
+        }
+        if (BIAS == 2 && S.head_first()) {
+          for (int i = tid; i < 2 * R + 1; i += 256) acc[i] = 0.f;
+          far_lo = far_hi = 0.f;
+          named_bar_sync(1, 256);
+        }
+      }
+      float du_lo = 0.f;      // (BIAS 2) sum of the thread's dU of a far tile
+      uint32_t v[2][32];
+      if (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&st_full[g % kStats], (g / kStats) & 1, status) &&
+                                         mbar_wait(s_full, g & 1, status));
+      }
+      const float* nl = reinterpret_cast<const float*>(smem + L::kStat) + (g % kStats) * 256 + 64 * w;
+      if (ok) {
+        tc_fence_after();
+        tmem_ld32(s_addr, v[0]);
+        tmem_ld32(s_addr + 32, v[1]);
+        tmem_ld_wait();
+        uint32_t gr[2][32];
+        TileBias B{};
+        if constexpr (BIAS != 0) B = tile_bias(tab, has_rel, R, H.slope2, t, U.u, kj - (t * kTile + 64 * w));
+        const bool masked = scored_masked(t, U.u, U.len, U.pre, p.win) || (t + 1) * kTile > U.len;
+        int lo = 0, hi = U.len - 1;
+        if (kj >= U.len) {
+          hi = -1;
+        } else if (kj >= U.pre) {
+          if (p.win.right >= 0) lo = kj - p.win.right;
+          if (p.win.left >= 0) hi = min(hi, kj + p.win.left);
+        }
+        lo -= t * kTile + 64 * w;
+        hi -= t * kTile + 64 * w;
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if constexpr (CAP) {
+            cap_chunk(v[c], H);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), inv_cap2));
+          }
+          if constexpr (BIAS != 0) bias_chunk<-1>(v[c], 32 * c, CAP ? 1.f : H.scale2, H.slope2, B);
+          if (masked) {
+            const uint32_t see = column_mask(lo, hi, 0, 32 * c);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[c][j] = (see >> j) & 1 ? v[c][j] : 0xff800000u;
+          }
+          const float2 f2 = make_float2(H.scale2, H.scale2);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 n4 = *reinterpret_cast<const float4*>(nl + 32 * c + j);
+            float2 e0 = make_float2(n4.x, n4.y), e1 = make_float2(n4.z, n4.w);
+            if constexpr (CAP || BIAS != 0) {
+              e0 = fadd2(pair_of(v[c], j), e0);
+              e1 = fadd2(pair_of(v[c], j + 2), e1);
+            } else {
+              e0 = ffma2(pair_of(v[c], j), f2, e0);
+              e1 = ffma2(pair_of(v[c], j + 2), f2, e1);
+            }
+            e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
+            e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
+            pk[16 * c + j / 2] = pack2(e0);
+            pk[16 * c + j / 2 + 1] = pack2(e1);
+            put_pair(v[c], j, e0);
+            put_pair(v[c], j + 2, e1);
+          }
+          if constexpr (CAP && BIAS != 2) {       // dS needs P (1 - tanh^2) alone
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) put_pair(v[c], j, fmul2(pair_of(v[c], j), pair_of(gr[c], j)));
+          }
+        }
+        tmem_st32(s_addr, pk);
+        tmem_st_wait();
+        if ((t + 1) * kTile > U.len) {
+          // queries behind the document: the products below sum over them
+          ok = __all_sync(0xffffffffu, mbar_wait(&do_full[g & 1], (g >> 1) & 1, status));
+          if (ok && t * kTile + r >= U.len)
+            clear_row<D>(smem + (w ? L::kQ : L::kDO) + (g & 1) * L::kTileBytes, r);
+          fence_proxy_async_smem();
+        }
+        if (ok) {
+          tc_fence_before();
+          mbar_arrive(p_ready);
+          ok = __all_sync(0xffffffffu, mbar_wait(dp_full, g & 1, status));
+        }
+        if (ok) {
+          tc_fence_after();
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t dp[32];
+            tmem_ld32(dp_addr + 32 * c, dp);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 d4 = *reinterpret_cast<const float4*>(nl + 128 + 32 * c + j);
+              float2 a0 = fmul2(pair_of(v[c], j), fadd2(pair_of(dp, j), make_float2(-d4.x, -d4.y)));
+              float2 a1 = fmul2(pair_of(v[c], j + 2), fadd2(pair_of(dp, j + 2), make_float2(-d4.z, -d4.w)));
+              if (masked) {     // a hidden pair's dP may be anything
+                a0.x = pair_of(v[c], j).x == 0.f ? 0.f : a0.x;
+                a0.y = pair_of(v[c], j).y == 0.f ? 0.f : a0.y;
+                a1.x = pair_of(v[c], j + 2).x == 0.f ? 0.f : a1.x;
+                a1.y = pair_of(v[c], j + 2).y == 0.f ? 0.f : a1.y;
+              }
+              if constexpr (BIAS == 2) {
+                put_pair(v[c], j, a0);
+                put_pair(v[c], j + 2, a1);
+                sum = fadd2(sum, fadd2(a0, a1));
+                if constexpr (CAP) {
+                  a0 = fmul2(a0, pair_of(gr[c], j));
+                  a1 = fmul2(a1, pair_of(gr[c], j + 2));
+                }
+              }
+              pk[16 * c + j / 2] = pack2(a0);
+              pk[16 * c + j / 2 + 1] = pack2(a1);
+            }
+          }
+          du_lo = sum.x + sum.y;
+          tmem_st32(dp_addr, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(ds_ready);
+          mbar_arrive(&st_empty[g % kStats]);
+        }
+      }
+      if constexpr (BIAS == 2) {
+        const int tile_rel = (U.u - t) * kTile;
+        if (tile_rel + kTile - 1 <= -R) {
+          far_lo += du_lo;
+        } else if (tile_rel - (kTile - 1) >= R) {
+          far_hi += du_lo;
+        } else {
+          // sums along the diagonals: a running value moves one lane up per column, so it stays on its
+          // diagonal; lane 31's is complete
+          float* dg = reinterpret_cast<float*>(smem + L::kDiag) + buf * (8 * 96);
+          float* mine = dg + (warp - 4) * 96;
+          float run = 0.f;
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            run += __uint_as_float(v[c / 32][c % 32]);
+            if (lane == 31) mine[94 - c] = run;
+            run = __shfl_up_sync(0xffffffffu, run, 1);
+            if (lane == 0) run = 0.f;
+          }
+          if (lane > 0) mine[lane - 1] = run;      // after the last shift lane l holds diagonal l - 1
+          named_bar_sync(1, 256);
+          if (tid < 255) {
+            const int x = tid - 127;               // key row - query column
+            float s = 0.f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const int at = x - 32 * (q & 3) + 64 * (q >> 2) + 63;
+              if (at >= 0 && at < 95) s += dg[q * 96 + at];
+            }
+            const int rel = tile_rel + x;
+            if (rel <= -R) far_lo += s;
+            else if (rel >= R) far_hi += s;
+            else acc[rel + R] += s;
+          }
+          buf ^= 1;
+        }
+        if (S.head_last()) {
+          // the head's sums of this key tile: the two ends over all threads in a fixed order
+          float* red = reinterpret_cast<float*>(smem + L::kDiag) + buf * (8 * 96);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) {
+            far_lo += __shfl_xor_sync(0xffffffffu, far_lo, o);
+            far_hi += __shfl_xor_sync(0xffffffffu, far_hi, o);
+          }
+          if (lane == 0) {
+            red[2 * (warp - 4)] = far_lo;
+            red[2 * (warp - 4) + 1] = far_hi;
+          }
+          named_bar_sync(1, 256);
+          float* part = p.drel_part + ((size_t)S.h * p.plan[kPlanBwdItems] + U.item) * (2 * R + 1);
+          for (int i = tid; i < 2 * R + 1; i += 256) {
+            float s = acc[i];
+            if (i == 0 || i == 2 * R) {
+              s = 0.f;
+              for (int q = 0; q < 8; ++q) s += red[2 * q + (i ? 1 : 0)];
+            }
+            part[i] = s;
+          }
+          named_bar_sync(1, 256);
+          buf ^= 1;
+        }
+      }
+      if (S.last() && ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, S.n & 1, status));
+        if (ok) {
+          tc_fence_after();
+          const bool valid = kj < U.len;
+          const int64_t at = ((int64_t)(U.start + kj) * p.hkv + U.hk) * D;
+          if (w == 0) store_acc<D>(lane_base + kTV, p.dv + at, 1.f, valid);
+          else store_acc<D>(lane_base + kTK, p.dk + at, p.scale, valid);
+          tc_fence_before();
+        }
+      }
+      more = S.next(p, pv);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// ================================================================ dQ
+// One CTA per SM walks (query tile, query head) units; a step is a key tile.  S = Q K^T and
+// dP = dO V^T have queries in the TMEM lanes; Q and dO are A operands from tensor memory,
+// copied there once a unit, which leaves shared memory to three K and three V tiles and
+// halves what these products read from it.  dS goes over dP's columns and is the A operand
+// of dQ += dS K.  The next step's S runs while P is computed, dP behind dQ.
+// Warps as above without the stager; the thread's row keeps its LSE and D in registers.
+// TMEM columns: dQ [0, D), S [128, 256), dP [256, 384), Q [384, ...), dO [448, ...).
+template <int D>
+struct DqSmem {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kStages = 3;
+  static constexpr int kK = 0;                                   // [kStages]
+  static constexpr int kV = kStages * kTileBytes;                // [kStages]
+  static constexpr int kBias = 2 * kStages * kTileBytes;         // [kBiasTab]
+  static constexpr int kBar = (kBias + kBiasTab * 4 + 15) & ~15;
+  static constexpr int kBytes = kBar + 256;
+  static constexpr int kAlloc = kBytes + 1024;
+};
+
+struct QuerySteps {
+  int n, n_units;
+  int h, hk, t, start, len, nt, pre;
+  KeyTiles kt;
+  int k;
+  // units: the two query tiles of a forward item for every head; an item of one tile has empty units
+  __device__ __forceinline__ bool unit(const ScoredParams& p, const PlanView& pv) {
+    for (;; ++n) {
+      const int i = unit_index(n, n_units);
+      if (i < 0) return false;
+      const int item_idx = i / (2 * p.hq), x = i % (2 * p.hq);
+      const int4 item = pv.fwd_items[item_idx];
+      const int w = kItemTiles - 1 - x / p.hq;        // the item's later tile first: it sees more
+      if (w >= item.z) continue;
+      const int2 span = pv.fwd_span[item_idx];
+      h = x % p.hq;
+      hk = h / (p.hq / p.hkv);
+      t = item.y + w;
+      start = span.x;
+      len = span.y;
+      nt = (len + kTile - 1) / kTile;
+      pre = prefix_of(p, item.x, len);
+      kt = key_tiles(t, t, nt, (pre + kTile - 1) / kTile, p.win);
+      k = 0;
+      return true;
+    }
+  }
+  __device__ __forceinline__ bool begin(const ScoredParams& p, const PlanView& pv) {
+    n = 0;
+    n_units = p.plan[kPlanFwdItems] * 2 * p.hq;
+    return unit(p, pv);
+  }
+  __device__ __forceinline__ bool first() const { return k == 0; }
+  __device__ __forceinline__ bool last() const { return k == kt.n - 1; }
+  __device__ __forceinline__ int tile() const { return kt.tile(k); }
+  __device__ __forceinline__ bool next(const ScoredParams& p, const PlanView& pv) {
+    if (last()) {
+      ++n;
+      return unit(p, pv);
+    }
+    ++k;
+    return true;
+  }
+};
+
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1)
+    scored_dq_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const ScoredParams p) {
+  using L = DqSmem<D>;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t *k_full = bars, *k_empty = bars + kStages, *v_full = bars + 2 * kStages, *v_empty = bars + 3 * kStages;
+  uint64_t *s_full = bars + 4 * kStages, *dp_full = s_full + 1, *acc_full = s_full + 2, *drain = s_full + 3;
+  uint64_t *s_free = s_full + 4, *ds_ready = s_full + 5, *q_ready = s_full + 6;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 7);
+  int* status = const_cast<int*>(p.plan) + kPlanStatus;
+  const PlanView pv = plan_view(p.plan, p.T, p.N);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4 * kStages + 4; ++i) mbar_init(bars + i, 1);
+    mbar_init(s_free, 256);
+    mbar_init(ds_ready, 256);
+    mbar_init(q_ready, 256);
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  constexpr uint32_t kTQ = 0, kTS = 128, kTP = 256, kTA = 384, kTB = 448;
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegCtl>();
+    QuerySteps S;
+    bool more = S.begin(p, pv), ok = true;
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
+      uint32_t nk = 0, nv = 0;                       // tiles loaded
+      for (; more && ok; more = S.next(p, pv)) {
+        const int row = S.start + S.tile() * kTile;
+        const uint32_t b = nk % kStages, par = (nk / kStages - 1) & 1;
+        if (nk >= kStages && !(ok = mbar_wait(&k_empty[b], par, status))) break;
+        load_tile<D>(smem + L::kK + b * L::kTileBytes, &tm_k, &k_full[b], S.hk, row);
+        ++nk;
+        if (nv >= kStages && !(ok = mbar_wait(&v_empty[b], par, status))) break;
+        load_tile<D>(smem + L::kV + b * L::kTileBytes, &tm_v, &v_full[b], S.hk, row);
+        ++nv;
+      }
+      for (uint32_t x = nk > kStages ? nk - kStages : 0; x < nk; ++x)
+        mbar_wait(&k_full[x % kStages], (x / kStages) & 1, status);
+      for (uint32_t x = nv > kStages ? nv - kStages : 0; x < nv; ++x)
+        mbar_wait(&v_full[x % kStages], (x / kStages) & 1, status);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      const bool leader = elect_one();
+      const uint32_t base16 = (smem_u32(smem) & 0x3FFFFu) >> 4;
+      auto scores = [&](uint32_t a, uint32_t b_off, uint32_t d, uint64_t* bar) {
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+          if (leader)
+            mma_bf16_ta(tbase + d, tbase + a + 8 * s,
+                        sdesc_at(base16, b_off + (s / 4) * kTile * 128 + (s % 4) * 32, 16, 1024, kSwizzle128B),
+                        idesc_bf16(128, 128, 0, 0), s > 0);
+        if (leader) mma_commit(bar);
+      };
+      auto issue_s = [&](uint32_t g) {
+        const uint32_t b = g % kStages;
+        if (!(ok = warp_wait(&k_full[b], (g / kStages) & 1, status))) return;
+        tc_fence_after();
+        scores(kTA, L::kK + b * L::kTileBytes, kTS, s_full);
+      };
+      auto issue_dp = [&](uint32_t g) {
+        const uint32_t b = g % kStages;
+        if (!(ok = warp_wait(&v_full[b], (g / kStages) & 1, status))) return;
+        tc_fence_after();
+        scores(kTB, L::kV + b * L::kTileBytes, kTP, dp_full);
+        if (leader) mma_commit(&v_empty[b]);
+      };
+      uint32_t units = 0;
+      for (uint32_t g = 0; more && ok; ++g) {
+        const bool first = S.first(), last = S.last();
+        const uint32_t b = g % kStages;
+        if (first) {
+          if (!(ok = warp_wait(q_ready, units++ & 1, status))) break;
+          tc_fence_after();
+          issue_s(g);
+          if (ok) issue_dp(g);
+          if (!ok) break;
+        }
+        if (!last) {
+          if (!(ok = warp_wait(s_free, g & 1, status))) break;
+          tc_fence_after();
+          issue_s(g + 1);
+          if (!ok) break;
+        }
+        if (!(ok = warp_wait(ds_ready, g & 1, status))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int s = 0; s < kTile / 16; ++s)
+          if (leader)
+            mma_bf16_ta(tbase + kTQ, tbase + kTP + (s < 4 ? 8 * s : 64 + 8 * (s - 4)),
+                        sdesc_at(base16, L::kK + b * L::kTileBytes + s * 2048, kTile * 128, 1024, kSwizzle128B),
+                        idesc_bf16(128, D, 0, 1), (!first || s > 0));
+        if (leader) {
+          mma_commit(&k_empty[b]);
+          if (last) mma_commit(acc_full);
+        }
+        if (!last) issue_dp(g + 1);
+        more = S.next(p, pv);
+      }
+      if (leader) {
+        mma_commit(drain);
+        mbar_wait(drain, 0, status);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ compute
+    setmaxnreg_inc<kRegCompute>();
+    const int w = (warp - 4) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane, tid = threadIdx.x - 128;
+    const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t s_addr = lane_base + kTS + 64 * w, dp_addr = lane_base + kTP + 64 * w;
+    float* tab = reinterpret_cast<float*>(smem + L::kBias);
+    const bool has_rel = BIAS && p.rel != nullptr;
+    ScoreHead H;
+    H.scale2 = p.scale * kLog2e;
+    H.zscale = CAP ? p.scale / p.cap : 0.f;
+    H.cap2 = p.cap * kLog2e;
+    H.slope2 = 0.f;
+    const float inv_cap2 = CAP ? 1.f / H.cap2 : 0.f;
+    int staged = -1;
+    bool ok = true;
+    float nl = 0.f, dv = 0.f;
+    int lo = 0, hi = 0;
+    QuerySteps S;
+    // The unit's A operands (warpgroup 0: Q, 1: dO; rows behind the document as zeros), LSE and D.
+    auto start_unit = [&]() {
+      const int qi = S.t * kTile + r;
+      const bool in = qi < S.len;
+      const int64_t tok = (int64_t)S.start + qi;
+      const uint4* src = reinterpret_cast<const uint4*>((w ? p.dout : p.q) + (tok * p.hq + S.h) * D);
+      uint32_t a[D / 2];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = in ? src[c] : make_uint4(0, 0, 0, 0);
+        a[4 * c] = x.x;
+        a[4 * c + 1] = x.y;
+        a[4 * c + 2] = x.z;
+        a[4 * c + 3] = x.w;
+      }
+      nl = in ? -p.lse[(int64_t)S.h * p.T + tok] * kLog2e : -INFINITY;
+      dv = in ? p.dvec[(int64_t)S.h * p.T + tok] : 0.f;
+      lo = p.win.left < 0 ? 0 : max(0, qi - p.win.left);
+      hi = p.win.right < 0 ? S.len - 1 : min(S.len - 1, qi + p.win.right);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        tmem_st32(lane_base + (w ? kTB : kTA) + 32 * c, reinterpret_cast<uint32_t(&)[32]>(a[32 * c]));
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(q_ready);
+    };
+    uint32_t g = 0, units = 0;
+    bool more = S.begin(p, pv);
+    if (more) start_unit();
+    for (; more; ++g) {
+      if constexpr (BIAS) {
+        if (S.first() && staged != S.h) {
+          if (p.slopes) H.slope2 = p.slopes[S.h] * kLog2e;
+          if (has_rel) {
+            named_bar_sync(1, 256);
+            stage_bias(tab, p.rel, p.R, S.h, tid, 256);
+            named_bar_sync(1, 256);
+          }
+          staged = S.h;
+        }
+      }
+      const int t = S.t, u = S.tile(), qi = t * kTile + r;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, g & 1, status));
+      if (ok) {
+        tc_fence_after();
+        uint32_t v[2][32], gr[2][32];
+        tmem_ld32(s_addr, v[0]);
+        tmem_ld32(s_addr + 32, v[1]);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(s_free);
+        TileBias B{};
+        if constexpr (BIAS) B = tile_bias(tab, has_rel, p.R, H.slope2, t, u, u * kTile + 64 * w - qi);
+        const bool masked = scored_masked(t, u, S.len, S.pre, p.win);
+        const int c0 = u * kTile + 64 * w;
+        const float2 f2 = make_float2(H.scale2, H.scale2), n2 = make_float2(nl, nl);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if constexpr (CAP) {
+            cap_chunk(v[c], H);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), inv_cap2));
+          }
+          if constexpr (BIAS) bias_chunk<1>(v[c], 32 * c, CAP ? 1.f : H.scale2, H.slope2, B);
+          if (masked) {
+            const uint32_t see = column_mask(lo - c0, hi - c0, S.pre - c0, 32 * c);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[c][j] = (see >> j) & 1 ? v[c][j] : 0xff800000u;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float2 e = (CAP || BIAS) ? fadd2(pair_of(v[c], j), n2) : ffma2(pair_of(v[c], j), f2, n2);
+            e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+            if constexpr (CAP) e = fmul2(e, pair_of(gr[c], j));
+            put_pair(v[c], j, e);
+          }
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(dp_full, g & 1, status));
+        if (ok) {
+          tc_fence_after();
+          const float2 d2 = make_float2(-dv, -dv);
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t dp[32];
+            tmem_ld32(dp_addr + 32 * c, dp);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 e = pair_of(v[c], j);
+              float2 a = fmul2(e, fadd2(pair_of(dp, j), d2));
+              if (masked) {     // a hidden pair's dP may be anything
+                a.x = e.x == 0.f ? 0.f : a.x;
+                a.y = e.y == 0.f ? 0.f : a.y;
+              }
+              pk[16 * c + j / 2] = pack2(a);
+            }
+          }
+          tmem_st32(dp_addr, pk);
+          tmem_st_wait();
+          if ((u + 1) * kTile > S.len) {       // keys behind the document: dQ sums over them
+            if (w == 0 && u * kTile + r >= S.len) clear_row<D>(smem + L::kK + (g % kStages) * L::kTileBytes, r);
+            fence_proxy_async_smem();
+          }
+          tc_fence_before();
+          mbar_arrive(ds_ready);
+        }
+      }
+      const bool last = S.last();
+      const int h = S.h;
+      const int64_t tok = (int64_t)S.start + qi;
+      const bool valid = qi < S.len;
+      more = S.next(p, pv);
+      if (last && ok) {
+        // every product that reads Q and dO of this unit has been waited for: the next unit's go in
+        // while its last dQ product runs
+        if (more) start_unit();
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, units++ & 1, status));
+        if (ok) {
+          tc_fence_after();
+          store_acc<D / 2>(lane_base + kTQ + w * (D / 2), p.dq + (tok * p.hq + h) * D + w * (D / 2), p.scale, valid);
+          tc_fence_before();
         }
       }
     }
   }
-  store_row<D>(p.dk + id * D, lane, dk, 1.f);
-  store_row<D>(p.dv + id * D, lane, dv, 1.f);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
 }
 
-inline unsigned blocks(int64_t rows) { return (unsigned)((rows + kWarps - 1) / kWarps); }
+// drel[h][i] = sum over the key tiles of their partial sums, in the plan's order.
+__global__ void scored_drel_kernel(const float* __restrict__ part, const int* __restrict__ plan, int R,
+                                   float* __restrict__ drel) {
+  const int width = 2 * R + 1, items = plan[kPlanBwdItems];
+  const int i = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y;
+  if (i >= width) return;
+  const float* src = part + (size_t)h * items * width + i;
+  float s = 0.f;
+  for (int n = 0; n < items; ++n) s += src[(size_t)n * width];
+  drel[(size_t)h * width + i] = s;
+}
 
-template <int D>
-cudaError_t bwd_d(const ScoredParams& p, cudaStream_t s) {
-  const int64_t rq = (int64_t)p.T * p.hq, rk = (int64_t)p.T * p.hkv;
-  if (p.drel) {
-    const cudaError_t e = cudaMemsetAsync(p.drel, 0, (size_t)p.hq * (2 * p.R + 1) * 4, s);
-    if (e != cudaSuccess) return e;
+template <int D, bool CAP, int BIAS>
+cudaError_t launch(const ScoredParams& p, cudaStream_t stream) {
+  CUtensorMap tq, tk, tv, tdo;
+  if (!make_tmap_bf16_3d(&tq, p.q, D, p.hq, p.T, D * 2, (uint64_t)p.hq * D * 2, 64, kTile) ||
+      !make_tmap_bf16_3d(&tk, p.k, D, p.hkv, p.T, D * 2, (uint64_t)p.hkv * D * 2, 64, kTile) ||
+      !make_tmap_bf16_3d(&tv, p.v, D, p.hkv, p.T, D * 2, (uint64_t)p.hkv * D * 2, 64, kTile) ||
+      !make_tmap_bf16_3d(&tdo, p.dout, D, p.hq, p.T, D * 2, (uint64_t)p.hq * D * 2, 64, kTile))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 0, regs1 = 0, regs2 = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  constexpr int smem1 = DkvSmem<D>::kAlloc, smem2 = DqSmem<D>::kAlloc;
+  static_assert(smem1 <= 232448 && smem2 <= 232448, "shared memory of one CTA");
+  if (e == cudaSuccess) e = prepare_kernel<scored_dkv_kernel<D, CAP, BIAS>>(smem1, &regs1);
+  if (e == cudaSuccess) e = prepare_kernel<scored_dq_kernel<D, CAP, BIAS != 0>>(smem2, &regs2);
+  if (e != cudaSuccess) return e;
+  if (regs1 != kLaunchRegs || regs2 != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  const int64_t tiles = (int64_t)p.T / kTile + p.N + 1, items = (int64_t)p.T / (kTile * kItemTiles) + p.N + 1;
+  constexpr int kRows = 256 / (D / 8);
+  const int64_t prep = (((int64_t)p.T + kRows - 1) / kRows) * p.hq;
+  if (tiles * p.hkv > 0x7FFFFFFF || items * 2 * p.hq > 0x7FFFFFFF || prep > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  scored_prep_kernel<D><<<(unsigned)prep, 256, 0, stream>>>(p);
+  const unsigned g1 = (unsigned)std::min<int64_t>(tiles * p.hkv, sms), g2 = (unsigned)std::min<int64_t>(items * 2 * p.hq, sms);
+  scored_dkv_kernel<D, CAP, BIAS><<<g1, kThreads, smem1, stream>>>(tq, tk, tv, tdo, p);
+  scored_dq_kernel<D, CAP, BIAS != 0><<<g2, kThreads, smem2, stream>>>(tk, tv, p);
+  if (BIAS == 2) {
+    const dim3 grid((2 * p.R + 1 + 63) / 64, p.hq);
+    scored_drel_kernel<<<grid, 64, 0, stream>>>(p.drel_part, p.plan, p.R, p.drel);
   }
-  scored_dvec_kernel<D><<<blocks(rq), kWarps * 32, 0, s>>>(p);
-  scored_dq_kernel<D><<<blocks(rq), kWarps * 32, 0, s>>>(p);
-  scored_dkv_kernel<D><<<blocks(rk), kWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
+}
+
+template <int D, bool CAP>
+cudaError_t launch_cap(const ScoredParams& p, cudaStream_t s) {
+  if (p.drel) return launch<D, CAP, 2>(p, s);
+  return p.slopes || p.rel ? launch<D, CAP, 1>(p, s) : launch<D, CAP, 0>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_scored_bwd(int D, const ScoredParams& p, cudaStream_t s) {
-  if ((int64_t)p.T * p.hq > 0x7fffffffLL * kWarps) return cudaErrorInvalidValue;
-  return D == 128 ? bwd_d<128>(p, s) : bwd_d<64>(p, s);
+  if (D == 128) return p.cap > 0.f ? launch_cap<128, true>(p, s) : launch_cap<128, false>(p, s);
+  return p.cap > 0.f ? launch_cap<64, true>(p, s) : launch_cap<64, false>(p, s);
 }
 
 }  // namespace flamia

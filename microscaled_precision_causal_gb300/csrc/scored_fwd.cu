@@ -65,7 +65,7 @@ __device__ __forceinline__ Unit make_unit(const ScoredParams& p, const PlanView&
   U.start = span.x;
   U.len = span.y;
   U.nt = (U.len + kTile - 1) / kTile;
-  U.pre = p.prefix ? min(max(p.prefix[item.x], 0), U.len) : 0;
+  U.pre = prefix_of(p, item.x, U.len);
   U.pre_tiles = (U.pre + kTile - 1) / kTile;
   U.klo0 = win_klo(U.t0, p.win);
   U.khi0 = win_khi(U.t0, U.nt, p.win);
@@ -73,14 +73,6 @@ __device__ __forceinline__ Unit make_unit(const ScoredParams& p, const PlanView&
   U.khi1 = win_khi(U.t0 + 1, U.nt, p.win);
   U.kt = key_tiles(U.t0, U.t0 + U.ntq - 1, U.nt, U.pre_tiles, p.win);
   return U;
-}
-
-// Unit number k of CTA c of G, or -1 (boustrophedon rounds over the cost-sorted list).
-__device__ __forceinline__ int unit_index(int k, int n_units) {
-  const int G = gridDim.x, c = blockIdx.x;
-  if ((int64_t)k * G >= n_units) return -1;
-  const int i = k * G + ((k & 1) ? G - 1 - c : c);
-  return i < n_units ? i : -1;
 }
 
 template <int D, bool CAP, bool BIAS>
@@ -370,19 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         if ((u + 1) * kTile > U.len) {
-          // V rows behind the document belong to the next one (or to nobody) and may hold anything:
-          // weight 0 does not silence an infinity, so they are cleared
           const uint32_t x = ring + 2 * k + 1, st = x % kSlots;
           ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[st], (x / kSlots) & 1, status));
           if (!ok) break;
-          if (u * kTile + r >= U.len) {
-#pragma unroll
-            for (int b = 0; b < D / 64; ++b) {
-              uint4* row = reinterpret_cast<uint4*>(smem + L::kKV + st * L::kTileBytes + b * kTile * 128 + r * 128);
-#pragma unroll
-              for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
-            }
-          }
+          if (u * kTile + r >= U.len) clear_row<D>(smem + L::kKV + st * L::kTileBytes, r);
           fence_proxy_async_smem();
         }
         tc_fence_before();
