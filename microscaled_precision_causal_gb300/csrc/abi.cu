@@ -169,7 +169,9 @@ ScoredParams scored_params(const void* q, const void* k, const void* v, const in
   p.T = (int)T;
   p.hq = hq;
   p.hkv = hkv;
-  p.scale = resolve_scale(scale, d);
+  const double sc = scale > 0.f ? (double)scale : 1.0 / std::sqrt((double)d);
+  p.scale = (float)sc;
+  p.scale2 = (float)(sc * 1.4426950408889634 * mma_gain(d));
   p.win = resolve_window(causal, o ? o->window_left : -1, o ? o->window_right : -1, T);
   if (o) {
     p.cap = o->softcap;

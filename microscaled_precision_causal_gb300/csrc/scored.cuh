@@ -12,6 +12,7 @@ struct ScoredParams {
   const int32_t* prefix;     // [N] or null
   int N, T, hq, hkv;
   float scale;               // softmax scale
+  float scale2;              // softmax scale log2 e, with the products' mean truncation taken back
   float cap;                 // 0: none
   const float* slopes;       // [hq] or null
   const float* rel;          // [hq, 2R+1] or null
@@ -41,6 +42,13 @@ inline ScoredBwdWorkspace scored_bwd_layout(int64_t T, int N, int hq, int R) {
   w.total = off > 0 ? off : 256;
   return w;
 }
+
+// The tensor core truncates as it accumulates, so a product of D terms comes out too small
+// by a part that does not depend on its size: measured on 65,536 rows of normal values
+// -9.9e-8 of the product at D = 128 (eight steps of 16 terms) and -5.5e-8 at D = 64, beside
+// a spread of 7e-8.  The score scale takes the mean back; it would enter every probability
+// with the score's own size as a factor.
+inline double mma_gain(int D) { return D == 128 ? 1.0 + 9.9e-8 : 1.0 + 5.5e-8; }
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -102,21 +110,22 @@ __device__ __forceinline__ void clear_row(uint8_t* tile, int r) {
 // ---------------------------------------------------------------- scores in base 2
 // The kernels hold u log2(e), so that the softmax is 2^x.
 //
-// tanh cap: y = cap tanh(z), z = s / cap.  Where every |z| of a warp's 32 columns is at
-// most kTanhPolyTo an odd polynomial of degree 11 gives tanh to 1.2e-7 (least squares,
-// reweighted towards equal ripple, on Chebyshev nodes of z^2); it runs on the fp32 pipe,
-// 4 packed instructions a pair.  Else tanh(z) = 1 - 2 / (1 + 2^(2 z log2 e)), to 2^-22
-// absolute, which costs two MUFU operations beside the softmax's own.
-constexpr float kTanhPolyTo = 0.875f;
+// tanh cap: y = cap tanh(z), z = s / cap.  Up to |z| = kTanhPolyTo, tanh(z) = z + z w Q(w)
+// with w = z^2 and Q of degree 4 (least squares in relative error, reweighted towards equal
+// ripple, on Chebyshev nodes of w: 6.5e-8, 1.4e-7 with the fp32 roundings), on the fp32 pipe
+// in packed pairs.  Beyond it tanh(z) = 1 - 2 / (1 + 2^(2 z log2 e)), which loses nothing
+// there but costs two MUFU operations beside the softmax's own; a warp takes that branch for
+// 32 columns when one of its values needs it.
+constexpr float kTanhPolyTo = 0.8f;
+// z w Q(w) / z = tanh(z) / z - 1.
 __device__ __forceinline__ float2 tanh_poly(float2 z) {
   const float2 w = fmul2(z, z);
   auto c = [](float x) { return make_float2(x, x); };
-  float2 p = ffma2(w, c(-0.0036076765973120928f), c(0.01778564415872097f));
-  p = ffma2(w, p, c(-0.05228739604353905f));
-  p = ffma2(w, p, c(0.13298341631889343f));
-  p = ffma2(w, p, c(-0.3333015441894531f));
-  p = ffma2(w, p, c(0.9999991655349731f));
-  return fmul2(z, p);
+  float2 p = ffma2(w, c(-0.004410882946103811f), c(0.01919075846672058f));
+  p = ffma2(w, p, c(-0.053176309913396835f));
+  p = ffma2(w, p, c(0.1332276612520218f));
+  p = ffma2(w, p, c(-0.3333286643028259f));
+  return fmul2(w, p);
 }
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
@@ -152,13 +161,23 @@ __device__ __forceinline__ void cap_chunk(uint32_t (&v)[32], const ScoreHead& H)
   float mx = 0.f;
 #pragma unroll
   for (int j = 0; j < 32; j += 2) mx = fmax3(mx, fabsf(__uint_as_float(v[j])), fabsf(__uint_as_float(v[j + 1])));
-  const float2 zs = make_float2(H.zscale, H.zscale), c2 = make_float2(H.cap2, H.cap2);
-  if (!__any_sync(0xffffffffu, !(mx * H.zscale <= kTanhPolyTo))) {
+  const float2 zs = make_float2(H.zscale, H.zscale), s2 = make_float2(H.scale2, H.scale2);
+  const bool big = __any_sync(0xffffffffu, !(mx * H.zscale <= kTanhPolyTo));
+  if (!big) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) put_pair(v, j, fmul2(tanh_poly(fmul2(pair_of(v, j), zs)), c2));
+    for (int j = 0; j < 32; j += 2) {
+      const float2 y = fmul2(pair_of(v, j), s2);
+      put_pair(v, j, ffma2(y, tanh_poly(fmul2(pair_of(v, j), zs)), y));
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(H.cap2 * tanh_any(__uint_as_float(v[j]) * H.zscale));
+    for (int j = 0; j < 32; j += 2) {
+      const float2 z = fmul2(pair_of(v, j), zs), y = fmul2(pair_of(v, j), s2);
+      float2 t = ffma2(y, tanh_poly(z), y);
+      if (!(fabsf(z.x) <= kTanhPolyTo)) t.x = H.cap2 * tanh_any(z.x);
+      if (!(fabsf(z.y) <= kTanhPolyTo)) t.y = H.cap2 * tanh_any(z.y);
+      put_pair(v, j, t);
+    }
   }
 }
 // x f + bias for columns c0 .. c0 + 31 (distance rel0 + DIR * column).

@@ -66,6 +66,12 @@ __global__ void __launch_bounds__(256) scored_prep_kernel(const ScoredParams p) 
   if (in && sub == 0) p.dvec[(int64_t)h * p.T + t] = s;
 }
 
+// a + (the part that a's last digits lost) += x.
+__device__ __forceinline__ void add_comp(float& a, float& lost, float x) {
+  const float s = __fadd_rn(a, x), b = __fsub_rn(s, a);
+  lost = __fadd_rn(lost, __fadd_rn(__fsub_rn(a, __fsub_rn(s, b)), __fsub_rn(x, b)));
+  a = s;
+}
 // One row of D / 2 fp32 accumulators (columns c0 ..) -> bf16 in global memory, times f.
 template <int COLS>
 __device__ __forceinline__ void store_acc(uint32_t taddr, __nv_bfloat16* dst, float f, bool valid) {
@@ -361,13 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool has_rel = BIAS && p.rel != nullptr;
     const int R = p.R;
     ScoreHead H;
-    H.scale2 = p.scale * kLog2e;
+    H.scale2 = p.scale2;
     H.zscale = CAP ? p.scale / p.cap : 0.f;
     H.cap2 = p.cap * kLog2e;
     H.slope2 = 0.f;
     const float inv_cap2 = CAP ? 1.f / H.cap2 : 0.f;
     int staged = -1, buf = 0;
-    float far_lo = 0.f, far_hi = 0.f;
+    float far_lo = 0.f, far_hi = 0.f, lost_lo = 0.f, lost_hi = 0.f;
     bool ok = true;
     KeySteps S;
     // a warp whose wait ran out goes on through the steps without work: it still meets the others
@@ -388,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (BIAS == 2 && S.head_first()) {
           for (int i = tid; i < 2 * R + 1; i += 256) acc[i] = 0.f;
-          far_lo = far_hi = 0.f;
+          far_lo = far_hi = lost_lo = lost_hi = 0.f;
           named_bar_sync(1, 256);
         }
       }
@@ -512,9 +518,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (BIAS == 2) {
         const int tile_rel = (U.u - t) * kTile;
         if (tile_rel + kTile - 1 <= -R) {
-          far_lo += du_lo;
+          add_comp(far_lo, lost_lo, du_lo);
         } else if (tile_rel - (kTile - 1) >= R) {
-          far_hi += du_lo;
+          add_comp(far_hi, lost_hi, du_lo);
         } else {
           // sums along the diagonals: a running value moves one lane up per column, so it stays on its
           // diagonal; lane 31's is complete
@@ -539,8 +545,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (at >= 0 && at < 95) s += dg[q * 96 + at];
             }
             const int rel = tile_rel + x;
-            if (rel <= -R) far_lo += s;
-            else if (rel >= R) far_hi += s;
+            if (rel <= -R) add_comp(far_lo, lost_lo, s);
+            else if (rel >= R) add_comp(far_hi, lost_hi, s);
             else acc[rel + R] += s;
           }
           buf ^= 1;
@@ -548,6 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (S.head_last()) {
           // the head's sums of this key tile: the two ends over all threads in a fixed order
           float* red = reinterpret_cast<float*>(smem + L::kDiag) + buf * (8 * 96);
+          far_lo += lost_lo;
+          far_hi += lost_hi;
 #pragma unroll
           for (int o = 16; o; o >>= 1) {
             far_lo += __shfl_xor_sync(0xffffffffu, far_lo, o);
@@ -788,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* tab = reinterpret_cast<float*>(smem + L::kBias);
     const bool has_rel = BIAS && p.rel != nullptr;
     ScoreHead H;
-    H.scale2 = p.scale * kLog2e;
+    H.scale2 = p.scale2;
     H.zscale = CAP ? p.scale / p.cap : 0.f;
     H.cap2 = p.cap * kLog2e;
     H.slope2 = 0.f;
@@ -932,16 +940,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// drel[h][i] = sum over the key tiles of their partial sums, in the plan's order.
-__global__ void scored_drel_kernel(const float* __restrict__ part, const int* __restrict__ plan, int R,
-                                   float* __restrict__ drel) {
-  const int width = 2 * R + 1, items = plan[kPlanBwdItems];
-  const int i = blockIdx.x * blockDim.x + threadIdx.x, h = blockIdx.y;
-  if (i >= width) return;
-  const float* src = part + (size_t)h * items * width + i;
-  float s = 0.f;
-  for (int n = 0; n < items; ++n) s += src[(size_t)n * width];
-  drel[(size_t)h * width + i] = s;
+// drel[h][i] = sum over the key tiles of their partial sums: a warp per eighth of the tiles,
+// in 64 bits (a chain of hundreds of fp32 sums would cost the last digits), then the warps' in order.
+__global__ void __launch_bounds__(256) scored_drel_kernel(const float* __restrict__ part, const int* __restrict__ plan,
+                                                          int R, float* __restrict__ drel) {
+  __shared__ double sums[8][32];
+  const int width = 2 * R + 1, items = plan[kPlanBwdItems], h = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+  double s = 0.0;
+  if (i < width) {
+    const float* src = part + (size_t)h * items * width + i;
+#pragma unroll 4
+    for (int n = warp; n < items; n += 8) s += (double)src[(size_t)n * width];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && i < width) {
+    for (int q = 1; q < 8; ++q) s += sums[q][lane];
+    drel[(size_t)h * width + i] = (float)s;
+  }
 }
 
 template <int D, bool CAP, int BIAS>
@@ -970,8 +987,8 @@ cudaError_t launch(const ScoredParams& p, cudaStream_t stream) {
   scored_dkv_kernel<D, CAP, BIAS><<<g1, kThreads, smem1, stream>>>(tq, tk, tv, tdo, p);
   scored_dq_kernel<D, CAP, BIAS != 0><<<g2, kThreads, smem2, stream>>>(tk, tv, p);
   if (BIAS == 2) {
-    const dim3 grid((2 * p.R + 1 + 63) / 64, p.hq);
-    scored_drel_kernel<<<grid, 64, 0, stream>>>(p.drel_part, p.plan, p.R, p.drel);
+    const dim3 grid((2 * p.R + 1 + 31) / 32, p.hq);
+    scored_drel_kernel<<<grid, 256, 0, stream>>>(p.drel_part, p.plan, p.R, p.drel);
   }
   return cudaGetLastError();
 }

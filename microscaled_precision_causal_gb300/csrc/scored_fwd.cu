@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int staged = -1;
     bool ok = true;
     ScoreHead H;
-    H.scale2 = p.scale * kLog2e;
+    H.scale2 = p.scale2;
     H.zscale = CAP ? p.scale / p.cap : 0.f;
     H.cap2 = p.cap * kLog2e;
     H.slope2 = 0.f;
