@@ -136,18 +136,20 @@ __device__ __forceinline__ float tanh_any(float z) {
   return fmaf(-2.f, fast_rcp(1.f + fast_exp2(z * (2.f * kLog2e))), 1.f);
 }
 
-// Constants of one query head, and how the bias enters one tile.
+// Constants of a call.
 struct ScoreHead {
   float scale2;     // softmax scale log2 e
   float zscale;     // softmax scale / cap
   float cap2;       // cap log2 e
-  float slope2;     // slope log2 e (0: none)
 };
+// A tile's bias is a function of the distance: near the diagonal (some distance below R, or
+// both signs of it) a value per distance from a staged table; elsewhere a constant, or with a
+// slope a constant and a multiple of the column, which is staged too.
 struct TileBias {
-  const float* tab; // table entry of the thread's column 0, or null: the constant c
-  float c;
-  float rel0;       // distance (key - query) at the thread's column 0
-  float sl;         // bias per unit of distance; 0: none, NaN: both signs occur in the tile
+  const float* tab; // table entry of the thread's column 0, or null
+  const float* col; // the slope's part of columns 0 .. 127, or null
+  float c;          // the rest, added in the exponent
+  __device__ __forceinline__ bool plain() const { return !tab && !col; }
 };
 __device__ __forceinline__ float2 pair_of(const uint32_t (&v)[32], int j) {
   return make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
@@ -158,9 +160,13 @@ __device__ __forceinline__ void put_pair(uint32_t (&v)[32], int j, float2 x) {
 }
 // 32 raw products -> cap log2 e tanh(s / cap).
 __device__ __forceinline__ void cap_chunk(uint32_t (&v)[32], const ScoreHead& H) {
-  float mx = 0.f;
+  float ma = 0.f, mb = 0.f;
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) mx = fmax3(mx, fabsf(__uint_as_float(v[j])), fabsf(__uint_as_float(v[j + 1])));
+  for (int j = 0; j < 32; j += 4) {
+    ma = fmax3(ma, fabsf(__uint_as_float(v[j])), fabsf(__uint_as_float(v[j + 1])));
+    mb = fmax3(mb, fabsf(__uint_as_float(v[j + 2])), fabsf(__uint_as_float(v[j + 3])));
+  }
+  const float mx = fmaxf(ma, mb);
   const float2 zs = make_float2(H.zscale, H.zscale), s2 = make_float2(H.scale2, H.scale2);
   const bool big = __any_sync(0xffffffffu, !(mx * H.zscale <= kTanhPolyTo));
   if (!big) {
@@ -180,67 +186,77 @@ __device__ __forceinline__ void cap_chunk(uint32_t (&v)[32], const ScoreHead& H)
     }
   }
 }
-// x f + bias for columns c0 .. c0 + 31 (distance rel0 + DIR * column).
+// x f + the table's or the slope's part for columns c0 .. c0 + 31 (column c: distance DIR c more).
 template <int DIR>
-__device__ __forceinline__ void bias_chunk(uint32_t (&v)[32], int c0, float f, float slope2, const TileBias& B) {
+__device__ __forceinline__ void bias_chunk(uint32_t (&v)[32], int c0, float f, const TileBias& B) {
   const float2 f2 = make_float2(f, f);
   if (B.tab) {
     const float* tab = B.tab + DIR * c0;
 #pragma unroll
     for (int j = 0; j < 32; j += 2) put_pair(v, j, ffma2(pair_of(v, j), f2, make_float2(tab[DIR * j], tab[DIR * (j + 1)])));
-  } else {
-    const float2 b2 = make_float2(B.c, B.c);
+  } else if (B.col) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) put_pair(v, j, ffma2(pair_of(v, j), f2, b2));
-  }
-  if (B.sl != 0.f) {
-    const float r0 = B.rel0 + (float)(DIR * c0);
-    if (B.sl == B.sl) {
-      const float2 s2 = make_float2(B.sl, B.sl), r2 = make_float2(r0, r0);
-#pragma unroll
-      for (int j = 0; j < 32; j += 2)
-        put_pair(v, j, ffma2(fadd2(r2, make_float2((float)(DIR * j), (float)(DIR * (j + 1)))), s2, pair_of(v, j)));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        v[j] = __float_as_uint(fmaf(fabsf(r0 + (float)(DIR * j)), -slope2, __uint_as_float(v[j])));
+    for (int j = 0; j < 32; j += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(B.col + c0 + j);
+      put_pair(v, j, ffma2(pair_of(v, j), f2, make_float2(b.x, b.y)));
+      put_pair(v, j + 2, ffma2(pair_of(v, j + 2), f2, make_float2(b.z, b.w)));
     }
   }
 }
-// 32 raw products of columns c0 .. c0 + 31 -> u log2 e.  Without CAP and BIAS the raw
-// products stay: the caller's exponent scales them.
-template <bool CAP, bool BIAS, int DIR>
-__device__ __forceinline__ void score_chunk(uint32_t (&v)[32], int c0, const ScoreHead& H, const TileBias& B) {
-  if constexpr (CAP) cap_chunk(v, H);
-  if constexpr (BIAS) bias_chunk<DIR>(v, c0, CAP ? 1.f : H.scale2, H.slope2, B);
-}
 
-// Staged bias of one head: entry r + R + 255 holds the bias of distance r log2 e, clipped
-// to R on both sides and long enough for every tile that holds a distance below R, so that
-// no index is clipped in the loops.
+// Staged bias of one head in base 2: entry r + R + 255 of the table holds the bias of distance
+// r, clipped to R on both sides and long enough for every tile that holds a distance below R,
+// so that no index is clipped in the loops.  Without a bias by distance R counts as 1: the
+// table then serves the tiles on the diagonal, where a slope's sign changes.
+// Before it: the slope times column (128), and its negative (128).
 constexpr int kBiasReach = 2 * kTile - 1;
-constexpr int kBiasTab = 2 * (FLAMIA_REL_MAX + kBiasReach) + 1;
+constexpr int kBiasTab = 2 * kTile + 2 * (FLAMIA_REL_MAX + kBiasReach) + 2;
 __device__ __forceinline__ float bias_base2(float b) {
   return b < kHideBelow ? -INFINITY : fminf(b, -kHideBelow) * kLog2e;
 }
-__device__ __forceinline__ void stage_bias(float* tab, const float* rel, int R, int h, int first, int stride) {
-  const float* src = rel + (size_t)h * (2 * R + 1);
-  for (int i = first; i < 2 * (R + kBiasReach) + 1; i += stride)
-    tab[i] = bias_base2(src[min(max(i - kBiasReach, 0), 2 * R)]);
+__device__ __forceinline__ int bias_range(const ScoredParams& p) { return p.rel ? p.R : 1; }
+__device__ __forceinline__ float head_slope2(const ScoredParams& p, int h) {
+  return p.slopes ? p.slopes[h] * kLog2e : 0.f;
+}
+__device__ __forceinline__ void stage_bias(float* buf, const ScoredParams& p, int h, int first, int stride) {
+  const int R = bias_range(p);
+  const float slope2 = head_slope2(p, h);
+  const float* src = p.rel ? p.rel + (size_t)h * (2 * R + 1) : nullptr;
+  for (int i = first; i < 2 * kTile; i += stride) buf[i] = slope2 * (float)(i < kTile ? i : kTile - i);
+  for (int i = first; i < 2 * (R + kBiasReach) + 1; i += stride) {
+    const float b = src ? bias_base2(src[min(max(i - kBiasReach, 0), 2 * R)]) : 0.f;
+    buf[2 * kTile + i] = fmaf(fabsf((float)(i - R - kBiasReach)), -slope2, b);
+  }
+}
+struct HeadBias {
+  float slope2, lo, hi;      // slope, and the bias of the distances up to -R and from R on
+};
+__device__ __forceinline__ HeadBias head_bias(const ScoredParams& p, int h) {
+  HeadBias H;
+  H.slope2 = head_slope2(p, h);
+  H.lo = p.rel ? bias_base2(p.rel[(size_t)h * (2 * p.R + 1)]) : 0.f;
+  H.hi = p.rel ? bias_base2(p.rel[(size_t)h * (2 * p.R + 1) + 2 * p.R]) : 0.f;
+  return H;
 }
 // The bias of query tile t x key tile u for the thread whose column 0 has distance rel0.
-__device__ __forceinline__ TileBias tile_bias(const float* tab, bool has_rel, int R, float slope2, int t, int u, int rel0) {
+template <int DIR>
+__device__ __forceinline__ TileBias tile_bias(const float* buf, const HeadBias& H, int R, int t, int u, int rel0) {
   const int rmax = (u - t) * kTile + kTile - 1, rmin = (u - t) * kTile - (kTile - 1);
+  const float* tab = buf + 2 * kTile;
   TileBias B;
-  B.tab = nullptr;
+  B.tab = B.col = nullptr;
   B.c = 0.f;
-  B.rel0 = (float)rel0;
-  if (has_rel) {
-    if (rmax <= -R) B.c = tab[0];
-    else if (rmin >= R) B.c = tab[2 * (R + kBiasReach)];
-    else B.tab = tab + rel0 + R + kBiasReach;
+  if (rmax > -R && rmin < R) {
+    B.tab = tab + rel0 + R + kBiasReach;
+    return B;
   }
-  B.sl = slope2 == 0.f ? 0.f : (rmax <= 0 ? slope2 : (rmin >= 0 ? -slope2 : __int_as_float(0x7fffffff)));
+  const bool low = rmax <= -R;
+  B.c = low ? H.lo : H.hi;
+  if (H.slope2 != 0.f) {
+    const float sl = low ? H.slope2 : -H.slope2;      // bias per unit of distance
+    B.c = fmaf(sl, (float)rel0, B.c);
+    B.col = buf + ((low == (DIR > 0)) ? 0 : kTile);
+  }
   return B;
 }
 

@@ -130,7 +130,7 @@ struct DkvSmem {
   static constexpr int kDO = 4 * kTileBytes;                   // [2]
   static constexpr int kStat = 6 * kTileBytes;                 // [kStats][-LSE log2 e 128, D 128]
   static constexpr int kBias = kStat + kStats * 1024;          // [kBiasTab]
-  static constexpr int kAcc = kBias + (kBiasTab + 1) * 4;      // [2 R + 1] drel of the current head
+  static constexpr int kAcc = kBias + kBiasTab * 4;      // [2 R + 1] drel of the current head
   static constexpr int kDiag = kAcc + (2 * FLAMIA_REL_MAX + 2) * 4;   // [2][8 warps][96]
   static constexpr int kBar = (kDiag + 2 * 8 * 96 * 4 + 15) & ~15;
   static constexpr int kBytes = kBar + 256;
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     setmaxnreg_dec<kRegCtl>();
-    KeySteps S;
+    KeySteps S{};
     bool more = S.begin(p, pv), ok = true;
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- producer
@@ -364,18 +364,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = lane_base + kTS + 64 * w, dp_addr = lane_base + kTP + 64 * w;
     float* tab = reinterpret_cast<float*>(smem + L::kBias);
     float* acc = reinterpret_cast<float*>(smem + L::kAcc);
-    const bool has_rel = BIAS && p.rel != nullptr;
-    const int R = p.R;
+    const int R = bias_range(p);
+    HeadBias HB{};
     ScoreHead H;
     H.scale2 = p.scale2;
     H.zscale = CAP ? p.scale / p.cap : 0.f;
     H.cap2 = p.cap * kLog2e;
-    H.slope2 = 0.f;
     const float inv_cap2 = CAP ? 1.f / H.cap2 : 0.f;
     int staged = -1, buf = 0;
     float far_lo = 0.f, far_hi = 0.f, lost_lo = 0.f, lost_hi = 0.f;
     bool ok = true;
-    KeySteps S;
+    KeySteps S{};
     // a warp whose wait ran out goes on through the steps without work: it still meets the others
     // at the barriers
     uint32_t g = 0;
@@ -384,12 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = S.t, kj = U.u * kTile + r;
       if constexpr (BIAS != 0) {
         if (S.head_first() && staged != S.h) {
-          if (p.slopes) H.slope2 = p.slopes[S.h] * kLog2e;
-          if (has_rel) {
-            named_bar_sync(1, 256);
-            stage_bias(tab, p.rel, R, S.h, tid, 256);
-            named_bar_sync(1, 256);
-          }
+          HB = head_bias(p, S.h);
+          named_bar_sync(1, 256);
+          stage_bias(tab, p, S.h, tid, 256);
+          named_bar_sync(1, 256);
           staged = S.h;
         }
         if (BIAS == 2 && S.head_first()) {
@@ -412,7 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         uint32_t gr[2][32];
         TileBias B{};
-        if constexpr (BIAS != 0) B = tile_bias(tab, has_rel, R, H.slope2, t, U.u, kj - (t * kTile + 64 * w));
+        if constexpr (BIAS != 0) B = tile_bias<-1>(tab, HB, R, t, U.u, kj - (t * kTile + 64 * w));
+        const bool plain = !BIAS || B.plain();
+        const float f = (CAP || !plain) ? 1.f : H.scale2;     // products still raw: scaled in the exponent
         const bool masked = scored_masked(t, U.u, U.len, U.pre, p.win) || (t + 1) * kTile > U.len;
         int lo = 0, hi = U.len - 1;
         if (kj >= U.len) {
@@ -431,24 +430,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), inv_cap2));
           }
-          if constexpr (BIAS != 0) bias_chunk<-1>(v[c], 32 * c, CAP ? 1.f : H.scale2, H.slope2, B);
+          if constexpr (BIAS != 0) bias_chunk<-1>(v[c], 32 * c, CAP ? 1.f : H.scale2, B);
           if (masked) {
             const uint32_t see = column_mask(lo, hi, 0, 32 * c);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[c][j] = (see >> j) & 1 ? v[c][j] : 0xff800000u;
           }
-          const float2 f2 = make_float2(H.scale2, H.scale2);
+          const float2 f2 = make_float2(f, f), c2 = make_float2(B.c, B.c);
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 n4 = *reinterpret_cast<const float4*>(nl + 32 * c + j);
             float2 e0 = make_float2(n4.x, n4.y), e1 = make_float2(n4.z, n4.w);
-            if constexpr (CAP || BIAS != 0) {
-              e0 = fadd2(pair_of(v[c], j), e0);
-              e1 = fadd2(pair_of(v[c], j + 2), e1);
-            } else {
-              e0 = ffma2(pair_of(v[c], j), f2, e0);
-              e1 = ffma2(pair_of(v[c], j + 2), f2, e1);
+            if constexpr (BIAS != 0) {
+              e0 = fadd2(e0, c2);
+              e1 = fadd2(e1, c2);
             }
+            e0 = ffma2(pair_of(v[c], j), f2, e0);
+            e1 = ffma2(pair_of(v[c], j + 2), f2, e1);
             e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
             e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
             pk[16 * c + j / 2] = pack2(e0);
@@ -704,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     setmaxnreg_dec<kRegCtl>();
-    QuerySteps S;
+    QuerySteps S{};
     bool more = S.begin(p, pv), ok = true;
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- producer
@@ -794,18 +792,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_addr = lane_base + kTS + 64 * w, dp_addr = lane_base + kTP + 64 * w;
     float* tab = reinterpret_cast<float*>(smem + L::kBias);
-    const bool has_rel = BIAS && p.rel != nullptr;
+    const int R = bias_range(p);
+    HeadBias HB{};
     ScoreHead H;
     H.scale2 = p.scale2;
     H.zscale = CAP ? p.scale / p.cap : 0.f;
     H.cap2 = p.cap * kLog2e;
-    H.slope2 = 0.f;
     const float inv_cap2 = CAP ? 1.f / H.cap2 : 0.f;
     int staged = -1;
     bool ok = true;
     float nl = 0.f, dv = 0.f;
     int lo = 0, hi = 0;
-    QuerySteps S;
+    QuerySteps S{};
     // The unit's A operands (warpgroup 0: Q, 1: dO; rows behind the document as zeros), LSE and D.
     auto start_unit = [&]() {
       const int qi = S.t * kTile + r;
@@ -838,12 +836,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; more; ++g) {
       if constexpr (BIAS) {
         if (S.first() && staged != S.h) {
-          if (p.slopes) H.slope2 = p.slopes[S.h] * kLog2e;
-          if (has_rel) {
-            named_bar_sync(1, 256);
-            stage_bias(tab, p.rel, p.R, S.h, tid, 256);
-            named_bar_sync(1, 256);
-          }
+          HB = head_bias(p, S.h);
+          named_bar_sync(1, 256);
+          stage_bias(tab, p, S.h, tid, 256);
+          named_bar_sync(1, 256);
           staged = S.h;
         }
       }
@@ -858,10 +854,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(s_free);
         TileBias B{};
-        if constexpr (BIAS) B = tile_bias(tab, has_rel, p.R, H.slope2, t, u, u * kTile + 64 * w - qi);
+        if constexpr (BIAS) B = tile_bias<1>(tab, HB, R, t, u, u * kTile + 64 * w - qi);
+        const bool plain = !BIAS || B.plain();
+        const float f = (CAP || !plain) ? 1.f : H.scale2;
         const bool masked = scored_masked(t, u, S.len, S.pre, p.win);
         const int c0 = u * kTile + 64 * w;
-        const float2 f2 = make_float2(H.scale2, H.scale2), n2 = make_float2(nl, nl);
+        const float2 f2 = make_float2(f, f), n2 = make_float2(nl + B.c, nl + B.c);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           if constexpr (CAP) {
@@ -869,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), inv_cap2));
           }
-          if constexpr (BIAS) bias_chunk<1>(v[c], 32 * c, CAP ? 1.f : H.scale2, H.slope2, B);
+          if constexpr (BIAS) bias_chunk<1>(v[c], 32 * c, CAP ? 1.f : H.scale2, B);
           if (masked) {
             const uint32_t see = column_mask(lo - c0, hi - c0, S.pre - c0, 32 * c);
 #pragma unroll
@@ -877,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            float2 e = (CAP || BIAS) ? fadd2(pair_of(v[c], j), n2) : ffma2(pair_of(v[c], j), f2, n2);
+            float2 e = ffma2(pair_of(v[c], j), f2, n2);
             e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
             if constexpr (CAP) e = fmul2(e, pair_of(gr[c], j));
             put_pair(v[c], j, e);

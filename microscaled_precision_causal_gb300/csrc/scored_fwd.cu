@@ -16,7 +16,11 @@
 // they outgrow it by more than 8 (in base 2): until then p stays below 2^8, which bf16 and
 // the fp32 sums hold as exactly, and O needs no rescaling pass.
 //
-// TMEM columns: S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 [256, 256 + D), O_1 [384, ...).
+// TMEM columns: S_0 [0, 128), S_1 [128, 256), O_0 [256, 256 + D), O_1 [256 + D, 256 + 2 D).  At
+// D = 128 that is all of it and P_w takes the first half of S_w's columns.  At D = 64 the
+// P_w have columns of their own behind O (split): the next scores are then ready before the
+// softmax asks for them, which matters there because two products of a tile take half as
+// long and the exponentials bound the kernel.
 #include "ptx.cuh"
 #include "scored.cuh"
 #include "tmap.h"
@@ -87,10 +91,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = bars;                  // [2]
   uint64_t* q_empty = bars + 2;             // [2]
   uint64_t* s_full = bars + 4;              // [2]
-  uint64_t* p_full = bars + 6;              // [2]
-  uint64_t* o_full = bars + 8;              // [2]
-  uint64_t* drain = bars + 10;
-  uint64_t* kv_full = bars + 11;            // [kSlots]
+  uint64_t* o_full = bars + 6;              // [2]
+  uint64_t* s_free = bars + 8;              // [2] (split)
+  uint64_t* p_full = bars + 10;             // [2 query tiles][2 halves of 64 keys]
+  uint64_t* drain = bars + 14;
+  uint64_t* kv_full = bars + 15;            // [kSlots]
   uint64_t* kv_empty = kv_full + kSlots;    // [kSlots]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + kSlots);
   int* status = const_cast<int*>(p.plan) + kPlanStatus;
@@ -103,8 +108,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
+      mbar_init(&s_free[i], 128);
+      mbar_init(&p_full[2 * i], 128);
+      mbar_init(&p_full[2 * i + 1], 128);
     }
     mbar_init(drain, 1);
     for (int i = 0; i < kSlots; ++i) {
@@ -124,6 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  constexpr bool kSplit = D == 64;
+  constexpr uint32_t kO = 256, kP = 384;
 
   if (warp < 4) {
     setmaxnreg_dec<kRegCtl>();
@@ -162,87 +171,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- MMA issuer
       const bool leader = elect_one();
       const uint32_t base16 = (smem_u32(smem) & 0x3FFFFu) >> 4;
-      uint32_t ring = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+      uint32_t ring = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0, ns0 = 0, ns1 = 0;
       bool ok = true;
-      auto issue_s = [&](int w, uint32_t st) {
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s / 4) * kTile * 128 + (s % 4) * 32;
-          if (leader)
-            mma_bf16(tbase + w * 128, sdesc_at(base16, L::kQ + w * L::kTileBytes + off, 16, 1024, kSwizzle128B),
-                     sdesc_at(base16, L::kKV + st * L::kTileBytes + off, 16, 1024, kSwizzle128B),
-                     idesc_bf16(128, 128, 0, 0), s > 0);
-        }
-        if (leader) mma_commit(&s_full[w]);
-      };
-      auto issue_pv = [&](int w, uint32_t st, bool first) {
-#pragma unroll
-        for (int s = 0; s < kTile / 16; ++s)
-          if (leader)
-            mma_bf16_ta(tbase + 256 + w * 128, tbase + w * 128 + s * 8,
-                        sdesc_at(base16, L::kKV + st * L::kTileBytes + s * 2048, kTile * 128, 1024, kSwizzle128B),
-                        idesc_bf16(128, D, 0, 1), (!first || s > 0));
-      };
       for (int n = 0; ok; ++n) {
         const int i = unit_index(n, n_units);
         if (i < 0) break;
         const Unit U = make_unit(p, pv, i);
         const int nk = U.kt.n;
-        int last[2], first[2] = {-1, -1};        // a tile's last and first key tile, as a place in the list
+        int first0 = -1, first1 = -1, last0 = nk - 1, last1 = nk - 1;      // places in the list of key tiles
+        while (last0 >= 0 && !U.sees(0, last0)) --last0;
+        while (last1 >= 0 && !U.sees(1, last1)) --last1;
+        // S of query tile w and key tile k (whose K is in the ring's slot st)
+        auto scores = [&](int w, int k, uint32_t st) {
+          int& first = w ? first1 : first0;
+          if (first < 0) {
+            first = k;
+            if (!(ok = warp_wait(&q_full[w], (w ? nq1++ : nq0++) & 1, status))) return;
+          }
+          if (kSplit) {                            // the last scores have been read
+            uint32_t& ns = w ? ns1 : ns0;
+            if (ns && !(ok = warp_wait(&s_free[w], (ns - 1) & 1, status))) return;
+            ++ns;
+          }
+          tc_fence_after();
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          last[w] = nk - 1;
-          while (last[w] >= 0 && !U.sees(w, last[w])) --last[w];
-        }
-        auto scores = [&](int k) {               // S of key tile k for every query tile that sees it
-          const uint32_t x = ring + 2 * k, st = x % kSlots;
-          if (!(ok = warp_wait(&kv_full[st], (x / kSlots) & 1, status))) return;
-          tc_fence_after();
-          for (int w = 0; w < U.ntq; ++w) {
-            if (!U.sees(w, k)) continue;
-            if (first[w] < 0) {
-              first[w] = k;
-              if (!(ok = warp_wait(&q_full[w], nq[w]++ & 1, status))) return;
-              tc_fence_after();
-            }
-            issue_s(w, st);
-            if (k == last[w] && leader) mma_commit(&q_empty[w]);
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = (s / 4) * kTile * 128 + (s % 4) * 32;
+            if (leader)
+              mma_bf16(tbase + w * 128, sdesc_at(base16, L::kQ + w * L::kTileBytes + off, 16, 1024, kSwizzle128B),
+                       sdesc_at(base16, L::kKV + st * L::kTileBytes + off, 16, 1024, kSwizzle128B),
+                       idesc_bf16(128, 128, 0, 0), s > 0);
           }
-          if (leader) mma_commit(&kv_empty[st]);
-        };
-        auto values = [&](int w, int k) {
-          if (!(ok = warp_wait(&p_full[w], np[w]++ & 1, status))) return;
-          const uint32_t x = ring + 2 * k + 1, st = x % kSlots;
-          if (!(ok = warp_wait(&kv_full[st], (x / kSlots) & 1, status))) return;
-          tc_fence_after();
-          issue_pv(w, st, k == first[w]);
-          if (k == last[w] && leader) mma_commit(&o_full[w]);
-        };
-        scores(0);
-        for (int k = 0; k < nk && ok; ++k) {
-          // PV of each query tile, its next scores right behind it (the other tile's softmax runs meanwhile)
-          const uint32_t xk = ring + 2 * (k + 1), sk = xk % kSlots;
-          bool loaded = false;
-          for (int w = 0; w < U.ntq && ok; ++w) {
-            if (U.sees(w, k)) values(w, k);
-            if (!ok || k + 1 >= nk || !U.sees(w, k + 1)) continue;
-            if (!loaded) {
-              if (!(ok = warp_wait(&kv_full[sk], (xk / kSlots) & 1, status))) break;
-              tc_fence_after();
-              loaded = true;
-            }
-            if (first[w] < 0) {
-              first[w] = k + 1;
-              if (!(ok = warp_wait(&q_full[w], nq[w]++ & 1, status))) break;
-              tc_fence_after();
-            }
-            issue_s(w, sk);
-            if (k + 1 == last[w] && leader) mma_commit(&q_empty[w]);
-          }
-          if (!ok) break;
           if (leader) {
-            mma_commit(&kv_empty[(ring + 2 * k + 1) % kSlots]);
-            if (k + 1 < nk) mma_commit(&kv_empty[sk]);
+            mma_commit(&s_full[w]);
+            if (k == (w ? last1 : last0)) mma_commit(&q_empty[w]);
+          }
+        };
+        // O += P V, half of the keys at a time as the softmax hands them in
+        auto values = [&](int w, int k, uint32_t st) {
+          const uint32_t par = (w ? np1++ : np0++) & 1;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = warp_wait(&p_full[2 * w + half], par, status))) return;
+            tc_fence_after();
+#pragma unroll
+            for (int s = 4 * half; s < 4 * half + 4; ++s)
+              if (leader)
+                mma_bf16_ta(tbase + kO + w * D, tbase + (kSplit ? kP + 64 * w : 128 * w) + s * 8,
+                            sdesc_at(base16, L::kKV + st * L::kTileBytes + s * 2048, kTile * 128, 1024, kSwizzle128B),
+                            idesc_bf16(128, D, 0, 1), (k != (w ? first1 : first0) || s > 0));
+          }
+          if (leader && (kSplit || k == (w ? last1 : last0))) mma_commit(&o_full[w]);
+        };
+        auto landed = [&](uint32_t x) { return ok = warp_wait(&kv_full[x % kSlots], (x / kSlots) & 1, status); };
+        if (!landed(ring)) break;
+        for (int w = 0; w < 2 && ok; ++w)
+          if (U.sees(w, 0)) scores(w, 0, ring % kSlots);
+        if (!ok) break;
+        if (leader) mma_commit(&kv_empty[ring % kSlots]);
+        for (int k = 0; k < nk && ok; ++k) {
+          const uint32_t xv = ring + 2 * k + 1, xk = xv + 1;
+          const bool more = k + 1 < nk;
+          if (kSplit && more) {
+            if (!landed(xk)) break;
+            for (int w = 0; w < 2 && ok; ++w)
+              if (U.sees(w, k + 1)) scores(w, k + 1, xk % kSlots);
+            if (!ok) break;
+            if (leader) mma_commit(&kv_empty[xk % kSlots]);
+          }
+          if (!landed(xv)) break;
+          for (int w = 0; w < 2 && ok; ++w) {
+            if (U.sees(w, k)) values(w, k, xv % kSlots);
+            // its next scores go over P, right behind its product; the other tile's softmax runs meanwhile
+            if (!kSplit && ok && more && U.sees(w, k + 1) && landed(xk)) scores(w, k + 1, xk % kSlots);
+          }
+          if (ok && leader) {
+            mma_commit(&kv_empty[xv % kSlots]);
+            if (!kSplit && more) mma_commit(&kv_empty[xk % kSlots]);
           }
         }
         ring += 2 * nk;
@@ -259,9 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t s_addr = lane_base + w * 128, o_addr = lane_base + 256 + w * 128;
+    const uint32_t s_addr = lane_base + w * 128, o_addr = lane_base + kO + w * D;
+    const uint32_t p_addr = kSplit ? lane_base + kP + 64 * w : s_addr;
     float* tab = reinterpret_cast<float*>(smem + L::kBias) + w * kBiasTab;
-    const bool has_rel = BIAS && p.rel != nullptr;
+    const int R = bias_range(p);
     uint32_t ring = 0, ns = 0, no = 0;
     int staged = -1;
     bool ok = true;
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     H.scale2 = p.scale2;
     H.zscale = CAP ? p.scale / p.cap : 0.f;
     H.cap2 = p.cap * kLog2e;
-    H.slope2 = 0.f;
+    HeadBias HB{};
     // a warp whose wait ran out goes on through the units without work: it still meets its
     // warpgroup at the barriers around the bias
     for (int n = 0;; ++n) {
@@ -277,10 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i < 0) break;
       const Unit U = make_unit(p, pv, i);
       if constexpr (BIAS) {
-        if (p.slopes) H.slope2 = p.slopes[U.h] * kLog2e;
-        if (has_rel && staged != U.h) {      // each warpgroup has a table: the two need not meet
+        if (staged != U.h) {      // each warpgroup has a table: the two need not meet
+          HB = head_bias(p, U.h);
           named_bar_sync(1 + w, 128);
-          stage_bias(tab, p.rel, p.R, U.h, r, 128);
+          stage_bias(tab, p, U.h, r, 128);
           named_bar_sync(1 + w, 128);
           staged = U.h;
         }
@@ -290,40 +296,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lo = p.win.left < 0 ? 0 : max(0, qi - p.win.left);
       const int hi = p.win.right < 0 ? U.len - 1 : min(U.len - 1, qi + p.win.right);
       float m = -INFINITY;
-      float2 l2 = make_float2(0.f, 0.f);
+      float2 la = make_float2(0.f, 0.f), lb = la;
       bool first = true;
       for (int k = 0; k < U.kt.n; ++k) {
         if (!U.sees(w, k)) continue;
         const int u = U.kt.tile(k);
+        TileBias B{};
+        if constexpr (BIAS) B = tile_bias<1>(tab, HB, R, t, u, u * kTile - qi);
+        const bool masked = scored_masked(t, u, U.len, U.pre, p.win);
+        const bool plain = !BIAS || B.plain();
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[w], ns++ & 1, status));
         if (!ok) break;
         tc_fence_after();
         uint32_t v[4][32];
+        float cm[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) tmem_ld32(s_addr + 32 * g, v[g]);
+        for (int g = 0; g < 4; ++g) tmem_ld32_max(s_addr + 32 * g, v[g], cm[g]);
         tmem_ld_wait();
-        TileBias B{};
-        if constexpr (BIAS) B = tile_bias(tab, has_rel, p.R, H.slope2, t, u, u * kTile - qi);
+        if (kSplit) {
+          tc_fence_before();
+          mbar_arrive(&s_free[w]);
+        }
+        // products still raw (no cap, no bias but a constant): scaled in the exponent
+        const float f = (CAP || !plain) ? 1.f : H.scale2;
+        if constexpr (CAP) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) score_chunk<CAP, BIAS, 1>(v[g], 32 * g, H, B);
-        if (scored_masked(t, u, U.len, U.pre, p.win)) {
-          const int c = u * kTile;
+          for (int g = 0; g < 4; ++g) cap_chunk(v[g], H);
+        }
+        if constexpr (BIAS) {
+          if (!plain) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t see = column_mask(lo - c, hi - c, U.pre - c, 32 * g);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[g][j] = (see >> j) & 1 ? v[g][j] : 0xff800000u;
+            for (int g = 0; g < 4; ++g) bias_chunk<1>(v[g], 32 * g, CAP ? 1.f : H.scale2, B);
           }
         }
-        float mx = -INFINITY;
+        float mx;
+        if (masked || !plain) {
+          if (masked) {
+            const int c = u * kTile;
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+            for (int g = 0; g < 4; ++g) {
+              const uint32_t see = column_mask(lo - c, hi - c, U.pre - c, 32 * g);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[g][j] = (see >> j) & 1 ? v[g][j] : 0xff800000u;
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) cm[g] = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 32; j += 2)
-            mx = fmax3(mx, __uint_as_float(v[g][j]), __uint_as_float(v[g][j + 1]));
-        // without cap and bias the products are still raw: scale (positive) them in the exponent
-        const float f = (CAP || BIAS) ? 1.f : H.scale2;
-        mx *= f;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) cm[g] = fmax3(cm[g], __uint_as_float(v[g][j]), __uint_as_float(v[g][j + 1]));
+          mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);
+        } else {
+          mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);      // the load's own maximum of the raw products
+          if constexpr (CAP) mx = H.cap2 * tanh_any(mx * H.zscale);      // monotone
+        }
+        mx = fmaf(mx, f, B.c);
+        if (kSplit && !first) {          // the last P has been read, O is whole
+          ok = __all_sync(0xffffffffu, mbar_wait(&o_full[w], no++ & 1, status));
+          if (!ok) break;
+          tc_fence_after();
+        }
         if (first) {
           m = mx;
           first = false;
@@ -340,27 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(o_addr + 32 * c, o);
           }
           tmem_st_wait();
-          l2 = fmul2(l2, make_float2(alpha, alpha));
+          la = fmul2(la, make_float2(alpha, alpha));
+          lb = fmul2(lb, make_float2(alpha, alpha));
           m = m_new;
         }
-        const float neg = m == -INFINITY ? 0.f : -m;
-        const float2 f2 = make_float2(f, f), n2 = make_float2(neg, neg);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int j = 0; j < 64; j += 2) {
-            const float2 s2 = make_float2(__uint_as_float(v[2 * half + j / 32][j % 32]),
-                                          __uint_as_float(v[2 * half + j / 32][j % 32 + 1]));
-            float2 e = (CAP || BIAS) ? fadd2(s2, n2) : ffma2(s2, f2, n2);
-            e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-            l2 = fadd2(l2, e);
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(e.x, e.y);
-            pk[j / 2] = *reinterpret_cast<const uint32_t*>(&b2);
-          }
-          tmem_st32(s_addr + 32 * half, pk);
-        }
-        tmem_st_wait();
         if ((u + 1) * kTile > U.len) {
           const uint32_t x = ring + 2 * k + 1, st = x % kSlots;
           ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[st], (x / kSlots) & 1, status));
@@ -368,15 +384,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (u * kTile + r >= U.len) clear_row<D>(smem + L::kKV + st * L::kTileBytes, r);
           fence_proxy_async_smem();
         }
-        tc_fence_before();
-        mbar_arrive(&p_full[w]);
+        const float neg = (m == -INFINITY ? 0.f : -m) + B.c;
+        const float2 f2 = make_float2(f, f), n2 = make_float2(neg, neg);
+        // P in two halves of 64 keys: the first one's product starts while the second is computed
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int j = 0; j < 64; j += 4) {
+            const int g = 2 * half + j / 32, c = j % 32;
+            float2 e0 = ffma2(pair_of(v[g], c), f2, n2), e1 = ffma2(pair_of(v[g], c + 2), f2, n2);
+            e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
+            e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
+            la = fadd2(la, e0);
+            lb = fadd2(lb, e1);
+            const __nv_bfloat162 b0 = __floats2bfloat162_rn(e0.x, e0.y), b1 = __floats2bfloat162_rn(e1.x, e1.y);
+            pk[j / 2] = *reinterpret_cast<const uint32_t*>(&b0);
+            pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&b1);
+          }
+          tmem_st32(p_addr + 32 * half, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[2 * w + half]);
+        }
       }
       ring += 2 * U.kt.n;
       if (!ok || w >= U.ntq) continue;
       ok = __all_sync(0xffffffffu, mbar_wait(&o_full[w], no++ & 1, status));
       if (!ok) continue;
       tc_fence_after();
-      const float l = l2.x + l2.y;
+      const float l = (la.x + la.y) + (lb.x + lb.y);
       const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);     // a row that sees nothing: O = 0
       const bool al32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
       const bool row_valid = qi < U.len;
