@@ -157,6 +157,11 @@ int check_score_opts(const flamia_score_options* o) {
   return FLAMIA_OK;
 }
 
+// A scale whose square or reciprocal leaves the fp32 range has no use.
+int check_score_scale(float s) {
+  return s > 0.f && (s < 7.8886091e-31f || s > 1.2676506e30f) ? FLAMIA_ERR_UNSUPPORTED : FLAMIA_OK;   // 2^-100 .. 2^100
+}
+
 ScoredParams scored_params(const void* q, const void* k, const void* v, const int32_t* cu, int N, int64_t T, int hq,
                            int hkv, int d, int causal, float scale, const flamia_score_options* o, const void* plan) {
   ScoredParams p{};
@@ -175,6 +180,7 @@ ScoredParams scored_params(const void* q, const void* k, const void* v, const in
   p.win = resolve_window(causal, o ? o->window_left : -1, o ? o->window_right : -1, T);
   if (o) {
     p.cap = o->softcap;
+    p.capf = cap_form(sc * mma_gain(d), (double)o->softcap);
     p.slopes = o->slopes;
     p.rel = o->rel_bias;
     p.R = o->rel_bias ? o->rel_max : 0;
@@ -415,6 +421,7 @@ int flamia_scored_fwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
   int rc = check_common(total_tokens, num_seqs, cu_seqlens, plan);
   if (!rc) rc = check_heads(hq, hkv, head_dim);
   if (!rc) rc = check_score_opts(opt);
+  if (!rc) rc = check_score_scale(softmax_scale);
   if (rc) return rc;
   if (causal != 0 && causal != 1) return FLAMIA_ERR_INVALID_ARG;
   if (!q_bf16 || !k_bf16 || !v_bf16 || !out_bf16 || !lse) return FLAMIA_ERR_INVALID_ARG;
@@ -444,6 +451,7 @@ int flamia_scored_bwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
   int rc = check_common(total_tokens, num_seqs, cu_seqlens, plan);
   if (!rc) rc = check_heads(hq, hkv, head_dim);
   if (!rc) rc = check_score_opts(opt);
+  if (!rc) rc = check_score_scale(softmax_scale);
   if (rc) return rc;
   if (causal != 0 && causal != 1) return FLAMIA_ERR_INVALID_ARG;
   if (!q_bf16 || !k_bf16 || !v_bf16 || !out_bf16 || !lse || !dout_bf16 || !dq_bf16 || !dk_bf16 || !dv_bf16 || !workspace)

@@ -5,6 +5,15 @@
 
 namespace flamia {
 
+// tanh cap of raw products S (s = softmax scale S): S (1 + t) with t = tanh(z) / z - 1 and
+// z = zscale S, the capped score over the softmax scale.
+struct CapForm {
+  float zscale;      // softmax scale / cap
+  float inv;         // cap / softmax scale
+  float t3, t5;      // up to this |S| the polynomials of 3 and of 5 coefficients serve (0: never)
+  float k3[3], k5[5];     // their coefficients of S^2, S^4, ...
+};
+
 struct ScoredParams {
   const __nv_bfloat16 *q, *k, *v;
   const int32_t* cu;
@@ -14,6 +23,7 @@ struct ScoredParams {
   float scale;               // softmax scale
   float scale2;              // softmax scale log2 e, with the products' mean truncation taken back
   float cap;                 // 0: none
+  CapForm capf;
   const float* slopes;       // [hq] or null
   const float* rel;          // [hq, 2R+1] or null
   int R;
@@ -73,10 +83,28 @@ __device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int nt, int pre_ti
   s.n = s.a + hi - s.lo + 1;
   return s;
 }
-// True when some key of key tile u is hidden from a query of tile t or lies outside the document.
-__device__ __forceinline__ bool scored_masked(int t, int u, int len, int pre, Window w) {
-  if ((u + 1) * kTile > len) return true;
-  return (u + 1) * kTile > pre && win_masked(t, u, len, w);
+// Key tiles that every query of query tile t sees whole: those below pre, and [lo, hi].
+struct FullTiles {
+  int pre, lo, hi;
+  __device__ __forceinline__ bool has(int u) const { return u < pre || (u >= lo && u <= hi); }
+};
+__device__ __forceinline__ FullTiles full_tiles(int t, int len, int pre, Window w) {
+  FullTiles f;
+  f.pre = pre / kTile;                       // pre <= len
+  f.lo = w.left < 0 ? 0 : max(0, t * kTile + 2 * kTile - 2 - w.left) / kTile;
+  f.hi = len / kTile - 1;
+  if (w.right >= 0) f.hi = min(f.hi, (t * kTile + w.right + 1) / kTile - 1);
+  return f;
+}
+// Query tiles of which every query sees key tile u whole: [lo, hi] (whole query tiles only).
+__device__ __forceinline__ int2 full_queries(int u, int len, int pre, Window w) {
+  int lo = 0, hi = len / kTile - 1;
+  if ((u + 1) * kTile > len) hi = -1;
+  if ((u + 1) * kTile > pre) {
+    if (w.right >= 0) lo = max(0, u * kTile + 2 * kTile - 2 - w.right) / kTile;
+    if (w.left >= 0) hi = min(hi, u * kTile + w.left >= kTile - 1 ? (u * kTile + w.left - (kTile - 1)) / kTile : -1);
+  }
+  return make_int2(lo, hi);
 }
 // Bits of 32 columns starting at column c0: the columns [lo, hi] and those below pre.
 __device__ __forceinline__ uint32_t below_mask(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u); }
@@ -110,22 +138,33 @@ __device__ __forceinline__ void clear_row(uint8_t* tile, int r) {
 // ---------------------------------------------------------------- scores in base 2
 // The kernels hold u log2(e), so that the softmax is 2^x.
 //
-// tanh cap: y = cap tanh(z), z = s / cap.  Up to |z| = kTanhPolyTo, tanh(z) = z + z w Q(w)
-// with w = z^2 and Q of degree 4 (least squares in relative error, reweighted towards equal
-// ripple, on Chebyshev nodes of w: 6.5e-8, 1.4e-7 with the fp32 roundings), on the fp32 pipe
-// in packed pairs.  Beyond it tanh(z) = 1 - 2 / (1 + 2^(2 z log2 e)), which loses nothing
-// there but costs two MUFU operations beside the softmax's own; a warp takes that branch for
-// 32 columns when one of its values needs it.
-constexpr float kTanhPolyTo = 0.8f;
-// z w Q(w) / z = tanh(z) / z - 1.
-__device__ __forceinline__ float2 tanh_poly(float2 z) {
-  const float2 w = fmul2(z, z);
-  auto c = [](float x) { return make_float2(x, x); };
-  float2 p = ffma2(w, c(-0.004410882946103811f), c(0.01919075846672058f));
-  p = ffma2(w, p, c(-0.053176309913396835f));
-  p = ffma2(w, p, c(0.1332276612520218f));
-  p = ffma2(w, p, c(-0.3333286643028259f));
-  return fmul2(w, p);
+// tanh cap.  tanh(z) / z - 1 = w Q(w), w = z^2, by least squares in relative error reweighted
+// towards equal ripple on Chebyshev nodes of w: three coefficients up to |z| = 0.375 (7e-8),
+// five up to 0.8 (6.5e-8), each with zscale folded in, so that a capped product costs n + 2
+// packed fp32 operations and stays in the products' units.  The fp32 pipe bounds this (one
+// operation an element is 128 cycles a tile, a tile's two products at D = 128 are 1024), so a
+// warp takes the shorter form when all its values allow it.  Beyond 0.8, tanh(z) = 1 - 2 /
+// (1 + 2^(2 z log2 e)), which loses nothing there.
+constexpr float kTanh3To = 0.375f, kTanh5To = 0.8f;
+constexpr float kTanh3[3] = {-0.33332332968711853f, 0.1328972578048706f, -0.048487283289432526f};
+constexpr float kTanh5a = -0.3333286643028259f, kTanh5b = 0.1332276612520218f, kTanh5c = -0.053176309913396835f,
+                kTanh5d = 0.01919075846672058f, kTanh5e = -0.004410882946103811f;
+inline CapForm cap_form(double scale, double cap) {
+  CapForm c{};
+  if (!(cap > 0.0)) return c;
+  const double z = scale / cap;
+  c.zscale = (float)z;
+  c.inv = (float)(cap / scale);
+  // the folded coefficients have to stay inside the fp32 range
+  c.t3 = z > 1e-6 && z < 1e6 ? (float)(kTanh3To / z) : 0.f;
+  c.t5 = z > 3e-4 && z < 1e3 ? (float)(kTanh5To / z) : 0.f;
+  const float k5[5] = {kTanh5a, kTanh5b, kTanh5c, kTanh5d, kTanh5e};
+  double f = z * z;
+  for (int i = 0; i < 5; ++i, f *= z * z) {
+    if (i < 3) c.k3[i] = (float)(kTanh3[i] * f);
+    c.k5[i] = (float)(k5[i] * f);
+  }
+  return c;
 }
 __device__ __forceinline__ float fast_rcp(float x) {
   float y;
@@ -136,20 +175,15 @@ __device__ __forceinline__ float tanh_any(float z) {
   return fmaf(-2.f, fast_rcp(1.f + fast_exp2(z * (2.f * kLog2e))), 1.f);
 }
 
-// Constants of a call.
-struct ScoreHead {
-  float scale2;     // softmax scale log2 e
-  float zscale;     // softmax scale / cap
-  float cap2;       // cap log2 e
-};
 // A tile's bias is a function of the distance: near the diagonal (some distance below R, or
 // both signs of it) a value per distance from a staged table; elsewhere a constant, or with a
-// slope a constant and a multiple of the column, which is staged too.
+// slope a constant and a multiple of the column.
 struct TileBias {
   const float* tab; // table entry of the thread's column 0, or null
-  const float* col; // the slope's part of columns 0 .. 127, or null
+  float col;        // the slope's part per unit of distance, in the products' units
   float c;          // the rest, added in the exponent
-  __device__ __forceinline__ bool plain() const { return !tab && !col; }
+  __device__ __forceinline__ bool plain() const { return !tab && col == 0.f; }
+  __device__ __forceinline__ float factor(float scale2) const { return tab ? 1.f : scale2; }
 };
 __device__ __forceinline__ float2 pair_of(const uint32_t (&v)[32], int j) {
   return make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
@@ -158,49 +192,67 @@ __device__ __forceinline__ void put_pair(uint32_t (&v)[32], int j, float2 x) {
   v[j] = __float_as_uint(x.x);
   v[j + 1] = __float_as_uint(x.y);
 }
-// 32 raw products -> cap log2 e tanh(s / cap).
-__device__ __forceinline__ void cap_chunk(uint32_t (&v)[32], const ScoreHead& H) {
-  float ma = 0.f, mb = 0.f;
+// A group of N x 32 raw products -> capped, in the same units.
+template <int N>
+__device__ __forceinline__ void cap_products(uint32_t (&v)[N][32], const CapForm& F) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    ma = fmax3(ma, fabsf(__uint_as_float(v[j])), fabsf(__uint_as_float(v[j + 1])));
-    mb = fmax3(mb, fabsf(__uint_as_float(v[j + 2])), fabsf(__uint_as_float(v[j + 3])));
-  }
-  const float mx = fmaxf(ma, mb);
-  const float2 zs = make_float2(H.zscale, H.zscale), s2 = make_float2(H.scale2, H.scale2);
-  const bool big = __any_sync(0xffffffffu, !(mx * H.zscale <= kTanhPolyTo));
-  if (!big) {
+  for (int g = 0; g < N; ++g)
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const float2 y = fmul2(pair_of(v, j), s2);
-      put_pair(v, j, ffma2(y, tanh_poly(fmul2(pair_of(v, j), zs)), y));
-    }
+    for (int j = 0; j < 32; j += 2)
+      m[(j / 2) % 4] = fmax3(m[(j / 2) % 4], fabsf(__uint_as_float(v[g][j])), fabsf(__uint_as_float(v[g][j + 1])));
+  const float am = fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
+  auto c = [](float x) { return make_float2(x, x); };
+  if (!__any_sync(0xffffffffu, !(am <= F.t3))) {
+#pragma unroll
+    for (int g = 0; g < N; ++g)
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float2 x = pair_of(v[g], j), w = fmul2(x, x);
+        float2 t = ffma2(w, c(F.k3[2]), c(F.k3[1]));
+        t = ffma2(w, t, c(F.k3[0]));
+        put_pair(v[g], j, ffma2(x, fmul2(w, t), x));
+      }
+  } else if (!__any_sync(0xffffffffu, !(am <= F.t5))) {
+#pragma unroll
+    for (int g = 0; g < N; ++g)
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float2 x = pair_of(v[g], j), w = fmul2(x, x);
+        float2 t = ffma2(w, c(F.k5[4]), c(F.k5[3]));
+        t = ffma2(w, t, c(F.k5[2]));
+        t = ffma2(w, t, c(F.k5[1]));
+        t = ffma2(w, t, c(F.k5[0]));
+        put_pair(v[g], j, ffma2(x, fmul2(w, t), x));
+      }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const float2 z = fmul2(pair_of(v, j), zs), y = fmul2(pair_of(v, j), s2);
-      float2 t = ffma2(y, tanh_poly(z), y);
-      if (!(fabsf(z.x) <= kTanhPolyTo)) t.x = H.cap2 * tanh_any(z.x);
-      if (!(fabsf(z.y) <= kTanhPolyTo)) t.y = H.cap2 * tanh_any(z.y);
-      put_pair(v, j, t);
-    }
+    for (int g = 0; g < N; ++g)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float x = __uint_as_float(v[g][j]), z = x * F.zscale, w = z * z;
+        float t = fmaf(w, kTanh5e, kTanh5d);
+        t = fmaf(w, t, kTanh5c);
+        t = fmaf(w, t, kTanh5b);
+        t = fmaf(w, t, kTanh5a);
+        v[g][j] = __float_as_uint(fabsf(z) <= kTanh5To ? fmaf(x, w * t, x) : F.inv * tanh_any(z));
+      }
   }
 }
-// x f + the table's or the slope's part for columns c0 .. c0 + 31 (column c: distance DIR c more).
+// The table's or the slope's part for columns c0 .. c0 + 31 (column c: distance DIR c more);
+// with a table the result is in base 2, else the products' units stay.
 template <int DIR>
-__device__ __forceinline__ void bias_chunk(uint32_t (&v)[32], int c0, float f, const TileBias& B) {
-  const float2 f2 = make_float2(f, f);
+__device__ __forceinline__ void bias_chunk(uint32_t (&v)[32], int c0, float scale2, const TileBias& B) {
   if (B.tab) {
+    const float2 f2 = make_float2(scale2, scale2);
     const float* tab = B.tab + DIR * c0;
 #pragma unroll
     for (int j = 0; j < 32; j += 2) put_pair(v, j, ffma2(pair_of(v, j), f2, make_float2(tab[DIR * j], tab[DIR * (j + 1)])));
-  } else if (B.col) {
+  } else if (B.col != 0.f) {
+    const float2 s2 = make_float2(B.col, B.col);
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const float4 b = *reinterpret_cast<const float4*>(B.col + c0 + j);
-      put_pair(v, j, ffma2(pair_of(v, j), f2, make_float2(b.x, b.y)));
-      put_pair(v, j + 2, ffma2(pair_of(v, j + 2), f2, make_float2(b.z, b.w)));
-    }
+    for (int j = 0; j < 32; j += 2)
+      put_pair(v, j, ffma2(make_float2((float)(DIR * (c0 + j)), (float)(DIR * (c0 + j + 1))), s2, pair_of(v, j)));
   }
 }
 
@@ -208,9 +260,8 @@ __device__ __forceinline__ void bias_chunk(uint32_t (&v)[32], int c0, float f, c
 // r, clipped to R on both sides and long enough for every tile that holds a distance below R,
 // so that no index is clipped in the loops.  Without a bias by distance R counts as 1: the
 // table then serves the tiles on the diagonal, where a slope's sign changes.
-// Before it: the slope times column (128), and its negative (128).
 constexpr int kBiasReach = 2 * kTile - 1;
-constexpr int kBiasTab = 2 * kTile + 2 * (FLAMIA_REL_MAX + kBiasReach) + 2;
+constexpr int kBiasTab = 2 * (FLAMIA_REL_MAX + kBiasReach) + 2;
 __device__ __forceinline__ float bias_base2(float b) {
   return b < kHideBelow ? -INFINITY : fminf(b, -kHideBelow) * kLog2e;
 }
@@ -222,10 +273,9 @@ __device__ __forceinline__ void stage_bias(float* buf, const ScoredParams& p, in
   const int R = bias_range(p);
   const float slope2 = head_slope2(p, h);
   const float* src = p.rel ? p.rel + (size_t)h * (2 * R + 1) : nullptr;
-  for (int i = first; i < 2 * kTile; i += stride) buf[i] = slope2 * (float)(i < kTile ? i : kTile - i);
   for (int i = first; i < 2 * (R + kBiasReach) + 1; i += stride) {
     const float b = src ? bias_base2(src[min(max(i - kBiasReach, 0), 2 * R)]) : 0.f;
-    buf[2 * kTile + i] = fmaf(fabsf((float)(i - R - kBiasReach)), -slope2, b);
+    buf[i] = fmaf(fabsf((float)(i - R - kBiasReach)), -slope2, b);
   }
 }
 struct HeadBias {
@@ -238,25 +288,17 @@ __device__ __forceinline__ HeadBias head_bias(const ScoredParams& p, int h) {
   H.hi = p.rel ? bias_base2(p.rel[(size_t)h * (2 * p.R + 1) + 2 * p.R]) : 0.f;
   return H;
 }
+// Key tiles closer to the query tile than this hold a distance below R.
+__device__ __forceinline__ int near_tiles(int R) { return (R + kTile - 2) / kTile; }
 // The bias of query tile t x key tile u for the thread whose column 0 has distance rel0.
-template <int DIR>
-__device__ __forceinline__ TileBias tile_bias(const float* buf, const HeadBias& H, int R, int t, int u, int rel0) {
-  const int rmax = (u - t) * kTile + kTile - 1, rmin = (u - t) * kTile - (kTile - 1);
-  const float* tab = buf + 2 * kTile;
+__device__ __forceinline__ TileBias tile_bias(const float* tab, const HeadBias& H, int R, int near, float inv_scale2, int t,
+                                              int u, int rel0) {
   TileBias B;
-  B.tab = B.col = nullptr;
-  B.c = 0.f;
-  if (rmax > -R && rmin < R) {
-    B.tab = tab + rel0 + R + kBiasReach;
-    return B;
-  }
-  const bool low = rmax <= -R;
-  B.c = low ? H.lo : H.hi;
-  if (H.slope2 != 0.f) {
-    const float sl = low ? H.slope2 : -H.slope2;      // bias per unit of distance
-    B.c = fmaf(sl, (float)rel0, B.c);
-    B.col = buf + ((low == (DIR > 0)) ? 0 : kTile);
-  }
+  const bool low = u < t;
+  const float sl = low ? H.slope2 : -H.slope2;      // bias per unit of distance
+  B.tab = abs(u - t) <= near ? tab + rel0 + R + kBiasReach : nullptr;
+  B.c = B.tab ? 0.f : fmaf(sl, (float)rel0, low ? H.lo : H.hi);
+  B.col = sl * inv_scale2;
   return B;
 }
 

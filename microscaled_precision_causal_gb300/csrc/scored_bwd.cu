@@ -99,9 +99,9 @@ __device__ __forceinline__ uint32_t pack2(float2 x) {
   const __nv_bfloat162 b2 = __floats2bfloat162_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&b2);
 }
-// 1 - tanh^2 from the capped score y = cap log2 e tanh.
-__device__ __forceinline__ float2 cap_slope(float2 y, float inv_cap2) {
-  const float2 t = fmul2(y, make_float2(inv_cap2, inv_cap2));
+// 1 - tanh^2 from the capped product y = tanh / zscale.
+__device__ __forceinline__ float2 cap_slope(float2 y, float zscale) {
+  const float2 t = fmul2(y, make_float2(zscale, zscale));
   return ffma2(t, make_float2(-t.x, -t.y), make_float2(1.f, 1.f));
 }
 
@@ -139,18 +139,26 @@ struct DkvSmem {
 
 struct KeyUnit {
   int item, hk, u, start, len, nt, pre, tlo, nq;
+  int2 full;                // query tiles that see the key tile whole
 };
-__device__ __forceinline__ KeyUnit key_unit(const ScoredParams& p, const PlanView& pv, int i) {
+// What a unit's first loads bring; fetched a unit ahead, so that their latency is not met.
+struct RawUnit {
+  int i;
+  int4 item;
+  int2 span;
+};
+__device__ __forceinline__ KeyUnit key_unit(const ScoredParams& p, const RawUnit& raw) {
   KeyUnit U;
-  U.item = i / p.hkv;
-  U.hk = i % p.hkv;
-  const int4 item = pv.bwd_items[U.item];
-  const int2 span = pv.bwd_span[U.item];
+  U.item = raw.i / p.hkv;
+  U.hk = raw.i % p.hkv;
+  const int4 item = raw.item;
+  const int2 span = raw.span;
   U.u = item.y;
   U.start = span.x;
   U.len = span.y;
   U.nt = (U.len + kTile - 1) / kTile;
   U.pre = prefix_of(p, item.x, U.len);
+  U.full = full_queries(U.u, U.len, U.pre, p.win);
   const bool all = U.u * kTile < U.pre;        // every query of the document sees a prefix key
   U.tlo = all ? 0 : win_tlo(U.u, p.win);
   U.nq = (all ? U.nt - 1 : win_thi(U.u, U.nt, p.win)) - U.tlo + 1;
@@ -161,11 +169,18 @@ __device__ __forceinline__ KeyUnit key_unit(const ScoredParams& p, const PlanVie
 struct KeySteps {
   int n, n_units, group;
   KeyUnit U;
+  RawUnit raw;              // the next unit's
   int h, t;                 // the step's query head and query tile
+  __device__ __forceinline__ void fetch(const ScoredParams& p, const PlanView& pv, int k) {
+    raw.i = unit_index(k, n_units);
+    if (raw.i < 0) return;
+    raw.item = pv.bwd_items[raw.i / p.hkv];
+    raw.span = pv.bwd_span[raw.i / p.hkv];
+  }
   __device__ __forceinline__ bool unit(const ScoredParams& p, const PlanView& pv) {
-    const int i = unit_index(n, n_units);
-    if (i < 0) return false;
-    U = key_unit(p, pv, i);
+    if (raw.i < 0) return false;
+    U = key_unit(p, raw);
+    fetch(p, pv, n + 1);
     h = U.hk * group;
     t = U.tlo;
     return true;
@@ -174,6 +189,7 @@ struct KeySteps {
     n = 0;
     n_units = p.plan[kPlanBwdItems] * p.hkv;
     group = p.hq / p.hkv;
+    fetch(p, pv, 0);
     return unit(p, pv);
   }
   __device__ __forceinline__ bool head_first() const { return t == U.tlo; }
@@ -365,12 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* tab = reinterpret_cast<float*>(smem + L::kBias);
     float* acc = reinterpret_cast<float*>(smem + L::kAcc);
     const int R = bias_range(p);
+    const int near = near_tiles(R);
+    const float scale2 = p.scale2, inv_scale2 = 1.f / p.scale2;
     HeadBias HB{};
-    ScoreHead H;
-    H.scale2 = p.scale2;
-    H.zscale = CAP ? p.scale / p.cap : 0.f;
-    H.cap2 = p.cap * kLog2e;
-    const float inv_cap2 = CAP ? 1.f / H.cap2 : 0.f;
     int staged = -1, buf = 0;
     float far_lo = 0.f, far_hi = 0.f, lost_lo = 0.f, lost_hi = 0.f;
     bool ok = true;
@@ -409,10 +422,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         uint32_t gr[2][32];
         TileBias B{};
-        if constexpr (BIAS != 0) B = tile_bias<-1>(tab, HB, R, t, U.u, kj - (t * kTile + 64 * w));
-        const bool plain = !BIAS || B.plain();
-        const float f = (CAP || !plain) ? 1.f : H.scale2;     // products still raw: scaled in the exponent
-        const bool masked = scored_masked(t, U.u, U.len, U.pre, p.win) || (t + 1) * kTile > U.len;
+        if constexpr (BIAS != 0) B = tile_bias(tab, HB, R, near, inv_scale2, t, U.u, kj - (t * kTile + 64 * w));
+        const float f = BIAS != 0 ? B.factor(scale2) : scale2;
+        const bool masked = t < U.full.x || t > U.full.y;
+        if constexpr (CAP) {
+          cap_products(v, p.capf);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), p.capf.zscale));
+        }
         int lo = 0, hi = U.len - 1;
         if (kj >= U.len) {
           hi = -1;
@@ -425,12 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pk[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if constexpr (CAP) {
-            cap_chunk(v[c], H);
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), inv_cap2));
-          }
-          if constexpr (BIAS != 0) bias_chunk<-1>(v[c], 32 * c, CAP ? 1.f : H.scale2, B);
+          if constexpr (BIAS != 0) bias_chunk<-1>(v[c], 32 * c, scale2, B);
           if (masked) {
             const uint32_t see = column_mask(lo, hi, 0, 32 * c);
 #pragma unroll
@@ -621,44 +635,50 @@ struct DqSmem {
 
 struct QuerySteps {
   int n, n_units;
+  RawUnit raw;              // the next unit's
   int h, hk, t, start, len, nt, pre;
   KeyTiles kt;
   int k;
-  // units: the two query tiles of a forward item for every head; an item of one tile has empty units
-  __device__ __forceinline__ bool unit(const ScoredParams& p, const PlanView& pv) {
+  // units: the two query tiles of a forward item for every head, the later one first (it sees
+  // more); an item of one tile has empty units
+  __device__ __forceinline__ void fetch(const ScoredParams& p, const PlanView& pv) {
     for (;; ++n) {
-      const int i = unit_index(n, n_units);
-      if (i < 0) return false;
-      const int item_idx = i / (2 * p.hq), x = i % (2 * p.hq);
-      const int4 item = pv.fwd_items[item_idx];
-      const int w = kItemTiles - 1 - x / p.hq;        // the item's later tile first: it sees more
-      if (w >= item.z) continue;
-      const int2 span = pv.fwd_span[item_idx];
-      h = x % p.hq;
-      hk = h / (p.hq / p.hkv);
-      t = item.y + w;
-      start = span.x;
-      len = span.y;
-      nt = (len + kTile - 1) / kTile;
-      pre = prefix_of(p, item.x, len);
-      kt = key_tiles(t, t, nt, (pre + kTile - 1) / kTile, p.win);
-      k = 0;
-      return true;
+      raw.i = unit_index(n, n_units);
+      if (raw.i < 0) return;
+      raw.item = pv.fwd_items[raw.i / (2 * p.hq)];
+      raw.span = pv.fwd_span[raw.i / (2 * p.hq)];
+      if (kItemTiles - 1 - raw.i % (2 * p.hq) / p.hq < raw.item.z) {
+        ++n;
+        return;
+      }
     }
+  }
+  __device__ __forceinline__ bool unit(const ScoredParams& p, const PlanView& pv) {
+    if (raw.i < 0) return false;
+    const int x = raw.i % (2 * p.hq);
+    h = x % p.hq;
+    hk = h / (p.hq / p.hkv);
+    t = raw.item.y + kItemTiles - 1 - x / p.hq;
+    start = raw.span.x;
+    len = raw.span.y;
+    nt = (len + kTile - 1) / kTile;
+    pre = prefix_of(p, raw.item.x, len);
+    kt = key_tiles(t, t, nt, (pre + kTile - 1) / kTile, p.win);
+    k = 0;
+    fetch(p, pv);
+    return true;
   }
   __device__ __forceinline__ bool begin(const ScoredParams& p, const PlanView& pv) {
     n = 0;
     n_units = p.plan[kPlanFwdItems] * 2 * p.hq;
+    fetch(p, pv);
     return unit(p, pv);
   }
   __device__ __forceinline__ bool first() const { return k == 0; }
   __device__ __forceinline__ bool last() const { return k == kt.n - 1; }
   __device__ __forceinline__ int tile() const { return kt.tile(k); }
   __device__ __forceinline__ bool next(const ScoredParams& p, const PlanView& pv) {
-    if (last()) {
-      ++n;
-      return unit(p, pv);
-    }
+    if (last()) return unit(p, pv);
     ++k;
     return true;
   }
@@ -793,16 +813,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = lane_base + kTS + 64 * w, dp_addr = lane_base + kTP + 64 * w;
     float* tab = reinterpret_cast<float*>(smem + L::kBias);
     const int R = bias_range(p);
+    const int near = near_tiles(R);
+    const float scale2 = p.scale2, inv_scale2 = 1.f / p.scale2;
     HeadBias HB{};
-    ScoreHead H;
-    H.scale2 = p.scale2;
-    H.zscale = CAP ? p.scale / p.cap : 0.f;
-    H.cap2 = p.cap * kLog2e;
-    const float inv_cap2 = CAP ? 1.f / H.cap2 : 0.f;
     int staged = -1;
     bool ok = true;
     float nl = 0.f, dv = 0.f;
     int lo = 0, hi = 0;
+    FullTiles full{};
     QuerySteps S{};
     // The unit's A operands (warpgroup 0: Q, 1: dO; rows behind the document as zeros), LSE and D.
     auto start_unit = [&]() {
@@ -823,6 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       dv = in ? p.dvec[(int64_t)S.h * p.T + tok] : 0.f;
       lo = p.win.left < 0 ? 0 : max(0, qi - p.win.left);
       hi = p.win.right < 0 ? S.len - 1 : min(S.len - 1, qi + p.win.right);
+      full = full_tiles(S.t, S.len, S.pre, p.win);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
         tmem_st32(lane_base + (w ? kTB : kTA) + 32 * c, reinterpret_cast<uint32_t(&)[32]>(a[32 * c]));
@@ -854,20 +873,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(s_free);
         TileBias B{};
-        if constexpr (BIAS) B = tile_bias<1>(tab, HB, R, t, u, u * kTile + 64 * w - qi);
-        const bool plain = !BIAS || B.plain();
-        const float f = (CAP || !plain) ? 1.f : H.scale2;
-        const bool masked = scored_masked(t, u, S.len, S.pre, p.win);
+        if constexpr (BIAS) B = tile_bias(tab, HB, R, near, inv_scale2, t, u, u * kTile + 64 * w - qi);
+        const float f = BIAS ? B.factor(scale2) : scale2;
+        const bool masked = !full.has(u);
+        if constexpr (CAP) {
+          cap_products(v, p.capf);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), p.capf.zscale));
+        }
         const int c0 = u * kTile + 64 * w;
         const float2 f2 = make_float2(f, f), n2 = make_float2(nl + B.c, nl + B.c);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          if constexpr (CAP) {
-            cap_chunk(v[c], H);
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), inv_cap2));
-          }
-          if constexpr (BIAS) bias_chunk<1>(v[c], 32 * c, CAP ? 1.f : H.scale2, B);
+          if constexpr (BIAS) bias_chunk<1>(v[c], 32 * c, scale2, B);
           if (masked) {
             const uint32_t see = column_mask(lo - c0, hi - c0, S.pre - c0, 32 * c);
 #pragma unroll

@@ -41,41 +41,50 @@ struct FwdSmem {
   static constexpr int kSlots = D == 128 ? 4 : 8;           // K and V tiles in turn
   static constexpr int kQ = 0;                              // [2]
   static constexpr int kKV = 2 * kTileBytes;
-  static constexpr int kBias = kKV + kSlots * kTileBytes;   // [2 warpgroups][kBiasTab] floats
+  static constexpr int kBias = kKV + kSlots * kTileBytes;   // [2 query tiles][kBiasTab] floats
   static constexpr int kBar = (kBias + 2 * kBiasTab * 4 + 15) & ~15;
   static constexpr int kBytes = kBar + 256;
   static constexpr int kAlloc = kBytes + 1024;
 };
 
-struct Unit {
-  int h, hk, t0, ntq, start, len, nt, pre;
-  KeyTiles kt;
-  int pre_tiles, klo0, klo1, khi0, khi1;
-  __device__ __forceinline__ bool sees(int w, int k) const {
-    const int u = kt.tile(k);
-    return w < ntq && (u < pre_tiles || (w ? u >= klo1 && u <= khi1 : u >= klo0 && u <= khi0));
+// What a unit's first loads bring; fetched a unit ahead, so that their latency is not met.
+struct RawUnit {
+  int i;
+  int4 item;
+  int2 span;
+  __device__ __forceinline__ void fetch(const ScoredParams& p, const PlanView& pv, int n, int n_units) {
+    i = unit_index(n, n_units);
+    if (i < 0) return;
+    item = pv.fwd_items[i / p.hq];
+    span = pv.fwd_span[i / p.hq];
   }
 };
 
-__device__ __forceinline__ Unit make_unit(const ScoredParams& p, const PlanView& pv, int i) {
+struct Unit {
+  int h, hk, t0, ntq, start, len, pre;
+  KeyTiles kt;
+  int skip0, skip1;       // the one place of the list that the first / second query tile does not see, or -1
+  __device__ __forceinline__ bool sees(int w, int k) const { return w < ntq && k != (w ? skip1 : skip0); }
+  __device__ __forceinline__ int last(int w) const { return kt.n - 1 - ((w ? skip1 : skip0) == kt.n - 1 ? 1 : 0); }
+};
+
+__device__ __forceinline__ Unit make_unit(const ScoredParams& p, const RawUnit& raw) {
   Unit U;
-  const int item_idx = i / p.hq;
-  U.h = i % p.hq;
+  U.h = raw.i % p.hq;
   U.hk = U.h / (p.hq / p.hkv);
-  const int4 item = pv.fwd_items[item_idx];
-  const int2 span = pv.fwd_span[item_idx];
-  U.t0 = item.y;
-  U.ntq = item.z;
-  U.start = span.x;
-  U.len = span.y;
-  U.nt = (U.len + kTile - 1) / kTile;
-  U.pre = prefix_of(p, item.x, U.len);
-  U.pre_tiles = (U.pre + kTile - 1) / kTile;
-  U.klo0 = win_klo(U.t0, p.win);
-  U.khi0 = win_khi(U.t0, U.nt, p.win);
-  U.klo1 = win_klo(U.t0 + 1, p.win);
-  U.khi1 = win_khi(U.t0 + 1, U.nt, p.win);
-  U.kt = key_tiles(U.t0, U.t0 + U.ntq - 1, U.nt, U.pre_tiles, p.win);
+  U.t0 = raw.item.y;
+  U.ntq = raw.item.z;
+  U.start = raw.span.x;
+  U.len = raw.span.y;
+  U.pre = prefix_of(p, raw.item.x, U.len);
+  const int nt = (U.len + kTile - 1) / kTile, pt = (U.pre + kTile - 1) / kTile, t1 = U.t0 + U.ntq - 1;
+  U.kt = key_tiles(U.t0, t1, nt, pt, p.win);
+  // the two windows start and end at most a tile apart: the second may miss the window's first
+  // tile, the first its last one
+  const bool late = t1 > U.t0 && win_klo(t1, p.win) > U.kt.lo && U.kt.lo >= pt;
+  const bool early = t1 > U.t0 && win_khi(U.t0, nt, p.win) < U.kt.tile(U.kt.n - 1) && U.kt.tile(U.kt.n - 1) >= pt;
+  U.skip1 = late ? U.kt.a : -1;
+  U.skip0 = early ? U.kt.n - 1 : -1;
   return U;
 }
 
@@ -146,10 +155,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int b = 0; b < D / 64; ++b) tma_load_3d(dst + b * kTile * 128, tm, bar, 64 * b, h, row);
       };
-      for (int n = 0; ok; ++n) {
-        const int i = unit_index(n, n_units);
-        if (i < 0) break;
-        const Unit U = make_unit(p, pv, i);
+      RawUnit raw;
+      raw.fetch(p, pv, 0, n_units);
+      for (int n = 1; ok && raw.i >= 0; ++n) {
+        const Unit U = make_unit(p, raw);
+        raw.fetch(p, pv, n, n_units);
         for (int w = 0; w < U.ntq && ok; ++w) {
           if (nq[w] && !(ok = mbar_wait(&q_empty[w], (nq[w] - 1) & 1, status))) break;
           ++nq[w];
@@ -173,14 +183,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t base16 = (smem_u32(smem) & 0x3FFFFu) >> 4;
       uint32_t ring = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0, ns0 = 0, ns1 = 0;
       bool ok = true;
-      for (int n = 0; ok; ++n) {
-        const int i = unit_index(n, n_units);
-        if (i < 0) break;
-        const Unit U = make_unit(p, pv, i);
-        const int nk = U.kt.n;
-        int first0 = -1, first1 = -1, last0 = nk - 1, last1 = nk - 1;      // places in the list of key tiles
-        while (last0 >= 0 && !U.sees(0, last0)) --last0;
-        while (last1 >= 0 && !U.sees(1, last1)) --last1;
+      RawUnit raw;
+      raw.fetch(p, pv, 0, n_units);
+      for (int n = 1; ok && raw.i >= 0; ++n) {
+        const Unit U = make_unit(p, raw);
+        raw.fetch(p, pv, n, n_units);
+        const int nk = U.kt.n, last0 = U.last(0), last1 = U.last(1);
+        int first0 = -1, first1 = -1;              // places in the list of key tiles
         // S of query tile w and key tile k (whose K is in the ring's slot st)
         auto scores = [&](int w, int k, uint32_t st) {
           int& first = w ? first1 : first0;
@@ -267,21 +276,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = lane_base + w * 128, o_addr = lane_base + kO + w * D;
     const uint32_t p_addr = kSplit ? lane_base + kP + 64 * w : s_addr;
     float* tab = reinterpret_cast<float*>(smem + L::kBias) + w * kBiasTab;
-    const int R = bias_range(p);
+    const int R = bias_range(p), near = near_tiles(R);
+    const float scale2 = p.scale2, inv_scale2 = 1.f / p.scale2;
     uint32_t ring = 0, ns = 0, no = 0;
     int staged = -1;
     bool ok = true;
-    ScoreHead H;
-    H.scale2 = p.scale2;
-    H.zscale = CAP ? p.scale / p.cap : 0.f;
-    H.cap2 = p.cap * kLog2e;
     HeadBias HB{};
+    RawUnit raw;
+    raw.fetch(p, pv, 0, n_units);
     // a warp whose wait ran out goes on through the units without work: it still meets its
     // warpgroup at the barriers around the bias
-    for (int n = 0;; ++n) {
-      const int i = unit_index(n, n_units);
-      if (i < 0) break;
-      const Unit U = make_unit(p, pv, i);
+    for (int n = 1; raw.i >= 0; ++n) {
+      const Unit U = make_unit(p, raw);
+      raw.fetch(p, pv, n, n_units);
       if constexpr (BIAS) {
         if (staged != U.h) {      // each warpgroup has a table: the two need not meet
           HB = head_bias(p, U.h);
@@ -295,15 +302,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = U.t0 + w, qi = t * kTile + r;
       const int lo = p.win.left < 0 ? 0 : max(0, qi - p.win.left);
       const int hi = p.win.right < 0 ? U.len - 1 : min(U.len - 1, qi + p.win.right);
+      const FullTiles full = full_tiles(t, U.len, U.pre, p.win);
+      const int skip = w >= U.ntq ? -2 : (w ? U.skip1 : U.skip0);
       float m = -INFINITY;
       float2 la = make_float2(0.f, 0.f), lb = la;
       bool first = true;
-      for (int k = 0; k < U.kt.n; ++k) {
-        if (!U.sees(w, k)) continue;
+      for (int k = 0; k < U.kt.n && skip != -2; ++k) {
+        if (k == skip) continue;
         const int u = U.kt.tile(k);
         TileBias B{};
-        if constexpr (BIAS) B = tile_bias<1>(tab, HB, R, t, u, u * kTile - qi);
-        const bool masked = scored_masked(t, u, U.len, U.pre, p.win);
+        if constexpr (BIAS) B = tile_bias(tab, HB, R, near, inv_scale2, t, u, u * kTile - qi);
+        const bool masked = !full.has(u);
         const bool plain = !BIAS || B.plain();
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[w], ns++ & 1, status));
         if (!ok) break;
@@ -317,20 +326,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           mbar_arrive(&s_free[w]);
         }
-        // products still raw (no cap, no bias but a constant): scaled in the exponent
-        const float f = (CAP || !plain) ? 1.f : H.scale2;
+        float mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);      // of the raw products, from the load
         if constexpr (CAP) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) cap_chunk(v[g], H);
+          cap_products(v, p.capf);
+          const float z = mx * p.capf.zscale;                       // monotone
+          mx = fabsf(z) < 1e-3f ? mx : p.capf.inv * tanh_any(z);
         }
-        if constexpr (BIAS) {
-          if (!plain) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) bias_chunk<1>(v[g], 32 * g, CAP ? 1.f : H.scale2, B);
-          }
-        }
-        float mx;
+        const float f = BIAS ? B.factor(scale2) : scale2;
         if (masked || !plain) {
+          if constexpr (BIAS) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) bias_chunk<1>(v[g], 32 * g, scale2, B);
+          }
           if (masked) {
             const int c = u * kTile;
 #pragma unroll
@@ -347,22 +354,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g) cm[g] = fmax3(cm[g], __uint_as_float(v[g][j]), __uint_as_float(v[g][j + 1]));
           mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);
-        } else {
-          mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);      // the load's own maximum of the raw products
-          if constexpr (CAP) mx = H.cap2 * tanh_any(mx * H.zscale);      // monotone
         }
         mx = fmaf(mx, f, B.c);
-        if (kSplit && !first) {          // the last P has been read, O is whole
-          ok = __all_sync(0xffffffffu, mbar_wait(&o_full[w], no++ & 1, status));
-          if (!ok) break;
-          tc_fence_after();
-        }
         if (first) {
           m = mx;
-          first = false;
         } else if (__any_sync(0xffffffffu, mx > m + kRescaleAbove)) {
           const float m_new = fmaxf(m, mx);
           const float alpha = m_new == m ? 1.f : fast_exp2(m - m_new);      // 0 where nothing was visible yet
+          la = fmul2(la, make_float2(alpha, alpha));
+          lb = fmul2(lb, make_float2(alpha, alpha));
+          m = m_new;
+          if (kSplit) {                // the last product has to be in
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[w], no & 1, status));
+            if (!ok) break;
+            tc_fence_after();
+          }
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -373,9 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(o_addr + 32 * c, o);
           }
           tmem_st_wait();
-          la = fmul2(la, make_float2(alpha, alpha));
-          lb = fmul2(lb, make_float2(alpha, alpha));
-          m = m_new;
         }
         if ((u + 1) * kTile > U.len) {
           const uint32_t x = ring + 2 * k + 1, st = x % kSlots;
@@ -402,11 +405,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[j / 2] = *reinterpret_cast<const uint32_t*>(&b0);
             pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&b1);
           }
+          if (kSplit && half == 0 && !first) {       // the last P has been read
+            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[w], no++ & 1, status));
+            if (!ok) break;
+            tc_fence_after();
+          }
           tmem_st32(p_addr + 32 * half, pk);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(&p_full[2 * w + half]);
         }
+        first = false;
+        if (!ok) break;
       }
       ring += 2 * U.kt.n;
       if (!ok || w >= U.ntq) continue;
