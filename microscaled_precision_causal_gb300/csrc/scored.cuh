@@ -11,7 +11,8 @@ struct CapForm {
   float zscale;      // softmax scale / cap
   float inv;         // cap / softmax scale
   float t3, t5;      // up to this |S| the polynomials of 3 and of 5 coefficients serve (0: never)
-  float k3[3], k5[5];     // their coefficients of S^2, S^4, ...
+  float2 k3[3], k5[5];    // their coefficients of S^2, S^4, ... (twice: packed operands)
+  float2 e3[4], e5[6];    // the same with 1 in front, times the scale in base 2
 };
 
 struct ScoredParams {
@@ -68,12 +69,17 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kHideBelow = -1.2676506002282294e30f;   // -2^100
 
 // ---------------------------------------------------------------- visible tiles
-// Key tiles that a run of query tiles [t0, t1] of a document sees, in increasing order:
-// the a tiles of the prefix that lie before the window's first tile, then the n - a tiles
-// from lo on (the window's, and prefix tiles behind its first).
+// Key tiles that a run of query tiles [t0, t1] of a document sees: the a tiles of the prefix
+// that lie before the window's first tile, then the n - a tiles from lo on (the window's, and
+// prefix tiles behind its first).  They are walked from the last to the first: a bias that
+// falls with the distance then puts a causal row's maximum into its first tiles, and the
+// running maximum stays.
 struct KeyTiles {
   int a, lo, n;
-  __device__ __forceinline__ int tile(int k) const { return k < a ? k : lo + (k - a); }
+  __device__ __forceinline__ int tile(int k) const {
+    const int x = n - 1 - k;
+    return x < a ? x : lo + (x - a);
+  }
 };
 __device__ __forceinline__ KeyTiles key_tiles(int t0, int t1, int nt, int pre_tiles, Window w) {
   KeyTiles s;
@@ -150,6 +156,8 @@ constexpr float kTanh3[3] = {-0.33332332968711853f, 0.1328972578048706f, -0.0484
 constexpr float kTanh5a = -0.3333286643028259f, kTanh5b = 0.1332276612520218f, kTanh5c = -0.053176309913396835f,
                 kTanh5d = 0.01919075846672058f, kTanh5e = -0.004410882946103811f;
 inline CapForm cap_form(double scale, double cap) {
+  const double scale2 = scale * 1.4426950408889634;
+  auto two = [](double x) { return make_float2((float)x, (float)x); };
   CapForm c{};
   if (!(cap > 0.0)) return c;
   const double z = scale / cap;
@@ -161,9 +169,10 @@ inline CapForm cap_form(double scale, double cap) {
   const float k5[5] = {kTanh5a, kTanh5b, kTanh5c, kTanh5d, kTanh5e};
   double f = z * z;
   for (int i = 0; i < 5; ++i, f *= z * z) {
-    if (i < 3) c.k3[i] = (float)(kTanh3[i] * f);
-    c.k5[i] = (float)(k5[i] * f);
+    if (i < 3) c.k3[i] = two(kTanh3[i] * f), c.e3[i + 1] = two(kTanh3[i] * f * scale2);
+    c.k5[i] = two(k5[i] * f), c.e5[i + 1] = two(k5[i] * f * scale2);
   }
+  c.e3[0] = c.e5[0] = two(scale2);
   return c;
 }
 __device__ __forceinline__ float fast_rcp(float x) {
@@ -202,15 +211,14 @@ __device__ __forceinline__ void cap_products(uint32_t (&v)[N][32], const CapForm
     for (int j = 0; j < 32; j += 2)
       m[(j / 2) % 4] = fmax3(m[(j / 2) % 4], fabsf(__uint_as_float(v[g][j])), fabsf(__uint_as_float(v[g][j + 1])));
   const float am = fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
-  auto c = [](float x) { return make_float2(x, x); };
   if (!__any_sync(0xffffffffu, !(am <= F.t3))) {
 #pragma unroll
     for (int g = 0; g < N; ++g)
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
         const float2 x = pair_of(v[g], j), w = fmul2(x, x);
-        float2 t = ffma2(w, c(F.k3[2]), c(F.k3[1]));
-        t = ffma2(w, t, c(F.k3[0]));
+        float2 t = ffma2(w, F.k3[2], F.k3[1]);
+        t = ffma2(w, t, F.k3[0]);
         put_pair(v[g], j, ffma2(x, fmul2(w, t), x));
       }
   } else if (!__any_sync(0xffffffffu, !(am <= F.t5))) {
@@ -219,10 +227,10 @@ __device__ __forceinline__ void cap_products(uint32_t (&v)[N][32], const CapForm
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
         const float2 x = pair_of(v[g], j), w = fmul2(x, x);
-        float2 t = ffma2(w, c(F.k5[4]), c(F.k5[3]));
-        t = ffma2(w, t, c(F.k5[2]));
-        t = ffma2(w, t, c(F.k5[1]));
-        t = ffma2(w, t, c(F.k5[0]));
+        float2 t = ffma2(w, F.k5[4], F.k5[3]);
+        t = ffma2(w, t, F.k5[2]);
+        t = ffma2(w, t, F.k5[1]);
+        t = ffma2(w, t, F.k5[0]);
         put_pair(v[g], j, ffma2(x, fmul2(w, t), x));
       }
   } else {
@@ -261,32 +269,29 @@ __device__ __forceinline__ void bias_chunk(uint32_t (&v)[32], int c0, float scal
 // so that no index is clipped in the loops.  Without a bias by distance R counts as 1: the
 // table then serves the tiles on the diagonal, where a slope's sign changes.
 constexpr int kBiasReach = 2 * kTile - 1;
-constexpr int kBiasTab = 2 * (FLAMIA_REL_MAX + kBiasReach) + 2;
+constexpr int kBiasHead = 2 * (FLAMIA_REL_MAX + kBiasReach) + 2;  // behind the table: the head's constants
+constexpr int kBiasTab = kBiasHead + 4;                            // floats, an even number
 __device__ __forceinline__ float bias_base2(float b) {
   return b < kHideBelow ? -INFINITY : fminf(b, -kHideBelow) * kLog2e;
 }
 __device__ __forceinline__ int bias_range(const ScoredParams& p) { return p.rel ? p.R : 1; }
-__device__ __forceinline__ float head_slope2(const ScoredParams& p, int h) {
-  return p.slopes ? p.slopes[h] * kLog2e : 0.f;
-}
-__device__ __forceinline__ void stage_bias(float* buf, const ScoredParams& p, int h, int first, int stride) {
-  const int R = bias_range(p);
-  const float slope2 = head_slope2(p, h);
-  const float* src = p.rel ? p.rel + (size_t)h * (2 * R + 1) : nullptr;
-  for (int i = first; i < 2 * (R + kBiasReach) + 1; i += stride) {
-    const float b = src ? bias_base2(src[min(max(i - kBiasReach, 0), 2 * R)]) : 0.f;
-    buf[i] = fmaf(fabsf((float)(i - R - kBiasReach)), -slope2, b);
-  }
-}
 struct HeadBias {
   float slope2, lo, hi;      // slope, and the bias of the distances up to -R and from R on
 };
-__device__ __forceinline__ HeadBias head_bias(const ScoredParams& p, int h) {
-  HeadBias H;
-  H.slope2 = head_slope2(p, h);
-  H.lo = p.rel ? bias_base2(p.rel[(size_t)h * (2 * p.R + 1)]) : 0.f;
-  H.hi = p.rel ? bias_base2(p.rel[(size_t)h * (2 * p.R + 1) + 2 * p.R]) : 0.f;
-  return H;
+__device__ __forceinline__ void stage_bias(float* tab, const ScoredParams& p, int h, int first, int stride) {
+  const int R = bias_range(p);
+  const float slope2 = p.slopes ? p.slopes[h] * kLog2e : 0.f;
+  const float* src = p.rel ? p.rel + (size_t)h * (2 * R + 1) : nullptr;
+  for (int i = first; i < 2 * (R + kBiasReach) + 1; i += stride) {
+    const float b = src ? bias_base2(src[min(max(i - kBiasReach, 0), 2 * R)]) : 0.f;
+    tab[i] = fmaf(fabsf((float)(i - R - kBiasReach)), -slope2, b);
+    if (i == 0) tab[kBiasHead] = slope2;
+    if (i == 0) tab[kBiasHead + 1] = b;
+    if (i == 2 * (R + kBiasReach)) tab[kBiasHead + 2] = b;
+  }
+}
+__device__ __forceinline__ HeadBias head_bias(const float* tab) {
+  return HeadBias{tab[kBiasHead], tab[kBiasHead + 1], tab[kBiasHead + 2]};
 }
 // Key tiles closer to the query tile than this hold a distance below R.
 __device__ __forceinline__ int near_tiles(int R) { return (R + kTile - 2) / kTile; }

@@ -396,10 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = S.t, kj = U.u * kTile + r;
       if constexpr (BIAS != 0) {
         if (S.head_first() && staged != S.h) {
-          HB = head_bias(p, S.h);
           named_bar_sync(1, 256);
           stage_bias(tab, p, S.h, tid, 256);
           named_bar_sync(1, 256);
+          HB = head_bias(tab);
           staged = S.h;
         }
         if (BIAS == 2 && S.head_first()) {
@@ -855,10 +855,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; more; ++g) {
       if constexpr (BIAS) {
         if (S.first() && staged != S.h) {
-          HB = head_bias(p, S.h);
           named_bar_sync(1, 256);
           stage_bias(tab, p, S.h, tid, 256);
           named_bar_sync(1, 256);
+          HB = head_bias(tab);
           staged = S.h;
         }
       }

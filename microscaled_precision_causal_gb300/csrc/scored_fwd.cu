@@ -5,22 +5,40 @@
 //
 // A unit is a forward work item of the plan (up to two document-local 128-query tiles) and
 // a query head; one CTA per SM walks the cost-sorted units in boustrophedon order.  Roles
-// (384 threads): warp 0 TMA producer, warp 1 MMA issuer, warp 2 TMEM allocator, warps 4-7
-// and 8-11 the softmax of the item's first and second query tile (thread = query row).
-// While one warpgroup converts its score tile the tensor core runs the other's products.
+// (512 threads):
+//   warp 0        TMA producer: Q tiles, K and V tiles through a ring
+//   warp 1        MMA issuer: a query tile's products (O += P V, then its next scores over P)
+//                 are queued whole before the other's, so that the two softmax warpgroups get
+//                 their scores half a step apart.  Queued side by side they would finish together,
+//                 and the arithmetic of both would alternate with the products of both (2.03
+//                 instead of 1.73 ms on four causal documents of 8192, 32 heads on 8, slopes).
+//                 At D = 64 the scores come ahead of the softmax anyway, and warp 3 issues the
+//                 second query tile's, so that neither waits for the other (0.64 instead of 0.78
+//                 ms on two noncausal documents of 8192, 16 heads)
+//   warp 2        TMEM allocator; describes the units ahead of the other roles
+//   warps 4-11    softmax, a warpgroup per query tile, thread = query row
+//   warps 12-15   stage the next unit's bias table and write the finished O, while the softmax
+//                 warps are in the next unit already
 //
 // P enters the PV product in bf16 (V is bf16 and an MMA's operands share a type): half a
 // step of 2^-8 per weight, the size of the rounding of O itself.  It stays in tensor memory,
 // over the first half of the score columns it came from, so no shared memory is written and
-// the PV product reads V alone from there.  The running maximum follows the scores only when
-// they outgrow it by more than 8 (in base 2): until then p stays below 2^8, which bf16 and
-// the fp32 sums hold as exactly, and O needs no rescaling pass.
+// the PV product reads V alone from there.
+//
+// m is a reference near the row's maximum, not the maximum: p = 2^(x - m) only has to stay in
+// range, as bf16 and fp32 hold 2^-60 and 2^8 alike.  It moves when a tile outgrows it by more
+// than 8, so that O is seldom rescaled, and where every key of a tile is seen it comes from the
+// tensor memory load's own reduction of the raw products (plain: their maximum; capped: their
+// largest magnitude, which also says how long a polynomial the cap needs; slopes: their maximum
+// and the tile's largest bias), as long as it can be no more than 2^64 too high.
 //
 // TMEM columns: S_0 [0, 128), S_1 [128, 256), O_0 [256, 256 + D), O_1 [256 + D, 256 + 2 D).  At
 // D = 128 that is all of it and P_w takes the first half of S_w's columns.  At D = 64 the
 // P_w have columns of their own behind O (split): the next scores are then ready before the
 // softmax asks for them, which matters there because two products of a tile take half as
 // long and the exponentials bound the kernel.
+#include <type_traits>
+
 #include "ptx.cuh"
 #include "scored.cuh"
 #include "tmap.h"
@@ -29,11 +47,59 @@ namespace flamia {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr float kRescaleAbove = 8.f;
+constexpr int kThreads = 512;
+constexpr float kRescaleAbove = 8.f, kLoose = 64.f;
 constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
-constexpr int kRegCtl = 88, kRegSoftmax = 208;
-static_assert(kRegCtl * 128 + kRegSoftmax * 256 <= kLaunchRegs * kThreads, "register split");
+constexpr int kRegCtl = 64, kRegAux = 80, kRegSoftmax = 184;
+static_assert(kRegCtl * 128 + kRegAux * 128 + kRegSoftmax * 256 <= kLaunchRegs * kThreads, "register split");
+
+// A unit's description, worked out by one warp some units ahead and read by every role from
+// shared memory: the divisions and the dependent loads behind it stay off their paths.
+struct Unit {
+  int h, hk, t0, ntq;     // ntq 0: no more units
+  int start, len, pre, skip0;
+  KeyTiles kt;
+  int skip1;              // skip0 / 1: the one place of the list that the first / second query tile does not see, or -1
+};
+static_assert(sizeof(Unit) == 48, "read as three 16-byte words");
+constexpr int kUnits = 8;  // described at a time: more units than the K / V ring can hold tiles of
+
+__device__ __forceinline__ Unit make_unit(const ScoredParams& p, const PlanView& pv, int i) {
+  Unit U{};
+  if (i < 0) return U;
+  const int4 item = pv.fwd_items[i / p.hq];
+  const int2 span = pv.fwd_span[i / p.hq];
+  U.h = i % p.hq;
+  U.hk = U.h / (p.hq / p.hkv);
+  U.t0 = item.y;
+  U.ntq = item.z;
+  U.start = span.x;
+  U.len = span.y;
+  U.pre = prefix_of(p, item.x, U.len);
+  const int nt = (U.len + kTile - 1) / kTile, pt = (U.pre + kTile - 1) / kTile, t1 = U.t0 + U.ntq - 1;
+  U.kt = key_tiles(U.t0, t1, nt, pt, p.win);
+  // the two windows start and end at most a tile apart: the second may miss the window's first
+  // tile, the first its last one
+  const bool late = t1 > U.t0 && win_klo(t1, p.win) > U.kt.lo && U.kt.lo >= pt;
+  const bool early = t1 > U.t0 && win_khi(U.t0, nt, p.win) < U.kt.tile(0) && U.kt.tile(0) >= pt;
+  U.skip1 = late ? U.kt.n - 1 - U.kt.a : -1;
+  U.skip0 = early ? 0 : -1;
+  return U;
+}
+// Unit n of the CTA; ntq 0 when there is none, or when the wait ran out.
+__device__ __forceinline__ Unit read_unit(const uint8_t* units, uint64_t* full, int n, bool whole_warp, bool& ok, int* status) {
+  ok = mbar_wait(&full[n % kUnits], (n / kUnits) & 1, status);
+  if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+  union {
+    Unit u;
+    int4 w[3];
+  } x;
+  const int4* src = reinterpret_cast<const int4*>(units + (n % kUnits) * sizeof(Unit));
+#pragma unroll
+  for (int i = 0; i < 3; ++i) x.w[i] = src[i];
+  if (!ok) x.u.ntq = 0;
+  return x.u;
+}
 
 template <int D>
 struct FwdSmem {
@@ -41,52 +107,13 @@ struct FwdSmem {
   static constexpr int kSlots = D == 128 ? 4 : 8;           // K and V tiles in turn
   static constexpr int kQ = 0;                              // [2]
   static constexpr int kKV = 2 * kTileBytes;
-  static constexpr int kBias = kKV + kSlots * kTileBytes;   // [2 query tiles][kBiasTab] floats
-  static constexpr int kBar = (kBias + 2 * kBiasTab * 4 + 15) & ~15;
-  static constexpr int kBytes = kBar + 256;
+  static constexpr int kBias = kKV + kSlots * kTileBytes;   // [2 units in turn][kBiasTab] floats
+  static constexpr int kInv = kBias + 2 * kBiasTab * 4;     // [2 query tiles][128] 1 / l
+  static constexpr int kUnit = kInv + 1024;                 // [kUnits]
+  static constexpr int kBar = kUnit + kUnits * 48;
+  static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;
 };
-
-// What a unit's first loads bring; fetched a unit ahead, so that their latency is not met.
-struct RawUnit {
-  int i;
-  int4 item;
-  int2 span;
-  __device__ __forceinline__ void fetch(const ScoredParams& p, const PlanView& pv, int n, int n_units) {
-    i = unit_index(n, n_units);
-    if (i < 0) return;
-    item = pv.fwd_items[i / p.hq];
-    span = pv.fwd_span[i / p.hq];
-  }
-};
-
-struct Unit {
-  int h, hk, t0, ntq, start, len, pre;
-  KeyTiles kt;
-  int skip0, skip1;       // the one place of the list that the first / second query tile does not see, or -1
-  __device__ __forceinline__ bool sees(int w, int k) const { return w < ntq && k != (w ? skip1 : skip0); }
-  __device__ __forceinline__ int last(int w) const { return kt.n - 1 - ((w ? skip1 : skip0) == kt.n - 1 ? 1 : 0); }
-};
-
-__device__ __forceinline__ Unit make_unit(const ScoredParams& p, const RawUnit& raw) {
-  Unit U;
-  U.h = raw.i % p.hq;
-  U.hk = U.h / (p.hq / p.hkv);
-  U.t0 = raw.item.y;
-  U.ntq = raw.item.z;
-  U.start = raw.span.x;
-  U.len = raw.span.y;
-  U.pre = prefix_of(p, raw.item.x, U.len);
-  const int nt = (U.len + kTile - 1) / kTile, pt = (U.pre + kTile - 1) / kTile, t1 = U.t0 + U.ntq - 1;
-  U.kt = key_tiles(U.t0, t1, nt, pt, p.win);
-  // the two windows start and end at most a tile apart: the second may miss the window's first
-  // tile, the first its last one
-  const bool late = t1 > U.t0 && win_klo(t1, p.win) > U.kt.lo && U.kt.lo >= pt;
-  const bool early = t1 > U.t0 && win_khi(U.t0, nt, p.win) < U.kt.tile(U.kt.n - 1) && U.kt.tile(U.kt.n - 1) >= pt;
-  U.skip1 = late ? U.kt.a : -1;
-  U.skip0 = early ? U.kt.n - 1 : -1;
-  return U;
-}
 
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -94,22 +121,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_v, const ScoredParams p) {
   using L = FwdSmem<D>;
   constexpr int kSlots = L::kSlots;
+  constexpr bool kSplit = D == 64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
-  uint64_t* q_full = bars;                  // [2]
-  uint64_t* q_empty = bars + 2;             // [2]
-  uint64_t* s_full = bars + 4;              // [2]
-  uint64_t* o_full = bars + 6;              // [2]
-  uint64_t* s_free = bars + 8;              // [2] (split)
-  uint64_t* p_full = bars + 10;             // [2 query tiles][2 halves of 64 keys]
-  uint64_t* drain = bars + 14;
-  uint64_t* kv_full = bars + 15;            // [kSlots]
+  uint64_t* q_full = bars;                  // [2 query tiles], as the next seven
+  uint64_t* q_empty = bars + 2;
+  uint64_t* s_full = bars + 4;
+  uint64_t* s_free = bars + 6;              // (split) scores read
+  uint64_t* pv_done = bars + 8;             // (split) P read
+  uint64_t* o_full = bars + 10;             // the unit's O is whole
+  uint64_t* o_free = bars + 12;             // and written out
+  uint64_t* l_ready = bars + 14;
+  uint64_t* p_full = bars + 16;             // [2 query tiles][2 halves of 64 keys]
+  uint64_t* tab_full = bars + 20;           // [2 units in turn]
+  uint64_t* drain = bars + 22;              // [2 issuers]
+  uint64_t* unit_done = bars + 24;
+  uint64_t* unit_full = bars + 25;          // [kUnits]
+  uint64_t* kv_full = unit_full + kUnits;   // [kSlots]
   uint64_t* kv_empty = kv_full + kSlots;    // [kSlots]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + kSlots);
   int* status = const_cast<int*>(p.plan) + kPlanStatus;
   const PlanView pv = plan_view(p.plan, p.T, p.N);
   const int n_units = p.plan[kPlanFwdItems] * p.hq;
+  uint8_t* units = smem + L::kUnit;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -117,15 +152,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&o_full[i], 1);
       mbar_init(&s_free[i], 128);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 128);
+      mbar_init(&l_ready[i], 128);
       mbar_init(&p_full[2 * i], 128);
       mbar_init(&p_full[2 * i + 1], 128);
+      mbar_init(&tab_full[i], 128);
+      mbar_init(&drain[i], 1);
     }
-    mbar_init(drain, 1);
+    mbar_init(unit_done, 1);
+    for (int i = 0; i < kUnits; ++i) mbar_init(&unit_full[i], 1);
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], kSplit ? 2 : 1);      // issuers
     }
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
@@ -140,7 +181,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  constexpr bool kSplit = D == 64;
   constexpr uint32_t kO = 256, kP = 384;
 
   if (warp < 4) {
@@ -155,11 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int b = 0; b < D / 64; ++b) tma_load_3d(dst + b * kTile * 128, tm, bar, 64 * b, h, row);
       };
-      RawUnit raw;
-      raw.fetch(p, pv, 0, n_units);
-      for (int n = 1; ok && raw.i >= 0; ++n) {
-        const Unit U = make_unit(p, raw);
-        raw.fetch(p, pv, n, n_units);
+      for (int n = 0; ok; ++n) {
+        const Unit U = read_unit(units, unit_full, n, false, ok, status);
+        if (U.ntq == 0) break;
         for (int w = 0; w < U.ntq && ok; ++w) {
           if (nq[w] && !(ok = mbar_wait(&q_empty[w], (nq[w] - 1) & 1, status))) break;
           ++nq[w];
@@ -177,48 +215,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&kv_full[x % kSlots], (x / kSlots) & 1, status);
       for (int w = 0; w < 2; ++w)
         if (nq[w]) mbar_wait(&q_full[w], (nq[w] - 1) & 1, status);
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issuer
+    } else if (warp == 2 && lane == 0) {
+      // ---------------------------------------------------------- unit descriptions
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        if (n >= kUnits && !(ok = mbar_wait(unit_done, (n - kUnits) & 1, status))) break;
+        const Unit U = make_unit(p, pv, unit_index(n, n_units));
+        *reinterpret_cast<Unit*>(units + (n % kUnits) * sizeof(Unit)) = U;
+        mbar_arrive(&unit_full[n % kUnits]);
+        if (U.ntq == 0) break;
+      }
+    } else if (warp == 1 || (kSplit && warp == 3)) {
+      // ---------------------------------------------------------- MMA issuer of query tiles w0 .. w1 - 1
+      const int w0 = kSplit ? warp >> 1 : 0, w1 = kSplit ? w0 + 1 : 2;
       const bool leader = elect_one();
       const uint32_t base16 = (smem_u32(smem) & 0x3FFFFu) >> 4;
+      const uint32_t tb = (uint32_t)warp_uniform((int)tbase);
       uint32_t ring = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0, ns0 = 0, ns1 = 0;
       bool ok = true;
-      RawUnit raw;
-      raw.fetch(p, pv, 0, n_units);
-      for (int n = 1; ok && raw.i >= 0; ++n) {
-        const Unit U = make_unit(p, raw);
-        raw.fetch(p, pv, n, n_units);
-        const int nk = U.kt.n, last0 = U.last(0), last1 = U.last(1);
-        int first0 = -1, first1 = -1;              // places in the list of key tiles
-        // S of query tile w and key tile k (whose K is in the ring's slot st)
-        auto scores = [&](int w, int k, uint32_t st) {
-          int& first = w ? first1 : first0;
-          if (first < 0) {
-            first = k;
-            if (!(ok = warp_wait(&q_full[w], (w ? nq1++ : nq0++) & 1, status))) return;
-          }
-          if (kSplit) {                            // the last scores have been read
-            uint32_t& ns = w ? ns1 : ns0;
-            if (ns && !(ok = warp_wait(&s_free[w], (ns - 1) & 1, status))) return;
-            ++ns;
-          }
+      for (int n = 0; ok; ++n) {
+        const Unit U = read_unit(units, unit_full, n, true, ok, status);
+        const int ntq = warp_uniform(U.ntq);
+        if (ntq == 0) break;
+        const int nk = warp_uniform(U.kt.n), skip0 = warp_uniform(U.skip0), skip1 = warp_uniform(U.skip1);
+        auto sees = [&](int w, int k) { return w < ntq && k != (w ? skip1 : skip0); };
+        auto first = [&](int w) { return (w ? skip1 : skip0) == 0 ? 1 : 0; };
+        auto last = [&](int w) { return (w ? skip1 : skip0) == nk - 1 ? nk - 2 : nk - 1; };
+        auto landed = [&](uint32_t x) { return ok = warp_wait(&kv_full[x % kSlots], (x / kSlots) & 1, status); };
+        auto release = [&](uint32_t x) {
+          if (leader) mma_commit(&kv_empty[x % kSlots]);
+        };
+        auto scores = [&](int w, int k) {          // S of key tile k
+          const uint32_t x = ring + 2 * k, st = x % kSlots;
+          if (k == first(w) && !(ok = warp_wait(&q_full[w], (w ? nq1 : nq0) & 1, status))) return;
+          uint32_t& ns = w ? ns1 : ns0;
+          if (kSplit && ns && !(ok = warp_wait(&s_free[w], (ns - 1) & 1, status))) return;   // the last ones have been read
+          ++ns;
+          if (!landed(x)) return;
           tc_fence_after();
+          const uint32_t kv16 = base16 + st * (L::kTileBytes / 16);
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
             const uint32_t off = (s / 4) * kTile * 128 + (s % 4) * 32;
             if (leader)
-              mma_bf16(tbase + w * 128, sdesc_at(base16, L::kQ + w * L::kTileBytes + off, 16, 1024, kSwizzle128B),
-                       sdesc_at(base16, L::kKV + st * L::kTileBytes + off, 16, 1024, kSwizzle128B),
-                       idesc_bf16(128, 128, 0, 0), s > 0);
+              mma_bf16(tb + w * 128, sdesc_at(base16, L::kQ + w * L::kTileBytes + off, 16, 1024, kSwizzle128B),
+                       sdesc_at(kv16, L::kKV + off, 16, 1024, kSwizzle128B), idesc_bf16(128, 128, 0, 0), s > 0);
           }
           if (leader) {
             mma_commit(&s_full[w]);
-            if (k == (w ? last1 : last0)) mma_commit(&q_empty[w]);
+            if (k == last(w)) mma_commit(&q_empty[w]);
           }
         };
-        // O += P V, half of the keys at a time as the softmax hands them in
-        auto values = [&](int w, int k, uint32_t st) {
-          const uint32_t par = (w ? np1++ : np0++) & 1;
+        auto values = [&](int w, int k) {          // O += P V, half of the keys at a time as they are handed in
+          const uint32_t x = ring + 2 * k + 1, st = x % kSlots;
+          if (!landed(x)) return;
+          const uint32_t nq = w ? nq1 : nq0;
+          if (k == first(w) && nq && !(ok = warp_wait(&o_free[w], (nq - 1) & 1, status))) return;
+          const uint32_t par = (w ? np1++ : np0++) & 1, kv16 = base16 + st * (L::kTileBytes / 16);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             if (!(ok = warp_wait(&p_full[2 * w + half], par, status))) return;
@@ -226,48 +279,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int s = 4 * half; s < 4 * half + 4; ++s)
               if (leader)
-                mma_bf16_ta(tbase + kO + w * D, tbase + (kSplit ? kP + 64 * w : 128 * w) + s * 8,
-                            sdesc_at(base16, L::kKV + st * L::kTileBytes + s * 2048, kTile * 128, 1024, kSwizzle128B),
-                            idesc_bf16(128, D, 0, 1), (k != (w ? first1 : first0) || s > 0));
+                mma_bf16_ta(tb + kO + w * D, tb + (kSplit ? kP + 64 * w : 128 * w) + s * 8,
+                            sdesc_at(kv16, L::kKV + s * 2048, kTile * 128, 1024, kSwizzle128B), idesc_bf16(128, D, 0, 1),
+                            (k != first(w) || s > 0));
           }
-          if (leader && (kSplit || k == (w ? last1 : last0))) mma_commit(&o_full[w]);
+          if (leader) {
+            if (kSplit) mma_commit(&pv_done[w]);
+            if (k == last(w)) mma_commit(&o_full[w]);
+          }
         };
-        auto landed = [&](uint32_t x) { return ok = warp_wait(&kv_full[x % kSlots], (x / kSlots) & 1, status); };
-        if (!landed(ring)) break;
-        for (int w = 0; w < 2 && ok; ++w)
-          if (U.sees(w, 0)) scores(w, 0, ring % kSlots);
-        if (!ok) break;
-        if (leader) mma_commit(&kv_empty[ring % kSlots]);
-        for (int k = 0; k < nk && ok; ++k) {
-          const uint32_t xv = ring + 2 * k + 1, xk = xv + 1;
-          const bool more = k + 1 < nk;
-          if (kSplit && more) {
-            if (!landed(xk)) break;
-            for (int w = 0; w < 2 && ok; ++w)
-              if (U.sees(w, k + 1)) scores(w, k + 1, xk % kSlots);
-            if (!ok) break;
-            if (leader) mma_commit(&kv_empty[xk % kSlots]);
-          }
-          if (!landed(xv)) break;
-          for (int w = 0; w < 2 && ok; ++w) {
-            if (U.sees(w, k)) values(w, k, xv % kSlots);
-            // its next scores go over P, right behind its product; the other tile's softmax runs meanwhile
-            if (!kSplit && ok && more && U.sees(w, k + 1) && landed(xk)) scores(w, k + 1, xk % kSlots);
-          }
-          if (ok && leader) {
-            mma_commit(&kv_empty[xv % kSlots]);
-            if (!kSplit && more) mma_commit(&kv_empty[xk % kSlots]);
-          }
+        for (int w = w0; w < w1 && ok; ++w) {
+          if (sees(w, 0)) scores(w, 0);
+          else if (kSplit) landed(ring);           // (a tile that nobody else of this issuer has waited for)
         }
+        if (ok) release(ring);
+        for (int k = 0; k < nk && ok; ++k) {
+          for (int w = w0; w < w1 && ok; ++w) {
+            const bool next = k + 1 < nk && sees(w, k + 1);
+            if (kSplit && next) scores(w, k + 1);
+            if (ok && sees(w, k)) values(w, k);
+            else if (kSplit && ok) landed(ring + 2 * k + 1);
+            if (kSplit && ok && !next && k + 1 < nk) landed(ring + 2 * k + 2);
+            if (!kSplit && next && ok) scores(w, k + 1);     // over P, right behind its product
+          }
+          if (!ok) break;
+          release(ring + 2 * k + 1);
+          if (k + 1 < nk) release(ring + 2 * k + 2);
+        }
+        ++nq0;
+        if (ntq > 1) ++nq1;
         ring += 2 * nk;
       }
       // every MMA has finished before tensor memory is freed
       if (leader) {
-        mma_commit(drain);
-        mbar_wait(drain, 0, status);
+        mma_commit(&drain[w0]);
+        mbar_wait(&drain[w0], 0, status);
       }
     }
-  } else {
+  } else if (warp < 12) {
     // ------------------------------------------------------------ softmax
     setmaxnreg_inc<kRegSoftmax>();
     const int w = (warp - 4) >> 2, quarter = warp & 3;
@@ -275,70 +324,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_addr = lane_base + w * 128, o_addr = lane_base + kO + w * D;
     const uint32_t p_addr = kSplit ? lane_base + kP + 64 * w : s_addr;
-    float* tab = reinterpret_cast<float*>(smem + L::kBias) + w * kBiasTab;
+    float* inv_l = reinterpret_cast<float*>(smem + L::kInv) + w * 128;
     const int R = bias_range(p), near = near_tiles(R);
     const float scale2 = p.scale2, inv_scale2 = 1.f / p.scale2;
-    uint32_t ring = 0, ns = 0, no = 0;
-    int staged = -1;
+    uint32_t ring = 0, ns = 0, nu = 0;
     bool ok = true;
-    HeadBias HB{};
-    RawUnit raw;
-    raw.fetch(p, pv, 0, n_units);
-    // a warp whose wait ran out goes on through the units without work: it still meets its
-    // warpgroup at the barriers around the bias
-    for (int n = 1; raw.i >= 0; ++n) {
-      const Unit U = make_unit(p, raw);
-      raw.fetch(p, pv, n, n_units);
-      if constexpr (BIAS) {
-        if (staged != U.h) {      // each warpgroup has a table: the two need not meet
-          HB = head_bias(p, U.h);
-          named_bar_sync(1 + w, 128);
-          stage_bias(tab, p, U.h, r, 128);
-          named_bar_sync(1 + w, 128);
-          staged = U.h;
-        }
+    for (int n = 0; ok; ++n) {
+      const Unit U = read_unit(units, unit_full, n, true, ok, status);
+      if (U.ntq == 0) break;
+      const float* tab = reinterpret_cast<const float*>(smem + L::kBias) + (n & 1) * kBiasTab;
+      const int nk = U.kt.n, skip = w >= U.ntq ? -2 : (w ? U.skip1 : U.skip0);
+      HeadBias HB{};
+      if constexpr (BIAS) {      // (of every unit, so that the barrier's phases stay in step)
+        ok = __all_sync(0xffffffffu, mbar_wait(&tab_full[n & 1], (n >> 1) & 1, status));
+        if (!ok) break;
+        HB = head_bias(tab);
       }
-      if (!ok) continue;
+      if (skip == -2) {
+        ring += 2 * nk;
+        continue;
+      }
       const int t = U.t0 + w, qi = t * kTile + r;
       const int lo = p.win.left < 0 ? 0 : max(0, qi - p.win.left);
       const int hi = p.win.right < 0 ? U.len - 1 : min(U.len - 1, qi + p.win.right);
       const FullTiles full = full_tiles(t, U.len, U.pre, p.win);
-      const int skip = w >= U.ntq ? -2 : (w ? U.skip1 : U.skip0);
+      const float steep = HB.slope2 * (float)(kTile - 1);
       float m = -INFINITY;
       float2 la = make_float2(0.f, 0.f), lb = la;
       bool first = true;
-      for (int k = 0; k < U.kt.n && skip != -2; ++k) {
+      for (int k = 0; k < nk; ++k) {
         if (k == skip) continue;
         const int u = U.kt.tile(k);
         TileBias B{};
         if constexpr (BIAS) B = tile_bias(tab, HB, R, near, inv_scale2, t, u, u * kTile - qi);
-        const bool masked = !full.has(u);
-        const bool plain = !BIAS || B.plain();
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[w], ns++ & 1, status));
+        const bool seen = full.has(u);
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[w], ns & 1, status));
         if (!ok) break;
         tc_fence_after();
         uint32_t v[4][32];
         float cm[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) tmem_ld32_max(s_addr + 32 * g, v[g], cm[g]);
+        for (int g = 0; g < 4; ++g) {
+          if constexpr (CAP) tmem_ld32_absmax(s_addr + 32 * g, v[g], cm[g]);
+          else tmem_ld32_max(s_addr + 32 * g, v[g], cm[g]);
+        }
         tmem_ld_wait();
         if (kSplit) {
           tc_fence_before();
           mbar_arrive(&s_free[w]);
         }
-        float mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);      // of the raw products, from the load
+        float mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);      // of the raw products, or of their magnitudes
+        // form 0: v f + n; 1, 2: capped by 3 or 5 coefficients, then as 0; 3: v f + n + slope column
+        int form = 0;
+        bool quick = seen && (!BIAS || !B.tab);
         if constexpr (CAP) {
-          cap_products(v, p.capf);
-          const float z = mx * p.capf.zscale;                       // monotone
-          mx = fabsf(z) < 1e-3f ? mx : p.capf.inv * tanh_any(z);
+          quick = quick && B.col == 0.f && !__any_sync(0xffffffffu, !(mx <= p.capf.t5 && mx * scale2 <= kLoose * 0.5f));
+          form = __any_sync(0xffffffffu, !(mx <= p.capf.t3)) ? 2 : 1;
+        } else if constexpr (BIAS) {
+          quick = quick && fabsf(steep) <= kLoose;
+          form = 3;
         }
-        const float f = BIAS ? B.factor(scale2) : scale2;
-        if (masked || !plain) {
+        if (!quick) {
+          form = 0;
+          if constexpr (CAP) cap_products(v, p.capf);
           if constexpr (BIAS) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) bias_chunk<1>(v[g], 32 * g, scale2, B);
           }
-          if (masked) {
+          if (!seen) {
             const int c = u * kTile;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -355,7 +408,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int g = 0; g < 4; ++g) cm[g] = fmax3(cm[g], __uint_as_float(v[g][j]), __uint_as_float(v[g][j + 1]));
           mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);
         }
+        const float f = BIAS ? B.factor(scale2) : scale2;
         mx = fmaf(mx, f, B.c);
+        if (BIAS && quick) mx += fmaxf(u < t ? steep : -steep, 0.f);
         if (first) {
           m = mx;
         } else if (__any_sync(0xffffffffu, mx > m + kRescaleAbove)) {
@@ -365,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lb = fmul2(lb, make_float2(alpha, alpha));
           m = m_new;
           if (kSplit) {                // the last product has to be in
-            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[w], no & 1, status));
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[w], (ns - 1) & 1, status));
             if (!ok) break;
             tc_fence_after();
           }
@@ -388,78 +443,152 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
         }
         const float neg = (m == -INFINITY ? 0.f : -m) + B.c;
-        const float2 f2 = make_float2(f, f), n2 = make_float2(neg, neg);
         // P in two halves of 64 keys: the first one's product starts while the second is computed
+        auto exps = [&](auto FORM) {
+          constexpr int kForm = decltype(FORM)::value;
+          const float2 f2 = make_float2(f, f), n2 = make_float2(neg, neg);
+          const float s2 = B.col * scale2;
+          const CapForm& F = p.capf;
+          auto arg = [&](int g, int c) {
+            const float2 x = pair_of(v[g], c);
+            if constexpr (kForm == 1 || kForm == 2) {       // x (scale2 + scale2 t(x^2)) + n
+              const float2 q = fmul2(x, x);
+              float2 y;
+              if constexpr (kForm == 1) {
+                y = ffma2(q, F.e3[3], F.e3[2]);
+                y = ffma2(q, y, F.e3[1]);
+                y = ffma2(q, y, F.e3[0]);
+              } else {
+                y = ffma2(q, F.e5[5], F.e5[4]);
+                y = ffma2(q, y, F.e5[3]);
+                y = ffma2(q, y, F.e5[2]);
+                y = ffma2(q, y, F.e5[1]);
+                y = ffma2(q, y, F.e5[0]);
+              }
+              return ffma2(x, y, n2);
+            } else if constexpr (kForm == 3) {
+              const float j = (float)(32 * g + c);
+              return ffma2(x, f2, make_float2(fmaf(s2, j, neg), fmaf(s2, j + 1.f, neg)));
+            } else {
+              return ffma2(x, f2, n2);
+            }
+          };
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
 #pragma unroll
-          for (int j = 0; j < 64; j += 4) {
-            const int g = 2 * half + j / 32, c = j % 32;
-            float2 e0 = ffma2(pair_of(v[g], c), f2, n2), e1 = ffma2(pair_of(v[g], c + 2), f2, n2);
-            e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
-            e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
-            la = fadd2(la, e0);
-            lb = fadd2(lb, e1);
-            const __nv_bfloat162 b0 = __floats2bfloat162_rn(e0.x, e0.y), b1 = __floats2bfloat162_rn(e1.x, e1.y);
-            pk[j / 2] = *reinterpret_cast<const uint32_t*>(&b0);
-            pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&b1);
+            for (int j = 0; j < 64; j += 4) {
+              const int g = 2 * half + j / 32, c = j % 32;
+              float2 e0 = arg(g, c), e1 = arg(g, c + 2);
+              e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
+              e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
+              la = fadd2(la, e0);
+              lb = fadd2(lb, e1);
+              const __nv_bfloat162 b0 = __floats2bfloat162_rn(e0.x, e0.y), b1 = __floats2bfloat162_rn(e1.x, e1.y);
+              pk[j / 2] = *reinterpret_cast<const uint32_t*>(&b0);
+              pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&b1);
+            }
+            if (kSplit && half == 0 && ns) {       // the last P has been read
+              ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[w], (ns - 1) & 1, status));
+              if (!ok) return;
+              tc_fence_after();
+            }
+            tmem_st32(p_addr + 32 * half, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&p_full[2 * w + half]);
           }
-          if (kSplit && half == 0 && !first) {       // the last P has been read
-            ok = __all_sync(0xffffffffu, mbar_wait(&o_full[w], no++ & 1, status));
-            if (!ok) break;
-            tc_fence_after();
-          }
-          tmem_st32(p_addr + 32 * half, pk);
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&p_full[2 * w + half]);
+        };
+        if constexpr (CAP) {
+          if (form == 1) exps(std::integral_constant<int, 1>{});
+          else if (form == 2) exps(std::integral_constant<int, 2>{});
+          else exps(std::integral_constant<int, 0>{});
+        } else if constexpr (BIAS) {
+          if (form == 3 && B.col != 0.f) exps(std::integral_constant<int, 3>{});
+          else exps(std::integral_constant<int, 0>{});
+        } else {
+          exps(std::integral_constant<int, 0>{});
         }
-        first = false;
         if (!ok) break;
+        ++ns;
+        first = false;
       }
-      ring += 2 * U.kt.n;
-      if (!ok || w >= U.ntq) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[w], no++ & 1, status));
-      if (!ok) continue;
-      tc_fence_after();
+      ring += 2 * nk;
+      if (!ok) break;
+      // the last unit's 1 / l has been used
+      if (nu && !(ok = __all_sync(0xffffffffu, mbar_wait(&o_free[w], (nu - 1) & 1, status)))) break;
+      ++nu;
       const float l = (la.x + la.y) + (lb.x + lb.y);
-      const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);     // a row that sees nothing: O = 0
-      const bool al32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-      const bool row_valid = qi < U.len;
-      const int64_t tok = (int64_t)U.start + qi;
-      __nv_bfloat16* orow = p.out + (tok * p.hq + U.h) * D;
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(o_addr + 32 * c, o);
-        tmem_ld_wait();
-        uint32_t pk[16];
+      inv_l[r] = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);     // a row that sees nothing: O = 0
+      mbar_arrive(&l_ready[w]);
+      if (qi < U.len) p.lse[(int64_t)U.h * p.T + U.start + qi] = l == 0.f ? INFINITY : (m + __log2f(l)) * kLn2;
+    }
+  } else {
+    // ------------------------------------------------------------ bias tables, O
+    setmaxnreg_dec<kRegAux>();
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
+    float* tab = reinterpret_cast<float*>(smem + L::kBias);
+    const bool al32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+    uint32_t nu[2] = {0, 0};
+    bool ok = true;
+    Unit U = read_unit(units, unit_full, 0, true, ok, status);
+    if (BIAS && U.ntq) {
+      stage_bias(tab, p, U.h, r, 128);
+      mbar_arrive(&tab_full[0]);
+    }
+    for (int n = 0; ok && U.ntq; ++n) {
+      const int h = U.h, t0 = U.t0, ntq = U.ntq, start = U.start, len = U.len;
+      U = read_unit(units, unit_full, n + 1, true, ok, status);
+      if (BIAS && U.ntq) {            // into the table of the last unit but one, whose O is out
+        stage_bias(tab + ((n + 1) & 1) * kBiasTab, p, U.h, r, 128);
+        mbar_arrive(&tab_full[(n + 1) & 1]);
+      }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const __nv_bfloat162 b2 =
-              __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-          pk[j] = *reinterpret_cast<const uint32_t*>(&b2);
-        }
-        if (row_valid) {
-          __nv_bfloat16* dst = orow + 32 * c;
-          if (al32) {
-            st_global_v8(dst, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
-            st_global_v8(dst + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
-          } else {
+      for (int w = 0; w < 2; ++w) {
+        if (w >= ntq || !ok) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(&l_ready[w], nu[w] & 1, status) && mbar_wait(&o_full[w], nu[w] & 1, status));
+        if (!ok) continue;
+        ++nu[w];
+        tc_fence_after();
+        const float inv = reinterpret_cast<const float*>(smem + L::kInv)[w * 128 + r];
+        const int qi = (t0 + w) * kTile + r;
+        __nv_bfloat16* orow = p.out + (((int64_t)start + qi) * p.hq + h) * D;
+#pragma unroll 2
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(lane_base + kO + w * D + 32 * c, o);
+          tmem_ld_wait();
+          uint32_t pk[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4*>(dst + 8 * q) = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 b2 =
+                __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+            pk[j] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          if (c == D / 32 - 1) {
+            tc_fence_before();
+            mbar_arrive(&o_free[w]);
+          }
+          if (qi < len) {
+            __nv_bfloat16* dst = orow + 32 * c;
+            if (al32) {
+              st_global_v8(dst, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
+              st_global_v8(dst + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(dst + 8 * q) = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+            }
           }
         }
       }
-      tc_fence_before();
-      if (row_valid) p.lse[(int64_t)U.h * p.T + tok] = l == 0.f ? INFINITY : (m + __log2f(l)) * kLn2;
+      if (r == 0 && ok) mbar_arrive(unit_done);
     }
     // rows outside every document: O = 0, LSE = +inf
     const int valid = p.plan[kPlanValid];
     const int64_t rows = (int64_t)(p.T - valid) * p.hq;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x - 128; i < rows; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = (int64_t)blockIdx.x * 128 + r; i < rows; i += (int64_t)gridDim.x * 128) {
       const int64_t row = valid + i / p.hq;
       const int h = (int)(i % p.hq);
       uint4* dst = reinterpret_cast<uint4*>(p.out + (row * p.hq + h) * D);
