@@ -23,10 +23,11 @@ namespace flamia {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kCompute = 512;    // compute threads: four warpgroups, each 32 of a tile's 128 columns
+constexpr int kThreads = 128 + kCompute;
 constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
-constexpr int kRegCtl = 88, kRegCompute = 208;
-static_assert(kRegCtl * 128 + kRegCompute * 256 <= kLaunchRegs * kThreads, "register split");
+constexpr int kRegCtl = 64, kRegCompute = 104;
+static_assert(kRegCtl * 128 + kRegCompute * kCompute <= kLaunchRegs * kThreads, "register split");
 constexpr int kStats = 4;        // staged LSE / D rows in flight
 
 // ---------------------------------------------------------------- D = rowsum(dO o O)
@@ -99,6 +100,14 @@ __device__ __forceinline__ uint32_t pack2(float2 x) {
   const __nv_bfloat162 b2 = __floats2bfloat162_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&b2);
 }
+// dP where P is not 0: rows of another document, or of nobody, may hold anything, and weight
+// 0 does not silence an infinity.  (In its own branch: selects in the loops over every tile run
+// on all of them, two operations an element.)
+__device__ __forceinline__ void drop_hidden(uint32_t (&dp)[32], const uint32_t (&pr)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (__uint_as_float(pr[j]) == 0.f) dp[j] = 0u;
+}
 // 1 - tanh^2 from the capped product y = tanh / zscale.
 __device__ __forceinline__ float2 cap_slope(float2 y, float zscale) {
   const float2 t = fmul2(y, make_float2(zscale, zscale));
@@ -120,7 +129,8 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, u
 // behind dK (while the next P^T is computed), across units too: K is free once the unit's
 // last S^T is done, V once its last dP^T is.
 // Roles: warp 0 TMA, warp 1 MMA, warp 2 TMEM, warp 3 stages LSE and D of a step's queries,
-// warps 4-11 compute: thread = key row, warpgroup = 64 of the 128 query columns.
+// warps 4-19 compute: thread = key row, warpgroup = 32 of the 128 query columns.  A warp's work
+// on a step is a chain of loads, exponentials and stores; four warps a scheduler hide it.
 // TMEM columns: dV [0, D), dK [128, 128 + D), S^T [256, 384), dP^T [384, 512).
 template <int D>
 struct DkvSmem {
@@ -131,8 +141,8 @@ struct DkvSmem {
   static constexpr int kStat = 6 * kTileBytes;                 // [kStats][-LSE log2 e 128, D 128]
   static constexpr int kBias = kStat + kStats * 1024;          // [kBiasTab]
   static constexpr int kAcc = kBias + kBiasTab * 4;      // [2 R + 1] drel of the current head
-  static constexpr int kDiag = kAcc + (2 * FLAMIA_REL_MAX + 2) * 4;   // [2][8 warps][96]
-  static constexpr int kBar = (kDiag + 2 * 8 * 96 * 4 + 15) & ~15;
+  static constexpr int kDiag = kAcc + (2 * FLAMIA_REL_MAX + 2) * 4;   // [2][16 warps][64]
+  static constexpr int kBar = (kDiag + 2 * 16 * 64 * 4 + 15) & ~15;
   static constexpr int kBytes = kBar + 256;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -233,13 +243,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 14; ++i) mbar_init(bars + i, 1);
-    mbar_init(p_ready, 256);
-    mbar_init(ds_ready, 256);
+    mbar_init(p_ready, kCompute);
+    mbar_init(ds_ready, kCompute);
     mbar_init(acc_full, 1);
     mbar_init(drain, 1);
     for (int i = 0; i < kStats; ++i) {
       mbar_init(&st_full[i], 32);
-      mbar_init(&st_empty[i], 256);
+      mbar_init(&st_empty[i], kCompute);
     }
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int s = 0; s < kTile / 16; ++s)
           if (leader)
-            mma_bf16_ta(tbase + d, tbase + a + (s < 4 ? 8 * s : 64 + 8 * (s - 4)),
+            mma_bf16_ta(tbase + d, tbase + a + 32 * (s >> 1) + 8 * (s & 1),
                         sdesc_at(base16, b_off + s * 2048, kTile * 128, 1024, kSwizzle128B), idesc_bf16(128, D, 0, 1),
                         (!first || s > 0));
       };
@@ -377,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane, tid = threadIdx.x - 128;
     const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t s_addr = lane_base + kTS + 64 * w, dp_addr = lane_base + kTP + 64 * w;
+    const uint32_t s_addr = lane_base + kTS + 32 * w, dp_addr = lane_base + kTP + 32 * w;
     float* tab = reinterpret_cast<float*>(smem + L::kBias);
     float* acc = reinterpret_cast<float*>(smem + L::kAcc);
     const int R = bias_range(p);
@@ -396,39 +406,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = S.t, kj = U.u * kTile + r;
       if constexpr (BIAS != 0) {
         if (S.head_first() && staged != S.h) {
-          named_bar_sync(1, 256);
-          stage_bias(tab, p, S.h, tid, 256);
-          named_bar_sync(1, 256);
+          named_bar_sync(1, kCompute);
+          stage_bias(tab, p, S.h, tid, kCompute);
+          named_bar_sync(1, kCompute);
           HB = head_bias(tab);
           staged = S.h;
         }
         if (BIAS == 2 && S.head_first()) {
-          for (int i = tid; i < 2 * R + 1; i += 256) acc[i] = 0.f;
+          for (int i = tid; i < 2 * R + 1; i += kCompute) acc[i] = 0.f;
           far_lo = far_hi = lost_lo = lost_hi = 0.f;
-          named_bar_sync(1, 256);
+          named_bar_sync(1, kCompute);
         }
       }
       float du_lo = 0.f;      // (BIAS 2) sum of the thread's dU of a far tile
-      uint32_t v[2][32];
+      uint32_t v[1][32];
       if (ok) {
         ok = __all_sync(0xffffffffu, mbar_wait(&st_full[g % kStats], (g / kStats) & 1, status) &&
                                          mbar_wait(s_full, g & 1, status));
       }
-      const float* nl = reinterpret_cast<const float*>(smem + L::kStat) + (g % kStats) * 256 + 64 * w;
+      const float* nl = reinterpret_cast<const float*>(smem + L::kStat) + (g % kStats) * 256 + 32 * w;
       if (ok) {
         tc_fence_after();
         tmem_ld32(s_addr, v[0]);
-        tmem_ld32(s_addr + 32, v[1]);
         tmem_ld_wait();
-        uint32_t gr[2][32];
+        uint32_t gr[1][32];
         TileBias B{};
-        if constexpr (BIAS != 0) B = tile_bias(tab, HB, R, near, inv_scale2, t, U.u, kj - (t * kTile + 64 * w));
+        if constexpr (BIAS != 0) B = tile_bias(tab, HB, R, near, inv_scale2, t, U.u, kj - (t * kTile + 32 * w));
         const float f = BIAS != 0 ? B.factor(scale2) : scale2;
         const bool masked = t < U.full.x || t > U.full.y;
+        const bool edge = (t + 1) * kTile > U.len || (BIAS == 2 && (U.u + 1) * kTile > U.len);
         if constexpr (CAP) {
           cap_products(v, p.capf);
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 1; ++c)
 #pragma unroll
             for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), p.capf.zscale));
         }
@@ -439,11 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.win.right >= 0) lo = kj - p.win.right;
           if (p.win.left >= 0) hi = min(hi, kj + p.win.left);
         }
-        lo -= t * kTile + 64 * w;
-        hi -= t * kTile + 64 * w;
-        uint32_t pk[32];
+        lo -= t * kTile + 32 * w;
+        hi -= t * kTile + 32 * w;
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 1; ++c) {
           if constexpr (BIAS != 0) bias_chunk<-1>(v[c], 32 * c, scale2, B);
           if (masked) {
             const uint32_t see = column_mask(lo, hi, 0, 32 * c);
@@ -473,12 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; j += 2) put_pair(v[c], j, fmul2(pair_of(v[c], j), pair_of(gr[c], j)));
           }
         }
-        tmem_st32(s_addr, pk);
+        tmem_st16(s_addr, pk);
         tmem_st_wait();
         if ((t + 1) * kTile > U.len) {
           // queries behind the document: the products below sum over them
           ok = __all_sync(0xffffffffu, mbar_wait(&do_full[g & 1], (g >> 1) & 1, status));
-          if (ok && t * kTile + r >= U.len)
+          if (ok && w < 2 && t * kTile + r >= U.len)
             clear_row<D>(smem + (w ? L::kQ : L::kDO) + (g & 1) * L::kTileBytes, r);
           fence_proxy_async_smem();
         }
@@ -491,21 +501,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < 1; ++c) {
             uint32_t dp[32];
             tmem_ld32(dp_addr + 32 * c, dp);
             tmem_ld_wait();
+            if (edge) drop_hidden(dp, v[c]);
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
               const float4 d4 = *reinterpret_cast<const float4*>(nl + 128 + 32 * c + j);
               float2 a0 = fmul2(pair_of(v[c], j), fadd2(pair_of(dp, j), make_float2(-d4.x, -d4.y)));
               float2 a1 = fmul2(pair_of(v[c], j + 2), fadd2(pair_of(dp, j + 2), make_float2(-d4.z, -d4.w)));
-              if (masked) {     // a hidden pair's dP may be anything
-                a0.x = pair_of(v[c], j).x == 0.f ? 0.f : a0.x;
-                a0.y = pair_of(v[c], j).y == 0.f ? 0.f : a0.y;
-                a1.x = pair_of(v[c], j + 2).x == 0.f ? 0.f : a1.x;
-                a1.y = pair_of(v[c], j + 2).y == 0.f ? 0.f : a1.y;
-              }
               if constexpr (BIAS == 2) {
                 put_pair(v[c], j, a0);
                 put_pair(v[c], j + 2, a1);
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           du_lo = sum.x + sum.y;
-          tmem_st32(dp_addr, pk);
+          tmem_st16(dp_addr, pk);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(ds_ready);
@@ -536,25 +541,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // sums along the diagonals: a running value moves one lane up per column, so it stays on its
           // diagonal; lane 31's is complete
-          float* dg = reinterpret_cast<float*>(smem + L::kDiag) + buf * (8 * 96);
-          float* mine = dg + (warp - 4) * 96;
+          float* dg = reinterpret_cast<float*>(smem + L::kDiag) + buf * (16 * 64);
+          float* mine = dg + (warp - 4) * 64;
           float run = 0.f;
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            run += __uint_as_float(v[c / 32][c % 32]);
-            if (lane == 31) mine[94 - c] = run;
+          for (int c = 0; c < 32; ++c) {
+            run += __uint_as_float(v[0][c]);
+            if (lane == 31) mine[62 - c] = run;
             run = __shfl_up_sync(0xffffffffu, run, 1);
             if (lane == 0) run = 0.f;
           }
           if (lane > 0) mine[lane - 1] = run;      // after the last shift lane l holds diagonal l - 1
-          named_bar_sync(1, 256);
+          named_bar_sync(1, kCompute);
           if (tid < 255) {
             const int x = tid - 127;               // key row - query column
             float s = 0.f;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const int at = x - 32 * (q & 3) + 64 * (q >> 2) + 63;
-              if (at >= 0 && at < 95) s += dg[q * 96 + at];
+            for (int q = 0; q < 16; ++q) {
+              const int at = x - 32 * (q & 3) + 32 * (q >> 2) + 31;
+              if (at >= 0 && at < 63) s += dg[q * 64 + at];
             }
             const int rel = tile_rel + x;
             if (rel <= -R) add_comp(far_lo, lost_lo, s);
@@ -565,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (S.head_last()) {
           // the head's sums of this key tile: the two ends over all threads in a fixed order
-          float* red = reinterpret_cast<float*>(smem + L::kDiag) + buf * (8 * 96);
+          float* red = reinterpret_cast<float*>(smem + L::kDiag) + buf * (16 * 64);
           far_lo += lost_lo;
           far_hi += lost_hi;
 #pragma unroll
@@ -577,17 +582,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             red[2 * (warp - 4)] = far_lo;
             red[2 * (warp - 4) + 1] = far_hi;
           }
-          named_bar_sync(1, 256);
+          named_bar_sync(1, kCompute);
           float* part = p.drel_part + ((size_t)S.h * p.plan[kPlanBwdItems] + U.item) * (2 * R + 1);
-          for (int i = tid; i < 2 * R + 1; i += 256) {
+          for (int i = tid; i < 2 * R + 1; i += kCompute) {
             float s = acc[i];
             if (i == 0 || i == 2 * R) {
               s = 0.f;
-              for (int q = 0; q < 8; ++q) s += red[2 * q + (i ? 1 : 0)];
+              for (int q = 0; q < 16; ++q) s += red[2 * q + (i ? 1 : 0)];
             }
             part[i] = s;
           }
-          named_bar_sync(1, 256);
+          named_bar_sync(1, kCompute);
           buf ^= 1;
         }
       }
@@ -597,8 +602,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const bool valid = kj < U.len;
           const int64_t at = ((int64_t)(U.start + kj) * p.hkv + U.hk) * D;
-          if (w == 0) store_acc<D>(lane_base + kTV, p.dv + at, 1.f, valid);
-          else store_acc<D>(lane_base + kTK, p.dk + at, p.scale, valid);
+          const int c = (w & 1) * (D / 2);
+          if (w < 2) store_acc<D / 2>(lane_base + kTV + c, p.dv + at + c, 1.f, valid);
+          else store_acc<D / 2>(lane_base + kTK + c, p.dk + at + c, p.scale, valid);
           tc_fence_before();
         }
       }
@@ -703,9 +709,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4 * kStages + 4; ++i) mbar_init(bars + i, 1);
-    mbar_init(s_free, 256);
-    mbar_init(ds_ready, 256);
-    mbar_init(q_ready, 256);
+    mbar_init(s_free, kCompute);
+    mbar_init(ds_ready, kCompute);
+    mbar_init(q_ready, kCompute);
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -789,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int s = 0; s < kTile / 16; ++s)
           if (leader)
-            mma_bf16_ta(tbase + kTQ, tbase + kTP + (s < 4 ? 8 * s : 64 + 8 * (s - 4)),
+            mma_bf16_ta(tbase + kTQ, tbase + kTP + 32 * (s >> 1) + 8 * (s & 1),
                         sdesc_at(base16, L::kK + b * L::kTileBytes + s * 2048, kTile * 128, 1024, kSwizzle128B),
                         idesc_bf16(128, D, 0, 1), (!first || s > 0));
         if (leader) {
@@ -810,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane, tid = threadIdx.x - 128;
     const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t s_addr = lane_base + kTS + 64 * w, dp_addr = lane_base + kTP + 64 * w;
+    const uint32_t s_addr = lane_base + kTS + 32 * w, dp_addr = lane_base + kTP + 32 * w;
     float* tab = reinterpret_cast<float*>(smem + L::kBias);
     const int R = bias_range(p);
     const int near = near_tiles(R);
@@ -822,29 +828,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     int lo = 0, hi = 0;
     FullTiles full{};
     QuerySteps S{};
-    // The unit's A operands (warpgroup 0: Q, 1: dO; rows behind the document as zeros), LSE and D.
+    // The unit's A operands (warpgroups 0 and 1: Q, 2 and 3: dO; rows behind the document as zeros), LSE and D.
     auto start_unit = [&]() {
       const int qi = S.t * kTile + r;
       const bool in = qi < S.len;
       const int64_t tok = (int64_t)S.start + qi;
-      const uint4* src = reinterpret_cast<const uint4*>((w ? p.dout : p.q) + (tok * p.hq + S.h) * D);
-      uint32_t a[D / 2];
+      const int c = (w & 1) * (D / 2);
+      const uint4* src = reinterpret_cast<const uint4*>((w < 2 ? p.q : p.dout) + (tok * p.hq + S.h) * D + c);
+      uint32_t a[D / 4];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = in ? src[c] : make_uint4(0, 0, 0, 0);
-        a[4 * c] = x.x;
-        a[4 * c + 1] = x.y;
-        a[4 * c + 2] = x.z;
-        a[4 * c + 3] = x.w;
+      for (int i = 0; i < D / 16; ++i) {
+        const uint4 x = in ? src[i] : make_uint4(0, 0, 0, 0);
+        a[4 * i] = x.x;
+        a[4 * i + 1] = x.y;
+        a[4 * i + 2] = x.z;
+        a[4 * i + 3] = x.w;
       }
       nl = in ? -p.lse[(int64_t)S.h * p.T + tok] * kLog2e : -INFINITY;
       dv = in ? p.dvec[(int64_t)S.h * p.T + tok] : 0.f;
       lo = p.win.left < 0 ? 0 : max(0, qi - p.win.left);
       hi = p.win.right < 0 ? S.len - 1 : min(S.len - 1, qi + p.win.right);
       full = full_tiles(S.t, S.len, S.pre, p.win);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        tmem_st32(lane_base + (w ? kTB : kTA) + 32 * c, reinterpret_cast<uint32_t(&)[32]>(a[32 * c]));
+      const uint32_t at = lane_base + (w < 2 ? kTA : kTB) + c / 2;
+      if constexpr (D == 128) tmem_st32(at, a);
+      else tmem_st16(at, a);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(q_ready);
@@ -855,9 +862,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; more; ++g) {
       if constexpr (BIAS) {
         if (S.first() && staged != S.h) {
-          named_bar_sync(1, 256);
-          stage_bias(tab, p, S.h, tid, 256);
-          named_bar_sync(1, 256);
+          named_bar_sync(1, kCompute);
+          stage_bias(tab, p, S.h, tid, kCompute);
+          named_bar_sync(1, kCompute);
           HB = head_bias(tab);
           staged = S.h;
         }
@@ -866,27 +873,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, g & 1, status));
       if (ok) {
         tc_fence_after();
-        uint32_t v[2][32], gr[2][32];
+        uint32_t v[1][32], gr[1][32];
         tmem_ld32(s_addr, v[0]);
-        tmem_ld32(s_addr + 32, v[1]);
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(s_free);
         TileBias B{};
-        if constexpr (BIAS) B = tile_bias(tab, HB, R, near, inv_scale2, t, u, u * kTile + 64 * w - qi);
+        if constexpr (BIAS) B = tile_bias(tab, HB, R, near, inv_scale2, t, u, u * kTile + 32 * w - qi);
         const float f = BIAS ? B.factor(scale2) : scale2;
         const bool masked = !full.has(u);
         if constexpr (CAP) {
           cap_products(v, p.capf);
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 1; ++c)
 #pragma unroll
             for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), p.capf.zscale));
         }
-        const int c0 = u * kTile + 64 * w;
+        const int c0 = u * kTile + 32 * w;
         const float2 f2 = make_float2(f, f), n2 = make_float2(nl + B.c, nl + B.c);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 1; ++c) {
           if constexpr (BIAS) bias_chunk<1>(v[c], 32 * c, scale2, B);
           if (masked) {
             const uint32_t see = column_mask(lo - c0, hi - c0, S.pre - c0, 32 * c);
@@ -905,24 +911,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           tc_fence_after();
           const float2 d2 = make_float2(-dv, -dv);
-          uint32_t pk[32];
+          uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < 1; ++c) {
             uint32_t dp[32];
             tmem_ld32(dp_addr + 32 * c, dp);
             tmem_ld_wait();
+            if ((u + 1) * kTile > S.len) drop_hidden(dp, v[c]);
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
               const float2 e = pair_of(v[c], j);
-              float2 a = fmul2(e, fadd2(pair_of(dp, j), d2));
-              if (masked) {     // a hidden pair's dP may be anything
-                a.x = e.x == 0.f ? 0.f : a.x;
-                a.y = e.y == 0.f ? 0.f : a.y;
-              }
+              const float2 a = fmul2(e, fadd2(pair_of(dp, j), d2));
               pk[16 * c + j / 2] = pack2(a);
             }
           }
-          tmem_st32(dp_addr, pk);
+          tmem_st16(dp_addr, pk);
           tmem_st_wait();
           if ((u + 1) * kTile > S.len) {       // keys behind the document: dQ sums over them
             if (w == 0 && u * kTile + r >= S.len) clear_row<D>(smem + L::kK + (g % kStages) * L::kTileBytes, r);
@@ -944,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(acc_full, units++ & 1, status));
         if (ok) {
           tc_fence_after();
-          store_acc<D / 2>(lane_base + kTQ + w * (D / 2), p.dq + (tok * p.hq + h) * D + w * (D / 2), p.scale, valid);
+          if (w < D / 32) store_acc<32>(lane_base + kTQ + 32 * w, p.dq + (tok * p.hq + h) * D + 32 * w, p.scale, valid);
           tc_fence_before();
         }
       }
