@@ -503,31 +503,38 @@ class FlamiaScoredAttention:
         self._want("k", k, (self.T, self.hkv, self.d), torch.bfloat16)
         self._want("v", v, (self.T, self.hkv, self.d), torch.bfloat16)
 
-    def _on_device(self):
+    def _run(self, call, stream):
+        """call(stream handle) with the object's device current, on `stream` or its current stream."""
         import torch
         if self.device.type != "cuda":
             raise FlamiaError(f"FlamiaScoredAttention runs on a CUDA device, not on {self.device}")
-        return torch.cuda.device(self.device)
+        index = self.device.index
+        if torch._C._cuda_getDevice() != index:
+            with torch.cuda.device(self.device):
+                return call(_stream(stream))
+        if stream is None:             # the common case without the Python objects behind it: a small call is host-bound
+            stream = torch._C._cuda_getCurrentRawStream(index)
+        return call(_stream(stream))
 
     def plan_build(self, cu_seqlens, stream=None):
         import torch
         self._want("cu_seqlens", cu_seqlens, (self.N + 1,), torch.int32)
-        with self._on_device():
-            flamia_plan_build_window(cu_seqlens, self.N, self.T, self.causal, self.window[0], self.window[1], self.plan,
-                                     stream)
+        self._run(lambda stm: flamia_plan_build_window(cu_seqlens, self.N, self.T, self.causal, self.window[0],
+                                                       self.window[1], self.plan, stm), stream)
 
     def forward(self, q, k, v, cu_seqlens, softmax_scale: float = 0.0, slopes=None, prefix_lens=None, table=None,
                 stream=None):
         """(out bf16 [T, hq, d], lse fp32 [hq, T])."""
         self._inputs(q, k, v)
         o = self._options(cu_seqlens, slopes, prefix_lens, table)
-        with self._on_device():
-            stream = _stream(stream)
+
+        def call(stm):
             if table is not None:
-                flamia_relbias_expand(table, self.max_distance, self.bidirectional, self.rel_bias, stream)
+                flamia_relbias_expand(table, self.max_distance, self.bidirectional, self.rel_bias, stm)
             flamia_scored_fwd(q, k, v, cu_seqlens, self.N, self.plan, self.out, self.lse, softmax_scale, o, self.causal,
-                              stream)
-        return self.out, self.lse
+                              stm)
+            return self.out, self.lse
+        return self._run(call, stream)
 
     def backward(self, q, k, v, out, lse, dout, cu_seqlens, softmax_scale: float = 0.0, slopes=None, prefix_lens=None,
                  table=None, stream=None):
@@ -539,18 +546,18 @@ class FlamiaScoredAttention:
         self._want("dout", dout, (self.T, self.hq, self.d), torch.bfloat16)
         self._want("lse", lse, (self.hq, self.T), torch.float32)
         o = self._options(cu_seqlens, slopes, prefix_lens, table)
-        with self._on_device():
-            stream = _stream(stream)
+
+        def call(stm):
             if table is not None:
-                flamia_relbias_expand(table, self.max_distance, self.bidirectional, self.rel_bias, stream)
+                flamia_relbias_expand(table, self.max_distance, self.bidirectional, self.rel_bias, stm)
             flamia_scored_bwd(q, k, v, out, lse, dout, cu_seqlens, self.N, self.plan, self.dq, self.dk, self.dv,
                               self.workspace, self.drel_bias if table is not None else None, softmax_scale, o,
-                              self.causal, stream)
+                              self.causal, stm)
             if table is None:
                 return self.dq, self.dk, self.dv
-            flamia_relbias_reduce(self.drel_bias, self.max_distance, self.bidirectional, self.dtable, stream)
-        return self.dq, self.dk, self.dv, self.dtable
+            flamia_relbias_reduce(self.drel_bias, self.max_distance, self.bidirectional, self.dtable, stm)
+            return self.dq, self.dk, self.dv, self.dtable
+        return self._run(call, stream)
 
     def device_status(self, stream=None) -> int:
-        with self._on_device():
-            return flamia_get_device_status(self.plan, stream)
+        return self._run(lambda stm: flamia_get_device_status(self.plan, stm), stream)

@@ -128,14 +128,14 @@ __device__ __forceinline__ int unit_index(int k, int n_units) {
 __device__ __forceinline__ int prefix_of(const ScoredParams& p, int doc, int len) {
   return p.prefix ? min(max(p.prefix[doc], 0), len) : 0;
 }
-// Clear rows first .. 127 of a TMA-staged [128][D] bf16 tile (64-column boxes): the tile's
-// rows behind the document belong to the next one, or to nobody, and may hold anything;
-// weight 0 does not silence an infinity.  r: the calling thread's row.
-template <int D>
+// Clear row r of a TMA-staged [ROWS][D] bf16 tile (64-column boxes): a tile's rows
+// behind the document belong to the next one, or to nobody, and may hold anything;
+// weight 0 does not silence an infinity.
+template <int D, int ROWS = kTile>
 __device__ __forceinline__ void clear_row(uint8_t* tile, int r) {
 #pragma unroll
   for (int b = 0; b < D / 64; ++b) {
-    uint4* row = reinterpret_cast<uint4*>(tile + b * kTile * 128 + r * 128);
+    uint4* row = reinterpret_cast<uint4*>(tile + b * ROWS * 128 + r * 128);
 #pragma unroll
     for (int c = 0; c < 8; ++c) row[c] = make_uint4(0, 0, 0, 0);
   }

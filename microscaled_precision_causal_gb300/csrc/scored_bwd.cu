@@ -14,6 +14,7 @@
 // P and dS enter their products in bf16 (their partners are bf16): half a step of 2^-8 per
 // element, as the rounding of the gradients themselves; sums stay in fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "ptx.cuh"
 #include "scored.cuh"
@@ -114,36 +115,42 @@ __device__ __forceinline__ float2 cap_slope(float2 y, float zscale) {
   return ffma2(t, make_float2(-t.x, -t.y), make_float2(1.f, 1.f));
 }
 
-template <int D>
+template <int D, int ROWS = kTile>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int h, int row) {
-  mbar_arrive_expect_tx(bar, kTile * D * 2);
+  mbar_arrive_expect_tx(bar, ROWS * D * 2);
 #pragma unroll
-  for (int b = 0; b < D / 64; ++b) tma_load_3d(dst + b * kTile * 128, tm, bar, 64 * b, h, row);
+  for (int b = 0; b < D / 64; ++b) tma_load_3d(dst + b * ROWS * 128, tm, bar, 64 * b, h, row);
 }
 
 // ================================================================ dK, dV
 // One CTA per SM walks (key tile, kv head) units; a step is a query tile of one of the kv
 // head's query heads.  S^T = K Q^T and dP^T = V dO^T have keys in the TMEM lanes, so P^T and
 // dS^T are written back over their own columns and are the A operands of dV += P^T dO and
-// dK += dS^T Q.  The next step's S^T runs behind dV (while dS^T is computed), its dP^T
-// behind dK (while the next P^T is computed), across units too: K is free once the unit's
-// last S^T is done, V once its last dP^T is.
+// dK += dS^T Q.
+// A step's 128 queries go in two halves, each with its own 64-query operand tiles, products
+// and compute warps, half a step apart: while one half's P^T is computed the other's dS^T is,
+// so that the waits, loads and stores of the one hide behind the arithmetic of the other.  (As
+// one tile all warps were in the same phase and the kernel ran at its latencies: XXX.)  The
+// price is that a product with 64 columns reads more shared memory than it multiplies: 48
+// cycles instead of 32 for S^T and dP^T a step of 16.  K is free for the next unit once the
+// unit's last S^T is done, V once its last dP^T is.
 // Roles: warp 0 TMA, warp 1 MMA, warp 2 TMEM, warp 3 stages LSE and D of a step's queries,
-// warps 4-19 compute: thread = key row, warpgroup = 32 of the 128 query columns.  A warp's work
-// on a step is a chain of loads, exponentials and stores; four warps a scheduler hide it.
+// warps 4-19 compute: thread = key row, warpgroup = 32 of the 128 query columns, two a half.
 // TMEM columns: dV [0, D), dK [128, 128 + D), S^T [256, 384), dP^T [384, 512).
 template <int D>
 struct DkvSmem {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kK = 0, kV = kTileBytes;
-  static constexpr int kQ = 2 * kTileBytes;                    // [2]
-  static constexpr int kDO = 4 * kTileBytes;                   // [2]
+  static constexpr int kHalf = kTileBytes / 2;
+  static constexpr int kQ = 2 * kTileBytes;                    // [2 halves][2 stages]
+  static constexpr int kDO = 4 * kTileBytes;                   // [2 halves][2 stages]
+  static constexpr int half_at(int half, uint32_t g) { return (half * 2 + (int)(g & 1)) * kHalf; }
   static constexpr int kStat = 6 * kTileBytes;                 // [kStats][-LSE log2 e 128, D 128]
   static constexpr int kBias = kStat + kStats * 1024;          // [kBiasTab]
   static constexpr int kAcc = kBias + kBiasTab * 4;      // [2 R + 1] drel of the current head
   static constexpr int kDiag = kAcc + (2 * FLAMIA_REL_MAX + 2) * 4;   // [2][16 warps][64]
   static constexpr int kBar = (kDiag + 2 * 16 * 64 * 4 + 15) & ~15;
-  static constexpr int kBytes = kBar + 256;
+  static constexpr int kBytes = kBar + 384;
   static constexpr int kAlloc = kBytes + 1024;
 };
 
@@ -232,21 +239,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t *k_full = bars, *k_empty = bars + 1, *v_full = bars + 2, *v_empty = bars + 3;
-  uint64_t *q_full = bars + 4, *q_empty = bars + 6, *do_full = bars + 8, *do_empty = bars + 10;   // [2] each
-  uint64_t *s_full = bars + 12, *dp_full = bars + 13, *p_ready = bars + 14, *ds_ready = bars + 15;
-  uint64_t *acc_full = bars + 16, *drain = bars + 17;
-  uint64_t *st_full = bars + 18, *st_empty = st_full + kStats;
+  uint64_t *q_full = bars + 4, *q_empty = bars + 8, *do_full = bars + 12, *do_empty = bars + 16;   // [2 halves][2 stages]
+  uint64_t *s_full = bars + 20, *dp_full = bars + 22, *p_ready = bars + 24, *ds_ready = bars + 26;  // [2 halves]
+  uint64_t *acc_full = bars + 28, *acc_free = bars + 29, *drain = bars + 30;                       // drain [2]
+  uint64_t *st_full = bars + 32, *st_empty = st_full + kStats;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(st_empty + kStats);
   int* status = const_cast<int*>(p.plan) + kPlanStatus;
   const PlanView pv = plan_view(p.plan, p.T, p.N);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 14; ++i) mbar_init(bars + i, 1);
-    mbar_init(p_ready, kCompute);
-    mbar_init(ds_ready, kCompute);
-    mbar_init(acc_full, 1);
+    for (int i = 0; i < 24; ++i) mbar_init(bars + i, 1);
+    for (int i = 24; i < 28; ++i) mbar_init(bars + i, kCompute / 2);
+    mbar_init(acc_full, 2);
+    mbar_init(acc_free, kCompute);
     mbar_init(drain, 1);
+    mbar_init(drain + 1, 1);
     for (int i = 0; i < kStats; ++i) {
       mbar_init(&st_full[i], 32);
       mbar_init(&st_empty[i], kCompute);
@@ -273,91 +281,109 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = S.begin(p, pv), ok = true;
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- producer
-      uint32_t nk = 0, nv = 0, nq = 0, nd = 0;       // tiles loaded
+      uint32_t nk = 0, nv = 0, nq = 0, nd = 0;       // tiles and half tiles loaded
       for (; more && ok; more = S.next(p, pv)) {
-        const int row = S.U.start + S.t * kTile, krow = S.U.start + S.U.u * kTile;
+        const int krow = S.U.start + S.U.u * kTile;
         if (S.first()) {
           if (nk && !(ok = mbar_wait(k_empty, (nk - 1) & 1, status))) break;
           load_tile<D>(smem + L::kK, &tm_k, k_full, S.U.hk, krow);
           ++nk;
         }
-        if (nq >= 2 && !(ok = mbar_wait(&q_empty[nq & 1], ((nq >> 1) - 1) & 1, status))) break;
-        load_tile<D>(smem + L::kQ + (nq & 1) * L::kTileBytes, &tm_q, &q_full[nq & 1], S.h, row);
-        ++nq;
-        if (S.first()) {
-          if (nv && !(ok = mbar_wait(v_empty, (nv - 1) & 1, status))) break;
-          load_tile<D>(smem + L::kV, &tm_v, v_full, S.U.hk, krow);
-          ++nv;
+        for (int half = 0; half < 2 && ok; ++half) {
+          const int row = S.U.start + S.t * kTile + 64 * half;
+          const uint32_t gq = nq >> 1, gd = nd >> 1;
+          const int bq = half * 2 + (gq & 1), bd = half * 2 + (gd & 1);
+          if (gq >= 2 && !(ok = mbar_wait(&q_empty[bq], ((gq >> 1) - 1) & 1, status))) break;
+          load_tile<D, 64>(smem + L::kQ + L::half_at(half, gq), &tm_q, &q_full[bq], S.h, row);
+          ++nq;
+          if (half == 0 && S.first()) {
+            if (nv && !(ok = mbar_wait(v_empty, (nv - 1) & 1, status))) break;
+            load_tile<D>(smem + L::kV, &tm_v, v_full, S.U.hk, krow);
+            ++nv;
+          }
+          // dV has read the tile, and dP too: dK, which gave Q's stage back above, came after it
+          if (gd >= 2 && !(ok = mbar_wait(&do_empty[bd], ((gd >> 1) - 1) & 1, status))) break;
+          load_tile<D, 64>(smem + L::kDO + L::half_at(half, gd), &tm_do, &do_full[bd], S.h, row);
+          ++nd;
         }
-        if (nd >= 2 && !(ok = mbar_wait(&do_empty[nd & 1], ((nd >> 1) - 1) & 1, status))) break;
-        load_tile<D>(smem + L::kDO + (nd & 1) * L::kTileBytes, &tm_do, &do_full[nd & 1], S.h, row);
-        ++nd;
       }
       // nothing may land after the CTA has left (open only when a wait ran out)
       if (nk) mbar_wait(k_full, (nk - 1) & 1, status);
       if (nv) mbar_wait(v_full, (nv - 1) & 1, status);
-      for (uint32_t x = nq > 2 ? nq - 2 : 0; x < nq; ++x) mbar_wait(&q_full[x & 1], (x >> 1) & 1, status);
-      for (uint32_t x = nd > 2 ? nd - 2 : 0; x < nd; ++x) mbar_wait(&do_full[x & 1], (x >> 1) & 1, status);
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issuer
+      for (uint32_t x = nq > 4 ? nq - 4 : 0; x < nq; ++x)
+        mbar_wait(&q_full[(x & 1) * 2 + ((x >> 1) & 1)], (x >> 2) & 1, status);
+      for (uint32_t x = nd > 4 ? nd - 4 : 0; x < nd; ++x)
+        mbar_wait(&do_full[(x & 1) * 2 + ((x >> 1) & 1)], (x >> 2) & 1, status);
+    } else if (warp == 1 || warp == 2) {
+      // ---------------------------------------------------------- MMA issuers
+      // warp 1: S^T and dV, warp 2: dP^T and dK; each half's next scores go out behind the product
+      // that read what they overwrite
       const bool leader = elect_one();
       const uint32_t base16 = (smem_u32(smem) & 0x3FFFFu) >> 4;
-      auto scores = [&](uint32_t a_off, uint32_t b_off, uint32_t d, uint64_t* bar) {     // both operands K-major
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s / 4) * kTile * 128 + (s % 4) * 32;
-          if (leader)
-            mma_bf16(tbase + d, sdesc_at(base16, a_off + off, 16, 1024, kSwizzle128B),
-                     sdesc_at(base16, b_off + off, 16, 1024, kSwizzle128B), idesc_bf16(128, 128, 0, 0), s > 0);
-        }
-        if (leader) mma_commit(bar);
-      };
-      auto accum = [&](uint32_t a, uint32_t b_off, uint32_t d, bool first) {             // A from TMEM, B over its rows
-#pragma unroll
-        for (int s = 0; s < kTile / 16; ++s)
-          if (leader)
-            mma_bf16_ta(tbase + d, tbase + a + 32 * (s >> 1) + 8 * (s & 1),
-                        sdesc_at(base16, b_off + s * 2048, kTile * 128, 1024, kSwizzle128B), idesc_bf16(128, D, 0, 1),
-                        (!first || s > 0));
-      };
-      auto issue_s = [&](uint32_t g) {
-        if (S.first() && !(ok = warp_wait(k_full, S.n & 1, status))) return;
-        if (!(ok = warp_wait(&q_full[g & 1], (g >> 1) & 1, status))) return;
-        tc_fence_after();
-        scores(L::kK, L::kQ + (g & 1) * L::kTileBytes, kTS, s_full);
-        if (S.last() && leader) mma_commit(k_empty);
-      };
-      auto issue_dp = [&](uint32_t g) {
-        if (S.first() && !(ok = warp_wait(v_full, S.n & 1, status))) return;
-        if (!(ok = warp_wait(&do_full[g & 1], (g >> 1) & 1, status))) return;
-        tc_fence_after();
-        scores(L::kV, L::kDO + (g & 1) * L::kTileBytes, kTP, dp_full);
-        if (S.last() && leader) mma_commit(v_empty);
-      };
-      if (more) {
-        issue_s(0);
-        if (ok) issue_dp(0);
-        for (uint32_t g = 0; more && ok; ++g) {
-          const bool first = S.first(), last = S.last();
-          if (!(ok = warp_wait(p_ready, g & 1, status))) break;
+      auto run = [&](auto WHICH) {
+        constexpr bool kP = decltype(WHICH)::value;      // the chain of P
+        constexpr uint32_t kA = kP ? L::kK : L::kV, kB = kP ? L::kQ : L::kDO, kB2 = kP ? L::kDO : L::kQ;
+        constexpr uint32_t kT = kP ? kTS : kTP, kSum = kP ? kTV : kTK;
+        uint64_t *a_full = kP ? k_full : v_full, *a_empty = kP ? k_empty : v_empty;
+        uint64_t *b_full = kP ? q_full : do_full, *b2_empty = kP ? do_empty : q_empty;
+        uint64_t *out = kP ? s_full : dp_full, *in = kP ? p_ready : ds_ready;
+        auto scores = [&](int half, uint32_t g, int unit, bool first, bool last) {      // of step g, both operands K-major
+          const uint32_t b = half * 2 + (g & 1), b16 = base16 + (g & 1) * (L::kHalf / 16);
+          if (half == 0 && first && !(ok = warp_wait(a_full, unit & 1, status))) return;
+          if (!(ok = warp_wait(&b_full[b], (g >> 1) & 1, status))) return;
           tc_fence_after();
-          accum(kTS, L::kDO + (g & 1) * L::kTileBytes, kTV, first);
-          if (leader) mma_commit(&do_empty[g & 1]);
-          more = S.next(p, pv);
-          if (more) issue_s(g + 1);
-          if (!ok || !(ok = warp_wait(ds_ready, g & 1, status))) break;
-          tc_fence_after();
-          accum(kTP, L::kQ + (g & 1) * L::kTileBytes, kTK, first);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            if (leader)
+              mma_bf16(tbase + kT + 64 * half, sdesc_at(base16, kA + (s / 4) * kTile * 128 + (s % 4) * 32, 16, 1024, kSwizzle128B),
+                       sdesc_at(b16, kB + half * 2 * L::kHalf + (s / 4) * 64 * 128 + (s % 4) * 32, 16, 1024, kSwizzle128B),
+                       idesc_bf16(128, 64, 0, 0), s > 0);
           if (leader) {
-            mma_commit(&q_empty[g & 1]);
-            if (last) mma_commit(acc_full);
+            mma_commit(&out[half]);
+            if (half == 1 && last) mma_commit(a_empty);
           }
-          if (more) issue_dp(g + 1);
+        };
+        auto product = [&](int half, uint32_t g, bool first) {      // A from TMEM, B over its rows
+          if (!(ok = warp_wait(&in[half], g & 1, status))) return;
+          tc_fence_after();
+          const uint32_t b16 = base16 + (g & 1) * (L::kHalf / 16);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            if (leader)
+              mma_bf16_ta(tbase + kSum, tbase + kT + 64 * half + 32 * (s >> 1) + 8 * (s & 1),
+                          sdesc_at(b16, kB2 + half * 2 * L::kHalf + s * 2048, 64 * 128, 1024, kSwizzle128B),
+                          idesc_bf16(128, D, 0, 1), (!(first && half == 0) || s > 0));
+          if (leader) mma_commit(&b2_empty[half * 2 + (g & 1)]);
+        };
+        int steps = more ? S.group * S.U.nq : 0;      // of the unit
+        if (steps) {
+          scores(0, 0, 0, true, steps == 1);
+          if (ok) scores(1, 0, 0, true, steps == 1);
         }
-      }
+        uint32_t g = 0;
+        for (int unit = 0; steps && ok; ++unit) {
+          ++S.n;
+          const int next_steps = S.unit(p, pv) ? S.group * S.U.nq : 0;
+          // the unit's first product overwrites the sums of the last one: those have to be out
+          if (unit && !(ok = warp_wait(acc_free, (unit - 1) & 1, status))) break;
+          for (int i = 0; i < steps && ok; ++i, ++g) {
+            const bool last = i == steps - 1, next = !last || next_steps;
+            const bool next_last = last ? next_steps == 1 : i + 2 == steps;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (ok) product(half, g, i == 0);
+              if (ok && next) scores(half, g + 1, unit + last, last, next_last);
+            }
+            if (ok && last && leader) mma_commit(acc_full);
+          }
+          steps = next_steps;
+        }
+      };
+      if (warp == 1) run(std::true_type{});
+      else run(std::false_type{});
       if (leader) {
-        mma_commit(drain);
-        mbar_wait(drain, 0, status);
+        mma_commit(&drain[warp - 1]);
+        mbar_wait(&drain[warp - 1], 0, status);
       }
     } else if (warp == 3) {
       // ---------------------------------------------------------- LSE and D of a step's queries
@@ -384,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ compute
     setmaxnreg_inc<kRegCompute>();
-    const int w = (warp - 4) >> 2, quarter = warp & 3;
+    const int w = (warp - 4) >> 2, quarter = warp & 3, half = w >> 1;
     const int r = quarter * 32 + lane, tid = threadIdx.x - 128;
     const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_addr = lane_base + kTS + 32 * w, dp_addr = lane_base + kTP + 32 * w;
@@ -401,30 +427,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a warp whose wait ran out goes on through the steps without work: it still meets the others
     // at the barriers
     uint32_t g = 0;
-    for (bool more = S.begin(p, pv); more; ++g) {
-      const KeyUnit& U = S.U;
-      const int t = S.t, kj = U.u * kTile + r;
+    for (bool more = S.begin(p, pv); more; ++S.n, more = S.unit(p, pv)) {
+     const KeyUnit U = S.U;
+     const int kj = U.u * kTile + r;
+     int lo0 = 0, hi0 = U.len - 1;              // queries that see the key
+     if (kj >= U.len) {
+       hi0 = -1;
+     } else if (kj >= U.pre) {
+       if (p.win.right >= 0) lo0 = kj - p.win.right;
+       if (p.win.left >= 0) hi0 = min(hi0, kj + p.win.left);
+     }
+     for (int h = U.hk * S.group; h < (U.hk + 1) * S.group; ++h) {
       if constexpr (BIAS != 0) {
-        if (S.head_first() && staged != S.h) {
+        if (staged != h) {
           named_bar_sync(1, kCompute);
-          stage_bias(tab, p, S.h, tid, kCompute);
+          stage_bias(tab, p, h, tid, kCompute);
           named_bar_sync(1, kCompute);
           HB = head_bias(tab);
-          staged = S.h;
+          staged = h;
         }
-        if (BIAS == 2 && S.head_first()) {
+        if (BIAS == 2) {
           for (int i = tid; i < 2 * R + 1; i += kCompute) acc[i] = 0.f;
           far_lo = far_hi = lost_lo = lost_hi = 0.f;
           named_bar_sync(1, kCompute);
         }
       }
+      for (int t = U.tlo; t < U.tlo + U.nq; ++t, ++g) {
       float du_lo = 0.f;      // (BIAS 2) sum of the thread's dU of a far tile
       uint32_t v[1][32];
-      if (ok) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&st_full[g % kStats], (g / kStats) & 1, status) &&
-                                         mbar_wait(s_full, g & 1, status));
-      }
       const float* nl = reinterpret_cast<const float*>(smem + L::kStat) + (g % kStats) * 256 + 32 * w;
+      ok = ok && mbar_wait(&st_full[g % kStats], (g / kStats) & 1, status);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[half], g & 1, status));
       if (ok) {
         tc_fence_after();
         tmem_ld32(s_addr, v[0]);
@@ -442,15 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), p.capf.zscale));
         }
-        int lo = 0, hi = U.len - 1;
-        if (kj >= U.len) {
-          hi = -1;
-        } else if (kj >= U.pre) {
-          if (p.win.right >= 0) lo = kj - p.win.right;
-          if (p.win.left >= 0) hi = min(hi, kj + p.win.left);
-        }
-        lo -= t * kTile + 32 * w;
-        hi -= t * kTile + 32 * w;
+        const int lo = lo0 - (t * kTile + 32 * w), hi = hi0 - (t * kTile + 32 * w);
         uint32_t pk[16];
 #pragma unroll
         for (int c = 0; c < 1; ++c) {
@@ -463,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 f2 = make_float2(f, f), c2 = make_float2(B.c, B.c);
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 n4 = *reinterpret_cast<const float4*>(nl + 32 * c + j);
+            const float4 n4 = *reinterpret_cast<const float4*>(nl + j);
             float2 e0 = make_float2(n4.x, n4.y), e1 = make_float2(n4.z, n4.w);
             if constexpr (BIAS != 0) {
               e0 = fadd2(e0, c2);
@@ -485,17 +510,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st16(s_addr, pk);
         tmem_st_wait();
-        if ((t + 1) * kTile > U.len) {
+        if (t * kTile + 64 * half + 64 > U.len) {
           // queries behind the document: the products below sum over them
-          ok = __all_sync(0xffffffffu, mbar_wait(&do_full[g & 1], (g >> 1) & 1, status));
-          if (ok && w < 2 && t * kTile + r >= U.len)
-            clear_row<D>(smem + (w ? L::kQ : L::kDO) + (g & 1) * L::kTileBytes, r);
+          ok = __all_sync(0xffffffffu, mbar_wait(&do_full[half * 2 + (g & 1)], (g >> 1) & 1, status));
+          if (ok && r < 64 && t * kTile + 64 * half + r >= U.len)
+            clear_row<D, 64>(smem + (w & 1 ? L::kQ : L::kDO) + L::half_at(half, g), r);
           fence_proxy_async_smem();
         }
         if (ok) {
           tc_fence_before();
-          mbar_arrive(p_ready);
-          ok = __all_sync(0xffffffffu, mbar_wait(dp_full, g & 1, status));
+          mbar_arrive(&p_ready[half]);
+          ok = __all_sync(0xffffffffu, mbar_wait(&dp_full[half], g & 1, status));
         }
         if (ok) {
           tc_fence_after();
@@ -508,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (edge) drop_hidden(dp, v[c]);
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const float4 d4 = *reinterpret_cast<const float4*>(nl + 128 + 32 * c + j);
+              const float4 d4 = *reinterpret_cast<const float4*>(nl + 128 + j);
               float2 a0 = fmul2(pair_of(v[c], j), fadd2(pair_of(dp, j), make_float2(-d4.x, -d4.y)));
               float2 a1 = fmul2(pair_of(v[c], j + 2), fadd2(pair_of(dp, j + 2), make_float2(-d4.z, -d4.w)));
               if constexpr (BIAS == 2) {
@@ -528,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16(dp_addr, pk);
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(ds_ready);
+          mbar_arrive(&ds_ready[half]);
           mbar_arrive(&st_empty[g % kStats]);
         }
       }
@@ -568,35 +593,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           buf ^= 1;
         }
-        if (S.head_last()) {
-          // the head's sums of this key tile: the two ends over all threads in a fixed order
-          float* red = reinterpret_cast<float*>(smem + L::kDiag) + buf * (16 * 64);
-          far_lo += lost_lo;
-          far_hi += lost_hi;
-#pragma unroll
-          for (int o = 16; o; o >>= 1) {
-            far_lo += __shfl_xor_sync(0xffffffffu, far_lo, o);
-            far_hi += __shfl_xor_sync(0xffffffffu, far_hi, o);
-          }
-          if (lane == 0) {
-            red[2 * (warp - 4)] = far_lo;
-            red[2 * (warp - 4) + 1] = far_hi;
-          }
-          named_bar_sync(1, kCompute);
-          float* part = p.drel_part + ((size_t)S.h * p.plan[kPlanBwdItems] + U.item) * (2 * R + 1);
-          for (int i = tid; i < 2 * R + 1; i += kCompute) {
-            float s = acc[i];
-            if (i == 0 || i == 2 * R) {
-              s = 0.f;
-              for (int q = 0; q < 16; ++q) s += red[2 * q + (i ? 1 : 0)];
-            }
-            part[i] = s;
-          }
-          named_bar_sync(1, kCompute);
-          buf ^= 1;
-        }
       }
-      if (S.last() && ok) {
+      }
+      if constexpr (BIAS == 2) {
+        // the head's sums of this key tile: the two ends over all threads in a fixed order
+        float* red = reinterpret_cast<float*>(smem + L::kDiag) + buf * (16 * 64);
+        far_lo += lost_lo;
+        far_hi += lost_hi;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          far_lo += __shfl_xor_sync(0xffffffffu, far_lo, o);
+          far_hi += __shfl_xor_sync(0xffffffffu, far_hi, o);
+        }
+        if (lane == 0) {
+          red[2 * (warp - 4)] = far_lo;
+          red[2 * (warp - 4) + 1] = far_hi;
+        }
+        named_bar_sync(1, kCompute);
+        float* part = p.drel_part + ((size_t)h * p.plan[kPlanBwdItems] + U.item) * (2 * R + 1);
+        for (int i = tid; i < 2 * R + 1; i += kCompute) {
+          float s = acc[i];
+          if (i == 0 || i == 2 * R) {
+            s = 0.f;
+            for (int q = 0; q < 16; ++q) s += red[2 * q + (i ? 1 : 0)];
+          }
+          part[i] = s;
+        }
+        named_bar_sync(1, kCompute);
+        buf ^= 1;
+      }
+     }
+     if (ok) {
         ok = __all_sync(0xffffffffu, mbar_wait(acc_full, S.n & 1, status));
         if (ok) {
           tc_fence_after();
@@ -606,9 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (w < 2) store_acc<D / 2>(lane_base + kTV + c, p.dv + at + c, 1.f, valid);
           else store_acc<D / 2>(lane_base + kTK + c, p.dk + at + c, p.scale, valid);
           tc_fence_before();
+          mbar_arrive(acc_free);
         }
       }
-      more = S.next(p, pv);
     }
   }
   tc_fence_before();
@@ -985,10 +1012,10 @@ __global__ void __launch_bounds__(256) scored_drel_kernel(const float* __restric
 template <int D, bool CAP, int BIAS>
 cudaError_t launch(const ScoredParams& p, cudaStream_t stream) {
   CUtensorMap tq, tk, tv, tdo;
-  if (!make_tmap_bf16_3d(&tq, p.q, D, p.hq, p.T, D * 2, (uint64_t)p.hq * D * 2, 64, kTile) ||
+  if (!make_tmap_bf16_3d(&tq, p.q, D, p.hq, p.T, D * 2, (uint64_t)p.hq * D * 2, 64, kTile / 2) ||
       !make_tmap_bf16_3d(&tk, p.k, D, p.hkv, p.T, D * 2, (uint64_t)p.hkv * D * 2, 64, kTile) ||
       !make_tmap_bf16_3d(&tv, p.v, D, p.hkv, p.T, D * 2, (uint64_t)p.hkv * D * 2, 64, kTile) ||
-      !make_tmap_bf16_3d(&tdo, p.dout, D, p.hq, p.T, D * 2, (uint64_t)p.hq * D * 2, 64, kTile))
+      !make_tmap_bf16_3d(&tdo, p.dout, D, p.hq, p.T, D * 2, (uint64_t)p.hq * D * 2, 64, kTile / 2))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0, regs1 = 0, regs2 = 0;
   cudaError_t e = cudaGetDevice(&dev);
