@@ -424,11 +424,11 @@ int flamia_scored_fwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
   if (!rc) rc = check_score_scale(softmax_scale);
   if (rc) return rc;
   if (causal != 0 && causal != 1) return FLAMIA_ERR_INVALID_ARG;
+  if (total_tokens == 0) return FLAMIA_OK;
   if (!q_bf16 || !k_bf16 || !v_bf16 || !out_bf16 || !lse) return FLAMIA_ERR_INVALID_ARG;
   if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(out_bf16) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u))
     return FLAMIA_ERR_MISALIGNED;
-  if (total_tokens == 0) return FLAMIA_OK;
   ScoredParams p = scored_params(q_bf16, k_bf16, v_bf16, cu_seqlens, num_seqs, total_tokens, hq, hkv, head_dim, causal,
                                  softmax_scale, opt, plan);
   p.out = static_cast<__nv_bfloat16*>(out_bf16);
@@ -454,21 +454,23 @@ int flamia_scored_bwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
   if (!rc) rc = check_score_scale(softmax_scale);
   if (rc) return rc;
   if (causal != 0 && causal != 1) return FLAMIA_ERR_INVALID_ARG;
+  if (drel_bias && !(opt && opt->rel_bias)) return FLAMIA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(drel_bias) & 3u) return FLAMIA_ERR_MISALIGNED;
+  if (total_tokens == 0)
+    return drel_bias ? cuda_status(cudaMemsetAsync(drel_bias, 0, (size_t)hq * (2 * opt->rel_max + 1) * 4,
+                                                   (cudaStream_t)stream))
+                     : FLAMIA_OK;
   if (!q_bf16 || !k_bf16 || !v_bf16 || !out_bf16 || !lse || !dout_bf16 || !dq_bf16 || !dk_bf16 || !dv_bf16 || !workspace)
     return FLAMIA_ERR_INVALID_ARG;
-  if (drel_bias && !(opt && opt->rel_bias)) return FLAMIA_ERR_INVALID_ARG;
   if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(out_bf16) || !aligned16(dout_bf16) ||
       !aligned16(dq_bf16) || !aligned16(dk_bf16) || !aligned16(dv_bf16) ||
-      (reinterpret_cast<uintptr_t>(workspace) & 255u) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
-      (reinterpret_cast<uintptr_t>(drel_bias) & 3u))
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return FLAMIA_ERR_MISALIGNED;
   ScoredParams p = scored_params(q_bf16, k_bf16, v_bf16, cu_seqlens, num_seqs, total_tokens, hq, hkv, head_dim, causal,
                                  softmax_scale, opt, plan);
   const ScoredBwdWorkspace w = scored_bwd_layout(total_tokens, num_seqs, hq, drel_bias ? p.R : 0);
   if (workspace_bytes < w.total) return FLAMIA_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
-  if (total_tokens == 0)
-    return drel_bias ? cuda_status(cudaMemsetAsync(drel_bias, 0, (size_t)hq * (2 * p.R + 1) * 4, s)) : FLAMIA_OK;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.out = const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>(out_bf16));
   p.lse = const_cast<float*>(lse);

@@ -201,9 +201,18 @@ __device__ __forceinline__ void put_pair(uint32_t (&v)[32], int j, float2 x) {
   v[j] = __float_as_uint(x.x);
   v[j + 1] = __float_as_uint(x.y);
 }
-// A group of N x 32 raw products -> capped, in the same units.
+// x for the columns of a row without their bit in the mask.
+__device__ __forceinline__ void hide(uint32_t (&v)[32], uint32_t see, uint32_t x) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = (see >> j) & 1 ? v[j] : x;
+}
+constexpr uint32_t kMinusInf = 0xff800000u;
+// A group of N x 32 raw products -> capped, in the same units.  The warp's length of the
+// polynomial shows in a result's last bits, so only products that count choose it: those of
+// hidden pairs are 0 by now, and a row outside the document (counts false) has no say.  A
+// result thus depends on its warp's 32 rows of the document and on keys that they see.
 template <int N>
-__device__ __forceinline__ void cap_products(uint32_t (&v)[N][32], const CapForm& F) {
+__device__ __forceinline__ void cap_products(uint32_t (&v)[N][32], const CapForm& F, bool counts) {
   float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int g = 0; g < N; ++g)
@@ -211,7 +220,7 @@ __device__ __forceinline__ void cap_products(uint32_t (&v)[N][32], const CapForm
     for (int j = 0; j < 32; j += 2)
       m[(j / 2) % 4] = fmax3(m[(j / 2) % 4], fabsf(__uint_as_float(v[g][j])), fabsf(__uint_as_float(v[g][j + 1])));
   const float am = fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
-  if (!__any_sync(0xffffffffu, !(am <= F.t3))) {
+  if (!__any_sync(0xffffffffu, counts && !(am <= F.t3))) {
 #pragma unroll
     for (int g = 0; g < N; ++g)
 #pragma unroll
@@ -221,7 +230,7 @@ __device__ __forceinline__ void cap_products(uint32_t (&v)[N][32], const CapForm
         t = ffma2(w, t, F.k3[0]);
         put_pair(v[g], j, ffma2(x, fmul2(w, t), x));
       }
-  } else if (!__any_sync(0xffffffffu, !(am <= F.t5))) {
+  } else if (!__any_sync(0xffffffffu, counts && !(am <= F.t5))) {
 #pragma unroll
     for (int g = 0; g < N; ++g)
 #pragma unroll
@@ -246,6 +255,9 @@ __device__ __forceinline__ void cap_products(uint32_t (&v)[N][32], const CapForm
         v[g][j] = __float_as_uint(fabsf(z) <= kTanh5To ? fmaf(x, w * t, x) : F.inv * tanh_any(z));
       }
   }
+}
+__device__ __forceinline__ void cap_products(uint32_t (&v)[32], const CapForm& F, bool counts) {
+  cap_products(reinterpret_cast<uint32_t(&)[1][32]>(v), F, counts);
 }
 // The table's or the slope's part for columns c0 .. c0 + 31 (column c: distance DIR c more);
 // with a table the result is in base 2, else the products' units stay.

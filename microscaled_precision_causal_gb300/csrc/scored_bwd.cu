@@ -454,59 +454,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int t = U.tlo; t < U.tlo + U.nq; ++t, ++g) {
       float du_lo = 0.f;      // (BIAS 2) sum of the thread's dU of a far tile
-      uint32_t v[1][32];
+      uint32_t v[32];
       const float* nl = reinterpret_cast<const float*>(smem + L::kStat) + (g % kStats) * 256 + 32 * w;
       ok = ok && mbar_wait(&st_full[g % kStats], (g / kStats) & 1, status);
       ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[half], g & 1, status));
       if (ok) {
         tc_fence_after();
-        tmem_ld32(s_addr, v[0]);
+        tmem_ld32(s_addr, v);
         tmem_ld_wait();
-        uint32_t gr[1][32];
+        uint32_t gr[32];
         TileBias B{};
         if constexpr (BIAS != 0) B = tile_bias(tab, HB, R, near, inv_scale2, t, U.u, kj - (t * kTile + 32 * w));
         const float f = BIAS != 0 ? B.factor(scale2) : scale2;
         const bool masked = t < U.full.x || t > U.full.y;
         const bool edge = (t + 1) * kTile > U.len || (BIAS == 2 && (U.u + 1) * kTile > U.len);
-        if constexpr (CAP) {
-          cap_products(v, p.capf);
-#pragma unroll
-          for (int c = 0; c < 1; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), p.capf.zscale));
-        }
         const int lo = lo0 - (t * kTile + 32 * w), hi = hi0 - (t * kTile + 32 * w);
+        const uint32_t see = masked ? column_mask(lo, hi, 0, 0) : ~0u;
+        if constexpr (CAP) {
+          if (masked) hide(v, see, 0u);
+          cap_products(v, p.capf, true);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) put_pair(gr, j, cap_slope(pair_of(v, j), p.capf.zscale));
+        }
         uint32_t pk[16];
+        if constexpr (BIAS != 0) bias_chunk<-1>(v, 0, scale2, B);
+        if (masked) hide(v, see, kMinusInf);
+        const float2 f2 = make_float2(f, f), c2 = make_float2(B.c, B.c);
 #pragma unroll
-        for (int c = 0; c < 1; ++c) {
-          if constexpr (BIAS != 0) bias_chunk<-1>(v[c], 32 * c, scale2, B);
-          if (masked) {
-            const uint32_t see = column_mask(lo, hi, 0, 32 * c);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[c][j] = (see >> j) & 1 ? v[c][j] : 0xff800000u;
+        for (int j = 0; j < 32; j += 4) {
+          const float4 n4 = *reinterpret_cast<const float4*>(nl + j);
+          float2 e0 = make_float2(n4.x, n4.y), e1 = make_float2(n4.z, n4.w);
+          if constexpr (BIAS != 0) {
+            e0 = fadd2(e0, c2);
+            e1 = fadd2(e1, c2);
           }
-          const float2 f2 = make_float2(f, f), c2 = make_float2(B.c, B.c);
+          e0 = ffma2(pair_of(v, j), f2, e0);
+          e1 = ffma2(pair_of(v, j + 2), f2, e1);
+          e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
+          e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
+          pk[j / 2] = pack2(e0);
+          pk[j / 2 + 1] = pack2(e1);
+          put_pair(v, j, e0);
+          put_pair(v, j + 2, e1);
+        }
+        if constexpr (CAP && BIAS != 2) {       // dS needs P (1 - tanh^2) alone
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 n4 = *reinterpret_cast<const float4*>(nl + j);
-            float2 e0 = make_float2(n4.x, n4.y), e1 = make_float2(n4.z, n4.w);
-            if constexpr (BIAS != 0) {
-              e0 = fadd2(e0, c2);
-              e1 = fadd2(e1, c2);
-            }
-            e0 = ffma2(pair_of(v[c], j), f2, e0);
-            e1 = ffma2(pair_of(v[c], j + 2), f2, e1);
-            e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
-            e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
-            pk[16 * c + j / 2] = pack2(e0);
-            pk[16 * c + j / 2 + 1] = pack2(e1);
-            put_pair(v[c], j, e0);
-            put_pair(v[c], j + 2, e1);
-          }
-          if constexpr (CAP && BIAS != 2) {       // dS needs P (1 - tanh^2) alone
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) put_pair(v[c], j, fmul2(pair_of(v[c], j), pair_of(gr[c], j)));
-          }
+          for (int j = 0; j < 32; j += 2) put_pair(v, j, fmul2(pair_of(v, j), pair_of(gr, j)));
         }
         tmem_st16(s_addr, pk);
         tmem_st_wait();
@@ -525,29 +518,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           tc_fence_after();
           float2 sum = make_float2(0.f, 0.f);
+          uint32_t dp[32];
+          tmem_ld32(dp_addr, dp);
+          tmem_ld_wait();
+          if (edge) drop_hidden(dp, v);
 #pragma unroll
-          for (int c = 0; c < 1; ++c) {
-            uint32_t dp[32];
-            tmem_ld32(dp_addr + 32 * c, dp);
-            tmem_ld_wait();
-            if (edge) drop_hidden(dp, v[c]);
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 d4 = *reinterpret_cast<const float4*>(nl + 128 + j);
-              float2 a0 = fmul2(pair_of(v[c], j), fadd2(pair_of(dp, j), make_float2(-d4.x, -d4.y)));
-              float2 a1 = fmul2(pair_of(v[c], j + 2), fadd2(pair_of(dp, j + 2), make_float2(-d4.z, -d4.w)));
-              if constexpr (BIAS == 2) {
-                put_pair(v[c], j, a0);
-                put_pair(v[c], j + 2, a1);
-                sum = fadd2(sum, fadd2(a0, a1));
-                if constexpr (CAP) {
-                  a0 = fmul2(a0, pair_of(gr[c], j));
-                  a1 = fmul2(a1, pair_of(gr[c], j + 2));
-                }
+          for (int j = 0; j < 32; j += 4) {
+            const float4 d4 = *reinterpret_cast<const float4*>(nl + 128 + j);
+            float2 a0 = fmul2(pair_of(v, j), fadd2(pair_of(dp, j), make_float2(-d4.x, -d4.y)));
+            float2 a1 = fmul2(pair_of(v, j + 2), fadd2(pair_of(dp, j + 2), make_float2(-d4.z, -d4.w)));
+            if constexpr (BIAS == 2) {
+              put_pair(v, j, a0);
+              put_pair(v, j + 2, a1);
+              sum = fadd2(sum, fadd2(a0, a1));
+              if constexpr (CAP) {
+                a0 = fmul2(a0, pair_of(gr, j));
+                a1 = fmul2(a1, pair_of(gr, j + 2));
               }
-              pk[16 * c + j / 2] = pack2(a0);
-              pk[16 * c + j / 2 + 1] = pack2(a1);
             }
+            pk[j / 2] = pack2(a0);
+            pk[j / 2 + 1] = pack2(a1);
           }
           du_lo = sum.x + sum.y;
           tmem_st16(dp_addr, pk);
@@ -571,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float run = 0.f;
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            run += __uint_as_float(v[0][c]);
+            run += __uint_as_float(v[c]);
             if (lane == 31) mine[62 - c] = run;
             run = __shfl_up_sync(0xffffffffu, run, 1);
             if (lane == 0) run = 0.f;
@@ -900,8 +890,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, g & 1, status));
       if (ok) {
         tc_fence_after();
-        uint32_t v[1][32], gr[1][32];
-        tmem_ld32(s_addr, v[0]);
+        uint32_t v[32], gr[32];
+        tmem_ld32(s_addr, v);
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(s_free);
@@ -909,48 +899,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (BIAS) B = tile_bias(tab, HB, R, near, inv_scale2, t, u, u * kTile + 32 * w - qi);
         const float f = BIAS ? B.factor(scale2) : scale2;
         const bool masked = !full.has(u);
-        if constexpr (CAP) {
-          cap_products(v, p.capf);
-#pragma unroll
-          for (int c = 0; c < 1; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) put_pair(gr[c], j, cap_slope(pair_of(v[c], j), p.capf.zscale));
-        }
         const int c0 = u * kTile + 32 * w;
+        const uint32_t see = masked ? column_mask(lo - c0, hi - c0, S.pre - c0, 0) : ~0u;
+        if constexpr (CAP) {
+          if (masked) hide(v, see, 0u);
+          cap_products(v, p.capf, qi < S.len);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) put_pair(gr, j, cap_slope(pair_of(v, j), p.capf.zscale));
+        }
         const float2 f2 = make_float2(f, f), n2 = make_float2(nl + B.c, nl + B.c);
+        if constexpr (BIAS) bias_chunk<1>(v, 0, scale2, B);
+        if (masked) hide(v, see, kMinusInf);
 #pragma unroll
-        for (int c = 0; c < 1; ++c) {
-          if constexpr (BIAS) bias_chunk<1>(v[c], 32 * c, scale2, B);
-          if (masked) {
-            const uint32_t see = column_mask(lo - c0, hi - c0, S.pre - c0, 32 * c);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[c][j] = (see >> j) & 1 ? v[c][j] : 0xff800000u;
-          }
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float2 e = ffma2(pair_of(v[c], j), f2, n2);
-            e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
-            if constexpr (CAP) e = fmul2(e, pair_of(gr[c], j));
-            put_pair(v[c], j, e);
-          }
+        for (int j = 0; j < 32; j += 2) {
+          float2 e = ffma2(pair_of(v, j), f2, n2);
+          e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+          if constexpr (CAP) e = fmul2(e, pair_of(gr, j));
+          put_pair(v, j, e);
         }
         ok = __all_sync(0xffffffffu, mbar_wait(dp_full, g & 1, status));
         if (ok) {
           tc_fence_after();
           const float2 d2 = make_float2(-dv, -dv);
           uint32_t pk[16];
+          uint32_t dp[32];
+          tmem_ld32(dp_addr, dp);
+          tmem_ld_wait();
+          if ((u + 1) * kTile > S.len) drop_hidden(dp, v);
 #pragma unroll
-          for (int c = 0; c < 1; ++c) {
-            uint32_t dp[32];
-            tmem_ld32(dp_addr + 32 * c, dp);
-            tmem_ld_wait();
-            if ((u + 1) * kTile > S.len) drop_hidden(dp, v[c]);
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float2 e = pair_of(v[c], j);
-              const float2 a = fmul2(e, fadd2(pair_of(dp, j), d2));
-              pk[16 * c + j / 2] = pack2(a);
-            }
+          for (int j = 0; j < 32; j += 2) {
+            const float2 e = pair_of(v, j);
+            const float2 a = fmul2(e, fadd2(pair_of(dp, j), d2));
+            pk[j / 2] = pack2(a);
           }
           tmem_st16(dp_addr, pk);
           tmem_st_wait();

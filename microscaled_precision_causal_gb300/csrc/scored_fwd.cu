@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const int t = U.t0 + w, qi = t * kTile + r;
+      const bool row_in = qi < U.len;      // rows behind the document take no part in the warp's choices
       const int lo = p.win.left < 0 ? 0 : max(0, qi - p.win.left);
       const int hi = p.win.right < 0 ? U.len - 1 : min(U.len - 1, qi + p.win.right);
       const FullTiles full = full_tiles(t, U.len, U.pre, p.win);
@@ -378,27 +379,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         int form = 0;
         bool quick = seen && (!BIAS || !B.tab);
         if constexpr (CAP) {
-          quick = quick && B.col == 0.f && !__any_sync(0xffffffffu, !(mx <= p.capf.t5 && mx * scale2 <= kLoose * 0.5f));
-          form = __any_sync(0xffffffffu, !(mx <= p.capf.t3)) ? 2 : 1;
+          quick = quick && B.col == 0.f && !__any_sync(0xffffffffu, row_in && !(mx <= p.capf.t5 && mx * scale2 <= kLoose * 0.5f));
+          form = __any_sync(0xffffffffu, row_in && !(mx <= p.capf.t3)) ? 2 : 1;
         } else if constexpr (BIAS) {
           quick = quick && fabsf(steep) <= kLoose;
           form = 3;
         }
         if (!quick) {
           form = 0;
-          if constexpr (CAP) cap_products(v, p.capf);
+          uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+          if (!seen) {
+            const int c = u * kTile;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) see[g] = column_mask(lo - c, hi - c, U.pre - c, 32 * g);
+          }
+          if constexpr (CAP) {
+            if (!seen) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g) hide(v[g], see[g], 0u);
+            }
+            cap_products(v, p.capf, row_in);
+          }
           if constexpr (BIAS) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) bias_chunk<1>(v[g], 32 * g, scale2, B);
           }
           if (!seen) {
-            const int c = u * kTile;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const uint32_t see = column_mask(lo - c, hi - c, U.pre - c, 32 * g);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[g][j] = (see >> j) & 1 ? v[g][j] : 0xff800000u;
-            }
+            for (int g = 0; g < 4; ++g) hide(v[g], see[g], kMinusInf);
           }
 #pragma unroll
           for (int g = 0; g < 4; ++g) cm[g] = -INFINITY;
@@ -413,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (BIAS && quick) mx += fmaxf(u < t ? steep : -steep, 0.f);
         if (first) {
           m = mx;
-        } else if (__any_sync(0xffffffffu, mx > m + kRescaleAbove)) {
+        } else if (__any_sync(0xffffffffu, row_in && mx > m + kRescaleAbove)) {
           const float m_new = fmaxf(m, mx);
           const float alpha = m_new == m ? 1.f : fast_exp2(m - m_new);      // 0 where nothing was visible yet
           la = fmul2(la, make_float2(alpha, alpha));

@@ -152,3 +152,268 @@ def test_sliding_window_skips_tiles(F, causal):
 
 def test_given_scale_and_large_scores(F):
     Problem(F, [260], 2, 2, 64, seed=7, scale=1.0, gain=4.0).check()
+
+
+# ------------------------------------------------------------------ masks, garbage, edges of the range
+
+def bits(*ts):
+    import torch
+    return [t.clone().view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32) for t in ts]
+
+
+def same(a, b):
+    import torch
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def run_all(p):
+    import torch
+    out, lse = p.forward()
+    got = p.backward(out, lse)
+    torch.cuda.synchronize()
+    assert p.att.device_status() == 0
+    return bits(out, lse, *got)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", [dict(softcap=9.0, prefix=[30, 100]), dict(slopes=True, causal=False),
+                                dict(buckets=(16, 40, False))], ids=["cap", "slopes", "buckets"])
+def test_rows_behind_the_last_document_may_hold_anything(F, d, kw):
+    import torch
+    p = Problem(F, [150, 131], 4, 2, d, pad=200, seed=11, **kw)
+    want = run_all(p)
+    for fill in (float("nan"), float("inf")):
+        for t in (p.q, p.k, p.v, p.do):
+            t[281:] = fill
+        p.att.out.fill_(float("nan"))
+        p.att.dk.fill_(float("nan"))
+        assert same(run_all(p), want)
+    assert (p.att.out[281:] == 0).all() and torch.isinf(p.att.lse[:, 281:]).all() and (p.att.dv[281:] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_document_of_infinities_stays_alone(F, d):
+    kw = dict(softcap=9.0, buckets=(16, 40, True), causal=False)
+    p = Problem(F, [100, 77, 259], 2, 1, d, seed=12, **kw)
+    want = run_all(p)
+    for t, x in ((p.q, float("nan")), (p.k, float("inf")), (p.v, float("-inf")), (p.do, float("nan"))):
+        t[100:177] = x
+    out, lse = p.forward()
+    got = bits(out, lse.t(), *p.backward(out, lse)[:3])
+    want = [want[0], want[1].t()] + want[2:5]
+    for rows in (slice(0, 100), slice(177, 436)):
+        assert same([t[rows].contiguous() for t in got], [t[rows].contiguous() for t in want])
+
+
+@pytest.mark.parametrize("value", [float("-inf"), -3.4028234663852886e38, -2.0 ** 101])
+@pytest.mark.parametrize("far", [False, True])
+def test_a_bias_that_hides(F, value, far):
+    """Hidden buckets: near ones (the row's own key among them) leave a document's first rows empty."""
+    p = Problem(F, [200, 3, 140], 2, 2, 64, seed=13, buckets=(8, 20, False))
+    p.table[(slice(6, 8) if far else slice(0, 3)), 1] = value
+    p.ref_kw["rel"] = S.bucket_bias(f64(p.table), 20, False, 20)[0]
+    out, lse, got = p.check()
+    if not far:
+        empty = [0, 1, 2, 200, 201, 202, 203, 204, 205]
+        assert (out[empty, 1] == 0).all() and (got[0][empty, 1] == 0).all() and np.isinf(f64(lse)[1, empty]).all()
+    assert (got[3][6 if far else 0, 1] == 0).all()
+
+
+def test_largest_relative_range(F):
+    Problem(F, [2300], 1, 1, 64, seed=14, buckets=(64, 1024, True), causal=False).check()
+
+
+@pytest.mark.parametrize("scale", [1e-6, 0.02, 3.0])
+def test_scales(F, scale):
+    Problem(F, [140, 60], 2, 1, 128, seed=15, scale=scale, softcap=4.0, slopes=True).check()
+
+
+@pytest.mark.parametrize("cap", [1e-3, 0.05, 700.0, 1e6])
+def test_caps_of_every_size(F, cap):
+    Problem(F, [140, 60], 2, 1, 128, seed=16, softcap=cap, gain=4.0).check()
+
+
+def test_negative_slopes_and_many_documents(F):
+    Problem(F, [1] * 40 + [7] * 20 + [129] * 3, 3, 3, 64, seed=17, slopes=[-0.4, 0.0, 1.0], pad=1).check()
+
+
+def test_no_tokens(F):
+    import torch
+    att = F.FlamiaScoredAttention(0, 2, 2, 1, 64, buckets=(8, 20, False))
+    cu = dev([0, 0, 0], torch.int32)
+    att.plan_build(cu)
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")
+    out, lse = att.forward(z(0, 2, 64), z(0, 1, 64), z(0, 1, 64), cu, table=z(8, 2, dtype=torch.float32))
+    att.drel_bias.fill_(3.0)
+    got = att.backward(z(0, 2, 64), z(0, 1, 64), z(0, 1, 64), out, lse, out, cu, table=z(8, 2, dtype=torch.float32))
+    assert out.numel() == 0 and (got[3] == 0).all()
+    Problem(F, [0, 0], 2, 1, 64, pad=5, softcap=3.0).check()
+
+
+def test_bad_cu_seqlens(F):
+    import torch
+    p = Problem(F, [100, 28], 2, 1, 64, seed=18, softcap=3.0)
+    p.cu.copy_(dev([0, 90, 40], torch.int32))
+    p.att.plan_build(p.cu)
+    out, lse = p.forward()
+    got = p.backward(out, lse)
+    assert p.att.device_status() == F.DEV_BAD_CU_SEQLENS
+    assert (out == 0).all() and torch.isinf(lse).all() and all((g == 0).all() for g in got)
+
+
+# ------------------------------------------------------------------ how the calls are made
+
+KW = dict(softcap=20.0, slopes=True, buckets=(16, 100, False), prefix=[50, 0])
+
+
+def test_equal_inputs_give_equal_bits(F):
+    p = Problem(F, [900, 333], 6, 2, 128, seed=21, **KW)
+    want = run_all(p)
+    for _ in range(3):
+        assert same(run_all(p), want)
+
+
+def test_any_plan_of_the_same_documents(F):
+    p = Problem(F, [700, 333], 2, 1, 64, seed=22, window=(200, -1), softcap=20.0)
+    want = run_all(p)
+    F.flamia_plan_build(p.cu, 2, p.T, p.att.plan)          # a plan of the plain causal call
+    assert same(run_all(p), want)
+
+
+def test_captured_and_replayed(F):
+    import torch
+    p = Problem(F, [700, 333], 4, 2, 128, seed=23, **KW)
+    want = run_all(p)
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        p.att.plan_build(p.cu)
+        out, lse = p.forward()
+    with torch.cuda.graph(g2):
+        p.backward(out, lse)
+    outs = (p.att.out, p.att.lse, p.att.dq, p.att.dk, p.att.dv, p.att.dtable)
+    for _ in range(2):
+        for t in outs:
+            t.fill_(float("nan"))
+        p.att.workspace.fill_(255)
+        g1.replay()
+        g2.replay()
+        torch.cuda.synchronize()
+        assert same(bits(*outs), want)
+
+
+def test_other_streams_and_two_calls_at_once(F):
+    import torch
+    p1 = Problem(F, [1500, 333], 4, 2, 128, seed=24, **KW)
+    p2 = Problem(F, [64, 2000], 8, 8, 64, seed=25, softcap=5.0, causal=False)
+    want = run_all(p1), run_all(p2)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for p, s in ((p1, s1), (p2, s2)):
+            p.extra["stream"] = s
+            out, lse = p.forward()
+            p.backward(out, lse)
+    torch.cuda.synchronize()
+    for p, w in ((p1, want[0]), (p2, want[1])):
+        a = p.att
+        assert same(bits(a.out, a.lse, a.dq, a.dk, a.dv, *([a.dtable] if p.table is not None else [])), w)
+
+
+def test_two_calls_on_one_plan(F):
+    """The plan is only read: two forwards on it overlap."""
+    import torch
+    p = Problem(F, [1500, 700], 4, 4, 128, seed=26, softcap=20.0)
+    want = bits(*p.forward())
+    o = F.default_score_options()
+    o.softcap = 20.0
+    outs = [(torch.empty_like(p.att.out), torch.empty_like(p.att.lse)) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for (out, lse), s in zip(outs, streams):
+        F.flamia_scored_fwd(p.q, p.k, p.v, p.cu, 2, p.att.plan, out, lse, opts=o, stream=s)
+    torch.cuda.synchronize()
+    for x in outs:
+        assert same(bits(*x), want)
+
+
+def test_outputs_at_the_smallest_alignment(F):
+    """16-byte aligned tensors (views that start eight elements into an allocation)."""
+    import torch
+    p = Problem(F, [300, 77], 2, 1, 64, seed=27, softcap=20.0)
+    want = run_all(p)
+
+    def moved(t):
+        n = 16 // t.element_size()
+        buf = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")
+        v = buf[n:].view(t.shape)
+        v.copy_(t)
+        return v
+    for n in ("q", "k", "v", "do"):
+        setattr(p, n, moved(getattr(p, n)))
+    for n in ("out", "dq", "dk", "dv", "lse"):
+        setattr(p.att, n, moved(getattr(p.att, n)))
+    assert same(run_all(p), want)
+
+
+def test_offsets_past_32_bits(F):
+    """2.3e9 query elements: the last documents' rows against the definition."""
+    import torch
+    n, hq, d = 18000, 1000, 128
+    lengths = [120] * (n // 120)
+    T = n
+    att = F.FlamiaScoredAttention(T, len(lengths), hq, 1, d, softcap=20.0)
+    cu = dev(np.concatenate([[0], np.cumsum(lengths)]), torch.int32)
+    att.plan_build(cu)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.empty(T, hq, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    do = torch.empty_like(q).normal_(generator=g)
+    k, v = (torch.empty(T, 1, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    assert q.numel() > 1 << 31
+    out, lse = att.forward(q, k, v, cu)
+    dq, dk, dv = att.backward(q, k, v, out, lse, do, cu)
+    torch.cuda.synchronize()
+    assert att.device_status() == 0
+    rows = slice(T - 120, T)
+    heads = [0, 1, 499, 998, 999]
+    ref = S.run(f64(q[rows][:, heads]), f64(k[rows].expand(-1, 5, -1)), f64(v[rows].expand(-1, 5, -1)), [120],
+                dout=f64(do[rows][:, heads]), out=f64(out[rows][:, heads]), lse=f64(lse[heads][:, rows]), softcap=20.0)
+    within("o", f64(out[rows][:, heads]), ref["o"], ref["tol_o"])
+    within("dq", f64(dq[rows][:, heads]), ref["dq"], ref["tol_dq"])
+    assert (out[:5].float().abs().sum((1, 2)) > 0).all() and torch.isfinite(dk.float()).all() and torch.isfinite(dv.float()).all()
+
+
+def test_layers_of_a_training_step(F):
+    """Two layers as a model uses them: capped scores with a prefix, then a bucketed bias; the second's
+    gradient with respect to its queries is the first's dO.  Against the definition on the same bf16 values."""
+    import torch
+    lengths = [400, 57, 130]
+    a = Problem(F, lengths, 4, 2, 64, seed=31, softcap=15.0, prefix=[100, 0, 9], gain=3.0)
+    b = Problem(F, lengths, 4, 2, 64, seed=32, buckets=(32, 128, False))
+    o1, l1 = a.forward()
+    b.q = o1.clone()
+    o2, l2 = b.forward()
+    dq2 = b.backward(o2, l2)
+    a.do = dq2[0].clone()
+    dq1 = a.backward(o1, l1)
+    torch.cuda.synchronize()
+    r2 = S.run(f64(b.q), f64(b.k), f64(b.v), dout=f64(b.do), out=f64(o2), lse=f64(l2), **b.ref_kw)
+    r1 = S.run(f64(a.q), f64(a.k), f64(a.v), dout=f64(a.do), out=f64(o1), lse=f64(l1), **a.ref_kw)
+    for got, ref in ((dq2, r2), (dq1, r1)):
+        for name, t in zip(("dq", "dk", "dv"), got):
+            within(name, f64(t), ref[name], ref["tol_" + name])
+    # a step along the whole chain's gradient lowers <o2, do> by its own size (differences of the bf16 chain)
+    eps = 0.02
+    dirn = f64(dq1[0]) / np.linalg.norm(f64(dq1[0]))
+    q0 = f64(a.q)
+
+    def loss(s):
+        a.q = torch.from_numpy(q0 + s * dirn * np.sqrt(dirn.size)).to(torch.bfloat16).cuda()
+        b.q = a.forward()[0].clone()
+        x = f64(a.q)
+        return float((f64(b.forward()[0]) * f64(b.do)).sum()), x
+    (hi, xh), (lo, xl) = loss(eps), loss(-eps)
+    want = float((f64(dq1[0]) * (xh - xl)).sum())
+    # o2 is rounded to bf16 once and o1 in between: 2^-8 of each of the 150,000 terms, random in sign
+    noise = 4 * 2.0 ** -8 * np.sqrt(2 * (f64(b.att.out) ** 2 * f64(b.do) ** 2).sum()) + 4 * 2.0 ** -8 * np.sqrt(
+        2 * (f64(o1) ** 2 * f64(dq2[0]) ** 2).sum())
+    assert abs((hi - lo) - want) <= noise + 0.1 * abs(want)
