@@ -438,9 +438,8 @@ int flamia_scored_fwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
 
 size_t flamia_scored_bwd_workspace_bytes(int64_t total_tokens, int num_seqs, int hq, int hkv, int head_dim,
                                          int rel_max) {
-  (void)hkv;
-  if (total_tokens < 0 || num_seqs < 0 || hq <= 0 || head_dim <= 0 || rel_max < 0) return 0;
-  return scored_bwd_layout(total_tokens, num_seqs, hq, rel_max).total;
+  if (total_tokens < 0 || num_seqs < 0 || hq <= 0 || hkv <= 0 || head_dim <= 0 || rel_max < 0) return 0;
+  return scored_bwd_layout(total_tokens, num_seqs, hq, hkv, head_dim, rel_max).total;
 }
 
 int flamia_scored_bwd(const void* q_bf16, const void* k_bf16, const void* v_bf16, const void* out_bf16,
@@ -468,7 +467,7 @@ int flamia_scored_bwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
     return FLAMIA_ERR_MISALIGNED;
   ScoredParams p = scored_params(q_bf16, k_bf16, v_bf16, cu_seqlens, num_seqs, total_tokens, hq, hkv, head_dim, causal,
                                  softmax_scale, opt, plan);
-  const ScoredBwdWorkspace w = scored_bwd_layout(total_tokens, num_seqs, hq, drel_bias ? p.R : 0);
+  const ScoredBwdWorkspace w = scored_bwd_layout(total_tokens, num_seqs, hq, hkv, head_dim, drel_bias ? p.R : 0);
   if (workspace_bytes < w.total) return FLAMIA_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -481,6 +480,10 @@ int flamia_scored_bwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
   p.drel = drel_bias;
   p.dvec = reinterpret_cast<float*>(ws + w.dvec);
   p.drel_part = reinterpret_cast<float*>(ws + w.drel);
+  if (scored_bwd_split(total_tokens, num_seqs, hq, hkv)) {
+    p.dk_part = reinterpret_cast<float*>(ws + w.dk);
+    p.dv_part = reinterpret_cast<float*>(ws + w.dv);
+  }
   return cuda_status(launch_scored_bwd(head_dim, p, s));
 }
 

@@ -5,19 +5,30 @@
 // same, so the scored attention kernels see a bias by clipped distance: 2R + 1 floats a
 // head instead of a bucket per pair.  Both kernels touch a few KB (32 buckets, 16 heads,
 // R = 128: 16 KB each) and are bound by their launch.
+#include <cmath>
+
 #include "common.cuh"
 
 namespace flamia {
 
 namespace {
 
-// Bucket of distance r (key minus query).  The logarithms are in 64 bits: a distance n
-// with ((n / e) ^ (B - e) a whole power of max_distance / e) lies on a bucket's border, and
-// 2^-30 puts it into the upper bucket whatever the last bit of the quotient; no other n up
-// to 1024 comes that close to a border from below.
-__device__ int rel_bucket(int r, int nb, int md, int both) {
-  int base = 0, n;
-  if (both) {
+struct Buckets {
+  int nb, md, both;
+  double per_log;      // far buckets per unit of the logarithm
+};
+Buckets make_buckets(int nb, int md, int both) {
+  const int side = both ? nb / 2 : nb, e = side / 2;
+  return {nb, md, both, (side - e) / std::log((double)md / e)};
+}
+
+// Bucket of distance r (key minus query).  The logarithm is in 64 bits: a distance n with
+// (n / e) ^ (B - e) a whole power of max_distance / e lies on a bucket's border, and 2^-30
+// puts it into the upper bucket whatever the last bit of the product; no other n up to 1024
+// comes that close to a border from below.
+__device__ int rel_bucket(int r, const Buckets& B) {
+  int base = 0, n, nb = B.nb;
+  if (B.both) {
     nb >>= 1;
     base = r > 0 ? nb : 0;
     n = r < 0 ? -r : r;
@@ -26,39 +37,40 @@ __device__ int rel_bucket(int r, int nb, int md, int both) {
   }
   const int e = nb >> 1;
   if (n < e) return base + n;
-  if (n >= md) return base + nb - 1;
-  const double x = log((double)n / e) / log((double)md / e) * (nb - e);
-  const int b = e + (int)floor(x + 0x1p-30);
+  if (n >= B.md) return base + nb - 1;
+  const int b = e + (int)floor(log((double)n / e) * B.per_log + 0x1p-30);
   return base + (b < nb - 1 ? b : nb - 1);
 }
 
-__global__ void relbias_expand_kernel(const float* __restrict__ table, int nb, int hq, int md, int both,
-                                      float* __restrict__ rel, int R) {
+__global__ void relbias_expand_kernel(const float* __restrict__ table, int hq, Buckets B, float* __restrict__ rel,
+                                      int R) {
   const int width = 2 * R + 1;
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= width) return;
-  const int b = rel_bucket(i - R, nb, md, both);
+  const int b = rel_bucket(i - R, B);
   for (int h = blockIdx.y; h < hq; h += gridDim.y) rel[(size_t)h * width + i] = table[(size_t)b * hq + h];
 }
 
-// One block per head: the entries' buckets go to shared memory, then thread b sums its own
-// bucket's entries in increasing distance.  A bucket's entries are consecutive distances on
-// each side, so the scan over all 2R + 1 (one shared read per entry, broadcast) is short.
-__global__ void relbias_reduce_kernel(const float* __restrict__ drel, int R, int nb, int hq, int md, int both,
-                                      float* __restrict__ dtable) {
+// One block per head: the entries' buckets go to shared memory, then a warp sums a bucket at
+// a time, lane l the distances l, l + 32, ... in order, and the lanes' sums in a fixed tree.
+__global__ void __launch_bounds__(512) relbias_reduce_kernel(const float* __restrict__ drel, int R, int hq, Buckets B,
+                                                             float* __restrict__ dtable) {
   __shared__ float val[2 * FLAMIA_REL_MAX + 1];
   __shared__ short id[2 * FLAMIA_REL_MAX + 1];
   const int width = 2 * R + 1, h = blockIdx.x;
   for (int i = threadIdx.x; i < width; i += blockDim.x) {
     val[i] = drel[(size_t)h * width + i];
-    id[i] = (short)rel_bucket(i - R, nb, md, both);
+    id[i] = (short)rel_bucket(i - R, B);
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < nb; b += blockDim.x) {
+  const int lane = threadIdx.x & 31;
+  for (int b = threadIdx.x >> 5; b < B.nb; b += blockDim.x >> 5) {
     float s = 0.f;
-    for (int i = 0; i < width; ++i)
+    for (int i = lane; i < width; i += 32)
       if (id[i] == b) s += val[i];
-    dtable[(size_t)b * hq + h] = s;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) dtable[(size_t)b * hq + h] = s;
   }
 }
 
@@ -66,14 +78,14 @@ __global__ void relbias_reduce_kernel(const float* __restrict__ drel, int R, int
 
 cudaError_t launch_relbias_expand(const float* table, int nb, int hq, int md, int both, float* rel, int R,
                                   cudaStream_t s) {
-  const dim3 grid((2 * R + 1 + 127) / 128, hq < 32 ? hq : 32);
-  relbias_expand_kernel<<<grid, 128, 0, s>>>(table, nb, hq, md, both, rel, R);
+  const dim3 grid((2 * R + 1 + 127) / 128, hq < 128 ? hq : 128);
+  relbias_expand_kernel<<<grid, 128, 0, s>>>(table, hq, make_buckets(nb, md, both), rel, R);
   return cudaGetLastError();
 }
 
 cudaError_t launch_relbias_reduce(const float* drel, int R, int nb, int hq, int md, int both, float* dtable,
                                   cudaStream_t s) {
-  relbias_reduce_kernel<<<hq, 256, 0, s>>>(drel, R, nb, hq, md, both, dtable);
+  relbias_reduce_kernel<<<hq, 512, 0, s>>>(drel, R, hq, make_buckets(nb, md, both), dtable);
   return cudaGetLastError();
 }
 

@@ -37,12 +37,21 @@ struct ScoredParams {
   float* drel;               // [hq, 2R+1] or null
   float* dvec;               // workspace: D [hq, T]
   float* drel_part;          // workspace: partial sums of drel
+  float *dk_part, *dv_part;  // workspace: dK, dV of each query head [T, hq, D] (split) or null
 };
 
+// The dK/dV units are key tiles of a kv head, which walk the query heads that share it one
+// after the other.  With fewer than four such units an SM the longest one sets the time (a
+// prefix that every query sees: one unit of 132 steps beside 70 on average), so each query
+// head's share becomes a unit of its own, and its sums go through memory in fp32.
+constexpr int64_t kSplitBelow = 4 * 152;
+inline bool scored_bwd_split(int64_t T, int N, int hq, int hkv) {
+  return hq > hkv && plan_capacity(T, N) * hkv < kSplitBelow;
+}
 struct ScoredBwdWorkspace {
-  size_t dvec, drel, total;
+  size_t dvec, drel, dk, dv, total;
 };
-inline ScoredBwdWorkspace scored_bwd_layout(int64_t T, int N, int hq, int R) {
+inline ScoredBwdWorkspace scored_bwd_layout(int64_t T, int N, int hq, int hkv, int d, int R) {
   auto round256 = [](size_t x) { return (x + 255) & ~size_t(255); };
   ScoredBwdWorkspace w;
   size_t off = 0;
@@ -50,6 +59,10 @@ inline ScoredBwdWorkspace scored_bwd_layout(int64_t T, int N, int hq, int R) {
   off = round256(off + (size_t)T * hq * 4);
   w.drel = off;
   if (R > 0) off = round256(off + (size_t)plan_capacity(T, N) * hq * (2 * R + 1) * 4);
+  const size_t part = scored_bwd_split(T, N, hq, hkv) ? round256((size_t)T * hq * d * 4) : 0;
+  w.dk = off;
+  w.dv = off + part;
+  off += 2 * part;
   w.total = off > 0 ? off : 256;
   return w;
 }

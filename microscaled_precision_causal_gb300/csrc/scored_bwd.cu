@@ -97,6 +97,21 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, __nv_bfloat16* dst, fl
     }
   }
 }
+// The same in fp32.
+template <int COLS>
+__device__ __forceinline__ void store_part(uint32_t taddr, float* dst, bool valid) {
+#pragma unroll 1
+  for (int c = 0; c < COLS / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld32(taddr + 32 * c, o);
+    tmem_ld_wait();
+    if (valid) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4*>(dst + 32 * c + 4 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    }
+  }
+}
 __device__ __forceinline__ uint32_t pack2(float2 x) {
   const __nv_bfloat162 b2 = __floats2bfloat162_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&b2);
@@ -155,7 +170,7 @@ struct DkvSmem {
 };
 
 struct KeyUnit {
-  int item, hk, u, start, len, nt, pre, tlo, nq;
+  int item, h0, hk, u, start, len, nt, pre, tlo, nq;      // h0: the unit's first query head
   int2 full;                // query tiles that see the key tile whole
 };
 // What a unit's first loads bring; fetched a unit ahead, so that their latency is not met.
@@ -164,10 +179,13 @@ struct RawUnit {
   int4 item;
   int2 span;
 };
+// Units per key tile, and query heads per unit.
+__device__ __forceinline__ int unit_heads(const ScoredParams& p) { return p.dk_part ? p.hq : p.hkv; }
 __device__ __forceinline__ KeyUnit key_unit(const ScoredParams& p, const RawUnit& raw) {
   KeyUnit U;
-  U.item = raw.i / p.hkv;
-  U.hk = raw.i % p.hkv;
+  U.item = raw.i / unit_heads(p);
+  U.h0 = raw.i % unit_heads(p) * (p.hq / unit_heads(p));
+  U.hk = U.h0 / (p.hq / p.hkv);
   const int4 item = raw.item;
   const int2 span = raw.span;
   U.u = item.y;
@@ -191,28 +209,28 @@ struct KeySteps {
   __device__ __forceinline__ void fetch(const ScoredParams& p, const PlanView& pv, int k) {
     raw.i = unit_index(k, n_units);
     if (raw.i < 0) return;
-    raw.item = pv.bwd_items[raw.i / p.hkv];
-    raw.span = pv.bwd_span[raw.i / p.hkv];
+    raw.item = pv.bwd_items[raw.i / unit_heads(p)];
+    raw.span = pv.bwd_span[raw.i / unit_heads(p)];
   }
   __device__ __forceinline__ bool unit(const ScoredParams& p, const PlanView& pv) {
     if (raw.i < 0) return false;
     U = key_unit(p, raw);
     fetch(p, pv, n + 1);
-    h = U.hk * group;
+    h = U.h0;
     t = U.tlo;
     return true;
   }
   __device__ __forceinline__ bool begin(const ScoredParams& p, const PlanView& pv) {
     n = 0;
-    n_units = p.plan[kPlanBwdItems] * p.hkv;
-    group = p.hq / p.hkv;
+    n_units = p.plan[kPlanBwdItems] * unit_heads(p);
+    group = p.hq / unit_heads(p);
     fetch(p, pv, 0);
     return unit(p, pv);
   }
   __device__ __forceinline__ bool head_first() const { return t == U.tlo; }
   __device__ __forceinline__ bool head_last() const { return t == U.tlo + U.nq - 1; }
-  __device__ __forceinline__ bool first() const { return h == U.hk * group && head_first(); }
-  __device__ __forceinline__ bool last() const { return h == (U.hk + 1) * group - 1 && head_last(); }
+  __device__ __forceinline__ bool first() const { return h == U.h0 && head_first(); }
+  __device__ __forceinline__ bool last() const { return h == U.h0 + group - 1 && head_last(); }
   __device__ __forceinline__ bool next(const ScoredParams& p, const PlanView& pv) {
     if (last()) {
       ++n;
@@ -437,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
        if (p.win.right >= 0) lo0 = kj - p.win.right;
        if (p.win.left >= 0) hi0 = min(hi0, kj + p.win.left);
      }
-     for (int h = U.hk * S.group; h < (U.hk + 1) * S.group; ++h) {
+     for (int h = U.h0; h < U.h0 + S.group; ++h) {
       if constexpr (BIAS != 0) {
         if (staged != h) {
           named_bar_sync(1, kCompute);
@@ -618,10 +636,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           tc_fence_after();
           const bool valid = kj < U.len;
-          const int64_t at = ((int64_t)(U.start + kj) * p.hkv + U.hk) * D;
           const int c = (w & 1) * (D / 2);
-          if (w < 2) store_acc<D / 2>(lane_base + kTV + c, p.dv + at + c, 1.f, valid);
-          else store_acc<D / 2>(lane_base + kTK + c, p.dk + at + c, p.scale, valid);
+          const uint32_t sum = lane_base + (w < 2 ? kTV : kTK) + c;
+          if (p.dk_part) {
+            float* part = w < 2 ? p.dv_part : p.dk_part;
+            store_part<D / 2>(sum, part + ((int64_t)(U.start + kj) * p.hq + U.h0) * D + c, valid);
+          } else {
+            __nv_bfloat16* out = w < 2 ? p.dv : p.dk;
+            store_acc<D / 2>(sum, out + ((int64_t)(U.start + kj) * p.hkv + U.hk) * D + c, w < 2 ? 1.f : p.scale, valid);
+          }
           tc_fence_before();
           mbar_arrive(acc_free);
         }
@@ -989,6 +1012,30 @@ __global__ void __launch_bounds__(256) scored_drel_kernel(const float* __restric
   }
 }
 
+// dK and dV of a kv head from those of its query heads, in their order (split): four columns
+// a thread.
+template <int D>
+__global__ void __launch_bounds__(256) scored_heads_kernel(const ScoredParams p) {
+  const int group = p.hq / p.hkv;
+  const int64_t n = (int64_t)p.plan[kPlanValid] * p.hkv * (D / 4);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / (D / 4);                       // token * hkv + kv head
+    const int c = (int)(i % (D / 4)) * 4;
+    const float* part = blockIdx.y ? p.dv_part : p.dk_part;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; g < group; ++g) {
+      const float4 x = *reinterpret_cast<const float4*>(part + (row * group + g) * D + c);
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+    const float f = blockIdx.y ? 1.f : p.scale;
+    const uint2 out = make_uint2(pack2(make_float2(s.x * f, s.y * f)), pack2(make_float2(s.z * f, s.w * f)));
+    *reinterpret_cast<uint2*>((blockIdx.y ? p.dv : p.dk) + row * D + c) = out;
+  }
+}
+
 template <int D, bool CAP, int BIAS>
 cudaError_t launch(const ScoredParams& p, cudaStream_t stream) {
   CUtensorMap tq, tk, tv, tdo;
@@ -1009,10 +1056,11 @@ cudaError_t launch(const ScoredParams& p, cudaStream_t stream) {
   const int64_t tiles = (int64_t)p.T / kTile + p.N + 1, items = (int64_t)p.T / (kTile * kItemTiles) + p.N + 1;
   constexpr int kRows = 256 / (D / 8);
   const int64_t prep = (((int64_t)p.T + kRows - 1) / kRows) * p.hq;
-  if (tiles * p.hkv > 0x7FFFFFFF || items * 2 * p.hq > 0x7FFFFFFF || prep > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  if (tiles * p.hq > 0x7FFFFFFF || items * 2 * p.hq > 0x7FFFFFFF || prep > 0x7FFFFFFF) return cudaErrorInvalidValue;
   scored_prep_kernel<D><<<(unsigned)prep, 256, 0, stream>>>(p);
-  const unsigned g1 = (unsigned)std::min<int64_t>(tiles * p.hkv, sms), g2 = (unsigned)std::min<int64_t>(items * 2 * p.hq, sms);
+  const unsigned g1 = (unsigned)std::min<int64_t>(tiles * (p.dk_part ? p.hq : p.hkv), sms), g2 = (unsigned)std::min<int64_t>(items * 2 * p.hq, sms);
   scored_dkv_kernel<D, CAP, BIAS><<<g1, kThreads, smem1, stream>>>(tq, tk, tv, tdo, p);
+  if (p.dk_part) scored_heads_kernel<D><<<dim3(sms, 2), 256, 0, stream>>>(p);
   scored_dq_kernel<D, CAP, BIAS != 0><<<g2, kThreads, smem2, stream>>>(tk, tv, p);
   if (BIAS == 2) {
     const dim3 grid((2 * p.R + 1 + 31) / 32, p.hq);
