@@ -4,8 +4,15 @@
 //   O += bf16(p) V,  O = bf16(O / l), LSE = (m + log2 l) ln 2.
 //
 // A unit is a forward work item of the plan (up to two document-local 128-query tiles) and
-// a query head; one CTA per SM walks the cost-sorted units in boustrophedon order.  Roles
-// (512 threads):
+// a query head, in the plan's cost order.  Below kTakeBelow units per SM the grid has a CTA
+// per unit, and a running CTA takes over one that has not started (cluster launch control):
+// units go to whoever is free, and a CTA's pipelines run on across them.  Taken over against dealt
+// out in boustrophedon rounds to a CTA per SM, D = 128, us: documents of 84 to 2886, 16384 rows,
+// 8 units per SM 205 / 220, 16 units 400 / 425, 32 units 785 / 836; two documents of 16384,
+// 14 units 1698 / 1815; four of 8192, 7 units 453 / 492, 28 units 1820 / 1760.  With many units a
+// round evens itself out, and rounds keep the query heads of one kv head at the same keys,
+// which pays where the keys and values of a round are more than L2 holds.
+// Roles (512 threads):
 //   warp 0        TMA producer: Q tiles, K and V tiles through a ring
 //   warp 1        MMA issuer: a query tile's products (O += P V, then its next scores over P)
 //                 are queued whole before the other's, so that the two softmax warpgroups get
@@ -55,20 +62,24 @@ static_assert(kRegCtl * 128 + kRegAux * 128 + kRegSoftmax * 256 <= kLaunchRegs *
 
 // A unit's description, worked out by one warp some units ahead and read by every role from
 // shared memory: the divisions and the dependent loads behind it stay off their paths.
-struct Unit {
+struct alignas(16) Unit {
   int h, hk, t0, ntq;     // ntq 0: no more units
   int start, len, pre, skip0;
   KeyTiles kt;
+  int index;              // in the list
   int skip1;              // skip0 / 1: the one place of the list that the first / second query tile does not see, or -1
 };
-static_assert(sizeof(Unit) == 48, "read as three 16-byte words");
+static_assert(sizeof(Unit) == 64, "read as four 16-byte words");
 constexpr int kUnits = 8;  // described at a time: more units than the K / V ring can hold tiles of
+constexpr int kTakeBelow = 24;              // units per SM below which they are taken over, not dealt out
+constexpr int kAskAhead = 1;                // the next unit is asked for before the last so many key tiles of one are loaded
 
 __device__ __forceinline__ Unit make_unit(const ScoredParams& p, const PlanView& pv, int i) {
   Unit U{};
   if (i < 0) return U;
   const int4 item = pv.fwd_items[i / p.hq];
   const int2 span = pv.fwd_span[i / p.hq];
+  U.index = i;
   U.h = i % p.hq;
   U.hk = U.h / (p.hq / p.hkv);
   U.t0 = item.y;
@@ -92,11 +103,11 @@ __device__ __forceinline__ Unit read_unit(const uint8_t* units, uint64_t* full, 
   if (whole_warp) ok = __all_sync(0xffffffffu, ok);
   union {
     Unit u;
-    int4 w[3];
+    int4 w[4];
   } x;
   const int4* src = reinterpret_cast<const int4*>(units + (n % kUnits) * sizeof(Unit));
 #pragma unroll
-  for (int i = 0; i < 3; ++i) x.w[i] = src[i];
+  for (int i = 0; i < 4; ++i) x.w[i] = src[i];
   if (!ok) x.u.ntq = 0;
   return x.u;
 }
@@ -110,7 +121,8 @@ struct FwdSmem {
   static constexpr int kBias = kKV + kSlots * kTileBytes;   // [2 units in turn][kBiasTab] floats
   static constexpr int kInv = kBias + 2 * kBiasTab * 4;     // [2 query tiles][128] 1 / l
   static constexpr int kUnit = kInv + 1024;                 // [kUnits]
-  static constexpr int kBar = kUnit + kUnits * 48;
+  static constexpr int kClc = kUnit + kUnits * 64;          // answer to a request for another CTA's unit
+  static constexpr int kBar = kClc + 16;
   static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -118,7 +130,7 @@ struct FwdSmem {
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     scored_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const ScoredParams p) {
+                      const __grid_constant__ CUtensorMap tm_v, const ScoredParams p, const bool take) {
   using L = FwdSmem<D>;
   constexpr int kSlots = L::kSlots;
   constexpr bool kSplit = D == 64;
@@ -136,9 +148,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = bars + 16;             // [2 query tiles][2 halves of 64 keys]
   uint64_t* tab_full = bars + 20;           // [2 units in turn]
   uint64_t* drain = bars + 22;              // [2 issuers]
-  uint64_t* unit_done = bars + 24;
-  uint64_t* unit_full = bars + 25;          // [kUnits]
-  uint64_t* kv_full = unit_full + kUnits;   // [kSlots]
+  uint64_t* unit_ask = bars + 24;
+  uint64_t* clc_bar = bars + 25;
+  uint64_t* unit_full = bars + 26;          // [kUnits]
+  uint64_t* unit_done = unit_full + kUnits; // [kUnits]
+  uint64_t* kv_full = unit_done + kUnits;   // [kSlots]
   uint64_t* kv_empty = kv_full + kSlots;    // [kSlots]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + kSlots);
   int* status = const_cast<int*>(p.plan) + kPlanStatus;
@@ -146,6 +160,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_units = p.plan[kPlanFwdItems] * p.hq;
   uint8_t* units = smem + L::kUnit;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Rows outside every document (O = 0, LSE = +inf) are dealt out to the units, or to all CTAs
+  // where there is none.
+  auto clear_tail = [&](int64_t part, int64_t parts, int r, int threads) {
+    const int valid = p.plan[kPlanValid];
+    const int64_t rows = (int64_t)(p.T - valid) * p.hq;
+    for (int64_t i = part * threads + r; i < rows; i += parts * threads) {
+      const int64_t row = valid + i / p.hq;
+      const int h = (int)(i % p.hq);
+      uint4* dst = reinterpret_cast<uint4*>(p.out + (row * p.hq + h) * D);
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) dst[j] = make_uint4(0, 0, 0, 0);
+      p.lse[(int64_t)h * p.T + row] = INFINITY;
+    }
+  };
+  if ((int64_t)blockIdx.x >= n_units) {        // the grid goes by a bound on the units
+    if (n_units == 0) clear_tail(blockIdx.x, gridDim.x, threadIdx.x, kThreads);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -162,8 +194,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tab_full[i], 128);
       mbar_init(&drain[i], 1);
     }
-    mbar_init(unit_done, 1);
-    for (int i = 0; i < kUnits; ++i) mbar_init(&unit_full[i], 1);
+    mbar_init(unit_ask, 1);
+    mbar_init(clc_bar, 1);
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&unit_full[i], 1);
+      mbar_init(&unit_done[i], 1);
+    }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], kSplit ? 2 : 1);      // issuers
@@ -205,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int k = 0; k < 2 * U.kt.n && ok; ++k, ++ring) {
           const uint32_t st = ring % kSlots;
+          if (k == max(2 * (U.kt.n - kAskAhead), 0)) mbar_arrive(unit_ask);
           if (ring >= kSlots && !(ok = mbar_wait(&kv_empty[st], (ring / kSlots - 1) & 1, status))) break;
           load(smem + L::kKV + st * L::kTileBytes, (k & 1) ? &tm_v : &tm_k, &kv_full[st], U.hk,
                U.start + U.kt.tile(k >> 1) * kTile);
@@ -216,11 +253,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int w = 0; w < 2; ++w)
         if (nq[w]) mbar_wait(&q_full[w], (nq[w] - 1) & 1, status);
     } else if (warp == 2 && lane == 0) {
-      // ---------------------------------------------------------- unit descriptions
+      // ---------------------------------------------------------- units
+      // Dealt out: in boustrophedon order, described as far ahead as there are slots.  Taken over: the
+      // CTA's own unit first; then, whenever the loads of a unit come to their end, the unit of a CTA
+      // that has not started, whose launch is cancelled.
       bool ok = true;
+      int i = blockIdx.x;
+      uint32_t asked = 0;
       for (int n = 0; ok; ++n) {
-        if (n >= kUnits && !(ok = mbar_wait(unit_done, (n - kUnits) & 1, status))) break;
-        const Unit U = make_unit(p, pv, unit_index(n, n_units));
+        if (n >= kUnits && !(ok = mbar_wait(&unit_done[n % kUnits], (n / kUnits - 1) & 1, status))) break;
+        if (!take) {
+          i = unit_index(n, n_units);
+        } else if (n > 0) {
+          if (!(ok = mbar_wait(unit_ask, (n - 1) & 1, status))) break;
+          do {
+            fence_proxy_async_smem();          // the last answer was read before the next one lands
+            mbar_arrive_expect_tx(clc_bar, 16);
+            clc_try_cancel(smem + L::kClc, clc_bar);
+            if (!(ok = mbar_wait(clc_bar, asked++ & 1, status))) break;
+            i = clc_cancelled_x(smem + L::kClc);
+          } while (i >= n_units);              // a CTA without a unit
+        }
+        const Unit U = make_unit(p, pv, ok ? i : -1);
         *reinterpret_cast<Unit*>(units + (n % kUnits) * sizeof(Unit)) = U;
         mbar_arrive(&unit_full[n % kUnits]);
         if (U.ntq == 0) break;
@@ -546,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&tab_full[0]);
     }
     for (int n = 0; ok && U.ntq; ++n) {
-      const int h = U.h, t0 = U.t0, ntq = U.ntq, start = U.start, len = U.len;
+      const int h = U.h, t0 = U.t0, ntq = U.ntq, start = U.start, len = U.len, index = U.index;
       U = read_unit(units, unit_full, n + 1, true, ok, status);
       if (BIAS && U.ntq) {            // into the table of the last unit but one, whose O is out
         stage_bias(tab + ((n + 1) & 1) * kBiasTab, p, U.h, r, 128);
@@ -591,18 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (r == 0 && ok) mbar_arrive(unit_done);
-    }
-    // rows outside every document: O = 0, LSE = +inf
-    const int valid = p.plan[kPlanValid];
-    const int64_t rows = (int64_t)(p.T - valid) * p.hq;
-    for (int64_t i = (int64_t)blockIdx.x * 128 + r; i < rows; i += (int64_t)gridDim.x * 128) {
-      const int64_t row = valid + i / p.hq;
-      const int h = (int)(i % p.hq);
-      uint4* dst = reinterpret_cast<uint4*>(p.out + (row * p.hq + h) * D);
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) dst[j] = make_uint4(0, 0, 0, 0);
-      p.lse[(int64_t)h * p.T + row] = INFINITY;
+      if (r == 0 && ok) mbar_arrive(&unit_done[n % kUnits]);
+      clear_tail(index, n_units, r, 128);
     }
   }
   tc_fence_before();
@@ -621,15 +665,18 @@ cudaError_t launch(const ScoredParams& p, cudaStream_t stream) {
       !make_tmap_bf16_3d(&tv, p.v, D, p.hkv, p.T, D * 2, (uint64_t)p.hkv * D * 2, 64, kTile))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0, regs = 0;
+  constexpr int smem = FwdSmem<D>::kAlloc;
+  static_assert(smem <= 232448, "shared memory of one CTA");
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  constexpr int smem = FwdSmem<D>::kAlloc;
   if (e == cudaSuccess) e = prepare_kernel<scored_fwd_kernel<D, CAP, BIAS>>(smem, &regs);
   if (e != cudaSuccess) return e;
   if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;    // the register split relies on it
   const int64_t units = ((int64_t)p.T / (kTile * kItemTiles) + p.N + 1) * p.hq;
   if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  scored_fwd_kernel<D, CAP, BIAS><<<(unsigned)(units < sms ? units : sms), kThreads, smem, stream>>>(tq, tk, tv, p);
+  const bool take = units < (int64_t)kTakeBelow * sms;
+  scored_fwd_kernel<D, CAP, BIAS>
+      <<<(unsigned)(take || units < sms ? units : sms), kThreads, smem, stream>>>(tq, tk, tv, p, take);
   return cudaGetLastError();
 }
 

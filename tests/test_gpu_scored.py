@@ -237,6 +237,25 @@ def test_negative_slopes_and_many_documents(F):
     Problem(F, [1] * 40 + [7] * 20 + [129] * 3, 3, 3, 64, seed=17, slopes=[-0.4, 0.0, 1.0], pad=1).check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_units_dealt_out_and_taken_over(F, d):
+    """Many units are dealt out in rounds, fewer are taken over by whoever is free: a document's bits are the same."""
+    import torch
+    lengths = [300] + [40 + i % 50 for i in range(75)]
+    many, few = (Problem(F, ls, 64, 8, d, pad=9, softcap=6.0) for ls in (lengths, lengths[:1]))
+    for a in ("q", "k", "v"):
+        getattr(few, a).copy_(getattr(many, a)[:309])
+    out, lse, _ = many.check()
+    o, l = few.forward()
+    torch.cuda.synchronize()
+    assert torch.equal(o[:300], out[:300]) and torch.equal(l[:, :300], lse[:, :300])
+    assert torch.count_nonzero(o[300:]) == 0 and torch.isposinf(l[:, 300:]).all()
+
+
+def test_no_valid_tokens(F):
+    Problem(F, [0, 0, 0], 4, 2, 64, pad=300, slopes=True, causal=False).check()
+
+
 def test_no_tokens(F):
     import torch
     att = F.FlamiaScoredAttention(0, 2, 2, 1, 64, buckets=(8, 20, False))
