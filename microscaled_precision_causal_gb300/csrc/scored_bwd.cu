@@ -29,7 +29,18 @@ constexpr int kThreads = 128 + kCompute;
 constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
 constexpr int kRegCtl = 64, kRegCompute = 104;
 static_assert(kRegCtl * 128 + kRegCompute * kCompute <= kLaunchRegs * kThreads, "register split");
-constexpr int kStats = 4;        // staged LSE / D rows in flight
+#ifndef F128
+#define F128 0
+#define F128G 1
+#define H128 2
+#define H128G 1
+#endif
+
+// One arrival for a warp, behind what all its lanes did.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 
 // ---------------------------------------------------------------- D = rowsum(dO o O)
 // D/8 threads a row, one 16-byte load of each operand per thread; rows outside every
@@ -130,6 +141,17 @@ __device__ __forceinline__ float2 cap_slope(float2 y, float zscale) {
   return ffma2(t, make_float2(-t.x, -t.y), make_float2(1.f, 1.f));
 }
 
+// x as the sum of three bf16 (24 bits, all of it), infinities as the largest that a bf16 holds.
+__device__ __forceinline__ void split3(float x, uint32_t (&part)[3]) {
+  if (fabsf(x) > 3e38f) x = copysignf(3e38f, x);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __nv_bfloat16 b = __float2bfloat16_rn(x);
+    part[i] = __bfloat16_as_ushort(b);
+    x -= __bfloat162float(b);
+  }
+}
+
 template <int D, int ROWS = kTile>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int h, int row) {
   mbar_arrive_expect_tx(bar, ROWS * D * 2);
@@ -152,20 +174,31 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, u
 // Roles: warp 0 TMA, warp 1 MMA, warp 2 TMEM, warp 3 stages LSE and D of a step's queries,
 // warps 4-19 compute: thread = key row, warpgroup = 32 of the 128 query columns, two a half.
 // TMEM columns: dV [0, D), dK [128, 128 + D), S^T [256, 384), dP^T [384, 512).
-template <int D>
+template <int D, int BIAS>
 struct DkvSmem {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kK = 0, kV = kTileBytes;
-  static constexpr int kHalf = kTileBytes / 2;
-  static constexpr int kQ = 2 * kTileBytes;                    // [2 halves][2 stages]
-  static constexpr int kDO = 4 * kTileBytes;                   // [2 halves][2 stages]
-  static constexpr int half_at(int half, uint32_t g) { return (half * 2 + (int)(g & 1)) * kHalf; }
-  static constexpr int kStat = 6 * kTileBytes;                 // [kStats][-LSE log2 e 128, D 128]
-  static constexpr int kBias = kStat + kStats * 1024;          // [kBiasTab]
+  static constexpr int kHalves = D == 64 ? 1 : BIAS == 2 ? H128G : H128;
+  static constexpr bool kFold = D == 64 || (BIAS == 2 ? F128G : F128);
+  static constexpr int kStats = kFold ? 2 : 4;                 // steps whose LSE and D are staged
+  static constexpr int kRows = kTile / kHalves;
+  static constexpr int kStages = D == 128 ? 2 : 3;
+  static constexpr int kSBuf = D == 128 || kHalves == 2 ? 1 : 2;
+  static constexpr int kPartBytes = kTileBytes / kHalves;
+  static constexpr int kQ = 2 * kTileBytes;                    // [halves][stages]
+  static constexpr int kDO = kQ + kStages * kTileBytes;        // [halves][stages]
+  static __device__ __forceinline__ int part_at(int half, uint32_t g) { return (half * kStages + (int)(g % kStages)) * kPartBytes; }
+  // folded: [kStats][2 halves][64 queries][8], their LSE and D
+  static constexpr int kRow = kDO + kStages * kTileBytes;
+  static constexpr int kPick = kRow + (kFold ? kStats * 2048 : 0);   // [128 keys][8]: 1 where LSE is, then the same for D
+  static constexpr int kZero = kPick + (kFold ? 4096 : 0);
+  static constexpr int kLse = kZero + (kFold ? 2048 : 0);      // not folded: [kStats][128] -LSE log2 e, 128 D]
+  static constexpr int kStat = kFold ? 128 : 256;
+  static constexpr int kBias = kLse + kStats * kStat * 4;            // [kBiasTab]
   static constexpr int kAcc = kBias + kBiasTab * 4;      // [2 R + 1] drel of the current head
-  static constexpr int kDiag = kAcc + (2 * FLAMIA_REL_MAX + 2) * 4;   // [2][16 warps][64]
-  static constexpr int kBar = (kDiag + 2 * 16 * 64 * 4 + 15) & ~15;
-  static constexpr int kBytes = kBar + 384;
+  static constexpr int kDiag = kAcc + (2 * FLAMIA_REL_MAX + 2) * 4;   // [16 warps][64]
+  static constexpr int kBar = (kDiag + 16 * 64 * 4 + 15) & ~15;
+  static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;
 };
 
@@ -252,30 +285,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     scored_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                       const ScoredParams p) {
-  using L = DkvSmem<D>;
+  using L = DkvSmem<D, BIAS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t *k_full = bars, *k_empty = bars + 1, *v_full = bars + 2, *v_empty = bars + 3;
-  uint64_t *q_full = bars + 4, *q_empty = bars + 8, *do_full = bars + 12, *do_empty = bars + 16;   // [2 halves][2 stages]
-  uint64_t *s_full = bars + 20, *dp_full = bars + 22, *p_ready = bars + 24, *ds_ready = bars + 26;  // [2 halves]
-  uint64_t *acc_full = bars + 28, *acc_free = bars + 29, *drain = bars + 30;                       // drain [2]
-  uint64_t *st_full = bars + 32, *st_empty = st_full + kStats;
+  constexpr int kHalves = L::kHalves, kStages = L::kStages, kSBuf = L::kSBuf, kRows = L::kRows, kStats = L::kStats;
+  constexpr bool kFold = L::kFold, kReadStat = CAP || !kFold;
+  uint64_t *q_full = bars + 4, *q_empty = bars + 10, *do_full = bars + 16, *do_empty = bars + 22;   // [halves][stages]
+  uint64_t *s_full = bars + 28, *dp_full = bars + 30, *p_ready = bars + 32, *ds_ready = bars + 34;  // [halves or buffers]
+  uint64_t *acc_full = bars + 36, *acc_free = bars + 37, *drain = bars + 38;                       // drain [2]
+  uint64_t *st_full = bars + 40, *st_empty = st_full + kStats;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(st_empty + kStats);
   int* status = const_cast<int*>(p.plan) + kPlanStatus;
   const PlanView pv = plan_view(p.plan, p.T, p.N);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 24; ++i) mbar_init(bars + i, 1);
-    for (int i = 24; i < 28; ++i) mbar_init(bars + i, kCompute / 2);
+    for (int i = 0; i < 32; ++i) mbar_init(bars + i, 1);
+    for (int i = 32; i < 36; ++i) mbar_init(bars + i, kCompute / 32 / kHalves);
     mbar_init(acc_full, 2);
     mbar_init(acc_free, kCompute);
     mbar_init(drain, 1);
     mbar_init(drain + 1, 1);
     for (int i = 0; i < kStats; ++i) {
-      mbar_init(&st_full[i], 32);
-      mbar_init(&st_empty[i], kCompute);
+      mbar_init(&st_full[i], 1);
+      mbar_init(&st_empty[i], (kReadStat ? kCompute / 32 : 0) + (kFold ? (CAP ? 1 : 2) : 0));
     }
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
@@ -283,6 +318,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_v);
     tma_prefetch_desc(&tm_do);
   }
+  if (kFold && threadIdx.x < 384) {        // the ones that pick a row's LSE or D, and the zeros
+    const uint32_t one = 0x3F80u;
+    const int which = threadIdx.x >> 7;
+    *reinterpret_cast<uint4*>(smem + L::kPick + threadIdx.x * 16) =
+        which == 0 ? make_uint4(one | one << 16, one, 0, 0)
+                   : which == 1 ? make_uint4(0, one << 16, one | one << 16, 0) : make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
   if (warp == 2) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -291,7 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  constexpr uint32_t kTV = 0, kTK = 128, kTS = 256, kTP = 384;
+  constexpr uint32_t kTV = 0, kTK = D, kTS = kSBuf == 2 ? 128 : 256, kTP = 384;
+  // S^T and P^T alternate between kSBuf places, with barriers of their own
+  auto s_at = [&](int half, uint32_t g) { return kSBuf == 2 ? (int)(g & 1) : half; };
+  auto s_phase = [&](uint32_t g) { return (kSBuf == 2 ? g >> 1 : g) & 1; };
 
   if (warp < 4) {
     setmaxnreg_dec<kRegCtl>();
@@ -299,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = S.begin(p, pv), ok = true;
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- producer
-      uint32_t nk = 0, nv = 0, nq = 0, nd = 0;       // tiles and half tiles loaded
+      uint32_t nk = 0, nv = 0, nq = 0, nd = 0;       // tiles and parts of tiles loaded
       for (; more && ok; more = S.next(p, pv)) {
         const int krow = S.U.start + S.U.u * kTile;
         if (S.first()) {
@@ -307,12 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_tile<D>(smem + L::kK, &tm_k, k_full, S.U.hk, krow);
           ++nk;
         }
-        for (int half = 0; half < 2 && ok; ++half) {
-          const int row = S.U.start + S.t * kTile + 64 * half;
-          const uint32_t gq = nq >> 1, gd = nd >> 1;
-          const int bq = half * 2 + (gq & 1), bd = half * 2 + (gd & 1);
-          if (gq >= 2 && !(ok = mbar_wait(&q_empty[bq], ((gq >> 1) - 1) & 1, status))) break;
-          load_tile<D, 64>(smem + L::kQ + L::half_at(half, gq), &tm_q, &q_full[bq], S.h, row);
+#pragma unroll 1
+        for (int half = 0; half < kHalves && ok; ++half) {
+          const int row = S.U.start + S.t * kTile + kRows * half;
+          const uint32_t g = nq / kHalves, b = half * kStages + g % kStages, ph = (g / kStages - 1) & 1;
+          if (g >= kStages && !(ok = mbar_wait(&q_empty[b], ph, status))) break;
+          load_tile<D, kRows>(smem + L::kQ + L::part_at(half, g), &tm_q, &q_full[b], S.h, row);
           ++nq;
           if (half == 0 && S.first()) {
             if (nv && !(ok = mbar_wait(v_empty, (nv - 1) & 1, status))) break;
@@ -320,18 +366,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++nv;
           }
           // dV has read the tile, and dP too: dK, which gave Q's stage back above, came after it
-          if (gd >= 2 && !(ok = mbar_wait(&do_empty[bd], ((gd >> 1) - 1) & 1, status))) break;
-          load_tile<D, 64>(smem + L::kDO + L::half_at(half, gd), &tm_do, &do_full[bd], S.h, row);
+          if (g >= kStages && !(ok = mbar_wait(&do_empty[b], ph, status))) break;
+          load_tile<D, kRows>(smem + L::kDO + L::part_at(half, g), &tm_do, &do_full[b], S.h, row);
           ++nd;
         }
       }
       // nothing may land after the CTA has left (open only when a wait ran out)
       if (nk) mbar_wait(k_full, (nk - 1) & 1, status);
       if (nv) mbar_wait(v_full, (nv - 1) & 1, status);
-      for (uint32_t x = nq > 4 ? nq - 4 : 0; x < nq; ++x)
-        mbar_wait(&q_full[(x & 1) * 2 + ((x >> 1) & 1)], (x >> 2) & 1, status);
-      for (uint32_t x = nd > 4 ? nd - 4 : 0; x < nd; ++x)
-        mbar_wait(&do_full[(x & 1) * 2 + ((x >> 1) & 1)], (x >> 2) & 1, status);
+      auto landed = [&](uint64_t* full, uint32_t n) {
+        for (uint32_t x = n > kHalves * kStages ? n - kHalves * kStages : 0; x < n; ++x)
+          mbar_wait(&full[x % kHalves * kStages + x / kHalves % kStages], (x / kHalves / kStages) & 1, status);
+      };
+      landed(q_full, nq);
+      landed(do_full, nd);
     } else if (warp == 1 || warp == 2) {
       // ---------------------------------------------------------- MMA issuers
       // warp 1: S^T and dV, warp 2: dP^T and dK; each half's next scores go out behind the product
@@ -346,51 +394,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t *b_full = kP ? q_full : do_full, *b2_empty = kP ? do_empty : q_empty;
         uint64_t *out = kP ? s_full : dp_full, *in = kP ? p_ready : ds_ready;
         auto scores = [&](int half, uint32_t g, int unit, bool first, bool last) {      // of step g, both operands K-major
-          const uint32_t b = half * 2 + (g & 1), b16 = base16 + (g & 1) * (L::kHalf / 16);
+          const uint32_t b = half * kStages + g % kStages, b16 = base16 + g % kStages * (L::kPartBytes / 16);
+          const uint32_t sum = tbase + kT + (kP && kSBuf == 2 ? 128 * (g & 1) : kRows * half);
           if (half == 0 && first && !(ok = warp_wait(a_full, unit & 1, status))) return;
-          if (!(ok = warp_wait(&b_full[b], (g >> 1) & 1, status))) return;
+          if (!(ok = warp_wait(&b_full[b], (g / kStages) & 1, status))) return;
           tc_fence_after();
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
             if (leader)
-              mma_bf16(tbase + kT + 64 * half, sdesc_at(base16, kA + (s / 4) * kTile * 128 + (s % 4) * 32, 16, 1024, kSwizzle128B),
-                       sdesc_at(b16, kB + half * 2 * L::kHalf + (s / 4) * 64 * 128 + (s % 4) * 32, 16, 1024, kSwizzle128B),
-                       idesc_bf16(128, 64, 0, 0), s > 0);
+              mma_bf16(sum, sdesc_at(base16, kA + (s / 4) * kTile * 128 + (s % 4) * 32, 16, 1024, kSwizzle128B),
+                       sdesc_at(b16, kB + half * kStages * L::kPartBytes + (s / 4) * kRows * 128 + (s % 4) * 32, 16, 1024, kSwizzle128B),
+                       idesc_bf16(128, kRows, 0, 0), s > 0);
+          if constexpr (kFold && (!kP || !CAP)) {        // less the query's LSE or D
+            const uint32_t row = L::kRow + half * kRows * 16, st = g % kStats;
+            if (half == 0 && !(ok = warp_wait(&st_full[st], (g / kStats) & 1, status))) return;
+            constexpr uint32_t pick = kP ? L::kPick : L::kPick + 2048;
+            if (leader) {
+              mma_bf16(sum, sdesc_at(base16, pick, L::kZero - pick, 128, kSwizzleNone),
+                       sdesc_at(base16 + st * 128, row, kStats * 2048, 128, kSwizzleNone), idesc_bf16(128, kRows, 0, 0), 1);
+              if (half == kHalves - 1) mma_commit(&st_empty[st]);
+            }
+          }
           if (leader) {
-            mma_commit(&out[half]);
-            if (half == 1 && last) mma_commit(a_empty);
+            mma_commit(&out[kP ? s_at(half, g) : half]);
+            if (half == kHalves - 1 && last) mma_commit(a_empty);
           }
         };
         auto product = [&](int half, uint32_t g, bool first) {      // A from TMEM, B over its rows
-          if (!(ok = warp_wait(&in[half], g & 1, status))) return;
+          if (!(ok = warp_wait(&in[kP ? s_at(half, g) : half], kP ? s_phase(g) : g & 1, status))) return;
           tc_fence_after();
-          const uint32_t b16 = base16 + (g & 1) * (L::kHalf / 16);
+          const uint32_t b16 = base16 + g % kStages * (L::kPartBytes / 16);
+          const uint32_t a = tbase + kT + (kP && kSBuf == 2 ? 128 * (g & 1) : kRows * half);
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
+          for (int s = 0; s < kRows / 16; ++s)
             if (leader)
-              mma_bf16_ta(tbase + kSum, tbase + kT + 64 * half + 32 * (s >> 1) + 8 * (s & 1),
-                          sdesc_at(b16, kB2 + half * 2 * L::kHalf + s * 2048, 64 * 128, 1024, kSwizzle128B),
+              mma_bf16_ta(tbase + kSum, a + 32 * (s >> 1) + 8 * (s & 1),
+                          sdesc_at(b16, kB2 + half * kStages * L::kPartBytes + s * 2048, kRows * 128, 1024, kSwizzle128B),
                           idesc_bf16(128, D, 0, 1), (!(first && half == 0) || s > 0));
-          if (leader) mma_commit(&b2_empty[half * 2 + (g & 1)]);
+          if (leader) mma_commit(&b2_empty[half * kStages + g % kStages]);
         };
         int steps = more ? S.group * S.U.nq : 0;      // of the unit
         if (steps) {
           scores(0, 0, 0, true, steps == 1);
-          if (ok) scores(1, 0, 0, true, steps == 1);
+          if (kHalves == 2 && ok) scores(1, 0, 0, true, steps == 1);
         }
         uint32_t g = 0;
         for (int unit = 0; steps && ok; ++unit) {
           ++S.n;
           const int next_steps = S.unit(p, pv) ? S.group * S.U.nq : 0;
-          // the unit's first product overwrites the sums of the last one: those have to be out
-          if (unit && !(ok = warp_wait(acc_free, (unit - 1) & 1, status))) break;
           for (int i = 0; i < steps && ok; ++i, ++g) {
             const bool last = i == steps - 1, next = !last || next_steps;
             const bool next_last = last ? next_steps == 1 : i + 2 == steps;
+            // with a second place for them the next scores need not wait for this P
+            const bool ahead = kP && kSBuf == 2 && !last;
+            if (ahead) scores(0, g + 1, unit, false, next_last);
+            // the unit's first product overwrites the sums of the last one: those have to be out
+            if (ok && i == 0 && unit) ok = warp_wait(acc_free, (unit - 1) & 1, status);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < kHalves; ++half) {
               if (ok) product(half, g, i == 0);
-              if (ok && next) scores(half, g + 1, unit + last, last, next_last);
+              if (ok && next && !ahead) scores(half, g + 1, unit + last, last, next_last);
             }
             if (ok && last && leader) mma_commit(acc_full);
           }
@@ -405,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 3) {
       // ---------------------------------------------------------- LSE and D of a step's queries
-      float* stat = reinterpret_cast<float*>(smem + L::kStat);
+      // as rows of eight bf16: minus LSE in three parts, minus D in three, 0, 0
+      const float to_products = -kLog2e / p.scale2;
       for (uint32_t g = 0; more && ok; more = S.next(p, pv), ++g) {
         const int b = g % kStats;
         float l[4], d[4];
@@ -419,26 +483,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (g >= kStats && !(ok = warp_wait(&st_empty[b], (g / kStats - 1) & 1, status))) break;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          stat[b * 256 + 32 * e + lane] = -l[e] * kLog2e;
-          stat[b * 256 + 128 + 32 * e + lane] = d[e];
+          float* stat = reinterpret_cast<float*>(smem + L::kLse) + b * L::kStat + 32 * e + lane;
+          if (kReadStat) stat[0] = -l[e] * kLog2e;
+          if constexpr (!kFold) {
+            stat[128] = d[e];
+            continue;
+          }
+          uint32_t x[3] = {0, 0, 0}, y[3];
+          if (!CAP) split3(l[e] * to_products, x);
+          split3(-d[e], y);
+          *reinterpret_cast<uint4*>(smem + L::kRow + b * 2048 + (32 * e + lane) * 16) =
+              make_uint4(x[0] | x[1] << 16, x[2] | y[0] << 16, y[1] | y[2] << 16, 0);
         }
-        mbar_arrive(&st_full[b]);
+        if (kFold) fence_proxy_async_smem();
+        warp_arrive(&st_full[b]);
       }
     }
   } else {
     // ------------------------------------------------------------ compute
     setmaxnreg_inc<kRegCompute>();
-    const int w = (warp - 4) >> 2, quarter = warp & 3, half = w >> 1;
+    const int w = (warp - 4) >> 2, quarter = warp & 3, half = kHalves == 2 ? w >> 1 : 0;
     const int r = quarter * 32 + lane, tid = threadIdx.x - 128;
     const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t s_addr = lane_base + kTS + 32 * w, dp_addr = lane_base + kTP + 32 * w;
+    const uint32_t dp_addr = lane_base + kTP + 32 * w;
     float* tab = reinterpret_cast<float*>(smem + L::kBias);
     float* acc = reinterpret_cast<float*>(smem + L::kAcc);
     const int R = bias_range(p);
     const int near = near_tiles(R);
     const float scale2 = p.scale2, inv_scale2 = 1.f / p.scale2;
     HeadBias HB{};
-    int staged = -1, buf = 0;
+    int staged = -1;
     float far_lo = 0.f, far_hi = 0.f, lost_lo = 0.f, lost_hi = 0.f;
     bool ok = true;
     KeySteps S{};
@@ -473,9 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = U.tlo; t < U.tlo + U.nq; ++t, ++g) {
       float du_lo = 0.f;      // (BIAS 2) sum of the thread's dU of a far tile
       uint32_t v[32];
-      const float* nl = reinterpret_cast<const float*>(smem + L::kStat) + (g % kStats) * 256 + 32 * w;
-      ok = ok && mbar_wait(&st_full[g % kStats], (g / kStats) & 1, status);
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[half], g & 1, status));
+      const float* nl = reinterpret_cast<const float*>(smem + L::kLse) + (g % kStats) * L::kStat + 32 * w;
+      if (kReadStat) ok = ok && mbar_wait(&st_full[g % kStats], (g / kStats) & 1, status);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[s_at(half, g)], s_phase(g), status));
+      const uint32_t s_addr = lane_base + kTS + (kSBuf == 2 ? 128 * (g & 1) : 0) + 32 * w;
       if (ok) {
         tc_fence_after();
         tmem_ld32(s_addr, v);
@@ -500,14 +575,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 f2 = make_float2(f, f), c2 = make_float2(B.c, B.c);
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
-          const float4 n4 = *reinterpret_cast<const float4*>(nl + j);
-          float2 e0 = make_float2(n4.x, n4.y), e1 = make_float2(n4.z, n4.w);
-          if constexpr (BIAS != 0) {
-            e0 = fadd2(e0, c2);
-            e1 = fadd2(e1, c2);
+          float2 e0 = pair_of(v, j), e1 = pair_of(v, j + 2);
+          if constexpr (kReadStat) {
+            const float4 n4 = *reinterpret_cast<const float4*>(nl + j);
+            float2 n0 = make_float2(n4.x, n4.y), n1 = make_float2(n4.z, n4.w);
+            if constexpr (BIAS != 0) {
+              n0 = fadd2(n0, c2);
+              n1 = fadd2(n1, c2);
+            }
+            e0 = ffma2(e0, f2, n0);
+            e1 = ffma2(e1, f2, n1);
+          } else if constexpr (BIAS != 0) {
+            e0 = ffma2(e0, f2, c2);
+            e1 = ffma2(e1, f2, c2);
+          } else {
+            e0 = fmul2(e0, f2);
+            e1 = fmul2(e1, f2);
           }
-          e0 = ffma2(pair_of(v, j), f2, e0);
-          e1 = ffma2(pair_of(v, j + 2), f2, e1);
           e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
           e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
           pk[j / 2] = pack2(e0);
@@ -521,16 +605,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st16(s_addr, pk);
         tmem_st_wait();
-        if (t * kTile + 64 * half + 64 > U.len) {
+        if (t * kTile + kRows * half + kRows > U.len) {
           // queries behind the document: the products below sum over them
-          ok = __all_sync(0xffffffffu, mbar_wait(&do_full[half * 2 + (g & 1)], (g >> 1) & 1, status));
-          if (ok && r < 64 && t * kTile + 64 * half + r >= U.len)
-            clear_row<D, 64>(smem + (w & 1 ? L::kQ : L::kDO) + L::half_at(half, g), r);
+          ok = __all_sync(0xffffffffu, mbar_wait(&do_full[half * kStages + g % kStages], (g / kStages) & 1, status));
+          const int which = w % (4 / kHalves);
+          if (ok && which < 2 && r < kRows && t * kTile + kRows * half + r >= U.len)
+            clear_row<D, kRows>(smem + (which ? L::kQ : L::kDO) + L::part_at(half, g), r);
           fence_proxy_async_smem();
         }
         if (ok) {
           tc_fence_before();
-          mbar_arrive(&p_ready[half]);
+          warp_arrive(&p_ready[s_at(half, g)]);
           ok = __all_sync(0xffffffffu, mbar_wait(&dp_full[half], g & 1, status));
         }
         if (ok) {
@@ -542,9 +627,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (edge) drop_hidden(dp, v);
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 d4 = *reinterpret_cast<const float4*>(nl + 128 + j);
-            float2 a0 = fmul2(pair_of(v, j), fadd2(pair_of(dp, j), make_float2(-d4.x, -d4.y)));
-            float2 a1 = fmul2(pair_of(v, j + 2), fadd2(pair_of(dp, j + 2), make_float2(-d4.z, -d4.w)));
+            float2 a0 = pair_of(dp, j), a1 = pair_of(dp, j + 2);
+            if constexpr (!kFold) {
+              const float4 d4 = *reinterpret_cast<const float4*>(nl + 128 + j);
+              a0 = fadd2(a0, make_float2(-d4.x, -d4.y));
+              a1 = fadd2(a1, make_float2(-d4.z, -d4.w));
+            }
+            a0 = fmul2(pair_of(v, j), a0);
+            a1 = fmul2(pair_of(v, j + 2), a1);
             if constexpr (BIAS == 2) {
               put_pair(v, j, a0);
               put_pair(v, j + 2, a1);
@@ -561,8 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16(dp_addr, pk);
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(&ds_ready[half]);
-          mbar_arrive(&st_empty[g % kStats]);
+          warp_arrive(&ds_ready[half]);
+          if (kReadStat && lane == 0) mbar_arrive(&st_empty[g % kStats]);
         }
       }
       if constexpr (BIAS == 2) {
@@ -574,7 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // sums along the diagonals: a running value moves one lane up per column, so it stays on its
           // diagonal; lane 31's is complete
-          float* dg = reinterpret_cast<float*>(smem + L::kDiag) + buf * (16 * 64);
+          float* dg = reinterpret_cast<float*>(smem + L::kDiag);
+          named_bar_sync(1, kCompute);           // the last tile's are read
           float* mine = dg + (warp - 4) * 64;
           float run = 0.f;
 #pragma unroll
@@ -599,13 +690,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             else if (rel >= R) add_comp(far_hi, lost_hi, s);
             else acc[rel + R] += s;
           }
-          buf ^= 1;
         }
       }
       }
       if constexpr (BIAS == 2) {
         // the head's sums of this key tile: the two ends over all threads in a fixed order
-        float* red = reinterpret_cast<float*>(smem + L::kDiag) + buf * (16 * 64);
+        float* red = reinterpret_cast<float*>(smem + L::kDiag);
+        named_bar_sync(1, kCompute);
         far_lo += lost_lo;
         far_hi += lost_hi;
 #pragma unroll
@@ -628,7 +719,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[i] = s;
         }
         named_bar_sync(1, kCompute);
-        buf ^= 1;
       }
      }
      if (ok) {
@@ -735,22 +825,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     scored_dq_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const ScoredParams p) {
   using L = DqSmem<D>;
-  constexpr int kStages = L::kStages;
+  constexpr int kStages = L::kStages, kPBuf = D == 64 ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t *k_full = bars, *k_empty = bars + kStages, *v_full = bars + 2 * kStages, *v_empty = bars + 3 * kStages;
-  uint64_t *s_full = bars + 4 * kStages, *dp_full = s_full + 1, *acc_full = s_full + 2, *drain = s_full + 3;
-  uint64_t *s_free = s_full + 4, *ds_ready = s_full + 5, *q_ready = s_full + 6;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 7);
+  uint64_t *s_full = bars + 4 * kStages, *acc_full = s_full + 1, *drain = s_full + 2, *dp_full = s_full + 3;   // dp_full [2]
+  uint64_t *s_free = s_full + 5, *q_ready = s_full + 6, *ds_ready = s_full + 7;                                // ds_ready [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 9);
   int* status = const_cast<int*>(p.plan) + kPlanStatus;
   const PlanView pv = plan_view(p.plan, p.T, p.N);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4 * kStages + 4; ++i) mbar_init(bars + i, 1);
-    mbar_init(s_free, kCompute);
-    mbar_init(ds_ready, kCompute);
+    for (int i = 0; i < 4 * kStages + 5; ++i) mbar_init(bars + i, 1);
+    mbar_init(s_free, kCompute / 32);
+    mbar_init(ds_ready, kCompute / 32);
+    mbar_init(ds_ready + 1, kCompute / 32);
     mbar_init(q_ready, kCompute);
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
@@ -764,7 +855,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  constexpr uint32_t kTQ = 0, kTS = 128, kTP = 256, kTA = 384, kTB = 448;
+  constexpr uint32_t kTQ = 0, kTS = 128, kTP = 256, kTA = D == 64 ? 64 : 384, kTB = D == 64 ? 96 : 448;
+  // dP and dS alternate between kPBuf places, with barriers of their own
+  auto p_at = [&](uint32_t g) { return kPBuf == 2 ? g & 1 : 0; };
+  auto p_phase = [&](uint32_t g) { return (kPBuf == 2 ? g >> 1 : g) & 1; };
 
   if (warp < 4) {
     setmaxnreg_dec<kRegCtl>();
@@ -810,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b = g % kStages;
         if (!(ok = warp_wait(&v_full[b], (g / kStages) & 1, status))) return;
         tc_fence_after();
-        scores(kTB, L::kV + b * L::kTileBytes, kTP, dp_full);
+        scores(kTB, L::kV + b * L::kTileBytes, kTP + 128 * p_at(g), &dp_full[p_at(g)]);
         if (leader) mma_commit(&v_empty[b]);
       };
       uint32_t units = 0;
@@ -828,21 +922,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = warp_wait(s_free, g & 1, status))) break;
           tc_fence_after();
           issue_s(g + 1);
+          if (ok && kPBuf == 2) issue_dp(g + 1);
           if (!ok) break;
         }
-        if (!(ok = warp_wait(ds_ready, g & 1, status))) break;
+        if (!(ok = warp_wait(&ds_ready[p_at(g)], p_phase(g), status))) break;
         tc_fence_after();
 #pragma unroll
         for (int s = 0; s < kTile / 16; ++s)
           if (leader)
-            mma_bf16_ta(tbase + kTQ, tbase + kTP + 32 * (s >> 1) + 8 * (s & 1),
+            mma_bf16_ta(tbase + kTQ, tbase + kTP + 128 * p_at(g) + 32 * (s >> 1) + 8 * (s & 1),
                         sdesc_at(base16, L::kK + b * L::kTileBytes + s * 2048, kTile * 128, 1024, kSwizzle128B),
                         idesc_bf16(128, D, 0, 1), (!first || s > 0));
         if (leader) {
           mma_commit(&k_empty[b]);
           if (last) mma_commit(acc_full);
         }
-        if (!last) issue_dp(g + 1);
+        if (!last && kPBuf == 1) issue_dp(g + 1);
         more = S.next(p, pv);
       }
       if (leader) {
@@ -856,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane, tid = threadIdx.x - 128;
     const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t s_addr = lane_base + kTS + 32 * w, dp_addr = lane_base + kTP + 32 * w;
+    const uint32_t s_addr = lane_base + kTS + 32 * w, dp_base = lane_base + kTP + 32 * w;
     float* tab = reinterpret_cast<float*>(smem + L::kBias);
     const int R = bias_range(p);
     const int near = near_tiles(R);
@@ -917,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(s_addr, v);
         tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(s_free);
+        warp_arrive(s_free);
         TileBias B{};
         if constexpr (BIAS) B = tile_bias(tab, HB, R, near, inv_scale2, t, u, u * kTile + 32 * w - qi);
         const float f = BIAS ? B.factor(scale2) : scale2;
@@ -940,12 +1035,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (CAP) e = fmul2(e, pair_of(gr, j));
           put_pair(v, j, e);
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(dp_full, g & 1, status));
+        ok = __all_sync(0xffffffffu, mbar_wait(&dp_full[p_at(g)], p_phase(g), status));
         if (ok) {
           tc_fence_after();
           const float2 d2 = make_float2(-dv, -dv);
           uint32_t pk[16];
           uint32_t dp[32];
+          const uint32_t dp_addr = dp_base + 128 * p_at(g);
           tmem_ld32(dp_addr, dp);
           tmem_ld_wait();
           if ((u + 1) * kTile > S.len) drop_hidden(dp, v);
@@ -962,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
           }
           tc_fence_before();
-          mbar_arrive(ds_ready);
+          warp_arrive(&ds_ready[p_at(g)]);
         }
       }
       const bool last = S.last();
@@ -1039,15 +1135,15 @@ __global__ void __launch_bounds__(256) scored_heads_kernel(const ScoredParams p)
 template <int D, bool CAP, int BIAS>
 cudaError_t launch(const ScoredParams& p, cudaStream_t stream) {
   CUtensorMap tq, tk, tv, tdo;
-  if (!make_tmap_bf16_3d(&tq, p.q, D, p.hq, p.T, D * 2, (uint64_t)p.hq * D * 2, 64, kTile / 2) ||
+  if (!make_tmap_bf16_3d(&tq, p.q, D, p.hq, p.T, D * 2, (uint64_t)p.hq * D * 2, 64, DkvSmem<D, BIAS>::kRows) ||
       !make_tmap_bf16_3d(&tk, p.k, D, p.hkv, p.T, D * 2, (uint64_t)p.hkv * D * 2, 64, kTile) ||
       !make_tmap_bf16_3d(&tv, p.v, D, p.hkv, p.T, D * 2, (uint64_t)p.hkv * D * 2, 64, kTile) ||
-      !make_tmap_bf16_3d(&tdo, p.dout, D, p.hq, p.T, D * 2, (uint64_t)p.hq * D * 2, 64, kTile / 2))
+      !make_tmap_bf16_3d(&tdo, p.dout, D, p.hq, p.T, D * 2, (uint64_t)p.hq * D * 2, 64, DkvSmem<D, BIAS>::kRows))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0, regs1 = 0, regs2 = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  constexpr int smem1 = DkvSmem<D>::kAlloc, smem2 = DqSmem<D>::kAlloc;
+  constexpr int smem1 = DkvSmem<D, BIAS>::kAlloc, smem2 = DqSmem<D>::kAlloc;
   static_assert(smem1 <= 232448 && smem2 <= 232448, "shared memory of one CTA");
   if (e == cudaSuccess) e = prepare_kernel<scored_dkv_kernel<D, CAP, BIAS>>(smem1, &regs1);
   if (e == cudaSuccess) e = prepare_kernel<scored_dq_kernel<D, CAP, BIAS != 0>>(smem2, &regs2);
