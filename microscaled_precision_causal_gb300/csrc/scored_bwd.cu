@@ -825,24 +825,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     scored_dq_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const ScoredParams p) {
   using L = DqSmem<D>;
-  constexpr int kStages = L::kStages, kPBuf = D == 64 ? 2 : 1;
+  constexpr int kStages = L::kStages, kPBuf = D == 64 ? 2 : 1, kHalves = D == 64 || CAP ? 1 : 2, kCols = kTile / kHalves;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t *k_full = bars, *k_empty = bars + kStages, *v_full = bars + 2 * kStages, *v_empty = bars + 3 * kStages;
-  uint64_t *s_full = bars + 4 * kStages, *acc_full = s_full + 1, *drain = s_full + 2, *dp_full = s_full + 3;   // dp_full [2]
-  uint64_t *s_free = s_full + 5, *q_ready = s_full + 6, *ds_ready = s_full + 7;                                // ds_ready [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 9);
+  uint64_t *s_full = bars + 4 * kStages, *dp_full = s_full + 2, *s_free = s_full + 4, *ds_ready = s_full + 6;   // [halves or places]
+  uint64_t *acc_full = s_full + 8, *acc_free = s_full + 9, *q_ready = s_full + 10, *drain = s_full + 11;        // drain [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 13);
   int* status = const_cast<int*>(p.plan) + kPlanStatus;
   const PlanView pv = plan_view(p.plan, p.T, p.N);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4 * kStages + 5; ++i) mbar_init(bars + i, 1);
-    mbar_init(s_free, kCompute / 32);
-    mbar_init(ds_ready, kCompute / 32);
-    mbar_init(ds_ready + 1, kCompute / 32);
+    for (int i = 0; i < 4 * kStages + 4; ++i) mbar_init(bars + i, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(s_free + i, kCompute / 32 / kHalves);
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, kCompute / 32);
     mbar_init(q_ready, kCompute);
+    mbar_init(drain, 1);
+    mbar_init(drain + 1, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -857,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tbase = *tmem_slot;
   constexpr uint32_t kTQ = 0, kTS = 128, kTP = 256, kTA = D == 64 ? 64 : 384, kTB = D == 64 ? 96 : 448;
   // dP and dS alternate between kPBuf places, with barriers of their own
-  auto p_at = [&](uint32_t g) { return kPBuf == 2 ? g & 1 : 0; };
+  auto p_at = [&](int half, uint32_t g) { return kPBuf == 2 ? (int)(g & 1) : half; };
   auto p_phase = [&](uint32_t g) { return (kPBuf == 2 ? g >> 1 : g) & 1; };
 
   if (warp < 4) {
@@ -881,74 +883,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&k_full[x % kStages], (x / kStages) & 1, status);
       for (uint32_t x = nv > kStages ? nv - kStages : 0; x < nv; ++x)
         mbar_wait(&v_full[x % kStages], (x / kStages) & 1, status);
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issuer
+    } else if (warp == 1 || warp == 2) {
+      // ---------------------------------------------------------- MMA issuers
+      // warp 1: S, warp 2: dP and dQ
       const bool leader = elect_one();
       const uint32_t base16 = (smem_u32(smem) & 0x3FFFFu) >> 4;
-      auto scores = [&](uint32_t a, uint32_t b_off, uint32_t d, uint64_t* bar) {
+      auto scores = [&](uint32_t a, uint32_t b_off, uint32_t d, int half) {
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
           if (leader)
             mma_bf16_ta(tbase + d, tbase + a + 8 * s,
-                        sdesc_at(base16, b_off + (s / 4) * kTile * 128 + (s % 4) * 32, 16, 1024, kSwizzle128B),
-                        idesc_bf16(128, 128, 0, 0), s > 0);
-        if (leader) mma_commit(bar);
+                        sdesc_at(base16, b_off + (s / 4) * kTile * 128 + half * kCols * 128 + (s % 4) * 32, 16, 1024, kSwizzle128B),
+                        idesc_bf16(128, kCols, 0, 0), s > 0);
       };
-      auto issue_s = [&](uint32_t g) {
+      auto issue_s = [&](uint32_t g, int half) {
         const uint32_t b = g % kStages;
-        if (!(ok = warp_wait(&k_full[b], (g / kStages) & 1, status))) return;
+        if (half == 0 && !(ok = warp_wait(&k_full[b], (g / kStages) & 1, status))) return;
         tc_fence_after();
-        scores(kTA, L::kK + b * L::kTileBytes, kTS, s_full);
+        scores(kTA, L::kK + b * L::kTileBytes, kTS + kCols * half, half);
+        if (leader) mma_commit(&s_full[half]);
       };
-      auto issue_dp = [&](uint32_t g) {
+      auto issue_dp = [&](uint32_t g, int half) {
         const uint32_t b = g % kStages;
-        if (!(ok = warp_wait(&v_full[b], (g / kStages) & 1, status))) return;
+        if (half == 0 && !(ok = warp_wait(&v_full[b], (g / kStages) & 1, status))) return;
         tc_fence_after();
-        scores(kTB, L::kV + b * L::kTileBytes, kTP + 128 * p_at(g), &dp_full[p_at(g)]);
-        if (leader) mma_commit(&v_empty[b]);
+        scores(kTB, L::kV + b * L::kTileBytes, kTP + (kPBuf == 2 ? 128 * (g & 1) : kCols * half), half);
+        if (leader) {
+          mma_commit(&dp_full[p_at(half, g)]);
+          if (half == kHalves - 1) mma_commit(&v_empty[b]);
+        }
       };
       uint32_t units = 0;
       for (uint32_t g = 0; more && ok; ++g) {
         const bool first = S.first(), last = S.last();
-        const uint32_t b = g % kStages;
         if (first) {
           if (!(ok = warp_wait(q_ready, units++ & 1, status))) break;
           tc_fence_after();
-          issue_s(g);
-          if (ok) issue_dp(g);
-          if (!ok) break;
-        }
-        if (!last) {
-          if (!(ok = warp_wait(s_free, g & 1, status))) break;
-          tc_fence_after();
-          issue_s(g + 1);
-          if (ok && kPBuf == 2) issue_dp(g + 1);
-          if (!ok) break;
-        }
-        if (!(ok = warp_wait(&ds_ready[p_at(g)], p_phase(g), status))) break;
-        tc_fence_after();
 #pragma unroll
-        for (int s = 0; s < kTile / 16; ++s)
-          if (leader)
-            mma_bf16_ta(tbase + kTQ, tbase + kTP + 128 * p_at(g) + 32 * (s >> 1) + 8 * (s & 1),
-                        sdesc_at(base16, L::kK + b * L::kTileBytes + s * 2048, kTile * 128, 1024, kSwizzle128B),
-                        idesc_bf16(128, D, 0, 1), (!first || s > 0));
-        if (leader) {
-          mma_commit(&k_empty[b]);
-          if (last) mma_commit(acc_full);
+          for (int half = 0; half < kHalves; ++half) {
+            if (!ok) continue;
+            if (warp == 1) issue_s(g, half);
+            else issue_dp(g, half);
+          }
         }
-        if (!last && kPBuf == 1) issue_dp(g + 1);
+        if (warp == 1) {
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half)
+            if (ok && !last && (ok = warp_wait(&s_free[half], g & 1, status))) issue_s(g + 1, half);
+        } else {
+          const uint32_t b = g % kStages;
+          if (ok && kPBuf == 2 && !last) issue_dp(g + 1, 0);
+          // the unit's first product overwrites the sums of the last one: those have to be out
+          if (ok && first && units > 1) ok = warp_wait(acc_free, units & 1, status);
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half) {
+            if (!ok || !(ok = warp_wait(&ds_ready[p_at(half, g)], p_phase(g), status))) continue;
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < kCols / 16; ++s)
+              if (leader)
+                mma_bf16_ta(tbase + kTQ, tbase + kTP + (kPBuf == 2 ? 128 * (g & 1) : kCols * half) + 32 * (s >> 1) + 8 * (s & 1),
+                            sdesc_at(base16, L::kK + b * L::kTileBytes + half * kCols * 128 + s * 2048, kTile * 128, 1024, kSwizzle128B),
+                            idesc_bf16(128, D, 0, 1), (!(first && half == 0) || s > 0));
+            if (leader && half == kHalves - 1) {
+              mma_commit(&k_empty[b]);
+              if (last) mma_commit(acc_full);
+            }
+            if (!last && kPBuf == 1) issue_dp(g + 1, half);
+          }
+        }
         more = S.next(p, pv);
       }
       if (leader) {
-        mma_commit(drain);
-        mbar_wait(drain, 0, status);
+        mma_commit(&drain[warp - 1]);
+        mbar_wait(&drain[warp - 1], 0, status);
       }
     }
   } else {
     // ------------------------------------------------------------ compute
     setmaxnreg_inc<kRegCompute>();
-    const int w = (warp - 4) >> 2, quarter = warp & 3;
+    const int w = (warp - 4) >> 2, quarter = warp & 3, half = kHalves == 2 ? w >> 1 : 0;
     const int r = quarter * 32 + lane, tid = threadIdx.x - 128;
     const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_addr = lane_base + kTS + 32 * w, dp_base = lane_base + kTP + 32 * w;
@@ -1005,14 +1019,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const int t = S.t, u = S.tile(), qi = t * kTile + r;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, g & 1, status));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&s_full[half], g & 1, status));
       if (ok) {
         tc_fence_after();
         uint32_t v[32], gr[32];
         tmem_ld32(s_addr, v);
         tmem_ld_wait();
         tc_fence_before();
-        warp_arrive(s_free);
+        warp_arrive(&s_free[half]);
         TileBias B{};
         if constexpr (BIAS) B = tile_bias(tab, HB, R, near, inv_scale2, t, u, u * kTile + 32 * w - qi);
         const float f = BIAS ? B.factor(scale2) : scale2;
@@ -1035,13 +1049,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (CAP) e = fmul2(e, pair_of(gr, j));
           put_pair(v, j, e);
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(&dp_full[p_at(g)], p_phase(g), status));
+        ok = __all_sync(0xffffffffu, mbar_wait(&dp_full[p_at(half, g)], p_phase(g), status));
         if (ok) {
           tc_fence_after();
           const float2 d2 = make_float2(-dv, -dv);
           uint32_t pk[16];
           uint32_t dp[32];
-          const uint32_t dp_addr = dp_base + 128 * p_at(g);
+          const uint32_t dp_addr = dp_base + (kPBuf == 2 ? 128 * (g & 1) : 0);
           tmem_ld32(dp_addr, dp);
           tmem_ld_wait();
           if ((u + 1) * kTile > S.len) drop_hidden(dp, v);
@@ -1054,11 +1068,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16(dp_addr, pk);
           tmem_st_wait();
           if ((u + 1) * kTile > S.len) {       // keys behind the document: dQ sums over them
-            if (w == 0 && u * kTile + r >= S.len) clear_row<D>(smem + L::kK + (g % kStages) * L::kTileBytes, r);
+            if (w % (4 / kHalves) == 0 && r / kCols == half && u * kTile + r >= S.len) clear_row<D>(smem + L::kK + (g % kStages) * L::kTileBytes, r);
             fence_proxy_async_smem();
           }
           tc_fence_before();
-          warp_arrive(&ds_ready[p_at(g)]);
+          warp_arrive(&ds_ready[p_at(half, g)]);
         }
       }
       const bool last = S.last();
@@ -1067,14 +1081,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = qi < S.len;
       more = S.next(p, pv);
       if (last && ok) {
-        // every product that reads Q and dO of this unit has been waited for: the next unit's go in
-        // while its last dQ product runs
-        if (more) start_unit();
-        ok = __all_sync(0xffffffffu, mbar_wait(acc_full, units++ & 1, status));
+        // when every product that reads Q and dO of this unit is done, the next unit's go in, while its
+        // last dQ product runs
+        if (kHalves == 2)
+          ok = __all_sync(0xffffffffu, mbar_wait(w < 2 ? &s_full[1] : &dp_full[0], g & 1, status));
+        if (ok && more) start_unit();
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(acc_full, units & 1, status));
+        ++units;
         if (ok) {
           tc_fence_after();
           if (w < D / 32) store_acc<32>(lane_base + kTQ + 32 * w, p.dq + (tok * p.hq + h) * D + 32 * w, p.scale, valid);
           tc_fence_before();
+          warp_arrive(acc_free);
         }
       }
     }
