@@ -3,13 +3,13 @@
 //   P = 2^(u log2 e - LSE log2 e), dU = P o (dO V^T - D), dS = dU o (1 - tanh^2),
 //   dV = P^T dO, dK = scale dS^T Q, dQ = scale dS K, drel[h][r] = sum of dU at distance r.
 //
-// Three launches: D = rowsum(dO o O) (memory-bound), then dK and dV per key tile, then dQ
-// per query tile.  P and dS are computed in both of the latter: 7 tile products a pair of
-// tiles instead of the 5 of a single pass.  A single pass has to add its dQ partials into
-// memory from every key tile: an fp32 tile (64 KB) per step through shared memory and L2,
-// in an order that changes from run to run, and needs dS^T once more as a shared-memory
-// operand.  Here dS and P are A operands straight from tensor memory, nothing is written to
-// shared memory in the loops, and the results are the same bits every time.
+// D = rowsum(dO o O) (memory-bound), then dK and dV per key tile (with few units per query
+// head, whose parts are then added), then dQ per query tile, then drel.  P and dS are
+// computed for dK and dV and again for dQ: 7 tile products a pair of tiles instead of the 5
+// of a single pass.  A single pass has to add its dQ partials into memory from every key
+// tile: an fp32 tile (64 KB) per step through shared memory and L2, in an order that changes
+// from run to run, and needs dS^T once more as a shared-memory operand.  Here dS and P are A
+// operands straight from tensor memory, and the results are the same bits every time.
 //
 // P and dS enter their products in bf16 (their partners are bf16): half a step of 2^-8 per
 // element, as the rounding of the gradients themselves; sums stay in fp32.
@@ -29,12 +29,6 @@ constexpr int kThreads = 128 + kCompute;
 constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
 constexpr int kRegCtl = 64, kRegCompute = 104;
 static_assert(kRegCtl * 128 + kRegCompute * kCompute <= kLaunchRegs * kThreads, "register split");
-#ifndef F128
-#define F128 0
-#define F128G 1
-#define H128 2
-#define H128G 1
-#endif
 
 // One arrival for a warp, behind what all its lanes did.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -160,39 +154,55 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, u
 }
 
 // ================================================================ dK, dV
-// One CTA per SM walks (key tile, kv head) units; a step is a query tile of one of the kv
-// head's query heads.  S^T = K Q^T and dP^T = V dO^T have keys in the TMEM lanes, so P^T and
-// dS^T are written back over their own columns and are the A operands of dV += P^T dO and
-// dK += dS^T Q.
-// A step's 128 queries go in two halves, each with its own 64-query operand tiles, products
-// and compute warps, half a step apart: while one half's P^T is computed the other's dS^T is,
-// so that the waits, loads and stores of the one hide behind the arithmetic of the other.  (As
-// one tile all warps were in the same phase and the kernel ran at its latencies: XXX.)  The
-// price is that a product with 64 columns reads more shared memory than it multiplies: 48
-// cycles instead of 32 for S^T and dP^T a step of 16.  K is free for the next unit once the
-// unit's last S^T is done, V once its last dP^T is.
-// Roles: warp 0 TMA, warp 1 MMA, warp 2 TMEM, warp 3 stages LSE and D of a step's queries,
-// warps 4-19 compute: thread = key row, warpgroup = 32 of the 128 query columns, two a half.
-// TMEM columns: dV [0, D), dK [128, 128 + D), S^T [256, 384), dP^T [384, 512).
+// One CTA per SM walks (key tile, kv head) units (or query head: scored_bwd_split); a step is a
+// query tile of one of the unit's query heads.  S^T = K Q^T and dP^T = V dO^T have keys in the
+// TMEM lanes, so P^T and dS^T are written back over their own columns and are the A operands
+// of dV += P^T dO and dK += dS^T Q.  A warp issues the chain of S^T and dV, another that of
+// dP^T and dK, so that neither waits for the other's operands.  K is free for the next unit
+// once the unit's last S^T is done, V once its last dP^T is.
+//
+// LSE and D vary along a thread's columns, so every warp would read both of every query from
+// shared memory: 4 quarters of keys x 128 queries x 2, at the one value a cycle that a broadcast
+// delivers, beside what the products read there.  The two together kept that path 99% busy at
+// D = 64.  (kFold) They go through the products instead: a last step of 16 multiplies rows of
+// eight bf16 per query (-LSE / scale2 in three parts, which hold all of its 24 bits, -D in three)
+// with ones, and the accumulators come out as S^T - LSE / scale2 and dP^T - D.  With a cap LSE
+// comes after the cap, and stays in shared memory.
+//
+// D = 64 leaves room for a second S^T (kSBuf): the next one runs while this P^T is computed.
+// Two noncausal documents of 8192, 16 heads, buckets, all three launches: 2.70 ms with halves as
+// below, 2.39 folded and whole, 2.22 with the second S^T.
+//
+// At D = 128 tensor memory is full, and a step's queries go in two halves, each with its own
+// 64-query tiles, products and warps, half a step apart: while one half's P^T is computed the
+// other's dS^T is.  (Whole, folded or not, all warps wait for the same product: 6.1 instead of 5.8
+// ms on four documents of 8192, 32 heads on 8, slopes.)  A product with 64 columns reads more
+// shared memory than it multiplies (48 cycles instead of 32 a step of 16), and the fold would
+// cost two more of them for nothing (6.0 ms).  Where drel is wanted the warps meet at barriers on
+// every tile near the diagonal anyway: whole and folded, 0.657 instead of 0.700 ms (packed
+// documents, 16384 rows, 16 heads).
+// Roles: warp 0 TMA, warps 1 and 2 MMA (2 also TMEM), warp 3 stages LSE and D of a step's queries,
+// warps 4-19 compute: thread = key row, warpgroup = 32 of the 128 query columns.
+// TMEM columns: dV [0, D), dK [D, 2 D), S^T [256, 384) (D = 64: [128, 384)), dP^T [384, 512).
 template <int D, int BIAS>
 struct DkvSmem {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kK = 0, kV = kTileBytes;
-  static constexpr int kHalves = D == 64 ? 1 : BIAS == 2 ? H128G : H128;
-  static constexpr bool kFold = D == 64 || (BIAS == 2 ? F128G : F128);
+  static constexpr int kHalves = D == 128 && BIAS != 2 ? 2 : 1;
+  static constexpr bool kFold = kHalves == 1;
   static constexpr int kStats = kFold ? 2 : 4;                 // steps whose LSE and D are staged
   static constexpr int kRows = kTile / kHalves;
   static constexpr int kStages = D == 128 ? 2 : 3;
-  static constexpr int kSBuf = D == 128 || kHalves == 2 ? 1 : 2;
+  static constexpr int kSBuf = D == 64 ? 2 : 1;                // places of S^T
   static constexpr int kPartBytes = kTileBytes / kHalves;
   static constexpr int kQ = 2 * kTileBytes;                    // [halves][stages]
   static constexpr int kDO = kQ + kStages * kTileBytes;        // [halves][stages]
   static __device__ __forceinline__ int part_at(int half, uint32_t g) { return (half * kStages + (int)(g % kStages)) * kPartBytes; }
-  // folded: [kStats][2 halves][64 queries][8], their LSE and D
+  // (kFold) [kStats][128 queries][8]: their LSE and D
   static constexpr int kRow = kDO + kStages * kTileBytes;
   static constexpr int kPick = kRow + (kFold ? kStats * 2048 : 0);   // [128 keys][8]: 1 where LSE is, then the same for D
   static constexpr int kZero = kPick + (kFold ? 4096 : 0);
-  static constexpr int kLse = kZero + (kFold ? 2048 : 0);      // not folded: [kStats][128] -LSE log2 e, 128 D]
+  static constexpr int kLse = kZero + (kFold ? 2048 : 0);      // [kStats][128 -LSE log2 e, (not kFold) 128 D]
   static constexpr int kStat = kFold ? 128 : 256;
   static constexpr int kBias = kLse + kStats * kStat * 4;            // [kBiasTab]
   static constexpr int kAcc = kBias + kBiasTab * 4;      // [2 R + 1] drel of the current head
@@ -754,9 +764,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dP = dO V^T have queries in the TMEM lanes; Q and dO are A operands from tensor memory,
 // copied there once a unit, which leaves shared memory to three K and three V tiles and
 // halves what these products read from it.  dS goes over dP's columns and is the A operand
-// of dQ += dS K.  The next step's S runs while P is computed, dP behind dQ.
-// Warps as above without the stager; the thread's row keeps its LSE and D in registers.
-// TMEM columns: dQ [0, D), S [128, 256), dP [256, 384), Q [384, ...), dO [448, ...).
+// of dQ += dS K.  The thread's row keeps its LSE and D in registers.
+// What bounds a step is the chain dS -> dQ -> dP -> dS, as the next S runs while P is computed.
+// At D = 64 there is room for a second dP (kPBuf), and the chain is cut: 2.22 -> 2.18 ms on
+// the noncausal case above, 2.13 with S on an issuing warp of its own.  At D = 128 a step goes in
+// two halves of 64 keys as above, which costs the products nothing here (A comes from tensor
+// memory: 33 cycles a step of 16 for half the columns): 5.65 -> 5.44 ms on the slopes case above.
+// A cap makes the arithmetic longer than the chain, and its warps agree on the polynomial by
+// votes: whole, 0.428 instead of 0.447 ms (odd prefix documents, 8 heads on 2).
+// Roles: warp 0 TMA, warp 1 issues S, warp 2 dP and dQ, warps 4-19 compute as above.
+// TMEM columns: dQ [0, D), S [128, 256), dP [256, 384), Q [384, ...), dO [448, ...); at D = 64
+// Q [64, ...), dO [96, ...), dP [256, 512).
 template <int D>
 struct DqSmem {
   static constexpr int kTileBytes = kTile * D * 2;
