@@ -371,15 +371,17 @@ int flamia_bwd_static_scratch(const flamia_qtensor* q, const flamia_qtensor* k, 
  * (causal = 1: right bound 0).  The prefix lengthens what a query sees; it
  * hides nothing, so under a window it keeps a document's first tokens visible.
  * A row whose visible keys all have bias -inf gets O 0 and LSE +inf, as rows
- * outside every document do, and contributes no gradient. */
+ * outside every document do, and contributes no gradient.  softmax_scale as in
+ * flamia_fwd; a positive one lies between 2^-100 and 2^100.  A softcap or scale
+ * outside its range is FLAMIA_ERR_UNSUPPORTED. */
 typedef struct flamia_score_options {
-  float softcap;              /* 0 (default): none; else a finite positive cap */
+  float softcap;              /* 0 (default): none; else a cap from 1e-30 to 1e30 */
   const float* slopes;        /* device float [hq], finite, or NULL (default): no distance bias.
                                  Constants of the call: no gradient is computed for them. */
   const float* rel_bias;      /* device float [hq, 2 rel_max + 1], entry r + rel_max for key minus
                                  query position r, or NULL (default): none.  Entries are finite or
                                  -inf; below -2^100 (the lowest float among them) they hide the
-                                 pair, as -inf does. */
+                                 pair, as -inf does; above 2^100 they count as 2^100. */
   int rel_max;                /* with rel_bias: 1 .. FLAMIA_REL_MAX; else ignored */
   const int32_t* prefix_lens; /* device int32 [num_seqs], or NULL (default): none; values are
                                  clamped to the document's length */
@@ -395,9 +397,10 @@ void flamia_default_score_options(flamia_score_options* opt);
  * (defaults).  plan: any plan of the same cu_seqlens; one built for the call's
  * own window orders the work best.  Non-finite values of K or V reach the rows
  * of their own document only, hidden or not: inside a document a hidden key
- * enters its tile's product with weight 0.  Rows behind the last document are
- * not read.  Calls on one plan may overlap on the GPU.  With total_tokens = 0
- * the tensors may be NULL. */
+ * enters its tile's product with weight 0.  Rows behind the last document may
+ * hold anything, and a document's results are the same bits whatever the call's
+ * other documents are.  Calls on one plan may overlap on the GPU.  With
+ * total_tokens = 0 the tensors may be NULL. */
 int flamia_scored_fwd(const void* q_bf16, const void* k_bf16, const void* v_bf16, const int32_t* cu_seqlens,
                       int num_seqs, int64_t total_tokens, int hq, int hkv, int head_dim, int causal,
                       float softmax_scale, const flamia_score_options* opt, const void* plan, void* out_bf16,
