@@ -112,6 +112,35 @@ __device__ __forceinline__ Unit read_unit(const uint8_t* units, uint64_t* full, 
   return x.u;
 }
 
+// The plan orders its items by what the window lets them see and knows no prefix.  With one, a call of
+// few items and several units per SM ranks them by their own work first (a thread an item,
+// before the roles part), so that the long units are not the last ones: 154 -> 133 us for odd
+// prefix documents of 9097 rows, 8 heads on 2.  (In the backward the same cost every call's
+// loops their registers, 5% of them, and gained 3% here.)
+constexpr int kRanked = 128, kRankSms = 152;
+__device__ __forceinline__ bool ranked(const ScoredParams& p, int n_units) {
+  return p.prefix && n_units > kRankSms && n_units <= kRanked * p.hq;
+}
+__device__ __forceinline__ void rank_items(const ScoredParams& p, const PlanView& pv, int n_units, uint8_t* order,
+                                           int* cost) {
+  if (!ranked(p, n_units)) return;
+  const int i = threadIdx.x, items = n_units / p.hq;
+  if (i < items) {
+    const Unit U = make_unit(p, pv, i * p.hq);
+    cost[i] = U.kt.n * (2 + U.ntq);      // a unit of one query tile takes three quarters of one of two
+  }
+  __syncthreads();
+  if (i < items) {
+    int rank = 0;
+    for (int j = 0; j < items; ++j) rank += cost[j] > cost[i] || (cost[j] == cost[i] && j < i);
+    order[rank] = (uint8_t)i;
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ int ranked_unit(const ScoredParams& p, int n_units, const uint8_t* order, int i) {
+  return i >= 0 && ranked(p, n_units) ? order[i / p.hq] * p.hq + i % p.hq : i;
+}
+
 template <int D>
 struct FwdSmem {
   static constexpr int kTileBytes = kTile * D * 2;
@@ -122,7 +151,8 @@ struct FwdSmem {
   static constexpr int kInv = kBias + 2 * kBiasTab * 4;     // [2 query tiles][128] 1 / l
   static constexpr int kUnit = kInv + 1024;                 // [kUnits]
   static constexpr int kClc = kUnit + kUnits * 64;          // answer to a request for another CTA's unit
-  static constexpr int kBar = kClc + 16;
+  static constexpr int kOrder = kClc + 16;                  // of the items, when they are ranked here, and their costs
+  static constexpr int kBar = kOrder + kRanked * 5;
   static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -178,6 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n_units == 0) clear_tail(blockIdx.x, gridDim.x, threadIdx.x, kThreads);
     return;
   }
+  uint8_t* order = smem + L::kOrder;
+  rank_items(p, pv, n_units, order, reinterpret_cast<int*>(order + kRanked));
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -274,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             i = clc_cancelled_x(smem + L::kClc);
           } while (i >= n_units);              // a CTA without a unit
         }
-        const Unit U = make_unit(p, pv, ok ? i : -1);
+        const Unit U = make_unit(p, pv, ok ? ranked_unit(p, n_units, order, i) : -1);
         *reinterpret_cast<Unit*>(units + (n % kUnits) * sizeof(Unit)) = U;
         mbar_arrive(&unit_full[n % kUnits]);
         if (U.ntq == 0) break;

@@ -436,3 +436,12 @@ def test_layers_of_a_training_step(F):
     noise = 4 * 2.0 ** -8 * np.sqrt(2 * (f64(b.att.out) ** 2 * f64(b.do) ** 2).sum()) + 4 * 2.0 ** -8 * np.sqrt(
         2 * (f64(o1) ** 2 * f64(dq2[0]) ** 2).sum())
     assert abs((hi - lo) - want) <= noise + 0.1 * abs(want)
+
+
+@pytest.mark.parametrize("docs", [20, 128, 129])
+def test_prefix_documents_ranked_or_not(F, docs):
+    """Up to 128 work items and more than 152 units the forward ranks the items by their work itself."""
+    rng = np.random.default_rng(docs)
+    lengths = [int(x) for x in rng.integers(1, 120, docs)]
+    lengths[3], lengths[7] = (700, 0) if docs == 20 else (121, 119)
+    Problem(F, lengths, 16, 4, 64, pad=5, softcap=8.0, prefix=[int(x) for x in rng.integers(0, 130, docs)], seed=3).check()
