@@ -112,6 +112,11 @@ __device__ __forceinline__ bool named_bar_and(int id, int n, bool pred) {
   return r != 0;
 }
 
+// Programmatic dependent launch: wait until the grid before this one in the stream is complete and
+// its writes are visible; let the grid behind this one start (once every CTA has said so or left).
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
