@@ -80,26 +80,31 @@ __device__ __forceinline__ void add_comp(float& a, float& lost, float x) {
   lost = __fadd_rn(lost, __fadd_rn(__fsub_rn(a, __fsub_rn(s, b)), __fsub_rn(x, b)));
   a = s;
 }
-// One row of D / 2 fp32 accumulators (columns c0 ..) -> bf16 in global memory, times f.
+__device__ __forceinline__ uint32_t pack2(float2 x) {
+  const __nv_bfloat162 b2 = __floats2bfloat162_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t*>(&b2);
+}
+// One row of fp32 accumulators (columns c0 ..) -> bf16 in global memory, times f.  A warp's rows
+// lie apart, so a store moves a sector of 32 bytes per lane where the rows allow it (wide): half as
+// many as with 16 bytes, and the store path is what this waits for.
 template <int COLS>
-__device__ __forceinline__ void store_acc(uint32_t taddr, __nv_bfloat16* dst, float f, bool valid) {
+__device__ __forceinline__ void store_acc(uint32_t taddr, __nv_bfloat16* dst, float f, bool valid, bool wide) {
 #pragma unroll 1
   for (int c = 0; c < COLS / 32; ++c) {
     uint32_t o[32];
     tmem_ld32(taddr + 32 * c, o);
     tmem_ld_wait();
-    if (valid) {
+    uint32_t w[16];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t w[4];
+    for (int e = 0; e < 16; ++e) w[e] = pack2(make_float2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f));
+    if (!valid) continue;
+    if (wide) {
+      st_global_v8(dst + 32 * c, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+      st_global_v8(dst + 32 * c + 16, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * q + 2 * e]) * f,
-                                                          __uint_as_float(o[8 * q + 2 * e + 1]) * f);
-          w[e] = *reinterpret_cast<const uint32_t*>(&b2);
-        }
-        *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
     }
   }
 }
@@ -111,16 +116,13 @@ __device__ __forceinline__ void store_part(uint32_t taddr, float* dst, bool vali
     uint32_t o[32];
     tmem_ld32(taddr + 32 * c, o);
     tmem_ld_wait();
-    if (valid) {
+    if (valid) {                 // (the workspace's rows are whole sectors)
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        *reinterpret_cast<uint4*>(dst + 32 * c + 4 * q) = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+      for (int q = 0; q < 4; ++q)
+        st_global_v8(dst + 32 * c + 8 * q, o[8 * q], o[8 * q + 1], o[8 * q + 2], o[8 * q + 3], o[8 * q + 4], o[8 * q + 5],
+                     o[8 * q + 6], o[8 * q + 7]);
     }
   }
-}
-__device__ __forceinline__ uint32_t pack2(float2 x) {
-  const __nv_bfloat162 b2 = __floats2bfloat162_rn(x.x, x.y);
-  return *reinterpret_cast<const uint32_t*>(&b2);
 }
 // dP where P is not 0: rows of another document, or of nobody, may hold anything, and weight
 // 0 does not silence an infinity.  (In its own branch: selects in the loops over every tile run
@@ -746,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             store_part<D / 2>(sum, part + ((int64_t)(U.start + kj) * p.hq + U.h0) * D + c, valid);
           } else {
             __nv_bfloat16* out = w < 2 ? p.dv : p.dk;
-            store_acc<D / 2>(sum, out + ((int64_t)(U.start + kj) * p.hkv + U.hk) * D + c, w < 2 ? 1.f : p.scale, valid);
+            store_acc<D / 2>(sum, out + ((int64_t)(U.start + kj) * p.hkv + U.hk) * D + c, w < 2 ? 1.f : p.scale, valid,
+                             (reinterpret_cast<uintptr_t>(out) & 31) == 0);
           }
           tc_fence_before();
           mbar_arrive(acc_free);
@@ -1111,7 +1114,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++units;
         if (ok) {
           tc_fence_after();
-          if (w < D / 32) store_acc<32>(lane_base + kTQ + 32 * w, p.dq + (tok * p.hq + h) * D + 32 * w, p.scale, valid);
+          if (w < D / 32) store_acc<32>(lane_base + kTQ + 32 * w, p.dq + (tok * p.hq + h) * D + 32 * w, p.scale, valid,
+                                       (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0);
           tc_fence_before();
           warp_arrive(acc_free);
         }
