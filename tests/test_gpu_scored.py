@@ -445,3 +445,14 @@ def test_prefix_documents_ranked_or_not(F, docs):
     lengths = [int(x) for x in rng.integers(1, 120, docs)]
     lengths[3], lengths[7] = (700, 0) if docs == 20 else (121, 119)
     Problem(F, lengths, 16, 4, 64, pad=5, softcap=8.0, prefix=[int(x) for x in rng.integers(0, 130, docs)], seed=3).check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("offset", [300.0, -4000.0])
+def test_a_bias_far_from_zero(F, d, offset):
+    """A constant added to the whole table changes no probability; only u's own roundings grow."""
+    p = Problem(F, [300, 129, 40], 4, 2, d, pad=3, causal=False, buckets=(32, 64, True), seed=5)
+    p.table += offset
+    p.rel, _ = S.bucket_bias(f64(p.table), p.buckets[1], p.buckets[2], p.buckets[1])
+    p.ref_kw["rel"] = p.rel
+    p.check()
