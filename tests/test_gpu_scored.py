@@ -456,3 +456,22 @@ def test_a_bias_far_from_zero(F, d, offset):
     p.rel, _ = S.bucket_bias(f64(p.table), p.buckets[1], p.buckets[2], p.buckets[1])
     p.ref_kw["rel"] = p.rel
     p.check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_captured_twice_in_a_row(F, d):
+    """Two whole calls in one graph, one workspace: launches that start early still come behind the call before."""
+    import torch
+    p = Problem(F, [1500, 333, 700], 4, 4, d, seed=31, causal=False, buckets=(32, 100, True))
+    want = run_all(p)
+    outs = (p.att.out, p.att.lse, p.att.dq, p.att.dk, p.att.dv, p.att.dtable)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(2):
+            p.backward(*p.forward())
+    for _ in range(3):
+        for t in outs:
+            t.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert same(bits(*outs), want)
