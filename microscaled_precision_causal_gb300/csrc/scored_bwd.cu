@@ -161,7 +161,8 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, u
 // query tile of one of the unit's query heads.  S^T = K Q^T and dP^T = V dO^T have keys in the
 // TMEM lanes, so P^T and dS^T are written back over their own columns and are the A operands
 // of dV += P^T dO and dK += dS^T Q.  A warp issues the chain of S^T and dV, another that of
-// dP^T and dK, so that neither waits for the other's operands.  K is free for the next unit
+// dP^T and dK, so that neither waits for the other's operands; each waits by itself for every
+// tile that its products read, as nothing that the other waited for stands before them.  K is free for the next unit
 // once the unit's last S^T is done, V once its last dP^T is.
 //
 // LSE and D vary along a thread's columns, so every warp would read both of every query from
@@ -404,9 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kA = kP ? L::kK : L::kV, kB = kP ? L::kQ : L::kDO, kB2 = kP ? L::kDO : L::kQ;
         constexpr uint32_t kT = kP ? kTS : kTP, kSum = kP ? kTV : kTK;
         uint64_t *a_full = kP ? k_full : v_full, *a_empty = kP ? k_empty : v_empty;
-        uint64_t *b_full = kP ? q_full : do_full, *b2_empty = kP ? do_empty : q_empty;
+        uint64_t *b_full = kP ? q_full : do_full, *b2_full = kP ? do_full : q_full, *b2_empty = kP ? do_empty : q_empty;
         uint64_t *out = kP ? s_full : dp_full, *in = kP ? p_ready : ds_ready;
-        auto scores = [&](int half, uint32_t g, int unit, bool first, bool last) {      // of step g, both operands K-major
+        // of step g, both operands K-major.  A (K or V): a_full at the unit's first step; B (Q or dO): b_full
+        auto scores = [&](int half, uint32_t g, int unit, bool first, bool last) {
           const uint32_t b = half * kStages + g % kStages, b16 = base16 + g % kStages * (L::kPartBytes / 16);
           const uint32_t sum = tbase + kT + (kP && kSBuf == 2 ? 128 * (g & 1) : kRows * half);
           if (half == 0 && first && !(ok = warp_wait(a_full, unit & 1, status))) return;
@@ -433,7 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (half == kHalves - 1 && last) mma_commit(a_empty);
           }
         };
-        auto product = [&](int half, uint32_t g, bool first) {      // A from TMEM, B over its rows
+        // A from TMEM (P^T or dS^T): in; B over its rows (dO or Q): b2_full.  `in` covers the query rows of a
+        // dK product, whose S^T was computed from them, but not the dO of a dV product: its load is asked for
+        // last, and P^T needs Q and K alone
+        auto product = [&](int half, uint32_t g, bool first) {
+          if (!(ok = warp_wait(&b2_full[half * kStages + g % kStages], (g / kStages) & 1, status))) return;
           if (!(ok = warp_wait(&in[kP ? s_at(half, g) : half], kP ? s_phase(g) : g & 1, status))) return;
           tc_fence_after();
           const uint32_t b16 = base16 + g % kStages * (L::kPartBytes / 16);
@@ -912,6 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // warp 1: S, warp 2: dP and dQ
       const bool leader = elect_one();
       const uint32_t base16 = (smem_u32(smem) & 0x3FFFFu) >> 4;
+      // A (Q or dO in TMEM): q_ready at the unit's first step; B (K or V): k_full, v_full
       auto scores = [&](uint32_t a, uint32_t b_off, uint32_t d, int half) {
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
@@ -957,7 +964,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const uint32_t b = g % kStages;
           if (ok && kPBuf == 2 && !last) issue_dp(g + 1, 0);
-          // the unit's first product overwrites the sums of the last one: those have to be out
+          // dQ += dS K.  A (dS in TMEM): ds_ready; B (K): ds_ready too, as the same threads have read the
+          // whole of the S that came from this K (k_full is the other warp's; it cannot have moved on,
+          // because this product gives the stage back).  The unit's first product overwrites the sums of
+          // the last one: those have to be out
           if (ok && first && units > 1) ok = warp_wait(acc_free, units & 1, status);
 #pragma unroll
           for (int half = 0; half < kHalves; ++half) {

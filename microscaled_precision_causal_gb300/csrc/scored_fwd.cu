@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto release = [&](uint32_t x) {
           if (leader) mma_commit(&kv_empty[x % kSlots]);
         };
-        auto scores = [&](int w, int k) {          // S of key tile k
+        auto scores = [&](int w, int k) {          // S of key tile k.  A (Q): q_full at the unit's first; B (K): kv_full
           const uint32_t x = ring + 2 * k, st = x % kSlots;
           if (k == first(w) && !(ok = warp_wait(&q_full[w], (w ? nq1 : nq0) & 1, status))) return;
           uint32_t& ns = w ? ns1 : ns0;
@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k == last(w)) mma_commit(&q_empty[w]);
           }
         };
-        auto values = [&](int w, int k) {          // O += P V, half of the keys at a time as they are handed in
+        // O += P V, half of the keys at a time as they are handed in.  A (P in TMEM): p_full; B (V): kv_full
+        auto values = [&](int w, int k) {
           const uint32_t x = ring + 2 * k + 1, st = x % kSlots;
           if (!landed(x)) return;
           const uint32_t nq = w ? nq1 : nq0;

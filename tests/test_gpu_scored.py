@@ -292,6 +292,39 @@ def test_equal_inputs_give_equal_bits(F):
         assert same(run_all(p), want)
 
 
+FORMS = {
+    "plain": dict(hkv=16), "cap": dict(hkv=16, softcap=50.0), "slopes": dict(hkv=8, slopes=True),
+    "prefix": dict(hkv=8, softcap=30.0, prefix=[1500, 0, 2999, 1, 129, 700, 64, 0, 33, 200, 4]),
+    "buckets": dict(hkv=16, buckets=(32, 128, False)),
+    "cap_buckets": dict(hkv=8, softcap=50.0, slopes=True, buckets=(32, 100, False)),
+}
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_bits_do_not_depend_on_when_a_load_lands(F, form, d):
+    """Many units per SM, operands from memory (L2 is overwritten and another problem runs in between): a product
+    that does not wait for its tile multiplies by what its stage held before."""
+    import torch
+    lengths = [4000, 129, 2886, 84, 1500, 3000, 700, 513, 2048, 1024, 500]
+    p = Problem(F, lengths, 16, d=d, seed=41, **FORMS[form])
+    other = Problem(F, [3000, 1000], 16, 16, d, seed=42, causal=False)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    o_out, o_lse = other.forward()
+    out, lse = (t.clone() for t in p.forward())
+    want = bits(out, lse, *p.backward(out, lse))
+    wrong = torch.zeros(len(want), dtype=torch.int64, device="cuda")
+    for i in range(100):
+        other.backward(o_out, o_lse)
+        flush.fill_(i)
+        p.forward()
+        flush.fill_(i)
+        got = p.backward(out, lse)
+        wrong += torch.stack([(a != b).sum() for a, b in zip(bits(p.att.out, p.att.lse, *got), want)])
+    assert wrong.tolist() == [0] * len(want)
+    assert p.att.device_status() == 0
+
+
 def test_any_plan_of_the_same_documents(F):
     p = Problem(F, [700, 333], 2, 1, 64, seed=22, window=(200, -1), softcap=20.0)
     want = run_all(p)
