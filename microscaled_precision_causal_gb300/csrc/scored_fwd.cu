@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* unit_ask = bars + 24;
   uint64_t* clc_bar = bars + 25;
   uint64_t* unit_full = bars + 26;          // [kUnits]
-  uint64_t* unit_done = unit_full + kUnits; // [kUnits]
+  uint64_t* unit_done = unit_full + kUnits; // [kUnits] written out, and read by the second query tile's softmax
   uint64_t* kv_full = unit_done + kUnits;   // [kSlots]
   uint64_t* kv_empty = kv_full + kSlots;    // [kSlots]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + kSlots);
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(clc_bar, 1);
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&unit_full[i], 1);
-      mbar_init(&unit_done[i], 1);
+      mbar_init(&unit_done[i], 1 + 4);              // (its four warps)
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
@@ -426,6 +426,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&tab_full[n & 1], (n >> 1) & 1, status));
         if (!ok) break;
         HB = head_bias(tab);
+      }
+      if (w == 1) {              // a unit of one query tile asks nothing else of these warps: nobody would wait for them
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&unit_done[n % kUnits]);
       }
       if (skip == -2) {
         ring += 2 * nk;
@@ -635,7 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; ok && U.ntq; ++n) {
       const int h = U.h, t0 = U.t0, ntq = U.ntq, start = U.start, len = U.len, index = U.index;
       U = read_unit(units, unit_full, n + 1, true, ok, status);
-      if (BIAS && U.ntq) {            // into the table of the last unit but one, whose O is out
+      if (BIAS && U.ntq) {            // into the table of the last unit but one, whose O is out and which all have read
+        if (n && !(ok = __all_sync(0xffffffffu, mbar_wait(&unit_done[(n - 1) % kUnits], ((n - 1) / kUnits) & 1, status)))) break;
         stage_bias(tab + ((n + 1) & 1) * kBiasTab, p, U.h, r, 128);
         mbar_arrive(&tab_full[(n + 1) & 1]);
       }

@@ -252,6 +252,17 @@ def test_units_dealt_out_and_taken_over(F, d):
     assert torch.count_nonzero(o[300:]) == 0 and torch.isposinf(l[:, 300:]).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (16, 8)])
+def test_runs_of_one_tile_units(F, hq, hkv, d):
+    """Documents of up to 128 rows: the second query tile's warps have nothing to do for many units on end, until
+    the one document of two tiles.  4 heads: units taken over; 16: dealt out."""
+    rng = np.random.default_rng(7)
+    lengths = [int(x) for x in rng.integers(1, 129, 300)]
+    lengths[250] = 200
+    Problem(F, lengths, hq, hkv, d, pad=7, seed=18, slopes=True, buckets=(16, 40, False)).check()
+
+
 def test_no_valid_tokens(F):
     Problem(F, [0, 0, 0], 4, 2, 64, pad=300, slopes=True, causal=False).check()
 
