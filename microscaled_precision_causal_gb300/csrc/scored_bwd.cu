@@ -86,12 +86,14 @@ __device__ __forceinline__ uint32_t pack2(float2 x) {
 }
 // One row of fp32 accumulators (columns c0 ..) -> bf16 in global memory, times f.  A warp's rows
 // lie apart, so a store moves a sector of 32 bytes per lane where the rows allow it (wide): half as
-// many as with 16 bytes, and the store path is what this waits for.
+// many as with 16 bytes, and the store path is what this waits for.  Where a document ends inside the
+// warp only some lanes store; the loads from tensor memory are the whole warp's, so it meets first.
 template <int COLS>
 __device__ __forceinline__ void store_acc(uint32_t taddr, __nv_bfloat16* dst, float f, bool valid, bool wide) {
 #pragma unroll 1
   for (int c = 0; c < COLS / 32; ++c) {
     uint32_t o[32];
+    __syncwarp();
     tmem_ld32(taddr + 32 * c, o);
     tmem_ld_wait();
     uint32_t w[16];
@@ -114,6 +116,7 @@ __device__ __forceinline__ void store_part(uint32_t taddr, float* dst, bool vali
 #pragma unroll 1
   for (int c = 0; c < COLS / 32; ++c) {
     uint32_t o[32];
+    __syncwarp();
     tmem_ld32(taddr + 32 * c, o);
     tmem_ld_wait();
     if (valid) {                 // (the workspace's rows are whole sectors)
@@ -711,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             else if (rel >= R) add_comp(far_hi, lost_hi, s);
             else acc[rel + R] += s;
           }
+          __syncwarp();
         }
       }
       }

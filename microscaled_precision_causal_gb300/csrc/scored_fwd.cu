@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (u * kTile + r >= U.len) clear_row<D>(smem + L::kKV + st * L::kTileBytes, r);
           fence_proxy_async_smem();
+          __syncwarp();              // P is stored by the whole warp
         }
         const float neg = (m == -INFINITY ? 0.f : -m) + B.c;
         // P in two halves of 64 keys: the first one's product starts while the second is computed
@@ -657,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 2
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
+          __syncwarp();              // (the rows of the document alone have stored the last columns)
           tmem_ld32(lane_base + kO + w * D + 32 * c, o);
           tmem_ld_wait();
           uint32_t pk[16];
