@@ -157,9 +157,11 @@ int check_score_opts(const flamia_score_options* o) {
   return FLAMIA_OK;
 }
 
-// A scale whose square or reciprocal leaves the fp32 range has no use.
-int check_score_scale(float s) {
-  return s > 0.f && (s < 7.8886091e-31f || s > 1.2676506e30f) ? FLAMIA_ERR_UNSUPPORTED : FLAMIA_OK;   // 2^-100 .. 2^100
+// A scale whose square or reciprocal leaves the fp32 range has no use, nor a cap that every product but 0
+// exceeds by 2^100 and more: its capped score and the cap over the scale leave that range too.
+int check_score_scale(float s, int d, const flamia_score_options* o) {
+  if (s > 0.f && (s < 7.8886091e-31f || s > 1.2676506e30f)) return FLAMIA_ERR_UNSUPPORTED;   // 2^-100 .. 2^100
+  return o && o->softcap > 0.f && (double)resolve_scale(s, d) / o->softcap > 1e30 ? FLAMIA_ERR_UNSUPPORTED : FLAMIA_OK;
 }
 
 ScoredParams scored_params(const void* q, const void* k, const void* v, const int32_t* cu, int N, int64_t T, int hq,
@@ -421,7 +423,7 @@ int flamia_scored_fwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
   int rc = check_common(total_tokens, num_seqs, cu_seqlens, plan);
   if (!rc) rc = check_heads(hq, hkv, head_dim);
   if (!rc) rc = check_score_opts(opt);
-  if (!rc) rc = check_score_scale(softmax_scale);
+  if (!rc) rc = check_score_scale(softmax_scale, head_dim, opt);
   if (rc) return rc;
   if (causal != 0 && causal != 1) return FLAMIA_ERR_INVALID_ARG;
   if (total_tokens == 0) return FLAMIA_OK;
@@ -450,7 +452,7 @@ int flamia_scored_bwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
   int rc = check_common(total_tokens, num_seqs, cu_seqlens, plan);
   if (!rc) rc = check_heads(hq, hkv, head_dim);
   if (!rc) rc = check_score_opts(opt);
-  if (!rc) rc = check_score_scale(softmax_scale);
+  if (!rc) rc = check_score_scale(softmax_scale, head_dim, opt);
   if (rc) return rc;
   if (causal != 0 && causal != 1) return FLAMIA_ERR_INVALID_ARG;
   if (drel_bias && !(opt && opt->rel_bias)) return FLAMIA_ERR_INVALID_ARG;

@@ -1,6 +1,9 @@
 // Scored attention: what its kernels and the ABI share (parameters, the bucket rule,
 // the visible-key sets and the backward's workspace layout).
 #pragma once
+#include <algorithm>
+#include <cmath>
+
 #include "common.cuh"
 
 namespace flamia {
@@ -10,7 +13,7 @@ namespace flamia {
 struct CapForm {
   float zscale;      // softmax scale / cap
   float inv;         // cap / softmax scale
-  float t3, t5;      // up to this |S| the polynomials of 3 and of 5 coefficients serve (0: never)
+  float t3, t5;      // up to this |S| the polynomials of 3 and of 5 coefficients serve (-1: never, not even for 0)
   float2 k3[3], k5[5];    // their coefficients of S^2, S^4, ... (twice: packed operands)
   float2 e3[4], e5[6];    // the same with 1 in front, times the scale in base 2
 };
@@ -177,14 +180,17 @@ inline CapForm cap_form(double scale, double cap) {
   const double z = scale / cap;
   c.zscale = (float)z;
   c.inv = (float)(cap / scale);
-  // the folded coefficients have to stay inside the fp32 range
-  c.t3 = z > 1e-6 && z < 1e6 ? (float)(kTanh3To / z) : 0.f;
-  c.t5 = z > 3e-4 && z < 1e3 ? (float)(kTanh5To / z) : 0.f;
+  // A folded coefficient that left the fp32 range would make 0 * inf of a product of 0 (a hidden pair's, a
+  // row of zeros'): where the largest one does, its polynomial serves nothing, and its coefficients stay 0.
+  const double most = std::max(1.0, scale2);
+  const bool use3 = z > 1e-6 && std::pow(z, 6) * most < 1e38, use5 = z > 3e-4 && std::pow(z, 10) * most < 1e38;
+  c.t3 = use3 ? (float)(kTanh3To / z) : -1.f;
+  c.t5 = use5 ? (float)(kTanh5To / z) : -1.f;
   const float k5[5] = {kTanh5a, kTanh5b, kTanh5c, kTanh5d, kTanh5e};
   double f = z * z;
   for (int i = 0; i < 5; ++i, f *= z * z) {
-    if (i < 3) c.k3[i] = two(kTanh3[i] * f), c.e3[i + 1] = two(kTanh3[i] * f * scale2);
-    c.k5[i] = two(k5[i] * f), c.e5[i + 1] = two(k5[i] * f * scale2);
+    if (use3 && i < 3) c.k3[i] = two(kTanh3[i] * f), c.e3[i + 1] = two(kTanh3[i] * f * scale2);
+    if (use5) c.k5[i] = two(k5[i] * f), c.e5[i + 1] = two(k5[i] * f * scale2);
   }
   c.e3[0] = c.e5[0] = two(scale2);
   return c;

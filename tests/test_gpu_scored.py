@@ -233,6 +233,17 @@ def test_caps_of_every_size(F, cap):
     Problem(F, [140, 60], 2, 1, 128, seed=16, softcap=cap, gain=4.0).check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,scale", [(1e-8, 0.0), (2e-7, 0.0), (1e-30, 0.0), (5.0, 0.0), (1.0, 1e30), (1e28, 1e30), (1e-8, 1e22)])
+def test_caps_that_dwarf_the_scores_and_products_of_zero(F, cap, scale, d):
+    """A cap far below the scores (folded coefficients past the fp32 range), with blocks of hidden pairs on the
+    diagonal, a head whose queries are zero and a document whose keys are."""
+    p = Problem(F, [140, 64, 60], 4, 2, d, seed=16, softcap=cap, scale=scale)
+    p.q[:, 1] = 0
+    p.k[140:204] = 0
+    p.check()
+
+
 def test_negative_slopes_and_many_documents(F):
     Problem(F, [1] * 40 + [7] * 20 + [129] * 3, 3, 3, 64, seed=17, slopes=[-0.4, 0.0, 1.0], pad=1).check()
 

@@ -96,6 +96,18 @@ def test_forward_refusals(F, i):
                                      0.0, ctypes.byref(o), a["plan"], a["out"], a["lse"], None) == want
 
 
+@pytest.mark.parametrize("softcap,scale,d,want", [
+    (1e-3, 1.2e30, 128, -2), (0.9, 1e30, 64, -2), (1e-30, 1.1, 64, -2), (1.1, 1e30, 64, -3), (1e-30, 0.9, 64, -3),
+    (1e-30, 0.0, 64, -3), (1e30, 8e-31, 128, -3), (0.0, 1.2e30, 128, -3), (0.0, 1.3e30, 128, -2), (0.0, 7e-31, 128, -2)])
+def test_cap_and_scale_ranges(F, softcap, scale, d, want):
+    """-3: the checks went on to the misaligned output."""
+    o = _opts(F, softcap=softcap)
+    assert F.lib().flamia_scored_fwd(256, 256, 256, 256, 1, 100, 4, 2, d, 1, scale, ctypes.byref(o), 256, 258, 256,
+                                     None) == want
+    assert F.lib().flamia_scored_bwd(256, 256, 256, 258, 256, 256, 256, 1, 100, 4, 2, d, 1, scale, ctypes.byref(o), 256, 256,
+                                     256, 256, None, 256, 1 << 30, None) == want
+
+
 BWD = FWD[:20] + [
     (dict(dout=0), {}, -1), (dict(dq=0), {}, -1), (dict(dk=0), {}, -1), (dict(dv=0), {}, -1), (dict(ws=0), {}, -1),
     (dict(dout=264), {}, -3), (dict(dq=264), {}, -3), (dict(dk=264), {}, -3), (dict(dv=264), {}, -3), (dict(ws=128), {}, -3),
