@@ -23,9 +23,11 @@ Buckets make_buckets(int nb, int md, int both) {
 }
 
 // Bucket of distance r (key minus query).  The logarithm is in 64 bits: a distance n with
-// (n / e) ^ (B - e) a whole power of max_distance / e lies on a bucket's border, and 2^-30
-// puts it into the upper bucket whatever the last bit of the product; no other n up to 1024
-// comes that close to a border from below.
+// (n / e) ^ (B - e) a whole power of max_distance / e lies on a bucket's border, and 2^-36
+// puts it into the upper bucket whatever the last bits of the product.  Over every B up to 1024,
+// max_distance up to 1024 and n (whole numbers decide what is a border) the product's error
+// there is at most 5e-13, and the nearest distance below a border lies 3.7e-10 from it (B 73,
+// max_distance 905, n 347): 2^-36, 1.5e-11, is between.
 __device__ int rel_bucket(int r, const Buckets& B) {
   int base = 0, n, nb = B.nb;
   if (B.both) {
@@ -38,7 +40,7 @@ __device__ int rel_bucket(int r, const Buckets& B) {
   const int e = nb >> 1;
   if (n < e) return base + n;
   if (n >= B.md) return base + nb - 1;
-  const int b = e + (int)floor(log((double)n / e) * B.per_log + 0x1p-30);
+  const int b = e + (int)floor(log((double)n / e) * B.per_log + 0x1p-36);
   return base + (b < nb - 1 ? b : nb - 1);
 }
 

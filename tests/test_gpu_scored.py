@@ -219,6 +219,24 @@ def test_a_bias_that_hides(F, value, far):
     assert (got[3][6 if far else 0, 1] == 0).all()
 
 
+@pytest.mark.parametrize("nb,md,both", [(73, 905, False), (146, 905, True), (21, 1006, False), (32, 128, True), (24, 96, False),
+                                        (64, 1024, True), (1024, 1024, True), (1023, 1023, False), (2, 2, False)])
+def test_buckets_at_their_borders(F, nb, md, both):
+    """Every distance of the table's range: on a border, just below one (73, 905: 347 by 3.7e-10), just above."""
+    import torch
+    R = min(md + 3, 1024)
+    want = np.array([S.bucket(r, nb, md, both) for r in range(-R, R + 1)])
+    table = torch.arange(nb, dtype=torch.float32, device="cuda")[:, None].repeat(1, 3) * torch.tensor([1.0, 2.0, 0.0], device="cuda")
+    rel = torch.full((3, 2 * R + 1), float("nan"), device="cuda")
+    F.flamia_relbias_expand(table.contiguous(), md, both, rel)
+    assert np.array_equal(f64(rel), np.stack([want, 2 * want, 0 * want]))
+    dtable = torch.full((nb, 3), float("nan"), device="cuda")
+    counts = torch.ones_like(rel) * torch.tensor([[1.0], [3.0], [0.0]], device="cuda")
+    F.flamia_relbias_reduce(counts, md, both, dtable)
+    n = np.bincount(want, minlength=nb)
+    assert np.array_equal(f64(dtable), np.stack([n, 3 * n, 0 * n], 1))
+
+
 def test_largest_relative_range(F):
     Problem(F, [2300], 1, 1, 64, seed=14, buckets=(64, 1024, True), causal=False).check()
 
