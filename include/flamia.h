@@ -378,7 +378,8 @@ int flamia_bwd_static_scratch(const flamia_qtensor* q, const flamia_qtensor* k, 
 typedef struct flamia_score_options {
   float softcap;              /* 0 (default): none; else a cap from 1e-30 to 1e30 */
   const float* slopes;        /* device float [hq], finite, or NULL (default): no distance bias.
-                                 Constants of the call: no gradient is computed for them. */
+                                 Beyond 2^100 in magnitude they count as 2^100.  Constants of the
+                                 call: no gradient is computed for them. */
   const float* rel_bias;      /* device float [hq, 2 rel_max + 1], entry r + rel_max for key minus
                                  query position r, or NULL (default): none.  Entries are finite or
                                  -inf; below -2^100 (the lowest float among them) they hide the

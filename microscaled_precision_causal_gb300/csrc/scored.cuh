@@ -211,7 +211,6 @@ struct TileBias {
   const float* tab; // table entry of the thread's column 0, or null
   float col;        // the slope's part per unit of distance, in the products' units
   float c;          // the rest, added in the exponent
-  __device__ __forceinline__ bool plain() const { return !tab && col == 0.f; }
   __device__ __forceinline__ float factor(float scale2) const { return tab ? 1.f : scale2; }
 };
 __device__ __forceinline__ float2 pair_of(const uint32_t (&v)[32], int j) {
@@ -318,36 +317,45 @@ constexpr int kBiasTab = kBiasHead + 4;                            // floats, an
 __device__ __forceinline__ float bias_base2(float b) {
   return b < kHideBelow ? -INFINITY : fminf(b, -kHideBelow) * kLog2e;
 }
+// A slope steeper than 2^100 counts as 2^100 (times the longest distance it stays in the fp32 range); in
+// the products' units it is held to 2^119, whose multiple by a column is finite too.  (At that steepness a
+// step of distance outweighs any score, so that only the nearest or the farthest visible key counts.)
+__device__ __forceinline__ float slope_base2(float s) { return fminf(fmaxf(s, kHideBelow), -kHideBelow) * kLog2e; }
+__device__ __forceinline__ float slope_products(float slope2, float scale2) {
+  return fminf(fmaxf(slope2 / scale2, -0x1p119f), 0x1p119f);
+}
 __device__ __forceinline__ int bias_range(const ScoredParams& p) { return p.rel ? p.R : 1; }
 struct HeadBias {
   float slope2, lo, hi;      // slope, and the bias of the distances up to -R and from R on
+  float col;                 // the slope in the products' units
 };
 __device__ __forceinline__ void stage_bias(float* tab, const ScoredParams& p, int h, int first, int stride) {
   const int R = bias_range(p);
-  const float slope2 = p.slopes ? p.slopes[h] * kLog2e : 0.f;
+  const float slope2 = p.slopes ? slope_base2(p.slopes[h]) : 0.f;
   const float* src = p.rel ? p.rel + (size_t)h * (2 * R + 1) : nullptr;
   for (int i = first; i < 2 * (R + kBiasReach) + 1; i += stride) {
     const float b = src ? bias_base2(src[min(max(i - kBiasReach, 0), 2 * R)]) : 0.f;
     tab[i] = fmaf(fabsf((float)(i - R - kBiasReach)), -slope2, b);
     if (i == 0) tab[kBiasHead] = slope2;
     if (i == 0) tab[kBiasHead + 1] = b;
+    if (i == 0) tab[kBiasHead + 3] = slope_products(slope2, p.scale2);
     if (i == 2 * (R + kBiasReach)) tab[kBiasHead + 2] = b;
   }
 }
 __device__ __forceinline__ HeadBias head_bias(const float* tab) {
-  return HeadBias{tab[kBiasHead], tab[kBiasHead + 1], tab[kBiasHead + 2]};
+  return HeadBias{tab[kBiasHead], tab[kBiasHead + 1], tab[kBiasHead + 2], tab[kBiasHead + 3]};
 }
 // Key tiles closer to the query tile than this hold a distance below R.
 __device__ __forceinline__ int near_tiles(int R) { return (R + kTile - 2) / kTile; }
 // The bias of query tile t x key tile u for the thread whose column 0 has distance rel0.
-__device__ __forceinline__ TileBias tile_bias(const float* tab, const HeadBias& H, int R, int near, float inv_scale2, int t,
-                                              int u, int rel0) {
+__device__ __forceinline__ TileBias tile_bias(const float* tab, const HeadBias& H, int R, int near, int t, int u,
+                                              int rel0) {
   TileBias B;
   const bool low = u < t;
   const float sl = low ? H.slope2 : -H.slope2;      // bias per unit of distance
   B.tab = abs(u - t) <= near ? tab + rel0 + R + kBiasReach : nullptr;
   B.c = B.tab ? 0.f : fmaf(sl, (float)rel0, low ? H.lo : H.hi);
-  B.col = sl * inv_scale2;
+  B.col = low ? H.col : -H.col;
   return B;
 }
 

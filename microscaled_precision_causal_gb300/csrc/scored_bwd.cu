@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* acc = reinterpret_cast<float*>(smem + L::kAcc);
     const int R = bias_range(p);
     const int near = near_tiles(R);
-    const float scale2 = p.scale2, inv_scale2 = 1.f / p.scale2;
+    const float scale2 = p.scale2;
     HeadBias HB{};
     int staged = -1;
     float far_lo = 0.f, far_hi = 0.f, lost_lo = 0.f, lost_hi = 0.f;
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         uint32_t gr[32];
         TileBias B{};
-        if constexpr (BIAS != 0) B = tile_bias(tab, HB, R, near, inv_scale2, t, U.u, kj - (t * kTile + 32 * w));
+        if constexpr (BIAS != 0) B = tile_bias(tab, HB, R, near, t, U.u, kj - (t * kTile + 32 * w));
         const float f = BIAS != 0 ? B.factor(scale2) : scale2;
         const bool masked = t < U.full.x || t > U.full.y;
         const bool edge = (t + 1) * kTile > U.len || (BIAS == 2 && (U.u + 1) * kTile > U.len);
@@ -1007,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* tab = reinterpret_cast<float*>(smem + L::kBias);
     const int R = bias_range(p);
     const int near = near_tiles(R);
-    const float scale2 = p.scale2, inv_scale2 = 1.f / p.scale2;
+    const float scale2 = p.scale2;
     HeadBias HB{};
     int staged = -1;
     bool ok = true;
@@ -1066,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         warp_arrive(&s_free[half]);
         TileBias B{};
-        if constexpr (BIAS) B = tile_bias(tab, HB, R, near, inv_scale2, t, u, u * kTile + 32 * w - qi);
+        if constexpr (BIAS) B = tile_bias(tab, HB, R, near, t, u, u * kTile + 32 * w - qi);
         const float f = BIAS ? B.factor(scale2) : scale2;
         const bool masked = !full.has(u);
         const int c0 = u * kTile + 32 * w;

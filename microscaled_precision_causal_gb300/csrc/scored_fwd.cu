@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t p_addr = kSplit ? lane_base + kP + 64 * w : s_addr;
     float* inv_l = reinterpret_cast<float*>(smem + L::kInv) + w * 128;
     const int R = bias_range(p), near = near_tiles(R);
-    const float scale2 = p.scale2, inv_scale2 = 1.f / p.scale2;
+    const float scale2 = p.scale2;
     uint32_t ring = 0, ns = 0, nu = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k == skip) continue;
         const int u = U.kt.tile(k);
         TileBias B{};
-        if constexpr (BIAS) B = tile_bias(tab, HB, R, near, inv_scale2, t, u, u * kTile - qi);
+        if constexpr (BIAS) B = tile_bias(tab, HB, R, near, t, u, u * kTile - qi);
         const bool seen = full.has(u);
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[w], ns & 1, status));
         if (!ok) break;

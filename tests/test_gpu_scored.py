@@ -262,6 +262,41 @@ def test_caps_that_dwarf_the_scores_and_products_of_zero(F, cap, scale, d):
     p.check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 9.0])
+@pytest.mark.parametrize("scale", [0.0, 1e-30])
+@pytest.mark.parametrize("causal", [True, False])
+def test_slopes_of_every_size(F, d, cap, scale, causal):
+    """Finite slopes up to the type's largest: a key a step farther weighs e^-slope less, here 0, so a row is its own
+    key's alone."""
+    import torch
+    p = Problem(F, [300, 1, 129], 4, 4, d, pad=3, seed=19, causal=causal, softcap=cap, scale=scale,
+                slopes=[3.4e38, 2.0 ** 100, 1e30, 3e9])
+    out, lse = p.forward()
+    dq, dk, dv = p.backward(out, lse)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:430], p.v[:430]) and torch.equal(dv[:430], p.do[:430])
+    q, k, v, do = (f64(t[:430]) for t in (p.q, p.k, p.v, p.do))
+    u = (scale or d ** -0.5) * (q * k).sum(2)
+    u = cap * np.tanh(u / cap) if cap else u
+    # the product's d terms and some roundings of the value itself
+    tol = 2.0 ** -24 * ((d + 8) * (scale or d ** -0.5) * np.abs(q * k).sum(2) + 16 * np.abs(u) + 16 * cap) + 2.0 ** -120
+    assert (np.abs(f64(lse)[:, :430] - u.T) <= tol.T).all()
+    # dP - D of equal sums: their roundings, times P = 1 (1 + 8 roundings of 1 + |LSE|)
+    ds = 2.0 ** -24 * 2 * (d + 8) * np.abs(do * v).sum(2, keepdims=True) * (scale or d ** -0.5) + 2.0 ** -126
+    assert (np.abs(f64(dq[:430])) <= 2 * ds * np.abs(k) + 2.0 ** -126).all()
+    assert (np.abs(f64(dk[:430])) <= 2 * ds * np.abs(q) + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_steep_negative_slopes(F, d):
+    """The farthest key takes all: a causal row is its document's first."""
+    p = Problem(F, [300, 129], 3, 3, d, seed=20, slopes=[-3.4e38, -1e30, -3e6])
+    out, lse = p.forward()
+    first = np.repeat([0, 300], [300, 129])
+    assert np.array_equal(f64(out), f64(p.v)[first]) and np.isfinite(f64(lse)).all()
+
+
 def test_negative_slopes_and_many_documents(F):
     Problem(F, [1] * 40 + [7] * 20 + [129] * 3, 3, 3, 64, seed=17, slopes=[-0.4, 0.0, 1.0], pad=1).check()
 
