@@ -294,7 +294,9 @@ def test_steep_negative_slopes(F, d):
     p = Problem(F, [300, 129], 3, 3, d, seed=20, slopes=[-3.4e38, -1e30, -3e6])
     out, lse = p.forward()
     first = np.repeat([0, 300], [300, 129])
-    assert np.array_equal(f64(out), f64(p.v)[first]) and np.isfinite(f64(lse)).all()
+    # P and O are rounded, half a step each; P need not be 1 where the bias leaves the scores no digits
+    assert (np.abs(f64(out) - f64(p.v)[first]) <= 2.1 * 2.0 ** -8 * np.abs(f64(p.v)[first])).all()
+    assert np.isfinite(f64(lse)).all()
 
 
 def test_negative_slopes_and_many_documents(F):
