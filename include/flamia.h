@@ -373,7 +373,7 @@ int flamia_bwd_static_scratch(const flamia_qtensor* q, const flamia_qtensor* k, 
  * A row whose visible keys all have bias -inf gets O 0 and LSE +inf, as rows
  * outside every document do, and contributes no gradient.  softmax_scale as in
  * flamia_fwd; a positive one lies between 2^-100 and 2^100, and with a softcap it
- * is at most 1e30 times the softcap.  A softcap or scale outside its range is
+ * is at most 2^100 times the softcap.  A softcap or scale outside its range is
  * FLAMIA_ERR_UNSUPPORTED. */
 typedef struct flamia_score_options {
   float softcap;              /* 0 (default): none; else a cap from 1e-30 to 1e30 */

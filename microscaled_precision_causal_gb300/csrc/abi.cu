@@ -161,7 +161,7 @@ int check_score_opts(const flamia_score_options* o) {
 // exceeds by 2^100 and more: its capped score and the cap over the scale leave that range too.
 int check_score_scale(float s, int d, const flamia_score_options* o) {
   if (s > 0.f && (s < 7.8886091e-31f || s > 1.2676506e30f)) return FLAMIA_ERR_UNSUPPORTED;   // 2^-100 .. 2^100
-  return o && o->softcap > 0.f && (double)resolve_scale(s, d) / o->softcap > 1e30 ? FLAMIA_ERR_UNSUPPORTED : FLAMIA_OK;
+  return o && o->softcap > 0.f && (double)resolve_scale(s, d) / o->softcap > 1.2676506e30 ? FLAMIA_ERR_UNSUPPORTED : FLAMIA_OK;
 }
 
 ScoredParams scored_params(const void* q, const void* k, const void* v, const int32_t* cu, int N, int64_t T, int hq,

@@ -97,7 +97,7 @@ def test_forward_refusals(F, i):
 
 
 @pytest.mark.parametrize("softcap,scale,d,want", [
-    (1e-3, 1.2e30, 128, -2), (0.9, 1e30, 64, -2), (1e-30, 1.1, 64, -2), (1.1, 1e30, 64, -3), (1e-30, 0.9, 64, -3),
+    (1e-3, 1.2e30, 128, -2), (0.75, 1e30, 64, -2), (1e-30, 1.3, 64, -2), (0.8, 1e30, 64, -3), (1e-30, 0.9, 64, -3),
     (1e-30, 0.0, 64, -3), (1e30, 8e-31, 128, -3), (0.0, 1.2e30, 128, -3), (0.0, 1.3e30, 128, -2), (0.0, 7e-31, 128, -2)])
 def test_cap_and_scale_ranges(F, softcap, scale, d, want):
     """-3: the checks went on to the misaligned output."""
