@@ -38,6 +38,11 @@
 // tensor memory load's own reduction of the raw products (plain: their maximum; capped: their
 // largest magnitude, which also says how long a polynomial the cap needs; slopes: their maximum
 // and the tile's largest bias), as long as it can be no more than 2^64 too high.
+// x - m is one multiply-add from the raw product, exact but for its own rounding, while m was rounded: from
+// |m| = 2^30 on the difference could pass 2^128.  No model means such scores, but a run that diverges has them: from
+// 2^28 on a row's x and m are shrunk by the power of two that brings m below 2^29.  Products that differ at all
+// there still differ by 16 and more.  (From m again in every tile: kept from tile to tile it costs 640 instead of 632
+// us on the noncausal buckets case of 2 x 8192, 16 heads, d = 64, and 622 without.)
 //
 // TMEM columns: S_0 [0, 128), S_1 [128, 256), O_0 [256, 256 + D), O_1 [256 + D, 256 + 2 D).  At
 // D = 128 that is all of it and P_w takes the first half of S_w's columns.  At D = 64 the
@@ -56,6 +61,10 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr float kRescaleAbove = 8.f, kLoose = 64.f;
+__device__ __forceinline__ float shrink_for(float m) {
+  const uint32_t e = (__float_as_uint(m) >> 23) & 255;       // of 2^(e - 127), 255: nothing visible yet
+  return e >= 127 + 28 && e < 255 ? __uint_as_float((2 * 127 + 28 - e) << 23) : 1.f;
+}
 constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
 constexpr int kRegCtl = 64, kRegAux = 80, kRegSoftmax = 184;
 static_assert(kRegCtl * 128 + kRegAux * 128 + kRegSoftmax * 256 <= kLaunchRegs * kThreads, "register split");
@@ -542,12 +551,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();              // P is stored by the whole warp
         }
-        const float neg = (m == -INFINITY ? 0.f : -m) + B.c;
+        const float shrink = shrink_for(m);
+        const float neg = ((m == -INFINITY ? 0.f : -m) + B.c) * shrink, fs = fmaxf(f * shrink, 0x1p-126f);   // (0 * -inf)
         // P in two halves of 64 keys: the first one's product starts while the second is computed
         auto exps = [&](auto FORM) {
           constexpr int kForm = decltype(FORM)::value;
-          const float2 f2 = make_float2(f, f), n2 = make_float2(neg, neg);
-          const float s2 = B.col * scale2;
+          const float2 f2 = make_float2(fs, fs), n2 = make_float2(neg, neg);
+          const float s2 = B.col * fs;
           const CapForm& F = p.capf;
           auto arg = [&](int g, int c) {
             const float2 x = pair_of(v[g], c);

@@ -252,7 +252,7 @@ def test_caps_of_every_size(F, cap):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("cap,scale", [(1e-8, 0.0), (2e-7, 0.0), (1e-30, 0.0), (5.0, 0.0), (1.0, 1e30), (1e28, 1e30), (1e-8, 1e22)])
+@pytest.mark.parametrize("cap,scale", [(1e-8, 0.0), (2e-7, 0.0), (1e-30, 0.0), (5.0, 0.0), (1.0, 1e30), (1e-8, 1e22)])
 def test_caps_that_dwarf_the_scores_and_products_of_zero(F, cap, scale, d):
     """A cap far below the scores (folded coefficients past the fp32 range), with blocks of hidden pairs on the
     diagonal, a head whose queries are zero and a document whose keys are."""
@@ -260,6 +260,63 @@ def test_caps_that_dwarf_the_scores_and_products_of_zero(F, cap, scale, d):
     p.q[:, 1] = 0
     p.k[140:204] = 0
     p.check()
+
+
+def forward_within(p, u):
+    """The forward of causal documents against the softmax of u(head, rows, queries, keys), where the scores are so
+    large that a row is its largest key's alone."""
+    import torch
+    out, lse = p.forward()
+    torch.cuda.synchronize()
+    assert p.att.device_status() == 0
+    base = 0
+    for n in p.lengths:
+        rows = slice(base, base + n)
+        base += n
+        for h in range(p.hq):
+            hk = h // (p.hq // p.hkv)
+            s = u(h, rows, f64(p.q[rows, h]) @ f64(p.k[rows, hk]).T)
+            s = np.where(np.tri(n, dtype=bool), s, -np.inf)
+            top, two = s.max(1), np.sort(s, 1)[:, -2] if n > 1 else np.full(n, -np.inf)
+            # decided whatever the roundings: (d + 8) 2^-24 of a product's terms, which add up to some 30 times it
+            sure = top - two > 2.0 ** -12 * np.abs(top) + 200
+            assert sure.mean() > 0.9
+            v = f64(p.v[rows, hk])[s.argmax(1)]
+            assert np.isfinite(f64(out[rows, h])).all()
+            assert (np.abs(f64(out[rows, h]) - v)[sure] <= 2.1 * 2.0 ** -8 * np.abs(v[sure])).all()
+            assert (np.abs(f64(lse[h, rows]) - top) <= 2.0 ** -12 * np.abs(top) + 64).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,scale", [(0.0, 1e30), (0.0, 1e10), (0.0, 1e7), (1e28, 1e30), (1e13, 1e10)])
+def test_scores_beyond_any_use(F, cap, scale, d):
+    """x - m is taken of rounded values: an exact product less a rounded maximum would reach 2^128."""
+    p = Problem(F, [300, 129, 1], 2, 1, d, seed=33, softcap=cap, scale=scale)
+    if cap == 1e28:
+        p.q[:, 1] = 0                          # folded coefficients past the range meet products of 0
+        p.forward()
+        assert np.isfinite(f64(p.att.out)).all()
+        p.q[:, 1] = p.q[:, 0]
+        p.q /= 8192                            # capped, but not all to the same
+    forward_within(p, lambda h, rows, x: cap * np.tanh(scale * x / cap) if cap else scale * x)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("slopes", [None, [0.5, 0.01]])
+@pytest.mark.parametrize("offset", [1e12, -1e12, -1e30, 1e30, 3e38])
+def test_a_bias_beyond_any_use(F, offset, slopes, d):
+    """Large scores under a bias that leaves them no digits: finite, and a mean of the document's values."""
+    import torch
+    p = Problem(F, [500, 1], 2, 1, d, seed=34, gain=40.0, buckets=(32, 64, False), slopes=slopes, pad=2)
+    p.table += offset
+    p.v.copy_(p.v.abs())
+    out, lse = p.forward()
+    torch.cuda.synchronize()
+    o, v = f64(out), f64(p.v)
+    assert np.isfinite(o).all() and (o[:500] <= 1.01 * v[:500].max(0)).all() and (o[:500] >= 0.99 * v[:500].min(0)).all()
+    limit = min(abs(offset), 2.0 ** 100)
+    assert (np.abs(np.abs(f64(lse)[:, :501]) - limit) <= 1e-6 * limit + 1e4).all()
+    assert np.array_equal(o[500], np.repeat(v[500], 2, 0))
 
 
 @pytest.mark.parametrize("d", [64, 128])
