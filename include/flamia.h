@@ -418,6 +418,8 @@ int flamia_scored_fwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
  *   distance is r (all documents).
  * dq: bf16 [T, hq, head_dim]; dk, dv: bf16 [T, hkv, head_dim]; drel_bias:
  * float [hq, 2 rel_max + 1], or NULL (not computed; needs rel_bias otherwise).
+ * A row whose LSE is 2^23 or more in magnitude contributes no gradient: in fp32
+ * such an LSE no longer says what its probabilities are.
  * Results do not depend on the order in which the GPU runs the call: equal
  * inputs give equal bits.  workspace: device scratch of
  * flamia_scored_bwd_workspace_bytes() bytes (rel_max = 0: a call without

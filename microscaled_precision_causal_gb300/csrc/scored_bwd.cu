@@ -30,6 +30,11 @@ constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
 constexpr int kRegCtl = 64, kRegCompute = 104;
 static_assert(kRegCtl * 128 + kRegCompute * kCompute <= kLaunchRegs * kThreads, "register split");
 
+// A row's LSE as the backward takes it.  P = exp(u - LSE) has the roundings of LSE and of u for its relative error;
+// from 2^23 on, where a step of LSE is 1, nothing of P is left (and far beyond, 2^x overflows): such a row gives
+// no gradient, as one that sees nothing.
+__device__ __forceinline__ float usable_lse(float l) { return fabsf(l) >= 0x1p23f ? INFINITY : l; }
+
 // One arrival for a warp, behind what all its lanes did.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e) {
           const int q = S.t * kTile + 32 * e + lane;
           const int64_t at = (int64_t)S.h * p.T + S.U.start + q;
-          l[e] = q < S.U.len ? p.lse[at] : INFINITY;
+          l[e] = q < S.U.len ? usable_lse(p.lse[at]) : INFINITY;
           d[e] = q < S.U.len ? p.dvec[at] : 0.f;
         }
         if (g >= kStats && !(ok = warp_wait(&st_empty[b], (g / kStats - 1) & 1, status))) break;
@@ -1031,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         a[4 * i + 2] = x.z;
         a[4 * i + 3] = x.w;
       }
-      nl = in ? -p.lse[(int64_t)S.h * p.T + tok] * kLog2e : -INFINITY;
+      nl = in ? -usable_lse(p.lse[(int64_t)S.h * p.T + tok]) * kLog2e : -INFINITY;
       dv = in ? p.dvec[(int64_t)S.h * p.T + tok] : 0.f;
       lo = p.win.left < 0 ? 0 : max(0, qi - p.win.left);
       hi = p.win.right < 0 ? S.len - 1 : min(S.len - 1, qi + p.win.right);

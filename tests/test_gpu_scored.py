@@ -317,6 +317,32 @@ def test_a_bias_beyond_any_use(F, offset, slopes, d):
     limit = min(abs(offset), 2.0 ** 100)
     assert (np.abs(np.abs(f64(lse)[:, :501]) - limit) <= 1e-6 * limit + 1e4).all()
     assert np.array_equal(o[500], np.repeat(v[500], 2, 0))
+    for t in p.backward(out, lse):                         # no LSE says what P was
+        assert (t == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+def test_rows_without_a_usable_lse_give_no_gradient(F, d, cap):
+    """A bias of -1e9 for the nearest keys, as masks are often written: a document's first rows see nothing else, and
+    the others weigh those keys 0.  The gradients are those of the other rows."""
+    import torch
+    p = Problem(F, [300, 3, 140], 4, 2, d, seed=35, softcap=cap, buckets=(8, 20, False))
+    p.table[:4, 1] = -1e9
+    out, lse = p.forward()
+    got = [f64(t) for t in p.backward(out, lse)]
+    few = np.concatenate([np.arange(n) < 4 for n in p.lengths])          # buckets 0 .. 3 are the distances 0 .. 3
+    assert np.array_equal(np.abs(f64(lse[1])) > 2.0 ** 23, few)
+    assert (np.abs(f64(lse[[0, 2, 3]])) < 1e4).all()
+    rel, _ = S.bucket_bias(f64(p.table), 20, False, 20)
+    rel = np.where(rel < -1e8, -np.inf, rel)                             # what it amounts to for every other row
+    keep = np.where(few, np.inf, f64(lse[1]))
+    ref_lse = f64(lse)
+    ref_lse[1] = keep
+    ref = S.run(f64(p.q), f64(p.k), f64(p.v), dout=f64(p.do), out=f64(out), lse=ref_lse, **dict(p.ref_kw, rel=rel))
+    for name, t in zip(("dq", "dk", "dv"), got):
+        within(name, t, ref[name], ref["tol_" + name])
+    assert (got[0][few][:, 1] == 0).all() and (got[3][:4, 1] == 0).all()
 
 
 @pytest.mark.parametrize("d", [64, 128])
