@@ -396,8 +396,8 @@ void flamia_default_score_options(flamia_score_options* opt);
 
 /* Forward.  q: bf16 [T, hq, head_dim]; k, v: bf16 [T, hkv, head_dim]; out: bf16
  * [T, hq, head_dim]; lse: float [hq, T] (natural log).  opt may be NULL
- * (defaults).  plan: any plan of the same cu_seqlens; one built for the call's
- * own window orders the work best.  Non-finite values of K or V reach the rows
+ * (defaults).  plan: any plan of the same cu_seqlens (the documents are read from
+ * it); one built for the call's own window orders the work best.  Non-finite values of K or V reach the rows
  * of their own document only, hidden or not: inside a document a hidden key
  * enters its tile's product with weight 0.  Rows behind the last document may
  * hold anything, and a document's results are the same bits whatever the call's

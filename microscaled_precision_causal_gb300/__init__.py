@@ -436,7 +436,11 @@ class FlamiaScoredAttention:
     the object's device: q [T, hq, d], k and v [T, hkv, d] bf16; cu_seqlens
     [N + 1] and prefix_lens [N] int32; slopes [hq] and table [buckets, hq] fp32.
     Anything else raises FlamiaError.  Calls run on `stream`, by default the
-    object's device's current stream."""
+    object's device's current stream.
+
+    The documents of a call are those of the last plan_build (which has to come
+    first): forward and backward take cu_seqlens as every call here does, but read
+    the plan."""
 
     def __init__(self, total_tokens: int, num_seqs: int, hq: int, hkv: int, head_dim: int, device="cuda",
                  causal: bool = True, window=(-1, -1), softcap: float = 0.0, buckets=None):
@@ -465,7 +469,9 @@ class FlamiaScoredAttention:
             self.rel_bias = torch.empty(hq, 2 * self.rel_max + 1, dtype=f32, device=dev)
             self.drel_bias = torch.empty_like(self.rel_bias)
             self.dtable = torch.empty(self.num_buckets, hq, dtype=f32, device=dev)
-        self.plan = torch.empty(flamia_plan_bytes(total_tokens, num_seqs), dtype=torch.uint8, device=dev)
+        # zeros: a plan without documents, should a captured plan_build not have been replayed yet
+        self.plan = torch.zeros(flamia_plan_bytes(total_tokens, num_seqs), dtype=torch.uint8, device=dev)
+        self._planned = False
         self.out = torch.empty(total_tokens, hq, head_dim, dtype=bf16, device=dev)
         self.lse = torch.empty(hq, total_tokens, dtype=f32, device=dev)
         self.dq = torch.empty_like(self.out)
@@ -521,6 +527,11 @@ class FlamiaScoredAttention:
         self._want("cu_seqlens", cu_seqlens, (self.N + 1,), torch.int32)
         self._run(lambda stm: flamia_plan_build_window(cu_seqlens, self.N, self.T, self.causal, self.window[0],
                                                        self.window[1], self.plan, stm), stream)
+        self._planned = True
+
+    def _need_plan(self):
+        if not self._planned:
+            raise FlamiaError("FlamiaScoredAttention: plan_build has not been called")
 
     def forward(self, q, k, v, cu_seqlens, softmax_scale: float = 0.0, slopes=None, prefix_lens=None, table=None,
                 stream=None):
@@ -529,6 +540,7 @@ class FlamiaScoredAttention:
         o = self._options(cu_seqlens, slopes, prefix_lens, table)
 
         def call(stm):
+            self._need_plan()
             if table is not None:
                 flamia_relbias_expand(table, self.max_distance, self.bidirectional, self.rel_bias, stm)
             flamia_scored_fwd(q, k, v, cu_seqlens, self.N, self.plan, self.out, self.lse, softmax_scale, o, self.causal,
@@ -548,6 +560,7 @@ class FlamiaScoredAttention:
         o = self._options(cu_seqlens, slopes, prefix_lens, table)
 
         def call(stm):
+            self._need_plan()
             if table is not None:
                 flamia_relbias_expand(table, self.max_distance, self.bidirectional, self.rel_bias, stm)
             flamia_scored_bwd(q, k, v, out, lse, dout, cu_seqlens, self.N, self.plan, self.dq, self.dk, self.dv,

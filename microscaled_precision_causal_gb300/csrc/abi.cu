@@ -164,13 +164,12 @@ int check_score_scale(float s, int d, const flamia_score_options* o) {
   return o && o->softcap > 0.f && (double)resolve_scale(s, d) / o->softcap > 1.2676506e30 ? FLAMIA_ERR_UNSUPPORTED : FLAMIA_OK;
 }
 
-ScoredParams scored_params(const void* q, const void* k, const void* v, const int32_t* cu, int N, int64_t T, int hq,
-                           int hkv, int d, int causal, float scale, const flamia_score_options* o, const void* plan) {
+ScoredParams scored_params(const void* q, const void* k, const void* v, int N, int64_t T, int hq, int hkv, int d,
+                           int causal, float scale, const flamia_score_options* o, const void* plan) {
   ScoredParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.v = static_cast<const __nv_bfloat16*>(v);
-  p.cu = cu;
   p.plan = static_cast<const int*>(plan);
   p.N = N;
   p.T = (int)T;
@@ -431,7 +430,7 @@ int flamia_scored_fwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
   if (!aligned16(q_bf16) || !aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(out_bf16) ||
       (reinterpret_cast<uintptr_t>(lse) & 3u))
     return FLAMIA_ERR_MISALIGNED;
-  ScoredParams p = scored_params(q_bf16, k_bf16, v_bf16, cu_seqlens, num_seqs, total_tokens, hq, hkv, head_dim, causal,
+  ScoredParams p = scored_params(q_bf16, k_bf16, v_bf16, num_seqs, total_tokens, hq, hkv, head_dim, causal,
                                  softmax_scale, opt, plan);
   p.out = static_cast<__nv_bfloat16*>(out_bf16);
   p.lse = lse;
@@ -467,7 +466,7 @@ int flamia_scored_bwd(const void* q_bf16, const void* k_bf16, const void* v_bf16
       !aligned16(dq_bf16) || !aligned16(dk_bf16) || !aligned16(dv_bf16) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return FLAMIA_ERR_MISALIGNED;
-  ScoredParams p = scored_params(q_bf16, k_bf16, v_bf16, cu_seqlens, num_seqs, total_tokens, hq, hkv, head_dim, causal,
+  ScoredParams p = scored_params(q_bf16, k_bf16, v_bf16, num_seqs, total_tokens, hq, hkv, head_dim, causal,
                                  softmax_scale, opt, plan);
   const ScoredBwdWorkspace w = scored_bwd_layout(total_tokens, num_seqs, hq, hkv, head_dim, drel_bias ? p.R : 0);
   if (workspace_bytes < w.total) return FLAMIA_ERR_WORKSPACE;

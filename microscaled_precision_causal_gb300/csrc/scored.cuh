@@ -20,7 +20,6 @@ struct CapForm {
 
 struct ScoredParams {
   const __nv_bfloat16 *q, *k, *v;
-  const int32_t* cu;
   const int* plan;
   const int32_t* prefix;     // [N] or null
   int N, T, hq, hkv;

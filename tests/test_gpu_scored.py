@@ -429,6 +429,25 @@ def test_no_tokens(F):
     Problem(F, [0, 0], 2, 1, 64, pad=5, softcap=3.0).check()
 
 
+def test_calls_before_the_plan(F):
+    """Refused before a launch; a plan whose building is captured but not replayed holds no documents."""
+    import torch
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype, device="cuda")
+    q, k, lse, cu = z(40, 2, 64), z(40, 1, 64), z(2, 40, dtype=torch.float32), dev([0, 30, 40], torch.int32)
+    att = F.FlamiaScoredAttention(40, 2, 2, 1, 64)
+    assert torch.count_nonzero(att.plan) == 0
+    for call in (lambda: att.forward(q, k, k, cu), lambda: att.backward(q, k, k, q, lse, q, cu)):
+        with pytest.raises(F.FlamiaError, match="plan_build"):
+            call()
+    att.plan_build(cu)
+    torch.cuda.synchronize()
+    att.plan.zero_()
+    out, lse = att.forward(q, k, k, cu)
+    got = att.backward(q, k, k, out, lse, q, cu)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and torch.isposinf(lse).all() and all((g == 0).all() for g in got)
+
+
 def test_bad_cu_seqlens(F):
     import torch
     p = Problem(F, [100, 28], 2, 1, 64, seed=18, softcap=3.0)
