@@ -449,7 +449,7 @@ class FlamiaScoredAttention:
             raise FlamiaError(f"FlamiaScoredAttention: sizes {(total_tokens, num_seqs, hq, hkv, head_dim)} are not supported")
         self.T, self.N, self.hq, self.hkv, self.d = total_tokens, num_seqs, hq, hkv, head_dim
         self.causal = 1 if causal else 0
-        self.window = (int(window[0]), int(window[1]))
+        self.window = tuple(max(-1, min(int(x), 2**31 - 1)) for x in window)     # (a bound of T or more is none)
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())

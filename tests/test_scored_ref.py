@@ -144,6 +144,15 @@ def test_bucket_refusals(F, nb, hq, md, both, R, table, want):
     assert F.lib().flamia_relbias_reduce(table, R, nb, hq, md, both, 256, None) == want
 
 
+@pytest.mark.parametrize("window,want", [((-1, -1), (-1, -1)), ((2**32 + 5, 2**31), (2**31 - 1, 2**31 - 1)), ((3, -7), (3, -1)),
+                                         ((-2**33, 0), (-1, 0))])
+def test_windows_past_32_bits(F, window, want):
+    """As bounds that no document reaches, or none: ctypes would keep the low 32 bits."""
+    pytest.importorskip("torch")
+    att = F.FlamiaScoredAttention(10, 1, 1, 1, 64, device="cpu", window=window)
+    assert (att.opts.window_left, att.opts.window_right) == want == att.window
+
+
 def test_object_refusals(F):
     """What FlamiaScoredAttention refuses, on CPU tensors: nothing is launched."""
     torch = pytest.importorskip("torch")
