@@ -265,16 +265,23 @@ def flamia_scored_bwd(q, k, v, out, lse, dout, cu_seqlens, num_seqs: int, plan, 
                                    _stream(stream)), "flamia_scored_bwd")
 
 
+def _rel_max(rel, table) -> int:
+    """The width 2 rel_max + 1 says how far the kernels go, in as many rows as the table has heads."""
+    if rel.dim() != 2 or table.dim() != 2 or rel.shape[1] % 2 == 0 or rel.shape[0] != table.shape[1]:
+        raise FlamiaError(f"relative bias: want [{table.shape[-1]}, 2 rel_max + 1], got {tuple(rel.shape)}")
+    return rel.shape[1] // 2
+
+
 def flamia_relbias_expand(table, max_distance: int, bidirectional: bool, rel_bias, stream=None):
     """table: float [buckets, hq]; rel_bias: float [hq, 2 rel_max + 1] (written)."""
     _check(lib().flamia_relbias_expand(_ptr(table), table.shape[0], table.shape[1], max_distance, int(bidirectional),
-                                       _ptr(rel_bias), rel_bias.shape[1] // 2, _stream(stream)),
+                                       _ptr(rel_bias), _rel_max(rel_bias, table), _stream(stream)),
            "flamia_relbias_expand")
 
 
 def flamia_relbias_reduce(drel_bias, max_distance: int, bidirectional: bool, dtable, stream=None):
     """drel_bias: float [hq, 2 rel_max + 1]; dtable: float [buckets, hq] (written)."""
-    _check(lib().flamia_relbias_reduce(_ptr(drel_bias), drel_bias.shape[1] // 2, dtable.shape[0], dtable.shape[1],
+    _check(lib().flamia_relbias_reduce(_ptr(drel_bias), _rel_max(drel_bias, dtable), dtable.shape[0], dtable.shape[1],
                                        max_distance, int(bidirectional), _ptr(dtable), _stream(stream)),
            "flamia_relbias_reduce")
 

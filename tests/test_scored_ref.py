@@ -153,6 +153,17 @@ def test_windows_past_32_bits(F, window, want):
     assert (att.opts.window_left, att.opts.window_right) == want == att.window
 
 
+@pytest.mark.parametrize("shape", [(4, 16), (3, 17), (5, 17), (68,), (1, 4, 17)])
+def test_relative_bias_shapes(F, shape):
+    """An even width would be written past its end, and so would too few rows."""
+    torch = pytest.importorskip("torch")
+    table, rel = torch.zeros(8, 4), torch.zeros(shape)
+    with pytest.raises(F.FlamiaError, match="rel_max"):
+        F.flamia_relbias_expand(table, 8, False, rel, stream=0)
+    with pytest.raises(F.FlamiaError, match="rel_max"):
+        F.flamia_relbias_reduce(rel, 8, False, table, stream=0)
+
+
 def test_object_refusals(F):
     """What FlamiaScoredAttention refuses, on CPU tensors: nothing is launched."""
     torch = pytest.importorskip("torch")
