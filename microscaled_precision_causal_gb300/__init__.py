@@ -443,7 +443,9 @@ class FlamiaScoredAttention:
     the object's device: q [T, hq, d], k and v [T, hkv, d] bf16; cu_seqlens
     [N + 1] and prefix_lens [N] int32; slopes [hq] and table [buckets, hq] fp32.
     Anything else raises FlamiaError.  Calls run on `stream`, by default the
-    object's device's current stream.
+    object's device's current stream.  Calls of one object share its bias table and
+    workspace, forwards too: calls on two streams have to be ordered by the caller
+    (an object each lets them overlap).
 
     The documents of a call are those of the last plan_build (which has to come
     first): forward and backward take cu_seqlens as every call here does, but read
