@@ -504,6 +504,34 @@ def test_bits_do_not_depend_on_when_a_load_lands(F, form, d):
     assert p.att.device_status() == 0
 
 
+# Each with more units than SMs, several per CTA, and documents longer than the rings of tiles: what one unit or
+# head leaves behind for the next (tables, sums, tensor memory, barriers' phases).
+UNITS = {
+    "slopes_128": dict(hq=8, hkv=8, d=128, slopes=True),
+    "plain_128": dict(hq=8, hkv=8, d=128),
+    "plain_64": dict(hq=8, hkv=8, d=64),
+    "cap_64": dict(hq=8, hkv=8, d=64, softcap=12.0),
+    "slopes_noncausal_128": dict(hq=6, hkv=6, d=128, slopes=True, causal=False),
+    "buckets_128": dict(hq=12, hkv=12, d=128, buckets=(16, 90, False)),
+    "buckets_shared_128": dict(hq=16, hkv=8, d=128, buckets=(16, 90, False)),
+    "buckets_shared_64": dict(hq=16, hkv=8, d=64, buckets=(16, 200, True), causal=False),
+    "all_shared_128": dict(hq=16, hkv=8, d=128, softcap=9.0, slopes=True, buckets=(16, 90, False), window=(300, -1),
+                           prefix=[100, 0, 650, 7, 33, 129, 1]),
+    "all_shared_64": dict(hq=16, hkv=8, d=64, softcap=9.0, slopes=True, buckets=(16, 200, True), causal=False,
+                          prefix=[100, 0, 650, 7, 33, 129, 1]),
+}
+
+
+@pytest.mark.parametrize("form", UNITS)
+def test_many_units_against_the_definition(F, form):
+    kw = dict(UNITS[form])
+    lengths = [1300, 700, 900, 129, 513, 1100, 650]
+    if kw["hq"] > kw["hkv"]:                               # enough of them that query heads share a dK/dV unit
+        lengths, kw["prefix"] = lengths + [830, 470, 600, 700, 500], kw["prefix"] + [0, 300, 2, 700, 0] if "prefix" in kw else None
+        assert (sum(lengths) // 128 + len(lengths) + 1) * kw["hkv"] >= 608
+    Problem(F, lengths, pad=6, seed=43, **kw).check()
+
+
 def test_any_plan_of_the_same_documents(F):
     p = Problem(F, [700, 333], 2, 1, 64, seed=22, window=(200, -1), softcap=20.0)
     want = run_all(p)
