@@ -169,8 +169,8 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, u
 // query tile of one of the unit's query heads.  S^T = K Q^T and dP^T = V dO^T have keys in the
 // TMEM lanes, so P^T and dS^T are written back over their own columns and are the A operands
 // of dV += P^T dO and dK += dS^T Q.  A warp issues the chain of S^T and dV, another that of
-// dP^T and dK, so that neither waits for the other's operands; each waits by itself for every
-// tile that its products read, as nothing that the other waited for stands before them.  K is free for the next unit
+// dP^T and dK, so that neither waits for the other's operands; nothing that one has waited for
+// stands before the other's products.  K is free for the next unit
 // once the unit's last S^T is done, V once its last dP^T is.
 //
 // LSE and D vary along a thread's columns, so every warp would read both of every query from
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kA = kP ? L::kK : L::kV, kB = kP ? L::kQ : L::kDO, kB2 = kP ? L::kDO : L::kQ;
         constexpr uint32_t kT = kP ? kTS : kTP, kSum = kP ? kTV : kTK;
         uint64_t *a_full = kP ? k_full : v_full, *a_empty = kP ? k_empty : v_empty;
-        uint64_t *b_full = kP ? q_full : do_full, *b2_full = kP ? do_full : q_full, *b2_empty = kP ? do_empty : q_empty;
+        uint64_t *b_full = kP ? q_full : do_full, *b2_empty = kP ? do_empty : q_empty;
         uint64_t *out = kP ? s_full : dp_full, *in = kP ? p_ready : ds_ready;
         // of step g, both operands K-major.  A (K or V): a_full at the unit's first step; B (Q or dO): b_full
         auto scores = [&](int half, uint32_t g, int unit, bool first, bool last) {
@@ -442,12 +442,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit(&out[kP ? s_at(half, g) : half]);
             if (half == kHalves - 1 && last) mma_commit(a_empty);
           }
+          if (kP && kFold) ok = warp_wait(&do_full[b], (g / kStages) & 1, status);      // for this step's dV
         };
-        // A from TMEM (P^T or dS^T): in; B over its rows (dO or Q): b2_full.  `in` covers the query rows of a
-        // dK product, whose S^T was computed from them, but not the dO of a dV product: its load is asked for
-        // last, and P^T needs Q and K alone
+        // A from TMEM (P^T or dS^T): in; B over its rows: dK's Q by `in` too, as dS^T came from an S^T that had
+        // read it.  dV's dO not, as P^T needs Q and K alone and the producer asks for dO last: by a wait of its own,
+        // which takes 100 cycles of whoever makes it.  Not folded, the warp that stages D makes it, and `in` covers
+        // dO with D: 5990 us on four documents of 8192, 32 heads on 8, slopes, 6060 to 6130 with the wait behind the
+        // scores above, 6100 here.  Folded, S^T itself would wait for dO (2257 us on the noncausal case): the
+        // wait is behind the scores, 2230
         auto product = [&](int half, uint32_t g, bool first) {
-          if (!(ok = warp_wait(&b2_full[half * kStages + g % kStages], (g / kStages) & 1, status))) return;
           if (!(ok = warp_wait(&in[kP ? s_at(half, g) : half], kP ? s_phase(g) : g & 1, status))) return;
           tc_fence_after();
           const uint32_t b16 = base16 + g % kStages * (L::kPartBytes / 16);
@@ -525,6 +528,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(x[0] | x[1] << 16, x[2] | y[0] << 16, y[1] | y[2] << 16, 0);
         }
         if (kFold) fence_proxy_async_smem();
+        if (!kFold) {            // for this step's dV: no P^T is computed without D
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half)
+            if (ok) ok = warp_wait(&do_full[half * kStages + g % kStages], (g / kStages) & 1, status);
+          if (!ok) break;
+        }
         warp_arrive(&st_full[b]);
       }
     }
