@@ -98,7 +98,7 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, __nv_bfloat16* dst, fl
 #pragma unroll 1
   for (int c = 0; c < COLS / 32; ++c) {
     uint32_t o[32];
-    __syncwarp();
+    if (c) __syncwarp();
     tmem_ld32(taddr + 32 * c, o);
     tmem_ld_wait();
     uint32_t w[16];
@@ -121,7 +121,7 @@ __device__ __forceinline__ void store_part(uint32_t taddr, float* dst, bool vali
 #pragma unroll 1
   for (int c = 0; c < COLS / 32; ++c) {
     uint32_t o[32];
-    __syncwarp();
+    if (c) __syncwarp();
     tmem_ld32(taddr + 32 * c, o);
     tmem_ld_wait();
     if (valid) {                 // (the workspace's rows are whole sectors)
