@@ -70,11 +70,14 @@ inline ScoredBwdWorkspace scored_bwd_layout(int64_t T, int N, int hq, int hkv, i
   return w;
 }
 
-// The tensor core truncates as it accumulates, so a product of D terms comes out too small
-// by a part that does not depend on its size: measured on 65,536 rows of normal values
-// -9.9e-8 of the product at D = 128 (eight steps of 16 terms) and -5.5e-8 at D = 64, beside
-// a spread of 7e-8.  The score scale takes the mean back; it would enter every probability
-// with the score's own size as a factor.
+// The tensor core truncates as it accumulates, so a product of D terms comes out too small:
+// on 65,536 rows of normal values by 9.9e-8 of the product at D = 128 (eight steps of 16 terms)
+// and 5.5e-8 at D = 64 on average, beside a spread of 7e-8.  The score scale takes the mean back;
+// it would enter every probability with the score's own size as a factor.  How much a product
+// loses depends on its terms.  LSE's rms error over 2048 causal rows with it / without, 1e-7, D = 64
+// and 128: normal values 4.3 / 5.7, 4.4 / 6.6; positive 6.1 / 8.8, 8.0 / 15; of mean 1 7.0 / 11,
+// 7.8 / 18; one term alone 4.3 / 4.4, 4.2 / 4.3; uniform 4.2 / 4.3, 4.1 / 4.4; heavy tails 5.7 / 8.4,
+// 5.8 / 9.3; small whole numbers, whose sums lose nothing, 6.5 / 6.3, 6.9 / 5.2.
 inline double mma_gain(int D) { return D == 128 ? 1.0 + 9.9e-8 : 1.0 + 5.5e-8; }
 
 constexpr float kLog2e = 1.4426950408889634f;

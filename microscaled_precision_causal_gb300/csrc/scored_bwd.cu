@@ -92,7 +92,7 @@ __device__ __forceinline__ uint32_t pack2(float2 x) {
 // One row of fp32 accumulators (columns c0 ..) -> bf16 in global memory, times f.  A warp's rows
 // lie apart, so a store moves a sector of 32 bytes per lane where the rows allow it (wide): half as
 // many as with 16 bytes, and the store path is what this waits for.  Where a document ends inside the
-// warp only some lanes store; the loads from tensor memory are the whole warp's, so it meets first.
+// warp only some lanes store; the loads from tensor memory are the whole warp's, so it meets before the next.
 template <int COLS>
 __device__ __forceinline__ void store_acc(uint32_t taddr, __nv_bfloat16* dst, float f, bool valid, bool wide) {
 #pragma unroll 1
@@ -170,8 +170,8 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, u
 // TMEM lanes, so P^T and dS^T are written back over their own columns and are the A operands
 // of dV += P^T dO and dK += dS^T Q.  A warp issues the chain of S^T and dV, another that of
 // dP^T and dK, so that neither waits for the other's operands; nothing that one has waited for
-// stands before the other's products.  K is free for the next unit
-// once the unit's last S^T is done, V once its last dP^T is.
+// stands before the other's products.  K is free for the next unit once the unit's last S^T is
+// done, V once its last dP^T is.
 //
 // LSE and D vary along a thread's columns, so every warp would read both of every query from
 // shared memory: 4 quarters of keys x 128 queries x 2, at the one value a cycle that a broadcast
@@ -182,17 +182,17 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, u
 // comes after the cap, and stays in shared memory.
 //
 // D = 64 leaves room for a second S^T (kSBuf): the next one runs while this P^T is computed.
-// Two noncausal documents of 8192, 16 heads, buckets, all three launches: 2.70 ms with halves as
-// below, 2.39 folded and whole, 2.22 with the second S^T.
+// Two noncausal documents of 8192, 16 heads, buckets, all three launches: 2.25 ms with one S^T, 2.11
+// with two.
 //
 // At D = 128 tensor memory is full, and a step's queries go in two halves, each with its own
 // 64-query tiles, products and warps, half a step apart: while one half's P^T is computed the
-// other's dS^T is.  (Whole, folded or not, all warps wait for the same product: 6.1 instead of 5.8
+// other's dS^T is.  (Whole and folded, all warps wait for the same product: 6.03 instead of 5.86
 // ms on four documents of 8192, 32 heads on 8, slopes.)  A product with 64 columns reads more
 // shared memory than it multiplies (48 cycles instead of 32 a step of 16), and the fold would
-// cost two more of them for nothing (6.0 ms).  Where drel is wanted the warps meet at barriers on
-// every tile near the diagonal anyway: whole and folded, 0.657 instead of 0.700 ms (packed
-// documents, 16384 rows, 16 heads).
+// cost two more of them for nothing (3% more).  Where drel is wanted the warps meet at barriers on
+// every tile near the diagonal anyway: whole and folded, 6% less (packed documents, 16384 rows,
+// 16 heads).  (The last two were measured before dV waited for its dO.)
 // Roles: warp 0 TMA, warps 1 and 2 MMA (2 also TMEM), warp 3 stages LSE and D of a step's queries,
 // warps 4-19 compute: thread = key row, warpgroup = 32 of the 128 query columns.
 // TMEM columns: dV [0, D), dK [D, 2 D), S^T [256, 384) (D = 64: [128, 384)), dP^T [384, 512).
@@ -796,10 +796,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // halves what these products read from it.  dS goes over dP's columns and is the A operand
 // of dQ += dS K.  The thread's row keeps its LSE and D in registers.
 // What bounds a step is the chain dS -> dQ -> dP -> dS, as the next S runs while P is computed.
-// At D = 64 there is room for a second dP (kPBuf), and the chain is cut: 2.22 -> 2.18 ms on
-// the noncausal case above, 2.13 with S on an issuing warp of its own.  At D = 128 a step goes in
-// two halves of 64 keys as above, which costs the products nothing here (A comes from tensor
-// memory: 33 cycles a step of 16 for half the columns): 5.65 -> 5.44 ms on the slopes case above.
+// At D = 64 there is room for a second dP (kPBuf), which cuts the chain, and S has an issuing warp of
+// its own: 2% each on the noncausal case above when they came (now, with that warp, 2.08 ms with
+// one dP and 2.11 with two).  At D = 128 a step goes in two halves of 64 keys as above, which
+// costs the products nothing here (A comes from tensor memory: 33 cycles a step of 16 for half the
+// columns): 5.90 -> 5.86 ms on the slopes case above, 622 -> 608 us on packed buckets.
 // A cap makes the arithmetic longer than the chain, and its warps agree on the polynomial by
 // votes: whole, 0.428 instead of 0.447 ms (odd prefix documents, 8 heads on 2).
 // Roles: warp 0 TMA, warp 1 issues S, warp 2 dP and dQ, warps 4-19 compute as above.
