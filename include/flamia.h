@@ -397,12 +397,12 @@ void flamia_default_score_options(flamia_score_options* opt);
 /* Forward.  q: bf16 [T, hq, head_dim]; k, v: bf16 [T, hkv, head_dim]; out: bf16
  * [T, hq, head_dim]; lse: float [hq, T] (natural log).  opt may be NULL
  * (defaults).  plan: any plan of the same cu_seqlens (the documents are read from
- * it); one built for the call's own window orders the work best.  Non-finite values of K or V reach the rows
- * of their own document only, hidden or not: inside a document a hidden key
- * enters its tile's product with weight 0.  Rows behind the last document may
- * hold anything, and a document's results are the same bits whatever the call's
- * other documents are.  Calls on one plan may overlap on the GPU.  With
- * total_tokens = 0 the tensors may be NULL. */
+ * it); one built for the call's own window orders the work best.  Non-finite
+ * values of K or V reach the rows of their own document only, hidden or not:
+ * inside a document a hidden key enters its tile's product with weight 0.  Rows
+ * behind the last document may hold anything, and a document's results are the
+ * same bits whatever the call's other documents are.  Calls on one plan may
+ * overlap on the GPU.  With total_tokens = 0 the tensors may be NULL. */
 int flamia_scored_fwd(const void* q_bf16, const void* k_bf16, const void* v_bf16, const int32_t* cu_seqlens,
                       int num_seqs, int64_t total_tokens, int hq, int hkv, int head_dim, int causal,
                       float softmax_scale, const flamia_score_options* opt, const void* plan, void* out_bf16,
