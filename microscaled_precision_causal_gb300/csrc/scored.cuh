@@ -316,13 +316,14 @@ __device__ __forceinline__ void bias_chunk(uint32_t (&v)[32], int c0, float scal
 constexpr int kBiasReach = 2 * kTile - 1;
 constexpr int kBiasHead = 2 * (FLAMIA_REL_MAX + kBiasReach) + 2;  // behind the table: the head's constants
 constexpr int kBiasTab = kBiasHead + 4;                            // floats, an even number
+// (Comparisons that a NaN fails: it stays one, and shows in the outputs.)
 __device__ __forceinline__ float bias_base2(float b) {
-  return b < kHideBelow ? -INFINITY : fminf(b, -kHideBelow) * kLog2e;
+  return b < kHideBelow ? -INFINITY : (b > -kHideBelow ? -kHideBelow : b) * kLog2e;
 }
 // A slope steeper than 2^100 counts as 2^100 (times the longest distance it stays in the fp32 range); in
 // the products' units it is held to 2^119, whose multiple by a column is finite too.  (At that steepness a
 // step of distance outweighs any score, so that only the nearest or the farthest visible key counts.)
-__device__ __forceinline__ float slope_base2(float s) { return fminf(fmaxf(s, kHideBelow), -kHideBelow) * kLog2e; }
+__device__ __forceinline__ float slope_base2(float s) { return (fabsf(s) > -kHideBelow ? copysignf(-kHideBelow, s) : s) * kLog2e; }
 __device__ __forceinline__ float slope_products(float slope2, float scale2) {
   return fminf(fmaxf(slope2 / scale2, -0x1p119f), 0x1p119f);
 }

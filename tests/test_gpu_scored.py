@@ -237,6 +237,29 @@ def test_buckets_at_their_borders(F, nb, md, both):
     assert np.array_equal(f64(dtable), np.stack([n, 3 * n, 0 * n], 1))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", ["table", "slopes"])
+def test_nan_parameters_show(F, what, d):
+    """A NaN in a head's table or slope is not a number that counts: its rows are NaN, other heads keep their bits."""
+    import torch
+    p = Problem(F, [200, 140], 4, 4, d, seed=36, buckets=(8, 20, False), slopes=True)
+    out, lse = (t.clone() for t in p.forward())
+    want = [t.clone() for t in p.backward(out, lse)]
+    if what == "table":
+        p.table[5, 1] = float("nan")                       # distances 6 to 8
+    else:
+        p.slopes[1] = float("nan")
+    far = np.concatenate([np.arange(n) >= 8 for n in (200, 140)])
+    o, l = p.forward()
+    got = p.backward(o, l)
+    torch.cuda.synchronize()
+    assert p.att.device_status() == 0
+    assert np.isnan(f64(o)[far, 1]).all() and np.isnan(f64(l)[1, far]).all() and np.isnan(f64(got[0])[far, 1]).all()
+    others = [0, 2, 3]
+    assert torch.equal(o[:, others], out[:, others]) and torch.equal(l[others], lse[others])
+    assert all(torch.equal(a[:, others], b[:, others]) for a, b in zip(got, want))
+
+
 def test_largest_relative_range(F):
     Problem(F, [2300], 1, 1, 64, seed=14, buckets=(64, 1024, True), causal=False).check()
 
