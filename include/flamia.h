@@ -52,7 +52,10 @@ extern "C" {
 /* device status bits (plan status word) */
 #define FLAMIA_DEV_BAD_CU_SEQLENS 1   /* cu[0] != 0, decreasing, or cu[N] > total_tokens */
 #define FLAMIA_DEV_TIMEOUT 2          /* a bounded mbarrier wait expired; outputs invalid */
-#define FLAMIA_DEV_CAPACITY 4         /* more work items than the plan was sized for */
+#define FLAMIA_DEV_CAPACITY 4         /* more work items than the plan was sized for, or a chunk above max_chunk */
+#define FLAMIA_DEV_BAD_KV_LENS 8      /* kv_lens[n] below the sequence's new tokens or above max_keys */
+#define FLAMIA_DEV_BAD_PAGE 16        /* a page number outside the cache, or a position behind the page table */
+#define FLAMIA_DEV_PLAN_MISMATCH 32   /* a cache plan built for other sizes than the call's */
 
 /* ----------------------------------------------------------- options */
 typedef struct flamia_options {
@@ -456,6 +459,87 @@ int flamia_relbias_expand(const float* table, int num_buckets, int hq, int max_d
                           float* rel_bias, int rel_max, void* stream);
 int flamia_relbias_reduce(const float* drel_bias, int rel_max, int num_buckets, int hq, int max_distance,
                           int bidirectional, float* dtable, void* stream);
+
+/* ----------------------------------------------------------- paged key/value cache
+ * For generating with a model: the keys and values of earlier tokens, kept in
+ * pages.  Pools are [num_pages, hkv, page_size, head_dim]; position j of
+ * sequence n lives in page page_table[n][j / page_size], slot j % page_size
+ * (page_table: device int32 [num_seqs, max_pages]).  Two forms:
+ *   FLAMIA_CACHE_E4M3  E4M3 codes and one UE8M0 scale byte per token and head
+ *     (scales: uint8 [num_pages, hkv, page_size]), the per-token form of
+ *     flamia_quantize_tokenblock: e = least integer with amax <= 448 2^e (0 for
+ *     a row of zeros, clamped to [-127, 127]), byte e + 127, codes E4M3(x 2^-e)
+ *     rounded to nearest even.  A later token changes no earlier one's code.  A
+ *     row that holds a NaN gets byte 255 and reads as NaN; infinities read as
+ *     infinities (the row's finite values as 0, or as the multiples of 2^111
+ *     that are left).  Codes 0x7f and 0xff are not
+ *     written and not expected.
+ *   FLAMIA_CACHE_BF16  the values as they are.
+ *
+ * A call serves sequences that each bring c_n = cu_seqlens[n + 1] -
+ * cu_seqlens[n] new tokens (packed as documents are; c_n may be 0) and have
+ * kv_lens[n] keys with them: new token t stands at position kv_lens[n] - c_n +
+ * t.  flamia_cache_plan_build checks that on the device and lists the work; one
+ * plan serves all layers of a step, and its calls read cu_seqlens and kv_lens
+ * from it.  Where either is bad the plan's status word says so and the calls
+ * write nothing to the cache, read zeros, and give O 0 and LSE +inf.  A page
+ * number outside the cache sets FLAMIA_DEV_BAD_PAGE: such a token is not
+ * written and reads as zeros, and the attention rows of its sequence are
+ * unspecified; nothing outside the pools is touched.  Entries behind a
+ * sequence's last position are not looked at, and what a page holds behind it
+ * has no effect.  flamia_get_device_status reads the plan's status word.
+ *
+ * hq query heads share hkv heads as everywhere; max_chunk: no sequence brings
+ * more new tokens than that (at least 1); max_keys: max_pages * page_size of the
+ * call's table; window_left: as in flamia_options (the right bound is 0).  The
+ * attention's calls take the plan's own hq, max_chunk and window_left.
+ * page_size: 16, 32, 64 or 128; max_pages * page_size <= 2^30. */
+#define FLAMIA_CACHE_BF16 0
+#define FLAMIA_CACHE_E4M3 1
+typedef struct flamia_kv_cache {
+  void* k;            /* uint8 or bf16 [num_pages, hkv, page_size, head_dim], 16-byte aligned */
+  void* v;
+  void* k_scales;     /* uint8 [num_pages, hkv, page_size], 16-byte aligned; E4M3 only */
+  void* v_scales;
+  int num_pages;
+  int page_size;
+  int hkv;
+  int head_dim;       /* 64 or 128 */
+  int format;
+} flamia_kv_cache;
+
+size_t flamia_cache_plan_bytes(int64_t total_tokens, int num_seqs, int hq, int hkv);
+int flamia_cache_plan_build(const int32_t* cu_seqlens, const int32_t* kv_lens, int num_seqs, int64_t total_tokens,
+                            int hq, int hkv, int max_chunk, int64_t max_keys, int window_left, void* plan,
+                            size_t plan_bytes, void* stream);
+
+/* The new tokens' k and v (bf16 [T, hkv, head_dim]) into their places.  Two
+ * sequences of a call must not own the same slot of a page. */
+int flamia_cache_write(const flamia_kv_cache* cache, const int32_t* page_table, int max_pages, int num_seqs,
+                       int64_t total_tokens, const void* plan, const void* k_bf16, const void* v_bf16, void* stream);
+/* The same places read back as bf16 [T, hkv, head_dim] (the code times its
+ * scale, rounded to nearest), rows behind the last sequence 0.  A sequence whose
+ * kv_lens[n] is its c_n is read whole. */
+int flamia_cache_read(const flamia_kv_cache* cache, const int32_t* page_table, int max_pages, int num_seqs,
+                      int64_t total_tokens, const void* plan, void* k_bf16, void* v_bf16, void* stream);
+
+/* Attention of the new tokens over their sequences' keys in the cache, their own
+ * among them (written before): with s = softmax_scale q_i . k_j and t = softcap
+ * tanh(s / softcap) (softcap 0: t = s), position i sees key j iff
+ * i - window_left <= j <= i,
+ *   O_i = sum_j exp(t_ij - LSE_i) v_j,  LSE_i = ln sum_j exp(t_ij).
+ * q: bf16 [T, hq, head_dim]; out: bf16 [T, hq, head_dim]; lse: float [hq, T].
+ * Rows behind the last sequence: O 0, LSE +inf.  softcap and softmax_scale as in
+ * flamia_score_options and flamia_scored_fwd.  workspace: device scratch of
+ * flamia_cached_fwd_workspace_bytes() bytes, 256-byte aligned, its contents
+ * unspecified before and after; calls that overlap on the GPU need one each.
+ * Equal inputs give equal bits.  A non-finite key or value shows in rows of its
+ * own sequence only, hidden or not. */
+size_t flamia_cached_fwd_workspace_bytes(int hq, int hkv, int head_dim, int max_chunk);
+int flamia_cached_fwd(const void* q_bf16, const flamia_kv_cache* cache, const int32_t* page_table, int max_pages,
+                      int num_seqs, int64_t total_tokens, int hq, int max_chunk, int window_left, float softcap,
+                      float softmax_scale, const void* plan, void* out_bf16, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* ----------------------------------------------------------- status */
 /* Copy the plan's device status word into *status_out (synchronises `stream`). */

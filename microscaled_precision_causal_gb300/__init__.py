@@ -13,6 +13,9 @@ training call (quantize Q/K/V, forward, backward).  ``flamia_scored_fwd``,
 ``flamia_scored_bwd``, ``flamia_relbias_expand`` and ``flamia_relbias_reduce``
 are the bf16 attention calls with changed scores (tanh cap, distance bias,
 bucketed relative bias, prefix); ``FlamiaScoredAttention`` strings those.
+``flamia_cache_plan_build``, ``flamia_cache_write``, ``flamia_cache_read`` and
+``flamia_cached_fwd`` keep keys and values in pages (E4M3 or bf16) and attend to
+them; ``FlamiaPagedCache`` holds the pages, ``FlamiaCachedAttention`` a step's calls.
 """
 from __future__ import annotations
 
@@ -26,6 +29,7 @@ LIB_PATH = os.path.join(HERE, "libflamia.so")
 FLAMIA_OK = 0
 STATUS_NAMES = {0: "ok", -1: "invalid argument", -2: "unsupported", -3: "misaligned", -4: "workspace", -5: "cuda"}
 DEV_BAD_CU_SEQLENS, DEV_TIMEOUT, DEV_CAPACITY = 1, 2, 4
+DEV_BAD_KV_LENS, DEV_BAD_PAGE, DEV_PLAN_MISMATCH = 8, 16, 32
 
 EXPORTED = (
     "flamia_default_options", "flamia_plan_bytes", "flamia_plan_build", "flamia_quantize_tokenblock",
@@ -33,9 +37,13 @@ EXPORTED = (
     "flamia_status_string", "flamia_bwd_static_scratch", "flamia_quantize_nvfp4", "flamia_plan_build_window",
     "flamia_quantize_hadamard", "flamia_quantize_qkv", "flamia_default_score_options", "flamia_scored_fwd",
     "flamia_scored_bwd_workspace_bytes", "flamia_scored_bwd", "flamia_relbias_expand", "flamia_relbias_reduce",
+    "flamia_cache_plan_bytes", "flamia_cache_plan_build", "flamia_cache_write", "flamia_cache_read",
+    "flamia_cached_fwd_workspace_bytes", "flamia_cached_fwd",
 )
 STATIC_SCRATCH_BYTES = 64 << 20
 REL_MAX = 1024
+CACHE_FORMATS = {"bf16": 0, "e4m3": 1}
+PAGE_SIZES = (16, 32, 64, 128)
 
 
 class FlamiaError(RuntimeError):
@@ -69,6 +77,11 @@ class ScoreOptions(ctypes.Structure):
                 ("window_right", ctypes.c_int)]
 
 
+class KVCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scales", "v_scales")] + [
+        (n, ctypes.c_int) for n in ("num_pages", "page_size", "hkv", "head_dim", "format")]
+
+
 _lib = None
 
 
@@ -85,6 +98,7 @@ def lib():
     qp = ctypes.POINTER(QTensor)
     sp = ctypes.POINTER(ScoreOptions)
     op = ctypes.POINTER(Options)
+    cp = ctypes.POINTER(KVCache)
     sig = {
         "flamia_default_options": (None, [op]),
         "flamia_plan_bytes": (sz, [i64, i32]),
@@ -110,6 +124,12 @@ def lib():
                                     vp, vp, sz, vp]),
         "flamia_relbias_expand": (i32, [vp, i32, i32, i32, i32, vp, i32, vp]),
         "flamia_relbias_reduce": (i32, [vp, i32, i32, i32, i32, i32, vp, vp]),
+        "flamia_cache_plan_bytes": (sz, [i64, i32, i32, i32]),
+        "flamia_cache_plan_build": (i32, [vp, vp, i32, i64, i32, i32, i32, i64, i32, vp, sz, vp]),
+        "flamia_cache_write": (i32, [cp, vp, i32, i32, i64, vp, vp, vp, vp]),
+        "flamia_cache_read": (i32, [cp, vp, i32, i32, i64, vp, vp, vp, vp]),
+        "flamia_cached_fwd_workspace_bytes": (sz, [i32, i32, i32, i32]),
+        "flamia_cached_fwd": (i32, [vp, cp, vp, i32, i32, i64, i32, i32, i32, f32, f32, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -284,6 +304,40 @@ def flamia_relbias_reduce(drel_bias, max_distance: int, bidirectional: bool, dta
     _check(lib().flamia_relbias_reduce(_ptr(drel_bias), _rel_max(drel_bias, dtable), dtable.shape[0], dtable.shape[1],
                                        max_distance, int(bidirectional), _ptr(dtable), _stream(stream)),
            "flamia_relbias_reduce")
+
+
+def flamia_cache_plan_bytes(total_tokens: int, num_seqs: int, hq: int, hkv: int) -> int:
+    return int(lib().flamia_cache_plan_bytes(total_tokens, num_seqs, hq, hkv))
+
+
+def flamia_cache_plan_build(cu_seqlens, kv_lens, num_seqs: int, total_tokens: int, hq: int, hkv: int, max_chunk: int,
+                            max_keys: int, window_left: int, plan, stream=None):
+    _check(lib().flamia_cache_plan_build(_ptr(cu_seqlens), _ptr(kv_lens), num_seqs, total_tokens, hq, hkv, max_chunk,
+                                         max_keys, window_left, _ptr(plan), plan.numel() * plan.element_size(),
+                                         _stream(stream)), "flamia_cache_plan_build")
+
+
+def flamia_cache_write(cache: KVCache, page_table, num_seqs: int, plan, k, v, stream=None):
+    _check(lib().flamia_cache_write(ctypes.byref(cache), _ptr(page_table), page_table.shape[1], num_seqs, k.shape[0],
+                                    _ptr(plan), _ptr(k), _ptr(v), _stream(stream)), "flamia_cache_write")
+
+
+def flamia_cache_read(cache: KVCache, page_table, num_seqs: int, plan, k, v, stream=None):
+    """k and v: bf16 [T, hkv, head_dim] (written)."""
+    _check(lib().flamia_cache_read(ctypes.byref(cache), _ptr(page_table), page_table.shape[1], num_seqs, k.shape[0],
+                                   _ptr(plan), _ptr(k), _ptr(v), _stream(stream)), "flamia_cache_read")
+
+
+def flamia_cached_fwd_workspace_bytes(hq: int, hkv: int, head_dim: int, max_chunk: int) -> int:
+    return int(lib().flamia_cached_fwd_workspace_bytes(hq, hkv, head_dim, max_chunk))
+
+
+def flamia_cached_fwd(q, cache: KVCache, page_table, num_seqs: int, plan, out, lse, workspace, max_chunk: int,
+                      window_left: int = -1, softcap: float = 0.0, softmax_scale: float = 0.0, stream=None):
+    _check(lib().flamia_cached_fwd(_ptr(q), ctypes.byref(cache), _ptr(page_table), page_table.shape[1], num_seqs, q.shape[0],
+                                   q.shape[1], max_chunk, window_left, softcap, softmax_scale, _ptr(plan), _ptr(out),
+                                   _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                   _stream(stream)), "flamia_cached_fwd")
 
 
 def flamia_get_device_status(plan, stream=None) -> int:
@@ -522,7 +576,7 @@ class FlamiaScoredAttention:
         """call(stream handle) with the object's device current, on `stream` or its current stream."""
         import torch
         if self.device.type != "cuda":
-            raise FlamiaError(f"FlamiaScoredAttention runs on a CUDA device, not on {self.device}")
+            raise FlamiaError(f"{type(self).__name__} runs on a CUDA device, not on {self.device}")
         index = self.device.index
         if torch._C._cuda_getDevice() != index:
             with torch.cuda.device(self.device):
@@ -580,6 +634,142 @@ class FlamiaScoredAttention:
             flamia_relbias_reduce(self.drel_bias, self.max_distance, self.bidirectional, self.dtable, stm)
             return self.dq, self.dk, self.dv, self.dtable
         return self._run(call, stream)
+
+    def device_status(self, stream=None) -> int:
+        return self._run(lambda stm: flamia_get_device_status(self.plan, stm), stream)
+
+
+# ---------------------------------------------------------------- generation
+
+def _cuda_device(device):
+    import torch
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+class FlamiaPagedCache:
+    """The pages of one layer's keys and values.
+
+    k and v are [num_pages, hkv, page_size, head_dim], uint8 E4M3 codes with
+    k_scales and v_scales [num_pages, hkv, page_size] (uint8 UE8M0 exponents, one
+    a token and head) for fmt "e4m3", bf16 and no scales for "bf16".  They start
+    as zeros.  Which page holds which positions is the caller's page table."""
+
+    def __init__(self, num_pages: int, page_size: int, hkv: int, head_dim: int, fmt: str = "e4m3", device="cuda"):
+        import torch
+        if num_pages < 1 or page_size not in PAGE_SIZES or hkv < 1 or head_dim not in (64, 128) or fmt not in CACHE_FORMATS:
+            raise FlamiaError(f"FlamiaPagedCache: {(num_pages, page_size, hkv, head_dim, fmt)} is not supported")
+        self.num_pages, self.page_size, self.hkv, self.d, self.fmt = num_pages, page_size, hkv, head_dim, fmt
+        self.device = _cuda_device(device)
+        self.k_scales = self.v_scales = None
+        shape = (num_pages, hkv, page_size, head_dim)
+        if fmt == "e4m3":
+            self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=self.device) for _ in range(2))
+            self.k_scales, self.v_scales = (torch.zeros(shape[:3], dtype=torch.uint8, device=self.device) for _ in range(2))
+        else:
+            self.k, self.v = (torch.zeros(shape, dtype=torch.bfloat16, device=self.device) for _ in range(2))
+        self.view = KVCache(_ptr(self.k), _ptr(self.v), _ptr(self.k_scales), _ptr(self.v_scales), num_pages, page_size,
+                            hkv, head_dim, CACHE_FORMATS[fmt])
+
+
+class FlamiaCachedAttention:
+    """A step of generation over paged caches: its plan, its writes and its attention.
+
+    A step serves num_seqs sequences with up to total_tokens new tokens, packed;
+    sequence n brings cu_seqlens[n + 1] - cu_seqlens[n] <= max_chunk of them (one
+    in plain generation, a few that were drafted, a chunk of a prompt, or none)
+    and has kv_lens[n] keys with them.  plan_build(cu_seqlens, kv_lens) comes
+    first; one plan serves every layer's cache:
+
+        att.plan_build(cu_seqlens, kv_lens)
+        for layer in layers:
+            att.write(layer.cache, k, v, page_table)
+            out, lse = att.forward(layer.cache, q, page_table)
+
+    window: keys up to so many positions before a token's own are seen (-1: all);
+    softcap as in FlamiaScoredAttention.  read(cache, page_table, k, v) puts the
+    step's tokens back into k and v (with kv_lens the chunks themselves: whole
+    sequences).
+
+    Tensors are contiguous, on the object's device: q [T, hq, d], k and v [T,
+    hkv, d] bf16; cu_seqlens [N + 1], kv_lens [N] and page_table [N, max_pages]
+    int32.  Anything else raises FlamiaError.  Errors that the device finds (bad
+    lengths, a page outside the cache) show in device_status().  forward returns
+    the object's own out and lse, overwritten by its next call.  Nothing is
+    allocated per call, so calls can be captured into a CUDA graph: a replay reads
+    what the tensors hold by then.  Calls run on `stream`, by default the object's
+    device's current stream; calls of one object share its outputs and workspace,
+    so calls on two streams have to be ordered by the caller."""
+
+    def __init__(self, total_tokens: int, num_seqs: int, hq: int, hkv: int, head_dim: int, max_chunk: int,
+                 max_pages: int, page_size: int, device="cuda", window: int = -1, softcap: float = 0.0):
+        import torch
+        if (total_tokens < 0 or num_seqs < 0 or hq <= 0 or hkv <= 0 or hq % hkv or head_dim not in (64, 128) or max_chunk < 1
+                or max_pages < 1 or page_size not in PAGE_SIZES or max_pages * page_size > 1 << 30):
+            raise FlamiaError("FlamiaCachedAttention: sizes "
+                              f"{(total_tokens, num_seqs, hq, hkv, head_dim, max_chunk, max_pages, page_size)} are not supported")
+        self.T, self.N, self.hq, self.hkv, self.d = total_tokens, num_seqs, hq, hkv, head_dim
+        self.max_chunk, self.max_pages, self.page_size = int(max_chunk), int(max_pages), page_size
+        self.window = max(-1, min(int(window), 2**31 - 1))
+        self.softcap = float(softcap)
+        self.device = _cuda_device(device)
+        dev = self.device
+        # zeros: a plan of no call, should a captured plan_build not have been replayed yet
+        self.plan = torch.zeros(flamia_cache_plan_bytes(total_tokens, num_seqs, hq, hkv), dtype=torch.uint8, device=dev)
+        self._planned = False
+        self.out = torch.empty(total_tokens, hq, head_dim, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty(hq, total_tokens, dtype=torch.float32, device=dev)
+        self.workspace = torch.empty(flamia_cached_fwd_workspace_bytes(hq, hkv, head_dim, self.max_chunk), dtype=torch.uint8,
+                                     device=dev)
+
+    _want = FlamiaScoredAttention._want
+    _run = FlamiaScoredAttention._run
+
+    def _places(self, cache, page_table):
+        import torch
+        if (cache.page_size, cache.hkv, cache.d, cache.device) != (self.page_size, self.hkv, self.d, self.device):
+            raise FlamiaError(f"cache: want pages of {self.page_size}, {self.hkv} heads of {self.d} on {self.device}, got "
+                              f"{cache.page_size}, {cache.hkv}, {cache.d} on {cache.device}")
+        self._want("page_table", page_table, (self.N, self.max_pages), torch.int32)
+        if not self._planned:
+            raise FlamiaError("FlamiaCachedAttention: plan_build has not been called")
+
+    def plan_build(self, cu_seqlens, kv_lens, stream=None):
+        import torch
+        self._want("cu_seqlens", cu_seqlens, (self.N + 1,), torch.int32)
+        self._want("kv_lens", kv_lens, (self.N,), torch.int32)
+        self._run(lambda stm: flamia_cache_plan_build(cu_seqlens, kv_lens, self.N, self.T, self.hq, self.hkv, self.max_chunk,
+                                                      self.max_pages * self.page_size, self.window, self.plan, stm), stream)
+        self._planned = True
+
+    def write(self, cache: FlamiaPagedCache, k, v, page_table, stream=None):
+        """The new tokens' keys and values into the cache."""
+        import torch
+        self._places(cache, page_table)
+        self._want("k", k, (self.T, self.hkv, self.d), torch.bfloat16)
+        self._want("v", v, (self.T, self.hkv, self.d), torch.bfloat16)
+        self._run(lambda stm: flamia_cache_write(cache.view, page_table, self.N, self.plan, k, v, stm), stream)
+
+    def read(self, cache: FlamiaPagedCache, page_table, k, v, stream=None):
+        """The new tokens' keys and values from the cache into k and v, which are returned."""
+        import torch
+        self._places(cache, page_table)
+        self._want("k", k, (self.T, self.hkv, self.d), torch.bfloat16)
+        self._want("v", v, (self.T, self.hkv, self.d), torch.bfloat16)
+        self._run(lambda stm: flamia_cache_read(cache.view, page_table, self.N, self.plan, k, v, stm), stream)
+        return k, v
+
+    def forward(self, cache: FlamiaPagedCache, q, page_table, softmax_scale: float = 0.0, stream=None):
+        """(out bf16 [T, hq, d], lse fp32 [hq, T]) of the new tokens, whose keys and values have been written."""
+        import torch
+        self._places(cache, page_table)
+        self._want("q", q, (self.T, self.hq, self.d), torch.bfloat16)
+        self._run(lambda stm: flamia_cached_fwd(q, cache.view, page_table, self.N, self.plan, self.out, self.lse,
+                                                self.workspace, self.max_chunk, self.window, self.softcap, softmax_scale,
+                                                stm), stream)
+        return self.out, self.lse
 
     def device_status(self, stream=None) -> int:
         return self._run(lambda stm: flamia_get_device_status(self.plan, stm), stream)

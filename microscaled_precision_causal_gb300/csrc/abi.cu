@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "cache.cuh"
 #include "common.cuh"
 #include "scored.cuh"
 
@@ -43,6 +44,11 @@ cudaError_t launch_scored_bwd(int D, const ScoredParams& p, cudaStream_t stream)
 cudaError_t launch_relbias_expand(const float* table, int nb, int hq, int md, int both, float* rel, int R, cudaStream_t s);
 cudaError_t launch_relbias_reduce(const float* drel, int R, int nb, int hq, int md, int both, float* dtable,
                                   cudaStream_t s);
+cudaError_t launch_cache_plan(const int32_t* cu, const int32_t* kv, int N, int T, int hq, int hkv, int max_chunk,
+                              int64_t max_kv, int left, void* plan, cudaStream_t s);
+cudaError_t launch_cache_write(int D, bool e4m3, const CacheParams& p, const void* k, const void* v, cudaStream_t s);
+cudaError_t launch_cache_read(int D, bool e4m3, const CacheParams& p, void* k, void* v, cudaStream_t s);
+cudaError_t launch_cached_fwd(int D, bool e4m3, const CachedParams& p, cudaStream_t s);
 }  // namespace flamia
 
 using namespace flamia;
@@ -50,6 +56,7 @@ using namespace flamia;
 namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 26;   // row indices stay in int32 with headroom
+constexpr int64_t kMaxKeys = (int64_t)1 << 30;     // positions too, and a tile behind them
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -187,6 +194,40 @@ ScoredParams scored_params(const void* q, const void* k, const void* v, int N, i
     p.R = o->rel_bias ? o->rel_max : 0;
     p.prefix = o->prefix_lens;
   }
+  return p;
+}
+
+// A cache and the call's page table (host-visible arguments only).
+int check_cache(const flamia_kv_cache* c, const int32_t* table, int max_pages, int N, int64_t T, const void* plan) {
+  if (!c || T < 0 || N < 0 || max_pages < 1 || !plan || !c->k || !c->v || c->num_pages < 1 || c->hkv < 1)
+    return FLAMIA_ERR_INVALID_ARG;
+  if (c->format != FLAMIA_CACHE_BF16 && c->format != FLAMIA_CACHE_E4M3) return FLAMIA_ERR_INVALID_ARG;
+  if (c->format == FLAMIA_CACHE_E4M3 && (!c->k_scales || !c->v_scales)) return FLAMIA_ERR_INVALID_ARG;
+  if (N > 0 && !table) return FLAMIA_ERR_INVALID_ARG;
+  if (T > kMaxTokens || N > kMaxTokens || c->hkv > 1024 || (c->head_dim != 64 && c->head_dim != 128))
+    return FLAMIA_ERR_UNSUPPORTED;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return FLAMIA_ERR_UNSUPPORTED;
+  if ((int64_t)max_pages * c->page_size > kMaxKeys || (int64_t)c->num_pages * c->hkv > 0x7FFFFFFF)
+    return FLAMIA_ERR_UNSUPPORTED;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(plan) || (reinterpret_cast<uintptr_t>(table) & 3u) ||
+      (c->format == FLAMIA_CACHE_E4M3 && (!aligned16(c->k_scales) || !aligned16(c->v_scales))))
+    return FLAMIA_ERR_MISALIGNED;
+  return FLAMIA_OK;
+}
+CacheParams cache_params(const flamia_kv_cache* c, const int32_t* table, int max_pages, int N, int64_t T, const void* plan) {
+  CacheParams p{};
+  p.k = static_cast<uint8_t*>(c->k);
+  p.v = static_cast<uint8_t*>(c->v);
+  p.k_scales = static_cast<uint8_t*>(c->k_scales);
+  p.v_scales = static_cast<uint8_t*>(c->v_scales);
+  p.table = table;
+  p.num_pages = c->num_pages;
+  p.max_pages = max_pages;
+  while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
+  p.hkv = c->hkv;
+  p.plan = static_cast<int*>(const_cast<void*>(plan));     // (its status word is written)
+  p.N = N;
+  p.T = (int)T;
   return p;
 }
 
@@ -506,6 +547,93 @@ int flamia_relbias_reduce(const float* drel_bias, int rel_max, int num_buckets, 
   if ((reinterpret_cast<uintptr_t>(drel_bias) | reinterpret_cast<uintptr_t>(dtable)) & 3u) return FLAMIA_ERR_MISALIGNED;
   return cuda_status(launch_relbias_reduce(drel_bias, rel_max, num_buckets, hq, max_distance, bidirectional, dtable,
                                            (cudaStream_t)stream));
+}
+
+size_t flamia_cache_plan_bytes(int64_t total_tokens, int num_seqs, int hq, int hkv) {
+  if (total_tokens < 0 || num_seqs < 0 || total_tokens > kMaxTokens || num_seqs > kMaxTokens || hq <= 0 || hkv <= 0) return 0;
+  return cache_plan_bytes(total_tokens, num_seqs, hq, hkv);
+}
+
+int flamia_cache_plan_build(const int32_t* cu_seqlens, const int32_t* kv_lens, int num_seqs, int64_t total_tokens, int hq,
+                            int hkv, int max_chunk, int64_t max_keys, int window_left, void* plan, size_t plan_bytes_,
+                            void* stream) {
+  int rc = check_common(total_tokens, num_seqs, cu_seqlens, plan);
+  if (rc) return rc;
+  if (hq <= 0 || hkv <= 0 || max_chunk < 1 || max_keys < 1 || (num_seqs > 0 && !kv_lens)) return FLAMIA_ERR_INVALID_ARG;
+  if (hq % hkv != 0 || hq > 1024 || max_keys > kMaxKeys || (int64_t)max_chunk * (hq / hkv) > kMaxKeys)
+    return FLAMIA_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(kv_lens)) & 3u) return FLAMIA_ERR_MISALIGNED;
+  if (plan_bytes_ < cache_plan_bytes(total_tokens, num_seqs, hq, hkv)) return FLAMIA_ERR_WORKSPACE;
+  return cuda_status(launch_cache_plan(cu_seqlens, kv_lens, num_seqs, (int)total_tokens, hq, hkv, max_chunk, max_keys,
+                                       window_left < 0 ? -1 : window_left, plan, (cudaStream_t)stream));
+}
+
+int flamia_cache_write(const flamia_kv_cache* cache, const int32_t* page_table, int max_pages, int num_seqs,
+                       int64_t total_tokens, const void* plan, const void* k_bf16, const void* v_bf16, void* stream) {
+  const int rc = check_cache(cache, page_table, max_pages, num_seqs, total_tokens, plan);
+  if (rc) return rc;
+  if (total_tokens == 0) return FLAMIA_OK;
+  if (!k_bf16 || !v_bf16) return FLAMIA_ERR_INVALID_ARG;
+  if (!aligned16(k_bf16) || !aligned16(v_bf16)) return FLAMIA_ERR_MISALIGNED;
+  return cuda_status(launch_cache_write(cache->head_dim, cache->format == FLAMIA_CACHE_E4M3,
+                                        cache_params(cache, page_table, max_pages, num_seqs, total_tokens, plan), k_bf16,
+                                        v_bf16, (cudaStream_t)stream));
+}
+
+int flamia_cache_read(const flamia_kv_cache* cache, const int32_t* page_table, int max_pages, int num_seqs,
+                      int64_t total_tokens, const void* plan, void* k_bf16, void* v_bf16, void* stream) {
+  const int rc = check_cache(cache, page_table, max_pages, num_seqs, total_tokens, plan);
+  if (rc) return rc;
+  if (total_tokens == 0) return FLAMIA_OK;
+  if (!k_bf16 || !v_bf16) return FLAMIA_ERR_INVALID_ARG;
+  if (!aligned16(k_bf16) || !aligned16(v_bf16)) return FLAMIA_ERR_MISALIGNED;
+  return cuda_status(launch_cache_read(cache->head_dim, cache->format == FLAMIA_CACHE_E4M3,
+                                       cache_params(cache, page_table, max_pages, num_seqs, total_tokens, plan), k_bf16,
+                                       v_bf16, (cudaStream_t)stream));
+}
+
+size_t flamia_cached_fwd_workspace_bytes(int hq, int hkv, int head_dim, int max_chunk) {
+  if (hq <= 0 || hkv <= 0 || head_dim <= 0 || max_chunk <= 0) return 0;
+  return cached_workspace_bytes(hq, hkv, head_dim, max_chunk);
+}
+
+int flamia_cached_fwd(const void* q_bf16, const flamia_kv_cache* cache, const int32_t* page_table, int max_pages,
+                      int num_seqs, int64_t total_tokens, int hq, int max_chunk, int window_left, float softcap,
+                      float softmax_scale, const void* plan, void* out_bf16, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int rc = check_cache(cache, page_table, max_pages, num_seqs, total_tokens, plan);
+  if (rc) return rc;
+  const int d = cache->head_dim, hkv = cache->hkv;
+  rc = check_heads(hq, hkv, d);
+  if (rc) return rc;
+  if (max_chunk < 1) return FLAMIA_ERR_INVALID_ARG;
+  if ((int64_t)max_chunk * (hq / hkv) > kMaxKeys) return FLAMIA_ERR_UNSUPPORTED;
+  flamia_score_options o;
+  flamia_default_score_options(&o);
+  o.softcap = softcap;
+  rc = check_score_opts(&o);
+  if (!rc) rc = check_score_scale(softmax_scale, d, &o);
+  if (rc) return rc;
+  if (total_tokens == 0) return FLAMIA_OK;
+  if (!q_bf16 || !out_bf16 || !lse || !workspace) return FLAMIA_ERR_INVALID_ARG;
+  if (!aligned16(q_bf16) || !aligned16(out_bf16) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return FLAMIA_ERR_MISALIGNED;
+  if (workspace_bytes < cached_workspace_bytes(hq, hkv, d, max_chunk)) return FLAMIA_ERR_WORKSPACE;
+  CachedParams p{};
+  p.c = cache_params(cache, page_table, max_pages, num_seqs, total_tokens, plan);
+  p.q = static_cast<const __nv_bfloat16*>(q_bf16);
+  p.out = static_cast<__nv_bfloat16*>(out_bf16);
+  p.lse = lse;
+  p.hq = hq;
+  p.left = window_left < 0 ? -1 : window_left;
+  p.max_chunk = max_chunk;
+  const double sc = softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)d);
+  p.scale2 = (float)(sc * 1.4426950408889634);
+  p.cap = softcap;
+  p.capf = cap_form(sc, (double)softcap);
+  p.part = static_cast<float*>(workspace);
+  return cuda_status(launch_cached_fwd(d, cache->format == FLAMIA_CACHE_E4M3, p, (cudaStream_t)stream));
 }
 
 int flamia_get_device_status(const void* plan, int* status_out, void* stream) {

@@ -1,0 +1,122 @@
+// Paged key/value cache: what its kernels and the ABI share (the plan's layout, page look-up,
+// the attention's parameters and workspace).
+#pragma once
+#include "common.cuh"
+#include "scored.cuh"
+
+namespace flamia {
+
+// Rows of a kv head in a sequence: its new tokens times the query heads that share the head, token by token.
+constexpr int kStepRows = 16;      // up to so many the sequence is a step: one tile of rows, keys streamed past it
+constexpr int kChunkRows = 2 * kTile;   // rows of a unit otherwise
+constexpr int kStepTile = 64;      // keys a tile of a step
+
+// ---------------------------------------------------------------- plan
+enum CachePlanWord : int {
+  kCpStatus = 0,
+  kCpNumSeqs = 1,
+  kCpTotal = 2,
+  kCpHkv = 3,
+  kCpHq = 4,
+  kCpMaxChunk = 5,
+  kCpLeft = 6,
+  kCpValid = 7,        // rows of the sequences (0: the plan is bad)
+  kCpItems = 8,        // chunk items
+  kCpHeaderWords = 16,
+};
+// A chunk item: up to kChunkRows rows of a sequence, the same for every kv head.
+struct CacheItem {
+  int seq, row, tile, tiles;     // first row; first key tile (kTile keys) and their number
+};
+struct CachePlanView {
+  int* hdr;
+  int4* seq;               // [N] {first token, new tokens, keys with them, first key that the first new one sees}
+  int64_t* step_prefix;    // [N + 1] key tiles of the steps before
+  int64_t* item_base;      // [N + 1] chunk items before
+  CacheItem* items;        // [cap]
+  int64_t* item_prefix;    // [cap + 1] key tiles of the items before
+};
+__host__ __device__ inline int64_t cache_item_capacity(int64_t T, int N, int hq, int hkv) {
+  return T * (hq / hkv) / kChunkRows + N;
+}
+__host__ __device__ inline size_t cache_plan_bytes(int64_t T, int N, int hq, int hkv) {
+  const int64_t cap = cache_item_capacity(T, N, hq, hkv);
+  return (size_t)kCpHeaderWords * 4 + (size_t)N * 16 + (size_t)(N + 1) * 16 + (size_t)cap * 24 + 16;
+}
+// The sequences come first: writing and reading the cache need no more of the layout.
+__host__ __device__ inline CachePlanView cache_plan_view(const void* plan, int64_t T, int N, int hq, int hkv) {
+  CachePlanView v;
+  v.hdr = (int*)plan;
+  v.seq = (int4*)(v.hdr + kCpHeaderWords);
+  v.items = (CacheItem*)(v.seq + N);
+  v.step_prefix = (int64_t*)(v.items + cache_item_capacity(T, N, hq, hkv));
+  v.item_base = v.step_prefix + (N + 1);
+  v.item_prefix = v.item_base + (N + 1);
+  return v;
+}
+
+struct CacheParams {
+  uint8_t *k, *v;                  // [pages][hkv][P][d] E4M3 or bf16
+  uint8_t *k_scales, *v_scales;    // [pages][hkv][P] UE8M0 (E4M3)
+  const int32_t* table;            // [N][max_pages]
+  int num_pages, max_pages, page_shift, hkv;
+  int* plan;
+  int N, T;
+};
+// Rows that the plan says lie in sequences; 0 where it was built for another call.
+__device__ __forceinline__ int cache_valid_rows(const CacheParams& p) {
+  const int* h = p.plan;
+  if (h[kCpNumSeqs] == p.N && h[kCpTotal] == p.T && h[kCpHkv] == p.hkv) return h[kCpValid];
+  atomicOr(p.plan + kCpStatus, FLAMIA_DEV_PLAN_MISMATCH);
+  return 0;
+}
+// Page of index i of sequence n, or -1 (and the status bit) where the table has none.
+__device__ __forceinline__ int cache_page(const CacheParams& p, int n, int i) {
+  const int page = i < p.max_pages ? p.table[(int64_t)n * p.max_pages + i] : -1;
+  if ((unsigned)page < (unsigned)p.num_pages) return page;
+  atomicOr(p.plan + kCpStatus, FLAMIA_DEV_BAD_PAGE);
+  return -1;
+}
+// Largest n in [0, N) with at(n) <= x, at non-decreasing and at(0) <= x: 32 probes a round by a whole warp.
+template <class At, class X>
+__device__ __forceinline__ int warp_upper(int N, X x, At at) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = N;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const int below = __popc(__ballot_sync(0xffffffffu, lane * step < n && at(i) <= x)) - 1;
+    lo += below * step;
+    n = min(step, n - below * step);
+  }
+  return lo;
+}
+// 2^(b - 127), NaN for 255.
+__device__ __forceinline__ float cache_scale(uint32_t b) { return b == 255 ? __uint_as_float(0x7fc00000u) : ue8m0_to_f32(b); }
+
+// ---------------------------------------------------------------- attention
+struct CachedParams {
+  CacheParams c;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;
+  int hq, left, max_chunk;
+  float scale2;              // softmax scale log2 e
+  float cap;                 // 0: none
+  CapForm capf;
+  float* part;               // workspace
+};
+// A CTA leaves at most two unfinished pieces of units behind (the unit that its first key tile lies inside of, and the
+// one that its last lies inside of): a row's weighted values, its sum and its reference each.
+constexpr int kStepCtas = 304, kChunkCtas = 152;
+inline size_t cached_workspace_bytes(int hq, int hkv, int d, int max_chunk) {
+  const size_t row = (size_t)(d + 2) * 4;
+  return 2 * row * ((size_t)kStepCtas * kStepRows + ((int64_t)max_chunk * (hq / hkv) > kStepRows ? (size_t)kChunkCtas * kChunkRows : 0));
+}
+__device__ __forceinline__ int cached_valid_rows(const CachedParams& p) {
+  const int* h = p.c.plan;
+  if (h[kCpHq] == p.hq && h[kCpLeft] == p.left && h[kCpMaxChunk] == p.max_chunk) return cache_valid_rows(p.c);
+  atomicOr(p.c.plan + kCpStatus, FLAMIA_DEV_PLAN_MISMATCH);
+  return 0;
+}
+
+}  // namespace flamia
