@@ -119,4 +119,72 @@ __device__ __forceinline__ int cached_valid_rows(const CachedParams& p) {
   return 0;
 }
 
+
+// ---------------------------------------------------------------- units and shares
+// A unit is a tile of a sequence's rows (a step: all of them) and a kv head, over the key tiles that its rows see.
+// The key tiles of all units, unit after unit, are dealt out to the CTAs in equal shares, so that every CTA has
+// the same to do whatever the sequences' lengths are; a unit whose tiles lie in several shares is joined after.
+struct CachedUnit {
+  int seq, h, row, rows, tile, tiles;     // first row, rows, first key tile, key tiles
+  int start, count, keys, lo;             // of the sequence (CachePlanView::seq)
+  int64_t begin;                          // number of its first tile among all
+};
+template <bool STEP>
+__device__ __forceinline__ int64_t cached_tiles(const CachedParams& p, const CachePlanView& pv) {
+  return (STEP ? pv.step_prefix[p.c.N] : pv.item_prefix[pv.hdr[kCpItems]]) * p.c.hkv;
+}
+// The unit of tile f (found by a whole warp).
+template <bool STEP>
+__device__ __forceinline__ CachedUnit cached_unit(const CachedParams& p, const CachePlanView& pv, int64_t f) {
+  CachedUnit u;
+  const int64_t* prefix = STEP ? pv.step_prefix : pv.item_prefix;
+  const int hkv = p.c.hkv;
+  const int i = warp_upper(STEP ? p.c.N : pv.hdr[kCpItems], f, [&](int x) { return prefix[x] * hkv; });
+  const int64_t first = prefix[i] * hkv;
+  CacheItem item{i, 0, 0, 0};
+  if (!STEP) item = pv.items[i];
+  const int4 r = pv.seq[item.seq];
+  u.seq = item.seq;
+  u.start = r.x;
+  u.count = r.y;
+  u.keys = r.z;
+  u.lo = r.w;
+  const int rows = r.y * (p.hq / hkv);
+  u.row = item.row;
+  u.rows = STEP ? rows : min(rows - u.row, kChunkRows);
+  u.tile = STEP ? r.w / kStepTile : item.tile;
+  u.tiles = STEP ? (int)(prefix[i + 1] - prefix[i]) : item.tiles;
+  u.h = (int)((f - first) / u.tiles);
+  u.begin = first + (int64_t)u.h * u.tiles;
+  return u;
+}
+struct Shares {
+  int64_t total;
+  int n;              // CTAs with a share
+  __device__ __forceinline__ int64_t begin(int c) const { return total * c / n; }
+  __device__ __forceinline__ int of(int64_t f) const { return (int)(((f + 1) * n - 1) / total); }   // the last c with begin(c) <= f
+};
+// A CTA takes kLeast tiles at least: fewer would cost more in joining than they save.
+template <bool STEP>
+__device__ __forceinline__ Shares cached_shares(const CachedParams& p, const CachePlanView& pv) {
+  constexpr int kCtas = STEP ? kStepCtas : kChunkCtas, kLeast = STEP ? 4 : 2;
+  Shares s;
+  s.total = cached_tiles<STEP>(p, pv);
+  s.n = (int)min((int64_t)kCtas, (s.total + kLeast - 1) / kLeast);
+  return s;
+}
+// Unfinished pieces: the one that a CTA's share begins in the middle of (0), and the one that it ends in the middle of and
+// has the beginning of (1).  [rows][D] weighted values, [rows] references (base 2), [rows] sums.
+template <bool STEP, int D>
+__device__ __forceinline__ float* cached_part(const CachedParams& p, int cta, int slot) {
+  constexpr int kRows = STEP ? kStepRows : kChunkRows;
+  float* base = p.part + (STEP ? 0 : (size_t)2 * kStepCtas * kStepRows * (D + 2));
+  return base + (size_t)(2 * cta + slot) * kRows * (D + 2);
+}
+// Where row r of a unit is: token and query head.
+__device__ __forceinline__ int2 cached_row(const CachedParams& p, const CachedUnit& u, int r) {
+  const int group = p.hq / p.c.hkv, x = u.row + r;
+  return make_int2(u.start + x / group, u.h * group + x % group);
+}
+
 }  // namespace flamia

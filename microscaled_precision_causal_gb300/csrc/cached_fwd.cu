@@ -1,7 +1,11 @@
-// Attention of new tokens over the paged cache: a warp per query row and head, keys one by one in fp32.
+// Attention of new tokens over the paged cache: steps by the step kernel, the others a warp per query row and head,
+// keys one by one in fp32.
 #include "cache.cuh"
 
 namespace flamia {
+
+cudaError_t launch_cached_step(int D, bool e4m3, const CachedParams& p, cudaStream_t s);
+cudaError_t launch_cached_join(int D, bool step, const CachedParams& p, cudaStream_t s);
 
 namespace {
 
@@ -35,6 +39,7 @@ __global__ void __launch_bounds__(kWarps * 32) cached_rows_kernel(const CachedPa
     const int n = warp_upper(p.c.N, row, [&](int i) { return seq[i].x; });
     const int4 r = seq[n];
     const int pos = r.z - r.y + row - r.x;
+    if (r.y * (p.hq / p.c.hkv) <= kStepRows) return;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) q[i] = __bfloat162float(p.q[((int64_t)row * p.hq + h) * D + lane * kPer + i]);
     for (int j = p.left < 0 ? 0 : max(0, pos - p.left); j <= pos; ++j) {
@@ -66,6 +71,12 @@ __global__ void __launch_bounds__(kWarps * 32) cached_rows_kernel(const CachedPa
 }  // namespace
 
 cudaError_t launch_cached_fwd(int D, bool e4m3, const CachedParams& p, cudaStream_t s) {
+  const int group = p.hq / p.c.hkv;
+  if (group <= kStepRows) {
+    cudaError_t e = launch_cached_step(D, e4m3, p, s);
+    if (e == cudaSuccess) e = launch_cached_join(D, true, p, s);
+    if (e != cudaSuccess || (int64_t)p.max_chunk * group <= kStepRows) return e;
+  }
   const int64_t blocks = ((int64_t)p.c.T * p.hq + kWarps - 1) / kWarps;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const auto f = D == 128 ? (e4m3 ? cached_rows_kernel<128, true> : cached_rows_kernel<128, false>)
