@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libflamia.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["plan.cu", "quantize.cu", "attn_fwd.cu", "attn_fwd_coop.cu", "attn_bwd.cu", "abi.cu",
-           "static_scratch.cu", "scored_fwd.cu", "scored_bwd.cu", "relbias.cu", "cache.cu", "cached_fwd.cu", "cached_step.cu"]
+           "static_scratch.cu", "scored_fwd.cu", "scored_bwd.cu", "relbias.cu", "cache.cu", "cached_step.cu", "cached_chunk.cu"]
 HEADERS = ["common.cuh", "ptx.cuh", "tmap.h", "scored.cuh", "cache.cuh"]
 
 NVCC_FLAGS = [

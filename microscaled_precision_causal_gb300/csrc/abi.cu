@@ -629,6 +629,7 @@ int flamia_cached_fwd(const void* q_bf16, const flamia_kv_cache* cache, const in
   p.left = window_left < 0 ? -1 : window_left;
   p.max_chunk = max_chunk;
   const double sc = softmax_scale > 0.f ? (double)softmax_scale : 1.0 / std::sqrt((double)d);
+  p.scale = sc;
   p.scale2 = (float)(sc * 1.4426950408889634);
   p.cap = softcap;
   p.capf = cap_form(sc, (double)softcap);

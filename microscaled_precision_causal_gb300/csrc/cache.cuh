@@ -100,6 +100,7 @@ struct CachedParams {
   __nv_bfloat16* out;
   float* lse;
   int hq, left, max_chunk;
+  double scale;              // softmax scale
   float scale2;              // softmax scale log2 e
   float cap;                 // 0: none
   CapForm capf;

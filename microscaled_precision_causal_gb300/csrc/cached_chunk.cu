@@ -1,0 +1,742 @@
+// Attention over the paged cache for chunks: more than 16 rows of a kv head.
+//
+// The scored forward's scheme (bf16 tcgen05 MMAs, two tiles of 128 rows in turn, P in tensor memory over the
+// scores it came from, a reference m near the row's maximum) with three differences:
+//   - A tile's rows are a kv head's: the new tokens' query heads that share it, token by token.  With
+//     grouped heads a key tile thus serves all of them, and short chunks still fill a tile.
+//   - Key tiles come from pages, a TMA copy a page.  E4M3 codes go to a raw ring, from which four
+//     warps write the bf16 tiles that the products read: code times scale is exact in bf16.
+//     A thread unpacks a key's row, so the scale is one register; both sides are free of bank
+//     conflicts by the copies' and the products' swizzles.
+//   - All units' key tiles are dealt out in equal shares (cache.cuh): one chunk over a long context
+//     keeps every SM busy, and the pieces are joined after.
+// Keys behind the sequence or before every row's window are zeros to the products, whatever the page holds.
+//
+// Roles (512 threads):
+//   warp 0        producer: K and V tiles, page by page
+//   warp 1        MMA issuer (at D = 64 of the first row tile; warp 3 of the second)
+//   warp 2        TMEM allocator; finds the units ahead and loads their queries
+//   warps 4-11    softmax, a warpgroup per row tile, thread = row; they write the unit's O too
+//   warps 12-15   E4M3: unpack
+// TMEM columns as in the scored forward.
+#include <type_traits>
+
+#include "cache.cuh"
+#include "ptx.cuh"
+#include "tmap.h"
+
+namespace flamia {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr float kRescaleAbove = 8.f, kLoose = 64.f;
+constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
+constexpr int kRegCtl = 64, kRegAux = 80, kRegSoftmax = 184;
+static_assert(kRegCtl * 128 + kRegAux * 128 + kRegSoftmax * 256 <= kLaunchRegs * kThreads, "register split");
+
+// x - m is one multiply-add while m was rounded: from |m| = 2^28 on both are shrunk (as in the scored forward).
+__device__ __forceinline__ float shrink_for(float m) {
+  const uint32_t e = (__float_as_uint(m) >> 23) & 255;
+  return e >= 127 + 28 && e < 255 ? __uint_as_float((2 * 127 + 28 - e) << 23) : 1.f;
+}
+
+// A unit's piece as the roles need it.  Key tiles last, last - 1, ..., last - tiles + 1: a causal row's
+// largest scores tend to be near.
+struct alignas(16) Piece {
+  int tiles, last;                 // 0 tiles: no more
+  int h, row, rows, ntq;
+  int start, pos0, keys, lo;       // first token of the sequence, and its position; keys; first key seen by any row
+  int seq, slot;                   // slot of the workspace, or -1: a whole unit
+};
+static_assert(sizeof(Piece) == 48, "read as three 16-byte words");
+constexpr int kUnits = 4;
+
+__device__ __forceinline__ Piece read_piece(const uint8_t* units, uint64_t* full, uint64_t* done, int n, bool whole_warp, bool& ok,
+                                            int* status) {
+  ok = mbar_wait(&full[n % kUnits], (n / kUnits) & 1, status);
+  if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+  union {
+    Piece p;
+    int4 w[3];
+  } x;
+  const int4* src = reinterpret_cast<const int4*>(units + (n % kUnits) * sizeof(Piece));
+#pragma unroll
+  for (int i = 0; i < 3; ++i) x.w[i] = src[i];
+  if (whole_warp) __syncwarp();
+  if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(&done[n % kUnits]);
+  if (!ok) x.p.tiles = 0;
+  return x.p;
+}
+
+template <int D, bool E4M3>
+struct ChunkSmem {
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kSlots = D == 128 ? 4 : 8;           // K and V tiles in turn
+  static constexpr int kRaw = E4M3 ? (D == 128 ? 2 : 4) : 0;
+  static constexpr int kRawBytes = kTile * D;
+  static constexpr int kQ = 0;                              // [2]
+  static constexpr int kKV = 2 * kTileBytes;
+  static constexpr int kCodes = kKV + kSlots * kTileBytes;
+  static constexpr int kScales = kCodes + kRaw * kRawBytes; // [kRaw][128]
+  static constexpr int kUnit = kScales + kRaw * kTile;
+  static constexpr int kBar = kUnit + kUnits * (int)sizeof(Piece);
+  static constexpr int kBytes = kBar + 512;
+  static constexpr int kAlloc = kBytes + 1024;
+};
+
+__device__ __forceinline__ void chunk_bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+// Two codes, each in the upper byte of a half word, times 2^-120 as bf16: sign, exponent and mantissa bits moved to
+// their places (subnormal codes become subnormal bf16 values of the same meaning).
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t t) { return ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u); }
+
+// A row of codes -> bf16 values times their scale 2^(b - 127).  One factor 2^(b - 7) up to b = 134; above, 2^120
+// first, then 2^(b - 127).
+template <int D>
+__device__ __forceinline__ void unpack_row(const uint8_t* raw, uint8_t* tile, int r, uint32_t b, bool use) {
+  const bool big = b > 134;
+  const uint32_t f1 = big ? 0x7b807b80u : (b + 120) * 0x00800080u, f2 = b == 255 ? 0x7fc07fc0u : b * 0x00800080u;
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) {
+    const uint4 c = *reinterpret_cast<const uint4*>(raw + swz_offset(r, 16 * j, D));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[2 * i] = mul_bf16x2(codes_bf16(__byte_perm(w[i], 0, 0x1404)), f1);
+      y[2 * i + 1] = mul_bf16x2(codes_bf16(__byte_perm(w[i], 0, 0x3424)), f1);
+    }
+    if (big) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = mul_bf16x2(y[i], f2);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int col = 32 * j + 16 * i;       // byte of the row
+      *reinterpret_cast<uint4*>(tile + (col >> 7) * kTile * 128 + swz_offset(r, col & 127, 128)) =
+          use ? make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]) : make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+template <int D, bool E4M3, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    cached_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const CachedParams p, const bool tail) {
+  using L = ChunkSmem<D, E4M3>;
+  constexpr int kSlots = L::kSlots;
+  constexpr bool kSplit = D == 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* q_full = bars;                  // [2 row tiles], as the next six
+  uint64_t* q_empty = bars + 2;
+  uint64_t* s_full = bars + 4;
+  uint64_t* s_free = bars + 6;              // (split) scores read
+  uint64_t* pv_done = bars + 8;             // (split) P read
+  uint64_t* o_full = bars + 10;             // the unit's O is whole
+  uint64_t* o_free = bars + 12;             // and has been read
+  uint64_t* p_full = bars + 14;             // [2 row tiles][2 halves of 64 keys]
+  uint64_t* drain = bars + 18;              // [2 issuers]
+  uint64_t* unit_full = bars + 20;          // [kUnits]
+  uint64_t* unit_done = unit_full + kUnits; // [kUnits] read by every role
+  uint64_t* kv_full = unit_done + kUnits;   // [kSlots]
+  uint64_t* kv_empty = kv_full + kSlots;    // [kSlots]
+  uint64_t* raw_full = kv_empty + kSlots;   // [kRaw]
+  uint64_t* raw_empty = raw_full + L::kRaw; // [kRaw]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + L::kRaw);
+  int* status = p.c.plan + kCpStatus;
+  uint8_t* units = smem + L::kUnit;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_let_next();
+  const int valid = cached_valid_rows(p);
+  if (tail) {                               // O = 0, LSE = +inf behind the last sequence
+    const int64_t rows = (int64_t)(p.c.T - valid) * p.hq;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rows; i += (int64_t)gridDim.x * kThreads) {
+      const int64_t row = valid + i / p.hq;
+      const int h = (int)(i % p.hq);
+      uint4* dst = reinterpret_cast<uint4*>(p.out + (row * p.hq + h) * D);
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) dst[j] = make_uint4(0, 0, 0, 0);
+      p.lse[(int64_t)h * p.c.T + row] = INFINITY;
+    }
+  }
+  const CachePlanView pv = cache_plan_view(p.c.plan, p.c.T, p.c.N, p.hq, p.c.hkv);
+  Shares sh{};
+  if (valid) sh = cached_shares<false>(p, pv);
+  if ((int)blockIdx.x >= sh.n) {
+    grid_wait();                            // who comes behind this launch comes behind the one before it too
+    return;
+  }
+  const int64_t f0 = sh.begin(blockIdx.x), f1 = sh.begin(blockIdx.x + 1);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 128);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 128);
+      mbar_init(&p_full[2 * i], 128);
+      mbar_init(&p_full[2 * i + 1], 128);
+      mbar_init(&drain[i], 1);
+    }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&unit_full[i], 1);
+      mbar_init(&unit_done[i], 1 + (kSplit ? 2 : 1) + 8 + (E4M3 ? 4 : 0));
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&kv_full[i], E4M3 ? 4 : 1);
+      mbar_init(&kv_empty[i], kSplit ? 2 : 1);      // issuers
+    }
+    for (int i = 0; i < L::kRaw; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+  constexpr uint32_t kO = 256, kP = 384;
+
+  if (warp < 4) {
+    setmaxnreg_dec<kRegCtl>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      const int P = 1 << p.c.page_shift, per = kTile >> p.c.page_shift;       // pages a tile
+      constexpr int kRing = E4M3 ? L::kRaw : kSlots;
+      constexpr int kRowBytes = E4M3 ? D : 128;                                // of a box
+      uint64_t* full = E4M3 ? raw_full : kv_full;
+      uint64_t* empty = E4M3 ? raw_empty : kv_empty;
+      uint32_t ring = 0;
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const Piece U = read_piece(units, unit_full, unit_done, n, true, ok, status);
+        if (U.tiles == 0) break;
+        auto page_of = [&](int k) {            // lane's page of the k-th tile, or -1
+          const int pos = (U.last - k) * kTile + lane * P;
+          if (k >= U.tiles || lane >= per || pos >= U.keys || pos + P <= U.lo) return -1;
+          const int page = cache_page(p.c, U.seq, pos >> p.c.page_shift);
+          return page < 0 ? -1 : page * p.c.hkv + U.h;
+        };
+        int next = page_of(0);
+        for (int k = 0; k < U.tiles && ok; ++k) {
+          const int page = next;
+          next = page_of(k + 1);
+          const int pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
+#pragma unroll
+          for (int v = 0; v < 2; ++v, ++ring) {
+            const uint32_t st = ring % kRing;
+            if (ring >= kRing && !(ok = warp_wait(&empty[st], (ring / kRing - 1) & 1, status))) break;
+            if (lane == 0) {
+              if (pages) mbar_arrive_expect_tx(&full[st], pages * P * (E4M3 ? D + 1 : 2 * D));
+              else mbar_arrive(&full[st]);
+            }
+            __syncwarp();
+            if (page >= 0) {
+              uint8_t* dst = smem + (E4M3 ? L::kCodes + st * L::kRawBytes : L::kKV + st * L::kTileBytes) + lane * P * kRowBytes;
+#pragma unroll
+              for (int b = 0; b < (E4M3 ? 1 : D / 64); ++b)
+                tma_load_3d(dst + b * kTile * 128, v ? &tm_v : &tm_k, &full[st], 128 * b, page, 0);
+              if constexpr (E4M3)
+                chunk_bulk_load(smem + L::kScales + st * kTile + lane * P,
+                                (v ? p.c.v_scales : p.c.k_scales) + ((int64_t)page << p.c.page_shift), P, &full[st]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      // nothing may land after the CTA has left (reached early only when a wait ran out)
+      for (uint32_t x = ring > kRing ? ring - kRing : 0; x < ring; ++x) mbar_wait(&full[x % kRing], (x / kRing) & 1, status);
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- units and their queries
+      const int group = p.hq / p.c.hkv;
+      uint32_t nq[2] = {0, 0};
+      bool ok = true;
+      int64_t f = f0;
+      for (int n = 0; ok; ++n) {
+        if (n >= kUnits && !(ok = warp_wait(&unit_done[n % kUnits], (n / kUnits - 1) & 1, status))) break;
+        Piece U{};
+        if (f < f1) {
+          const CachedUnit u = cached_unit<false>(p, pv, f);
+          const int t0 = (int)(f - u.begin), t1 = (int)min((int64_t)u.tiles, f1 - u.begin);
+          f += t1 - t0;
+          U.tiles = t1 - t0;
+          U.last = u.tile + u.tiles - 1 - t0;
+          U.h = u.h;
+          U.row = u.row;
+          U.rows = u.rows;
+          U.ntq = u.rows > kTile ? 2 : 1;
+          U.start = u.start;
+          U.pos0 = u.keys - u.count;
+          U.keys = u.keys;
+          U.lo = p.left < 0 ? 0 : max(0, U.pos0 + u.row / group - p.left);
+          U.seq = u.seq;
+          U.slot = U.tiles == u.tiles ? -1 : (t0 == 0 ? 1 : 0);
+        }
+        if (lane == 0) {
+          *reinterpret_cast<Piece*>(units + (n % kUnits) * sizeof(Piece)) = U;
+          mbar_arrive(&unit_full[n % kUnits]);
+        }
+        __syncwarp();
+        if (U.tiles == 0) break;
+        // two (D = 128) or four rows at a time, 16 bytes a lane; rows behind the unit's are zeros
+        constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+        const int c = lane % kLanes, dt = kPer / group, dg = kPer % group;
+        int r = lane / kLanes, t = (U.row + r) / group, g = (U.row + r) % group;
+        for (int w = 0; w < U.ntq; ++w) {
+          if (nq[w] && !(ok = warp_wait(&q_empty[w], (nq[w] - 1) & 1, status))) break;
+          ++nq[w];
+          for (int i = 0; i < kTile / kPer; ++i) {
+            const bool in = r < U.rows;
+            const __nv_bfloat16* src = p.q + (in ? (((int64_t)U.start + t) * p.hq + U.h * group + g) * D + 8 * c : 0);
+            const uint32_t dst = smem_u32(smem + L::kQ + w * L::kTileBytes + (c >> 3) * kTile * 128 +
+                                          swz_offset(r & (kTile - 1), (c & 7) * 16, 128));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+            r += kPer;
+            t += dt;
+            g += dg;
+            if (g >= group) {
+              g -= group;
+              ++t;
+            }
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (w == 0 && U.ntq == 2) continue;
+          if (w == 1) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[0]);
+          }
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_full[w]);
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 1 || kSplit) {
+      // ---------------------------------------------------------- MMA issuer of row tiles w0 .. w1 - 1
+      const int w0 = kSplit ? warp >> 1 : 0, w1 = kSplit ? w0 + 1 : 2;
+      const bool leader = elect_one();
+      const uint32_t base16 = (smem_u32(smem) & 0x3FFFFu) >> 4;
+      const uint32_t tb = (uint32_t)warp_uniform((int)tbase);
+      uint32_t ring = 0, nq0 = 0, nq1 = 0, np0 = 0, np1 = 0, ns0 = 0, ns1 = 0;
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const Piece U = read_piece(units, unit_full, unit_done, n, true, ok, status);
+        const int nk = warp_uniform(U.tiles), ntq = warp_uniform(U.ntq);
+        if (nk == 0) break;
+        auto landed = [&](uint32_t x) { return ok = warp_wait(&kv_full[x % kSlots], (x / kSlots) & 1, status); };
+        auto release = [&](uint32_t x) {
+          if (leader) mma_commit(&kv_empty[x % kSlots]);
+        };
+        auto scores = [&](int w, int k) {          // S of key tile k.  A (Q): q_full at the unit's first; B (K): kv_full
+          const uint32_t x = ring + 2 * k, st = x % kSlots;
+          if (k == 0 && !(ok = warp_wait(&q_full[w], (w ? nq1 : nq0) & 1, status))) return;
+          uint32_t& ns = w ? ns1 : ns0;
+          if (kSplit && ns && !(ok = warp_wait(&s_free[w], (ns - 1) & 1, status))) return;   // the last ones have been read
+          ++ns;
+          if (!landed(x)) return;
+          tc_fence_after();
+          const uint32_t kv16 = base16 + st * (L::kTileBytes / 16);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = (s / 4) * kTile * 128 + (s % 4) * 32;
+            if (leader)
+              mma_bf16(tb + w * 128, sdesc_at(base16, L::kQ + w * L::kTileBytes + off, 16, 1024, kSwizzle128B),
+                       sdesc_at(kv16, L::kKV + off, 16, 1024, kSwizzle128B), idesc_bf16(128, 128, 0, 0), s > 0);
+          }
+          if (leader) {
+            mma_commit(&s_full[w]);
+            if (k == nk - 1) mma_commit(&q_empty[w]);
+          }
+        };
+        // O += P V, half of the keys at a time as they are handed in.  A (P in TMEM): p_full; B (V): kv_full
+        auto values = [&](int w, int k) {
+          const uint32_t x = ring + 2 * k + 1, st = x % kSlots;
+          if (!landed(x)) return;
+          const uint32_t nq = w ? nq1 : nq0;
+          if (k == 0 && nq && !(ok = warp_wait(&o_free[w], (nq - 1) & 1, status))) return;
+          const uint32_t par = (w ? np1++ : np0++) & 1, kv16 = base16 + st * (L::kTileBytes / 16);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = warp_wait(&p_full[2 * w + half], par, status))) return;
+            tc_fence_after();
+#pragma unroll
+            for (int s = 4 * half; s < 4 * half + 4; ++s)
+              if (leader)
+                mma_bf16_ta(tb + kO + w * D, tb + (kSplit ? kP + 64 * w : 128 * w) + s * 8,
+                            sdesc_at(kv16, L::kKV + s * 2048, kTile * 128, 1024, kSwizzle128B), idesc_bf16(128, D, 0, 1),
+                            (k != 0 || s > 0));
+          }
+          if (leader) {
+            if (kSplit) mma_commit(&pv_done[w]);
+            if (k == nk - 1) mma_commit(&o_full[w]);
+          }
+        };
+        for (int w = w0; w < w1 && ok; ++w) {
+          if (w < ntq) scores(w, 0);
+          else if (kSplit) landed(ring);           // (a tile that nobody else of this issuer has waited for)
+        }
+        if (ok) release(ring);
+        for (int k = 0; k < nk && ok; ++k) {
+          for (int w = w0; w < w1 && ok; ++w) {
+            const bool next = k + 1 < nk && w < ntq;
+            if (kSplit && next) scores(w, k + 1);
+            if (ok && w < ntq) values(w, k);
+            else if (kSplit && ok) landed(ring + 2 * k + 1);
+            if (kSplit && ok && !next && k + 1 < nk) landed(ring + 2 * k + 2);
+            if (!kSplit && next && ok) scores(w, k + 1);     // over P, right behind its product
+          }
+          if (!ok) break;
+          release(ring + 2 * k + 1);
+          if (k + 1 < nk) release(ring + 2 * k + 2);
+        }
+        ++nq0;
+        if (ntq > 1) ++nq1;
+        ring += 2 * nk;
+      }
+      // every MMA has finished before tensor memory is freed
+      if (leader) {
+        mma_commit(&drain[w0]);
+        mbar_wait(&drain[w0], 0, status);
+      }
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ softmax
+    setmaxnreg_inc<kRegSoftmax>();
+    const int w = (warp - 4) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = tbase + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t s_addr = lane_base + w * 128, o_addr = lane_base + kO + w * D;
+    const uint32_t p_addr = kSplit ? lane_base + kP + 64 * w : s_addr;
+    const float scale2 = p.scale2;
+    const int group = p.hq / p.c.hkv;
+    uint32_t ring = 0, ns = 0, nu = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      const Piece U = read_piece(units, unit_full, unit_done, n, true, ok, status);
+      if (U.tiles == 0) break;
+      const int nk = U.tiles;
+      if (w >= U.ntq) {
+        ring += 2 * nk;
+        continue;
+      }
+      const int rr = w * kTile + r;
+      const bool row_in = rr < U.rows;     // rows behind the unit's take no part in the warp's choices
+      const int x = U.row + min(rr, U.rows - 1);
+      const int pos = U.pos0 + x / group;
+      const int lo = p.left < 0 ? 0 : max(0, pos - p.left);
+      // tiles that every row of the row tile sees whole
+      const int full_hi = (U.pos0 + (U.row + w * kTile) / group + 1) / kTile - 1;
+      const int full_lo = p.left < 0 ? 0
+          : max(0, U.pos0 + (U.row + min(w * kTile + kTile, U.rows) - 1) / group - p.left + kTile - 1) / kTile;
+      float m = -INFINITY;
+      float2 la = make_float2(0.f, 0.f), lb = la;
+      bool first = true;
+      for (int k = 0; k < nk; ++k) {
+        const int u = U.last - k;
+        const bool seen = u >= full_lo && u <= full_hi;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[w], ns & 1, status));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t v[4][32];
+        float cm[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if constexpr (CAP) tmem_ld32_absmax(s_addr + 32 * g, v[g], cm[g]);
+          else tmem_ld32_max(s_addr + 32 * g, v[g], cm[g]);
+        }
+        tmem_ld_wait();
+        if (kSplit) {
+          tc_fence_before();
+          mbar_arrive(&s_free[w]);
+        }
+        float mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);      // of the raw products, or of their magnitudes
+        // form 0: v f + n; 1, 2: capped by 3 or 5 coefficients, then as 0
+        int form = 0;
+        bool quick = seen;
+        if constexpr (CAP) {
+          quick = quick && !__any_sync(0xffffffffu, row_in && !(mx <= p.capf.t5 && mx * scale2 <= kLoose * 0.5f));
+          form = __any_sync(0xffffffffu, row_in && !(mx <= p.capf.t3)) ? 2 : 1;
+        }
+        if (!quick) {
+          form = 0;
+          uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+          if (!seen) {
+            const int c = u * kTile;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) see[g] = column_mask(lo - c, pos - c, -1, 32 * g);
+          }
+          if constexpr (CAP) {
+            if (!seen) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g) hide(v[g], see[g], 0u);
+            }
+            cap_products(v, p.capf, row_in);
+          }
+          if (!seen) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) hide(v[g], see[g], kMinusInf);
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) cm[g] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) cm[g] = fmax3(cm[g], __uint_as_float(v[g][j]), __uint_as_float(v[g][j + 1]));
+          mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);
+        }
+        mx *= scale2;
+        if (first) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, row_in && mx > m + kRescaleAbove)) {
+          const float m_new = fmaxf(m, mx);
+          const float alpha = m_new == m ? 1.f : fast_exp2(m - m_new);      // 0 where nothing was visible yet
+          la = fmul2(la, make_float2(alpha, alpha));
+          lb = fmul2(lb, make_float2(alpha, alpha));
+          m = m_new;
+          if (kSplit) {                // the last product has to be in
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[w], (ns - 1) & 1, status));
+            if (!ok) break;
+            tc_fence_after();
+          }
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st32(o_addr + 32 * c, o);
+          }
+          tmem_st_wait();
+        }
+        if constexpr (!E4M3) {
+          if ((u + 1) * kTile > U.keys || u * kTile < U.lo) {      // weight 0 does not silence an infinity
+            const uint32_t y = ring + 2 * k + 1, st = y % kSlots;
+            ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[st], (y / kSlots) & 1, status));
+            if (!ok) break;
+            if (u * kTile + r >= U.keys || u * kTile + r < U.lo) clear_row<D>(smem + L::kKV + st * L::kTileBytes, r);
+            fence_proxy_async_smem();
+            __syncwarp();              // P is stored by the whole warp
+          }
+        }
+        const float shrink = shrink_for(m);
+        const float neg = (m == -INFINITY ? 0.f : -m) * shrink, fs = fmaxf(scale2 * shrink, 0x1p-126f);   // (0 * -inf)
+        // P in two halves of 64 keys: the first one's product starts while the second is computed
+        auto exps = [&](auto FORM) {
+          constexpr int kForm = decltype(FORM)::value;
+          const float2 f2 = make_float2(fs, fs), n2 = make_float2(neg, neg);
+          const CapForm& F = p.capf;
+          auto arg = [&](int g, int c) {
+            const float2 y = pair_of(v[g], c);
+            if constexpr (kForm == 1 || kForm == 2) {       // y (scale2 + scale2 t(y^2)) + n
+              const float2 q = fmul2(y, y);
+              float2 z;
+              if constexpr (kForm == 1) {
+                z = ffma2(q, F.e3[3], F.e3[2]);
+                z = ffma2(q, z, F.e3[1]);
+                z = ffma2(q, z, F.e3[0]);
+              } else {
+                z = ffma2(q, F.e5[5], F.e5[4]);
+                z = ffma2(q, z, F.e5[3]);
+                z = ffma2(q, z, F.e5[2]);
+                z = ffma2(q, z, F.e5[1]);
+                z = ffma2(q, z, F.e5[0]);
+              }
+              return ffma2(y, z, n2);
+            } else {
+              return ffma2(y, f2, n2);
+            }
+          };
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int j = 0; j < 64; j += 4) {
+              const int g = 2 * half + j / 32, c = j % 32;
+              float2 e0 = arg(g, c), e1 = arg(g, c + 2);
+              e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
+              e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
+              la = fadd2(la, e0);
+              lb = fadd2(lb, e1);
+              const __nv_bfloat162 b0 = __floats2bfloat162_rn(e0.x, e0.y), b1 = __floats2bfloat162_rn(e1.x, e1.y);
+              pk[j / 2] = *reinterpret_cast<const uint32_t*>(&b0);
+              pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&b1);
+            }
+            if (kSplit && half == 0 && ns) {       // the last P has been read
+              ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[w], (ns - 1) & 1, status));
+              if (!ok) return;
+              tc_fence_after();
+            }
+            tmem_st32(p_addr + 32 * half, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&p_full[2 * w + half]);
+          }
+        };
+        if constexpr (CAP) {
+          if (form == 1) exps(std::integral_constant<int, 1>{});
+          else if (form == 2) exps(std::integral_constant<int, 2>{});
+          else exps(std::integral_constant<int, 0>{});
+        } else {
+          exps(std::integral_constant<int, 0>{});
+        }
+        if (!ok) break;
+        ++ns;
+        first = false;
+      }
+      ring += 2 * nk;
+      if (!ok) break;
+      // O: of a whole unit divided and rounded, of a piece as it is
+      const float l = (la.x + la.y) + (lb.x + lb.y);
+      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[w], nu & 1, status));
+      if (!ok) break;
+      ++nu;
+      tc_fence_after();
+      const int64_t tok = (int64_t)U.start + x / group;
+      const int h = U.h * group + x % group;
+      float* part = cached_part<false, D>(p, blockIdx.x, max(U.slot, 0));
+      const float inv = 1.f / l;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        __syncwarp();              // (some rows alone have stored the last columns)
+        tmem_ld32(o_addr + 32 * c, o);
+        tmem_ld_wait();
+        if (c == D / 32 - 1) {
+          tc_fence_before();
+          mbar_arrive(&o_free[w]);
+        }
+        if (!row_in) continue;
+        if (U.slot < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + (tok * p.hq + h) * D + 32 * c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * i]) * inv,
+                                                              __uint_as_float(o[8 * j + 2 * i + 1]) * inv);
+              y[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            dst[j] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(part + (size_t)rr * D + 32 * c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      }
+      __syncwarp();
+      if (row_in) {
+        if (U.slot < 0) {
+          p.lse[(int64_t)h * p.c.T + tok] = (m + log2f(l)) * kLn2;
+        } else {
+          part[(size_t)kChunkRows * D + rr] = m;
+          part[(size_t)kChunkRows * (D + 1) + rr] = l;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ unpack
+    setmaxnreg_dec<kRegAux>();
+    if constexpr (E4M3) {
+      const int r = (warp & 3) * 32 + lane;
+      uint32_t ring = 0;
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        const Piece U = read_piece(units, unit_full, unit_done, n, true, ok, status);
+        if (U.tiles == 0) break;
+        for (int k = 0; k < 2 * U.tiles && ok; ++k, ++ring) {
+          const uint32_t st = ring % L::kRaw, to = ring % kSlots;
+          const int key = (U.last - (k >> 1)) * kTile + r;
+          if (!(ok = warp_wait(&raw_full[st], (ring / L::kRaw) & 1, status))) break;
+          if (ring >= kSlots && !(ok = warp_wait(&kv_empty[to], (ring / kSlots - 1) & 1, status))) break;
+          unpack_row<D>(smem + L::kCodes + st * L::kRawBytes, smem + L::kKV + to * L::kTileBytes, r,
+                        smem[L::kScales + st * kTile + r], key < U.keys && key >= U.lo);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&raw_empty[st]);
+            mbar_arrive(&kv_full[to]);
+          }
+        }
+      }
+    }
+  }
+  grid_wait();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int D, bool E4M3, bool CAP>
+cudaError_t launch(const CachedParams& p, bool tail, cudaStream_t stream) {
+  using L = ChunkSmem<D, E4M3>;
+  CUtensorMap tk, tv;
+  const uint64_t P = (uint64_t)1 << p.c.page_shift, pages = (uint64_t)p.c.num_pages * p.c.hkv, row = E4M3 ? D : 2 * D;
+  const uint32_t box = row < 128 ? (uint32_t)row : 128;
+  if (!make_tmap_u8_3d(&tk, p.c.k, row, pages, P, P * row, row, box, (uint32_t)P) ||
+      !make_tmap_u8_3d(&tv, p.c.v, row, pages, P, P * row, row, box, (uint32_t)P))
+    return cudaErrorInvalidValue;
+  int regs = 0;
+  static_assert(L::kAlloc <= 232448, "shared memory of one CTA");
+  cudaError_t e = prepare_kernel<cached_chunk_kernel<D, E4M3, CAP>>(L::kAlloc, &regs);
+  if (e != cudaSuccess) return e;
+  if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;    // the register split relies on it
+  // starts while the steps still run: it reads nothing of theirs
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kChunkCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = tail ? 0 : 1;
+  return cudaLaunchKernelEx(&cfg, cached_chunk_kernel<D, E4M3, CAP>, tk, tv, p, tail);
+}
+
+template <int D>
+cudaError_t launch_d(bool e4m3, CachedParams p, bool tail, cudaStream_t s) {
+  p.scale2 = (float)((double)p.scale2 * mma_gain(D));
+  p.capf = cap_form(p.scale * mma_gain(D), (double)p.cap);
+  if (e4m3) return p.cap > 0.f ? launch<D, true, true>(p, tail, s) : launch<D, true, false>(p, tail, s);
+  return p.cap > 0.f ? launch<D, false, true>(p, tail, s) : launch<D, false, false>(p, tail, s);
+}
+
+}  // namespace
+
+// tail: no steps are launched in front, so the rows behind the last sequence are cleared here.
+cudaError_t launch_cached_chunk(int D, bool e4m3, const CachedParams& p, bool tail, cudaStream_t s) {
+  return D == 128 ? launch_d<128>(e4m3, p, tail, s) : launch_d<64>(e4m3, p, tail, s);
+}
+
+}  // namespace flamia

@@ -29,6 +29,8 @@
 
 namespace flamia {
 
+cudaError_t launch_cached_chunk(int D, bool e4m3, const CachedParams& p, bool tail, cudaStream_t s);
+
 namespace {
 
 constexpr int kComputeWarps = 4, kThreads = (kComputeWarps + 1) * 32;
@@ -511,58 +513,70 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// The pieces of the unit that begins in CTA blockIdx.x's share and ends behind it: a warp a row.
+// Joins the pieces of the unit that begins in CTA c's share and ends behind it: a warp a row.
+constexpr int kJoinWarps = 4, kStepJoin = kStepRows / kJoinWarps, kChunkJoin = 8;      // blocks a unit
 template <int D, bool STEP>
-__global__ void __launch_bounds__(128) cached_join_kernel(const CachedParams p) {
+__device__ __forceinline__ void join(const CachedParams& p, int valid, int c, int first, int stride) {
   constexpr int kRows = STEP ? kStepRows : kChunkRows, kPer = D / 32;
-  const int valid = cached_valid_rows(p);
   const CachePlanView pv = cache_plan_view(p.c.plan, p.c.T, p.c.N, p.hq, p.c.hkv);
   Shares sh{};
   if (valid) sh = cached_shares<STEP>(p, pv);
-  const int c = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   CachedUnit u{};
   const bool some = c + 1 < sh.n;
   if (some) u = cached_unit<STEP>(p, pv, sh.begin(c + 1) - 1);
   grid_wait();
-  if (!some || u.begin < sh.begin(c) || u.begin + u.tiles <= sh.begin(c + 1) || r >= u.rows) return;
+  if (!some || u.begin < sh.begin(c) || u.begin + u.tiles <= sh.begin(c + 1)) return;
   const int n = sh.of(u.begin + u.tiles - 1) - c + 1;
   auto piece = [&](int i) { return cached_part<STEP, D>(p, c + i, i == 0 ? 1 : 0); };
-  float top = -INFINITY, l = 0.f;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, piece(i)[kRows * D + r]);
+  for (int r = first; r < u.rows; r += stride) {
+    float top = -INFINITY, l = 0.f;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, piece(i)[kRows * D + r]);
 #pragma unroll
-  for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-  const float neg = top == -INFINITY ? 0.f : -top;
-  float o[kPer] = {};
-  for (int b = 0; b < n; b += 32) {
-    const int i = b + lane;
-    const float wt = i < n ? fast_exp2(piece(i)[kRows * D + r] + neg) : 0.f;
-    if (i < n) l += wt * piece(i)[kRows * (D + 1) + r];
-    const int some = min(32, n - b);
+    for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    const float neg = top == -INFINITY ? 0.f : -top;
+    float o[kPer] = {};
+    for (int b = 0; b < n; b += 32) {
+      const int i = b + lane;
+      const float wt = i < n ? fast_exp2(piece(i)[kRows * D + r] + neg) : 0.f;
+      if (i < n) l += wt * piece(i)[kRows * (D + 1) + r];
+      const int here = min(32, n - b);
 #pragma unroll 8
-    for (int j = 0; j < some; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, wt, j);
-      const float* src = piece(b + j) + r * D + lane * kPer;
-      if constexpr (D == 128) {
-        const float4 y = *reinterpret_cast<const float4*>(src);
-        o[0] = fmaf(wj, y.x, o[0]);
-        o[1] = fmaf(wj, y.y, o[1]);
-        o[2] = fmaf(wj, y.z, o[2]);
-        o[3] = fmaf(wj, y.w, o[3]);
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(src);
-        o[0] = fmaf(wj, y.x, o[0]);
-        o[1] = fmaf(wj, y.y, o[1]);
+      for (int j = 0; j < here; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, wt, j);
+        const float* src = piece(b + j) + r * D + lane * kPer;
+        if constexpr (D == 128) {
+          const float4 y = *reinterpret_cast<const float4*>(src);
+          o[0] = fmaf(wj, y.x, o[0]);
+          o[1] = fmaf(wj, y.y, o[1]);
+          o[2] = fmaf(wj, y.z, o[2]);
+          o[3] = fmaf(wj, y.w, o[3]);
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          o[0] = fmaf(wj, y.x, o[0]);
+          o[1] = fmaf(wj, y.y, o[1]);
+        }
       }
     }
+#pragma unroll
+    for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+    const int2 at = cached_row(p, u, r);
+    const float inv = 1.f / l;
+    __nv_bfloat16* dst = p.out + ((int64_t)at.x * p.hq + at.y) * D + lane * kPer;
+#pragma unroll
+    for (int j = 0; j < kPer; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack2<false>(o[j] * inv, o[j + 1] * inv);
+    if (lane == 0) p.lse[(int64_t)at.y * p.c.T + at.x] = (top + log2f(l)) * kLn2;
   }
-#pragma unroll
-  for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-  const int2 at = cached_row(p, u, r);
-  const float inv = 1.f / l;
-  __nv_bfloat16* dst = p.out + ((int64_t)at.x * p.hq + at.y) * D + lane * kPer;
-#pragma unroll
-  for (int j = 0; j < kPer; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack2<false>(o[j] * inv, o[j + 1] * inv);
-  if (lane == 0) p.lse[(int64_t)at.y * p.c.T + at.x] = (top + log2f(l)) * kLn2;
+}
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) cached_join_kernel(const CachedParams p, const int step_blocks) {
+  const int valid = cached_valid_rows(p), warp = threadIdx.x >> 5, b = blockIdx.x;
+  if (b < step_blocks) {
+    join<D, true>(p, valid, b / kStepJoin, (b % kStepJoin) * kJoinWarps + warp, kStepRows);
+  } else {
+    const int x = b - step_blocks;
+    join<D, false>(p, valid, x / kChunkJoin, (x % kChunkJoin) * kJoinWarps + warp, kChunkJoin * kJoinWarps);
+  }
 }
 
 template <int D, bool E4M3, bool CAP>
@@ -586,25 +600,32 @@ cudaError_t launch_d(bool e4m3, const CachedParams& p, cudaStream_t s) {
   return p.cap > 0.f ? launch<D, false, true>(p, s) : launch<D, false, false>(p, s);
 }
 
-}  // namespace
-
-cudaError_t launch_cached_step(int D, bool e4m3, const CachedParams& p, cudaStream_t s) {
-  return D == 128 ? launch_d<128>(e4m3, p, s) : launch_d<64>(e4m3, p, s);
-}
-
-// Starts while the launch before still runs, and waits for it where its results are needed.
-cudaError_t launch_cached_join(int D, bool step, const CachedParams& p, cudaStream_t s) {
+template <int D>
+cudaError_t launch_all(bool e4m3, const CachedParams& p, cudaStream_t s) {
+  const int group = p.hq / p.c.hkv;
+  const bool steps = group <= kStepRows, chunks = (int64_t)p.max_chunk * group > kStepRows;
+  cudaError_t e = cudaSuccess;
+  if (steps) e = launch_d<D>(e4m3, p, s);
+  if (e == cudaSuccess && chunks) e = launch_cached_chunk(D, e4m3, p, !steps, s);
+  if (e != cudaSuccess) return e;
+  // starts while the launch before still runs, and waits for it where its results are needed
+  const int step_blocks = steps ? kStepCtas * kStepJoin : 0;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(step ? kStepCtas : kChunkCtas, (step ? kStepRows : kChunkRows) / 4);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(step_blocks + (chunks ? kChunkCtas * kChunkJoin : 0));
+  cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.stream = s;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  if (step) return D == 128 ? cudaLaunchKernelEx(&cfg, cached_join_kernel<128, true>, p) : cudaLaunchKernelEx(&cfg, cached_join_kernel<64, true>, p);
-  return D == 128 ? cudaLaunchKernelEx(&cfg, cached_join_kernel<128, false>, p) : cudaLaunchKernelEx(&cfg, cached_join_kernel<64, false>, p);
+  return cudaLaunchKernelEx(&cfg, cached_join_kernel<D>, p, step_blocks);
+}
+
+}  // namespace
+
+cudaError_t launch_cached_fwd(int D, bool e4m3, const CachedParams& p, cudaStream_t s) {
+  return D == 128 ? launch_all<128>(e4m3, p, s) : launch_all<64>(e4m3, p, s);
 }
 
 }  // namespace flamia
