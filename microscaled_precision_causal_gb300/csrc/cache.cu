@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         r.z = kv[n];
         r.w = left < 0 ? 0 : max(0, r.z - r.y - left);
         const int64_t rows = (int64_t)r.y * group;
-        if (rows <= kStepRows) st = (r.z + kStepTile - 1) / kStepTile - r.w / kStepTile;
+        if (rows <= kStepRows) st = (r.z + kStepTile - 1) / kStepTile - r.w / kStepTile + kStepExtra;
         else it = (rows + kChunkRows - 1) / kChunkRows;
       }
       pv.seq[n] = r;
@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(kPlanThreads)
       const int last = (int)(min((int64_t)x.row + kChunkRows, rows) - 1) / group;
       const int first = r.z - r.y + x.row / group;
       x.tile = (left < 0 ? 0 : max(0, first - left)) / kTile;
-      cost = x.tiles = (r.z - r.y + last) / kTile - x.tile + 1;
+      x.tiles = (r.z - r.y + last) / kTile - x.tile + 1;
+      cost = x.tiles + kChunkExtra;
       pv.items[i] = x;
     }
     int64_t tot;

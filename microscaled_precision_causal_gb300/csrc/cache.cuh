@@ -10,6 +10,8 @@ namespace flamia {
 constexpr int kStepRows = 16;      // up to so many the sequence is a step: one tile of rows, keys streamed past it
 constexpr int kChunkRows = 2 * kTile;   // rows of a unit otherwise
 constexpr int kStepTile = 64;      // keys a tile of a step
+// What a unit costs besides its key tiles, in key tiles, when the work is dealt out: its queries, its end.
+constexpr int kStepExtra = 3, kChunkExtra = 1;
 
 // ---------------------------------------------------------------- plan
 enum CachePlanWord : int {
@@ -31,10 +33,10 @@ struct CacheItem {
 struct CachePlanView {
   int* hdr;
   int4* seq;               // [N] {first token, new tokens, keys with them, first key that the first new one sees}
-  int64_t* step_prefix;    // [N + 1] key tiles of the steps before
+  int64_t* step_prefix;    // [N + 1] key tiles of the steps before, kStepExtra more for each
   int64_t* item_base;      // [N + 1] chunk items before
   CacheItem* items;        // [cap]
-  int64_t* item_prefix;    // [cap + 1] key tiles of the items before
+  int64_t* item_prefix;    // [cap + 1] key tiles of the items before, kChunkExtra more for each
 };
 __host__ __device__ inline int64_t cache_item_capacity(int64_t T, int N, int hq, int hkv) {
   return T * (hq / hkv) / kChunkRows + N;
@@ -123,20 +125,22 @@ __device__ __forceinline__ int cached_valid_rows(const CachedParams& p) {
 
 // ---------------------------------------------------------------- units and shares
 // A unit is a tile of a sequence's rows (a step: all of them) and a kv head, over the key tiles that its rows see.
-// The key tiles of all units, unit after unit, are dealt out to the CTAs in equal shares, so that every CTA has
-// the same to do whatever the sequences' lengths are; a unit whose tiles lie in several shares is joined after.
+// The places of all units, unit after unit, are dealt out to the CTAs in equal shares, so that every CTA has the same
+// to do whatever the sequences' lengths are: a unit has kExtra places, then one for each key tile.  A unit whose key
+// tiles lie in several shares is joined after.
 struct CachedUnit {
   int seq, h, row, rows, tile, tiles;     // first row, rows, first key tile, key tiles
   int start, count, keys, lo;             // of the sequence (CachePlanView::seq)
-  int64_t begin;                          // number of its first tile among all
+  int64_t begin;                          // its first place
 };
 template <bool STEP>
-__device__ __forceinline__ int64_t cached_tiles(const CachedParams& p, const CachePlanView& pv) {
+__device__ __forceinline__ int64_t cached_places(const CachedParams& p, const CachePlanView& pv) {
   return (STEP ? pv.step_prefix[p.c.N] : pv.item_prefix[pv.hdr[kCpItems]]) * p.c.hkv;
 }
-// The unit of tile f (found by a whole warp).
+// The unit of place f (found by a whole warp).
 template <bool STEP>
 __device__ __forceinline__ CachedUnit cached_unit(const CachedParams& p, const CachePlanView& pv, int64_t f) {
+  constexpr int kExtra = STEP ? kStepExtra : kChunkExtra;
   CachedUnit u;
   const int64_t* prefix = STEP ? pv.step_prefix : pv.item_prefix;
   const int hkv = p.c.hkv;
@@ -154,10 +158,19 @@ __device__ __forceinline__ CachedUnit cached_unit(const CachedParams& p, const C
   u.row = item.row;
   u.rows = STEP ? rows : min(rows - u.row, kChunkRows);
   u.tile = STEP ? r.w / kStepTile : item.tile;
-  u.tiles = STEP ? (int)(prefix[i + 1] - prefix[i]) : item.tiles;
-  u.h = (int)((f - first) / u.tiles);
-  u.begin = first + (int64_t)u.h * u.tiles;
+  u.tiles = STEP ? (int)(prefix[i + 1] - prefix[i]) - kExtra : item.tiles;
+  u.h = (int)((f - first) / (u.tiles + kExtra));
+  u.begin = first + (int64_t)u.h * (u.tiles + kExtra);
   return u;
+}
+// A share's part of a unit: key tiles [t0, t1), none where the share ends before the first; f moves behind it.
+template <bool STEP>
+__device__ __forceinline__ int2 cached_piece(const CachedUnit& u, int64_t& f, int64_t end) {
+  constexpr int kExtra = STEP ? kStepExtra : kChunkExtra;
+  const int64_t to = min(u.begin + kExtra + u.tiles, end);
+  const int2 t = make_int2(max((int)(f - u.begin) - kExtra, 0), max((int)(to - u.begin) - kExtra, 0));
+  f = to;
+  return t;
 }
 struct Shares {
   int64_t total;
@@ -165,14 +178,24 @@ struct Shares {
   __device__ __forceinline__ int64_t begin(int c) const { return total * c / n; }
   __device__ __forceinline__ int of(int64_t f) const { return (int)(((f + 1) * n - 1) / total); }   // the last c with begin(c) <= f
 };
-// A CTA takes kLeast tiles at least: fewer would cost more in joining than they save.
+// A CTA takes kLeast places at least: fewer would cost more in joining than they save.
 template <bool STEP>
 __device__ __forceinline__ Shares cached_shares(const CachedParams& p, const CachePlanView& pv) {
-  constexpr int kCtas = STEP ? kStepCtas : kChunkCtas, kLeast = STEP ? 4 : 2;
+  constexpr int kCtas = STEP ? kStepCtas : kChunkCtas, kLeast = STEP ? 4 + kStepExtra : 2 + kChunkExtra;
   Shares s;
-  s.total = cached_tiles<STEP>(p, pv);
+  s.total = cached_places<STEP>(p, pv);
   s.n = (int)min((int64_t)kCtas, (s.total + kLeast - 1) / kLeast);
   return s;
+}
+// The unit that begins in CTA c's share and ends behind it, whose pieces in c .. c + n - 1 are to be joined; n = 0: none.
+template <bool STEP>
+__device__ __forceinline__ int cached_split(const CachedParams& p, const CachePlanView& pv, const Shares& sh, int c,
+                                            CachedUnit& u) {
+  if (c + 1 >= sh.n) return 0;
+  u = cached_unit<STEP>(p, pv, sh.begin(c + 1) - 1);
+  const int64_t first = u.begin + (STEP ? kStepExtra : kChunkExtra), last = first + u.tiles - 1;
+  if (first < sh.begin(c) || first >= sh.begin(c + 1) || last < sh.begin(c + 1)) return 0;
+  return sh.of(last) - c + 1;
 }
 // Unfinished pieces: the one that a CTA's share begins in the middle of (0), and the one that it ends in the middle of and
 // has the beginning of (1).  [rows][D] weighted values, [rows] references (base 2), [rows] sums.

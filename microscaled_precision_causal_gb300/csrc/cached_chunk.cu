@@ -69,6 +69,39 @@ __device__ __forceinline__ Piece read_piece(const uint8_t* units, uint64_t* full
   return x.p;
 }
 
+// A row tile's products capped, in their own units: the short polynomials where every product of the warp's rows allows
+// one, else 1 - 2 / (1 + 2^(2 z log2 e)) for all.  Its error beside 0 is some 2^-22 of the cap, which only tiles
+// with scores near the cap get, and it has no branches: an element's choice between it and a polynomial
+// took three times as long (ragged chunks, cap 30, d 64: 206 us, without a cap 65).
+__device__ __forceinline__ void cap_tile(uint32_t (&v)[4][32], const CapForm& F, bool counts) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 32; j += 2)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) m[g] = fmax3(m[g], fabsf(__uint_as_float(v[g][j])), fabsf(__uint_as_float(v[g][j + 1])));
+  const float am = fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
+  if (!__any_sync(0xffffffffu, counts && !(am <= F.t5))) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float2 x = pair_of(v[g], j), w = fmul2(x, x);
+        float2 t = ffma2(w, F.k5[4], F.k5[3]);
+        t = ffma2(w, t, F.k5[2]);
+        t = ffma2(w, t, F.k5[1]);
+        t = ffma2(w, t, F.k5[0]);
+        put_pair(v[g], j, ffma2(x, fmul2(w, t), x));
+      }
+  } else {
+    const float z2 = F.zscale * (2.f * kLog2e), two = -2.f * F.inv;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        v[g][j] = __float_as_uint(fmaf(two, fast_rcp(1.f + fast_exp2(__uint_as_float(v[g][j]) * z2)), F.inv));
+  }
+}
+
 template <int D, bool E4M3>
 struct ChunkSmem {
   static constexpr int kTileBytes = kTile * D * 2;
@@ -95,36 +128,47 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&x);
 }
-// Two codes, each in the upper byte of a half word, times 2^-120 as bf16: sign, exponent and mantissa bits moved to
-// their places (subnormal codes become subnormal bf16 values of the same meaning).
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t t) { return ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u); }
-
-// A row of codes -> bf16 values times their scale 2^(b - 127).  One factor 2^(b - 7) up to b = 134; above, 2^120
-// first, then 2^(b - 127).
-template <int D>
-__device__ __forceinline__ void unpack_row(const uint8_t* raw, uint8_t* tile, int r, uint32_t b, bool use) {
-  const bool big = b > 134;
-  const uint32_t f1 = big ? 0x7b807b80u : (b + 120) * 0x00800080u, f2 = b == 255 ? 0x7fc07fc0u : b * 0x00800080u;
+// Two codes of a word (the pair that SEL picks, each extended by its sign to a half word) times 2^-120 as bf16: exponent
+// and mantissa bits four places up, the sign's other copies masked.  Subnormal codes become subnormal values of
+// the same meaning.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w) {
+  uint32_t x;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(x) : "r"(w), "n"(SEL));
+  return (x << 4) & 0x87f087f0u;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
+  return x;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// Row r of a tile of codes -> bf16 values times their scale 2^(b - 127).  One factor 2^(b - 7) up to b = 134; above,
+// 2^120 first, then 2^(b - 127) (NaN for 255).
+template <int D, bool BIG>
+__device__ __forceinline__ void unpack_row(uint32_t raw, uint32_t tile, int r, uint32_t b) {
+  const uint32_t f1 = BIG ? 0x7b807b80u : (b + 120) * 0x00800080u, f2 = b == 255 ? 0x7fc07fc0u : b * 0x00800080u;
+  const uint32_t src = raw + swz_offset(r, 0, D), dst = tile + swz_offset(r, 0, 128);
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
-    const uint4 c = *reinterpret_cast<const uint4*>(raw + swz_offset(r, 16 * j, D));
+    const uint4 c = lds128(src ^ (16 * j));
     const uint32_t w[4] = {c.x, c.y, c.z, c.w};
     uint32_t y[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      y[2 * i] = mul_bf16x2(codes_bf16(__byte_perm(w[i], 0, 0x1404)), f1);
-      y[2 * i + 1] = mul_bf16x2(codes_bf16(__byte_perm(w[i], 0, 0x3424)), f1);
+      y[2 * i] = mul_bf16x2(codes_bf16<0x9180>(w[i]), f1);
+      y[2 * i + 1] = mul_bf16x2(codes_bf16<0xb3a2>(w[i]), f1);
     }
-    if (big) {
+    if constexpr (BIG) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = mul_bf16x2(y[i], f2);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int col = 32 * j + 16 * i;       // byte of the row
-      *reinterpret_cast<uint4*>(tile + (col >> 7) * kTile * 128 + swz_offset(r, col & 127, 128)) =
-          use ? make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]) : make_uint4(0, 0, 0, 0);
-    }
+    // (the tiles are aligned to their swizzle's period, so a column is an exclusive or)
+    const uint32_t to = (dst ^ (32 * j & 127)) + (32 * j >> 7) * kTile * 128;
+    sts128(to, y[0], y[1], y[2], y[3]);
+    sts128(to ^ 16, y[4], y[5], y[6], y[7]);
   }
 }
 
@@ -276,10 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = 0; ok; ++n) {
         if (n >= kUnits && !(ok = warp_wait(&unit_done[n % kUnits], (n / kUnits - 1) & 1, status))) break;
         Piece U{};
-        if (f < f1) {
+        while (f < f1 && U.tiles == 0) {
           const CachedUnit u = cached_unit<false>(p, pv, f);
-          const int t0 = (int)(f - u.begin), t1 = (int)min((int64_t)u.tiles, f1 - u.begin);
-          f += t1 - t0;
+          const int2 piece = cached_piece<false>(u, f, f1);
+          const int t0 = piece.x, t1 = piece.y;
           U.tiles = t1 - t0;
           U.last = u.tile + u.tiles - 1 - t0;
           U.h = u.h;
@@ -494,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int g = 0; g < 4; ++g) hide(v[g], see[g], 0u);
             }
-            cap_products(v, p.capf, row_in);
+            cap_tile(v, p.capf, row_in);
           }
           if (!seen) {
 #pragma unroll
@@ -675,8 +719,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int key = (U.last - (k >> 1)) * kTile + r;
           if (!(ok = warp_wait(&raw_full[st], (ring / L::kRaw) & 1, status))) break;
           if (ring >= kSlots && !(ok = warp_wait(&kv_empty[to], (ring / kSlots - 1) & 1, status))) break;
-          unpack_row<D>(smem + L::kCodes + st * L::kRawBytes, smem + L::kKV + to * L::kTileBytes, r,
-                        smem[L::kScales + st * kTile + r], key < U.keys && key >= U.lo);
+          const uint32_t raw = smem_u32(smem + L::kCodes + st * L::kRawBytes), tile = smem_u32(smem + L::kKV + to * L::kTileBytes);
+          const uint32_t b = smem[L::kScales + st * kTile + r];
+          if (key >= U.keys || key < U.lo) clear_row<D>(smem + L::kKV + to * L::kTileBytes, r);
+          else if (b <= 134) unpack_row<D, false>(raw, tile, r, b);
+          else unpack_row<D, true>(raw, tile, r, b);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
