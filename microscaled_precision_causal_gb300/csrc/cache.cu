@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int64_t warp_sums[32];
   __shared__ int s_bad;
   const CachePlanView pv = cache_plan_view(plan, T, N, hq, hkv);
-  const int group = hq / hkv;
+  const int group = hq / hkv, limit = step_rows(group, max_chunk);
   if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
   for (int n = threadIdx.x; n < N; n += kPlanThreads) {
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         r.z = kv[n];
         r.w = left < 0 ? 0 : max(0, r.z - r.y - left);
         const int64_t rows = (int64_t)r.y * group;
-        if (rows <= kStepRows) st = (r.z + kStepTile - 1) / kStepTile - r.w / kStepTile + kStepExtra;
+        if (rows <= limit) st = (r.z + kStepTile - 1) / kStepTile - r.w / kStepTile + kStepExtra;
         else it = (rows + kChunkRows - 1) / kChunkRows;
       }
       pv.seq[n] = r;

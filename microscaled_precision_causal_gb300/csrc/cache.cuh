@@ -7,9 +7,14 @@
 namespace flamia {
 
 // Rows of a kv head in a sequence: its new tokens times the query heads that share the head, token by token.
-constexpr int kStepRows = 16;      // up to so many the sequence is a step: one tile of rows, keys streamed past it
+constexpr int kStepRows = 16;      // up to so many a sequence may be a step: one tile of rows, keys streamed past it
 constexpr int kChunkRows = 2 * kTile;   // rows of a unit otherwise
 constexpr int kStepTile = 64;      // keys a tile of a step
+// Rows up to which a call's sequences are steps.  In a call that has chunks too, 8 where a token's rows fit in: its steps
+// then cost half of what 16 rows do, and the few sequences between the two go with the chunks.
+__host__ __device__ inline int step_rows(int group, int64_t max_chunk) {
+  return max_chunk * group > kStepRows && group <= 8 ? 8 : kStepRows;
+}
 // What a unit costs besides its key tiles, in key tiles, when the work is dealt out: its queries, its end.
 constexpr int kStepExtra = 3, kChunkExtra = 1;
 
@@ -113,7 +118,7 @@ struct CachedParams {
 constexpr int kStepCtas = 304, kChunkCtas = 152;
 inline size_t cached_workspace_bytes(int hq, int hkv, int d, int max_chunk) {
   const size_t row = (size_t)(d + 2) * 4;
-  return 2 * row * ((size_t)kStepCtas * kStepRows + ((int64_t)max_chunk * (hq / hkv) > kStepRows ? (size_t)kChunkCtas * kChunkRows : 0));
+  return 2 * row * ((size_t)kStepCtas * kStepRows + ((int64_t)max_chunk * (hq / hkv) > step_rows(hq / hkv, max_chunk) ? (size_t)kChunkCtas * kChunkRows : 0));
 }
 __device__ __forceinline__ int cached_valid_rows(const CachedParams& p) {
   const int* h = p.c.plan;

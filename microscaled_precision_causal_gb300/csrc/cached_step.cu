@@ -4,22 +4,25 @@
 //   x = scale log2 e q.k (capped), m = running maximum, l += 2^(x - m), O += 2^(x - m) v
 //
 // Bound by memory: every key and value is read once, for 4 d flops a row.  A CTA streams its share of
-// the key tiles (64 keys, K and V) through shared memory: one warp issues TMA copies page by page,
-// four compute warps take 16 keys each with a softmax of their own and meet only where a unit ends.
+// the key tiles (64 keys, K and V) through shared memory: one warp issues TMA copies page by page, two compute
+// warps take every other tile each, 32 keys a warp with a softmax of its own, and meet only where a unit ends.
 // Two CTAs an SM, so that one streams while the other meets, with some 128 KB in flight between them.
 //
-// The products run as 16 x 8 x 16 MMAs from registers: 16 rows are one tile, and what is to be fast
-// here is the stream, not the products (tcgen05 would want 64 rows at least, and the codes unpacked into
-// shared memory).  Which of the head dimensions a lane's operand words stand for is free as long
-// as both operands agree, so a lane takes whole 16-byte words of a key's row, and for V of one head-dim
-// run in four keys' rows, whose bytes are paired by permutes; with the 128-byte swizzle of the copies
-// both are free of bank conflicts.
+// The products run as 16 x 8 x 16 MMAs from registers, keys (then head dimensions) as the 16 and query rows as the 8:
+// what is to be fast here is the stream, not the products, and a step's rows rarely fill more (tcgen05 would
+// want 64 at least and the codes unpacked into shared memory; rows as the 16 cost twice the softmax and twice
+// the accumulators: 98 instead of XX us on two sequences of 131972).  Which of the head dimensions a lane's operand
+// words stand for is free as long as both operands agree, so a lane takes whole 16-byte words of a key's row,
+// and for V of one head-dim run in four keys' rows, whose bytes are paired by permutes; with the copies' swizzle
+// both are free of bank conflicts.  The weights change from scores' to operands' places by a transpose
+// of 8 x 8 within the warp.
 //
 // E4M3: a code is exact in fp16, two are converted at a time, and the products run in fp16.  Queries are
 // scaled by a power of two a row, its largest value to [2^14, 2^15).  The key's scale multiplies the
 // score.  The value's scale 2^e enters the weight: w = 2^(x - m + e - M + 13) with a running maximum M of x - m + e
 // of its own (against m, so that scores of any size leave the exponents their digits): the largest w is in
-// [2^13, 2^15] whatever the scales are, and what falls below fp16's range is 2^-38 of it.  Rounding w to fp16 costs 2^-12 of it at most.
+// [2^13, 2^15] whatever the scales are, and what falls below fp16's range is 2^-38 of it.  Rounding w
+// to fp16 costs 2^-12 of it at most.
 // bf16: the products run in bf16, and so do the weights (2^-9 at most).
 #include <type_traits>
 
@@ -94,33 +97,31 @@ __device__ __forceinline__ float cap_one(float x, const CapForm& F) {
   return fabsf(z) <= kTanh5To ? fmaf(x, w * t, x) : F.inv * tanh_any(z);
 }
 
-template <int N>
-__device__ __forceinline__ void scale_rows(float (&o)[N][4], int r, float f) {
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    o[n][2 * r] *= f;
-    o[n][2 * r + 1] *= f;
-  }
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NT>
 struct StepSmem {
   static constexpr int kRowBytes = E4M3 ? D : 2 * D;
   static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;
   static constexpr int kBoxes = kRowBytes / kBoxBytes;
   static constexpr int kTileBytes = kStepTile * kRowBytes;                    // of K, or of V
-  [[maybe_unused]] static constexpr int kScales = 2 * kTileBytes;             // in a stage: K's and V's scale bytes
-  static constexpr int kStage = 2 * kTileBytes + (E4M3 ? 1024 : 0);           // (stages stay on 1024 bytes)
+  static constexpr int kScales = 2 * kTileBytes;                              // in a stage: K's and V's scale bytes
+  static constexpr int kStage = kScales + (E4M3 ? 1024 : 0);           // (stages stay on 1024 bytes)
   static constexpr int kStages = E4M3 ? (D == 128 ? 4 : 6) : (D == 128 ? 2 : 4);
-  static constexpr int kRed = kStages * kStage;                               // [4 warps][16 rows][D] floats
-  static constexpr int kStat = kRed + kComputeWarps * kStepRows * D * 4;      // [4 warps][m, l][16]
-  static constexpr int kQ = kStat + kComputeWarps * 2 * kStepRows * 4;        // [2 units in turn][16 rows] queries
-  static constexpr int kUnit = kQ + kUnits * kStepRows * D * 2;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kRed = kStages * kStage;                               // [4 warps][kRows][D] floats
+  static constexpr int kStat = kRed + kComputeWarps * kRows * D * 4;          // [4 warps][m, l][kRows]
+  static constexpr int kQ = kStat + kComputeWarps * 2 * kRows * 4;            // [2 units in turn][kRows] queries
+  static constexpr int kUnit = kQ + kUnits * kRows * D * 2;
   static constexpr int kBar = kUnit + kUnits * 64;
   static constexpr int kBytes = kBar + (2 * kStages + 2 * kUnits) * 8;
   static constexpr int kAlloc = kBytes + 1024;
 };
-static_assert(2 * (StepSmem<128, false>::kAlloc + 1024) <= 233472 && 2 * (StepSmem<128, true>::kAlloc + 1024) <= 233472,
+static_assert(2 * (StepSmem<128, false, 2>::kAlloc + 1024) <= 233472 && 2 * (StepSmem<128, true, 2>::kAlloc + 1024) <= 233472,
               "two CTAs an SM");
 
 // O = 0, LSE = +inf behind the last sequence.
@@ -135,11 +136,12 @@ __device__ __forceinline__ void clear_rows(const CachedParams& p, int D, int val
   }
 }
 
-template <int D, bool E4M3, bool CAP>
+// NT: tiles of 8 query rows.
+template <int D, bool E4M3, bool CAP, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     cached_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const CachedParams p) {
-  using L = StepSmem<D, E4M3>;
+  using L = StepSmem<D, E4M3, NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kComputeWarps);
+      mbar_init(&empty[i], kComputeWarps / 2);
     }
     for (int i = 0; i < kUnits; ++i) {
       mbar_init(&unit_full[i], 33);            // the producer's lanes as their copies land, and the description
@@ -212,12 +214,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       // queries: 16 bytes a lane and copy, rows behind the unit's are zeros
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;
 #pragma unroll
-      for (int i = 0; i < kStepRows / kPer; ++i) {
+      for (int i = 0; i < L::kRows / kPer; ++i) {
         const int r = i * kPer + lane / kLanes, c = lane % kLanes;
         const bool in = t1 > 0 && r < u.rows;
         const int2 at = in ? cached_row(p, u, r) : make_int2(0, 0);
         const __nv_bfloat16* src = p.q + ((int64_t)at.x * p.hq + at.y) * D + 8 * c;
-        const uint32_t dst = smem_u32(smem + L::kQ + ((n % kUnits) * kStepRows + r) * D * 2 + 16 * c);
+        const uint32_t dst = smem_u32(smem + L::kQ + ((n % kUnits) * L::kRows + r) * D * 2 + 16 * c);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&unit_full[n % kUnits])) : "memory");
@@ -276,269 +278,323 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
   // -------------------------------------------------------------- compute
-  constexpr int kSteps = D / 16, kOut = D / 8;
+  constexpr int kSteps = D / 16;
   constexpr int kWords = L::kRowBytes / 8 / 4;       // a lane's words of a value row
-  const int g = lane >> 2, q = lane & 3;
+  constexpr int kOut = D / 16;                       // tiles of 16 head dimensions
+  const int g = lane >> 2, q = lane & 3, pair = warp >> 1;
   float* red = reinterpret_cast<float*>(smem + L::kRed);
   float* stat = reinterpret_cast<float*>(smem + L::kStat);
-  // this lane's places in a stage: words of key row g (8 rows on: 8 rows' bytes on) and of value rows 2 q and 2 q + 1
+  // this lane's places in a stage: words of key row g and of value rows 2 q and 2 q + 1 of the warp's first 8 keys
   constexpr int kLoads = E4M3 ? D / 64 : 2;
+  const int key0 = 32 * (warp & 1);
   int at_k[kLoads], at_v[2];
 #pragma unroll
   for (int j = 0; j < kLoads; ++j)
-    at_k[j] = 16 * warp * L::kBoxBytes + (E4M3 ? swz_offset(g, (D / 4) * q + 16 * j, L::kBoxBytes) : swz_offset(g, (2 * q + j) * 16, 128));
+    at_k[j] = key0 * L::kBoxBytes + (E4M3 ? swz_offset(g, (D / 4) * q + 16 * j, L::kBoxBytes) : swz_offset(g, (2 * q + j) * 16, 128));
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    at_v[k] = L::kTileBytes + 16 * warp * L::kBoxBytes + swz_offset(2 * q + k, kWords >= 4 ? 16 * g : 8 * g, L::kBoxBytes);
+    at_v[k] = L::kTileBytes + key0 * L::kBoxBytes + swz_offset(2 * q + k, kWords >= 4 ? 16 * g : 8 * g, L::kBoxBytes);
   for (int n = 0; ok; ++n) {
     // (the warps meet here too: the last unit's sums have been read, and where a wait ran out all of them leave)
     ok = named_bar_and(1, kComputeWarps * 32, warp_wait(&unit_full[n % kUnits], (n / kUnits) & 1, status));
     if (!ok) break;
     const StepPiece u = *reinterpret_cast<const StepPiece*>(smem + L::kUnit + (n % kUnits) * sizeof(StepPiece));
     if (u.t1 == 0) break;
-    // queries: rows g and g + 8, four head dimensions a step of 16
-    uint32_t a[kSteps][4];
-    float rowf[2];
-    int pos[2];
+    // queries as the products' second operand: row 8 t + g, four head dimensions a step of 16.  Scores and
+    // weights then are of rows 8 t + 2 q and + 1
+    uint32_t b[kSteps][NT][2];
+    float2 rowf[NT];
+    int pos[NT][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i;
-      pos[i] = u.pos0 + (r < u.rows ? r : 0) / group;
-      const uint8_t* src = smem + L::kQ + ((n % kUnits) * kStepRows + r) * D * 2;
-      float x[kSteps][4];
+    for (int t = 0; t < NT; ++t) {
+      const uint8_t* src = smem + L::kQ + ((n % kUnits) * L::kRows + 8 * t + g) * D * 2;
       float top = 0.f;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const int d0 = E4M3 ? (D / 4) * q + 4 * s : (s >> 2) * 64 + (2 * q + ((s >> 1) & 1)) * 8 + (s & 1) * 4;
         const uint2 w = *reinterpret_cast<const uint2*>(src + d0 * 2);
+        b[s][t][0] = w.x;
+        b[s][t][1] = w.y;
         if constexpr (E4M3) {
-          x[s][0] = __uint_as_float(w.x << 16);
-          x[s][1] = __uint_as_float(w.x & 0xffff0000u);
-          x[s][2] = __uint_as_float(w.y << 16);
-          x[s][3] = __uint_as_float(w.y & 0xffff0000u);
-          top = fmaxf(fmax3(top, fabsf(x[s][0]), fabsf(x[s][1])), fmaxf(fabsf(x[s][2]), fabsf(x[s][3])));
-        } else {
-          a[s][i] = w.x;
-          a[s][2 + i] = w.y;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            top = fmax3(top, fabsf(__uint_as_float(b[s][t][k] << 16)), fabsf(__uint_as_float(b[s][t][k] & 0xffff0000u)));
         }
       }
-      rowf[i] = CAP ? 1.f : p.scale2;
+      const float f = CAP ? 1.f : p.scale2;
+      rowf[t] = make_float2(f, f);
       if constexpr (E4M3) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int shift = min(14 + 127 - (int)(__float_as_uint(top) >> 23), 126);     // (a row of zeros: any)
-        const float up = exp2i(shift);
-        rowf[i] *= exp2i(-shift);
+        const float up = exp2i(shift), down = f * exp2i(-shift);
+        rowf[t] = make_float2(__shfl_sync(0xffffffffu, down, 8 * q), __shfl_sync(0xffffffffu, down, 8 * q + 4));
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          a[s][i] = pack2<true>(x[s][0] * up, x[s][1] * up);
-          a[s][2 + i] = pack2<true>(x[s][2] * up, x[s][3] * up);
-        }
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            b[s][t][k] = pack2<true>(__uint_as_float(b[s][t][k] << 16) * up, __uint_as_float(b[s][t][k] & 0xffff0000u) * up);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = 8 * t + 2 * q + r;
+        pos[t][r] = u.pos0 + (row < u.rows ? row : 0) / group;
       }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&unit_done[n % kUnits]);
-    float o[kOut][4] = {};
-    float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY};
-    float neg[2] = {0.f, 0.f}, Neg[2] = {0.f, 0.f};      // -m and 13 - M, 0 while they are infinite
-    float2 l[2] = {};
+    float o[kOut][NT][4] = {};
+    float m[NT][2], M[NT][2];
+    float2 l[NT], neg[NT], Neg[NT];      // neg, Neg: -m and 13 - M, 0 while they are infinite
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = M[t][0] = M[t][1] = -INFINITY;
+      l[t] = neg[t] = Neg[t] = make_float2(0.f, 0.f);
+    }
+    auto scale_rows = [&](int t, float f0, float f1) {
+#pragma unroll
+      for (int d = 0; d < kOut; ++d) {
+        o[d][t][0] *= f0;
+        o[d][t][1] *= f1;
+        o[d][t][2] *= f0;
+        o[d][t][3] *= f1;
+      }
+    };
     const int all_see = u.pos0 + 1 - kStepTile;          // tiles up to this key hide none behind a row's position
     const int window = p.left < 0 ? -1 : u.pos0 + (u.rows - 1) / group - p.left;    // tiles from this key on none before one
-    for (int t = u.t0; t < u.t1; ++t, ++ring) {
+    for (int tile = u.t0; tile < u.t1; ++tile, ++ring) {
+      if ((ring & 1) != (uint32_t)pair) continue;
       const uint32_t st = ring % L::kStages;
       if (ok) ok = warp_wait(&full[st], (ring / L::kStages) & 1, status);
       if (!ok) continue;
       const uint8_t* stage = smem + st * L::kStage;
-      const int c0 = (u.tile + t) * kStepTile;
-      // scores: keys c0 + 16 warp + 8 i + 2 q + {0, 1}
-      float s[2][4] = {};
+      const int c0 = (u.tile + tile) * kStepTile;
+      const bool edge = c0 + kStepTile > u.keys || c0 < u.lo;       // what is no key of the sequence may be anything
+      // scores of keys c0 + key0 + 16 i + 8 h + g; two chains of products each
+      float2 x[2][2][NT];        // [i][h][t]
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        float s[2][NT][4] = {};
         if constexpr (E4M3) {
-          uint4 w[D / 64];
+          uint4 w[2][D / 64];
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) w[j] = *reinterpret_cast<const uint4*>(stage + at_k[j] + 8 * i * L::kBoxBytes);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j)
+              w[h][j] = *reinterpret_cast<const uint4*>(stage + at_k[j] + (16 * i + 8 * h) * L::kBoxBytes);
 #pragma unroll
           for (int j = 0; j < kSteps; ++j) {
-            const uint32_t x = (&w[j / 4].x)[j % 4];
-            mma16816<true>(s[i], a[j], codes_f16(x), codes_f16_hi(x));
+            const uint32_t w0 = (&w[0][j / 4].x)[j % 4], w1 = (&w[1][j / 4].x)[j % 4];
+            const uint32_t a[4] = {codes_f16(w0), codes_f16(w1), codes_f16_hi(w0), codes_f16_hi(w1)};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816<true>(s[j & 1][t], a, b[j][t][0], b[j][t][1]);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + at_k[j & 1] + (j >> 1) * kStepTile * 128 + 8 * i * 128);
-            mma16816<false>(s[i], a[2 * j], w.x, w.y);
-            mma16816<false>(s[i], a[2 * j + 1], w.z, w.w);
+            uint4 w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              w[h] = *reinterpret_cast<const uint4*>(stage + at_k[j & 1] + (j >> 1) * kStepTile * 128 + (16 * i + 8 * h) * 128);
+            const uint32_t a0[4] = {w[0].x, w[1].x, w[0].y, w[1].y}, a1[4] = {w[0].z, w[1].z, w[0].w, w[1].w};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              mma16816<false>(s[0][t], a0, b[2 * j][t][0], b[2 * j][t][1]);
+              mma16816<false>(s[1][t], a1, b[2 * j + 1][t][0], b[2 * j + 1][t][1]);
+            }
           }
         }
-      }
-      // values of the same keys, in flight while the softmax runs
-      uint32_t v[4][kWords];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint8_t* src = stage + at_v[k & 1] + 8 * (k >> 1) * L::kBoxBytes;
-        if constexpr (kWords >= 4) {
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int j = 0; j < kWords / 4; ++j) {
-            const uint4 w = *reinterpret_cast<const uint4*>(src + j * kStepTile * 128);
-            v[k][4 * j] = w.x;
-            v[k][4 * j + 1] = w.y;
-            v[k][4 * j + 2] = w.z;
-            v[k][4 * j + 3] = w.w;
-          }
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(src);
-          v[k][0] = w.x;
-          v[k][1] = w.y;
-        }
+          for (int h = 0; h < 2; ++h)
+            x[i][h][t] = fmul2(fadd2(make_float2(s[0][t][2 * h], s[0][t][2 * h + 1]), make_float2(s[1][t][2 * h], s[1][t][2 * h + 1])), rowf[t]);
       }
-      float2 x[2][2];        // [8 keys][row]
-      float2 e[2];           // exponents of the values' scales
+      float e[2][2];           // exponents of the values' scales
       if constexpr (E4M3) {
-        const uint8_t* sc = stage + L::kScales + 16 * warp + 2 * q;
-        float2 k[2];
+        float k[2][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t ks = *reinterpret_cast<const uint16_t*>(sc + 8 * i);
-          const uint32_t vs = *reinterpret_cast<const uint16_t*>(sc + kStepTile + 8 * i);
-          // 2^(byte - 127), but 0 for byte 0: a score that counts is beyond 2^-90
-          k[i] = make_float2(__uint_as_float(ks << 23 & 0x7f800000u), __uint_as_float(ks << 15 & 0x7f800000u));
-          // 2^23 + byte, by its bits
-          e[i] = fadd2(make_float2(__uint_as_float(__byte_perm(vs, 0x4b000000u, 0x7650)),
-                                   __uint_as_float(__byte_perm(vs, 0x4b000000u, 0x7651))),
-                       make_float2(-8388735.f, -8388735.f));
-        }
-        if (c0 + kStepTile > u.keys || c0 < u.lo) {       // what is no key of the sequence may be anything
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int j = c0 + 16 * warp + 8 * i + 2 * q;
-            if (j >= u.keys || j < u.lo) k[i].x = 1.f, e[i].x = 0.f;
-            if (j + 1 >= u.keys || j + 1 < u.lo) k[i].y = 1.f, e[i].y = 0.f;
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t* sc = stage + L::kScales + key0 + 16 * i + 8 * h + g;
+            // 2^(byte - 127), but 0 for byte 0: a score that counts is beyond 2^-90
+            k[i][h] = __uint_as_float((uint32_t)sc[0] << 23);
+            e[i][h] = __uint_as_float(0x4b000000u | sc[kStepTile]) - 8388735.f;       // (2^23 + byte by its bits) - 2^23 - 127
+            if (edge) {
+              const int key = c0 + key0 + 16 * i + 8 * h + g;
+              if (key >= u.keys || key < u.lo) k[i][h] = 1.f, e[i][h] = 0.f;
+            }
           }
-        }
         // byte 255: infinite, and 128
-        if (__any_sync(0xffffffffu, fmaxf(fmax3(k[0].x, k[0].y, k[1].x), k[1].y) == INFINITY ||
-                                        fmaxf(fmax3(e[0].x, e[0].y, e[1].x), e[1].y) > 127.5f)) {
+        if (__any_sync(0xffffffffu, fmaxf(fmax3(k[0][0], k[0][1], k[1][0]), k[1][1]) == INFINITY ||
+                                        fmaxf(fmax3(e[0][0], e[0][1], e[1][0]), e[1][1]) > 127.5f)) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (k[i].x == INFINITY) k[i].x = NAN;
-            if (k[i].y == INFINITY) k[i].y = NAN;
-            if (e[i].x > 127.5f) e[i].x = NAN;
-            if (e[i].y > 127.5f) e[i].y = NAN;
-          }
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (k[i][h] == INFINITY) k[i][h] = NAN;
+              if (e[i][h] > 127.5f) e[i][h] = NAN;
+            }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            x[i][r] = fmul2(fmul2(make_float2(s[i][2 * r], s[i][2 * r + 1]), make_float2(rowf[r], rowf[r])), k[i]);
-      } else {
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) x[i][r] = fmul2(make_float2(s[i][2 * r], s[i][2 * r + 1]), make_float2(rowf[r], rowf[r]));
+            for (int t = 0; t < NT; ++t) x[i][h][t] = fmul2(x[i][h][t], make_float2(k[i][h], k[i][h]));
       }
       if constexpr (CAP) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            x[i][r] = make_float2(cap_one(x[i][r].x, p.capf) * p.scale2, cap_one(x[i][r].y, p.capf) * p.scale2);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              x[i][h][t] = make_float2(cap_one(x[i][h][t].x, p.capf) * p.scale2, cap_one(x[i][h][t].y, p.capf) * p.scale2);
       }
       if (c0 > all_see || c0 < window) {
-        const int j = c0 + 16 * warp + 2 * q;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int j0 = j + 8 * i;
-            if (j0 > pos[r] || (p.left >= 0 && j0 < pos[r] - p.left)) x[i][r].x = -INFINITY;
-            if (j0 + 1 > pos[r] || (p.left >= 0 && j0 + 1 < pos[r] - p.left)) x[i][r].y = -INFINITY;
-          }
-        if (c0 + kStepTile > u.keys || c0 < u.lo) {       // weight 0 does not silence an infinity
+          for (int h = 0; h < 2; ++h) {
+            const int key = c0 + key0 + 16 * i + 8 * h + g;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int jv = j + 8 * (k >> 1) + (k & 1);
-            if (jv >= u.keys || jv < u.lo) {
-#pragma unroll
-              for (int w = 0; w < kWords; ++w) v[k][w] = 0;
+            for (int t = 0; t < NT; ++t) {
+              if (key > pos[t][0] || (p.left >= 0 && key < pos[t][0] - p.left)) x[i][h][t].x = -INFINITY;
+              if (key > pos[t][1] || (p.left >= 0 && key < pos[t][1] - p.left)) x[i][h][t].y = -INFINITY;
             }
           }
-        }
       }
-      float mx[2];
+      float mx[NT][2];
+      auto maxima = [&]() {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) mx[r] = fmaxf(fmax3(x[0][r].x, x[0][r].y, x[1][r].x), x[1][r].y);
-      if (__any_sync(0xffffffffu, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+        for (int t = 0; t < NT; ++t) {
+          mx[t][0] = fmaxf(fmax3(x[0][0][t].x, x[0][1][t].x, x[1][0][t].x), x[1][1][t].x);
+          mx[t][1] = fmaxf(fmax3(x[0][0][t].y, x[0][1][t].y, x[1][0][t].y), x[1][1][t].y);
+        }
+      };
+      auto over = [&](const float (&top)[NT][2]) {
+        bool any = false;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-          mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-          const float m1 = fmaxf(m[r], mx[r]), down = m1 == m[r] ? 0.f : m[r] - m1, f = fast_exp2(down);
-          m[r] = m1;
-          neg[r] = m1 == -INFINITY ? 0.f : -m1;
-          l[r] = fmul2(l[r], make_float2(f, f));
-          if constexpr (E4M3) {
-            M[r] += down;
-            Neg[r] = M[r] == -INFINITY ? 0.f : kBoost - M[r];
-          } else {
-            scale_rows(o, r, f);
+        for (int t = 0; t < NT; ++t) any = any || mx[t][0] > top[t][0] + kSlack || mx[t][1] > top[t][1] + kSlack;
+        return __any_sync(0xffffffffu, any);
+      };
+      auto reduce = [&](float y) {        // over the keys
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+        return fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+      };
+      maxima();
+      if (over(m)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float f[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float m1 = fmaxf(m[t][r], reduce(mx[t][r])), down = m1 == m[t][r] ? 0.f : m[t][r] - m1;
+            f[r] = fast_exp2(down);
+            m[t][r] = m1;
+            if constexpr (E4M3) M[t][r] += down;
           }
+          neg[t] = make_float2(m[t][0] == -INFINITY ? 0.f : -m[t][0], m[t][1] == -INFINITY ? 0.f : -m[t][1]);
+          l[t] = fmul2(l[t], make_float2(f[0], f[1]));
+          if constexpr (E4M3)
+            Neg[t] = make_float2(M[t][0] == -INFINITY ? 0.f : kBoost - M[t][0], M[t][1] == -INFINITY ? 0.f : kBoost - M[t][1]);
+          else
+            scale_rows(t, f[0], f[1]);
         }
       }
-      uint32_t w[4];
-      float2 pr[2][2];
+      uint32_t w[2][2][NT];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          x[i][r] = fadd2(x[i][r], make_float2(neg[r], neg[r]));
-          pr[i][r] = make_float2(fast_exp2(x[i][r].x), fast_exp2(x[i][r].y));
-          l[r] = fadd2(l[r], pr[i][r]);
-        }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            x[i][h][t] = fadd2(x[i][h][t], neg[t]);
+            const float2 y = make_float2(fast_exp2(x[i][h][t].x), fast_exp2(x[i][h][t].y));
+            l[t] = fadd2(l[t], y);
+            if constexpr (E4M3) x[i][h][t] = fadd2(x[i][h][t], make_float2(e[i][h], e[i][h]));
+            else w[i][h][t] = pack2<false>(y.x, y.y);
+          }
       if constexpr (E4M3) {
+        maxima();
+        if (over(M)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float f[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float M1 = fmaxf(M[t][r], reduce(mx[t][r]));
+              f[r] = fast_exp2(M1 == M[t][r] ? 0.f : M[t][r] - M1);
+              M[t][r] = M1;
+            }
+            Neg[t] = make_float2(M[t][0] == -INFINITY ? 0.f : kBoost - M[t][0], M[t][1] == -INFINITY ? 0.f : kBoost - M[t][1]);
+            scale_rows(t, f[0], f[1]);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) x[i][r] = fadd2(x[i][r], e[i]);
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) mx[r] = fmaxf(fmax3(x[0][r].x, x[0][r].y, x[1][r].x), x[1][r].y);
-        if (__any_sync(0xffffffffu, mx[0] > M[0] + kSlack || mx[1] > M[1] + kSlack)) {
+            for (int t = 0; t < NT; ++t) {
+              const float2 y = fadd2(x[i][h][t], Neg[t]);
+              w[i][h][t] = pack2<true>(fast_exp2(y.x), fast_exp2(y.y));
+            }
+      }
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-            const float M1 = fmaxf(M[r], mx[r]), down = M1 == M[r] ? 0.f : M[r] - M1;
-            M[r] = M1;
-            Neg[r] = M1 == -INFINITY ? 0.f : kBoost - M1;
-            scale_rows(o, r, fast_exp2(down));
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) w[i][h][t] = transpose8(w[i][h][t]);
+        // values of keys 16 i + 2 q, + 1, + 8, + 9
+        uint32_t v[4][kWords];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint8_t* src = stage + at_v[k & 1] + (16 * i + 8 * (k >> 1)) * L::kBoxBytes;
+          if constexpr (kWords >= 4) {
+#pragma unroll
+            for (int j = 0; j < kWords / 4; ++j) {
+              const uint4 y = *reinterpret_cast<const uint4*>(src + j * kStepTile * 128);
+              v[k][4 * j] = y.x;
+              v[k][4 * j + 1] = y.y;
+              v[k][4 * j + 2] = y.z;
+              v[k][4 * j + 3] = y.w;
+            }
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(src);
+            v[k][0] = y.x;
+            v[k][1] = y.y;
+          }
+          if (edge) {                              // weight 0 does not silence an infinity
+            const int key = c0 + key0 + 16 * i + 8 * (k >> 1) + 2 * q + (k & 1);
+            if (key >= u.keys || key < u.lo) {
+#pragma unroll
+              for (int j = 0; j < kWords; ++j) v[k][j] = 0;
+            }
           }
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int j = 0; j < kWords; ++j) {
+          if constexpr (E4M3) {
+            const uint32_t x0 = __byte_perm(v[0][j], v[1][j], 0x5140), x1 = __byte_perm(v[0][j], v[1][j], 0x7362);
+            const uint32_t y0 = __byte_perm(v[2][j], v[3][j], 0x5140), y1 = __byte_perm(v[2][j], v[3][j], 0x7362);
+            const uint32_t a0[4] = {codes_f16(x0), codes_f16_hi(x0), codes_f16(y0), codes_f16_hi(y0)};
+            const uint32_t a1[4] = {codes_f16(x1), codes_f16_hi(x1), codes_f16(y1), codes_f16_hi(y1)};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 y = fadd2(x[i][r], make_float2(Neg[r], Neg[r]));
-            w[2 * i + r] = pack2<true>(fast_exp2(y.x), fast_exp2(y.y));
+            for (int t = 0; t < NT; ++t) {
+              mma16816<true>(o[2 * j][t], a0, w[i][0][t], w[i][1][t]);
+              mma16816<true>(o[2 * j + 1][t], a1, w[i][0][t], w[i][1][t]);
+            }
+          } else {
+            const uint32_t a[4] = {__byte_perm(v[0][j], v[1][j], 0x5410), __byte_perm(v[0][j], v[1][j], 0x7632),
+                                   __byte_perm(v[2][j], v[3][j], 0x5410), __byte_perm(v[2][j], v[3][j], 0x7632)};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) mma16816<false>(o[j][t], a, w[i][0][t], w[i][1][t]);
           }
-      } else {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) w[2 * i + r] = pack2<false>(pr[i][r].x, pr[i][r].y);
-      }
-#pragma unroll
-      for (int j = 0; j < kWords; ++j) {
-        if constexpr (E4M3) {
-          const uint32_t a0 = __byte_perm(v[0][j], v[1][j], 0x5140), a1 = __byte_perm(v[0][j], v[1][j], 0x7362);
-          const uint32_t b0 = __byte_perm(v[2][j], v[3][j], 0x5140), b1 = __byte_perm(v[2][j], v[3][j], 0x7362);
-          mma16816<true>(o[4 * j], w, codes_f16(a0), codes_f16(b0));
-          mma16816<true>(o[4 * j + 1], w, codes_f16_hi(a0), codes_f16_hi(b0));
-          mma16816<true>(o[4 * j + 2], w, codes_f16(a1), codes_f16(b1));
-          mma16816<true>(o[4 * j + 3], w, codes_f16_hi(a1), codes_f16_hi(b1));
-        } else {
-          mma16816<false>(o[2 * j], w, __byte_perm(v[0][j], v[1][j], 0x5410), __byte_perm(v[2][j], v[3][j], 0x5410));
-          mma16816<false>(o[2 * j + 1], w, __byte_perm(v[0][j], v[1][j], 0x7632), __byte_perm(v[2][j], v[3][j], 0x7632));
         }
       }
       __syncwarp();
@@ -546,36 +602,40 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     // the unit's, or its piece's, end: the warps meet
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float sum = l[r].x + l[r].y;
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (q == 0) {
-        float* y = stat + warp * 2 * kStepRows + g + 8 * r;
-        y[0] = m[r];
-        y[kStepRows] = sum;
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float sum = r ? l[t].y : l[t].x;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (g == 0) {
+          float* y = stat + warp * 2 * L::kRows + 8 * t + 2 * q + r;
+          y[0] = m[t][r];
+          y[L::kRows] = sum;
+        }
       }
-    }
     ok = named_bar_and(1, kComputeWarps * 32, ok);
     if (!ok) break;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if (g + 8 * r >= u.rows) continue;
-      float top = -INFINITY;
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int w = 0; w < kComputeWarps; ++w) top = fmaxf(top, stat[w * 2 * kStepRows + g + 8 * r]);
-      float to = m[r] == top ? 0.f : m[r] - top;
-      if constexpr (E4M3) to += M[r] - kBoost;
-      to = m[r] == -INFINITY ? 0.f : fast_exp2(to);
-      float* dst = red + (warp * kStepRows + g + 8 * r) * D;
-      // columns 2 q and 2 q + 1 of product n
+      for (int r = 0; r < 2; ++r) {
+        const int row = 8 * t + 2 * q + r;
+        if (row >= u.rows) continue;
+        float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+        for (int w = 0; w < kComputeWarps; ++w) top = fmaxf(top, stat[w * 2 * L::kRows + row]);
+        float to = m[t][r] == top ? 0.f : m[t][r] - top;
+        if constexpr (E4M3) to += M[t][r] - kBoost;
+        to = m[t][r] == -INFINITY ? 0.f : fast_exp2(to);
+        // head dimensions (D / 8) g + 2 d and + 1 of product tile d; bf16: of each half of the row's 8 g + 2 (d mod 4)
+        float* dst = red + (warp * L::kRows + row) * D;
 #pragma unroll
-        for (int n = 0; n < kOut; n += 4)
-          *reinterpret_cast<float4*>(dst + (E4M3 ? (2 * q + c) * kOut + n : (n >> 3) * 64 + (2 * q + c) * 8 + (n & 7))) =
-              make_float4(o[n][2 * r + c] * to, o[n + 1][2 * r + c] * to, o[n + 2][2 * r + c] * to, o[n + 3][2 * r + c] * to);
-    }
+        for (int d = 0; d < kOut; d += 2)
+          *reinterpret_cast<float4*>(dst + (E4M3 ? (D / 8) * g + 2 * d : (d >> 2) * 64 + 8 * g + 2 * (d & 3))) =
+              make_float4(o[d][t][r] * to, o[d][t][2 + r] * to, o[d + 1][t][r] * to, o[d + 1][t][2 + r] * to);
+      }
     named_bar_sync(1, kComputeWarps * 32);
     const bool whole = u.t0 == 0 && u.t1 == u.tiles;
     float* part = cached_part<true, D>(p, blockIdx.x, u.t0 == 0 ? 1 : 0);
@@ -585,13 +645,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       float top = -INFINITY, tot = 0.f;
 #pragma unroll
-      for (int w = 0; w < kComputeWarps; ++w) top = fmaxf(top, stat[w * 2 * kStepRows + r]);
+      for (int w = 0; w < kComputeWarps; ++w) top = fmaxf(top, stat[w * 2 * L::kRows + r]);
 #pragma unroll
       for (int w = 0; w < kComputeWarps; ++w) {
-        const float4 z = *reinterpret_cast<const float4*>(red + (w * kStepRows + r) * D + 4 * c);
+        const float4 z = *reinterpret_cast<const float4*>(red + (w * L::kRows + r) * D + 4 * c);
         sum = make_float4(sum.x + z.x, sum.y + z.y, sum.z + z.z, sum.w + z.w);
-        const float mw = stat[w * 2 * kStepRows + r];
-        tot += mw == -INFINITY ? 0.f : stat[w * 2 * kStepRows + kStepRows + r] * fast_exp2(mw - top);
+        const float mw = stat[w * 2 * L::kRows + r];
+        tot += mw == -INFINITY ? 0.f : stat[w * 2 * L::kRows + L::kRows + r] * fast_exp2(mw - top);
       }
       if (whole) {
         const int64_t tok = u.start + r / group;
@@ -687,33 +747,35 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cached_join_kernel(const Cach
   }
 }
 
-template <int D, bool E4M3, bool CAP>
+template <int D, bool E4M3, bool CAP, int NT>
 cudaError_t launch(const CachedParams& p, cudaStream_t stream) {
-  using L = StepSmem<D, E4M3>;
+  using L = StepSmem<D, E4M3, NT>;
   CUtensorMap tk, tv;
   const uint64_t P = (uint64_t)1 << p.c.page_shift, pages = (uint64_t)p.c.num_pages * p.c.hkv;
   const uint32_t rows = P < kStepTile ? (uint32_t)P : kStepTile;
   if (!make_tmap_u8_3d(&tk, p.c.k, L::kRowBytes, pages, P, P * L::kRowBytes, L::kRowBytes, L::kBoxBytes, rows) ||
       !make_tmap_u8_3d(&tv, p.c.v, L::kRowBytes, pages, P, P * L::kRowBytes, L::kRowBytes, L::kBoxBytes, rows))
     return cudaErrorInvalidValue;
-  cudaError_t e = prepare_kernel<cached_step_kernel<D, E4M3, CAP>>(L::kAlloc);
+  cudaError_t e = prepare_kernel<cached_step_kernel<D, E4M3, CAP, NT>>(L::kAlloc);
   if (e != cudaSuccess) return e;
-  cached_step_kernel<D, E4M3, CAP><<<kStepCtas, kThreads, L::kAlloc, stream>>>(tk, tv, p);
+  cached_step_kernel<D, E4M3, CAP, NT><<<kStepCtas, kThreads, L::kAlloc, stream>>>(tk, tv, p);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch_d(bool e4m3, const CachedParams& p, cudaStream_t s) {
-  if (e4m3) return p.cap > 0.f ? launch<D, true, true>(p, s) : launch<D, true, false>(p, s);
-  return p.cap > 0.f ? launch<D, false, true>(p, s) : launch<D, false, false>(p, s);
+  if (e4m3) return p.cap > 0.f ? launch<D, true, true, NT>(p, s) : launch<D, true, false, NT>(p, s);
+  return p.cap > 0.f ? launch<D, false, true, NT>(p, s) : launch<D, false, false, NT>(p, s);
 }
 
 template <int D>
 cudaError_t launch_all(bool e4m3, const CachedParams& p, cudaStream_t s) {
   const int group = p.hq / p.c.hkv;
-  const bool steps = group <= kStepRows, chunks = (int64_t)p.max_chunk * group > kStepRows;
+  const int64_t most = (int64_t)p.max_chunk * group;
+  const int limit = step_rows(group, p.max_chunk);
+  const bool steps = group <= limit, chunks = most > limit;
   cudaError_t e = cudaSuccess;
-  if (steps) e = launch_d<D>(e4m3, p, s);
+  if (steps) e = (most < limit ? most : limit) <= 8 ? launch_d<D, 1>(e4m3, p, s) : launch_d<D, 2>(e4m3, p, s);
   if (e == cudaSuccess && chunks) e = launch_cached_chunk(D, e4m3, p, !steps, s);
   if (e != cudaSuccess) return e;
   // starts while the launch before still runs, and waits for it where its results are needed
