@@ -51,6 +51,7 @@ struct alignas(16) Piece {
 };
 static_assert(sizeof(Piece) == 48, "read as three 16-byte words");
 constexpr int kUnits = 4;
+constexpr int kScaleCopies = kTile / 16;     // of 16 bytes, a tile
 
 __device__ __forceinline__ Piece read_piece(const uint8_t* units, uint64_t* full, uint64_t* done, int n, bool whole_warp, bool& ok,
                                             int* status) {
@@ -118,12 +119,6 @@ struct ChunkSmem {
   static constexpr int kAlloc = kBytes + 1024;
 };
 
-__device__ __forceinline__ void chunk_bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&x);
@@ -245,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&kv_empty[i], kSplit ? 2 : 1);      // issuers
     }
     for (int i = 0; i < L::kRaw; ++i) {
-      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_full[i], 1 + kScaleCopies);
       mbar_init(&raw_empty[i], 4);
     }
     fence_mbar_init();
@@ -292,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t st = ring % kRing;
             if (ring >= kRing && !(ok = warp_wait(&empty[st], (ring / kRing - 1) & 1, status))) break;
             if (lane == 0) {
-              if (pages) mbar_arrive_expect_tx(&full[st], pages * P * (E4M3 ? D + 1 : 2 * D));
+              if (pages) mbar_arrive_expect_tx(&full[st], pages * P * (E4M3 ? D : 2 * D));
               else mbar_arrive(&full[st]);
             }
             __syncwarp();
@@ -301,9 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int b = 0; b < (E4M3 ? 1 : D / 64); ++b)
                 tma_load_3d(dst + b * kTile * 128, v ? &tm_v : &tm_k, &full[st], 128 * b, page, 0);
-              if constexpr (E4M3)
-                chunk_bulk_load(smem + L::kScales + st * kTile + lane * P,
-                                (v ? p.c.v_scales : p.c.k_scales) + ((int64_t)page << p.c.page_shift), P, &full[st]);
+            }
+            if constexpr (E4M3) {              // a lane 16 keys' scales
+              const int at_page = __shfl_sync(0xffffffffu, page, lane * 16 / P & 31);
+              if (lane < kScaleCopies) {
+                if (at_page >= 0)
+                  cp_async16(smem + L::kScales + st * kTile + lane * 16,
+                             (v ? p.c.v_scales : p.c.k_scales) + ((int64_t)at_page << p.c.page_shift) + (lane * 16 & (P - 1)));
+                cp_async_arrive(&full[st]);
+              }
             }
             __syncwarp();
           }
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // nothing may land after the CTA has left (reached early only when a wait ran out)
       for (uint32_t x = ring > kRing ? ring - kRing : 0; x < ring; ++x) mbar_wait(&full[x % kRing], (x / kRing) & 1, status);
+      asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 2) {
       // ---------------------------------------------------------- units and their queries
       const int group = p.hq / p.c.hkv;

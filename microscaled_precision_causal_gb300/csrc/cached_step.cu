@@ -38,6 +38,7 @@ namespace {
 
 constexpr int kComputeWarps = 4, kThreads = (kComputeWarps + 1) * 32;
 constexpr float kBoost = 13.f, kSlack = 2.f;
+constexpr int kScaleCopies = 2 * kStepTile / 16;     // of 16 bytes: a TMA copy that small takes as long as a page's
 constexpr int kUnits = 2;         // described and their queries fetched ahead
 
 // A unit's piece as the compute warps need it.
@@ -48,12 +49,6 @@ struct alignas(16) StepPiece {
 };
 static_assert(sizeof(StepPiece) == 64, "");
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16)
@@ -158,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if ((int)blockIdx.x >= sh.n) return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], E4M3 ? 1 + kScaleCopies : 1);
       mbar_init(&empty[i], kComputeWarps / 2);
     }
     for (int i = 0; i < kUnits; ++i) {
@@ -179,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------------------ producer
     const int64_t f1 = sh.begin(blockIdx.x + 1);
     const int P = 1 << p.c.page_shift, rows = min(P, kStepTile), per = kStepTile / rows;      // pages a tile
-    const uint32_t page_bytes = 2 * rows * (L::kRowBytes + (E4M3 ? 1 : 0));
+    const uint32_t page_bytes = 2 * rows * L::kRowBytes;
     CachedUnit u{};
     int64_t f = sh.begin(blockIdx.x);
     for (int n = 0; ok;) {
@@ -222,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t dst = smem_u32(smem + L::kQ + ((n % kUnits) * L::kRows + r) * D * 2 + 16 * c);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
       }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&unit_full[n % kUnits])) : "memory");
+      cp_async_arrive(&unit_full[n % kUnits]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&unit_full[n % kUnits]);
       ++n;
@@ -261,11 +256,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             tma_load_3d(dst + b * kStepTile * 128, &tm_k, &full[st], 128 * b, page, slot);
             tma_load_3d(dst + L::kTileBytes + b * kStepTile * 128, &tm_v, &full[st], 128 * b, page, slot);
           }
-          if constexpr (E4M3) {
-            const int64_t at = ((int64_t)page << p.c.page_shift) + slot;
-            uint8_t* sc = smem + st * L::kStage + L::kScales + lane * rows;
-            bulk_load(sc, p.c.k_scales + at, rows, &full[st]);
-            bulk_load(sc + kStepTile, p.c.v_scales + at, rows, &full[st]);
+        }
+        if constexpr (E4M3) {                  // a lane 16 keys' scales, K's then V's
+          const int key = lane % (kScaleCopies / 2) * 16;
+          const int at_page = __shfl_sync(0xffffffffu, now, (i - batch + key / rows) & 31);
+          if (lane < kScaleCopies) {
+            const bool v = lane >= kScaleCopies / 2;
+            if (at_page >= 0)
+              cp_async16(smem + st * L::kStage + L::kScales + (v ? kStepTile : 0) + key,
+                         (v ? p.c.v_scales : p.c.k_scales) + ((int64_t)at_page << p.c.page_shift) + ((i * rows + key) & (P - 1)));
+            cp_async_arrive(&full[st]);
           }
         }
         __syncwarp();

@@ -160,6 +160,15 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// One 16-byte copy of the calling thread to shared memory, and an arrival on bar (counted in its
+// initial value) once all of the thread's copies so far have landed.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Per-warpgroup register reallocation (all threads of the warpgroup execute it):
 // dec hands registers back to the CTA's pool, inc takes them (blocking until the
 // pool has them).  The sizes must add up to the launch allocation.
