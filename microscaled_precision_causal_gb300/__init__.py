@@ -670,8 +670,11 @@ class FlamiaPagedCache:
             self.k_scales, self.v_scales = (torch.zeros(shape[:3], dtype=torch.uint8, device=self.device) for _ in range(2))
         else:
             self.k, self.v = (torch.zeros(shape, dtype=torch.bfloat16, device=self.device) for _ in range(2))
+        # (what the calls get: the tensors above stay the pages for the object's life)
         self.view = KVCache(_ptr(self.k), _ptr(self.v), _ptr(self.k_scales), _ptr(self.v_scales), num_pages, page_size,
                             hkv, head_dim, CACHE_FORMATS[fmt])
+        self.ref = ctypes.pointer(self.view)
+        self.kind = (page_size, hkv, head_dim, self.device)
 
 
 class FlamiaCachedAttention:
@@ -721,18 +724,23 @@ class FlamiaCachedAttention:
         self._planned = False
         self.out = torch.empty(total_tokens, hq, head_dim, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(hq, total_tokens, dtype=torch.float32, device=dev)
-        self.workspace = torch.empty(flamia_cached_fwd_workspace_bytes(hq, hkv, head_dim, self.max_chunk), dtype=torch.uint8,
-                                     device=dev)
+        self._ws_bytes = flamia_cached_fwd_workspace_bytes(hq, hkv, head_dim, self.max_chunk)
+        self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
+        # a step's calls are many and small: what does not change is worked out once
+        self._lib, self._plan_ptr = lib(), self.plan.data_ptr()
+        self._kind = (page_size, hkv, head_dim, dev)
+        self._q_shape, self._kv_shape = (total_tokens, hq, head_dim), (total_tokens, hkv, head_dim)
+        self._table_shape = (num_seqs, self.max_pages)
 
     _want = FlamiaScoredAttention._want
     _run = FlamiaScoredAttention._run
 
     def _places(self, cache, page_table):
         import torch
-        if (cache.page_size, cache.hkv, cache.d, cache.device) != (self.page_size, self.hkv, self.d, self.device):
+        if cache.kind != self._kind:
             raise FlamiaError(f"cache: want pages of {self.page_size}, {self.hkv} heads of {self.d} on {self.device}, got "
                               f"{cache.page_size}, {cache.hkv}, {cache.d} on {cache.device}")
-        self._want("page_table", page_table, (self.N, self.max_pages), torch.int32)
+        self._want("page_table", page_table, self._table_shape, torch.int32)
         if not self._planned:
             raise FlamiaError("FlamiaCachedAttention: plan_build has not been called")
 
@@ -748,28 +756,34 @@ class FlamiaCachedAttention:
         """The new tokens' keys and values into the cache."""
         import torch
         self._places(cache, page_table)
-        self._want("k", k, (self.T, self.hkv, self.d), torch.bfloat16)
-        self._want("v", v, (self.T, self.hkv, self.d), torch.bfloat16)
-        self._run(lambda stm: flamia_cache_write(cache.view, page_table, self.N, self.plan, k, v, stm), stream)
+        self._want("k", k, self._kv_shape, torch.bfloat16)
+        self._want("v", v, self._kv_shape, torch.bfloat16)
+        rc = self._run(lambda stm: self._lib.flamia_cache_write(
+            cache.ref, page_table.data_ptr(), self.max_pages, self.N, self.T, self._plan_ptr, k.data_ptr(), v.data_ptr(), stm), stream)
+        _check(rc, "flamia_cache_write")
 
     def read(self, cache: FlamiaPagedCache, page_table, k, v, stream=None):
         """The new tokens' keys and values from the cache into k and v, which are returned."""
         import torch
         self._places(cache, page_table)
-        self._want("k", k, (self.T, self.hkv, self.d), torch.bfloat16)
-        self._want("v", v, (self.T, self.hkv, self.d), torch.bfloat16)
-        self._run(lambda stm: flamia_cache_read(cache.view, page_table, self.N, self.plan, k, v, stm), stream)
+        self._want("k", k, self._kv_shape, torch.bfloat16)
+        self._want("v", v, self._kv_shape, torch.bfloat16)
+        rc = self._run(lambda stm: self._lib.flamia_cache_read(
+            cache.ref, page_table.data_ptr(), self.max_pages, self.N, self.T, self._plan_ptr, k.data_ptr(), v.data_ptr(), stm), stream)
+        _check(rc, "flamia_cache_read")
         return k, v
 
     def forward(self, cache: FlamiaPagedCache, q, page_table, softmax_scale: float = 0.0, stream=None):
         """(out bf16 [T, hq, d], lse fp32 [hq, T]) of the new tokens, whose keys and values have been written."""
         import torch
         self._places(cache, page_table)
-        self._want("q", q, (self.T, self.hq, self.d), torch.bfloat16)
-        self._run(lambda stm: flamia_cached_fwd(q, cache.view, page_table, self.N, self.plan, self.out, self.lse,
-                                                self.workspace, self.max_chunk, self.window, self.softcap, softmax_scale,
-                                                stm), stream)
-        return self.out, self.lse
+        self._want("q", q, self._q_shape, torch.bfloat16)
+        out, lse, ws = self.out, self.lse, self.workspace
+        rc = self._run(lambda stm: self._lib.flamia_cached_fwd(
+            q.data_ptr(), cache.ref, page_table.data_ptr(), self.max_pages, self.N, self.T, self.hq, self.max_chunk, self.window,
+            self.softcap, softmax_scale, self._plan_ptr, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), self._ws_bytes, stm), stream)
+        _check(rc, "flamia_cached_fwd")
+        return out, lse
 
     def device_status(self, stream=None) -> int:
         return self._run(lambda stm: flamia_get_device_status(self.plan, stm), stream)

@@ -8,6 +8,8 @@
 // a later token changes no earlier one's code.  e = least integer with amax <= 448 2^e.
 // Both directions move every byte once and are bound by memory: a warp takes a token's rows (of
 // all heads, K and V), 16 bytes a lane and load, four loads in flight.
+#include <type_traits>
+
 #include "cache.cuh"
 
 namespace flamia {
@@ -72,16 +74,18 @@ __global__ void __launch_bounds__(kPlanThreads)
     h[kCpMaxChunk] = max_chunk;
     h[kCpLeft] = left;
     h[kCpValid] = bad || N == 0 ? 0 : cu[N];
-    h[kCpItems] = 0;
-    if (bad || N == 0) pv.step_prefix[N] = pv.item_prefix[0] = 0;
+    *reinterpret_cast<int64_t*>(h + kCpStepPlaces) = *reinterpret_cast<int64_t*>(h + kCpChunkPlaces) = 0;
+    h[kCpStepCtas] = h[kCpChunkCtas] = 0;
   }
-  if (bad) return;
-  // sequences, step tiles, chunk items
-  int64_t steps = 0, items = 0;
+  for (int i = threadIdx.x; i < kDone; i += kPlanThreads) pv.done[i] = 0;
+  if (bad || N == 0) return;
+  // sequences; steps with their places; chunk items before each sequence
+  int64_t step_places = 0, steps = 0, items = 0;
   for (int base = 0; base < N; base += kPlanThreads) {
     const int n = base + threadIdx.x;
     int4 r = make_int4(0, 0, 0, 0);
     int64_t st = 0, it = 0;
+    int tile = 0;
     if (n < N) {
       r.x = cu[n];
       r.y = cu[n + 1] - r.x;
@@ -89,53 +93,87 @@ __global__ void __launch_bounds__(kPlanThreads)
         r.z = kv[n];
         r.w = left < 0 ? 0 : max(0, r.z - r.y - left);
         const int64_t rows = (int64_t)r.y * group;
-        if (rows <= limit) st = (r.z + kStepTile - 1) / kStepTile - r.w / kStepTile + kStepExtra;
+        tile = r.w / kStepTile;
+        if (rows <= limit) st = (r.z + kStepTile - 1) / kStepTile - tile + kStepExtra;
         else it = (rows + kChunkRows - 1) / kChunkRows;
       }
       pv.seq[n] = r;
     }
     int64_t tot;
-    const int64_t a = block_scan(st, warp_sums, &tot);
-    if (n < N) pv.step_prefix[n] = steps + a;
+    const int64_t places = step_places + block_scan(st, warp_sums, &tot);
+    step_places += tot;
+    const int64_t number = steps + block_scan(st > 0, warp_sums, &tot);
     steps += tot;
+    if (st > 0) {
+      pv.items[1][number] = CacheItem{n, 0, tile, (int)st - kStepExtra};
+      pv.prefix[1][number] = places;
+    }
     const int64_t b = block_scan(it, warp_sums, &tot);
-    if (n < N) pv.item_base[n] = items + b;
+    if (n < N) pv.base[n] = items + b;
     items += tot;
   }
   if (threadIdx.x == 0) {
-    pv.step_prefix[N] = steps;
-    pv.item_base[N] = items;
-    pv.hdr[kCpItems] = (int)items;
+    pv.prefix[1][steps] = step_places;
+    pv.base[N] = items;
   }
   __syncthreads();
-  int64_t tiles = 0;
+  int64_t chunk_places = 0;
   for (int64_t base = 0; base < items; base += kPlanThreads) {
     const int64_t i = base + threadIdx.x;
     int cost = 0;
     if (i < items) {
-      int lo = 0, hi = N;          // item_base[lo] <= i < item_base[hi]
+      int lo = 0, hi = N;          // base[lo] <= i < base[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (pv.item_base[mid] <= i) lo = mid; else hi = mid;
+        if (pv.base[mid] <= i) lo = mid; else hi = mid;
       }
       const int4 r = pv.seq[lo];
       CacheItem x;
       x.seq = lo;
-      x.row = (int)(i - pv.item_base[lo]) * kChunkRows;
+      x.row = (int)(i - pv.base[lo]) * kChunkRows;
       const int64_t rows = (int64_t)r.y * group;
       const int last = (int)(min((int64_t)x.row + kChunkRows, rows) - 1) / group;
       const int first = r.z - r.y + x.row / group;
       x.tile = (left < 0 ? 0 : max(0, first - left)) / kTile;
       x.tiles = (r.z - r.y + last) / kTile - x.tile + 1;
       cost = x.tiles + kChunkExtra;
-      pv.items[i] = x;
+      pv.items[0][i] = x;
     }
     int64_t tot;
     const int64_t a = block_scan(cost, warp_sums, &tot);
-    if (i < items) pv.item_prefix[i] = tiles + a;
-    tiles += tot;
+    if (i < items) pv.prefix[0][i] = chunk_places + a;
+    chunk_places += tot;
   }
-  if (threadIdx.x == 0) pv.item_prefix[items] = tiles;
+  if (threadIdx.x == 0) pv.prefix[0][items] = chunk_places;
+  __syncthreads();
+  // shares: the CTAs that get one, and the unit that each begins in
+  auto shares = [&](auto STEP, int64_t total, int64_t n_items, int least, int ctas, int c) {
+    constexpr int kStep = decltype(STEP)::value;
+    Shares sh;
+    sh.total = total;
+    sh.n = (int)min((int64_t)ctas, (total + least - 1) / least);
+    if (c == 0) {
+      *reinterpret_cast<int64_t*>(pv.hdr + (kStep ? kCpStepPlaces : kCpChunkPlaces)) = total;
+      pv.hdr[kStep ? kCpStepCtas : kCpChunkCtas] = sh.n;
+    }
+    if (c >= sh.n) return;
+    const int64_t f = sh.begin(c);
+    int64_t lo = 0, hi = n_items;          // prefix[lo] hkv <= f < prefix[hi] hkv
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (pv.prefix[kStep][mid] * hkv <= f) lo = mid; else hi = mid;
+    }
+    CachedUnit u = cached_item<kStep != 0>(pv, (int)lo, hq, hkv);
+    const int len = u.tiles + (kStep ? kStepExtra : kChunkExtra);
+    u.h = (int)((f - u.begin) / len);
+    u.begin += (int64_t)u.h * len;
+    pv.first[kStep][c] = u;
+  };
+  // A CTA takes some places at least: fewer would cost more in joining than they save.
+  if (threadIdx.x < kStepCtas)
+    shares(std::integral_constant<int, 1>{}, step_places * hkv, steps, 4 + kStepExtra, kStepCtas, threadIdx.x);
+  else if (threadIdx.x < kStepCtas + kChunkCtas)
+    shares(std::integral_constant<int, 0>{}, chunk_places * hkv, items, 2 + kChunkExtra, kChunkCtas, threadIdx.x - kStepCtas);
 }
 
 // ---------------------------------------------------------------- write, read

@@ -28,38 +28,62 @@ enum CachePlanWord : int {
   kCpMaxChunk = 5,
   kCpLeft = 6,
   kCpValid = 7,        // rows of the sequences (0: the plan is bad)
-  kCpItems = 8,        // chunk items
+  kCpStepPlaces = 8,   // two words each, as the next: places of all steps, of all chunk units
+  kCpChunkPlaces = 10,
+  kCpStepCtas = 12,    // CTAs that they are dealt out to
+  kCpChunkCtas = 13,
   kCpHeaderWords = 16,
 };
-// A chunk item: up to kChunkRows rows of a sequence, the same for every kv head.
-struct CacheItem {
-  int seq, row, tile, tiles;     // first row; first key tile (kTile keys) and their number
+// An item: the units of a row tile, the same for every kv head (a step: all of its rows).
+struct alignas(16) CacheItem {
+  int seq, row, tile, tiles;     // first row; first key tile and their number
 };
+// A unit is an item for a kv head: a tile of a sequence's rows over the key tiles that they see.  The places of all
+// units, unit after unit, are dealt out to the CTAs in equal shares, so that every CTA has the same to do whatever
+// the sequences' lengths are: a unit has some places for what it costs besides (kStepExtra, kChunkExtra), then one
+// for each key tile.  A unit whose key tiles lie in several shares is joined after.
+struct CachedUnit {
+  int seq, h, row, rows, tile, tiles;     // first row, rows, first key tile, key tiles
+  int start, count, keys, lo;             // of the sequence (CachePlanView::seq)
+  int item, pad;
+  int64_t begin;                          // its first place
+};
+static_assert(sizeof(CachedUnit) == 56, "");
+constexpr int kStepCtas = 304, kChunkCtas = 152, kDone = kStepCtas + 8 * kChunkCtas;
 struct CachePlanView {
   int* hdr;
-  int4* seq;               // [N] {first token, new tokens, keys with them, first key that the first new one sees}
-  int64_t* step_prefix;    // [N + 1] key tiles of the steps before, kStepExtra more for each
-  int64_t* item_base;      // [N + 1] chunk items before
-  CacheItem* items;        // [cap]
-  int64_t* item_prefix;    // [cap + 1] key tiles of the items before, kChunkExtra more for each
+  int4* seq;                  // [N] {first token, new tokens, keys with them, first key that the first new one sees}
+  CacheItem* items[2];        // [cap] chunk items, [N] steps
+  int64_t* prefix[2];         // [items + 1] places of the items before, for one kv head
+  int64_t* base;              // [N + 1] chunk items before
+  CachedUnit* first[2];       // [CTAs] the unit that a CTA's share begins in
+  int* done;                  // [kStepCtas + 8 kChunkCtas] finished pieces of a split unit (of a chunk's 32 rows each), by
+                              // the CTA that has its beginning; 0 between calls
 };
 __host__ __device__ inline int64_t cache_item_capacity(int64_t T, int N, int hq, int hkv) {
   return T * (hq / hkv) / kChunkRows + N;
 }
-__host__ __device__ inline size_t cache_plan_bytes(int64_t T, int N, int hq, int hkv) {
-  const int64_t cap = cache_item_capacity(T, N, hq, hkv);
-  return (size_t)kCpHeaderWords * 4 + (size_t)N * 16 + (size_t)(N + 1) * 16 + (size_t)cap * 24 + 16;
-}
 // The sequences come first: writing and reading the cache need no more of the layout.
-__host__ __device__ inline CachePlanView cache_plan_view(const void* plan, int64_t T, int N, int hq, int hkv) {
+__host__ __device__ inline CachePlanView cache_plan_view(const void* plan, int64_t T, int N, int hq, int hkv, size_t* bytes = nullptr) {
+  const int64_t cap = cache_item_capacity(T, N, hq, hkv);
   CachePlanView v;
   v.hdr = (int*)plan;
   v.seq = (int4*)(v.hdr + kCpHeaderWords);
-  v.items = (CacheItem*)(v.seq + N);
-  v.step_prefix = (int64_t*)(v.items + cache_item_capacity(T, N, hq, hkv));
-  v.item_base = v.step_prefix + (N + 1);
-  v.item_prefix = v.item_base + (N + 1);
+  v.items[0] = (CacheItem*)(v.seq + N);
+  v.items[1] = v.items[0] + cap;
+  v.prefix[0] = (int64_t*)(v.items[1] + N);
+  v.prefix[1] = v.prefix[0] + (cap + 1);
+  v.base = v.prefix[1] + (N + 1);
+  v.first[0] = (CachedUnit*)(v.base + (N + 1));
+  v.first[1] = v.first[0] + kChunkCtas;
+  v.done = (int*)(v.first[1] + kStepCtas);
+  if (bytes) *bytes = (size_t)((const uint8_t*)(v.done + kDone) - (const uint8_t*)plan);
   return v;
+}
+inline size_t cache_plan_bytes(int64_t T, int N, int hq, int hkv) {
+  size_t n;
+  cache_plan_view(nullptr, T, N, hq, hkv, &n);
+  return n;
 }
 
 struct CacheParams {
@@ -115,7 +139,6 @@ struct CachedParams {
 };
 // A CTA leaves at most two unfinished pieces of units behind (the unit that its first key tile lies inside of, and the
 // one that its last lies inside of): a row's weighted values, its sum and its reference each.
-constexpr int kStepCtas = 304, kChunkCtas = 152;
 inline size_t cached_workspace_bytes(int hq, int hkv, int d, int max_chunk) {
   const size_t row = (size_t)(d + 2) * 4;
   return 2 * row * ((size_t)kStepCtas * kStepRows + ((int64_t)max_chunk * (hq / hkv) > step_rows(hq / hkv, max_chunk) ? (size_t)kChunkCtas * kChunkRows : 0));
@@ -129,44 +152,49 @@ __device__ __forceinline__ int cached_valid_rows(const CachedParams& p) {
 
 
 // ---------------------------------------------------------------- units and shares
-// A unit is a tile of a sequence's rows (a step: all of them) and a kv head, over the key tiles that its rows see.
-// The places of all units, unit after unit, are dealt out to the CTAs in equal shares, so that every CTA has the same
-// to do whatever the sequences' lengths are: a unit has kExtra places, then one for each key tile.  A unit whose key
-// tiles lie in several shares is joined after.
-struct CachedUnit {
-  int seq, h, row, rows, tile, tiles;     // first row, rows, first key tile, key tiles
-  int start, count, keys, lo;             // of the sequence (CachePlanView::seq)
-  int64_t begin;                          // its first place
+struct Shares {
+  int64_t total;      // places
+  int n;              // CTAs with a share
+  __device__ __forceinline__ int64_t begin(int c) const { return total * c / n; }
+  __device__ __forceinline__ int of(int64_t f) const { return (int)(((f + 1) * n - 1) / total); }   // the last c with begin(c) <= f
 };
 template <bool STEP>
-__device__ __forceinline__ int64_t cached_places(const CachedParams& p, const CachePlanView& pv) {
-  return (STEP ? pv.step_prefix[p.c.N] : pv.item_prefix[pv.hdr[kCpItems]]) * p.c.hkv;
+__device__ __forceinline__ Shares cached_shares(const int* hdr) {
+  Shares s;
+  s.total = *reinterpret_cast<const int64_t*>(hdr + (STEP ? kCpStepPlaces : kCpChunkPlaces));
+  s.n = hdr[STEP ? kCpStepCtas : kCpChunkCtas];
+  return s;
 }
-// The unit of place f (found by a whole warp).
+// The first unit of item i.
 template <bool STEP>
-__device__ __forceinline__ CachedUnit cached_unit(const CachedParams& p, const CachePlanView& pv, int64_t f) {
-  constexpr int kExtra = STEP ? kStepExtra : kChunkExtra;
+__device__ __forceinline__ CachedUnit cached_item(const CachePlanView& pv, int i, int hq, int hkv) {
+  const CacheItem x = pv.items[STEP][i];
+  const int4 r = pv.seq[x.seq];
   CachedUnit u;
-  const int64_t* prefix = STEP ? pv.step_prefix : pv.item_prefix;
-  const int hkv = p.c.hkv;
-  const int i = warp_upper(STEP ? p.c.N : pv.hdr[kCpItems], f, [&](int x) { return prefix[x] * hkv; });
-  const int64_t first = prefix[i] * hkv;
-  CacheItem item{i, 0, 0, 0};
-  if (!STEP) item = pv.items[i];
-  const int4 r = pv.seq[item.seq];
-  u.seq = item.seq;
+  u.seq = x.seq;
+  u.h = 0;
+  u.row = x.row;
+  u.rows = min(r.y * (hq / hkv) - x.row, STEP ? kStepRows : kChunkRows);
+  u.tile = x.tile;
+  u.tiles = x.tiles;
   u.start = r.x;
   u.count = r.y;
   u.keys = r.z;
   u.lo = r.w;
-  const int rows = r.y * (p.hq / hkv);
-  u.row = item.row;
-  u.rows = STEP ? rows : min(rows - u.row, kChunkRows);
-  u.tile = STEP ? r.w / kStepTile : item.tile;
-  u.tiles = STEP ? (int)(prefix[i + 1] - prefix[i]) - kExtra : item.tiles;
-  u.h = (int)((f - first) / (u.tiles + kExtra));
-  u.begin = first + (int64_t)u.h * (u.tiles + kExtra);
+  u.item = i;
+  u.pad = 0;
+  u.begin = pv.prefix[STEP][i] * hkv;
   return u;
+}
+// The unit after u.
+template <bool STEP>
+__device__ __forceinline__ void cached_next(const CachePlanView& pv, CachedUnit& u, int hq, int hkv) {
+  if (u.h + 1 < hkv) {
+    ++u.h;
+    u.begin += u.tiles + (STEP ? kStepExtra : kChunkExtra);
+  } else {
+    u = cached_item<STEP>(pv, u.item + 1, hq, hkv);
+  }
 }
 // A share's part of a unit: key tiles [t0, t1), none where the share ends before the first; f moves behind it.
 template <bool STEP>
@@ -177,30 +205,12 @@ __device__ __forceinline__ int2 cached_piece(const CachedUnit& u, int64_t& f, in
   f = to;
   return t;
 }
-struct Shares {
-  int64_t total;
-  int n;              // CTAs with a share
-  __device__ __forceinline__ int64_t begin(int c) const { return total * c / n; }
-  __device__ __forceinline__ int of(int64_t f) const { return (int)(((f + 1) * n - 1) / total); }   // the last c with begin(c) <= f
-};
-// A CTA takes kLeast places at least: fewer would cost more in joining than they save.
+// The CTAs whose pieces of u are to be joined: the first one, and their number.
 template <bool STEP>
-__device__ __forceinline__ Shares cached_shares(const CachedParams& p, const CachePlanView& pv) {
-  constexpr int kCtas = STEP ? kStepCtas : kChunkCtas, kLeast = STEP ? 4 + kStepExtra : 2 + kChunkExtra;
-  Shares s;
-  s.total = cached_places<STEP>(p, pv);
-  s.n = (int)min((int64_t)kCtas, (s.total + kLeast - 1) / kLeast);
-  return s;
-}
-// The unit that begins in CTA c's share and ends behind it, whose pieces in c .. c + n - 1 are to be joined; n = 0: none.
-template <bool STEP>
-__device__ __forceinline__ int cached_split(const CachedParams& p, const CachePlanView& pv, const Shares& sh, int c,
-                                            CachedUnit& u) {
-  if (c + 1 >= sh.n) return 0;
-  u = cached_unit<STEP>(p, pv, sh.begin(c + 1) - 1);
-  const int64_t first = u.begin + (STEP ? kStepExtra : kChunkExtra), last = first + u.tiles - 1;
-  if (first < sh.begin(c) || first >= sh.begin(c + 1) || last < sh.begin(c + 1)) return 0;
-  return sh.of(last) - c + 1;
+__device__ __forceinline__ int2 cached_owners(const CachedUnit& u, const Shares& sh) {
+  const int64_t first = u.begin + (STEP ? kStepExtra : kChunkExtra);
+  const int c = sh.of(first);
+  return make_int2(c, sh.of(first + u.tiles - 1) - c + 1);
 }
 // Unfinished pieces: the one that a CTA's share begins in the middle of (0), and the one that it ends in the middle of and
 // has the beginning of (1).  [rows][D] weighted values, [rows] references (base 2), [rows] sums.
@@ -210,10 +220,14 @@ __device__ __forceinline__ float* cached_part(const CachedParams& p, int cta, in
   float* base = p.part + (STEP ? 0 : (size_t)2 * kStepCtas * kStepRows * (D + 2));
   return base + (size_t)(2 * cta + slot) * kRows * (D + 2);
 }
-// Where row r of a unit is: token and query head.
-__device__ __forceinline__ int2 cached_row(const CachedParams& p, const CachedUnit& u, int r) {
-  const int group = p.hq / p.c.hkv, x = u.row + r;
-  return make_int2(u.start + x / group, u.h * group + x % group);
+// One more piece of a split unit is finished (the caller's writes and those of the threads it has met since are
+// visible to whoever sees the count): true for the last of n, who joins them, in the order of the keys whoever it is.
+__device__ __forceinline__ bool cached_last(int* done, int n) {
+  __threadfence();
+  const bool last = atomicAdd(done, 1) == n - 1;
+  if (last) *done = 0;
+  __threadfence();
+  return last;
 }
 
 }  // namespace flamia

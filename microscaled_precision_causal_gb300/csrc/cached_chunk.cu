@@ -48,8 +48,9 @@ struct alignas(16) Piece {
   int h, row, rows, ntq;
   int start, pos0, keys, lo;       // first token of the sequence, and its position; keys; first key seen by any row
   int seq, slot;                   // slot of the workspace, or -1: a whole unit
+  int owner, pieces, pad[2];       // of a split unit: the CTA that has its beginning, the CTAs that have pieces
 };
-static_assert(sizeof(Piece) == 48, "read as three 16-byte words");
+static_assert(sizeof(Piece) == 64, "read as four 16-byte words");
 constexpr int kUnits = 4;
 constexpr int kScaleCopies = kTile / 16;     // of 16 bytes, a tile
 
@@ -59,11 +60,11 @@ __device__ __forceinline__ Piece read_piece(const uint8_t* units, uint64_t* full
   if (whole_warp) ok = __all_sync(0xffffffffu, ok);
   union {
     Piece p;
-    int4 w[3];
+    int4 w[4];
   } x;
   const int4* src = reinterpret_cast<const int4*>(units + (n % kUnits) * sizeof(Piece));
 #pragma unroll
-  for (int i = 0; i < 3; ++i) x.w[i] = src[i];
+  for (int i = 0; i < 4; ++i) x.w[i] = src[i];
   if (whole_warp) __syncwarp();
   if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(&done[n % kUnits]);
   if (!ok) x.p.tiles = 0;
@@ -167,6 +168,48 @@ __device__ __forceinline__ void unpack_row(uint32_t raw, uint32_t tile, int r, u
   }
 }
 
+// The rows of a warp of row tile w from all pieces: eight lanes a row, so that four rows' loads are in flight.
+template <int D>
+__device__ __forceinline__ void join_rows(const CachedParams& p, const Piece& U, int w, int quarter, int lane) {
+  constexpr int kPer = D / 8;
+  const int sub = lane >> 3, seg = lane & 7, group = p.hq / p.c.hkv;
+  auto piece = [&](int i) { return cached_part<false, D>(p, U.owner + i, i == 0 ? 1 : 0); };
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += 4) {
+    const int r = w * kTile + quarter * 32 + r0 + sub;
+    if (r >= U.rows) break;
+    float top = -INFINITY, l = 0.f;
+    for (int i = 0; i < U.pieces; ++i) top = fmaxf(top, __ldcg(piece(i) + kChunkRows * D + r));
+    const float neg = top == -INFINITY ? 0.f : -top;
+    float o[kPer] = {};
+#pragma unroll 2
+    for (int i = 0; i < U.pieces; ++i) {
+      const float* src = piece(i);
+      const float wt = fast_exp2(__ldcg(src + kChunkRows * D + r) + neg);
+      l += wt * __ldcg(src + kChunkRows * (D + 1) + r);
+#pragma unroll
+      for (int k = 0; k < kPer; k += 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)r * D + k * 8 + 4 * seg));
+        o[k] = fmaf(wt, y.x, o[k]);
+        o[k + 1] = fmaf(wt, y.y, o[k + 1]);
+        o[k + 2] = fmaf(wt, y.z, o[k + 2]);
+        o[k + 3] = fmaf(wt, y.w, o[k + 3]);
+      }
+    }
+    const int x = U.row + r, h = U.h * group + x % group;
+    const int64_t tok = U.start + x / group;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int k = 0; k < kPer; k += 4) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv), b = __floats2bfloat162_rn(o[k + 2] * inv, o[k + 3] * inv);
+      *reinterpret_cast<uint2*>(p.out + (tok * p.hq + h) * D + k * 8 + 4 * seg) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+    if (seg == 0) p.lse[(int64_t)h * p.c.T + tok] = (top + log2f(l)) * kLn2;
+  }
+  __syncwarp();
+}
+
 template <int D, bool E4M3, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     cached_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -210,9 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   const CachePlanView pv = cache_plan_view(p.c.plan, p.c.T, p.c.N, p.hq, p.c.hkv);
-  Shares sh{};
-  if (valid) sh = cached_shares<false>(p, pv);
-  if ((int)blockIdx.x >= sh.n) {
+  const Shares sh = cached_shares<false>(pv.hdr);
+  if (valid == 0 || (int)blockIdx.x >= sh.n) {
     grid_wait();                            // who comes behind this launch comes behind the one before it too
     return;
   }
@@ -319,11 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t nq[2] = {0, 0};
       bool ok = true;
       int64_t f = f0;
+      CachedUnit u = pv.first[0][blockIdx.x];
       for (int n = 0; ok; ++n) {
         if (n >= kUnits && !(ok = warp_wait(&unit_done[n % kUnits], (n / kUnits - 1) & 1, status))) break;
         Piece U{};
         while (f < f1 && U.tiles == 0) {
-          const CachedUnit u = cached_unit<false>(p, pv, f);
+          if (f >= u.begin + kChunkExtra + u.tiles) cached_next<false>(pv, u, p.hq, p.c.hkv);
           const int2 piece = cached_piece<false>(u, f, f1);
           const int t0 = piece.x, t1 = piece.y;
           U.tiles = t1 - t0;
@@ -338,6 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           U.lo = p.left < 0 ? 0 : max(0, U.pos0 + u.row / group - p.left);
           U.seq = u.seq;
           U.slot = U.tiles == u.tiles ? -1 : (t0 == 0 ? 1 : 0);
+          if (U.slot >= 0) {
+            const int2 c = cached_owners<false>(u, sh);
+            U.owner = c.x;
+            U.pieces = c.y;
+          }
         }
         if (lane == 0) {
           *reinterpret_cast<Piece*>(units + (n % kUnits) * sizeof(Piece)) = U;
@@ -704,6 +752,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[(size_t)kChunkRows * D + rr] = m;
           part[(size_t)kChunkRows * (D + 1) + rr] = l;
         }
+      }
+      if (U.slot >= 0) {           // a warp's rows stay a warp's: the last of their pieces to be finished joins them
+        __syncwarp();
+        int last = lane == 0 && cached_last(pv.done + kStepCtas + 8 * U.owner + 4 * w + quarter, U.pieces);
+        if (__shfl_sync(0xffffffffu, last, 0)) join_rows<D>(p, U, w, quarter, lane);
       }
     }
   } else {

@@ -1,5 +1,4 @@
-// Attention over the paged cache for steps: a sequence's few new tokens (up to 16 rows of a kv head),
-// and the joining of pieces.
+// Attention over the paged cache for steps: a sequence's few new tokens (up to 16 rows of a kv head).
 //
 //   x = scale log2 e q.k (capped), m = running maximum, l += 2^(x - m), O += 2^(x - m) v
 //
@@ -45,7 +44,8 @@ constexpr int kUnits = 2;         // described and their queries fetched ahead
 struct alignas(16) StepPiece {
   int t0, t1, tiles, tile;        // key tiles [t0, t1) of the unit's; its first tile's number in the sequence.  t1 0: no more
   int h, rows, start, pos0;       // first token of the sequence, and its position
-  int keys, lo, pad[6];
+  int keys, lo;
+  int owner, pieces, pad[4];      // of a split unit: the CTA that has its beginning, the CTAs that have pieces
 };
 static_assert(sizeof(StepPiece) == 64, "");
 
@@ -112,7 +112,8 @@ struct StepSmem {
   static constexpr int kStat = kRed + kComputeWarps * kRows * D * 4;          // [4 warps][m, l][kRows]
   static constexpr int kQ = kStat + kComputeWarps * 2 * kRows * 4;            // [2 units in turn][kRows] queries
   static constexpr int kUnit = kQ + kUnits * kRows * D * 2;
-  static constexpr int kBar = kUnit + kUnits * 64;
+  static constexpr int kFlag = kUnit + kUnits * 64;
+  static constexpr int kBar = kFlag + 16;
   static constexpr int kBytes = kBar + (2 * kStages + 2 * kUnits) * 8;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -129,6 +130,53 @@ __device__ __forceinline__ void clear_rows(const CachedParams& p, int D, int val
     for (int j = 0; j < D / 8; ++j) dst[j] = make_uint4(0, 0, 0, 0);
     p.lse[(int64_t)h * p.c.T + row] = INFINITY;
   }
+}
+
+// Row r of a split unit, whose pieces may be hundreds: by a warp, a lane a piece for their weights.
+template <int D>
+__device__ __forceinline__ void join_row(const CachedParams& p, const StepPiece& u, int r, int lane) {
+  constexpr int kPer = D / 32;
+  auto piece = [&](int i) { return cached_part<true, D>(p, u.owner + i, i == 0 ? 1 : 0); };
+  float top = -INFINITY, l = 0.f;
+  for (int i = lane; i < u.pieces; i += 32) top = fmaxf(top, __ldcg(piece(i) + kStepRows * D + r));
+#pragma unroll
+  for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+  const float neg = top == -INFINITY ? 0.f : -top;
+  float o[kPer] = {};
+  for (int b = 0; b < u.pieces; b += 32) {
+    const int i = b + lane;
+    float wt = 0.f;
+    if (i < u.pieces) {
+      wt = fast_exp2(__ldcg(piece(i) + kStepRows * D + r) + neg);
+      l += wt * __ldcg(piece(i) + kStepRows * (D + 1) + r);
+    }
+    const int here = min(32, u.pieces - b);
+#pragma unroll 8
+    for (int j = 0; j < here; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, wt, j);
+      const float* src = piece(b + j) + r * D + lane * kPer;
+      if constexpr (kPer == 2) {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+        o[0] = fmaf(wj, y.x, o[0]);
+        o[1] = fmaf(wj, y.y, o[1]);
+      } else {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+        o[0] = fmaf(wj, y.x, o[0]);
+        o[1] = fmaf(wj, y.y, o[1]);
+        o[2] = fmaf(wj, y.z, o[2]);
+        o[3] = fmaf(wj, y.w, o[3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  const int group = p.hq / p.c.hkv, h = u.h * group + r % group;
+  const int64_t tok = u.start + r / group;
+  const float inv = 1.f / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (tok * p.hq + h) * D + lane * kPer);
+#pragma unroll
+  for (int j = 0; j < kPer / 2; ++j) dst[j] = pack2<false>(o[2 * j] * inv, o[2 * j + 1] * inv);
+  if (lane == 0) p.lse[(int64_t)h * p.c.T + tok] = (top + log2f(l)) * kLn2;
 }
 
 // NT: tiles of 8 query rows.
@@ -149,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   clear_rows(p, D, valid, threadIdx.x, kThreads);
   if (valid == 0) return;
   const CachePlanView pv = cache_plan_view(p.c.plan, p.c.T, p.c.N, p.hq, p.c.hkv);
-  const Shares sh = cached_shares<true>(p, pv);
+  const Shares sh = cached_shares<true>(pv.hdr);
   if ((int)blockIdx.x >= sh.n) return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
@@ -175,18 +223,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t f1 = sh.begin(blockIdx.x + 1);
     const int P = 1 << p.c.page_shift, rows = min(P, kStepTile), per = kStepTile / rows;      // pages a tile
     const uint32_t page_bytes = 2 * rows * L::kRowBytes;
-    CachedUnit u{};
+    CachedUnit u = pv.first[1][blockIdx.x];
     int64_t f = sh.begin(blockIdx.x);
     for (int n = 0; ok;) {
       int2 piece = make_int2(0, 0);
       if (f < f1) {
-        const int64_t next = u.begin + kStepExtra + u.tiles;
-        if (u.tiles && u.h + 1 < p.c.hkv) {    // the next head of the same sequence
-          ++u.h;
-          u.begin = next;
-        } else {
-          u = cached_unit<true>(p, pv, f);
-        }
+        if (n > 0) cached_next<true>(pv, u, p.hq, p.c.hkv);
         piece = cached_piece<true>(u, f, f1);
         if (piece.y == 0) continue;            // (only the share's end)
       }
@@ -204,6 +246,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         x.pos0 = u.keys - u.count;
         x.keys = u.keys;
         x.lo = u.lo;
+        if (t1 > 0 && t1 - t0 < u.tiles) {
+          const int2 c = cached_owners<true>(u, sh);
+          x.owner = c.x;
+          x.pieces = c.y;
+        }
         *reinterpret_cast<StepPiece*>(smem + L::kUnit + (n % kUnits) * sizeof(StepPiece)) = x;
       }
       // queries: 16 bytes a lane and copy, rows behind the unit's are zeros
@@ -212,8 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < L::kRows / kPer; ++i) {
         const int r = i * kPer + lane / kLanes, c = lane % kLanes;
         const bool in = t1 > 0 && r < u.rows;
-        const int2 at = in ? cached_row(p, u, r) : make_int2(0, 0);
-        const __nv_bfloat16* src = p.q + ((int64_t)at.x * p.hq + at.y) * D + 8 * c;
+        const __nv_bfloat16* src = p.q + (in ? (((int64_t)u.start + r / group) * p.hq + u.h * group + r % group) * D + 8 * c : 0);
         const uint32_t dst = smem_u32(smem + L::kQ + ((n % kUnits) * L::kRows + r) * D * 2 + 16 * c);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
       }
@@ -668,82 +714,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
-  }
-}
-
-// Joins the pieces of the unit that begins in CTA c's share and ends behind it.  A step's row may have hundreds of
-// pieces: a warp a row, a lane a piece for their weights.  A chunk's has few: eight lanes a row, so that a warp
-// has four rows' loads in flight.
-constexpr int kJoinWarps = 4, kStepJoin = kStepRows / kJoinWarps, kChunkJoin = kChunkRows / (4 * kJoinWarps);   // blocks a unit
-template <int D, bool STEP>
-__device__ __forceinline__ void join(const CachedParams& p, int valid, int c, int r) {
-  constexpr int kRows = STEP ? kStepRows : kChunkRows, kLanes = STEP ? 32 : 8, kPer = D / kLanes;
-  const CachePlanView pv = cache_plan_view(p.c.plan, p.c.T, p.c.N, p.hq, p.c.hkv);
-  Shares sh{};
-  if (valid) sh = cached_shares<STEP>(p, pv);
-  CachedUnit u{};
-  const int n = cached_split<STEP>(p, pv, sh, c, u);
-  grid_wait();
-  const int lane = threadIdx.x & (kLanes - 1);
-  if (n == 0 || (STEP && r >= u.rows)) return;
-  const bool in = r < u.rows;
-  if (!in) r = 0;
-  auto piece = [&](int i) { return cached_part<STEP, D>(p, c + i, i == 0 ? 1 : 0); };
-  float top = -INFINITY, l = 0.f;
-  for (int i = lane; i < n; i += kLanes) top = fmaxf(top, piece(i)[kRows * D + r]);
-#pragma unroll
-  for (int w = kLanes / 2; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-  const float neg = top == -INFINITY ? 0.f : -top;
-  float o[kPer] = {};
-  for (int b = 0; b < n; b += kLanes) {
-    const int i = b + lane;
-    const float wt = i < n ? fast_exp2(piece(i)[kRows * D + r] + neg) : 0.f;
-    if (i < n) l += wt * piece(i)[kRows * (D + 1) + r];
-    const int here = min(kLanes, n - b);
-#pragma unroll 4
-    for (int j = 0; j < here; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, wt, j, kLanes);
-      const float* src = piece(b + j) + r * D;
-      if constexpr (kPer == 2) {
-        const float2 y = *reinterpret_cast<const float2*>(src + 2 * lane);
-        o[0] = fmaf(wj, y.x, o[0]);
-        o[1] = fmaf(wj, y.y, o[1]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kPer; k += 4) {
-          const float4 y = *reinterpret_cast<const float4*>(src + k * kLanes + 4 * lane);
-          o[k] = fmaf(wj, y.x, o[k]);
-          o[k + 1] = fmaf(wj, y.y, o[k + 1]);
-          o[k + 2] = fmaf(wj, y.z, o[k + 2]);
-          o[k + 3] = fmaf(wj, y.w, o[k + 3]);
-        }
-      }
+    if (!whole) {                // the last of the unit's pieces to be finished joins them
+      int* flag = reinterpret_cast<int*>(smem + L::kFlag);
+      named_bar_sync(1, kComputeWarps * 32);
+      if (threadIdx.x == 0) *flag = cached_last(pv.done + u.owner, u.pieces);
+      named_bar_sync(1, kComputeWarps * 32);
+      if (*flag)
+        for (int r = warp; r < u.rows; r += kComputeWarps) join_row<D>(p, u, r, lane);
     }
-  }
-#pragma unroll
-  for (int w = kLanes / 2; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-  if (!in) return;
-  const int2 at = cached_row(p, u, r);
-  const float inv = 1.f / l;
-  __nv_bfloat16* dst = p.out + ((int64_t)at.x * p.hq + at.y) * D;
-  if constexpr (kPer == 2) {
-    *reinterpret_cast<uint32_t*>(dst + 2 * lane) = pack2<false>(o[0] * inv, o[1] * inv);
-  } else {
-#pragma unroll
-    for (int k = 0; k < kPer; k += 4)
-      *reinterpret_cast<uint2*>(dst + k * kLanes + 4 * lane) =
-          make_uint2(pack2<false>(o[k] * inv, o[k + 1] * inv), pack2<false>(o[k + 2] * inv, o[k + 3] * inv));
-  }
-  if (lane == 0) p.lse[(int64_t)at.y * p.c.T + at.x] = (top + log2f(l)) * kLn2;
-}
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) cached_join_kernel(const CachedParams p, const int step_blocks) {
-  const int valid = cached_valid_rows(p), warp = threadIdx.x >> 5, b = blockIdx.x;
-  if (b < step_blocks) {
-    join<D, true>(p, valid, b / kStepJoin, (b % kStepJoin) * kJoinWarps + warp);
-  } else {
-    const int x = b - step_blocks;
-    join<D, false>(p, valid, x / kChunkJoin, ((x % kChunkJoin) * kJoinWarps + warp) * 4 + (threadIdx.x & 31) / 8);
   }
 }
 
@@ -777,19 +755,7 @@ cudaError_t launch_all(bool e4m3, const CachedParams& p, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (steps) e = (most < limit ? most : limit) <= 8 ? launch_d<D, 1>(e4m3, p, s) : launch_d<D, 2>(e4m3, p, s);
   if (e == cudaSuccess && chunks) e = launch_cached_chunk(D, e4m3, p, !steps, s);
-  if (e != cudaSuccess) return e;
-  // starts while the launch before still runs, and waits for it where its results are needed
-  const int step_blocks = steps ? kStepCtas * kStepJoin : 0;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(step_blocks + (chunks ? kChunkCtas * kChunkJoin : 0));
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = s;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cached_join_kernel<D>, p, step_blocks);
+  return e;
 }
 
 }  // namespace
