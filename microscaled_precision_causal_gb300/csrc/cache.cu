@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int n = base + threadIdx.x;
     int4 r = make_int4(0, 0, 0, 0);
     int64_t st = 0, it = 0;
-    int tile = 0;
+    int tile = 0, row_tiles = 0;
     if (n < N) {
       r.x = cu[n];
       r.y = cu[n + 1] - r.x;
@@ -94,19 +94,21 @@ __global__ void __launch_bounds__(kPlanThreads)
         r.w = left < 0 ? 0 : max(0, r.z - r.y - left);
         const int64_t rows = (int64_t)r.y * group;
         tile = r.w / kStepTile;
-        if (rows <= limit) st = (r.z + kStepTile - 1) / kStepTile - tile + kStepExtra;
-        else it = (rows + kChunkRows - 1) / kChunkRows;
+        if (rows <= limit) {
+          st = (r.z + kStepTile - 1) / kStepTile - tile + kStepExtra;
+          row_tiles = (int)(rows + kStepRows - 1) / kStepRows;
+        } else it = (rows + kChunkRows - 1) / kChunkRows;
       }
       pv.seq[n] = r;
     }
     int64_t tot;
-    const int64_t places = step_places + block_scan(st, warp_sums, &tot);
+    const int64_t places = step_places + block_scan(st * row_tiles, warp_sums, &tot);
     step_places += tot;
-    const int64_t number = steps + block_scan(st > 0, warp_sums, &tot);
+    const int64_t number = steps + block_scan(row_tiles, warp_sums, &tot);
     steps += tot;
-    if (st > 0) {
-      pv.items[1][number] = CacheItem{n, 0, tile, (int)st - kStepExtra};
-      pv.prefix[1][number] = places;
+    for (int t = 0; t < row_tiles; ++t) {
+      pv.items[1][number + t] = CacheItem{n, t * kStepRows, tile, (int)st - kStepExtra};
+      pv.prefix[1][number + t] = places + t * st;
     }
     const int64_t b = block_scan(it, warp_sums, &tot);
     if (n < N) pv.base[n] = items + b;

@@ -7,13 +7,15 @@
 namespace flamia {
 
 // Rows of a kv head in a sequence: its new tokens times the query heads that share the head, token by token.
-constexpr int kStepRows = 16;      // up to so many a sequence may be a step: one tile of rows, keys streamed past it
+constexpr int kStepRows = 16;      // rows of a step's unit, past which its keys are streamed
+constexpr int kStepTiles = 2;      // row tiles that a step has at most
 constexpr int kChunkRows = 2 * kTile;   // rows of a unit otherwise
 constexpr int kStepTile = 64;      // keys a tile of a step
-// Rows up to which a call's sequences are steps.  In a call that has chunks too, 8 where a token's rows fit in: its steps
-// then cost half of what 16 rows do, and the few sequences between the two go with the chunks.
+// Rows up to which a call's sequences are steps, each row tile a stream of its own.  Beyond XX
+// In a call that has chunks too, 8 where a token's rows fit in: its steps then cost half of what 16 rows do, and the
+// few sequences between the two go with the chunks.
 __host__ __device__ inline int step_rows(int group, int64_t max_chunk) {
-  return max_chunk * group > kStepRows && group <= 8 ? 8 : kStepRows;
+  return max_chunk * group > kStepTiles * kStepRows && group <= 8 ? 8 : kStepTiles * kStepRows;
 }
 // What a unit costs besides its key tiles, in key tiles, when the work is dealt out: its queries, its end.
 constexpr int kStepExtra = 3, kChunkExtra = 1;
@@ -34,7 +36,7 @@ enum CachePlanWord : int {
   kCpChunkCtas = 13,
   kCpHeaderWords = 16,
 };
-// An item: the units of a row tile, the same for every kv head (a step: all of its rows).
+// An item: the units of a row tile, the same for every kv head.
 struct alignas(16) CacheItem {
   int seq, row, tile, tiles;     // first row; first key tile and their number
 };
@@ -53,7 +55,7 @@ constexpr int kStepCtas = 304, kChunkCtas = 152, kDone = kStepCtas + 8 * kChunkC
 struct CachePlanView {
   int* hdr;
   int4* seq;                  // [N] {first token, new tokens, keys with them, first key that the first new one sees}
-  CacheItem* items[2];        // [cap] chunk items, [N] steps
+  CacheItem* items[2];        // [cap] chunk items, [kStepTiles N] steps
   int64_t* prefix[2];         // [items + 1] places of the items before, for one kv head
   int64_t* base;              // [N + 1] chunk items before
   CachedUnit* first[2];       // [CTAs] the unit that a CTA's share begins in
@@ -71,9 +73,9 @@ __host__ __device__ inline CachePlanView cache_plan_view(const void* plan, int64
   v.seq = (int4*)(v.hdr + kCpHeaderWords);
   v.items[0] = (CacheItem*)(v.seq + N);
   v.items[1] = v.items[0] + cap;
-  v.prefix[0] = (int64_t*)(v.items[1] + N);
+  v.prefix[0] = (int64_t*)(v.items[1] + (int64_t)kStepTiles * N);
   v.prefix[1] = v.prefix[0] + (cap + 1);
-  v.base = v.prefix[1] + (N + 1);
+  v.base = v.prefix[1] + ((int64_t)kStepTiles * N + 1);
   v.first[0] = (CachedUnit*)(v.base + (N + 1));
   v.first[1] = v.first[0] + kChunkCtas;
   v.done = (int*)(v.first[1] + kStepCtas);

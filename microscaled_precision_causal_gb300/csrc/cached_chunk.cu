@@ -147,10 +147,13 @@ template <int D, bool BIG>
 __device__ __forceinline__ void unpack_row(uint32_t raw, uint32_t tile, int r, uint32_t b) {
   const uint32_t f1 = BIG ? 0x7b807b80u : (b + 120) * 0x00800080u, f2 = b == 255 ? 0x7fc07fc0u : b * 0x00800080u;
   const uint32_t src = raw + swz_offset(r, 0, D), dst = tile + swz_offset(r, 0, 128);
+  // (all loads first: one warp a scheduler unpacks, so what it waits for is its own latencies)
+  uint4 c[D / 16];
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) c[j] = lds128(src ^ (16 * j));
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) {
-    const uint4 c = lds128(src ^ (16 * j));
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
     uint32_t y[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -168,52 +171,65 @@ __device__ __forceinline__ void unpack_row(uint32_t raw, uint32_t tile, int r, u
   }
 }
 
-// The rows of a warp of row tile w from all pieces: eight lanes a row, so that four rows' loads are in flight.
+// The rows of a warp of row tile w from all pieces: references and sums with a lane a row, then values with eight
+// lanes a row, so that four rows' loads are in flight.
 template <int D>
 __device__ __forceinline__ void join_rows(const CachedParams& p, const Piece& U, int w, int quarter, int lane) {
   constexpr int kPer = D / 8;
-  const int sub = lane >> 3, seg = lane & 7, group = p.hq / p.c.hkv;
+  const int base = w * kTile + quarter * 32, sub = lane >> 3, seg = lane & 7, group = p.hq / p.c.hkv;
+  const int rows = min(32, U.rows - base);
   auto piece = [&](int i) { return cached_part<false, D>(p, U.owner + i, i == 0 ? 1 : 0); };
+  float top = -INFINITY, l = 0.f;
+  const int mine = base + min(lane, rows - 1);
+#pragma unroll 4
+  for (int i = 0; i < U.pieces; ++i) top = fmaxf(top, __ldcg(piece(i) + kChunkRows * D + mine));
+  const float neg = top == -INFINITY ? 0.f : -top;
+#pragma unroll 4
+  for (int i = 0; i < U.pieces; ++i)
+    l += fast_exp2(__ldcg(piece(i) + kChunkRows * D + mine) + neg) * __ldcg(piece(i) + kChunkRows * (D + 1) + mine);
+  if (lane < rows) {
+    const int x = U.row + mine;
+    p.lse[(int64_t)(U.h * group + x % group) * p.c.T + U.start + x / group] = (top + log2f(l)) * kLn2;
+  }
+  const float inv = 1.f / l;
 #pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += 4) {
-    const int r = w * kTile + quarter * 32 + r0 + sub;
-    if (r >= U.rows) break;
-    float top = -INFINITY, l = 0.f;
-    for (int i = 0; i < U.pieces; ++i) top = fmaxf(top, __ldcg(piece(i) + kChunkRows * D + r));
-    const float neg = top == -INFINITY ? 0.f : -top;
+  for (int r0 = 0; r0 < rows; r0 += 4) {
+    const int r = min(r0 + sub, rows - 1);
+    const float nr = __shfl_sync(0xffffffffu, neg, r), ir = __shfl_sync(0xffffffffu, inv, r);
     float o[kPer] = {};
-#pragma unroll 2
+#pragma unroll 3
     for (int i = 0; i < U.pieces; ++i) {
       const float* src = piece(i);
-      const float wt = fast_exp2(__ldcg(src + kChunkRows * D + r) + neg);
-      l += wt * __ldcg(src + kChunkRows * (D + 1) + r);
+      const float m = __ldcg(src + kChunkRows * D + base + r);
+      float4 y[kPer / 4];
 #pragma unroll
-      for (int k = 0; k < kPer; k += 4) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(src + (size_t)r * D + k * 8 + 4 * seg));
-        o[k] = fmaf(wt, y.x, o[k]);
-        o[k + 1] = fmaf(wt, y.y, o[k + 1]);
-        o[k + 2] = fmaf(wt, y.z, o[k + 2]);
-        o[k + 3] = fmaf(wt, y.w, o[k + 3]);
+      for (int k = 0; k < kPer / 4; ++k) y[k] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)(base + r) * D + k * 32 + 4 * seg));
+      const float wt = fast_exp2(m + nr) * ir;
+#pragma unroll
+      for (int k = 0; k < kPer / 4; ++k) {
+        o[4 * k] = fmaf(wt, y[k].x, o[4 * k]);
+        o[4 * k + 1] = fmaf(wt, y[k].y, o[4 * k + 1]);
+        o[4 * k + 2] = fmaf(wt, y[k].z, o[4 * k + 2]);
+        o[4 * k + 3] = fmaf(wt, y[k].w, o[4 * k + 3]);
       }
     }
-    const int x = U.row + r, h = U.h * group + x % group;
-    const int64_t tok = U.start + x / group;
-    const float inv = 1.f / l;
+    if (r0 + sub < rows) {
+      const int x = U.row + base + r, h = U.h * group + x % group;
+      __nv_bfloat16* dst = p.out + (((int64_t)U.start + x / group) * p.hq + h) * D + 4 * seg;
 #pragma unroll
-    for (int k = 0; k < kPer; k += 4) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv), b = __floats2bfloat162_rn(o[k + 2] * inv, o[k + 3] * inv);
-      *reinterpret_cast<uint2*>(p.out + (tok * p.hq + h) * D + k * 8 + 4 * seg) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      for (int k = 0; k < kPer / 4; ++k) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(o[4 * k], o[4 * k + 1]), b = __floats2bfloat162_rn(o[4 * k + 2], o[4 * k + 3]);
+        *reinterpret_cast<uint2*>(dst + 32 * k) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      }
     }
-    if (seg == 0) p.lse[(int64_t)h * p.c.T + tok] = (top + log2f(l)) * kLn2;
   }
   __syncwarp();
 }
 
 template <int D, bool E4M3, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
-    cached_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                        const CachedParams p, const bool tail) {
+    cached_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const CachedParams p, const bool tail) {
   using L = ChunkSmem<D, E4M3>;
   constexpr int kSlots = L::kSlots;
   constexpr bool kSplit = D == 64;
@@ -286,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&raw_empty[i], 4);
     }
     fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
@@ -393,13 +410,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (U.tiles == 0) break;
-        // two (D = 128) or four rows at a time, 16 bytes a lane; rows behind the unit's are zeros
+        // Where the heads that share a kv head divide a tile's rows, a box of their tokens is the tile (rows behind
+        // the unit's are other sequences', or zeros behind the last token: they have no say and are not stored).
+        if (kTile % group == 0) {
+          for (int w = 0; w < U.ntq; ++w) {
+            if (nq[w] && !(ok = warp_wait(&q_empty[w], (nq[w] - 1) & 1, status))) break;
+            ++nq[w];
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&q_full[w], L::kTileBytes);
+#pragma unroll
+              for (int b = 0; b < D / 64; ++b)
+                tma_load_3d(smem + L::kQ + w * L::kTileBytes + b * kTile * 128, &tm_q, &q_full[w], 64 * b, U.h * group,
+                            U.start + (U.row + w * kTile) / group);
+            }
+            __syncwarp();
+          }
+          continue;
+        }
+        // else two (D = 128) or four rows at a time, 16 bytes a lane; rows behind the unit's are zeros
         constexpr int kLanes = D / 8, kPer = 32 / kLanes;
         const int c = lane % kLanes, dt = kPer / group, dg = kPer % group;
         int r = lane / kLanes, t = (U.row + r) / group, g = (U.row + r) % group;
         for (int w = 0; w < U.ntq; ++w) {
           if (nq[w] && !(ok = warp_wait(&q_empty[w], (nq[w] - 1) & 1, status))) break;
           ++nq[w];
+#pragma unroll 8
           for (int i = 0; i < kTile / kPer; ++i) {
             const bool in = r < U.rows;
             const __nv_bfloat16* src = p.q + (in ? (((int64_t)U.start + t) * p.hq + U.h * group + g) * D + 8 * c : 0);
@@ -429,6 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (kTile % group == 0)                       // (reached early only when a wait ran out)
+        for (int w = 0; w < 2; ++w)
+          if (nq[w]) mbar_wait(&q_full[w], (nq[w] - 1) & 1, status);
     } else if (warp == 1 || kSplit) {
       // ---------------------------------------------------------- MMA issuer of row tiles w0 .. w1 - 1
       const int w0 = kSplit ? warp >> 1 : 0, w1 = kSplit ? w0 + 1 : 2;
@@ -527,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t p_addr = kSplit ? lane_base + kP + 64 * w : s_addr;
     const float scale2 = p.scale2;
     const int group = p.hq / p.c.hkv;
+    const bool al32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;       // (whole sectors where they can be)
     uint32_t ring = 0, ns = 0, nu = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -726,22 +765,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!row_in) continue;
         if (U.slot < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + (tok * p.hq + h) * D + 32 * c);
+          __nv_bfloat16* dst = p.out + (tok * p.hq + h) * D + 32 * c;
+          uint32_t y[16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t y[4];
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+            y[j] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          if (al32) {
+            st_global_v8(dst, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
+            st_global_v8(dst + 16, y[8], y[9], y[10], y[11], y[12], y[13], y[14], y[15]);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * i]) * inv,
-                                                              __uint_as_float(o[8 * j + 2 * i + 1]) * inv);
-              y[i] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            dst[j] = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
           }
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(part + (size_t)rr * D + 32 * c);
+          float* dst = part + (size_t)rr * D + 32 * c;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          for (int j = 0; j < 32; j += 8)
+            st_global_v8(dst + j, o[j], o[j + 1], o[j + 2], o[j + 3], o[j + 4], o[j + 5], o[j + 6], o[j + 7]);
         }
       }
       __syncwarp();
@@ -755,7 +798,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (U.slot >= 0) {           // a warp's rows stay a warp's: the last of their pieces to be finished joins them
         __syncwarp();
-        int last = lane == 0 && cached_last(pv.done + kStepCtas + 8 * U.owner + 4 * w + quarter, U.pieces);
+        const int rows = U.rows - (w * kTile + quarter * 32);
+        const int last = lane == 0 && rows > 0 && cached_last(pv.done + kStepCtas + 8 * U.owner + 4 * w + quarter, U.pieces);
         if (__shfl_sync(0xffffffffu, last, 0)) join_rows<D>(p, U, w, quarter, lane);
       }
     }
@@ -801,10 +845,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, bool E4M3, bool CAP>
 cudaError_t launch(const CachedParams& p, bool tail, cudaStream_t stream) {
   using L = ChunkSmem<D, E4M3>;
-  CUtensorMap tk, tv;
+  CUtensorMap tq, tk, tv;
   const uint64_t P = (uint64_t)1 << p.c.page_shift, pages = (uint64_t)p.c.num_pages * p.c.hkv, row = E4M3 ? D : 2 * D;
+  const int group = p.hq / p.c.hkv, heads = kTile % group == 0 ? group : 1;       // (1: the map is not used)
   const uint32_t box = row < 128 ? (uint32_t)row : 128;
-  if (!make_tmap_u8_3d(&tk, p.c.k, row, pages, P, P * row, row, box, (uint32_t)P) ||
+  if (!make_tmap_bf16_3d(&tq, p.q, D, p.hq, p.c.T, D * 2, (uint64_t)p.hq * D * 2, 64, kTile / heads, heads) ||
+      !make_tmap_u8_3d(&tk, p.c.k, row, pages, P, P * row, row, box, (uint32_t)P) ||
       !make_tmap_u8_3d(&tv, p.c.v, row, pages, P, P * row, row, box, (uint32_t)P))
     return cudaErrorInvalidValue;
   int regs = 0;
@@ -823,7 +869,7 @@ cudaError_t launch(const CachedParams& p, bool tail, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = tail ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, cached_chunk_kernel<D, E4M3, CAP>, tk, tv, p, tail);
+  return cudaLaunchKernelEx(&cfg, cached_chunk_kernel<D, E4M3, CAP>, tq, tk, tv, p, tail);
 }
 
 template <int D>

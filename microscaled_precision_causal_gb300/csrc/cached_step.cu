@@ -1,4 +1,4 @@
-// Attention over the paged cache for steps: a sequence's few new tokens (up to 16 rows of a kv head).
+// Attention over the paged cache for steps: a sequence's few new tokens, in tiles of up to 16 rows of a kv head.
 //
 //   x = scale log2 e q.k (capped), m = running maximum, l += 2^(x - m), O += 2^(x - m) v
 //
@@ -43,9 +43,9 @@ constexpr int kUnits = 2;         // described and their queries fetched ahead
 // A unit's piece as the compute warps need it.
 struct alignas(16) StepPiece {
   int t0, t1, tiles, tile;        // key tiles [t0, t1) of the unit's; its first tile's number in the sequence.  t1 0: no more
-  int h, rows, start, pos0;       // first token of the sequence, and its position
-  int keys, lo;
-  int owner, pieces, pad[4];      // of a split unit: the CTA that has its beginning, the CTAs that have pieces
+  int h, row, rows, start;        // first row, rows; first token of the sequence
+  int pos0, keys, lo;             // its position
+  int owner, pieces, pad[3];      // of a split unit: the CTA that has its beginning, the CTAs that have pieces
 };
 static_assert(sizeof(StepPiece) == 64, "");
 
@@ -170,8 +170,8 @@ __device__ __forceinline__ void join_row(const CachedParams& p, const StepPiece&
   }
 #pragma unroll
   for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-  const int group = p.hq / p.c.hkv, h = u.h * group + r % group;
-  const int64_t tok = u.start + r / group;
+  const int group = p.hq / p.c.hkv, h = u.h * group + (u.row + r) % group;
+  const int64_t tok = u.start + (u.row + r) / group;
   const float inv = 1.f / l;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (tok * p.hq + h) * D + lane * kPer);
 #pragma unroll
@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         x.tiles = u.tiles;
         x.tile = u.tile;
         x.h = u.h;
+        x.row = u.row;
         x.rows = u.rows;
         x.start = u.start;
         x.pos0 = u.keys - u.count;
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < L::kRows / kPer; ++i) {
         const int r = i * kPer + lane / kLanes, c = lane % kLanes;
         const bool in = t1 > 0 && r < u.rows;
-        const __nv_bfloat16* src = p.q + (in ? (((int64_t)u.start + r / group) * p.hq + u.h * group + r % group) * D + 8 * c : 0);
+        const __nv_bfloat16* src = p.q + (in ? (((int64_t)u.start + (u.row + r) / group) * p.hq + u.h * group + (u.row + r) % group) * D + 8 * c : 0);
         const uint32_t dst = smem_u32(smem + L::kQ + ((n % kUnits) * L::kRows + r) * D * 2 + 16 * c);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
       }
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = 8 * t + 2 * q + r;
-        pos[t][r] = u.pos0 + (row < u.rows ? row : 0) / group;
+        pos[t][r] = u.pos0 + (u.row + (row < u.rows ? row : 0)) / group;
       }
     }
     __syncwarp();
@@ -406,8 +407,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         o[d][t][3] *= f1;
       }
     };
-    const int all_see = u.pos0 + 1 - kStepTile;          // tiles up to this key hide none behind a row's position
-    const int window = p.left < 0 ? -1 : u.pos0 + (u.rows - 1) / group - p.left;    // tiles from this key on none before one
+    const int all_see = u.pos0 + u.row / group + 1 - kStepTile;          // tiles up to this key hide none behind a row's position
+    const int window = p.left < 0 ? -1 : u.pos0 + (u.row + u.rows - 1) / group - p.left;    // tiles from this key on none before one
     for (int tile = u.t0; tile < u.t1; ++tile, ++ring) {
       if ((ring & 1) != (uint32_t)pair) continue;
       const uint32_t st = ring % L::kStages;
@@ -700,8 +701,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         tot += mw == -INFINITY ? 0.f : stat[w * 2 * L::kRows + L::kRows + r] * fast_exp2(mw - top);
       }
       if (whole) {
-        const int64_t tok = u.start + r / group;
-        const int h = u.h * group + r % group;
+        const int64_t tok = u.start + (u.row + r) / group;
+        const int h = u.h * group + (u.row + r) % group;
         const float inv = 1.f / tot;
         *reinterpret_cast<uint2*>(p.out + (tok * p.hq + h) * D + 4 * c) =
             make_uint2(pack2<false>(sum.x * inv, sum.y * inv), pack2<false>(sum.z * inv, sum.w * inv));
