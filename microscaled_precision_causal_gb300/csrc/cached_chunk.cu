@@ -71,37 +71,61 @@ __device__ __forceinline__ Piece read_piece(const uint8_t* units, uint64_t* full
   return x.p;
 }
 
-// A row tile's products capped, in their own units: the short polynomials where every product of the warp's rows allows
-// one, else 1 - 2 / (1 + 2^(2 z log2 e)) for all.  Its error beside 0 is some 2^-22 of the cap, which only tiles
-// with scores near the cap get, and it has no branches: an element's choice between it and a polynomial
-// took three times as long (ragged chunks, cap 30, d 64: 206 us, without a cap 65).
-__device__ __forceinline__ void cap_tile(uint32_t (&v)[4][32], const CapForm& F, bool counts) {
-  float m[4] = {0.f, 0.f, 0.f, 0.f};
+// Four products x -> a + b / (1 + 2^(z2 x)): with b = -2 a the tanh cap, in whatever units a is.  Reciprocals are a quarter
+// as fast as exponentials, so the four share one, of their product (each at most 1 + 2^30: beyond, 1 - 2^-29).
+__device__ __forceinline__ void tanh4(float2& x, float2& y, float z2, float a, float b) {
+  x = fmul2(x, make_float2(z2, z2));
+  y = fmul2(y, make_float2(z2, z2));
+  const float2 one = make_float2(1.f, 1.f);
+  // (a NaN stays one)
+  x = fadd2(make_float2(fast_exp2(x.x > 30.f ? 30.f : x.x), fast_exp2(x.y > 30.f ? 30.f : x.y)), one);
+  y = fadd2(make_float2(fast_exp2(y.x > 30.f ? 30.f : y.x), fast_exp2(y.y > 30.f ? 30.f : y.y)), one);
+  const float2 xy = fmul2(make_float2(x.x, y.x), make_float2(x.y, y.y));
+  const float r = fast_rcp(xy.x * xy.y) * b;
+  const float2 rr = fmul2(make_float2(r, r), make_float2(xy.y, xy.x));
+  x = ffma2(make_float2(x.y, x.x), make_float2(rr.x, rr.x), make_float2(a, a));
+  y = ffma2(make_float2(y.y, y.x), make_float2(rr.y, rr.y), make_float2(a, a));
+}
+// 32 products of a row capped, in their own units: by a polynomial where every product of the warp's rows allows it, else
+// by tanh4, whose error beside 0 is some 2^-22 of the cap: only columns with scores near the cap get it.
+__device__ __forceinline__ void cap_columns(uint32_t (&v)[32], const CapForm& F, bool counts) {
+  float m[2] = {0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < 32; j += 2)
+  for (int j = 0; j < 32; j += 4)
 #pragma unroll
-    for (int g = 0; g < 4; ++g) m[g] = fmax3(m[g], fabsf(__uint_as_float(v[g][j])), fabsf(__uint_as_float(v[g][j + 1])));
-  const float am = fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
-  if (!__any_sync(0xffffffffu, counts && !(am <= F.t5))) {
+    for (int g = 0; g < 2; ++g) m[g] = fmax3(m[g], fabsf(__uint_as_float(v[j + 2 * g])), fabsf(__uint_as_float(v[j + 2 * g + 1])));
+  if (!__any_sync(0xffffffffu, counts && !(fmaxf(m[0], m[1]) <= F.t5))) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const float2 x = pair_of(v[g], j), w = fmul2(x, x);
-        float2 t = ffma2(w, F.k5[4], F.k5[3]);
-        t = ffma2(w, t, F.k5[2]);
-        t = ffma2(w, t, F.k5[1]);
-        t = ffma2(w, t, F.k5[0]);
-        put_pair(v[g], j, ffma2(x, fmul2(w, t), x));
-      }
+    for (int j = 0; j < 32; j += 2) {
+      const float2 x = pair_of(v, j), w = fmul2(x, x);
+      float2 t = ffma2(w, F.k5[4], F.k5[3]);
+      t = ffma2(w, t, F.k5[2]);
+      t = ffma2(w, t, F.k5[1]);
+      t = ffma2(w, t, F.k5[0]);
+      put_pair(v, j, ffma2(x, fmul2(w, t), x));
+    }
   } else {
-    const float z2 = F.zscale * (2.f * kLog2e), two = -2.f * F.inv;
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        v[g][j] = __float_as_uint(fmaf(two, fast_rcp(1.f + fast_exp2(__uint_as_float(v[g][j]) * z2)), F.inv));
+    for (int j = 0; j < 32; j += 4) {
+      float2 x = pair_of(v, j), y = pair_of(v, j + 2);
+      tanh4(x, y, F.zscale * (2.f * kLog2e), F.inv, -2.f * F.inv);
+      put_pair(v, j, x);
+      put_pair(v, j + 2, y);
+    }
   }
+}
+// Largest product of a row's 128, or largest magnitude.
+template <bool ABS>
+__device__ __forceinline__ float columns_max(uint32_t s_addr) {
+  uint32_t v[4][32];
+  float m[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if constexpr (ABS) tmem_ld32_absmax(s_addr + 32 * g, v[g], m[g]);
+    else tmem_ld32_max(s_addr + 32 * g, v[g], m[g]);
+  }
+  tmem_ld_wait();
+  return fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
 }
 
 template <int D, bool E4M3>
@@ -594,51 +618,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[w], ns & 1, status));
         if (!ok) break;
         tc_fence_after();
-        uint32_t v[4][32];
-        float cm[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          if constexpr (CAP) tmem_ld32_absmax(s_addr + 32 * g, v[g], cm[g]);
-          else tmem_ld32_max(s_addr + 32 * g, v[g], cm[g]);
-        }
-        tmem_ld_wait();
-        if (kSplit) {
-          tc_fence_before();
-          mbar_arrive(&s_free[w]);
-        }
-        float mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);      // of the raw products, or of their magnitudes
-        // form 0: v f + n; 1, 2: capped by 3 or 5 coefficients, then as 0
+        // Without a cap a row's products stay in registers, all code unrolled.  With one they are read again 32 columns at
+        // a time, in rolled loops: four forms of 128 columns are some 100 KB of instructions, whose first pass took 25 us
+        // a call, and spilled.
+        uint32_t v[CAP ? 1 : 4][32];
+        float mx;
+        // form 0: v f + n; 1, 2, 3: capped by 3 coefficients, by 5 or by tanh itself inside the exponent.  A capped row's
+        // reference is its largest magnitude where that is little, else its capped maximum.
         int form = 0;
-        bool quick = seen;
         if constexpr (CAP) {
-          quick = quick && !__any_sync(0xffffffffu, row_in && !(mx <= p.capf.t5 && mx * scale2 <= kLoose * 0.5f));
-          form = __any_sync(0xffffffffu, row_in && !(mx <= p.capf.t3)) ? 2 : 1;
-        }
-        if (!quick) {
-          form = 0;
-          uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-          if (!seen) {
-            const int c = u * kTile;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) see[g] = column_mask(lo - c, pos - c, -1, 32 * g);
+          bool plain = !seen;
+          if (seen) {
+            mx = columns_max<true>(s_addr);
+            plain = __any_sync(0xffffffffu, row_in && !(mx * scale2 < 0x1p27f));      // (beyond, x and m are shrunk below)
           }
-          if constexpr (CAP) {
-            if (!seen) {
+          if (plain) {
+            mx = -INFINITY;
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+              const uint32_t see = seen ? ~0u : column_mask(lo - u * kTile, pos - u * kTile, -1, 32 * g);
+              tmem_ld32(s_addr + 32 * g, v[0]);
+              tmem_ld_wait();
+              hide(v[0], see, 0u);
+              cap_columns(v[0], p.capf, row_in);
+              hide(v[0], see, kMinusInf);
+              float cm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-              for (int g = 0; g < 4; ++g) hide(v[g], see[g], 0u);
+              for (int j = 0; j < 32; j += 4)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  cm[i] = fmax3(cm[i], __uint_as_float(v[0][j + 2 * i]), __uint_as_float(v[0][j + 2 * i + 1]));
+              mx = fmax3(mx, cm[0], cm[1]);
+              tmem_st32(s_addr + 32 * g, v[0]);
             }
-            cap_tile(v, p.capf, row_in);
+            tmem_st_wait();
+          } else {
+            form = !__any_sync(0xffffffffu, row_in && !(mx <= p.capf.t3)) ? 1
+                   : !__any_sync(0xffffffffu, row_in && !(mx <= p.capf.t5)) ? 2 : 3;
+            if (__any_sync(0xffffffffu, row_in && !(mx * scale2 <= kLoose * 0.5f)))
+              mx = p.capf.inv * tanh_any(columns_max<false>(s_addr) * p.capf.zscale);
+          }
+        } else {
+          float cm[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) tmem_ld32_max(s_addr + 32 * g, v[g], cm[g]);
+          tmem_ld_wait();
+          if (kSplit) {
+            tc_fence_before();
+            mbar_arrive(&s_free[w]);
           }
           if (!seen) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) hide(v[g], see[g], kMinusInf);
+            for (int g = 0; g < 4; ++g) hide(v[g], column_mask(lo - u * kTile, pos - u * kTile, -1, 32 * g), kMinusInf);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) cm[g] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+#pragma unroll
+              for (int g = 0; g < 4; ++g) cm[g] = fmax3(cm[g], __uint_as_float(v[g][j]), __uint_as_float(v[g][j + 1]));
           }
-#pragma unroll
-          for (int g = 0; g < 4; ++g) cm[g] = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 32; j += 2)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) cm[g] = fmax3(cm[g], __uint_as_float(v[g][j]), __uint_as_float(v[g][j + 1]));
           mx = fmaxf(fmax3(cm[0], cm[1], cm[2]), cm[3]);
         }
         mx *= scale2;
@@ -679,63 +717,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float shrink = shrink_for(m);
         const float neg = (m == -INFINITY ? 0.f : -m) * shrink, fs = fmaxf(scale2 * shrink, 0x1p-126f);   // (0 * -inf)
         // P in two halves of 64 keys: the first one's product starts while the second is computed
-        auto exps = [&](auto FORM) {
+        auto weights = [&](auto FORM, const uint32_t (&y)[32], uint32_t* pk) {
           constexpr int kForm = decltype(FORM)::value;
           const float2 f2 = make_float2(fs, fs), n2 = make_float2(neg, neg);
           const CapForm& F = p.capf;
-          auto arg = [&](int g, int c) {
-            const float2 y = pair_of(v[g], c);
-            if constexpr (kForm == 1 || kForm == 2) {       // y (scale2 + scale2 t(y^2)) + n
-              const float2 q = fmul2(y, y);
-              float2 z;
-              if constexpr (kForm == 1) {
-                z = ffma2(q, F.e3[3], F.e3[2]);
-                z = ffma2(q, z, F.e3[1]);
-                z = ffma2(q, z, F.e3[0]);
-              } else {
-                z = ffma2(q, F.e5[5], F.e5[4]);
-                z = ffma2(q, z, F.e5[3]);
-                z = ffma2(q, z, F.e5[2]);
-                z = ffma2(q, z, F.e5[1]);
-                z = ffma2(q, z, F.e5[0]);
-              }
-              return ffma2(y, z, n2);
+          const float z2 = F.zscale * (2.f * kLog2e), top = F.inv * fs;
+          auto capped = [&](float2 x) {           // x (scale2 + scale2 t(x^2)) + n
+            const float2 q = fmul2(x, x);
+            float2 t;
+            if constexpr (kForm == 1) {
+              t = ffma2(q, F.e3[3], F.e3[2]);
+              t = ffma2(q, t, F.e3[1]);
+              t = ffma2(q, t, F.e3[0]);
             } else {
-              return ffma2(y, f2, n2);
+              t = ffma2(q, F.e5[5], F.e5[4]);
+              t = ffma2(q, t, F.e5[3]);
+              t = ffma2(q, t, F.e5[2]);
+              t = ffma2(q, t, F.e5[1]);
+              t = ffma2(q, t, F.e5[0]);
+            }
+            return ffma2(x, t, n2);
+          };
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            float2 e0 = pair_of(y, j), e1 = pair_of(y, j + 2);
+            if constexpr (kForm == 3) {
+              tanh4(e0, e1, z2, top + neg, -2.f * top);
+            } else if constexpr (kForm == 0) {
+              e0 = ffma2(e0, f2, n2);
+              e1 = ffma2(e1, f2, n2);
+            } else {
+              e0 = capped(e0);
+              e1 = capped(e1);
+            }
+            e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
+            e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
+            la = fadd2(la, e0);
+            lb = fadd2(lb, e1);
+            const __nv_bfloat162 b0 = __floats2bfloat162_rn(e0.x, e0.y), b1 = __floats2bfloat162_rn(e1.x, e1.y);
+            pk[j / 2] = *reinterpret_cast<const uint32_t*>(&b0);
+            pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&b1);
+          }
+        };
+        auto last_p_read = [&]() {               // (split)
+          if (!kSplit || !ns) return;
+          ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[w], (ns - 1) & 1, status));
+          tc_fence_after();
+        };
+        auto hand_in = [&](int half) {
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[2 * w + half]);
+        };
+        if constexpr (CAP) {
+          last_p_read();
+          if (!ok) break;
+          auto columns = [&](auto FORM) {
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {       // (over the scores: P's 16 columns end before the next 32 begin)
+              tmem_ld32(s_addr + 32 * g, v[0]);
+              tmem_ld_wait();
+              if (kSplit && g == 3) {
+                tc_fence_before();
+                mbar_arrive(&s_free[w]);
+              }
+              uint32_t pk[16];
+              weights(FORM, v[0], pk);
+              tmem_st16(p_addr + 16 * g, pk);
+              if (g & 1) hand_in(g >> 1);
             }
           };
+          if (form == 1) columns(std::integral_constant<int, 1>{});
+          else if (form == 2) columns(std::integral_constant<int, 2>{});
+          else if (form == 3) columns(std::integral_constant<int, 3>{});
+          else columns(std::integral_constant<int, 0>{});
+        } else {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t pk[32];
-#pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-              const int g = 2 * half + j / 32, c = j % 32;
-              float2 e0 = arg(g, c), e1 = arg(g, c + 2);
-              e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
-              e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
-              la = fadd2(la, e0);
-              lb = fadd2(lb, e1);
-              const __nv_bfloat162 b0 = __floats2bfloat162_rn(e0.x, e0.y), b1 = __floats2bfloat162_rn(e1.x, e1.y);
-              pk[j / 2] = *reinterpret_cast<const uint32_t*>(&b0);
-              pk[j / 2 + 1] = *reinterpret_cast<const uint32_t*>(&b1);
-            }
-            if (kSplit && half == 0 && ns) {       // the last P has been read
-              ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[w], (ns - 1) & 1, status));
-              if (!ok) return;
-              tc_fence_after();
-            }
+            weights(std::integral_constant<int, 0>{}, v[2 * half], pk);
+            weights(std::integral_constant<int, 0>{}, v[2 * half + 1], pk + 16);
+            if (half == 0) last_p_read();
+            if (!ok) break;
             tmem_st32(p_addr + 32 * half, pk);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&p_full[2 * w + half]);
+            hand_in(half);
           }
-        };
-        if constexpr (CAP) {
-          if (form == 1) exps(std::integral_constant<int, 1>{});
-          else if (form == 2) exps(std::integral_constant<int, 2>{});
-          else exps(std::integral_constant<int, 0>{});
-        } else {
-          exps(std::integral_constant<int, 0>{});
         }
         if (!ok) break;
         ++ns;

@@ -348,7 +348,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     const StepPiece u = *reinterpret_cast<const StepPiece*>(smem + L::kUnit + (n % kUnits) * sizeof(StepPiece));
     if (u.t1 == 0) break;
     // queries as the products' second operand: row 8 t + g, four head dimensions a step of 16.  Scores and
-    // weights then are of rows 8 t + 2 q and + 1
+    // weights then are of rows 8 t + 2 q and + 1.  Two row tiles' operands are kept in shared memory, in the
+    // queries' place, a 16-byte word a lane and step: in registers they spill (179 instead of XX us on two
+    // sequences of 131972, 16 rows)
+    constexpr bool kShared = NT == 2;
+    uint8_t* frag = smem + L::kQ + (n % kUnits) * L::kRows * D * 2 + lane * 16;
     uint32_t b[kSteps][NT][2];
     float2 rowf[NT];
     int pos[NT][2];
@@ -388,8 +392,29 @@ __global__ void __launch_bounds__(kThreads, 2)
         pos[t][r] = u.pos0 + (u.row + (row < u.rows ? row : 0)) / group;
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&unit_done[n % kUnits]);
+    if constexpr (kShared) {
+      named_bar_sync(1, kComputeWarps * 32);           // every warp has read the queries
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        if (s / (kSteps / kComputeWarps) == warp)
+          *reinterpret_cast<uint4*>(frag + s * 512) = make_uint4(b[s][0][0], b[s][0][1], b[s][NT - 1][0], b[s][NT - 1][1]);
+      named_bar_sync(1, kComputeWarps * 32);
+    } else {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&unit_done[n % kUnits]);
+    }
+    auto operand = [&](int s, uint32_t (&y)[NT][2]) {
+      if constexpr (kShared) {
+        const uint4 f = *reinterpret_cast<const uint4*>(frag + s * 512);
+        y[0][0] = f.x;
+        y[0][1] = f.y;
+        y[NT - 1][0] = f.z;
+        y[NT - 1][1] = f.w;
+      } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) y[t][0] = b[s][t][0], y[t][1] = b[s][t][1];
+      }
+    };
     float o[kOut][NT][4] = {};
     float m[NT][2], M[NT][2];
     float2 l[NT], neg[NT], Neg[NT];      // neg, Neg: -m and 13 - M, 0 while they are infinite
@@ -417,45 +442,63 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint8_t* stage = smem + st * L::kStage;
       const int c0 = (u.tile + tile) * kStepTile;
       const bool edge = c0 + kStepTile > u.keys || c0 < u.lo;       // what is no key of the sequence may be anything
-      // scores of keys c0 + key0 + 16 i + 8 h + g; two chains of products each
+      // scores of keys c0 + key0 + 16 i + 8 h + g, in four chains of products
+      constexpr int kChains = NT == 1 ? 2 : 1;
       float2 x[2][2][NT];        // [i][h][t]
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float s[2][NT][4] = {};
+      {
+        float s[2][kChains][NT][4] = {};
         if constexpr (E4M3) {
-          uint4 w[2][D / 64];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int j = 0; j < D / 64; ++j) {
+            uint4 w[2][2];
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j)
-              w[h][j] = *reinterpret_cast<const uint4*>(stage + at_k[j] + (16 * i + 8 * h) * L::kBoxBytes);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < kSteps; ++j) {
-            const uint32_t w0 = (&w[0][j / 4].x)[j % 4], w1 = (&w[1][j / 4].x)[j % 4];
-            const uint32_t a[4] = {codes_f16(w0), codes_f16(w1), codes_f16_hi(w0), codes_f16_hi(w1)};
+              for (int h = 0; h < 2; ++h) w[i][h] = *reinterpret_cast<const uint4*>(stage + at_k[j] + (16 * i + 8 * h) * L::kBoxBytes);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16816<true>(s[j & 1][t], a, b[j][t][0], b[j][t][1]);
+            for (int k = 0; k < 4; ++k) {
+              uint32_t y[NT][2];
+              operand(4 * j + k, y);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t w0 = (&w[i][0].x)[k], w1 = (&w[i][1].x)[k];
+                const uint32_t a[4] = {codes_f16(w0), codes_f16(w1), codes_f16_hi(w0), codes_f16_hi(w1)};
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16816<true>(s[i][k % kChains][t], a, y[t][0], y[t][1]);
+              }
+            }
           }
         } else {
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
-            uint4 w[2];
+            uint32_t y0[NT][2], y1[NT][2];
+            operand(2 * j, y0);
+            operand(2 * j + 1, y1);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              w[h] = *reinterpret_cast<const uint4*>(stage + at_k[j & 1] + (j >> 1) * kStepTile * 128 + (16 * i + 8 * h) * 128);
-            const uint32_t a0[4] = {w[0].x, w[1].x, w[0].y, w[1].y}, a1[4] = {w[0].z, w[1].z, w[0].w, w[1].w};
+            for (int i = 0; i < 2; ++i) {
+              uint4 w[2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              mma16816<false>(s[0][t], a0, b[2 * j][t][0], b[2 * j][t][1]);
-              mma16816<false>(s[1][t], a1, b[2 * j + 1][t][0], b[2 * j + 1][t][1]);
+              for (int h = 0; h < 2; ++h)
+                w[h] = *reinterpret_cast<const uint4*>(stage + at_k[j & 1] + (j >> 1) * kStepTile * 128 + (16 * i + 8 * h) * 128);
+              const uint32_t a0[4] = {w[0].x, w[1].x, w[0].y, w[1].y}, a1[4] = {w[0].z, w[1].z, w[0].w, w[1].w};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                mma16816<false>(s[i][0][t], a0, y0[t][0], y0[t][1]);
+                mma16816<false>(s[i][kChains - 1][t], a1, y1[t][0], y1[t][1]);
+              }
             }
           }
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            x[i][h][t] = fmul2(fadd2(make_float2(s[0][t][2 * h], s[0][t][2 * h + 1]), make_float2(s[1][t][2 * h], s[1][t][2 * h + 1])), rowf[t]);
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              x[i][h][t] = make_float2(s[i][0][t][2 * h], s[i][0][t][2 * h + 1]);
+              if constexpr (kChains == 2) x[i][h][t] = fadd2(x[i][h][t], make_float2(s[i][1][t][2 * h], s[i][1][t][2 * h + 1]));
+              x[i][h][t] = fmul2(x[i][h][t], rowf[t]);
+            }
       }
       float e[2][2];           // exponents of the values' scales
       if constexpr (E4M3) {
@@ -662,6 +705,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           y[L::kRows] = sum;
         }
       }
+    if (kShared) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&unit_done[n % kUnits]);
+    }
     ok = named_bar_and(1, kComputeWarps * 32, ok);
     if (!ok) break;
 #pragma unroll
