@@ -544,7 +544,7 @@ class FlamiaScoredAttention:
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
 
     def _want(self, name, t, shape, dtype):
-        if t.dtype != dtype or tuple(t.shape) != shape or t.device != self.device or not t.is_contiguous():
+        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
             raise FlamiaError(f"{name}: want contiguous {dtype} {shape} on {self.device}, got {t.dtype} {tuple(t.shape)} "
                               f"on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
@@ -727,7 +727,7 @@ class FlamiaCachedAttention:
         self._ws_bytes = flamia_cached_fwd_workspace_bytes(hq, hkv, head_dim, self.max_chunk)
         self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
         # a step's calls are many and small: what does not change is worked out once
-        self._lib, self._plan_ptr = lib(), self.plan.data_ptr()
+        self._lib, self._plan_ptr, self._bf16, self._i32 = lib(), self.plan.data_ptr(), torch.bfloat16, torch.int32
         self._kind = (page_size, hkv, head_dim, dev)
         self._q_shape, self._kv_shape = (total_tokens, hq, head_dim), (total_tokens, hkv, head_dim)
         self._table_shape = (num_seqs, self.max_pages)
@@ -736,53 +736,51 @@ class FlamiaCachedAttention:
     _run = FlamiaScoredAttention._run
 
     def _places(self, cache, page_table):
-        import torch
         if cache.kind != self._kind:
             raise FlamiaError(f"cache: want pages of {self.page_size}, {self.hkv} heads of {self.d} on {self.device}, got "
                               f"{cache.page_size}, {cache.hkv}, {cache.d} on {cache.device}")
-        self._want("page_table", page_table, self._table_shape, torch.int32)
+        self._want("page_table", page_table, self._table_shape, self._i32)
         if not self._planned:
             raise FlamiaError("FlamiaCachedAttention: plan_build has not been called")
 
     def plan_build(self, cu_seqlens, kv_lens, stream=None):
-        import torch
-        self._want("cu_seqlens", cu_seqlens, (self.N + 1,), torch.int32)
-        self._want("kv_lens", kv_lens, (self.N,), torch.int32)
+        self._want("cu_seqlens", cu_seqlens, (self.N + 1,), self._i32)
+        self._want("kv_lens", kv_lens, (self.N,), self._i32)
         self._run(lambda stm: flamia_cache_plan_build(cu_seqlens, kv_lens, self.N, self.T, self.hq, self.hkv, self.max_chunk,
                                                       self.max_pages * self.page_size, self.window, self.plan, stm), stream)
         self._planned = True
 
     def write(self, cache: FlamiaPagedCache, k, v, page_table, stream=None):
         """The new tokens' keys and values into the cache."""
-        import torch
         self._places(cache, page_table)
-        self._want("k", k, self._kv_shape, torch.bfloat16)
-        self._want("v", v, self._kv_shape, torch.bfloat16)
+        self._want("k", k, self._kv_shape, self._bf16)
+        self._want("v", v, self._kv_shape, self._bf16)
         rc = self._run(lambda stm: self._lib.flamia_cache_write(
             cache.ref, page_table.data_ptr(), self.max_pages, self.N, self.T, self._plan_ptr, k.data_ptr(), v.data_ptr(), stm), stream)
-        _check(rc, "flamia_cache_write")
+        if rc:
+            _check(rc, "flamia_cache_write")
 
     def read(self, cache: FlamiaPagedCache, page_table, k, v, stream=None):
         """The new tokens' keys and values from the cache into k and v, which are returned."""
-        import torch
         self._places(cache, page_table)
-        self._want("k", k, self._kv_shape, torch.bfloat16)
-        self._want("v", v, self._kv_shape, torch.bfloat16)
+        self._want("k", k, self._kv_shape, self._bf16)
+        self._want("v", v, self._kv_shape, self._bf16)
         rc = self._run(lambda stm: self._lib.flamia_cache_read(
             cache.ref, page_table.data_ptr(), self.max_pages, self.N, self.T, self._plan_ptr, k.data_ptr(), v.data_ptr(), stm), stream)
-        _check(rc, "flamia_cache_read")
+        if rc:
+            _check(rc, "flamia_cache_read")
         return k, v
 
     def forward(self, cache: FlamiaPagedCache, q, page_table, softmax_scale: float = 0.0, stream=None):
         """(out bf16 [T, hq, d], lse fp32 [hq, T]) of the new tokens, whose keys and values have been written."""
-        import torch
         self._places(cache, page_table)
-        self._want("q", q, self._q_shape, torch.bfloat16)
+        self._want("q", q, self._q_shape, self._bf16)
         out, lse, ws = self.out, self.lse, self.workspace
         rc = self._run(lambda stm: self._lib.flamia_cached_fwd(
             q.data_ptr(), cache.ref, page_table.data_ptr(), self.max_pages, self.N, self.T, self.hq, self.max_chunk, self.window,
             self.softcap, softmax_scale, self._plan_ptr, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), self._ws_bytes, stm), stream)
-        _check(rc, "flamia_cached_fwd")
+        if rc:
+            _check(rc, "flamia_cached_fwd")
         return out, lse
 
     def device_status(self, stream=None) -> int:

@@ -4,10 +4,9 @@
 // work: the steps' key tiles and the chunk items, each with the running sum of its key tiles, so
 // that a kernel can deal the key tiles out evenly whatever the sequences are.
 //
-// Writing quantizes each (token, head) row by itself, the per-token form of the operand quantizer:
-// a later token changes no earlier one's code.  e = least integer with amax <= 448 2^e.
-// Both directions move every byte once and are bound by memory: a warp takes a token's rows (of
-// all heads, K and V), 16 bytes a lane and load, four loads in flight.
+// Writing quantizes each (token, head) row by itself, the per-token form of the operand quantizer: a later token changes
+// no earlier one's code.  Both directions move every byte once.
+#include <algorithm>
 #include <type_traits>
 
 #include "cache.cuh"
@@ -178,141 +177,192 @@ __global__ void __launch_bounds__(kPlanThreads)
     shares(std::integral_constant<int, 0>{}, chunk_places * hkv, items, 2 + kChunkExtra, kChunkCtas, threadIdx.x - kStepCtas);
 }
 
-// ---------------------------------------------------------------- write, read
-constexpr int kWarps = 8;
-constexpr int kRowsPerWarp = 16;      // of a token's 2 hkv rows
-
-// A warp's token and where its rows live: false where there is nothing to do.
-struct TokenPlace {
-  int token, first;      // first of its rows
-  bool tail;             // behind the last sequence, or its page is none
-  int64_t base;          // row of kv head 0 in the pools
-};
-__device__ __forceinline__ bool place_token(const CacheParams& p, TokenPlace& t) {
-  const int parts = (2 * p.hkv + kRowsPerWarp - 1) / kRowsPerWarp;
-  const int64_t job = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (job >= (int64_t)p.T * parts) return false;
-  t.token = (int)(job / parts);
-  t.first = (int)(job % parts) * kRowsPerWarp;
-  t.tail = t.token >= cache_valid_rows(p);
-  t.base = 0;
-  if (t.tail) return true;
-  const int4* seq = reinterpret_cast<const int4*>(p.plan + kCpHeaderWords);
-  const int n = warp_upper(p.N, t.token, [&](int i) { return seq[i].x; });
-  const int4 r = seq[n];
-  const int pos = r.z - r.y + t.token - r.x;
-  const int page = cache_page(p, n, pos >> p.page_shift);
-  t.tail = page < 0;
-  t.base = ((int64_t)page * p.hkv << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
-  return true;
+// The sequence and the position of each row.
+__global__ void __launch_bounds__(256) cache_rows_kernel(int N, int T, int hq, int hkv, void* plan) {
+  const CachePlanView pv = cache_plan_view(plan, T, N, hq, hkv);
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= pv.hdr[kCpValid]) return;
+  int lo = 0, hi = N;          // the last sequence that begins at t or before
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pv.seq[mid].x <= t) lo = mid; else hi = mid;
+  }
+  const int4 r = pv.seq[lo];
+  pv.row[t] = make_int2(lo, r.z - r.y + t - r.x);
 }
+
+// ---------------------------------------------------------------- write, read
+// A warp takes the rows (of all heads) of some tokens, of K or of V: a stream on the packed side.  16 elements a lane, so that
+// what a row needs once (its largest value, its scale, its place) is shared by few lanes: with 8 the
+// instructions bound it (write of 16384 tokens, 16 heads, d 128: XX us, 70% of the issue slots).  Where the tokens live
+// it looks up once, a lane a token.
+constexpr int kWarps = 8;
+constexpr int kRowsPerWarp = 64;
+
+struct TokenGroup {
+  int token, n;      // first token, tokens
+  bool v;            // V's rows, not K's
+};
+__device__ __forceinline__ TokenGroup token_group(const CacheParams& p, int per) {
+  const int64_t job = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), at = (job >> 1) * per;
+  TokenGroup g;
+  g.v = job & 1;
+  g.token = (int)min(at, (int64_t)p.T);
+  g.n = min(per, p.T - g.token);
+  return g;
+}
+// The lane's token's place (row of kv head 0 in the pools), -1 where it has none: behind the last sequence, or no page.
+__device__ __forceinline__ int64_t token_place(const CacheParams& p, const TokenGroup& g, int lane, int valid) {
+  if (lane >= g.n || g.token + lane >= valid) return -1;
+  const int2 r = reinterpret_cast<const int2*>(p.plan + kCpHeaderWords)[g.token + lane];
+  const int page = cache_page(p, r.x, r.y >> p.page_shift);
+  return page < 0 ? -1 : ((int64_t)page * p.hkv << p.page_shift) + (r.y & ((1 << p.page_shift) - 1));
+}
+// A row's lanes: 16-byte words seg and seg + kLanes of it; kPer rows a load.
+template <int D>
+struct RowLanes {
+  static constexpr int kLanes = D / 16, kPer = 32 / kLanes, kUnroll = 2;
+};
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CacheParams p, const uint4* __restrict__ k,
-                                                                  const uint4* __restrict__ v) {
-  constexpr int kLanes = D / 8, kPer = 32 / kLanes;      // lanes a row, rows a load
-  TokenPlace t;
-  if (!place_token(p, t) || t.tail) return;
-  const int lane = threadIdx.x & 31, sub = lane / kLanes, seg = lane % kLanes;
-  const int rows = min(2 * p.hkv, t.first + kRowsPerWarp);
-  constexpr int kUnroll = 4;
-  for (int r0 = t.first; r0 < rows; r0 += kUnroll * kPer) {
-    uint4 x[kUnroll];
+                                                                  const uint4* __restrict__ v, const int per,
+                                                                  const uint32_t inv_hkv) {
+  using R = RowLanes<D>;
+  const TokenGroup g = token_group(p, per);
+  if (g.n <= 0) return;
+  const int lane = threadIdx.x & 31, sub = lane / R::kLanes, seg = lane % R::kLanes, rows = g.n * p.hkv;
+  const uint4* src = (g.v ? v : k) + (int64_t)g.token * p.hkv * (D / 8) + seg;
+  uint8_t* pool = g.v ? p.v : p.k;
+  uint8_t* scales = g.v ? p.v_scales : p.k_scales;
+  int64_t places = -2;
+  for (int r0 = 0; r0 < rows; r0 += R::kUnroll * R::kPer) {
+    uint4 x[R::kUnroll][2];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + u * kPer + sub, h = r < p.hkv ? r : r - p.hkv;
-      x[u] = r < rows ? ((r < p.hkv ? k : v)[((int64_t)t.token * p.hkv + h) * kLanes + seg]) : make_uint4(0, 0, 0, 0);
-    }
+    for (int u = 0; u < R::kUnroll; ++u)
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + u * kPer + sub, h = r < p.hkv ? r : r - p.hkv;
-      const int64_t at = t.base + ((int64_t)h << p.page_shift);
-      uint8_t* pool = r < p.hkv ? p.k : p.v;
+      for (int j = 0; j < 2; ++j) {
+        const int r = r0 + u * R::kPer + sub;
+        x[u][j] = r < rows ? src[r * (D / 8) + j * R::kLanes] : make_uint4(0, 0, 0, 0);
+      }
+    if (places == -2) places = token_place(p, g, lane, cache_valid_rows(p));     // (while the first loads fly)
+#pragma unroll
+    for (int u = 0; u < R::kUnroll; ++u) {
+      const int r = r0 + u * R::kPer + sub, i = p.hkv == 1 ? r : (int)__umulhi((uint32_t)r, inv_hkv);     // token r / hkv
+      const int64_t base = __shfl_sync(0xffffffffu, places, i & 31);
+      const int64_t at = base + ((int64_t)(r - i * p.hkv) << p.page_shift);
+      const bool use = r < rows && base >= 0;
       if constexpr (E4M3) {
-        // the largest magnitude by its bits: a NaN's are above infinity's
+        // the largest magnitude by its bits (a NaN's are above infinity's): e = least integer with amax <= 448 2^e is
+        // the exponent less 8, and one more above 1.75; byte e + 127
         const uint32_t m7 = 0x7fff7fffu;
-        uint32_t m = __vmaxu2(__vmaxu2(x[u].x & m7, x[u].y & m7), __vmaxu2(x[u].z & m7, x[u].w & m7));
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[u][j].x & m7, x[u][j].y & m7), __vmaxu2(x[u][j].z & m7, x[u][j].w & m7)));
+#pragma unroll
+        for (int o = R::kLanes / 2; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
         m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const bool nan = m > 0x7f80u;
-        const int e = nan ? 128 : roundup_exp(__uint_as_float(m << 16));
-        const float inv = nan ? 0.f : exp2i(-e);
-        uint32_t c[4];
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        const uint32_t byte = nan ? 255u : m == 0 ? 127u : max((m + 31) >> 7, 8u) - 8;
+        const float f = nan ? 0.f : __uint_as_float((254 - byte) << 23);      // 2^-e
+        const float2 f2 = make_float2(f, f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = __uint_as_float(w[i] << 16) * inv, b = __uint_as_float(w[i] & 0xffff0000u) * inv;
-          c[i] = nan ? 0u : e4m3x2(a, b);
+        for (int j = 0; j < 2; ++j) {
+          uint32_t c[4];
+          const uint32_t w[4] = {x[u][j].x, x[u][j].y, x[u][j].z, x[u][j].w};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const float2 y = fmul2(make_float2(__uint_as_float(w[t] << 16), __uint_as_float(w[t] & 0xffff0000u)), f2);
+            c[t] = e4m3x2(y.x, y.y);
+          }
+          if (use)
+            *reinterpret_cast<uint2*>(pool + at * D + (j * R::kLanes + seg) * 8) =
+                nan ? make_uint2(0, 0) : make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
         }
-        if (r < rows) {
-          *reinterpret_cast<uint2*>(pool + at * D + seg * 8) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-          if (seg == 0) (r < p.hkv ? p.k_scales : p.v_scales)[at] = (uint8_t)(e + 127);
-        }
-      } else if (r < rows) {
-        *reinterpret_cast<uint4*>(pool + (at * D + seg * 8) * 2) = x[u];
+        if (use && seg == 0) scales[at] = (uint8_t)byte;
+      } else if (use) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4*>(pool + (at * D + (j * R::kLanes + seg) * 8) * 2) = x[u][j];
       }
     }
   }
 }
 
-__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t bf16x2_bits(float2 a) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y);
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const CacheParams p, uint4* __restrict__ k,
-                                                                 uint4* __restrict__ v) {
-  constexpr int kLanes = D / 8, kPer = 32 / kLanes;
-  TokenPlace t;
-  if (!place_token(p, t)) return;
-  const int lane = threadIdx.x & 31, sub = lane / kLanes, seg = lane % kLanes;
-  const int rows = min(2 * p.hkv, t.first + kRowsPerWarp);
-  constexpr int kUnroll = 4;
-  for (int r0 = t.first; r0 < rows; r0 += kUnroll * kPer) {
-    uint4 x[kUnroll];
-    float f[kUnroll];
+                                                                 uint4* __restrict__ v, const int per,
+                                                                 const uint32_t inv_hkv) {
+  using R = RowLanes<D>;
+  const TokenGroup g = token_group(p, per);
+  if (g.n <= 0) return;
+  const int lane = threadIdx.x & 31, sub = lane / R::kLanes, seg = lane % R::kLanes, rows = g.n * p.hkv;
+  uint4* dst = (g.v ? v : k) + (int64_t)g.token * p.hkv * (D / 8) + seg;
+  const uint8_t* pool = g.v ? p.v : p.k;
+  const uint8_t* scales = g.v ? p.v_scales : p.k_scales;
+  const int64_t places = token_place(p, g, lane, cache_valid_rows(p));
+  for (int r0 = 0; r0 < rows; r0 += R::kUnroll * R::kPer) {
+    uint4 x[R::kUnroll][2];
+    uint32_t b[R::kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + u * kPer + sub, h = r < p.hkv ? r : r - p.hkv;
-      const int64_t at = t.base + ((int64_t)h << p.page_shift);
-      const uint8_t* pool = r < p.hkv ? p.k : p.v;
-      x[u] = make_uint4(0, 0, 0, 0);
-      f[u] = 0.f;
-      if (r < rows && !t.tail) {
+    for (int u = 0; u < R::kUnroll; ++u) {
+      const int r = r0 + u * R::kPer + sub, i = p.hkv == 1 ? r : (int)__umulhi((uint32_t)r, inv_hkv);
+      const int64_t base = __shfl_sync(0xffffffffu, places, i & 31);
+      const int64_t at = base + ((int64_t)(r - i * p.hkv) << p.page_shift);
+      const bool use = r < rows && base >= 0;
+      b[u] = E4M3 && use ? scales[at] : 127;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[u][j] = make_uint4(0, 0, 0, 0);
         if constexpr (E4M3) {
-          const uint2 c = *reinterpret_cast<const uint2*>(pool + at * D + seg * 8);
-          x[u].x = c.x;
-          x[u].y = c.y;
-          f[u] = cache_scale((r < p.hkv ? p.k_scales : p.v_scales)[at]);
-        } else {
-          x[u] = *reinterpret_cast<const uint4*>(pool + (at * D + seg * 8) * 2);
+          const uint2 c = use ? *reinterpret_cast<const uint2*>(pool + at * D + (j * R::kLanes + seg) * 8) : make_uint2(0, 0);
+          x[u][j].x = c.x;
+          x[u][j].y = c.y;
+        } else if (use) {
+          x[u][j] = *reinterpret_cast<const uint4*>(pool + (at * D + (j * R::kLanes + seg) * 8) * 2);
         }
       }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + u * kPer + sub, h = r < p.hkv ? r : r - p.hkv;
-      if constexpr (E4M3) {
-        uint32_t y[4];
-        const uint32_t w[2] = {x[u].x, x[u].y};
+    for (int u = 0; u < R::kUnroll; ++u) {
+      const int r = r0 + u * R::kPer + sub;
+      const float f = cache_scale(b[u]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
-          const float2 ab = __half22float2(__half2(hr));
-          y[i] = bf16x2_bits(ab.x * f[u], ab.y * f[u]);
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (E4M3) {
+          uint32_t y[4];
+          const uint32_t w[2] = {x[u][j].x, x[u][j].y};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[t / 2] >> (16 * (t & 1))), __NV_E4M3);
+            y[t] = bf16x2_bits(fmul2(__half22float2(__half2(hr)), make_float2(f, f)));
+          }
+          x[u][j] = make_uint4(y[0], y[1], y[2], y[3]);
         }
-        x[u] = make_uint4(y[0], y[1], y[2], y[3]);
+        if (r < rows) dst[r * (D / 8) + j * R::kLanes] = x[u][j];
       }
-      if (r < rows) (r < p.hkv ? k : v)[((int64_t)t.token * p.hkv + h) * kLanes + seg] = x[u];
     }
   }
 }
 
-inline int64_t token_blocks(const CacheParams& p) {
-  const int64_t parts = (2 * p.hkv + kRowsPerWarp - 1) / kRowsPerWarp;
-  return ((int64_t)p.T * parts + kWarps - 1) / kWarps;
+// Tokens a warp: kRowsPerWarp rows where that leaves the GPU's warps busy.
+struct TokenGrid {
+  int per;
+  int64_t blocks;
+  uint32_t inv_hkv;      // ceil(2^32 / hkv): r / hkv by a multiplication, exact for r below 2^32 / hkv
+};
+inline TokenGrid token_grid(const CacheParams& p) {
+  TokenGrid g;
+  const int64_t most = std::min<int64_t>(32, (kRowsPerWarp + p.hkv - 1) / p.hkv);
+  g.per = (int)std::min<int64_t>(std::max<int64_t>((int64_t)p.T * 2 / (152 * 32), 1), most);
+  g.blocks = (((int64_t)p.T + g.per - 1) / g.per * 2 + kWarps - 1) / kWarps;
+  g.inv_hkv = (uint32_t)((((uint64_t)1 << 32) + p.hkv - 1) / p.hkv);
+  return g;
 }
 
 }  // namespace
@@ -320,24 +370,25 @@ inline int64_t token_blocks(const CacheParams& p) {
 cudaError_t launch_cache_plan(const int32_t* cu, const int32_t* kv, int N, int T, int hq, int hkv, int max_chunk,
                               int64_t max_kv, int left, void* plan, cudaStream_t s) {
   cache_plan_kernel<<<1, kPlanThreads, 0, s>>>(cu, kv, N, T, hq, hkv, max_chunk, max_kv, left, plan);
+  if (T > 0) cache_rows_kernel<<<(T + 255) / 256, 256, 0, s>>>(N, T, hq, hkv, plan);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_write(int D, bool e4m3, const CacheParams& p, const void* k, const void* v, cudaStream_t s) {
-  const int64_t blocks = token_blocks(p);
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const TokenGrid g = token_grid(p);
+  if (g.blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const auto f = D == 128 ? (e4m3 ? cache_write_kernel<128, true> : cache_write_kernel<128, false>)
                           : (e4m3 ? cache_write_kernel<64, true> : cache_write_kernel<64, false>);
-  f<<<(unsigned)blocks, kWarps * 32, 0, s>>>(p, static_cast<const uint4*>(k), static_cast<const uint4*>(v));
+  f<<<(unsigned)g.blocks, kWarps * 32, 0, s>>>(p, static_cast<const uint4*>(k), static_cast<const uint4*>(v), g.per, g.inv_hkv);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(int D, bool e4m3, const CacheParams& p, void* k, void* v, cudaStream_t s) {
-  const int64_t blocks = token_blocks(p);
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const TokenGrid g = token_grid(p);
+  if (g.blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const auto f = D == 128 ? (e4m3 ? cache_read_kernel<128, true> : cache_read_kernel<128, false>)
                           : (e4m3 ? cache_read_kernel<64, true> : cache_read_kernel<64, false>);
-  f<<<(unsigned)blocks, kWarps * 32, 0, s>>>(p, static_cast<uint4*>(k), static_cast<uint4*>(v));
+  f<<<(unsigned)g.blocks, kWarps * 32, 0, s>>>(p, static_cast<uint4*>(k), static_cast<uint4*>(v), g.per, g.inv_hkv);
   return cudaGetLastError();
 }
 

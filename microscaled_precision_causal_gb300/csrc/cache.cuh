@@ -54,6 +54,7 @@ static_assert(sizeof(CachedUnit) == 56, "");
 constexpr int kStepCtas = 304, kChunkCtas = 152, kDone = kStepCtas + 8 * kChunkCtas;
 struct CachePlanView {
   int* hdr;
+  int2* row;                  // [T] {sequence, position} of the sequences' rows
   int4* seq;                  // [N] {first token, new tokens, keys with them, first key that the first new one sees}
   CacheItem* items[2];        // [cap] chunk items, [kStepTiles N] steps
   int64_t* prefix[2];         // [items + 1] places of the items before, for one kv head
@@ -65,12 +66,13 @@ struct CachePlanView {
 __host__ __device__ inline int64_t cache_item_capacity(int64_t T, int N, int hq, int hkv) {
   return T * (hq / hkv) / kChunkRows + N;
 }
-// The sequences come first: writing and reading the cache need no more of the layout.
+// The rows come first: writing and reading the cache need no more of the layout.
 __host__ __device__ inline CachePlanView cache_plan_view(const void* plan, int64_t T, int N, int hq, int hkv, size_t* bytes = nullptr) {
   const int64_t cap = cache_item_capacity(T, N, hq, hkv);
   CachePlanView v;
   v.hdr = (int*)plan;
-  v.seq = (int4*)(v.hdr + kCpHeaderWords);
+  v.row = (int2*)(v.hdr + kCpHeaderWords);
+  v.seq = (int4*)(v.row + ((T + 1) & ~(int64_t)1));
   v.items[0] = (CacheItem*)(v.seq + N);
   v.items[1] = v.items[0] + cap;
   v.prefix[0] = (int64_t*)(v.items[1] + (int64_t)kStepTiles * N);
@@ -109,19 +111,6 @@ __device__ __forceinline__ int cache_page(const CacheParams& p, int n, int i) {
   if ((unsigned)page < (unsigned)p.num_pages) return page;
   atomicOr(p.plan + kCpStatus, FLAMIA_DEV_BAD_PAGE);
   return -1;
-}
-// Largest n in [0, N) with at(n) <= x, at non-decreasing and at(0) <= x: 32 probes a round by a whole warp.
-template <class At, class X>
-__device__ __forceinline__ int warp_upper(int N, X x, At at) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = N;
-  while (n > 1) {
-    const int step = (n + 31) / 32, i = lo + lane * step;
-    const int below = __popc(__ballot_sync(0xffffffffu, lane * step < n && at(i) <= x)) - 1;
-    lo += below * step;
-    n = min(step, n - below * step);
-  }
-  return lo;
 }
 // 2^(b - 127), NaN for 255.
 __device__ __forceinline__ float cache_scale(uint32_t b) { return b == 255 ? __uint_as_float(0x7fc00000u) : ue8m0_to_f32(b); }

@@ -17,7 +17,8 @@
 //   warp 1        MMA issuer (at D = 64 of the first row tile; warp 3 of the second)
 //   warp 2        TMEM allocator; finds the units ahead and loads their queries
 //   warps 4-11    softmax, a warpgroup per row tile, thread = row; they write the unit's O too
-//   warps 12-15   E4M3: unpack
+//   warps 12-15   E4M3: unpack (eight warps, four each for K and V, at 136 registers for the softmax: 475 instead of 419
+//                 us for a chunk of 2048 behind 14336)
 // TMEM columns as in the scored forward.
 #include <type_traits>
 
@@ -29,11 +30,12 @@ namespace flamia {
 
 namespace {
 
+
 constexpr int kThreads = 512;
 constexpr float kRescaleAbove = 8.f, kLoose = 64.f;
 constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
-constexpr int kRegCtl = 64, kRegAux = 80, kRegSoftmax = 184;
-static_assert(kRegCtl * 128 + kRegAux * 128 + kRegSoftmax * 256 <= kLaunchRegs * kThreads, "register split");
+constexpr int kRegCtl = 64, kRegUnpack = 80, kRegSoftmax = 184;
+static_assert(kRegCtl * 128 + kRegUnpack * 128 + kRegSoftmax * 256 <= kLaunchRegs * kThreads, "register split");
 
 // x - m is one multiply-add while m was rounded: from |m| = 2^28 on both are shrunk (as in the scored forward).
 __device__ __forceinline__ float shrink_for(float m) {
@@ -618,19 +620,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[w], ns & 1, status));
         if (!ok) break;
         tc_fence_after();
-        // Without a cap a row's products stay in registers, all code unrolled.  With one they are read again 32 columns at
-        // a time, in rolled loops: four forms of 128 columns are some 100 KB of instructions, whose first pass took 25 us
-        // a call, and spilled.
-        uint32_t v[CAP ? 1 : 4][32];
+        // At D = 64 without a cap a row's products stay in registers, all code unrolled: the scores' place is free for the
+        // next ones early (1.31 instead of 1.50 us a key tile).  Else they are read again 32 columns at a time, in rolled loops:
+        // with a cap four forms of 128 columns were some 100 KB of instructions, whose first pass took 25 us a call, and
+        // spilled; at D = 128 P lies over the scores anyway (E4M3 419 instead of 427 us for a chunk of 2048 behind 14336,
+        // bf16 376 and 375).
+        constexpr bool kRolled = CAP || D == 128;
+        uint32_t v[kRolled ? 1 : 4][32];
         float mx;
         // form 0: v f + n; 1, 2, 3: capped by 3 coefficients, by 5 or by tanh itself inside the exponent.  A capped row's
         // reference is its largest magnitude where that is little, else its capped maximum.
         int form = 0;
-        if constexpr (CAP) {
+        if constexpr (kRolled) {
           bool plain = !seen;
           if (seen) {
-            mx = columns_max<true>(s_addr);
-            plain = __any_sync(0xffffffffu, row_in && !(mx * scale2 < 0x1p27f));      // (beyond, x and m are shrunk below)
+            mx = columns_max<CAP>(s_addr);
+            if (CAP) plain = __any_sync(0xffffffffu, row_in && !(mx * scale2 < 0x1p27f));      // (beyond, x and m are shrunk below)
           }
           if (plain) {
             mx = -INFINITY;
@@ -639,8 +644,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t see = seen ? ~0u : column_mask(lo - u * kTile, pos - u * kTile, -1, 32 * g);
               tmem_ld32(s_addr + 32 * g, v[0]);
               tmem_ld_wait();
-              hide(v[0], see, 0u);
-              cap_columns(v[0], p.capf, row_in);
+              if (CAP) {
+                hide(v[0], see, 0u);
+                cap_columns(v[0], p.capf, row_in);
+              }
               hide(v[0], see, kMinusInf);
               float cm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -652,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st32(s_addr + 32 * g, v[0]);
             }
             tmem_st_wait();
-          } else {
+          } else if (CAP) {
             form = !__any_sync(0xffffffffu, row_in && !(mx <= p.capf.t3)) ? 1
                    : !__any_sync(0xffffffffu, row_in && !(mx <= p.capf.t5)) ? 2 : 3;
             if (__any_sync(0xffffffffu, row_in && !(mx * scale2 <= kLoose * 0.5f)))
@@ -769,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           mbar_arrive(&p_full[2 * w + half]);
         };
-        if constexpr (CAP) {
+        if constexpr (kRolled) {
           last_p_read();
           if (!ok) break;
           auto columns = [&](auto FORM) {
@@ -787,9 +794,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (g & 1) hand_in(g >> 1);
             }
           };
-          if (form == 1) columns(std::integral_constant<int, 1>{});
-          else if (form == 2) columns(std::integral_constant<int, 2>{});
-          else if (form == 3) columns(std::integral_constant<int, 3>{});
+          if (CAP && form == 1) columns(std::integral_constant<int, 1>{});
+          else if (CAP && form == 2) columns(std::integral_constant<int, 2>{});
+          else if (CAP && form == 3) columns(std::integral_constant<int, 3>{});
           else columns(std::integral_constant<int, 0>{});
         } else {
 #pragma unroll
@@ -871,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ unpack
-    setmaxnreg_dec<kRegAux>();
+    setmaxnreg_dec<kRegUnpack>();
     if constexpr (E4M3) {
       const int r = (warp & 3) * 32 + lane;
       uint32_t ring = 0;
