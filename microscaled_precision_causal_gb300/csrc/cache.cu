@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(256) cache_rows_kernel(int N, int T, int hq, i
 // instructions bound it (write of 16384 tokens, 16 heads, d 128: XX us, 70% of the issue slots).  Where the tokens live
 // it looks up once, a lane a token.
 constexpr int kWarps = 8;
-constexpr int kRowsPerWarp = 64;
+constexpr int kRowsPerWarp = 32;
 
 struct TokenGroup {
   int token, n;      // first token, tokens
