@@ -148,11 +148,11 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (threadIdx.x == 0) pv.prefix[0][items] = chunk_places;
   __syncthreads();
   // shares: the CTAs that get one, and the unit that each begins in
-  auto shares = [&](auto STEP, int64_t total, int64_t n_items, int least, int ctas, int c) {
+  auto shares = [&](auto STEP, int64_t total, int64_t n_items, int n, int c) {
     constexpr int kStep = decltype(STEP)::value;
     Shares sh;
     sh.total = total;
-    sh.n = (int)min((int64_t)ctas, (total + least - 1) / least);
+    sh.n = n;
     if (c == 0) {
       *reinterpret_cast<int64_t*>(pv.hdr + (kStep ? kCpStepPlaces : kCpChunkPlaces)) = total;
       pv.hdr[kStep ? kCpStepCtas : kCpChunkCtas] = sh.n;
@@ -170,11 +170,20 @@ __global__ void __launch_bounds__(kPlanThreads)
     u.begin += (int64_t)u.h * len;
     pv.first[kStep][c] = u;
   };
-  // A CTA takes some places at least: fewer would cost more in joining than they save.
-  if (threadIdx.x < kStepCtas)
-    shares(std::integral_constant<int, 1>{}, step_places * hkv, steps, 4 + kStepExtra, kStepCtas, threadIdx.x);
+  // A CTA takes some places at least: fewer would cost more in joining than they save.  Where steps are the lesser part
+  // beside chunks they get a CTA a SM on as many SMs as their part is (a place of theirs takes about a third of a
+  // chunk's), and the chunks the others: a chunk's CTA does not fit beside a step's, and waiting for it came last (XX us).
+  const int64_t steps_all = step_places * hkv, chunks_all = chunk_places * hkv;
+  int step_n = (int)min((int64_t)kStepCtas, (steps_all + 3 + kStepExtra) / (4 + kStepExtra));
+  int chunk_n = (int)min((int64_t)kChunkCtas, (chunks_all + 1 + kChunkExtra) / (2 + kChunkExtra));
+  if (steps_all > 0 && chunks_all > 0 && steps_all < 3 * chunks_all) {
+    const int part = (int)(kChunkCtas * steps_all / (steps_all + 3 * chunks_all)) + 1;
+    step_n = min(step_n, part);
+    chunk_n = min(chunk_n, kChunkCtas - step_n);
+  }
+  if (threadIdx.x < kStepCtas) shares(std::integral_constant<int, 1>{}, steps_all, steps, step_n, threadIdx.x);
   else if (threadIdx.x < kStepCtas + kChunkCtas)
-    shares(std::integral_constant<int, 0>{}, chunk_places * hkv, items, 2 + kChunkExtra, kChunkCtas, threadIdx.x - kStepCtas);
+    shares(std::integral_constant<int, 0>{}, chunks_all, items, chunk_n, threadIdx.x - kStepCtas);
 }
 
 // The sequence and the position of each row.

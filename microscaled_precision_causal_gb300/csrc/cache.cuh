@@ -17,8 +17,8 @@ constexpr int kStepTile = 64;      // keys a tile of a step
 __host__ __device__ inline int step_rows(int group, int64_t max_chunk) {
   return max_chunk * group > kStepTiles * kStepRows && group <= 8 ? 8 : kStepTiles * kStepRows;
 }
-// What a unit costs besides its key tiles, in key tiles, when the work is dealt out: its queries, its end.
-constexpr int kStepExtra = 3, kChunkExtra = 1;
+// What a unit costs besides its key tiles, in key tiles, when the work is dealt out: its queries, its start, its end.
+constexpr int kStepExtra = 3, kChunkExtra = 3;
 
 // ---------------------------------------------------------------- plan
 enum CachePlanWord : int {

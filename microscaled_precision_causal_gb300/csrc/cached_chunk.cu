@@ -141,7 +141,8 @@ struct ChunkSmem {
   static constexpr int kCodes = kKV + kSlots * kTileBytes;
   static constexpr int kScales = kCodes + kRaw * kRawBytes; // [kRaw][128]
   static constexpr int kUnit = kScales + kRaw * kTile;
-  static constexpr int kBar = kUnit + kUnits * (int)sizeof(Piece);
+  static constexpr int kSplits = kUnit + kUnits * (int)sizeof(Piece);   // the share's split units, by slot
+  static constexpr int kBar = kSplits + 2 * (int)sizeof(Piece);
   static constexpr int kBytes = kBar + 512;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -198,10 +199,10 @@ __device__ __forceinline__ void unpack_row(uint32_t raw, uint32_t tile, int r, u
 }
 
 // The rows of a warp of row tile w from all pieces: references and sums with a lane a row, then values with eight
-// lanes a row, so that four rows' loads are in flight.
+// lanes a row, of some rows and four pieces at a time: it is a matter of loads in flight.
 template <int D>
 __device__ __forceinline__ void join_rows(const CachedParams& p, const Piece& U, int w, int quarter, int lane) {
-  constexpr int kPer = D / 8;
+  constexpr int kPer = D / 32, kGroups = D == 64 ? 4 : 2, kPieces = 4;       // 16-byte words a lane, groups of four rows
   const int base = w * kTile + quarter * 32, sub = lane >> 3, seg = lane & 7, group = p.hq / p.c.hkv;
   const int rows = min(32, U.rows - base);
   auto piece = [&](int i) { return cached_part<false, D>(p, U.owner + i, i == 0 ? 1 : 0); };
@@ -219,37 +220,55 @@ __device__ __forceinline__ void join_rows(const CachedParams& p, const Piece& U,
   }
   const float inv = 1.f / l;
 #pragma unroll 1
-  for (int r0 = 0; r0 < rows; r0 += 4) {
-    const int r = min(r0 + sub, rows - 1);
-    const float nr = __shfl_sync(0xffffffffu, neg, r), ir = __shfl_sync(0xffffffffu, inv, r);
-    float o[kPer] = {};
-#pragma unroll 3
-    for (int i = 0; i < U.pieces; ++i) {
-      const float* src = piece(i);
-      const float m = __ldcg(src + kChunkRows * D + base + r);
-      float4 y[kPer / 4];
+  for (int r0 = 0; r0 < rows; r0 += 4 * kGroups) {
+    float4 o[kGroups][kPer] = {};
+#pragma unroll 1
+    for (int b = 0; b < U.pieces; b += kPieces) {
+      float4 y[kPieces][kGroups][kPer];
+      float m[kPieces];
 #pragma unroll
-      for (int k = 0; k < kPer / 4; ++k) y[k] = __ldcg(reinterpret_cast<const float4*>(src + (size_t)(base + r) * D + k * 32 + 4 * seg));
-      const float wt = fast_exp2(m + nr) * ir;
+      for (int i = 0; i < kPieces; ++i) {
+        const float* src = piece(min(b + i, U.pieces - 1));
+        m[i] = b + i < U.pieces ? __ldcg(src + kChunkRows * D + mine) : -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kPer / 4; ++k) {
-        o[4 * k] = fmaf(wt, y[k].x, o[4 * k]);
-        o[4 * k + 1] = fmaf(wt, y[k].y, o[4 * k + 1]);
-        o[4 * k + 2] = fmaf(wt, y[k].z, o[4 * k + 2]);
-        o[4 * k + 3] = fmaf(wt, y[k].w, o[4 * k + 3]);
+        for (int q = 0; q < kGroups; ++q) {
+          const int r = min(r0 + 4 * q + sub, rows - 1);
+#pragma unroll
+          for (int k = 0; k < kPer; ++k)
+            y[i][q][k] = b + i < U.pieces ? __ldcg(reinterpret_cast<const float4*>(src + (size_t)(base + r) * D + k * 32 + 4 * seg))
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const float wm = b + i < U.pieces ? fast_exp2(m[i] + neg) * inv : 0.f;
+#pragma unroll
+        for (int q = 0; q < kGroups; ++q) {
+          const float wt = __shfl_sync(0xffffffffu, wm, min(r0 + 4 * q + sub, rows - 1));
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            o[q][k].x = fmaf(wt, y[i][q][k].x, o[q][k].x);
+            o[q][k].y = fmaf(wt, y[i][q][k].y, o[q][k].y);
+            o[q][k].z = fmaf(wt, y[i][q][k].z, o[q][k].z);
+            o[q][k].w = fmaf(wt, y[i][q][k].w, o[q][k].w);
+          }
+        }
       }
     }
-    if (r0 + sub < rows) {
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q) {
+      const int r = r0 + 4 * q + sub;
+      if (r >= rows) continue;
       const int x = U.row + base + r, h = U.h * group + x % group;
       __nv_bfloat16* dst = p.out + (((int64_t)U.start + x / group) * p.hq + h) * D + 4 * seg;
 #pragma unroll
-      for (int k = 0; k < kPer / 4; ++k) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(o[4 * k], o[4 * k + 1]), b = __floats2bfloat162_rn(o[4 * k + 2], o[4 * k + 3]);
+      for (int k = 0; k < kPer; ++k) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(o[q][k].x, o[q][k].y), b = __floats2bfloat162_rn(o[q][k].z, o[q][k].w);
         *reinterpret_cast<uint2*>(dst + 32 * k) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
       }
     }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 template <int D, bool E4M3, bool CAP>
@@ -327,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&raw_full[i], 1 + kScaleCopies);
       mbar_init(&raw_empty[i], 4);
     }
+    for (int i = 0; i < 2; ++i) reinterpret_cast<Piece*>(smem + L::kSplits)[i].tiles = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
@@ -432,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) {
           *reinterpret_cast<Piece*>(units + (n % kUnits) * sizeof(Piece)) = U;
+          if (U.slot >= 0 && U.tiles) *reinterpret_cast<Piece*>(smem + L::kSplits + U.slot * sizeof(Piece)) = U;
           mbar_arrive(&unit_full[n % kUnits]);
         }
         __syncwarp();
@@ -592,6 +613,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale2 = p.scale2;
     const int group = p.hq / p.c.hkv;
     const bool al32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;       // (whole sectors where they can be)
+    // The piece that the share begins with is counted some key tiles into the next unit: right where it ends, the wait for
+    // its stores kept that unit waiting (3 us).  pending: key tiles until then, -1: no such piece so far.
+    int pending = -1;
+    bool join_first = false;
+    auto count_piece = [&](const Piece& U) {
+      const int last = lane == 0 && cached_last(pv.done + kStepCtas + 8 * U.owner + 4 * w + quarter, U.pieces);
+      return __shfl_sync(0xffffffffu, last, 0) != 0;
+    };
     uint32_t ring = 0, ns = 0, nu = 0;
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -811,6 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
+        if (pending > 0 && --pending == 0) join_first = count_piece(*reinterpret_cast<const Piece*>(smem + L::kSplits));
         ++ns;
         first = false;
       }
@@ -869,11 +899,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[(size_t)kChunkRows * (D + 1) + rr] = l;
         }
       }
-      if (U.slot >= 0) {           // a warp's rows stay a warp's: the last of their pieces to be finished joins them
-        __syncwarp();
-        const int rows = U.rows - (w * kTile + quarter * 32);
-        const int last = lane == 0 && rows > 0 && cached_last(pv.done + kStepCtas + 8 * U.owner + 4 * w + quarter, U.pieces);
-        if (__shfl_sync(0xffffffffu, last, 0)) join_rows<D>(p, U, w, quarter, lane);
+      if (U.slot == 0 && U.rows > w * kTile + quarter * 32) pending = 3;
+    }
+    // Split units: a warp's rows stay a warp's, and the last of their pieces to be finished joins them, at its share's end.
+    if (ok) {
+      __syncwarp();
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const Piece U = *reinterpret_cast<const Piece*>(smem + L::kSplits + i * sizeof(Piece));
+        const bool counted = i == 0 && pending == 0;
+        if (U.tiles == 0 || U.rows <= w * kTile + quarter * 32) continue;
+        if (!counted) join_first = count_piece(U);
+        if (join_first) join_rows<D>(p, U, w, quarter, lane);
       }
     }
   } else {

@@ -45,7 +45,7 @@ struct alignas(16) StepPiece {
   int t0, t1, tiles, tile;        // key tiles [t0, t1) of the unit's; its first tile's number in the sequence.  t1 0: no more
   int h, row, rows, start;        // first row, rows; first token of the sequence
   int pos0, keys, lo;             // its position
-  int owner, pieces, pad[3];      // of a split unit: the CTA that has its beginning, the CTAs that have pieces
+  int owner, pieces, last, pad[2];      // of a split unit: the CTA that has its beginning, the CTAs that have pieces
 };
 static_assert(sizeof(StepPiece) == 64, "");
 
@@ -112,8 +112,8 @@ struct StepSmem {
   static constexpr int kStat = kRed + kComputeWarps * kRows * D * 4;          // [4 warps][m, l][kRows]
   static constexpr int kQ = kStat + kComputeWarps * 2 * kRows * 4;            // [2 units in turn][kRows] queries
   static constexpr int kUnit = kQ + kUnits * kRows * D * 2;
-  static constexpr int kFlag = kUnit + kUnits * 64;
-  static constexpr int kBar = kFlag + 16;
+  static constexpr int kSplits = kUnit + kUnits * 64;        // the share's split units, by slot
+  static constexpr int kBar = kSplits + 2 * 64;
   static constexpr int kBytes = kBar + (2 * kStages + 2 * kUnits) * 8;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(&unit_full[i], 33);            // the producer's lanes as their copies land, and the description
       mbar_init(&unit_done[i], kComputeWarps);
     }
+    for (int i = 0; i < 2; ++i) reinterpret_cast<StepPiece*>(smem + L::kSplits)[i].tiles = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const int2 c = cached_owners<true>(u, sh);
           x.owner = c.x;
           x.pieces = c.y;
+          reinterpret_cast<StepPiece*>(smem + L::kSplits)[t0 == 0 ? 1 : 0] = x;
         }
         *reinterpret_cast<StepPiece*>(smem + L::kUnit + (n % kUnits) * sizeof(StepPiece)) = x;
       }
@@ -341,10 +343,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     at_v[k] = L::kTileBytes + key0 * L::kBoxBytes + swz_offset(2 * q + k, kWords >= 4 ? 16 * g : 8 * g, L::kBoxBytes);
+  StepPiece* splits = reinterpret_cast<StepPiece*>(smem + L::kSplits);
+  int pending = -1;
   for (int n = 0; ok; ++n) {
     // (the warps meet here too: the last unit's sums have been read, and where a wait ran out all of them leave)
     ok = named_bar_and(1, kComputeWarps * 32, warp_wait(&unit_full[n % kUnits], (n / kUnits) & 1, status));
     if (!ok) break;
+    // a split unit's piece is counted here and not where it ended: by now its stores have landed
+    if (pending >= 0 && threadIdx.x == 0) splits[pending].last = cached_last(pv.done + splits[pending].owner, splits[pending].pieces);
+    pending = -1;
     const StepPiece u = *reinterpret_cast<const StepPiece*>(smem + L::kUnit + (n % kUnits) * sizeof(StepPiece));
     if (u.t1 == 0) break;
     // queries as the products' second operand: row 8 t + g, four head dimensions a step of 16.  Scores and
@@ -732,6 +739,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     named_bar_sync(1, kComputeWarps * 32);
     const bool whole = u.t0 == 0 && u.t1 == u.tiles;
+    if (!whole) pending = u.t0 == 0 ? 1 : 0;
     float* part = cached_part<true, D>(p, blockIdx.x, u.t0 == 0 ? 1 : 0);
     constexpr int kQuads = D / 4;
     for (int y = threadIdx.x; y < u.rows * kQuads; y += kComputeWarps * 32) {
@@ -762,14 +770,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
-    if (!whole) {                // the last of the unit's pieces to be finished joins them
-      int* flag = reinterpret_cast<int*>(smem + L::kFlag);
-      named_bar_sync(1, kComputeWarps * 32);
-      if (threadIdx.x == 0) *flag = cached_last(pv.done + u.owner, u.pieces);
-      named_bar_sync(1, kComputeWarps * 32);
-      if (*flag)
-        for (int r = warp; r < u.rows; r += kComputeWarps) join_row<D>(p, u, r, lane);
-    }
+  }
+  // Split units: the last of their pieces to be finished joins them, at its share's end.
+  if (!ok) return;
+  named_bar_sync(1, kComputeWarps * 32);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const StepPiece u = splits[i];
+    if (u.tiles && u.last)
+      for (int r = warp; r < u.rows; r += kComputeWarps) join_row<D>(p, u, r, lane);
   }
 }
 
