@@ -728,6 +728,8 @@ class FlamiaCachedAttention:
         self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
         # a step's calls are many and small: what does not change is worked out once
         self._lib, self._plan_ptr, self._bf16, self._i32 = lib(), self.plan.data_ptr(), torch.bfloat16, torch.int32
+        self._index = dev.index if dev.type == "cuda" else None
+        self._device_now, self._stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         self._kind = (page_size, hkv, head_dim, dev)
         self._q_shape, self._kv_shape = (total_tokens, hq, head_dim), (total_tokens, hkv, head_dim)
         self._table_shape = (num_seqs, self.max_pages)
@@ -750,37 +752,40 @@ class FlamiaCachedAttention:
                                                       self.max_pages * self.page_size, self.window, self.plan, stm), stream)
         self._planned = True
 
+    def _call(self, what, f, stream, *args):
+        """f(*args, stream handle) with the object's device current, on `stream` or its current stream."""
+        if stream is None and self._index is not None and self._device_now() == self._index:
+            rc = f(*args, self._stream_now(self._index))
+        else:
+            rc = self._run(lambda stm: f(*args, stm), stream)
+        if rc:
+            _check(rc, what)
+
     def write(self, cache: FlamiaPagedCache, k, v, page_table, stream=None):
         """The new tokens' keys and values into the cache."""
         self._places(cache, page_table)
         self._want("k", k, self._kv_shape, self._bf16)
         self._want("v", v, self._kv_shape, self._bf16)
-        rc = self._run(lambda stm: self._lib.flamia_cache_write(
-            cache.ref, page_table.data_ptr(), self.max_pages, self.N, self.T, self._plan_ptr, k.data_ptr(), v.data_ptr(), stm), stream)
-        if rc:
-            _check(rc, "flamia_cache_write")
+        self._call("flamia_cache_write", self._lib.flamia_cache_write, stream, cache.ref, page_table.data_ptr(), self.max_pages,
+                   self.N, self.T, self._plan_ptr, k.data_ptr(), v.data_ptr())
 
     def read(self, cache: FlamiaPagedCache, page_table, k, v, stream=None):
         """The new tokens' keys and values from the cache into k and v, which are returned."""
         self._places(cache, page_table)
         self._want("k", k, self._kv_shape, self._bf16)
         self._want("v", v, self._kv_shape, self._bf16)
-        rc = self._run(lambda stm: self._lib.flamia_cache_read(
-            cache.ref, page_table.data_ptr(), self.max_pages, self.N, self.T, self._plan_ptr, k.data_ptr(), v.data_ptr(), stm), stream)
-        if rc:
-            _check(rc, "flamia_cache_read")
+        self._call("flamia_cache_read", self._lib.flamia_cache_read, stream, cache.ref, page_table.data_ptr(), self.max_pages,
+                   self.N, self.T, self._plan_ptr, k.data_ptr(), v.data_ptr())
         return k, v
 
     def forward(self, cache: FlamiaPagedCache, q, page_table, softmax_scale: float = 0.0, stream=None):
         """(out bf16 [T, hq, d], lse fp32 [hq, T]) of the new tokens, whose keys and values have been written."""
         self._places(cache, page_table)
         self._want("q", q, self._q_shape, self._bf16)
-        out, lse, ws = self.out, self.lse, self.workspace
-        rc = self._run(lambda stm: self._lib.flamia_cached_fwd(
-            q.data_ptr(), cache.ref, page_table.data_ptr(), self.max_pages, self.N, self.T, self.hq, self.max_chunk, self.window,
-            self.softcap, softmax_scale, self._plan_ptr, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), self._ws_bytes, stm), stream)
-        if rc:
-            _check(rc, "flamia_cached_fwd")
+        out, lse = self.out, self.lse
+        self._call("flamia_cached_fwd", self._lib.flamia_cached_fwd, stream, q.data_ptr(), cache.ref, page_table.data_ptr(),
+                   self.max_pages, self.N, self.T, self.hq, self.max_chunk, self.window, self.softcap, softmax_scale,
+                   self._plan_ptr, out.data_ptr(), lse.data_ptr(), self.workspace.data_ptr(), self._ws_bytes)
         return out, lse
 
     def device_status(self, stream=None) -> int:

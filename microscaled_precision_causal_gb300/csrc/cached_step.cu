@@ -132,51 +132,79 @@ __device__ __forceinline__ void clear_rows(const CachedParams& p, int D, int val
   }
 }
 
-// Row r of a split unit, whose pieces may be hundreds: by a warp, a lane a piece for their weights.
-template <int D>
-__device__ __forceinline__ void join_row(const CachedParams& p, const StepPiece& u, int r, int lane) {
-  constexpr int kPer = D / 32;
+// A split unit's rows warp, warp + 4, ... at once (so that their loads fly together); its pieces may be hundreds: a lane a
+// piece for their weights.
+template <int D, int ROWS>
+__device__ __forceinline__ void join_rows(const CachedParams& p, const StepPiece& u, int warp, int lane) {
+  constexpr int kPer = D / 32, kMine = (ROWS + kComputeWarps - 1) / kComputeWarps;
   auto piece = [&](int i) { return cached_part<true, D>(p, u.owner + i, i == 0 ? 1 : 0); };
-  float top = -INFINITY, l = 0.f;
-  for (int i = lane; i < u.pieces; i += 32) top = fmaxf(top, __ldcg(piece(i) + kStepRows * D + r));
+  int row[kMine];
+  float neg[kMine], l[kMine];
 #pragma unroll
-  for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-  const float neg = top == -INFINITY ? 0.f : -top;
-  float o[kPer] = {};
+  for (int k = 0; k < kMine; ++k) {
+    row[k] = min(warp + kComputeWarps * k, u.rows - 1);
+    neg[k] = -INFINITY;
+    l[k] = 0.f;
+  }
+  for (int i = lane; i < u.pieces; i += 32)
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) neg[k] = fmaxf(neg[k], __ldcg(piece(i) + kStepRows * D + row[k]));
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+#pragma unroll
+    for (int w = 16; w; w >>= 1) neg[k] = fmaxf(neg[k], __shfl_xor_sync(0xffffffffu, neg[k], w));
+  }
+  float top[kMine];
+  float o[kMine][kPer] = {};
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) {
+    top[k] = neg[k];
+    neg[k] = top[k] == -INFINITY ? 0.f : -top[k];
+  }
   for (int b = 0; b < u.pieces; b += 32) {
     const int i = b + lane;
-    float wt = 0.f;
-    if (i < u.pieces) {
-      wt = fast_exp2(__ldcg(piece(i) + kStepRows * D + r) + neg);
-      l += wt * __ldcg(piece(i) + kStepRows * (D + 1) + r);
-    }
+    float wt[kMine] = {};
+    if (i < u.pieces)
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        wt[k] = fast_exp2(__ldcg(piece(i) + kStepRows * D + row[k]) + neg[k]);
+        l[k] += wt[k] * __ldcg(piece(i) + kStepRows * (D + 1) + row[k]);
+      }
     const int here = min(32, u.pieces - b);
-#pragma unroll 8
+#pragma unroll 4
     for (int j = 0; j < here; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, wt, j);
-      const float* src = piece(b + j) + r * D + lane * kPer;
-      if constexpr (kPer == 2) {
-        const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
-        o[0] = fmaf(wj, y.x, o[0]);
-        o[1] = fmaf(wj, y.y, o[1]);
-      } else {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
-        o[0] = fmaf(wj, y.x, o[0]);
-        o[1] = fmaf(wj, y.y, o[1]);
-        o[2] = fmaf(wj, y.z, o[2]);
-        o[3] = fmaf(wj, y.w, o[3]);
+      const float* src = piece(b + j) + lane * kPer;
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        const float wj = __shfl_sync(0xffffffffu, wt[k], j);
+        if constexpr (kPer == 2) {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(src + row[k] * D));
+          o[k][0] = fmaf(wj, y.x, o[k][0]);
+          o[k][1] = fmaf(wj, y.y, o[k][1]);
+        } else {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(src + row[k] * D));
+          o[k][0] = fmaf(wj, y.x, o[k][0]);
+          o[k][1] = fmaf(wj, y.y, o[k][1]);
+          o[k][2] = fmaf(wj, y.z, o[k][2]);
+          o[k][3] = fmaf(wj, y.w, o[k][3]);
+        }
       }
     }
   }
+  const int group = p.hq / p.c.hkv;
 #pragma unroll
-  for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-  const int group = p.hq / p.c.hkv, h = u.h * group + (u.row + r) % group;
-  const int64_t tok = u.start + (u.row + r) / group;
-  const float inv = 1.f / l;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (tok * p.hq + h) * D + lane * kPer);
+  for (int k = 0; k < kMine; ++k) {
 #pragma unroll
-  for (int j = 0; j < kPer / 2; ++j) dst[j] = pack2<false>(o[2 * j] * inv, o[2 * j + 1] * inv);
-  if (lane == 0) p.lse[(int64_t)h * p.c.T + tok] = (top + log2f(l)) * kLn2;
+    for (int w = 16; w; w >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], w);
+    if (warp + kComputeWarps * k >= u.rows) continue;
+    const int h = u.h * group + (u.row + row[k]) % group;
+    const int64_t tok = u.start + (u.row + row[k]) / group;
+    const float inv = 1.f / l[k];
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (tok * p.hq + h) * D + lane * kPer);
+#pragma unroll
+    for (int j = 0; j < kPer / 2; ++j) dst[j] = pack2<false>(o[k][2 * j] * inv, o[k][2 * j + 1] * inv);
+    if (lane == 0) p.lse[(int64_t)h * p.c.T + tok] = (top[k] + log2f(l[k])) * kLn2;
+  }
 }
 
 // NT: tiles of 8 query rows.
@@ -777,8 +805,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
     const StepPiece u = splits[i];
-    if (u.tiles && u.last)
-      for (int r = warp; r < u.rows; r += kComputeWarps) join_row<D>(p, u, r, lane);
+    if (u.tiles && u.last) join_rows<D, L::kRows>(p, u, warp, lane);
   }
 }
 
