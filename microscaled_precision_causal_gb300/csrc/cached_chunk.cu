@@ -50,7 +50,8 @@ struct alignas(16) Piece {
   int h, row, rows, ntq;
   int start, pos0, keys, lo;       // first token of the sequence, and its position; keys; first key seen by any row
   int seq, slot;                   // slot of the workspace, or -1: a whole unit
-  int owner, pieces, pad[2];       // of a split unit: the CTA that has its beginning, the CTAs that have pieces
+  int owner, pieces;               // of a split unit: the CTA that has its beginning, the CTAs that have pieces
+  uint8_t ended[8];                // whether this CTA's piece was finished last, by the rows' warps
 };
 static_assert(sizeof(Piece) == 64, "read as four 16-byte words");
 constexpr int kUnits = 4;
@@ -614,12 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = p.hq / p.c.hkv;
     const bool al32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;       // (whole sectors where they can be)
     // The piece that the share begins with is counted some key tiles into the next unit: right where it ends, the wait for
-    // its stores kept that unit waiting (3 us).  pending: key tiles until then, -1: no such piece so far.
-    int pending = -1;
-    bool join_first = false;
-    auto count_piece = [&](const Piece& U) {
-      const int last = lane == 0 && cached_last(pv.done + kStepCtas + 8 * U.owner + 4 * w + quarter, U.pieces);
-      return __shfl_sync(0xffffffffu, last, 0) != 0;
+    // its stores kept that unit waiting (3 us).  count_at: when ns will say so, 0: no such piece so far.
+    uint32_t count_at = 0;
+    auto count_piece = [&](int slot) {       // (what it says is kept in shared memory until the share's end)
+      if (lane == 0) {
+        Piece& U = reinterpret_cast<Piece*>(smem + L::kSplits)[slot];
+        U.ended[4 * w + quarter] = cached_last(pv.done + kStepCtas + 8 * U.owner + 4 * w + quarter, U.pieces);
+      }
+      __syncwarp();
     };
     uint32_t ring = 0, ns = 0, nu = 0;
     bool ok = true;
@@ -667,25 +670,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (CAP) plain = __any_sync(0xffffffffu, row_in && !(mx * scale2 < 0x1p27f));      // (beyond, x and m are shrunk below)
           }
           if (plain) {
+            // (most of a masked tile's columns are seen by all of a warp's rows)
             mx = -INFINITY;
 #pragma unroll 1
             for (int g = 0; g < 4; ++g) {
               const uint32_t see = seen ? ~0u : column_mask(lo - u * kTile, pos - u * kTile, -1, 32 * g);
-              tmem_ld32(s_addr + 32 * g, v[0]);
+              const bool all = __all_sync(0xffffffffu, see == ~0u);
+              float cm;
+              tmem_ld32_max(s_addr + 32 * g, v[0], cm);
               tmem_ld_wait();
               if (CAP) {
-                hide(v[0], see, 0u);
+                if (!all) hide(v[0], see, 0u);
                 cap_columns(v[0], p.capf, row_in);
               }
-              hide(v[0], see, kMinusInf);
-              float cm[2] = {-INFINITY, -INFINITY};
+              if (!all) hide(v[0], see, kMinusInf);
+              if (CAP || !all) {
+                float c2[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-              for (int j = 0; j < 32; j += 4)
+                for (int j = 0; j < 32; j += 4)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  cm[i] = fmax3(cm[i], __uint_as_float(v[0][j + 2 * i]), __uint_as_float(v[0][j + 2 * i + 1]));
-              mx = fmax3(mx, cm[0], cm[1]);
-              tmem_st32(s_addr + 32 * g, v[0]);
+                  for (int i = 0; i < 2; ++i)
+                    c2[i] = fmax3(c2[i], __uint_as_float(v[0][j + 2 * i]), __uint_as_float(v[0][j + 2 * i + 1]));
+                cm = fmaxf(c2[0], c2[1]);
+                tmem_st32(s_addr + 32 * g, v[0]);
+              }
+              mx = fmaxf(mx, cm);
             }
             tmem_st_wait();
           } else if (CAP) {
@@ -840,8 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        if (pending > 0 && --pending == 0) join_first = count_piece(*reinterpret_cast<const Piece*>(smem + L::kSplits));
-        ++ns;
+        if (++ns == count_at) count_piece(0);
         first = false;
       }
       ring += 2 * nk;
@@ -899,18 +907,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           part[(size_t)kChunkRows * (D + 1) + rr] = l;
         }
       }
-      if (U.slot == 0 && U.rows > w * kTile + quarter * 32) pending = 3;
+      if (U.slot == 0 && U.rows > w * kTile + quarter * 32) count_at = ns + 3;
     }
     // Split units: a warp's rows stay a warp's, and the last of their pieces to be finished joins them, at its share's end.
     if (ok) {
       __syncwarp();
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
-        const Piece U = *reinterpret_cast<const Piece*>(smem + L::kSplits + i * sizeof(Piece));
-        const bool counted = i == 0 && pending == 0;
+        const Piece& U = reinterpret_cast<const Piece*>(smem + L::kSplits)[i];
         if (U.tiles == 0 || U.rows <= w * kTile + quarter * 32) continue;
-        if (!counted) join_first = count_piece(U);
-        if (join_first) join_rows<D>(p, U, w, quarter, lane);
+        if (i == 1 || ns < count_at) count_piece(i);
+        if (U.ended[4 * w + quarter]) join_rows<D>(p, U, w, quarter, lane);
       }
     }
   } else {
@@ -984,8 +991,11 @@ cudaError_t launch(const CachedParams& p, bool tail, cudaStream_t stream) {
 
 template <int D>
 cudaError_t launch_d(bool e4m3, CachedParams p, bool tail, cudaStream_t s) {
-  p.scale2 = (float)((double)p.scale2 * mma_gain(D));
-  p.capf = cap_form(p.scale * mma_gain(D), (double)p.cap);
+  // (products of four-bit keys lose nothing that shows as the tensor core adds them up: with the factor LSE came out
+  // 4e-6 too large on 2048 behind 14336, scores of some tens)
+  const double gain = e4m3 ? 1.0 : mma_gain(D);
+  p.scale2 = (float)(p.scale * gain * 1.4426950408889634);
+  p.capf = cap_form(p.scale * gain, (double)p.cap);
   if (e4m3) return p.cap > 0.f ? launch<D, true, true>(p, tail, s) : launch<D, true, false>(p, tail, s);
   return p.cap > 0.f ? launch<D, false, true>(p, tail, s) : launch<D, false, false>(p, tail, s);
 }
