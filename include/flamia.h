@@ -485,15 +485,23 @@ int flamia_relbias_reduce(const float* drel_bias, int rel_max, int num_buckets, 
  * write nothing to the cache, read zeros, and give O 0 and LSE +inf.  A page
  * number outside the cache sets FLAMIA_DEV_BAD_PAGE: such a token is not
  * written and reads as zeros, and the attention rows of its sequence are
- * unspecified; nothing outside the pools is touched.  Entries behind a
- * sequence's last position are not looked at, and what a page holds behind it
- * has no effect.  flamia_get_device_status reads the plan's status word.
+ * unspecified; nothing outside the pools is touched.  Table entries behind a
+ * sequence's last position are not looked at, nor are those of pages that lie
+ * wholly before what a window leaves visible to the attention's rows; what a
+ * page holds at positions that no row sees for either reason has no effect.
+ * flamia_get_device_status reads the plan's status word.
+ *
+ * The attention keeps count of split work in the plan: of its calls on one plan
+ * no two may overlap on the GPU, and after FLAMIA_DEV_TIMEOUT the plan has to be
+ * built again.  Writes and reads may overlap on one plan.
  *
  * hq query heads share hkv heads as everywhere; max_chunk: no sequence brings
- * more new tokens than that (at least 1); max_keys: max_pages * page_size of the
- * call's table; window_left: as in flamia_options (the right bound is 0).  The
- * attention's calls take the plan's own hq, max_chunk and window_left.
- * page_size: 16, 32, 64 or 128; max_pages * page_size <= 2^30. */
+ * more new tokens than that (at least 1; calls are fastest where it is the
+ * largest that comes); max_keys: max_pages * page_size of the call's table;
+ * window_left: as in flamia_options (the right bound is 0).  The attention's
+ * calls take the plan's own hq, max_chunk and window_left; a plan of other sizes
+ * sets FLAMIA_DEV_PLAN_MISMATCH and counts as bad.  page_size: 16, 32, 64 or 128;
+ * max_pages * page_size <= 2^30. */
 #define FLAMIA_CACHE_BF16 0
 #define FLAMIA_CACHE_E4M3 1
 typedef struct flamia_kv_cache {
@@ -532,9 +540,12 @@ int flamia_cache_read(const flamia_kv_cache* cache, const int32_t* page_table, i
  * Rows behind the last sequence: O 0, LSE +inf.  softcap and softmax_scale as in
  * flamia_score_options and flamia_scored_fwd.  workspace: device scratch of
  * flamia_cached_fwd_workspace_bytes() bytes, 256-byte aligned, its contents
- * unspecified before and after; calls that overlap on the GPU need one each.
- * Equal inputs give equal bits.  A non-finite key or value shows in rows of its
- * own sequence only, hidden or not. */
+ * unspecified before and after; calls that overlap on the GPU need one each (and a
+ * plan each).  Equal calls give equal bits; how a sequence's keys are split over
+ * the GPU, and with that the last bits of its rows, depends on the call's other
+ * sequences.  A non-finite key or value of a visible or hidden position of the
+ * sequence shows in rows of its own sequence only.  Scores have to stay finite in
+ * fp32. */
 size_t flamia_cached_fwd_workspace_bytes(int hq, int hkv, int head_dim, int max_chunk);
 int flamia_cached_fwd(const void* q_bf16, const flamia_kv_cache* cache, const int32_t* page_table, int max_pages,
                       int num_seqs, int64_t total_tokens, int hq, int max_chunk, int window_left, float softcap,

@@ -691,8 +691,9 @@ class FlamiaCachedAttention:
             att.write(layer.cache, k, v, page_table)
             out, lse = att.forward(layer.cache, q, page_table)
 
-    window: keys up to so many positions before a token's own are seen (-1: all);
-    softcap as in FlamiaScoredAttention.  read(cache, page_table, k, v) puts the
+    window: keys up to so many positions before a token's own are seen (-1: all;
+    pages wholly before that may be given back); softcap as in
+    FlamiaScoredAttention.  read(cache, page_table, k, v) puts the
     step's tokens back into k and v (with kv_lens the chunks themselves: whole
     sequences).
 
@@ -703,8 +704,8 @@ class FlamiaCachedAttention:
     the object's own out and lse, overwritten by its next call.  Nothing is
     allocated per call, so calls can be captured into a CUDA graph: a replay reads
     what the tensors hold by then.  Calls run on `stream`, by default the object's
-    device's current stream; calls of one object share its outputs and workspace,
-    so calls on two streams have to be ordered by the caller."""
+    device's current stream; calls of one object share its plan, outputs and
+    workspace, so calls on two streams have to be ordered by the caller."""
 
     def __init__(self, total_tokens: int, num_seqs: int, hq: int, hkv: int, head_dim: int, max_chunk: int,
                  max_pages: int, page_size: int, device="cuda", window: int = -1, softcap: float = 0.0):

@@ -10,7 +10,7 @@
 // The products run as 16 x 8 x 16 MMAs from registers, keys (then head dimensions) as the 16 and query rows as the 8:
 // what is to be fast here is the stream, not the products, and a step's rows rarely fill more (tcgen05 would
 // want 64 at least and the codes unpacked into shared memory; rows as the 16 cost twice the softmax and twice
-// the accumulators: 98 instead of XX us on two sequences of 131972).  Which of the head dimensions a lane's operand
+// the accumulators: 98 instead of 91 us on two sequences of 131972).  Which of the head dimensions a lane's operand
 // words stand for is free as long as both operands agree, so a lane takes whole 16-byte words of a key's row,
 // and for V of one head-dim run in four keys' rows, whose bytes are paired by permutes; with the copies' swizzle
 // both are free of bank conflicts.  The weights change from scores' to operands' places by a transpose
@@ -106,7 +106,10 @@ struct StepSmem {
   static constexpr int kTileBytes = kStepTile * kRowBytes;                    // of K, or of V
   static constexpr int kScales = 2 * kTileBytes;                              // in a stage: K's and V's scale bytes
   static constexpr int kStage = kScales + (E4M3 ? 1024 : 0);           // (stages stay on 1024 bytes)
+  // (an even number: a pair of warps takes every other tile, so that a stage is always the same pair's, which sees each
+  // phase of its barrier; with an odd number a pair could not tell a phase from the last but one)
   static constexpr int kStages = E4M3 ? (D == 128 ? 4 : 6) : (D == 128 ? 2 : 4);
+  static_assert(kStages % 2 == 0, "see above");
   static constexpr int kRows = 8 * NT;
   static constexpr int kRed = kStages * kStage;                               // [4 warps][kRows][D] floats
   static constexpr int kStat = kRed + kComputeWarps * kRows * D * 4;          // [4 warps][m, l][kRows]
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (u.t1 == 0) break;
     // queries as the products' second operand: row 8 t + g, four head dimensions a step of 16.  Scores and
     // weights then are of rows 8 t + 2 q and + 1.  Two row tiles' operands are kept in shared memory, in the
-    // queries' place, a 16-byte word a lane and step: in registers they spill (179 instead of XX us on two
+    // queries' place, a 16-byte word a lane and step: in registers they spill (179 instead of 111 us on two
     // sequences of 131972, 16 rows)
     constexpr bool kShared = NT == 2;
     uint8_t* frag = smem + L::kQ + (n % kUnits) * L::kRows * D * 2 + lane * 16;

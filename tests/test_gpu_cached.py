@@ -272,6 +272,51 @@ def test_long_contexts_are_split_and_joined(F, shape, d):
     Batch(F, *shape, 4, 1, d, "e4m3", 64, seed=9).check()
 
 
+@BOTH
+@DIMS
+@pytest.mark.parametrize("hq,hkv,chunks", [(32, 1, [1, 1, 0, 1]), (24, 1, [1, 1]), (4, 1, [8, 5, 7]), (12, 4, [10, 9, 1]), (40, 1, [1, 1, 2]),
+                                           (160, 1, [1, 2, 0])])
+def test_rows_around_the_tiles(F, hq, hkv, chunks, d, fmt):
+    """One and two row tiles of a step, the least chunks, groups above both tiles' rows; many pieces to a unit."""
+    for before in (7000, 90):
+        Batch(F, chunks, [before + 100 * n for n in range(len(chunks))], hq, hkv, d, fmt, 64, seed=27, pad=2).check()
+
+
+@BOTH
+@DIMS
+def test_steps_beside_chunks(F, d, fmt):
+    """A few steps among chunks, and a few chunks among steps: either kind gets its SMs, and each result its definition."""
+    Batch(F, [300, 1, 200, 2, 1], [100, 3000, 700, 64, 5000], 4, 2, d, fmt, 16, seed=28, window=4000).check()
+    Batch(F, [1] * 30 + [40], [3000 + 50 * n for n in range(31)], 8, 4, d, fmt, 64, seed=29).check()
+
+
+@pytest.mark.parametrize("window,gone", [(100, [900 - 1 - 100, 2000 - 4 - 100, 700 - 300 - 100]), (0, [899, 1996, 400])])
+def test_pages_before_a_window_may_be_given_back(F, window, gone):
+    import torch
+    b = Batch(F, [1, 4, 300], [899, 1996, 400], 4, 2, 64, "e4m3", 16, seed=30, window=window)
+    want = [t.clone() for t in b.check()]
+    for n, first in enumerate(gone):
+        b.table[n, :first // 16] = -7
+    out = b.forward()
+    assert b.att.device_status() == 0 and all(torch.equal(x, y) for x, y in zip(out, want))
+
+
+def test_one_plan_serves_many_calls(F):
+    """Layers of a step on one plan, split units in all of them, one after the other without a wait between."""
+    import torch
+    layers = [Batch(F, [1, 200, 1], [9000, 3000, 64], 4, 1, 128, fmt, 64, seed=31 + i) for i, fmt in enumerate(("e4m3", "bf16", "e4m3"))]
+    att = layers[0].att
+    want = [[t.clone() for t in b.check()] for b in layers]
+    got = []
+    for _ in range(4):
+        for b in layers:
+            got.append([t.clone() for t in att.forward(b.cache, b.q, b.table)])
+    torch.cuda.synchronize()
+    assert att.device_status() == 0
+    for i, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, want[i % 3]))
+
+
 def test_many_sequences(F):
     rng = np.random.default_rng(10)
     chunks = rng.choice([0, 1, 1, 1, 2, 30], 1500)
