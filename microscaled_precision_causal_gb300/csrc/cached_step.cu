@@ -141,58 +141,69 @@ template <int D, int ROWS>
 __device__ __forceinline__ void join_rows(const CachedParams& p, const StepPiece& u, int warp, int lane) {
   constexpr int kPer = D / 32, kMine = (ROWS + kComputeWarps - 1) / kComputeWarps;
   auto piece = [&](int i) { return cached_part<true, D>(p, u.owner + i, i == 0 ? 1 : 0); };
+  using Vec = std::conditional_t<kPer == 2, float2, float4>;
+  constexpr int kAhead = 4;        // pieces whose values are fetched with the references
   int row[kMine];
-  float neg[kMine], l[kMine];
+  float top[kMine], neg[kMine], l[kMine], ref[kMine], sum[kMine];
+  Vec y[kAhead][kMine];
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
     row[k] = min(warp + kComputeWarps * k, u.rows - 1);
-    neg[k] = -INFINITY;
-    l[k] = 0.f;
+    ref[k] = top[k] = lane < u.pieces ? __ldcg(piece(lane) + kStepRows * D + row[k]) : -INFINITY;
+    sum[k] = lane < u.pieces ? __ldcg(piece(lane) + kStepRows * (D + 1) + row[k]) : 0.f;
   }
-  for (int i = lane; i < u.pieces; i += 32)
+  auto value = [&](int i, int k) { return __ldcg(reinterpret_cast<const Vec*>(piece(i) + row[k] * D + lane * kPer)); };
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) neg[k] = fmaxf(neg[k], __ldcg(piece(i) + kStepRows * D + row[k]));
+  for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-  for (int k = 0; k < kMine; ++k) {
+    for (int k = 0; k < kMine; ++k) y[j][k] = value(min(j, u.pieces - 1), k);
+  for (int i = lane + 32; i < u.pieces; i += 32)
 #pragma unroll
-    for (int w = 16; w; w >>= 1) neg[k] = fmaxf(neg[k], __shfl_xor_sync(0xffffffffu, neg[k], w));
-  }
-  float top[kMine];
+    for (int k = 0; k < kMine; ++k) top[k] = fmaxf(top[k], __ldcg(piece(i) + kStepRows * D + row[k]));
   float o[kMine][kPer] = {};
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
-    top[k] = neg[k];
+#pragma unroll
+    for (int w = 16; w; w >>= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], w));
     neg[k] = top[k] == -INFINITY ? 0.f : -top[k];
+    l[k] = 0.f;
   }
+  auto add = [&](const Vec& x, float w, float (&acc)[kPer]) {
+    acc[0] = fmaf(w, x.x, acc[0]);
+    acc[1] = fmaf(w, x.y, acc[1]);
+    if constexpr (kPer == 4) {
+      acc[2] = fmaf(w, x.z, acc[2]);
+      acc[3] = fmaf(w, x.w, acc[3]);
+    }
+  };
   for (int b = 0; b < u.pieces; b += 32) {
     const int i = b + lane;
     float wt[kMine] = {};
     if (i < u.pieces)
 #pragma unroll
       for (int k = 0; k < kMine; ++k) {
-        wt[k] = fast_exp2(__ldcg(piece(i) + kStepRows * D + row[k]) + neg[k]);
-        l[k] += wt[k] * __ldcg(piece(i) + kStepRows * (D + 1) + row[k]);
+        if (b) {
+          ref[k] = __ldcg(piece(i) + kStepRows * D + row[k]);
+          sum[k] = __ldcg(piece(i) + kStepRows * (D + 1) + row[k]);
+        }
+        wt[k] = fast_exp2(ref[k] + neg[k]);
+        l[k] += wt[k] * sum[k];
       }
     const int here = min(32, u.pieces - b);
-#pragma unroll 4
-    for (int j = 0; j < here; ++j) {
-      const float* src = piece(b + j) + lane * kPer;
+    int j = 0;
+    if (b == 0) {
 #pragma unroll
-      for (int k = 0; k < kMine; ++k) {
-        const float wj = __shfl_sync(0xffffffffu, wt[k], j);
-        if constexpr (kPer == 2) {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(src + row[k] * D));
-          o[k][0] = fmaf(wj, y.x, o[k][0]);
-          o[k][1] = fmaf(wj, y.y, o[k][1]);
-        } else {
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(src + row[k] * D));
-          o[k][0] = fmaf(wj, y.x, o[k][0]);
-          o[k][1] = fmaf(wj, y.y, o[k][1]);
-          o[k][2] = fmaf(wj, y.z, o[k][2]);
-          o[k][3] = fmaf(wj, y.w, o[k][3]);
+      for (; j < kAhead; ++j)
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+          const float w = __shfl_sync(0xffffffffu, wt[k], j);
+          if (j < u.pieces) add(y[j][k], w, o[k]);
         }
-      }
     }
+#pragma unroll 4
+    for (; j < here; ++j)
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) add(value(b + j, k), __shfl_sync(0xffffffffu, wt[k], j), o[k]);
   }
   const int group = p.hq / p.c.hkv;
 #pragma unroll
@@ -287,6 +298,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         *reinterpret_cast<StepPiece*>(smem + L::kUnit + (n % kUnits) * sizeof(StepPiece)) = x;
       }
+      // page (or half page) i of the unit's tiles: where its keys are, or -1
+      const int first = (u.tile + t0) * per, end = (u.tile + t1) * per;
+      auto page_of = [&](int i) {
+        const int pos = i * rows;
+        if (i >= end || pos >= u.keys || pos + rows <= u.lo) return -1;
+        const int page = cache_page(p.c, u.seq, pos >> p.c.page_shift);
+        return page < 0 ? -1 : page * p.c.hkv + u.h;
+      };
+      int batch = first, now = page_of(first + lane), next = page_of(first + 32 + lane);
       // queries: 16 bytes a lane and copy, rows behind the unit's are zeros
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;
 #pragma unroll
@@ -302,15 +322,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) mbar_arrive(&unit_full[n % kUnits]);
       ++n;
       if (t1 == 0) break;
-      // page (or half page) i of the unit's tiles: where its keys are, or -1
-      const int first = (u.tile + t0) * per, end = (u.tile + t1) * per;
-      auto page_of = [&](int i) {
-        const int pos = i * rows;
-        if (i >= end || pos >= u.keys || pos + rows <= u.lo) return -1;
-        const int page = cache_page(p.c, u.seq, pos >> p.c.page_shift);
-        return page < 0 ? -1 : page * p.c.hkv + u.h;
-      };
-      int batch = first, now = page_of(first + lane), next = page_of(first + 32 + lane);
       for (int t = t0; t < t1 && ok; ++t, ++ring) {
         const int i = (u.tile + t) * per;
         if (i >= batch + 32) {
@@ -747,20 +758,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&unit_done[n % kUnits]);
     }
-    ok = named_bar_and(1, kComputeWarps * 32, ok);
-    if (!ok) break;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = 8 * t + 2 * q + r;
         if (row >= u.rows) continue;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kComputeWarps; ++w) top = fmaxf(top, stat[w * 2 * L::kRows + row]);
-        float to = m[t][r] == top ? 0.f : m[t][r] - top;
-        if constexpr (E4M3) to += M[t][r] - kBoost;
-        to = m[t][r] == -INFINITY ? 0.f : fast_exp2(to);
+        // (values in units of 2^(M - 13) against m)
+        const float to = !E4M3 || M[t][r] == -INFINITY ? 1.f : fast_exp2(M[t][r] - kBoost);
         // head dimensions (D / 8) g + 2 d and + 1 of product tile d; bf16: of each half of the row's 8 g + 2 (d mod 4)
         float* dst = red + (warp * L::kRows + row) * D;
 #pragma unroll
@@ -768,7 +773,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           *reinterpret_cast<float4*>(dst + (E4M3 ? (D / 8) * g + 2 * d : (d >> 2) * 64 + 8 * g + 2 * (d & 3))) =
               make_float4(o[d][t][r] * to, o[d][t][2 + r] * to, o[d + 1][t][r] * to, o[d + 1][t][2 + r] * to);
       }
-    named_bar_sync(1, kComputeWarps * 32);
+    ok = named_bar_and(1, kComputeWarps * 32, ok);
+    if (!ok) break;
     const bool whole = u.t0 == 0 && u.t1 == u.tiles;
     if (!whole) pending = u.t0 == 0 ? 1 : 0;
     float* part = cached_part<true, D>(p, blockIdx.x, u.t0 == 0 ? 1 : 0);
@@ -782,9 +788,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int w = 0; w < kComputeWarps; ++w) {
         const float4 z = *reinterpret_cast<const float4*>(red + (w * L::kRows + r) * D + 4 * c);
-        sum = make_float4(sum.x + z.x, sum.y + z.y, sum.z + z.z, sum.w + z.w);
-        const float mw = stat[w * 2 * L::kRows + r];
-        tot += mw == -INFINITY ? 0.f : stat[w * 2 * L::kRows + L::kRows + r] * fast_exp2(mw - top);
+        const float mw = stat[w * 2 * L::kRows + r], f = mw == top ? 1.f : fast_exp2(mw - top);     // (a warp that saw nothing: 0)
+        sum = make_float4(fmaf(z.x, f, sum.x), fmaf(z.y, f, sum.y), fmaf(z.z, f, sum.z), fmaf(z.w, f, sum.w));
+        tot = fmaf(stat[w * 2 * L::kRows + L::kRows + r], f, tot);
       }
       if (whole) {
         const int64_t tok = u.start + (u.row + r) / group;
