@@ -20,6 +20,9 @@ __host__ __device__ inline int step_rows(int group, int64_t max_chunk) {
 }
 // What a unit costs besides its key tiles, in key tiles, when the work is dealt out: its queries, its start, its end.
 constexpr int kStepExtra = 3, kChunkExtra = 3;
+// What it costs to join pieces, in key tiles (chunks gained up to 9; steps of 5 sequences of 100 to 900 keys took 14.8
+// instead of 12.6 us whole, with 12).
+constexpr int kStepJoin = 9, kChunkJoin = 9;
 
 // ---------------------------------------------------------------- plan
 enum CachePlanWord : int {
@@ -43,15 +46,20 @@ struct alignas(16) CacheItem {
 };
 // A unit is an item for a kv head: a tile of a sequence's rows over the key tiles that they see.  The places of all
 // units, unit after unit, are dealt out to the CTAs in equal shares, so that every CTA has the same to do whatever
-// the sequences' lengths are: a unit has some places for what it costs besides (kStepExtra, kChunkExtra), then one
-// for each key tile.  A unit whose key tiles lie in several shares is joined after.
+// the sequences' lengths are (in whole units where that takes little longer): a unit has some places for what it costs
+// besides (kStepExtra, kChunkExtra), then one for each key tile.  A unit whose key tiles lie in several shares is joined
+// after.
 struct CachedUnit {
   int seq, h, row, rows, tile, tiles;     // first row, rows, first key tile, key tiles
   int start, count, keys, lo;             // of the sequence (CachePlanView::seq)
   int item, pad;
   int64_t begin;                          // its first place
 };
-static_assert(sizeof(CachedUnit) == 56, "");
+struct ShareStart {
+  CachedUnit u;                           // the unit that the share begins in
+  int64_t from, to;                       // its places
+};
+static_assert(sizeof(ShareStart) == 72, "");
 constexpr int kStepCtas = 304, kChunkCtas = 152, kDone = kStepCtas + 8 * kChunkCtas;
 struct CachePlanView {
   int* hdr;
@@ -60,7 +68,7 @@ struct CachePlanView {
   CacheItem* items[2];        // [cap] chunk items, [kStepTiles N] steps
   int64_t* prefix[2];         // [items + 1] places of the items before, for one kv head
   int64_t* base;              // [N + 1] chunk items before
-  CachedUnit* first[2];       // [CTAs] the unit that a CTA's share begins in
+  ShareStart* first[2];       // [CTAs] where a CTA's share begins and ends
   int* done;                  // [kStepCtas + 8 kChunkCtas] finished pieces of a split unit (of a chunk's 32 rows each), by
                               // the CTA that has its beginning; 0 between calls
 };
@@ -79,7 +87,7 @@ __host__ __device__ inline CachePlanView cache_plan_view(const void* plan, int64
   v.prefix[0] = (int64_t*)(v.items[1] + (int64_t)kStepTiles * N);
   v.prefix[1] = v.prefix[0] + (cap + 1);
   v.base = v.prefix[1] + ((int64_t)kStepTiles * N + 1);
-  v.first[0] = (CachedUnit*)(v.base + (N + 1));
+  v.first[0] = (ShareStart*)(v.base + (N + 1));
   v.first[1] = v.first[0] + kChunkCtas;
   v.done = (int*)(v.first[1] + kStepCtas);
   if (bytes) *bytes = (size_t)((const uint8_t*)(v.done + kDone) - (const uint8_t*)plan);

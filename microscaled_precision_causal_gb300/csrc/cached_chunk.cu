@@ -9,7 +9,9 @@
 //     A thread unpacks a key's row, so the scale is one register; both sides are free of bank
 //     conflicts by the copies' and the products' swizzles.
 //   - All units' key tiles are dealt out in equal shares (cache.cuh): one chunk over a long context
-//     keeps every SM busy, and the pieces are joined after.
+//     keeps every SM busy, and the pieces are joined after.  Both warpgroups on the key tiles of a unit of one row tile, in
+//     turn, gained little (16 sequences of 26 rows of 4 heads 16.7 -> 15.3 us, 11 of 86 17.4 -> 19.1) and cost the
+//     others (4 x 1024 with a window 74.5 -> 77.8).
 // Keys behind the sequence or before every row's window are zeros to the products, whatever the page holds.
 //
 // Roles (512 threads):
@@ -29,7 +31,6 @@
 namespace flamia {
 
 namespace {
-
 
 constexpr int kThreads = 512;
 constexpr float kRescaleAbove = 8.f, kLoose = 64.f;
@@ -320,7 +321,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_wait();                            // who comes behind this launch comes behind the one before it too
     return;
   }
-  const int64_t f0 = sh.begin(blockIdx.x), f1 = sh.begin(blockIdx.x + 1);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -424,8 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int group = p.hq / p.c.hkv;
       uint32_t nq[2] = {0, 0};
       bool ok = true;
-      int64_t f = f0;
-      CachedUnit u = pv.first[0][blockIdx.x];
+      const ShareStart share = pv.first[0][blockIdx.x];
+      int64_t f = share.from;
+      const int64_t f1 = share.to;
+      CachedUnit u = share.u;
       for (int n = 0; ok; ++n) {
         if (n >= kUnits && !(ok = warp_wait(&unit_done[n % kUnits], (n / kUnits - 1) & 1, status))) break;
         Piece U{};

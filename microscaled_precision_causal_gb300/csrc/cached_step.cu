@@ -263,11 +263,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == kComputeWarps) {
     // ------------------------------------------------------------ producer
-    const int64_t f1 = sh.begin(blockIdx.x + 1);
     const int P = 1 << p.c.page_shift, rows = min(P, kStepTile), per = kStepTile / rows;      // pages a tile
     const uint32_t page_bytes = 2 * rows * L::kRowBytes;
-    CachedUnit u = pv.first[1][blockIdx.x];
-    int64_t f = sh.begin(blockIdx.x);
+    const ShareStart share = pv.first[1][blockIdx.x];
+    const int64_t f1 = share.to;
+    CachedUnit u = share.u;
+    int64_t f = share.from;
     for (int n = 0; ok;) {
       int2 piece = make_int2(0, 0);
       if (f < f1) {

@@ -290,6 +290,16 @@ def test_steps_beside_chunks(F, d, fmt):
     Batch(F, [1] * 30 + [40], [3000 + 50 * n for n in range(31)], 8, 4, d, fmt, 64, seed=29).check()
 
 
+@BOTH
+@DIMS
+@pytest.mark.parametrize("chunk,count", [(1, 200), (26, 60)])
+@pytest.mark.parametrize("longest", [200, 30000])
+def test_short_sequences_and_a_long_one(F, longest, chunk, count, d, fmt):
+    """Many short units, some of them a CTA's, and the same ones beside one that has to be split."""
+    before = [7 * n % 190 for n in range(count - 1)] + [longest]
+    Batch(F, [chunk] * count, before, 16, 4, d, fmt, 64, seed=32, pad=1).check()
+
+
 @pytest.mark.parametrize("window,gone", [(100, [900 - 1 - 100, 2000 - 4 - 100, 700 - 300 - 100]), (0, [899, 1996, 400])])
 def test_pages_before_a_window_may_be_given_back(F, window, gone):
     import torch
