@@ -1,4 +1,4 @@
-// Attention over the paged cache for chunks: more than 16 rows of a kv head.
+// Attention over the paged cache for chunks: more rows of a kv head than a step takes.
 //
 // The scored forward's scheme (bf16 tcgen05 MMAs, two tiles of 128 rows in turn, P in tensor memory over the
 // scores it came from, a reference m near the row's maximum) with three differences:
@@ -22,6 +22,10 @@
 //   warps 12-15   E4M3: unpack (eight warps, four each for K and V, at 136 registers for the softmax: 475 instead of 419
 //                 us for a chunk of 2048 behind 14336)
 // TMEM columns as in the scored forward.
+//
+// Bound by the chain of scores, softmax and values of two row tiles in turn, the tensor cores busy half the time, and at d 64
+// by the softmax's arithmetic.  Measured: a chunk of 2048 behind 14336, 32 heads on 8, d 128, E4M3 418 us, 1230 TFLOP/s (65% of
+// cuBLAS's bf16; bf16 pages 376); 4 chunks of 1024 with a window of 2048, 16 heads, d 64 78 us.
 #include <type_traits>
 
 #include "cache.cuh"
