@@ -769,14 +769,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int r = 0; r < 2; ++r) {
         const int row = 8 * t + 2 * q + r;
         if (row >= u.rows) continue;
-        // (values in units of 2^(M - 13) against m)
-        const float to = !E4M3 || M[t][r] == -INFINITY ? 1.f : fast_exp2(M[t][r] - kBoost);
+        // (values in units of 2^(M - 13) against m; in two factors, of which neither falls below fp32's range)
+        const float to = !E4M3 || M[t][r] == -INFINITY ? 1.f : fast_exp2(M[t][r]), by = E4M3 ? exp2i(-(int)kBoost) : 1.f;
         // head dimensions (D / 8) g + 2 d and + 1 of product tile d; bf16: of each half of the row's 8 g + 2 (d mod 4)
         float* dst = red + (warp * L::kRows + row) * D;
 #pragma unroll
         for (int d = 0; d < kOut; d += 2)
           *reinterpret_cast<float4*>(dst + (E4M3 ? (D / 8) * g + 2 * d : (d >> 2) * 64 + 8 * g + 2 * (d & 3))) =
-              make_float4(o[d][t][r] * to, o[d][t][2 + r] * to, o[d + 1][t][r] * to, o[d + 1][t][2 + r] * to);
+              make_float4(o[d][t][r] * by * to, o[d][t][2 + r] * by * to, o[d + 1][t][r] * by * to, o[d + 1][t][2 + r] * by * to);
       }
     ok = named_bar_and(1, kComputeWarps * 32, ok);
     if (!ok) break;

@@ -266,6 +266,17 @@ def test_tokens_of_very_different_size(F, sizes, d, fmt):
     Batch(F, [1, 4, 150], [600, 300, 200], 4, 2, d, fmt, 16, seed=8, sizes=sizes, scale=2.0 ** -12, gain=0.01).check()
 
 
+@BOTH
+@DIMS
+@pytest.mark.parametrize("exponent", [-114, 100])
+def test_values_near_the_ends_of_their_range(F, exponent, d, fmt):
+    """Value scales down to a byte of some 6, and up to 2^95: steps of one and two row tiles, a chunk."""
+    for chunks in ([1, 4, 150], [1, 4, 8]):
+        b = Batch(F, chunks, [600, 300, 200], 8, 2, d, fmt, 16, seed=33)
+        b.fill("v", bf16(np.random.default_rng(34), *b.cache.v.shape, gain=2.0 ** exponent))
+        b.check()
+
+
 @pytest.mark.parametrize("shape", [([1], [16000]), ([1, 1], [9000, 20000]), ([2], [6000]), ([40], [12000]), ([300], [5000])])
 @DIMS
 def test_long_contexts_are_split_and_joined(F, shape, d):
