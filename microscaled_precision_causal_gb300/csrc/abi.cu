@@ -633,6 +633,7 @@ int flamia_cached_fwd(const void* q_bf16, const flamia_kv_cache* cache, const in
   p.scale2 = (float)(sc * 1.4426950408889634);
   p.cap = softcap;
   p.capf = cap_form(sc, (double)softcap);
+  p.inv_group = 65536u / (uint32_t)(hq / hkv) + 1;
   p.part = static_cast<float*>(workspace);
   return cuda_status(launch_cached_fwd(d, cache->format == FLAMIA_CACHE_E4M3, p, (cudaStream_t)stream));
 }

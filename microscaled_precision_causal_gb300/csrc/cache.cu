@@ -246,7 +246,7 @@ __device__ __forceinline__ TokenGroup token_group(const CacheParams& p, int per)
 // The lane's token's place (row of kv head 0 in the pools), -1 where it has none: behind the last sequence, or no page.
 __device__ __forceinline__ int64_t token_place(const CacheParams& p, const TokenGroup& g, int lane, int valid) {
   if (lane >= g.n || g.token + lane >= valid) return -1;
-  const int2 r = reinterpret_cast<const int2*>(p.plan + kCpHeaderWords)[g.token + lane];
+  const int2 r = reinterpret_cast<const int2*>(p.plan + kCpRowWords)[g.token + lane];
   const int page = cache_page(p, r.x, r.y >> p.page_shift);
   return page < 0 ? -1 : ((int64_t)page * p.hkv << p.page_shift) + (r.y & ((1 << p.page_shift) - 1));
 }

@@ -61,6 +61,9 @@ struct ShareStart {
 };
 static_assert(sizeof(ShareStart) == 72, "");
 constexpr int kStepCtas = 304, kChunkCtas = 152, kDone = kStepCtas + 8 * kChunkCtas;
+// Words before the rows' places, the same in every plan: so a kernel may read its share before it knows whose plan it has.
+constexpr int kCpRowWords = kCpHeaderWords + (kChunkCtas + kStepCtas) * (int)(sizeof(ShareStart) / 4);
+static_assert(kCpRowWords % 4 == 0, "");
 struct CachePlanView {
   int* hdr;
   int2* row;                  // [T] {sequence, position} of the sequences' rows
@@ -75,21 +78,21 @@ struct CachePlanView {
 __host__ __device__ inline int64_t cache_item_capacity(int64_t T, int N, int hq, int hkv) {
   return T * (hq / hkv) / kChunkRows + N;
 }
-// The rows come first: writing and reading the cache need no more of the layout.
+// The shares and the rows come first: writing and reading the cache need no more of the layout.
 __host__ __device__ inline CachePlanView cache_plan_view(const void* plan, int64_t T, int N, int hq, int hkv, size_t* bytes = nullptr) {
   const int64_t cap = cache_item_capacity(T, N, hq, hkv);
   CachePlanView v;
   v.hdr = (int*)plan;
-  v.row = (int2*)(v.hdr + kCpHeaderWords);
+  v.first[0] = (ShareStart*)(v.hdr + kCpHeaderWords);
+  v.first[1] = v.first[0] + kChunkCtas;
+  v.row = (int2*)(v.hdr + kCpRowWords);
   v.seq = (int4*)(v.row + ((T + 1) & ~(int64_t)1));
   v.items[0] = (CacheItem*)(v.seq + N);
   v.items[1] = v.items[0] + cap;
   v.prefix[0] = (int64_t*)(v.items[1] + (int64_t)kStepTiles * N);
   v.prefix[1] = v.prefix[0] + (cap + 1);
   v.base = v.prefix[1] + ((int64_t)kStepTiles * N + 1);
-  v.first[0] = (ShareStart*)(v.base + (N + 1));
-  v.first[1] = v.first[0] + kChunkCtas;
-  v.done = (int*)(v.first[1] + kStepCtas);
+  v.done = (int*)(v.base + (N + 1));
   if (bytes) *bytes = (size_t)((const uint8_t*)(v.done + kDone) - (const uint8_t*)plan);
   return v;
 }
@@ -135,6 +138,7 @@ struct CachedParams {
   float scale2;              // softmax scale log2 e
   float cap;                 // 0: none
   CapForm capf;
+  uint32_t inv_group;        // 2^16 / (hq / hkv) and a bit more: a division of a step's rows
   float* part;               // workspace
 };
 // A CTA leaves at most two unfinished pieces of units behind (the unit that its first key tile lies inside of, and the
@@ -149,7 +153,17 @@ __device__ __forceinline__ int cached_valid_rows(const CachedParams& p) {
   atomicOr(p.c.plan + kCpStatus, FLAMIA_DEV_PLAN_MISMATCH);
   return 0;
 }
-
+// O = 0, LSE = +inf behind the last sequence.
+template <int D>
+__device__ __forceinline__ void clear_rows(const CachedParams& p, int valid, int threads) {
+  for (int row = valid + blockIdx.x; row < p.c.T; row += gridDim.x) {
+    uint4* dst = reinterpret_cast<uint4*>(p.out + (int64_t)row * p.hq * D);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < p.hq * (D / 8); i += threads) dst[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int h = threadIdx.x; h < p.hq; h += threads) p.lse[(int64_t)h * p.c.T + row] = INFINITY;
+  }
+}
 
 // ---------------------------------------------------------------- units and shares
 struct Shares {
@@ -205,12 +219,19 @@ __device__ __forceinline__ int2 cached_piece(const CachedUnit& u, int64_t& f, in
   f = to;
   return t;
 }
-// The CTAs whose pieces of u are to be joined: the first one, and their number.
+// The CTAs whose pieces of u are to be joined, of which the caller has key tiles [t0, t1): the first one, and their number.
 template <bool STEP>
-__device__ __forceinline__ int2 cached_owners(const CachedUnit& u, const Shares& sh) {
+__device__ __forceinline__ int2 cached_owners(const CachedUnit& u, const Shares& sh, int t0, int t1) {
   const int64_t first = u.begin + (STEP ? kStepExtra : kChunkExtra);
-  const int c = sh.of(first);
-  return make_int2(c, sh.of(first + u.tiles - 1) - c + 1);
+  int2 c = make_int2(blockIdx.x, blockIdx.x);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {        // (mostly one division, of 64 bits)
+    if (i ? t1 == u.tiles : t0 == 0) continue;
+    const int y = sh.of(i ? first + u.tiles - 1 : first);
+    if (i) c.y = y;
+    else c.x = y;
+  }
+  return make_int2(c.x, c.y - c.x + 1);
 }
 // Unfinished pieces: the one that a CTA's share begins in the middle of (0), and the one that it ends in the middle of and
 // has the beginning of (1).  [rows][D] weighted values, [rows] references (base 2), [rows] sums.

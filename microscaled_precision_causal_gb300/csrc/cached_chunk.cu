@@ -307,19 +307,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* units = smem + L::kUnit;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_let_next();
-  const int valid = cached_valid_rows(p);
-  if (tail) {                               // O = 0, LSE = +inf behind the last sequence
-    const int64_t rows = (int64_t)(p.c.T - valid) * p.hq;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rows; i += (int64_t)gridDim.x * kThreads) {
-      const int64_t row = valid + i / p.hq;
-      const int h = (int)(i % p.hq);
-      uint4* dst = reinterpret_cast<uint4*>(p.out + (row * p.hq + h) * D);
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) dst[j] = make_uint4(0, 0, 0, 0);
-      p.lse[(int64_t)h * p.c.T + row] = INFINITY;
-    }
-  }
   const CachePlanView pv = cache_plan_view(p.c.plan, p.c.T, p.c.N, p.hq, p.c.hkv);
+  ShareStart share;
+  if (warp == 2) share = pv.first[0][blockIdx.x];      // (beside the header; of use if there is a share)
+  const int valid = cached_valid_rows(p);
+  if (tail) clear_rows<D>(p, valid, kThreads);
   const Shares sh = cached_shares<false>(pv.hdr);
   if (valid == 0 || (int)blockIdx.x >= sh.n) {
     grid_wait();                            // who comes behind this launch comes behind the one before it too
@@ -428,17 +420,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int group = p.hq / p.c.hkv;
       uint32_t nq[2] = {0, 0};
       bool ok = true;
-      const ShareStart share = pv.first[0][blockIdx.x];
       int64_t f = share.from;
       const int64_t f1 = share.to;
       CachedUnit u = share.u;
       for (int n = 0; ok; ++n) {
         if (n >= kUnits && !(ok = warp_wait(&unit_done[n % kUnits], (n / kUnits - 1) & 1, status))) break;
         Piece U{};
+        int2 tiles = make_int2(0, 0);
         while (f < f1 && U.tiles == 0) {
           if (f >= u.begin + kChunkExtra + u.tiles) cached_next<false>(pv, u, p.hq, p.c.hkv);
           const int2 piece = cached_piece<false>(u, f, f1);
           const int t0 = piece.x, t1 = piece.y;
+          tiles = piece;
           U.tiles = t1 - t0;
           U.last = u.tile + u.tiles - 1 - t0;
           U.h = u.h;
@@ -451,19 +444,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           U.lo = p.left < 0 ? 0 : max(0, U.pos0 + u.row / group - p.left);
           U.seq = u.seq;
           U.slot = U.tiles == u.tiles ? -1 : (t0 == 0 ? 1 : 0);
-          if (U.slot >= 0) {
-            const int2 c = cached_owners<false>(u, sh);
-            U.owner = c.x;
-            U.pieces = c.y;
-          }
         }
         if (lane == 0) {
           *reinterpret_cast<Piece*>(units + (n % kUnits) * sizeof(Piece)) = U;
-          if (U.slot >= 0 && U.tiles) *reinterpret_cast<Piece*>(smem + L::kSplits + U.slot * sizeof(Piece)) = U;
           mbar_arrive(&unit_full[n % kUnits]);
         }
         __syncwarp();
         if (U.tiles == 0) break;
+        // (read by the softmax warps from the next unit's start on)
+        auto keep_split = [&]() {
+          if (lane == 0 && U.slot >= 0) {
+            const int2 c = cached_owners<false>(u, sh, tiles.x, tiles.y);
+            U.owner = c.x;
+            U.pieces = c.y;
+            *reinterpret_cast<Piece*>(smem + L::kSplits + U.slot * sizeof(Piece)) = U;
+          }
+          __syncwarp();
+        };
         // Where the heads that share a kv head divide a tile's rows, a box of their tokens is the tile (rows behind
         // the unit's are other sequences', or zeros behind the last token: they have no say and are not stored).
         if (kTile % group == 0) {
@@ -479,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
+          keep_split();
           continue;
         }
         // else two (D = 128) or four rows at a time, 16 bytes a lane; rows behind the unit's are zeros
@@ -516,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&q_full[w]);
         }
+        keep_split();
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (kTile % group == 0)                       // (reached early only when a wait ran out)

@@ -127,43 +127,38 @@ struct StepSmem {
 static_assert(2 * (StepSmem<128, false, 2>::kAlloc + 1024) <= 233472 && 2 * (StepSmem<128, true, 2>::kAlloc + 1024) <= 233472,
               "two CTAs an SM");
 
-// O = 0, LSE = +inf behind the last sequence.
-__device__ __forceinline__ void clear_rows(const CachedParams& p, int D, int valid, int thread, int threads) {
-  const int64_t rows = (int64_t)(p.c.T - valid) * p.hq;
-  for (int64_t i = (int64_t)blockIdx.x * threads + thread; i < rows; i += (int64_t)gridDim.x * threads) {
-    const int64_t row = valid + i / p.hq;
-    const int h = (int)(i % p.hq);
-    uint4* dst = reinterpret_cast<uint4*>(p.out + (row * p.hq + h) * D);
-    for (int j = 0; j < D / 8; ++j) dst[j] = make_uint4(0, 0, 0, 0);
-    p.lse[(int64_t)h * p.c.T + row] = INFINITY;
-  }
-}
-
 // A split unit's rows warp, warp + 4, ... at once (so that their loads fly together); its pieces may be hundreds: a lane a
 // piece for their weights.
 template <int D, int ROWS>
 __device__ __forceinline__ void join_rows(const CachedParams& p, const StepPiece& u, int warp, int lane) {
   constexpr int kPer = D / 32, kMine = (ROWS + kComputeWarps - 1) / kComputeWarps;
-  auto piece = [&](int i) { return cached_part<true, D>(p, u.owner + i, i == 0 ? 1 : 0); };
   using Vec = std::conditional_t<kPer == 2, float2, float4>;
   constexpr int kAhead = 4;        // pieces whose values are fetched with the references
+  constexpr int kPieceFloats = kStepRows * (D + 2);
+  const float* base = cached_part<true, D>(p, u.owner, 0);
+  auto piece = [&](int i) { return (2 * i + (i == 0 ? 1 : 0)) * kPieceFloats; };
   int row[kMine];
   float top[kMine], neg[kMine], l[kMine], ref[kMine], sum[kMine];
   Vec y[kAhead][kMine];
+  {
+    const float* mine = base + piece(min(lane, u.pieces - 1)) + kStepRows * D;
 #pragma unroll
-  for (int k = 0; k < kMine; ++k) {
-    row[k] = min(warp + kComputeWarps * k, u.rows - 1);
-    ref[k] = top[k] = lane < u.pieces ? __ldcg(piece(lane) + kStepRows * D + row[k]) : -INFINITY;
-    sum[k] = lane < u.pieces ? __ldcg(piece(lane) + kStepRows * (D + 1) + row[k]) : 0.f;
+    for (int k = 0; k < kMine; ++k) {
+      row[k] = min(warp + kComputeWarps * k, u.rows - 1);
+      ref[k] = top[k] = __ldcg(mine + row[k]);
+      sum[k] = __ldcg(mine + kStepRows + row[k]);
+    }
   }
-  auto value = [&](int i, int k) { return __ldcg(reinterpret_cast<const Vec*>(piece(i) + row[k] * D + lane * kPer)); };
 #pragma unroll
-  for (int j = 0; j < kAhead; ++j)
+  for (int j = 0; j < kAhead; ++j) {
+    const float* from = base + piece(min(j, u.pieces - 1)) + lane * kPer;
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) y[j][k] = value(min(j, u.pieces - 1), k);
+    for (int k = 0; k < kMine; ++k) y[j][k] = __ldcg(reinterpret_cast<const Vec*>(from + row[k] * D));
+  }
+#pragma unroll 1
   for (int i = lane + 32; i < u.pieces; i += 32)
 #pragma unroll
-    for (int k = 0; k < kMine; ++k) top[k] = fmaxf(top[k], __ldcg(piece(i) + kStepRows * D + row[k]));
+    for (int k = 0; k < kMine; ++k) top[k] = fmaxf(top[k], __ldcg(base + piece(i) + kStepRows * D + row[k]));
   float o[kMine][kPer] = {};
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
@@ -180,6 +175,7 @@ __device__ __forceinline__ void join_rows(const CachedParams& p, const StepPiece
       acc[3] = fmaf(w, x.w, acc[3]);
     }
   };
+#pragma unroll 1
   for (int b = 0; b < u.pieces; b += 32) {
     const int i = b + lane;
     float wt[kMine] = {};
@@ -187,41 +183,49 @@ __device__ __forceinline__ void join_rows(const CachedParams& p, const StepPiece
 #pragma unroll
       for (int k = 0; k < kMine; ++k) {
         if (b) {
-          ref[k] = __ldcg(piece(i) + kStepRows * D + row[k]);
-          sum[k] = __ldcg(piece(i) + kStepRows * (D + 1) + row[k]);
+          ref[k] = __ldcg(base + piece(i) + kStepRows * D + row[k]);
+          sum[k] = __ldcg(base + piece(i) + kStepRows * (D + 1) + row[k]);
         }
         wt[k] = fast_exp2(ref[k] + neg[k]);
         l[k] += wt[k] * sum[k];
       }
     const int here = min(32, u.pieces - b);
-    int j = 0;
-    if (b == 0) {
+    // four pieces' values at a time, the next four on their way
+#pragma unroll 1
+    for (int j = 0; j < here; j += kAhead) {
 #pragma unroll
-      for (; j < kAhead; ++j)
+      for (int a = 0; a < kAhead; ++a) {
+        const float* from = base + piece(min(b + j + a + kAhead, u.pieces - 1)) + lane * kPer;
 #pragma unroll
         for (int k = 0; k < kMine; ++k) {
-          const float w = __shfl_sync(0xffffffffu, wt[k], j);
-          if (j < u.pieces) add(y[j][k], w, o[k]);
+          const float w = __shfl_sync(0xffffffffu, wt[k], (j + a) & 31);
+          if (j + a < here) add(y[a][k], w, o[k]);
+          y[a][k] = __ldcg(reinterpret_cast<const Vec*>(from + row[k] * D));
         }
+      }
     }
-#pragma unroll 4
-    for (; j < here; ++j)
-#pragma unroll
-      for (int k = 0; k < kMine; ++k) add(value(b + j, k), __shfl_sync(0xffffffffu, wt[k], j), o[k]);
   }
+  // a lane a row finishes its row's sums
   const int group = p.hq / p.c.hkv;
+  float mine_l = 1.f, mine_top = 0.f;
 #pragma unroll
   for (int k = 0; k < kMine; ++k) {
 #pragma unroll
     for (int w = 16; w; w >>= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], w);
-    if (warp + kComputeWarps * k >= u.rows) continue;
-    const int h = u.h * group + (u.row + row[k]) % group;
-    const int64_t tok = u.start + (u.row + row[k]) / group;
-    const float inv = 1.f / l[k];
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (tok * p.hq + h) * D + lane * kPer);
+    if (lane == k) mine_l = l[k], mine_top = top[k];
+  }
+  const int r = warp + kComputeWarps * lane, x = u.row + min(r, u.rows - 1), t = (int)(x * p.inv_group >> 16);
+  const int h = u.h * group + x - t * group;
+  const int64_t tok = u.start + t, at = (tok * p.hq + h) * D;
+  const float inv = 1.f / mine_l;
+  if (lane < kMine && r < u.rows) p.lse[(int64_t)h * p.c.T + tok] = (mine_top + log2f(mine_l)) * kLn2;
 #pragma unroll
-    for (int j = 0; j < kPer / 2; ++j) dst[j] = pack2<false>(o[k][2 * j] * inv, o[k][2 * j + 1] * inv);
-    if (lane == 0) p.lse[(int64_t)h * p.c.T + tok] = (top[k] + log2f(l[k])) * kLn2;
+  for (int k = 0; k < kMine; ++k) {
+    const float f = __shfl_sync(0xffffffffu, inv, k);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + __shfl_sync(0xffffffffu, at, k) + lane * kPer);
+    if (warp + kComputeWarps * k >= u.rows) continue;
+#pragma unroll
+    for (int j = 0; j < kPer / 2; ++j) dst[j] = pack2<false>(o[k][2 * j] * f, o[k][2 * j + 1] * f);
   }
 }
 
@@ -239,10 +243,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* unit_done = unit_full + kUnits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_let_next();
-  const int valid = cached_valid_rows(p);
-  clear_rows(p, D, valid, threadIdx.x, kThreads);
-  if (valid == 0) return;
   const CachePlanView pv = cache_plan_view(p.c.plan, p.c.T, p.c.N, p.hq, p.c.hkv);
+  ShareStart share;
+  if (warp == kComputeWarps) share = pv.first[1][blockIdx.x];      // (beside the header; of use if there is a share)
+  const int valid = cached_valid_rows(p);
+  clear_rows<D>(p, valid, kThreads);
+  if (valid == 0) return;
   const Shares sh = cached_shares<true>(pv.hdr);
   if ((int)blockIdx.x >= sh.n) return;
   if (threadIdx.x == 0) {
@@ -262,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   int* status = p.c.plan + kCpStatus;
   const int group = p.hq / p.c.hkv;
+  auto token_of = [&](int row) { return (int)(row * p.inv_group >> 16); };       // row / group
   bool ok = true;
   uint32_t ring = 0;
 
@@ -269,7 +276,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ------------------------------------------------------------ producer
     const int P = 1 << p.c.page_shift, rows = min(P, kStepTile), per = kStepTile / rows;      // pages a tile
     const uint32_t page_bytes = 2 * rows * L::kRowBytes;
-    const ShareStart share = pv.first[1][blockIdx.x];
     const int64_t f1 = share.to;
     CachedUnit u = share.u;
     int64_t f = share.from;
@@ -282,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (n >= kUnits && !(ok = warp_wait(&unit_done[n % kUnits], (n / kUnits - 1) & 1, status))) break;
       const int t0 = piece.x, t1 = piece.y;
+      StepPiece x{};
       if (lane == 0) {
-        StepPiece x{};
         x.t0 = t0;
         x.t1 = t1;
         x.tiles = u.tiles;
@@ -295,12 +301,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         x.pos0 = u.keys - u.count;
         x.keys = u.keys;
         x.lo = u.lo;
-        if (t1 > 0 && t1 - t0 < u.tiles) {
-          const int2 c = cached_owners<true>(u, sh);
-          x.owner = c.x;
-          x.pieces = c.y;
-          reinterpret_cast<StepPiece*>(smem + L::kSplits)[t0 == 0 ? 1 : 0] = x;
-        }
         *reinterpret_cast<StepPiece*>(smem + L::kUnit + (n % kUnits) * sizeof(StepPiece)) = x;
       }
       // page (or half page) i of the unit's tiles: where its keys are, or -1
@@ -312,13 +312,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         return page < 0 ? -1 : page * p.c.hkv + u.h;
       };
       int batch = first, now = page_of(first + lane), next = page_of(first + 32 + lane);
-      // queries: 16 bytes a lane and copy, rows behind the unit's are zeros
+      // queries: 16 bytes a lane and copy, rows behind the unit's are zeros.  A row's token and head by a lane a row
+      const int my_row = u.row + (lane < u.rows ? lane : 0), my_t = token_of(my_row);
+      const int64_t my_at = ((int64_t)u.start + my_t) * p.hq + u.h * group + my_row - my_t * group;
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;
 #pragma unroll
       for (int i = 0; i < L::kRows / kPer; ++i) {
         const int r = i * kPer + lane / kLanes, c = lane % kLanes;
         const bool in = t1 > 0 && r < u.rows;
-        const __nv_bfloat16* src = p.q + (in ? (((int64_t)u.start + (u.row + r) / group) * p.hq + u.h * group + (u.row + r) % group) * D + 8 * c : 0);
+        const int64_t at = __shfl_sync(0xffffffffu, my_at, r);
+        const __nv_bfloat16* src = p.q + (in ? at * D + 8 * c : 0);
         const uint32_t dst = smem_u32(smem + L::kQ + ((n % kUnits) * L::kRows + r) * D * 2 + 16 * c);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
       }
@@ -366,6 +369,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         __syncwarp();
       }
+      // (read by the compute warps from the next unit's start on)
+      if (lane == 0 && t1 - t0 < u.tiles) {
+        const int2 c = cached_owners<true>(u, sh, t0, t1);
+        x.owner = c.x;
+        x.pieces = c.y;
+        reinterpret_cast<StepPiece*>(smem + L::kSplits)[t0 == 0 ? 1 : 0] = x;
+      }
     }
     // nothing may land after the CTA has left (reached early only when a wait ran out)
     for (uint32_t x = ring > L::kStages ? ring - L::kStages : 0; x < ring; ++x)
@@ -390,6 +400,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     at_v[k] = L::kTileBytes + key0 * L::kBoxBytes + swz_offset(2 * q + k, kWords >= 4 ? 16 * g : 8 * g, L::kBoxBytes);
+  // (g's words lie 64 bytes apart with D = 128 codes, 32 otherwise)
+  auto turn = [](int row) { return E4M3 && D == 128 ? row >> 1 & 3 : (row >> 1 & 1) | (row >> 2 & 1) << 2; };
   StepPiece* splits = reinterpret_cast<StepPiece*>(smem + L::kSplits);
   int pending = -1;
   for (int n = 0; ok; ++n) {
@@ -443,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int row = 8 * t + 2 * q + r;
-        pos[t][r] = u.pos0 + (u.row + (row < u.rows ? row : 0)) / group;
+        pos[t][r] = u.pos0 + token_of(u.row + (row < u.rows ? row : 0));
       }
     }
     if constexpr (kShared) {
@@ -486,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         o[d][t][3] *= f1;
       }
     };
-    const int all_see = u.pos0 + u.row / group + 1 - kStepTile;          // tiles up to this key hide none behind a row's position
-    const int window = p.left < 0 ? -1 : u.pos0 + (u.row + u.rows - 1) / group - p.left;    // tiles from this key on none before one
+    const int all_see = u.pos0 + token_of(u.row) + 1 - kStepTile;          // tiles up to this key hide none behind a row's position
+    const int window = p.left < 0 ? -1 : u.pos0 + token_of(u.row + u.rows - 1) - p.left;    // tiles from this key on none before one
     for (int tile = u.t0; tile < u.t1; ++tile, ++ring) {
       if ((ring & 1) != (uint32_t)pair) continue;
       const uint32_t st = ring % L::kStages;
@@ -771,11 +783,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (row >= u.rows) continue;
         // (values in units of 2^(M - 13) against m; in two factors, of which neither falls below fp32's range)
         const float to = !E4M3 || M[t][r] == -INFINITY ? 1.f : fast_exp2(M[t][r]), by = E4M3 ? exp2i(-(int)kBoost) : 1.f;
-        // head dimensions (D / 8) g + 2 d and + 1 of product tile d; bf16: of each half of the row's 8 g + 2 (d mod 4)
+        // head dimensions (D / 8) g + 2 d and + 1 of product tile d; bf16: of each half of the row's 8 g + 2 (d mod 4).
+        // In words of 16 bytes whose places turn with the row, so that eight lanes (two g, four q) take all banks
         float* dst = red + (warp * L::kRows + row) * D;
 #pragma unroll
         for (int d = 0; d < kOut; d += 2)
-          *reinterpret_cast<float4*>(dst + (E4M3 ? (D / 8) * g + 2 * d : (d >> 2) * 64 + 8 * g + 2 * (d & 3))) =
+          *reinterpret_cast<float4*>(dst + 4 * (((E4M3 ? (D / 8) * g + 2 * d : (d >> 2) * 64 + 8 * g + 2 * (d & 3)) >> 2) ^ turn(row))) =
               make_float4(o[d][t][r] * by * to, o[d][t][2 + r] * by * to, o[d + 1][t][r] * by * to, o[d + 1][t][2 + r] * by * to);
       }
     ok = named_bar_and(1, kComputeWarps * 32, ok);
@@ -792,14 +805,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int w = 0; w < kComputeWarps; ++w) top = fmaxf(top, stat[w * 2 * L::kRows + r]);
 #pragma unroll
       for (int w = 0; w < kComputeWarps; ++w) {
-        const float4 z = *reinterpret_cast<const float4*>(red + (w * L::kRows + r) * D + 4 * c);
+        const float4 z = *reinterpret_cast<const float4*>(red + (w * L::kRows + r) * D + 4 * (c ^ turn(r)));
         const float mw = stat[w * 2 * L::kRows + r], f = mw == top ? 1.f : fast_exp2(mw - top);     // (a warp that saw nothing: 0)
         sum = make_float4(fmaf(z.x, f, sum.x), fmaf(z.y, f, sum.y), fmaf(z.z, f, sum.z), fmaf(z.w, f, sum.w));
         tot = fmaf(stat[w * 2 * L::kRows + L::kRows + r], f, tot);
       }
       if (whole) {
-        const int64_t tok = u.start + (u.row + r) / group;
-        const int h = u.h * group + (u.row + r) % group;
+        const int t = token_of(u.row + r), h = u.h * group + u.row + r - t * group;
+        const int64_t tok = u.start + t;
         const float inv = 1.f / tot;
         *reinterpret_cast<uint2*>(p.out + (tok * p.hq + h) * D + 4 * c) =
             make_uint2(pack2<false>(sum.x * inv, sum.y * inv), pack2<false>(sum.z * inv, sum.w * inv));
