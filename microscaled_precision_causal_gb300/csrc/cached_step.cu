@@ -6,10 +6,10 @@
 // the key tiles (64 keys, K and V) through shared memory: one warp issues TMA copies page by page, two compute
 // warps take every other tile each, 32 keys a warp with a softmax of its own, and meet only where a unit ends.
 // Two CTAs an SM, so that one streams while the other meets, with some 128 KB in flight between them.
-// Measured, 32 heads on 8, d 128, E4M3: a token each over 2 x 131972 keys 91 us, 6.0 TB/s (88% of a copy's rate); over 64
+// Measured, 32 heads on 8, d 128, E4M3: a token each over 2 x 131972 keys 90 us, 6.0 TB/s (89% of a copy's rate); over 64
 // sequences of 251670 keys in pages of 16 99 us (a page is a TMA copy of 2 KB, whose rate bounds it; 91 with pages of 64).
 // bf16, 16 heads, a window of 2048 of 32 sequences: 89 us, 5.7 TB/s.  With two row tiles (16 drafts of 4 tokens, 32 heads on 4,
-// 52000 keys: 37 us) the products and the softmax bound it, 0.85 us a key tile.
+// 52000 keys: 36 us) the products and the softmax bound it, 0.85 us a key tile.
 //
 // The products run as 16 x 8 x 16 MMAs from registers, keys (then head dimensions) as the 16 and query rows as the 8:
 // what is to be fast here is the stream, not the products, and a step's rows rarely fill more (tcgen05 would
