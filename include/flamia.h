@@ -472,8 +472,9 @@ int flamia_relbias_reduce(const float* drel_bias, int rel_max, int num_buckets, 
  *     rounded to nearest even.  A later token changes no earlier one's code.  A
  *     row that holds a NaN gets byte 255 and reads as NaN; infinities read as
  *     infinities (the row's finite values as 0, or as the multiples of 2^111
- *     that are left).  Codes 0x7f and 0xff are not
- *     written and not expected.
+ *     that are left), and so do values from 248 2^120 = 3.3e38 on, which round
+ *     to a code of 2^128: a code times its scale from there on is an infinity to
+ *     the attention too.  Codes 0x7f and 0xff are not written and not expected.
  *   FLAMIA_CACHE_BF16  the values as they are.
  *
  * A call serves sequences that each bring c_n = cu_seqlens[n + 1] -
@@ -545,7 +546,8 @@ int flamia_cache_read(const flamia_kv_cache* cache, const int32_t* page_table, i
  * the GPU, and with that the last bits of its rows, depends on the call's other
  * sequences.  A non-finite key or value of a visible or hidden position of the
  * sequence shows in rows of its own sequence only.  Scores have to stay finite in
- * fp32. */
+ * fp32, and so do the values' sums with weights of up to 2^8 times exp(t_ij -
+ * max_j t_ij): O of finite values past some 2^119 may come out infinite. */
 size_t flamia_cached_fwd_workspace_bytes(int hq, int hkv, int head_dim, int max_chunk);
 int flamia_cached_fwd(const void* q_bf16, const flamia_kv_cache* cache, const int32_t* page_table, int max_pages,
                       int num_seqs, int64_t total_tokens, int hq, int max_chunk, int window_left, float softcap,

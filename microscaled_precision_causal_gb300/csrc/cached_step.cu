@@ -25,7 +25,9 @@
 // score.  The value's scale 2^e enters the weight: w = 2^(x - m + e - M + 13) with a running maximum M of x - m + e
 // of its own (against m, so that scores of any size leave the exponents their digits): the largest w is in
 // [2^13, 2^15] whatever the scales are, and what falls below fp16's range is 2^-38 of it.  Rounding w
-// to fp16 costs 2^-12 of it at most.
+// to fp16 costs 2^-12 of it at most.  An infinity is a code whose scale takes it past fp32's range, which neither product
+// sees: tiles with scales that large (some 2^120) add their infinities besides, to the scores and to O.  The others
+// pay for that code's registers: 33.5 -> 34.3 us with two row tiles (the drafts below, in a graph), 88.0 -> 88.2 with one.
 // bf16: the products run in bf16, and so do the weights (2^-9 at most).
 #include <type_traits>
 
@@ -77,6 +79,12 @@ __device__ __forceinline__ uint32_t codes_f16_hi(uint32_t c) {
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(c));
   return r;
 }
+// A code times its scale 2^(b - 127) is past fp32's (and bf16's) range from 2^(255 - b) on: an infinity, as reading the cache and
+// the chunks have it.  The products have the code alone and cannot see that.  The least such code's magnitude; none for
+// b < 247 (448 2^119 is finite) and 255 (a NaN's row).
+constexpr uint32_t kNoInfinity = 128;
+__device__ __forceinline__ uint32_t infinite_from(uint32_t b) { return b < 247 || b == 255 ? kNoInfinity : (262 - b) << 3; }
+__device__ __forceinline__ float signed_infinity(uint32_t code) { return __uint_as_float(0x7f800000u | (code & 128) << 24); }
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (F16) {
@@ -582,9 +590,9 @@ __global__ void __launch_bounds__(kThreads, 2)
               if (key >= u.keys || key < u.lo) k[i][h] = 1.f, e[i][h] = 0.f;
             }
           }
-        // byte 255: infinite, and 128
-        if (__any_sync(0xffffffffu, fmaxf(fmax3(k[0][0], k[0][1], k[1][0]), k[1][1]) == INFINITY ||
-                                        fmaxf(fmax3(e[0][0], e[0][1], e[1][0]), e[1][1]) > 127.5f)) {
+        // byte 255: infinite, and 128; infinities have 247 or more
+        if (__any_sync(0xffffffffu, fmaxf(fmax3(k[0][0], k[0][1], k[1][0]), k[1][1]) >= 0x1p120f ||
+                                        fmaxf(fmax3(e[0][0], e[0][1], e[1][0]), e[1][1]) > 119.5f)) {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -592,6 +600,66 @@ __global__ void __launch_bounds__(kThreads, 2)
               if (k[i][h] == INFINITY) k[i][h] = NAN;
               if (e[i][h] > 127.5f) e[i][h] = NAN;
             }
+          // Infinities, a row of the cache at a time.  A row of values that is nothing but them and zeros then needs no weight: its
+          // scale must not cost the others theirs
+          uint32_t pure = 0;
+#pragma unroll 1
+          for (int n = 0; n < 32; ++n) {
+            const int key = c0 + key0 + n;
+            const uint32_t from_k = infinite_from(stage[L::kScales + key0 + n]), from_v = infinite_from(stage[L::kScales + kStepTile + key0 + n]);
+            if ((from_k & from_v) == kNoInfinity || key >= u.keys || key < u.lo) continue;
+            if (from_k != kNoInfinity) {        // products of row 8 t + g, then on top of the scores of rows 8 t + 2 q and + 1
+              float sum[NT] = {};
+#pragma unroll (kShared ? 1 : kSteps)
+              for (int s = 0; s < kSteps; ++s) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + key0 * L::kBoxBytes + swz_offset(n, (D / 4) * q + 4 * s, L::kBoxBytes));
+                uint32_t y[NT][2];
+                operand(s, y);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t c = w >> 8 * j & 255;
+#pragma unroll
+                  for (int t = 0; t < NT; ++t)
+                    if ((c & 127) >= from_k) sum[t] += signed_infinity(c) * __half2float(__ushort_as_half((unsigned short)(y[t][j >> 1] >> 16 * (j & 1))));
+                }
+              }
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], 1);
+                sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], 2);
+                const float s0 = __shfl_sync(0xffffffffu, sum[t], 8 * q), s1 = __shfl_sync(0xffffffffu, sum[t], 8 * q + 4);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    if (n == 16 * i + 8 * h + g) x[i][h][t] = make_float2(x[i][h][t].x + s0, x[i][h][t].y + s1);
+              }
+            }
+            if (from_v == kNoInfinity) continue;
+            const uint8_t* row = stage + L::kTileBytes + key0 * L::kBoxBytes + swz_offset(n, 4 * kWords * g, L::kBoxBytes);
+            bool sees[NT][2], finite = false;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) sees[t][r] = key <= pos[t][r] && !(p.left >= 0 && key < pos[t][r] - p.left);
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+              const uint32_t c = row[d];
+              const bool infinite = (c & 127) >= from_v;
+              finite = finite || (!infinite && (c & 127));
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                  if (infinite && sees[t][r]) o[d / 2][t][2 * (d & 1) + r] += signed_infinity(c);
+            }
+            if (!__any_sync(0xffffffffu, finite) && (n & 7) == g) pure |= 1u << (n >> 3);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (pure >> (2 * i + h) & 1) e[i][h] = -INFINITY;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -683,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const float M1 = fmaxf(M[t][r], reduce(mx[t][r]));
-              f[r] = fast_exp2(M1 == M[t][r] ? 0.f : M[t][r] - M1);
+              f[r] = fast_exp2(M1 == M[t][r] || M[t][r] == -INFINITY ? 0.f : M[t][r] - M1);      // (so far zeros, or infinities)
               M[t][r] = M1;
             }
             Neg[t] = make_float2(M[t][0] == -INFINITY ? 0.f : kBoost - M[t][0], M[t][1] == -INFINITY ? 0.f : kBoost - M[t][1]);

@@ -691,3 +691,106 @@ def test_generation_over_two_layers(F, fmt):
             ref = C.attend(f64(x["q"][i][s, :L]), f64(k[at:at + L]), f64(v[at:at + L]), hq // hkv)
             at += L
             assert (np.abs(outs[i][s] - ref["o"]) <= ref["tol_o"]).all() and (np.abs(lses[i][s] - ref["lse"]) <= ref["tol_lse"]).all()
+
+
+# ------------------------------------------------------------------ infinities of an E4M3 cache
+
+def _as_read(pool):
+    """The cache's values as reading gives them: a code times its scale past bf16's range is an infinity."""
+    import torch
+    return f64(torch.from_numpy(pool).to(torch.bfloat16))
+
+
+ROWS = {"steps": [1, 4, 1], "two_row_tiles": [1, 8, 1], "chunks": [1, 60, 1]}        # (of four heads on one)
+
+
+@BOTH
+@DIMS
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), 3.35e38])
+def test_an_infinite_key(F, value, softcap, rows, d, fmt):
+    """Scores +inf: nothing finite in the row.  Scores -inf: the key has no weight.  Capped: the cap."""
+    import torch
+    if fmt == "bf16" and abs(value) < float("inf"):
+        pytest.skip("finite there")
+    chunks = ROWS[rows]
+    b = Batch(F, chunks, [70, 200, 300], 8, 2, d, fmt, 16, seed=35, softcap=softcap)
+    a, big = 5, 40 * softcap * np.sqrt(d)       # (in its place: scores beyond 20 caps, tanh 1 in any precision)
+    sign = torch.from_numpy(np.random.default_rng(36).choice([-1.0, 1.0], (b.T, 8))).cuda()
+    b.q[:, :, a] = (sign * (0.5 + b.q[:, :, a].double().abs().clamp(max=1.5))).to(torch.bfloat16)
+    row = 1                                     # the second sequence's first new token, kv head 1
+    b.k[row, 1, a] = value
+    b.att.write(b.cache, b.k, b.v, b.table)
+    out, lse = b.forward()
+    assert b.att.device_status() == 0
+    keys, vals, q, at = [_as_read(x) for x in b.rows("k")], b.rows("v"), f64(b.q), 0
+    assert np.isinf(keys[1][200, 1, a]) and np.isfinite(keys[1]).sum() == keys[1].size - 1
+    up = f64(sign)[1:1 + chunks[1]] * np.sign(value) > 0
+    for n, c in enumerate(chunks):
+        o, l = f64(out[at:at + c]), f64(lse[:, at:at + c])
+        for h in range(8):
+            g, one = h // 4, q[at:at + c, h:h + 1]
+            K, V = keys[n][:, g:g + 1], vals[n][:, g:g + 1]
+            if n == 1 and g == 1:
+                K = np.where(np.isinf(K), np.sign(K) * big, K)
+            full = C.attend(one, K, V, 1, softcap=softcap)
+            if n == 1 and g == 1 and not softcap:
+                bad = up[:, h]
+                assert not np.isfinite(o[bad, h]).any() and not np.isfinite(l[h, bad]).any(), h
+                # the others: as without the key
+                keep = np.arange(len(K)) != 200
+                for t in np.nonzero(~bad)[0]:
+                    if t == 0 and keep[:201].sum() == 0:
+                        continue
+                    x = C.attend(one[t:t + 1], K[keep][:200 + t], V[keep][:200 + t], 1)
+                    assert (np.abs(o[t, h] - x["o"][0, 0]) <= x["tol_o"][0, 0]).all() and abs(l[h, t] - x["lse"][0, 0]) <= x["tol_lse"][0, 0]
+            else:
+                assert (np.abs(o[:, h] - full["o"][:, 0]) <= full["tol_o"][:, 0]).all(), (n, h)
+                assert (np.abs(l[h] - full["lse"][0]) <= full["tol_lse"][0]).all(), (n, h)
+        at += c
+
+
+@BOTH
+@DIMS
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), 3.35e38, 3.1e38])
+def test_an_infinite_value(F, value, softcap, rows, d, fmt):
+    """It shows in its head dimension of every row that sees it, however small its weight; the largest finite code does not."""
+    import torch
+    if fmt == "bf16" and abs(value) < float("inf"):
+        pytest.skip("finite there")
+    chunks = ROWS[rows]
+    b = Batch(F, chunks, [70, 200, 300], 8, 2, d, fmt, 16, seed=37, softcap=softcap, gain=0.5)
+    a, row = 9, 1
+    b.k[row, 1] = -b.q[row, 4:8].float().mean(0).sign().to(torch.bfloat16)      # a small weight for its own token's heads
+    b.v[row, 1, a] = value
+    b.att.write(b.cache, b.k, b.v, b.table)
+    out, lse = b.forward()
+    assert b.att.device_status() == 0
+    keys, vals, q, at = b.rows("k"), [_as_read(x) for x in b.rows("v")], f64(b.q), 0
+    shows = value != 3.1e38
+    assert np.isinf(vals[1]).sum() == shows
+    some = shows
+    for n, c in enumerate(chunks):
+        o, l = f64(out[at:at + c]), f64(lse[:, at:at + c])
+        for h in range(8):
+            g = h // 4
+            V = vals[n][:, g:g + 1]
+            ref = C.attend(q[at:at + c, h:h + 1], keys[n][:, g:g + 1], np.where(np.isinf(V), 0.0, V), 1, softcap=softcap)
+            sure = np.ones((c, d), bool)
+            if n == 1 and g == 1 and shows:
+                assert not np.isfinite(o[:, h, a]).any(), h
+                sure[:, a] = False
+            elif n == 1 and g == 1:
+                # finite where sums with weights of up to 2^8 times exp(t - the row's largest t) are (the header)
+                u = q[at:at + c, h] @ keys[n][:, g].T / np.sqrt(d)
+                u = softcap * np.tanh(u / softcap) if softcap else u
+                u = np.where(np.arange(len(V)) > np.arange(200, 200 + c)[:, None], -np.inf, u)
+                sure[:, a] = 2.0 ** 8 * np.exp(u - u.max(1, keepdims=True)) @ np.abs(V[:, 0, a]) < 2.0 ** 128
+                some |= sure[:, a].any()
+            assert ((np.abs(o[:, h] - ref["o"][:, 0]) <= ref["tol_o"][:, 0]) | ~sure).all(), (n, h)
+            assert (np.abs(l[h] - ref["lse"][0]) <= ref["tol_lse"][0]).all(), (n, h)
+        at += c
+    assert some or softcap                      # (capped at 5, every row's weights are too near one another)
