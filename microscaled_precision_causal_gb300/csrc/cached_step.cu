@@ -849,8 +849,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int r = 0; r < 2; ++r) {
         const int row = 8 * t + 2 * q + r;
         if (row >= u.rows) continue;
-        // (values in units of 2^(M - 13) against m; in two factors, of which neither falls below fp32's range)
-        const float to = !E4M3 || M[t][r] == -INFINITY ? 1.f : fast_exp2(M[t][r]), by = E4M3 ? exp2i(-(int)kBoost) : 1.f;
+        // values in units of 2^(M - 13) against m, M from some -130 to 130: in two factors that both stay within fp32's range
+        // (fast_exp2 gives 0 below 2^-126), the first one far from where the values would leave it
+        const float toward = M[t][r] < -64.f ? 64.f : M[t][r] > 64.f ? -64.f : 0.f;
+        const float to = !E4M3 || M[t][r] == -INFINITY ? 1.f : fast_exp2(M[t][r] + toward), by = E4M3 ? exp2i(-(int)(kBoost + toward)) : 1.f;
         // head dimensions (D / 8) g + 2 d and + 1 of product tile d; bf16: of each half of the row's 8 g + 2 (d mod 4).
         // In words of 16 bytes whose places turn with the row, so that eight lanes (two g, four q) take all banks
         float* dst = red + (warp * L::kRows + row) * D;

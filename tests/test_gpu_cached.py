@@ -794,3 +794,15 @@ def test_an_infinite_value(F, value, softcap, rows, d, fmt):
             assert (np.abs(l[h] - ref["lse"][0]) <= ref["tol_lse"][0]).all(), (n, h)
         at += c
     assert some or softcap                      # (capped at 5, every row's weights are too near one another)
+
+
+@DIMS
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("exponent", [-123, -121, -119, -117])
+@pytest.mark.parametrize("gain", [0.2, 4.0])
+def test_values_of_the_least_scales(F, gain, exponent, rows, d):
+    """Scale bytes 0 to some 5, with maxima that rise by less and by more than the slack of the weights' reference."""
+    b = Batch(F, ROWS[rows], [600, 300, 200], 8, 2, d, "e4m3", 16, seed=38, gain=gain)
+    b.fill("v", bf16(np.random.default_rng(39), *b.cache.v.shape, gain=2.0 ** exponent))
+    assert max(0, exponent + 119) <= b.cache.v_scales.min() <= max(0, exponent + 120)
+    b.check()
