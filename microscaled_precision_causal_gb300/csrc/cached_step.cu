@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int h = 0; h < 2; ++h) {
               x[i][h][t] = make_float2(s[i][0][t][2 * h], s[i][0][t][2 * h + 1]);
               if constexpr (kChains == 2) x[i][h][t] = fadd2(x[i][h][t], make_float2(s[i][1][t][2 * h], s[i][1][t][2 * h + 1]));
-              x[i][h][t] = fmul2(x[i][h][t], rowf[t]);
+              if constexpr (!E4M3) x[i][h][t] = fmul2(x[i][h][t], rowf[t]);
             }
       }
       float e[2][2];           // exponents of the values' scales
@@ -582,8 +582,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint8_t* sc = stage + L::kScales + key0 + 16 * i + 8 * h + g;
-            // 2^(byte - 127), but 0 for byte 0: a score that counts is beyond 2^-90
-            k[i][h] = __uint_as_float((uint32_t)sc[0] << 23);
+            k[i][h] = __uint_as_float(max((uint32_t)sc[0] << 23, 0x00400000u));       // 2^(byte - 127)
             e[i][h] = __uint_as_float(0x4b000000u | sc[kStepTile]) - 8388735.f;       // (2^23 + byte by its bits) - 2^23 - 127
             if (edge) {
               const int key = c0 + key0 + 16 * i + 8 * h + g;
@@ -666,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) x[i][h][t] = fmul2(x[i][h][t], make_float2(k[i][h], k[i][h]));
+            for (int t = 0; t < NT; ++t)           // (the scales first: with either alone a product may leave fp32's range)
+              x[i][h][t] = fmul2(x[i][h][t], fmul2(rowf[t], make_float2(k[i][h], k[i][h])));
       }
       if constexpr (CAP) {
 #pragma unroll

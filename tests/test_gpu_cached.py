@@ -806,3 +806,17 @@ def test_values_of_the_least_scales(F, gain, exponent, rows, d):
     b.fill("v", bf16(np.random.default_rng(39), *b.cache.v.shape, gain=2.0 ** exponent))
     assert max(0, exponent + 119) <= b.cache.v_scales.min() <= max(0, exponent + 120)
     b.check()
+
+
+@DIMS
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("queries,keys", [(118, -122), (119, -118), (110, -110), (-110, 110), (-118, 118)])
+@pytest.mark.parametrize("softcap", [0.0, 5.0])
+def test_queries_and_keys_of_opposite_size(F, softcap, queries, keys, rows, d):
+    """Scores of some units from queries and keys at either end of their type's range, a key's scale byte of 0 among them."""
+    b = Batch(F, ROWS[rows], [600, 300, 200], 8, 2, d, "e4m3", 16, seed=40, softcap=softcap, scale=2.0 ** -(queries + keys) / np.sqrt(d))
+    rng = np.random.default_rng(41)
+    b.q.copy_(bf16(rng, *b.q.shape, gain=2.0 ** queries))
+    b.fill("k", bf16(rng, *b.cache.k.shape, gain=2.0 ** keys))
+    assert (b.cache.k_scales == 0).any() or keys != -122
+    b.check()
