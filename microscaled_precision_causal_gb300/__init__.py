@@ -649,13 +649,47 @@ def _cuda_device(device):
     return device
 
 
+class _Kept:
+    """A tensor whose address an object's calls keep.  Another one takes its place by assignment, and the calls go there from
+    then on: contiguous, of the same type, shape and device, aligned to `align` bytes.  Anything else raises FlamiaError."""
+
+    def __init__(self, align: int = 16):
+        self.align = align
+
+    def __set_name__(self, owner, name):
+        self.name = name
+
+    def __get__(self, obj, owner=None):
+        return self if obj is None else obj.__dict__["_" + self.name]
+
+    def __set__(self, obj, t):
+        old = obj.__dict__.get("_" + self.name, t)
+        if t is not old:
+            if old is None or t is None:
+                raise FlamiaError(f"{self.name}: {'there is none in this format' if old is None else 'want a tensor'}")
+            if (t.dtype != old.dtype or t.shape != old.shape or t.device != old.device or not t.is_contiguous()
+                    or t.data_ptr() % self.align):
+                raise FlamiaError(f"{self.name}: want contiguous {old.dtype} {tuple(old.shape)} on {old.device}, aligned to "
+                                  f"{self.align} bytes, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                                  f"{'' if t.is_contiguous() else ', not contiguous'}")
+        obj.__dict__["_" + self.name] = t
+        obj._moved(self.name, t)
+
+
 class FlamiaPagedCache:
     """The pages of one layer's keys and values.
 
     k and v are [num_pages, hkv, page_size, head_dim], uint8 E4M3 codes with
     k_scales and v_scales [num_pages, hkv, page_size] (uint8 UE8M0 exponents, one
     a token and head) for fmt "e4m3", bf16 and no scales for "bf16".  They start
-    as zeros.  Which page holds which positions is the caller's page table."""
+    as zeros.  Which page holds which positions is the caller's page table.
+
+    The calls go to these tensors' memory.  Contents are replaced with copy_, or by
+    assigning another tensor of the same kind; a captured graph stays with the one
+    that it was captured with.  Changes of a tensor's own memory (set_, resize_,
+    .data) are not followed."""
+
+    k, v, k_scales, v_scales = _Kept(), _Kept(), _Kept(), _Kept()
 
     def __init__(self, num_pages: int, page_size: int, hkv: int, head_dim: int, fmt: str = "e4m3", device="cuda"):
         import torch
@@ -663,18 +697,20 @@ class FlamiaPagedCache:
             raise FlamiaError(f"FlamiaPagedCache: {(num_pages, page_size, hkv, head_dim, fmt)} is not supported")
         self.num_pages, self.page_size, self.hkv, self.d, self.fmt = num_pages, page_size, hkv, head_dim, fmt
         self.device = _cuda_device(device)
-        self.k_scales = self.v_scales = None
+        # what the calls get
+        self.view = KVCache(None, None, None, None, num_pages, page_size, hkv, head_dim, CACHE_FORMATS[fmt])
+        self.ref = ctypes.pointer(self.view)
         shape = (num_pages, hkv, page_size, head_dim)
         if fmt == "e4m3":
             self.k, self.v = (torch.zeros(shape, dtype=torch.uint8, device=self.device) for _ in range(2))
             self.k_scales, self.v_scales = (torch.zeros(shape[:3], dtype=torch.uint8, device=self.device) for _ in range(2))
         else:
             self.k, self.v = (torch.zeros(shape, dtype=torch.bfloat16, device=self.device) for _ in range(2))
-        # (what the calls get: the tensors above stay the pages for the object's life)
-        self.view = KVCache(_ptr(self.k), _ptr(self.v), _ptr(self.k_scales), _ptr(self.v_scales), num_pages, page_size,
-                            hkv, head_dim, CACHE_FORMATS[fmt])
-        self.ref = ctypes.pointer(self.view)
+            self.k_scales = self.v_scales = None
         self.kind = (page_size, hkv, head_dim, self.device)
+
+    def _moved(self, name, t):
+        setattr(self.view, name, _ptr(t))
 
 
 class FlamiaCachedAttention:

@@ -177,3 +177,30 @@ def test_object_refusals(F):
         for a, b in ((k.float(), k), (k, z(10, 4, 64)), (k, z(2, 10, 64).transpose(0, 1))):
             with pytest.raises(F.FlamiaError, match="want"):
                 f(a, b)
+
+
+def test_pages_are_replaced_by_tensors_of_their_kind_only(F):
+    """The calls' addresses follow an assignment; what does not fit is refused and changes nothing."""
+    torch = pytest.importorskip("torch")
+    for fmt, dtype, names in (("e4m3", torch.uint8, ("k", "v", "k_scales", "v_scales")), ("bf16", torch.bfloat16, ("k", "v"))):
+        c = F.FlamiaPagedCache(4, 16, 2, 64, fmt, device="cpu")
+        shapes = {"k": (4, 2, 16, 64), "v": (4, 2, 16, 64), "k_scales": (4, 2, 16), "v_scales": (4, 2, 16)}
+        for n in names:
+            old = getattr(c, n)
+            odd = torch.zeros(old.numel() + 1, dtype=dtype)[1:].view(old.shape)
+            for bad in (torch.zeros(shapes[n], dtype=torch.float32), torch.zeros(5, *shapes[n][1:], dtype=dtype), odd, None,
+                        torch.zeros(shapes[n], dtype=dtype).transpose(0, 1).contiguous().transpose(0, 1),
+                        torch.zeros(shapes[n], dtype=dtype, device="meta")):
+                with pytest.raises(F.FlamiaError, match=n + ": want"):
+                    setattr(c, n, bad)
+                assert getattr(c, n) is old and getattr(c.view, n) == old.data_ptr()
+            new = torch.ones_like(old)
+            setattr(c, n, new)
+            assert getattr(c, n) is new and getattr(c.view, n) == new.data_ptr() == getattr(c.ref.contents, n)
+            c.k += 1                                                  # (in place: the same tensor assigned)
+            assert c.view.k == c.k.data_ptr()
+        if fmt == "bf16":
+            c.k_scales = None
+            assert c.view.k_scales is None
+            with pytest.raises(F.FlamiaError, match="k_scales: there is none"):
+                c.k_scales = torch.zeros(4, 2, 16, dtype=torch.uint8)

@@ -820,3 +820,28 @@ def test_queries_and_keys_of_opposite_size(F, softcap, queries, keys, rows, d):
     b.fill("k", bf16(rng, *b.cache.k.shape, gain=2.0 ** keys))
     assert (b.cache.k_scales == 0).any() or keys != -122
     b.check()
+
+
+# ------------------------------------------------------------------ tensors that take another's place
+
+@BOTH
+def test_restored_pages(F, fmt):
+    """Pages assigned anew are what the calls read and write from then on, and the old ones' memory is left alone."""
+    import torch
+    b = Batch(F, [1, 40], [60, 100], 4, 2, 64, fmt, 16, seed=42)
+    want = [t.clone() for t in b.check()]
+    names = ["k", "v"] + (["k_scales", "v_scales"] if fmt == "e4m3" else [])
+    old = {n: getattr(b.cache, n) for n in names}
+    for n in names:
+        setattr(b.cache, n, old[n].clone())
+        old[n].fill_(7)
+    assert all(torch.equal(x, y) for x, y in zip(b.forward(), want))
+    b.att.write(b.cache, b.k, b.v, b.table)
+    torch.cuda.synchronize()
+    assert all((old[n] == 7).all() for n in names)
+    k, v = b.att.read(b.cache, b.table, torch.empty_like(b.k), torch.empty_like(b.v))
+    at = b.places()
+    for name, got in (("k", k), ("v", v)):
+        assert np.array_equal(f64(got), b.pool(name)[at[:, 0], :, at[:, 1]])
+    with pytest.raises(F.FlamiaError, match="k: want"):
+        b.cache.k = b.cache.k.cpu()
