@@ -20,6 +20,7 @@ them; ``FlamiaPagedCache`` holds the pages, ``FlamiaCachedAttention`` a step's c
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Optional
 
@@ -649,31 +650,25 @@ def _cuda_device(device):
     return device
 
 
-class _Kept:
-    """A tensor whose address an object's calls keep.  Another one takes its place by assignment, and the calls go there from
+def _kept(name: str, align: int = 16):
+    """A tensor that an object's calls read or write.  Another one takes its place by assignment, and the calls go there from
     then on: contiguous, of the same type, shape and device, aligned to `align` bytes.  Anything else raises FlamiaError."""
+    slot = "_" + name
 
-    def __init__(self, align: int = 16):
-        self.align = align
-
-    def __set_name__(self, owner, name):
-        self.name = name
-
-    def __get__(self, obj, owner=None):
-        return self if obj is None else obj.__dict__["_" + self.name]
-
-    def __set__(self, obj, t):
-        old = obj.__dict__.get("_" + self.name, t)
+    def assign(self, t):
+        old = getattr(self, slot, t)
         if t is not old:
             if old is None or t is None:
-                raise FlamiaError(f"{self.name}: {'there is none in this format' if old is None else 'want a tensor'}")
+                raise FlamiaError(f"{name}: {'there is none in this format' if old is None else 'want a tensor'}")
             if (t.dtype != old.dtype or t.shape != old.shape or t.device != old.device or not t.is_contiguous()
-                    or t.data_ptr() % self.align):
-                raise FlamiaError(f"{self.name}: want contiguous {old.dtype} {tuple(old.shape)} on {old.device}, aligned to "
-                                  f"{self.align} bytes, got {t.dtype} {tuple(t.shape)} on {t.device}"
-                                  f"{'' if t.is_contiguous() else ', not contiguous'}")
-        obj.__dict__["_" + self.name] = t
-        obj._moved(self.name, t)
+                    or t.data_ptr() % align):
+                raise FlamiaError(f"{name}: want contiguous {old.dtype} {tuple(old.shape)} on {old.device}, aligned to {align} bytes, "
+                                  f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+        setattr(self, slot, t)
+        self._moved(name, t)
+
+    # (read as often as a step has calls: without a Python function)
+    return property(operator.attrgetter(slot), assign)
 
 
 class FlamiaPagedCache:
@@ -689,7 +684,7 @@ class FlamiaPagedCache:
     that it was captured with.  Changes of a tensor's own memory (set_, resize_,
     .data) are not followed."""
 
-    k, v, k_scales, v_scales = _Kept(), _Kept(), _Kept(), _Kept()
+    k, v, k_scales, v_scales = (_kept(name) for name in ("k", "v", "k_scales", "v_scales"))
 
     def __init__(self, num_pages: int, page_size: int, hkv: int, head_dim: int, fmt: str = "e4m3", device="cuda"):
         import torch
@@ -741,7 +736,10 @@ class FlamiaCachedAttention:
     allocated per call, so calls can be captured into a CUDA graph: a replay reads
     what the tensors hold by then.  Calls run on `stream`, by default the object's
     device's current stream; calls of one object share its plan, outputs and
-    workspace, so calls on two streams have to be ordered by the caller."""
+    workspace, so calls on two streams have to be ordered by the caller.  plan, out,
+    lse and workspace may be assigned as a cache's tensors may."""
+
+    plan, out, lse, workspace = _kept("plan"), _kept("out"), _kept("lse", 4), _kept("workspace", 256)
 
     def __init__(self, total_tokens: int, num_seqs: int, hq: int, hkv: int, head_dim: int, max_chunk: int,
                  max_pages: int, page_size: int, device="cuda", window: int = -1, softcap: float = 0.0):
@@ -764,7 +762,7 @@ class FlamiaCachedAttention:
         self._ws_bytes = flamia_cached_fwd_workspace_bytes(hq, hkv, head_dim, self.max_chunk)
         self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
         # a step's calls are many and small: what does not change is worked out once
-        self._lib, self._plan_ptr, self._bf16, self._i32 = lib(), self.plan.data_ptr(), torch.bfloat16, torch.int32
+        self._lib, self._bf16, self._i32 = lib(), torch.bfloat16, torch.int32
         self._index = dev.index if dev.type == "cuda" else None
         self._device_now, self._stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         self._kind = (page_size, hkv, head_dim, dev)
@@ -773,6 +771,9 @@ class FlamiaCachedAttention:
 
     _want = FlamiaScoredAttention._want
     _run = FlamiaScoredAttention._run
+
+    def _moved(self, name, t):
+        pass                           # (the calls ask the tensors)
 
     def _places(self, cache, page_table):
         if cache.kind != self._kind:
@@ -804,7 +805,7 @@ class FlamiaCachedAttention:
         self._want("k", k, self._kv_shape, self._bf16)
         self._want("v", v, self._kv_shape, self._bf16)
         self._call("flamia_cache_write", self._lib.flamia_cache_write, stream, cache.ref, page_table.data_ptr(), self.max_pages,
-                   self.N, self.T, self._plan_ptr, k.data_ptr(), v.data_ptr())
+                   self.N, self.T, self._plan.data_ptr(), k.data_ptr(), v.data_ptr())
 
     def read(self, cache: FlamiaPagedCache, page_table, k, v, stream=None):
         """The new tokens' keys and values from the cache into k and v, which are returned."""
@@ -812,17 +813,17 @@ class FlamiaCachedAttention:
         self._want("k", k, self._kv_shape, self._bf16)
         self._want("v", v, self._kv_shape, self._bf16)
         self._call("flamia_cache_read", self._lib.flamia_cache_read, stream, cache.ref, page_table.data_ptr(), self.max_pages,
-                   self.N, self.T, self._plan_ptr, k.data_ptr(), v.data_ptr())
+                   self.N, self.T, self._plan.data_ptr(), k.data_ptr(), v.data_ptr())
         return k, v
 
     def forward(self, cache: FlamiaPagedCache, q, page_table, softmax_scale: float = 0.0, stream=None):
         """(out bf16 [T, hq, d], lse fp32 [hq, T]) of the new tokens, whose keys and values have been written."""
         self._places(cache, page_table)
         self._want("q", q, self._q_shape, self._bf16)
-        out, lse = self.out, self.lse
+        out, lse = self._out, self._lse
         self._call("flamia_cached_fwd", self._lib.flamia_cached_fwd, stream, q.data_ptr(), cache.ref, page_table.data_ptr(),
                    self.max_pages, self.N, self.T, self.hq, self.max_chunk, self.window, self.softcap, softmax_scale,
-                   self._plan_ptr, out.data_ptr(), lse.data_ptr(), self.workspace.data_ptr(), self._ws_bytes)
+                   self._plan.data_ptr(), out.data_ptr(), lse.data_ptr(), self._workspace.data_ptr(), self._ws_bytes)
         return out, lse
 
     def device_status(self, stream=None) -> int:

@@ -204,3 +204,23 @@ def test_pages_are_replaced_by_tensors_of_their_kind_only(F):
             assert c.view.k_scales is None
             with pytest.raises(F.FlamiaError, match="k_scales: there is none"):
                 c.k_scales = torch.zeros(4, 2, 16, dtype=torch.uint8)
+
+
+def test_a_steps_buffers_are_replaced_by_their_kind_only(F):
+    torch = pytest.importorskip("torch")
+    att = F.FlamiaCachedAttention(10, 2, 4, 2, 64, max_chunk=8, max_pages=3, page_size=16, device="cpu")
+    for n, align in (("plan", 16), ("out", 16), ("lse", 4), ("workspace", 256)):
+        old = getattr(att, n)
+        bads = [old[1:].clone(), torch.zeros(old.shape, dtype=torch.float64), None]
+        if old.dtype == torch.uint8:
+            room = torch.zeros(old.numel() + 2 * align, dtype=torch.uint8)
+            off = -room.data_ptr() % align + align // 2
+            bads.append(room[off:off + old.numel()])                  # (half of the alignment that it wants)
+        for bad in bads:
+            with pytest.raises(F.FlamiaError, match=n + ": want"):
+                setattr(att, n, bad)
+            assert getattr(att, n) is old
+        room = torch.zeros(old.numel() * old.element_size() + 256, dtype=torch.uint8)
+        new = room[-room.data_ptr() % 256:][:old.numel() * old.element_size()].view(old.dtype).view(old.shape)
+        setattr(att, n, new)
+        assert getattr(att, n) is new

@@ -845,3 +845,22 @@ def test_restored_pages(F, fmt):
         assert np.array_equal(f64(got), b.pool(name)[at[:, 0], :, at[:, 1]])
     with pytest.raises(F.FlamiaError, match="k: want"):
         b.cache.k = b.cache.k.cpu()
+
+
+def test_plans_and_outputs_take_turns(F):
+    """A plan kept for later and outputs of their own for each layer, by assignment."""
+    import torch
+    b = Batch(F, [1, 40], [900, 100], 4, 2, 64, page=16, seed=43)
+    want = [t.clone() for t in b.check()]
+    mine, first = b.att.plan, b.att.out
+    other = torch.zeros_like(mine)
+    b.att.plan = other
+    b.att.plan_build(b.cu, torch.ones_like(b.kv_lens))                # bad: O 0
+    assert (b.forward()[0] == 0).all() and b.att.device_status() == F.DEV_BAD_KV_LENS
+    b.att.plan, b.att.out, b.att.lse = mine, torch.empty_like(b.att.out), torch.empty_like(b.att.lse)
+    b.att.workspace = torch.full_like(b.att.workspace, 255)
+    out, lse = b.forward()
+    assert out is b.att.out and torch.equal(out, want[0]) and torch.equal(lse, want[1]) and (first == 0).all()
+    assert b.att.device_status() == 0
+    with pytest.raises(F.FlamiaError, match="workspace: want"):
+        b.att.workspace = b.att.workspace[:-256]
