@@ -226,9 +226,8 @@ __global__ void __launch_bounds__(256) cache_rows_kernel(int N, int T, int hq, i
 // A warp takes the rows (of all heads) of some tokens, of K or of V: a stream on the packed side.  16 elements a lane, so that
 // what a row needs once (its largest value, its scale, its place) is shared by few lanes: with 8 the
 // instructions bound it (write of 16384 tokens, 16 heads, d 128: 48 instead of 38 us, 70% of the issue slots).
-// 32 rows a warp: 35 us, and 37 for the read of 4 x 8192 of 8 heads; with 64 or 128 rows 38 and 36, 38 and 44.
-// What is quantized is read once: loads that say so leave L2 to the codes (34.3 -> 32.4 us, 6.2 TB/s; streaming
-// stores besides 31.1, but the attention reads the codes next; of bf16 43.5 -> 44.9; the read's 37.0 either way).
+// 32 rows a warp: 34.3 us, 5.9 TB/s (87% of a copy's rate), and 37 for the read of 4 x 8192 of 8 heads; with 64 or 128 rows
+// 38 and 36, 38 and 44.  With loads that are marked as streaming the write takes 36.8 in a row of calls.
 // Where the tokens live it looks up once, a lane a token.
 constexpr int kWarps = 8;
 constexpr int kRowsPerWarp = 32;
@@ -277,8 +276,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_kernel(const CachePar
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int r = r0 + u * R::kPer + sub;
-        const uint4* from = src + r * (D / 8) + j * R::kLanes;
-        x[u][j] = r >= rows ? make_uint4(0, 0, 0, 0) : E4M3 ? __ldcs(from) : *from;
+        x[u][j] = r < rows ? src[r * (D / 8) + j * R::kLanes] : make_uint4(0, 0, 0, 0);
       }
     if (places == -2) places = token_place(p, g, lane, cache_valid_rows(p));     // (while the first loads fly)
 #pragma unroll
