@@ -6,7 +6,7 @@
 // the key tiles (64 keys, K and V) through shared memory: one warp issues TMA copies page by page, two compute
 // warps take every other tile each, 32 keys a warp with a softmax of its own, and meet only where a unit ends.
 // Two CTAs an SM, so that one streams while the other meets, with some 128 KB in flight between them.
-// Measured, 32 heads on 8, d 128, E4M3: a token each over 2 x 131972 keys 90 us, 6.0 TB/s (89% of a copy's rate); over 64
+// Measured, 32 heads on 8, d 128, E4M3: a token each over 2 x 131972 keys 91 us, 6.0 TB/s (88% of a copy's rate); over 64
 // sequences of 251670 keys in pages of 16 99 us (a page is a TMA copy of 2 KB, whose rate bounds it; 91 with pages of 64).
 // bf16, 16 heads, a window of 2048 of 32 sequences: 89 us, 5.7 TB/s.  With two row tiles (16 drafts of 4 tokens, 32 heads on 4,
 // 52000 keys: 36 us) the products and the softmax bound it, 0.85 us a key tile.
@@ -27,7 +27,7 @@
 // [2^13, 2^15] whatever the scales are, and what falls below fp16's range is 2^-38 of it.  Rounding w
 // to fp16 costs 2^-12 of it at most.  An infinity is a code whose scale takes it past fp32's range, which neither product
 // sees: tiles with scales that large (some 2^120) add their infinities besides, to the scores and to O.  The others
-// pay for that code's registers: 33.5 -> 34.3 us with two row tiles (the drafts below, in a graph), 88.0 -> 88.2 with one.
+// pay for that code's registers: 33.4 -> 34.1 us with two row tiles (the drafts below, in a graph), 89.0 -> 89.4 with one.
 // bf16: the products run in bf16, and so do the weights (2^-9 at most).
 #include <type_traits>
 
@@ -85,6 +85,25 @@ __device__ __forceinline__ uint32_t codes_f16_hi(uint32_t c) {
 constexpr uint32_t kNoInfinity = 128;
 __device__ __forceinline__ uint32_t infinite_from(uint32_t b) { return b < 247 || b == 255 ? kNoInfinity : (262 - b) << 3; }
 __device__ __forceinline__ float signed_infinity(uint32_t code) { return __uint_as_float(0x7f800000u | (code & 128) << 24); }
+// Products of the infinities of a row of codes with a lane's queries of two row tiles (four of each of D / 16 steps, as they
+// are kept in shared memory).  A function that is called: inlined it has the rest spill more (drafts 34.7 instead of 34.1 us).
+template <int D>
+__device__ __noinline__ float2 infinite_products(const uint8_t* codes, const uint8_t* queries, uint32_t from) {
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+  for (int s = 0; s < D / 16; ++s) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(codes) ^ (4 * s & 16)) + (4 * s & 15));
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t c = w >> 8 * j & 255;
+      if ((c & 127) < from) continue;
+      const __half* y = reinterpret_cast<const __half*>(queries + s * 512) + j;
+      sum.x += signed_infinity(c) * __half2float(y[0]);
+      sum.y += signed_infinity(c) * __half2float(y[4]);
+    }
+  }
+  return sum;
+}
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (F16) {
@@ -609,17 +628,23 @@ __global__ void __launch_bounds__(kThreads, 2)
             if ((from_k & from_v) == kNoInfinity || key >= u.keys || key < u.lo) continue;
             if (from_k != kNoInfinity) {        // products of row 8 t + g, then on top of the scores of rows 8 t + 2 q and + 1
               float sum[NT] = {};
-#pragma unroll (kShared ? 1 : kSteps)
-              for (int s = 0; s < kSteps; ++s) {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + key0 * L::kBoxBytes + swz_offset(n, (D / 4) * q + 4 * s, L::kBoxBytes));
-                uint32_t y[NT][2];
-                operand(s, y);
+              if constexpr (kShared) {
+                const float2 y = infinite_products<D>(stage + key0 * L::kBoxBytes + swz_offset(n, (D / 4) * q, L::kBoxBytes), frag, from_k);
+                sum[0] = y.x;
+                sum[NT - 1] = y.y;
+              } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint32_t c = w >> 8 * j & 255;
+                for (int s = 0; s < kSteps; ++s) {
+                  const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + key0 * L::kBoxBytes + swz_offset(n, (D / 4) * q + 4 * s, L::kBoxBytes));
+                  uint32_t y[NT][2];
+                  operand(s, y);
 #pragma unroll
-                  for (int t = 0; t < NT; ++t)
-                    if ((c & 127) >= from_k) sum[t] += signed_infinity(c) * __half2float(__ushort_as_half((unsigned short)(y[t][j >> 1] >> 16 * (j & 1))));
+                  for (int j = 0; j < 4; ++j) {
+                    const uint32_t c = w >> 8 * j & 255;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                      if ((c & 127) >= from_k) sum[t] += signed_infinity(c) * __half2float(__ushort_as_half((unsigned short)(y[t][j >> 1] >> 16 * (j & 1))));
+                  }
                 }
               }
 #pragma unroll
