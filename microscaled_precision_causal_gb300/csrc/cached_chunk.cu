@@ -24,7 +24,7 @@
 // TMEM columns as in the scored forward.
 //
 // Bound by the chain of scores, softmax and values of two row tiles in turn, the tensor cores busy half the time, and at d 64
-// by the softmax's arithmetic.  Measured: a chunk of 2048 behind 14336, 32 heads on 8, d 128, E4M3 416 us, 1240 TFLOP/s (65% of
+// by the softmax's arithmetic.  Measured: a chunk of 2048 behind 14336, 32 heads on 8, d 128, E4M3 415 us, 1240 TFLOP/s (65% of
 // cuBLAS's bf16; bf16 pages 376); 4 chunks of 1024 with a window of 2048, 16 heads, d 64 76 us.
 #include <type_traits>
 
